@@ -62,7 +62,8 @@ typedef enum cfa_status {
     CFA_ERR_UNSUPPORTED = 2, /* a shape or cluster size this build does not run */
     CFA_ERR_CUDA = 3,        /* a CUDA runtime call failed (no device, launch, ...) */
     CFA_ERR_TIMEOUT = 4,     /* a bounded device-side wait gave up (see cfa_plan_status) */
-    CFA_ERR_ALIGNMENT = 5    /* a pointer is not 16-byte aligned */
+    CFA_ERR_ALIGNMENT = 5,   /* a pointer is not 16-byte aligned */
+    CFA_ERR_NO_PAGES = 6     /* a page pool ran out (see cfa_paged_status) */
 } cfa_status;
 
 /*
@@ -493,6 +494,165 @@ cfa_status cfa_mla_describe(const cfa_mla *mla, char *buf, int len);
  * fits.
  */
 cfa_status cfa_mla_set_row_splits(cfa_mla *mla, int splits);
+
+/* ==========================================================================
+ * Paged caches: block tables and slot maps built on the GPU, rotary embedding
+ * with the append to the cache, and attention of a ragged batch over a prefix
+ * that all its requests share and each request's own pages. A widening of the
+ * page's block (§1.1, one contiguous cache per sequence) to batches whose
+ * requests come and go, have several query tokens each (drafted tokens, prompt
+ * chunks) and start with the same tokens.
+ *
+ * Cache layout: k_pages and v_pages are bf16 [n_pages, n_kv_heads, page_size,
+ * head_dim]; row `off` of page `id` is slot id * page_size + off. A contiguous
+ * cache [B, n_heads, max_ctx, head_dim] of the calls above is such a cache
+ * with page_size = max_ctx and sequence b in page b (where max_ctx is an
+ * allowed page size). n_heads is a multiple of n_kv_heads: query heads
+ * [g G, (g + 1) G) read key head g, G = n_heads / n_kv_heads.
+ *
+ * Requests' lengths, offsets, tables and slots are device arrays (int32), read
+ * by the kernels on the device, so that a recorded graph serves every step. A
+ * value out of range is found there: it is flagged in the status word
+ * (cfa_paged_status) and nothing is read or written out of bounds. Results are
+ * bitwise reproducible. Conventions otherwise as above; integer arrays are
+ * 4-byte aligned, the bf16 ones 16-byte aligned.
+ *
+ * A plan owns a workspace: one plan must not run on two streams at once, nor
+ * in two graphs that may run at the same time.
+ * ========================================================================== */
+
+typedef struct cfa_paged cfa_paged; /* opaque */
+
+/*
+ * Plan on the current device for at most max_seqs (1..4096) requests and
+ * max_tokens (1..131072) new tokens per call. head_dim 64 or 128, n_heads <=
+ * 1024, page_size 16, 32 or a multiple of 64 up to 1<<22
+ * (CFA_ERR_UNSUPPORTED otherwise; CFA_ERR_INVALID_ARG for non-positive values
+ * or n_heads not a multiple of n_kv_heads). No rotation until
+ * cfa_paged_set_rope. NULL on failure; cfa_last_error() says why.
+ */
+cfa_paged *cfa_paged_create(int max_seqs, int max_tokens, int n_heads, int n_kv_heads,
+                            int head_dim, int page_size);
+
+/* Release the plan (synchronizes its device first). NULL is a no-op. */
+void cfa_paged_destroy(cfa_paged *paged);
+
+/* Scaling of the rotary frequencies for long contexts. */
+enum {
+    CFA_ROPE_PLAIN = 0,    /* f_i = theta^(-2i / rotary_dim) */
+    CFA_ROPE_LINEAR = 1,   /* f_i / factor */
+    CFA_ROPE_BY_PARTS = 2  /* between f_i and f_i / factor by the turns in original_ctx */
+};
+
+/*
+ * The rotation of the following cfa_paged_append and cfa_paged_layer calls:
+ * pair i of the first rotary_dim dims of a head at position n turns by n f_i,
+ * and its cosine and sine are multiplied by `magnitude` (1: a rotation). The
+ * pair is dims (i, i + rotary_dim/2), or (2i, 2i + 1) where interleaved != 0;
+ * dims from rotary_dim on pass through. rotary_dim is a multiple of 16 up to
+ * head_dim; 0 turns the rotation off. scaling is one of the three above;
+ * by parts, with r = original_ctx f_i / 2 pi turns over the original context
+ * and g = clamp((r - low_turns) / (high_turns - low_turns), 0, 1), the
+ * frequency is g f_i + (1 - g) f_i / factor. Needs theta >= 1, factor >= 1,
+ * magnitude > 0, all finite, and by parts 0 <= low_turns < high_turns and
+ * original_ctx >= 1 (CFA_ERR_INVALID_ARG; a rotary_dim that is no multiple of
+ * 16 or above head_dim: CFA_ERR_UNSUPPORTED). Held on the host: a recorded
+ * graph keeps the rotation it was recorded with.
+ */
+cfa_status cfa_paged_set_rope(cfa_paged *paged, double theta, int rotary_dim, int interleaved,
+                              int scaling, double factor, double low_turns, double high_turns,
+                              int original_ctx, double magnitude);
+
+/*
+ * Tables and slot maps of one step, in one kernel. Request b has lens[b]
+ * tokens in its pages and brings fresh[b] more (0 allowed):
+ *   - it is given the pages it lacks: tables[b][j] for
+ *     ceil(lens/page_size) <= j < ceil((lens + fresh)/page_size) are written with
+ *     free_pages[pool[0]], free_pages[pool[0] + 1], ... in the order of b and j
+ *     (free_pages [n_free]; pool[0] entries are taken so far, pool[1] <= n_free
+ *     there are). Other table entries are not written; those below are read.
+ *   - cu [n_seqs + 1] gets the first token row of every request and the total;
+ *   - token i of request b, in row cu[b] + i, gets position
+ *     base + lens[b] + i and slot id * page_size + (lens[b] + i) % page_size of its
+ *     page; rows from the total up to n_slots get position 0 and slot -1;
+ *   - lens_out [n_seqs] = lens + fresh, pool_out = {pool[0] + pages taken, pool[1]}
+ *     (lens_out may be lens and pool_out may be pool; no other overlap).
+ * tables is [n_seqs, table_width] (table_width <= 1<<18). All or nothing: a
+ * negative length, a total above n_slots, a request longer than
+ * table_width * page_size (then cfa_paged_status returns CFA_ERR_INVALID_ARG) or too few
+ * free pages (CFA_ERR_NO_PAGES) leave the tables as they were, lens_out = lens,
+ * pool_out = pool, every cu 0, every slot -1 and every position 0.
+ * Errors: CFA_ERR_INVALID_ARG (NULL, sizes out of the plan's range, overlaps),
+ * CFA_ERR_ALIGNMENT, CFA_ERR_CUDA.
+ */
+cfa_status cfa_paged_tables(cfa_paged *paged, int n_seqs, int base, const int *lens,
+                            const int *fresh, const int *free_pages, int n_free, const int *pool,
+                            int *tables, int table_width, int *lens_out, int *pool_out, int *cu,
+                            int *positions, int *slots, int n_slots, void *stream);
+
+/*
+ * Rotate q and k by positions [n_tokens] and put k and v into the cache, in
+ * one kernel: q_out[t] = rotated q[t] (bf16 [n_tokens, n_heads, head_dim]),
+ * row slots[t] of k_pages = rotated k[t], of v_pages = v[t]. q, k and v are
+ * rows of heads (dense within a row) with strides of q_stride, k_stride and
+ * v_stride elements (multiples of 8), so that they may be slices of one fused
+ * projection. q_out may be q where q_stride = n_heads * head_dim; it must not
+ * overlap q otherwise, nor k, v or the pages. Rows with a negative slot are
+ * skipped: their q_out row stays as it was. A slot of n_pages * page_size or
+ * more is skipped too and flagged (CFA_ERR_INVALID_ARG from cfa_paged_status).
+ * Two tokens with the same slot leave either's row there. With n_tokens 0
+ * this call and the next two do nothing (pointers may then be NULL).
+ */
+cfa_status cfa_paged_append(cfa_paged *paged, int n_tokens, const void *q, long long q_stride,
+                            const void *k, long long k_stride, const void *v, long long v_stride,
+                            const int *positions, const int *slots, int n_pages, void *k_pages,
+                            void *v_pages, void *q_out, void *stream);
+
+/*
+ * Attention of n_tokens query rows q (bf16, heads dense, row stride q_stride
+ * elements) of n_seqs requests: rows [cu[b], cu[b + 1]) are the last tokens
+ * of request b. Each attends every key of the prefix (prefix_len positions in
+ * the pages prefix_table lists; may be 0) and, of the lens[b] keys in the pages
+ * of tables[b] (its new tokens' own keys among them), those up to its own
+ * position: row cu[b] + i sees lens[b] - (cu[b + 1] - cu[b]) + i + 1 of them.
+ *   out  bf16 [n_tokens, n_heads, head_dim] = softmax(scale q . k) v
+ *   lse  fp32 [n_tokens, n_heads], the natural logarithm of the sum of
+ *        exp(scale q . k), or NULL
+ * A row that sees no key gets 0 and lse -inf. Rows outside [cu[0], cu[n_seqs])
+ * stay as they were. scale 0 means 1/sqrt(head_dim). Cache rows at positions
+ * that no row sees are read but never used: they may hold anything, NaN
+ * included. Flagged in the status word as CFA_ERR_INVALID_ARG: offsets cu that
+ * are not ascending within [0, n_tokens] (nothing is written then); a
+ * length outside [0, table_width * page_size] (taken as 0); a page id outside
+ * [0, n_pages) where a key is read (its keys and values count as zeros).
+ * out and lse must not overlap an input or each other.
+ */
+cfa_status cfa_paged_attention(cfa_paged *paged, int n_tokens, int n_seqs, const void *q,
+                               long long q_stride, const int *cu, const int *prefix_table,
+                               int prefix_len, const int *tables, int table_width,
+                               const int *lens, int n_pages, const void *k_pages,
+                               const void *v_pages, float scale, void *out, float *lse,
+                               void *stream);
+
+/*
+ * The attention half of one layer: cfa_paged_append (q rotated into q_out,
+ * which may be q), then cfa_paged_attention on q_out. Arguments as theirs; the
+ * requests' rows and slots as cfa_paged_tables made them, once per step for all layers.
+ */
+cfa_status cfa_paged_layer(cfa_paged *paged, int n_tokens, int n_seqs, const void *q,
+                           long long q_stride, const void *k, long long k_stride, const void *v,
+                           long long v_stride, const int *positions, const int *slots,
+                           const int *cu, const int *prefix_table, int prefix_len,
+                           const int *tables, int table_width, const int *lens, int n_pages,
+                           void *k_pages, void *v_pages, float scale, void *q_out, void *out,
+                           float *lse, void *stream);
+
+/* Synchronizes, reads and clears the plan's device status word (as
+ * cfa_plan_status; CFA_ERR_NO_PAGES after a refused cfa_paged_tables). */
+cfa_status cfa_paged_status(cfa_paged *paged);
+
+/* One-line JSON description (shape, rotation, grid, shared memory, workspace). */
+cfa_status cfa_paged_describe(const cfa_paged *paged, char *buf, int len);
 
 #ifdef __cplusplus
 }

@@ -108,12 +108,38 @@ _lib.cfa_stack_describe.argtypes = [_vp, ctypes.c_char_p, _i]
 _lib.cfa_plan_layout.restype = _i
 _lib.cfa_plan_layout.argtypes = [_i] * 12 + [ctypes.c_char_p, _i]
 
+_lib.cfa_paged_create.restype = _vp
+_lib.cfa_paged_create.argtypes = [_i] * 6
+_lib.cfa_paged_destroy.restype = None
+_lib.cfa_paged_destroy.argtypes = [_vp]
+_lib.cfa_paged_set_rope.restype = _i
+_lib.cfa_paged_set_rope.argtypes = [_vp, ctypes.c_double, _i, _i, _i, ctypes.c_double,
+                                    ctypes.c_double, ctypes.c_double, _i, ctypes.c_double]
+_ll = ctypes.c_longlong
+_lib.cfa_paged_tables.restype = _i
+_lib.cfa_paged_tables.argtypes = ([_vp, _i, _i, _vp, _vp, _vp, _i, _vp, _vp, _i] + [_vp] * 5
+                                  + [_i, _vp])
+_lib.cfa_paged_append.restype = _i
+_lib.cfa_paged_append.argtypes = [_vp, _i, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _i, _vp, _vp,
+                                  _vp, _vp]
+_lib.cfa_paged_attention.restype = _i
+_lib.cfa_paged_attention.argtypes = [_vp, _i, _i, _vp, _ll, _vp, _vp, _i, _vp, _i, _vp, _i, _vp,
+                                     _vp, ctypes.c_float, _vp, _vp, _vp]
+_lib.cfa_paged_layer.restype = _i
+_lib.cfa_paged_layer.argtypes = [_vp, _i, _i, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp,
+                                 _i, _vp, _i, _vp, _i, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp]
+_lib.cfa_paged_status.restype = _i
+_lib.cfa_paged_status.argtypes = [_vp]
+_lib.cfa_paged_describe.restype = _i
+_lib.cfa_paged_describe.argtypes = [_vp, ctypes.c_char_p, _i]
+
 CFA_OK = 0
 CFA_ERR_INVALID_ARG = 1
 CFA_ERR_UNSUPPORTED = 2
 CFA_ERR_CUDA = 3
 CFA_ERR_TIMEOUT = 4
 CFA_ERR_ALIGNMENT = 5
+CFA_ERR_NO_PAGES = 6
 
 EXPORTED_SYMBOLS = (
     "cfa_plan_create", "cfa_plan_destroy", "cfa_decode_step", "cfa_decode_step_ex",
@@ -131,6 +157,9 @@ EXPORTED_SYMBOLS = (
     "cfa_stack_step", "cfa_stack_step_graph", "cfa_stack_status", "cfa_stack_describe",
     "cfa_mla_create", "cfa_mla_destroy", "cfa_mla_step", "cfa_mla_status", "cfa_mla_describe",
     "cfa_mla_set_row_splits",
+    "cfa_paged_create", "cfa_paged_destroy", "cfa_paged_set_rope", "cfa_paged_tables",
+    "cfa_paged_append", "cfa_paged_attention", "cfa_paged_layer", "cfa_paged_status",
+    "cfa_paged_describe",
 )
 
 
@@ -709,4 +738,226 @@ class Mla:
                           rope_theta, eps, out, stream)
         if st != CFA_OK:
             raise CfaError(st, "cfa_mla_step")
+        return out
+
+
+# -------------------------------------------- paged caches and shared prefixes
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "by_parts": 2}
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+
+
+def cfa_paged_create(max_seqs: int, max_tokens: int, n_heads: int, n_kv_heads: int,
+                     head_dim: int, page_size: int) -> int:
+    h = _lib.cfa_paged_create(max_seqs, max_tokens, n_heads, n_kv_heads, head_dim, page_size)
+    if not h:
+        raise CfaError(cfa_last_error(), "cfa_paged_create")
+    return h
+
+
+def cfa_paged_destroy(paged: int) -> None:
+    _lib.cfa_paged_destroy(paged)
+
+
+def cfa_paged_status(paged) -> int:
+    return int(_lib.cfa_paged_status(paged))
+
+
+def cfa_paged_describe(paged) -> dict:
+    buf = ctypes.create_string_buffer(1024)
+    st = _lib.cfa_paged_describe(paged, buf, len(buf))
+    if st != CFA_OK:
+        raise CfaError(st, "cfa_paged_describe")
+    return json.loads(buf.value.decode())
+
+
+class Paged:
+    """Owns a cfa_paged: block tables, rotary append and shared-prefix attention.
+
+    k_pages and v_pages are bf16 [n_pages, n_kv_heads, page_size, head_dim];
+    q, k, v [tokens, heads, head_dim] may be slices of a fused projection (dense
+    within a row); every integer tensor is int32 on the plan's device."""
+
+    def __init__(self, max_seqs: int, max_tokens: int, n_heads: int, n_kv_heads: int,
+                 head_dim: int, page_size: int):
+        self.max_seqs, self.max_tokens = max_seqs, max_tokens
+        self.n_heads, self.n_kv_heads, self.head_dim, self.page_size = (
+            n_heads, n_kv_heads, head_dim, page_size)
+        self.handle = cfa_paged_create(max_seqs, max_tokens, n_heads, n_kv_heads, head_dim,
+                                       page_size)
+        self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def close(self):
+        if getattr(self, "handle", None):
+            cfa_paged_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def describe(self) -> dict:
+        return cfa_paged_describe(self.handle)
+
+    def status(self) -> int:
+        return cfa_paged_status(self.handle)
+
+    def set_rope(self, theta: float = 10000.0, rotary_dim: Optional[int] = None,
+                 interleaved: bool = False, scaling: str = "none", factor: float = 1.0,
+                 low_turns: float = 1.0, high_turns: float = 32.0, original_ctx: int = 4096,
+                 magnitude: float = 1.0) -> None:
+        """The rotation of the following append and layer calls (cfa_paged_set_rope);
+        rotary_dim None: the whole head, 0: no rotation."""
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+        rd = self.head_dim if rotary_dim is None else int(rotary_dim)
+        st = _lib.cfa_paged_set_rope(self.handle, float(theta), rd, 1 if interleaved else 0,
+                                     ROPE_SCALINGS[scaling], float(factor), float(low_turns),
+                                     float(high_turns), int(original_ctx), float(magnitude))
+        if st != CFA_OK:
+            raise CfaError(st, "cfa_paged_set_rope")
+
+    # Argument checks; each is a few attribute reads, since the smallest calls
+    # take the GPU only microseconds.
+
+    def _dense(self, name, t, shape, dtype):
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}")
+        return t.data_ptr()
+
+    def _rows(self, name, t, n, heads):
+        """Pointer and row stride of [n, heads, head_dim] with dense rows."""
+        if t.dtype is not _BF16:
+            raise TypeError(f"{name} must be {_BF16}")
+        if t.shape != (n, heads, self.head_dim):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                             f"{(n, heads, self.head_dim)}")
+        s = t.stride()
+        if s[2] != 1 or (heads > 1 and s[1] != self.head_dim):
+            raise ValueError(f"{name} must be dense within a row")
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}")
+        return t.data_ptr(), (s[0] if n > 1 else heads * self.head_dim)
+
+    def _pages(self, k_pages, v_pages):
+        n = k_pages.shape[0]
+        shape = (n, self.n_kv_heads, self.page_size, self.head_dim)
+        return n, self._dense("k_pages", k_pages, shape, _BF16), \
+            self._dense("v_pages", v_pages, shape, _BF16)
+
+    def _stream(self, stream):
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
+        return _stream(stream)
+
+    def build_tables(self, lens, fresh, free_pages, pool, tables, lens_out, pool_out, cu, positions,
+                     slots, base: int = 0, stream=None):
+        """Pages, offsets, positions and slots of one step (cfa_paged_tables):
+        lens, fresh, lens_out [B]; free_pages [n]; pool, pool_out [2]; tables
+        [B, width]; cu [B + 1]; positions, slots [rows]. base is the prefix's
+        length. Returns (cu, positions, slots)."""
+        B = lens.shape[0]
+        n = slots.shape[0]
+        if tables.dim() != 2:
+            raise ValueError("tables must be [requests, width]")
+        st = _lib.cfa_paged_tables(
+            self.handle, B, base, self._dense("lens", lens, (B,), _I32),
+            self._dense("fresh", fresh, (B,), _I32),
+            self._dense("free_pages", free_pages, (free_pages.numel(),), _I32),
+            free_pages.numel(), self._dense("pool", pool, (2,), _I32),
+            self._dense("tables", tables, (B, tables.shape[1]), _I32), tables.shape[1],
+            self._dense("lens_out", lens_out, (B,), _I32),
+            self._dense("pool_out", pool_out, (2,), _I32), self._dense("cu", cu, (B + 1,), _I32),
+            self._dense("positions", positions, (n,), _I32), self._dense("slots", slots, (n,), _I32),
+            n, self._stream(stream))
+        if st != CFA_OK:
+            raise CfaError(st, "cfa_paged_tables")
+        return cu, positions, slots
+
+    def append(self, q, k, v, positions, slots, k_pages, v_pages, q_out, stream=None):
+        """Rotate q into q_out and k into its page, put v into its page
+        (cfa_paged_append). Returns q_out."""
+        T = q.shape[0]
+        qp, qs = self._rows("q", q, T, self.n_heads)
+        kp, ks = self._rows("k", k, T, self.n_kv_heads)
+        vp, vs = self._rows("v", v, T, self.n_kv_heads)
+        n, kc, vc = self._pages(k_pages, v_pages)
+        st = _lib.cfa_paged_append(
+            self.handle, T, qp, qs, kp, ks, vp, vs, self._dense("positions", positions, (T,), _I32),
+            self._dense("slots", slots, (T,), _I32), n, kc, vc,
+            self._dense("q_out", q_out, (T, self.n_heads, self.head_dim), _BF16),
+            self._stream(stream))
+        if st != CFA_OK:
+            raise CfaError(st, "cfa_paged_append")
+        return q_out
+
+    def _attn(self, T, cu, lens, tables, prefix_table, prefix_len, out, lse):
+        B = lens.shape[0]
+        if tables.dim() != 2:
+            raise ValueError("tables must be [requests, width]")
+        if prefix_len < 0:
+            raise ValueError("prefix_len must not be negative")
+        pt = None
+        if prefix_len:
+            if prefix_table is None or prefix_table.numel() * self.page_size < prefix_len:
+                raise ValueError("prefix_table does not hold prefix_len positions")
+            pt = self._dense("prefix_table", prefix_table, (prefix_table.numel(),), _I32)
+        return (B, self._dense("cu", cu, (B + 1,), _I32), pt,
+                self._dense("tables", tables, (B, tables.shape[1]), _I32), tables.shape[1],
+                self._dense("lens", lens, (B,), _I32),
+                self._dense("out", out, (T, self.n_heads, self.head_dim), _BF16),
+                None if lse is None else self._dense("lse", lse, (T, self.n_heads), _F32))
+
+    def attend(self, q, cu, lens, tables, k_pages, v_pages, out, prefix_table=None,
+               prefix_len: int = 0, scale: Optional[float] = None, lse=None, stream=None):
+        """Attention over the shared prefix and each request's own pages
+        (cfa_paged_attention). scale None: 1/sqrt(head_dim). Returns out."""
+        T = q.shape[0]
+        qp, qs = self._rows("q", q, T, self.n_heads)
+        n, kc, vc = self._pages(k_pages, v_pages)
+        B, cup, pt, tp, width, lp, op, sp = self._attn(T, cu, lens, tables, prefix_table,
+                                                       prefix_len, out, lse)
+        if scale is not None and not scale > 0.0:
+            raise ValueError("scale must be positive")
+        st = _lib.cfa_paged_attention(self.handle, T, B, qp, qs, cup, pt, prefix_len, tp, width,
+                                      lp, n, kc, vc, scale or 0.0, op, sp, self._stream(stream))
+        if st != CFA_OK:
+            raise CfaError(st, "cfa_paged_attention")
+        return out
+
+    def layer(self, q, k, v, positions, slots, cu, lens, tables, k_pages, v_pages, q_out, out,
+              prefix_table=None, prefix_len: int = 0, scale: Optional[float] = None, lse=None,
+              stream=None):
+        """append, then attend on q_out (cfa_paged_layer). Returns out."""
+        T = q.shape[0]
+        qp, qs = self._rows("q", q, T, self.n_heads)
+        kp, ks = self._rows("k", k, T, self.n_kv_heads)
+        vp, vs = self._rows("v", v, T, self.n_kv_heads)
+        n, kc, vc = self._pages(k_pages, v_pages)
+        B, cup, pt, tp, width, lp, op, sp = self._attn(T, cu, lens, tables, prefix_table,
+                                                       prefix_len, out, lse)
+        if scale is not None and not scale > 0.0:
+            raise ValueError("scale must be positive")
+        st = _lib.cfa_paged_layer(self.handle, T, B, qp, qs, kp, ks, vp, vs,
+                                  self._dense("positions", positions, (T,), _I32),
+                                  self._dense("slots", slots, (T,), _I32), cup, pt, prefix_len, tp,
+                                  width, lp, n, kc, vc, scale or 0.0,
+                                  self._dense("q_out", q_out, (T, self.n_heads, self.head_dim),
+                                              _BF16), op, sp, self._stream(stream))
+        if st != CFA_OK:
+            raise CfaError(st, "cfa_paged_layer")
         return out

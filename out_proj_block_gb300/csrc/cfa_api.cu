@@ -442,6 +442,7 @@ const char *cfa_status_string(cfa_status s) {
         case CFA_ERR_CUDA: return "CFA_ERR_CUDA";
         case CFA_ERR_TIMEOUT: return "CFA_ERR_TIMEOUT";
         case CFA_ERR_ALIGNMENT: return "CFA_ERR_ALIGNMENT";
+        case CFA_ERR_NO_PAGES: return "CFA_ERR_NO_PAGES";
     }
     return "CFA_ERR_UNKNOWN";
 }

@@ -29,6 +29,8 @@ constexpr int kXStageMmaBytes = 2 * kMmaN * 128;   // x per stage on the tensor-
 // Status word bits, written by kernels and read by cfa_plan_status.
 constexpr unsigned kStatusTimeoutBit = 1u;
 constexpr unsigned kStatusBadLengthBit = 2u;  // a device-resident length was out of range
+constexpr unsigned kStatusNoPagesBit = 4u;    // the free list of a page pool ran out
+constexpr unsigned kStatusBadPageBit = 8u;    // a page id or slot was out of range
 constexpr unsigned kStatusSiteShift = 8;  // site code of the first timeout
 
 // A load warp's final wait for its own copies in flight uses this many times

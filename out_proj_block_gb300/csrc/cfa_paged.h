@@ -1,0 +1,70 @@
+// cfa_paged.h -- launch parameters of the paged-cache kernels (block tables,
+// rotary append, attention over a shared prefix). Not part of the public ABI.
+#pragma once
+
+#include <cstdint>
+
+namespace cfa {
+
+constexpr int kPagedMaxSeqs = 4096;         // requests per call
+constexpr int kPagedMaxTokens = 1 << 17;    // new tokens per call
+constexpr int kPagedMaxTableWidth = 1 << 18;
+
+// ------------------------------------------------- block tables and slot maps
+
+struct TablesParams {
+    const int *lens;        // [B] cached tokens of each request
+    const int *fresh;       // [B] new tokens of each request
+    const int *free_pages;  // ids of free pages
+    const int *pool;        // {entries of free_pages taken so far, entries there are}
+    int *tables;            // [B][width] page ids; entries past the held pages are written
+    int *lens_out;          // [B] lens + fresh (may be lens)
+    int *pool_out;          // [2] (may be pool)
+    int *cu;                // [B + 1] first token row of each request
+    int *positions;         // [n_slots]
+    int *slots;             // [n_slots]
+    unsigned *ticket;       // arrivals of the grid's blocks; 0 between calls
+    unsigned *status;
+    int B, width, page_size, n_free, n_slots, base;
+};
+
+constexpr int kTablesThreads = 512;
+
+// ------------------------------------------------------------ rotary append
+
+struct AppendParams {
+    const uint16_t *q, *k, *v;  // [T] rows of heads; strides in elements
+    long long q_stride, k_stride, v_stride;
+    const int *positions, *slots;
+    uint16_t *k_pages, *v_pages;  // [n_pages][n_kv][page_size][d]
+    uint16_t *q_out;              // [T][n_heads][d]
+    unsigned *status;
+    int n_heads, n_kv, d, page_size;
+    int n_rows;        // slots there are: n_pages * page_size
+    int rd;            // rotated dims of a head; 0: none
+    int interleaved;   // pairs (2i, 2i+1) instead of (i, i + rd/2)
+    float magnitude;   // factor on cos and sin
+    // turns per position of pair i as a fraction of 2^64
+    unsigned long long turns[64];
+};
+
+constexpr int kAppendThreads = 256;
+
+// ----------------------------------------- attention over a shared prefix
+
+struct PagedAttnParams {
+    const uint16_t *q;          // [T][n_heads][d], row stride q_stride elements
+    long long q_stride;
+    const uint16_t *k_pages, *v_pages;
+    const int *cu;              // [B + 1]
+    const int *lens;            // [B]
+    const int *tables;          // [B][width]
+    const int *prefix_table;    // [ceil(prefix_len / page_size)]
+    uint16_t *out;              // [T][n_heads][d]
+    float *lse;                 // [T][n_heads] or null
+    unsigned *status;
+    int T, B, n_heads, n_kv, page_size, n_pages, width, prefix_len;
+    float scale_log2;           // scale * log2(e)
+};
+
+}  // namespace cfa

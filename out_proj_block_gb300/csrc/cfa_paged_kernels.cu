@@ -1,0 +1,14 @@
+// Instantiations of the paged-cache kernels.
+#include "cfa_paged_attn.cuh"
+#include "cfa_paged_cache.cuh"
+
+namespace cfa {
+
+const void *paged_tables_kernel_ptr() { return reinterpret_cast<const void *>(&paged_tables_kernel); }
+const void *paged_append_kernel_ptr() { return reinterpret_cast<const void *>(&paged_append_kernel); }
+const void *paged_attention_kernel_ptr(int d) {
+    return d == 128 ? reinterpret_cast<const void *>(&paged_attention_simple_kernel<128>)
+                    : reinterpret_cast<const void *>(&paged_attention_simple_kernel<64>);
+}
+
+}  // namespace cfa
