@@ -14,11 +14,14 @@
 #include "cfa_host.h"
 #include "cfa_internal.h"
 #include "cfa_paged.h"
+#include "cfa_paged_split.h"
 
 namespace cfa {
 const void *paged_tables_kernel_ptr();
 const void *paged_append_kernel_ptr();
 const void *paged_attention_kernel_ptr(int d);
+const void *paged_merge_kernel_ptr(int d);
+int paged_attention_smem(int d, int seqs);
 }  // namespace cfa
 
 struct cfa_paged {
@@ -31,9 +34,15 @@ struct cfa_paged {
     unsigned long long turns[64] = {};
     // workspace
     unsigned *words = nullptr;  // [0] status, [1] arrivals of the tables' blocks
+    int *plan_ws = nullptr;     // the attention's scan, for its merge
+    float *rec_o = nullptr;     // records of the attention's pieces
+    float2 *rec_ml = nullptr;
+    long long rec_rows = 0;
 };
 
 namespace {
+
+constexpr unsigned long long kTimeoutNs = 2000000000ull;  // 2 s per device-side wait
 
 cfa_status fail(cfa_status s) { return cfa::set_last_error(s); }
 
@@ -84,7 +93,13 @@ cfa_status launch(const void *kernel, int grid, int threads, size_t smem, cudaSt
 
 void paged_free(cfa_paged *p) {
     if (p->words) cudaFree(p->words);
+    if (p->plan_ws) cudaFree(p->plan_ws);
+    if (p->rec_o) cudaFree(p->rec_o);
+    if (p->rec_ml) cudaFree(p->rec_ml);
     p->words = nullptr;
+    p->plan_ws = nullptr;
+    p->rec_o = nullptr;
+    p->rec_ml = nullptr;
 }
 
 // Rows of a cache of n_pages pages, or -1 where they pass the kernels' 32-bit
@@ -240,10 +255,30 @@ cfa_status launch_attention(cfa_paged *p, const AttnArgs &a, cudaStream_t stream
     kp.prefix_len = a.prefix_len;
     const double scale = a.scale > 0.0f ? a.scale : 1.0 / std::sqrt(static_cast<double>(p->D));
     kp.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
-    void *args[1] = {&kp};
-    const long long warps = static_cast<long long>(a.n_tokens) * p->nh;
-    return launch(cfa::paged_attention_kernel_ptr(p->D), static_cast<int>((warps + 7) / 8), 256, 0,
-                  stream, args);
+    kp.plan_ws = p->plan_ws;
+    kp.rec_o = p->rec_o;
+    kp.rec_ml = p->rec_ml;
+    kp.timeout_ns = kTimeoutNs;
+    // a box of rows lies inside one page and divides a block of 128 keys
+    kp.box_rows = p->ps % 128 == 0 ? 128 : p->ps % 64 == 0 ? 64 : p->ps;
+    CUtensorMap tk, tv;
+    const uint64_t rows = static_cast<uint64_t>(cache_rows(p, a.n_pages)), d = static_cast<uint64_t>(p->D);
+    if (cfa::encode_bf16_2d_ex(&tk, a.kp, d, rows, d, 64, static_cast<uint32_t>(kp.box_rows), true) != CFA_OK ||
+        cfa::encode_bf16_2d_ex(&tv, a.vp, d, rows, d, 64, static_cast<uint32_t>(kp.box_rows), true) != CFA_OK)
+        return CFA_ERR_CUDA;
+    void *args[3] = {&tk, &tv, &kp};
+    int grid = p->num_sms;
+    cfa_status st = launch(cfa::paged_attention_kernel_ptr(p->D), grid, cfa::kPagedThreads,
+                           static_cast<size_t>(cfa::paged_attention_smem(p->D, a.n_seqs)), stream, args);
+    if (st != CFA_OK) return st;
+    // rows that can share: all of them, or every request's most
+    const long long shared = std::min(static_cast<long long>(a.n_tokens) * (p->nh / p->nkv),
+                                      static_cast<long long>(a.n_seqs) * cfa::kPagedAloneRows);
+    int shared_blocks = static_cast<int>((shared + 31) / 32) * p->nkv;
+    void *margs[3] = {&kp, &grid, &shared_blocks};
+    const size_t pieces = static_cast<size_t>(grid) + 1;
+    return launch(cfa::paged_merge_kernel_ptr(p->D), shared_blocks + 8 * grid, 256,
+                  8u * (static_cast<size_t>(a.n_seqs) + 1) + pieces * 32 * 8, stream, margs);
 }
 
 }  // namespace
@@ -289,10 +324,22 @@ cfa_paged *cfa_paged_create(int max_seqs, int max_tokens, int n_heads, int n_kv_
     p->ps = page_size;
     p->device = device;
     p->num_sms = sms;
+    const int G = n_heads / n_kv_heads;
+    p->rec_rows = cfa::paged_record_rows(
+        cfa::PagedShape{G, n_kv_heads, 0, sms},
+        std::min(static_cast<long long>(max_tokens) * G, static_cast<long long>(max_seqs) * cfa::kPagedAloneRows));
     if (cudaFuncSetAttribute(cfa::paged_tables_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(sizeof(int)) * (3 * cfa::kPagedMaxSeqs + 2)) != cudaSuccess ||
+        cudaFuncSetAttribute(cfa::paged_attention_kernel_ptr(head_dim), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             cfa::paged_attention_smem(head_dim, cfa::kPagedMaxSeqs)) != cudaSuccess ||
+        cudaFuncSetAttribute(cfa::paged_merge_kernel_ptr(head_dim), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             8 * (cfa::kPagedMaxSeqs + 1) + (sms + 1) * 32 * 8) != cudaSuccess ||
         cudaMalloc(&p->words, 2 * sizeof(unsigned)) != cudaSuccess ||
-        cudaMemset(p->words, 0, 2 * sizeof(unsigned)) != cudaSuccess) {
+        cudaMemset(p->words, 0, 2 * sizeof(unsigned)) != cudaSuccess ||
+        cudaMalloc(&p->plan_ws, sizeof(int) * (cfa::kPagedPlanInts + 2 * (static_cast<size_t>(max_seqs) + 1))) !=
+            cudaSuccess ||
+        cudaMalloc(&p->rec_o, sizeof(float) * static_cast<size_t>(p->rec_rows) * head_dim) != cudaSuccess ||
+        cudaMalloc(&p->rec_ml, sizeof(float2) * static_cast<size_t>(p->rec_rows)) != cudaSuccess) {
         cudaGetLastError();
         paged_free(p);
         delete p;

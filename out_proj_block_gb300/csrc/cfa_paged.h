@@ -4,9 +4,11 @@
 
 #include <cstdint>
 
+#include <cuda_runtime.h>
+
 namespace cfa {
 
-constexpr int kPagedMaxSeqs = 4096;         // requests per call
+constexpr int kPagedMaxSeqs = 2048;         // requests per call
 constexpr int kPagedMaxTokens = 1 << 17;    // new tokens per call
 constexpr int kPagedMaxTableWidth = 1 << 18;
 
@@ -63,8 +65,17 @@ struct PagedAttnParams {
     uint16_t *out;              // [T][n_heads][d]
     float *lse;                 // [T][n_heads] or null
     unsigned *status;
+    int *plan_ws;               // the scan's totals (kPagedPlanInts) and arrays, for the merge
+    float *rec_o;               // records: unnormalised outputs, a piece's rows in 16-byte chunks,
+                                // [D / 4][rows][4]
+    float2 *rec_ml;             // and each row's maximum (base 2) and sum
     int T, B, n_heads, n_kv, page_size, n_pages, width, prefix_len;
+    int box_rows;               // cache rows of one TMA box
     float scale_log2;           // scale * log2(e)
+    unsigned long long timeout_ns;
 };
+
+constexpr int kPagedThreads = 320;    // 8 compute warps, a load warp, an MMA warp
+constexpr int kPagedPlanInts = 8;
 
 }  // namespace cfa

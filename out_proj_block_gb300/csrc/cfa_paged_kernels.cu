@@ -7,8 +7,15 @@ namespace cfa {
 const void *paged_tables_kernel_ptr() { return reinterpret_cast<const void *>(&paged_tables_kernel); }
 const void *paged_append_kernel_ptr() { return reinterpret_cast<const void *>(&paged_append_kernel); }
 const void *paged_attention_kernel_ptr(int d) {
-    return d == 128 ? reinterpret_cast<const void *>(&paged_attention_simple_kernel<128>)
-                    : reinterpret_cast<const void *>(&paged_attention_simple_kernel<64>);
+    return d == 128 ? reinterpret_cast<const void *>(&paged_attention_kernel<128>)
+                    : reinterpret_cast<const void *>(&paged_attention_kernel<64>);
+}
+const void *paged_merge_kernel_ptr(int d) {
+    return d == 128 ? reinterpret_cast<const void *>(&paged_merge_kernel<128>)
+                    : reinterpret_cast<const void *>(&paged_merge_kernel<64>);
+}
+int paged_attention_smem(int d, int seqs) {
+    return d == 128 ? PagedSmem<128>::bytes(seqs) : PagedSmem<64>::bytes(seqs);
 }
 
 }  // namespace cfa

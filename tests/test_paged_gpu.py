@@ -85,7 +85,7 @@ def want_tables(c, ps, base=0):
 
 
 @pytest.mark.parametrize("B,ps,fresh", [(1, 16, 1), (3, 64, 5), (16, 16, 1), (33, 32, 90),
-                                        (513, 16, 2), (1025, 192, 1), (4096, 64, 3)])
+                                        (513, 16, 2), (1025, 192, 1), (2048, 64, 3)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_tables(cfa, B, ps, fresh, in_place):
     c = tables_case(B, ps, B, most_fresh=fresh)
