@@ -75,7 +75,7 @@ struct PagedAttnParams {
     unsigned long long timeout_ns;
 };
 
-constexpr int kPagedThreads = 320;    // 8 compute warps, a load warp, an MMA warp
+constexpr int kPagedThreads = 384;    // 8 compute warps; load, MMA, address and prep warps
 constexpr int kPagedPlanInts = 8;
 
 }  // namespace cfa

@@ -93,9 +93,66 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Register share of the calling warpgroup. The block is launched with 384 x 168 =
+// 64,512; the two compute warpgroups take 208 a thread and the third keeps 88:
+// 128 x (208 + 208 + 88) = 64,512.
+__device__ __forceinline__ void registers_for_compute() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+}
+__device__ __forceinline__ void registers_for_issue() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+}
+
+// Two fp32 lanes in one instruction.
+__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair_f32(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// Two fp32 to packed bf16, rounded to nearest even, in one conversion.
+__device__ __forceinline__ uint32_t pack2_bf16_cvt(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(n) : "memory");
 }
+
+// Blocks of keys whose cache rows the address warp finds ahead of the load warp, four
+// at a time: entries of 12 ints (up to 8 boxes' rows, their number, the piece's blocks
+// and order), groups of 4 entries.
+constexpr int kPagedGroups = 4;
+constexpr int kPagedEntry = 12;
+
+// A piece as the prep warp lays it out for the compute and MMA warps, one ahead.
+template <int D>
+struct PagedSlot {
+    static constexpr int kRow = 128;                 // after the PagedPiece: int2 [256] token, output row
+    static constexpr int kQ = kRow + 256 * 8;        // up to 16 query rows, [D / 64][16][64] swizzled
+    static constexpr int kBytes = kQ + 16 * D * 2;
+};
 
 // Shared memory of the attention kernel for head_dim D.
 template <int D>
@@ -106,12 +163,26 @@ struct PagedSmem {
     static constexpr int kQTile = 128 * D * 2;
     static constexpr int kQ = 0;                                // two query tiles; scratch otherwise
     static constexpr int kRing = 2 * kQTile;
-    static constexpr int kRow = kRing + kStages * kStage;       // int2 [256]: token, output row
-    static constexpr int kMl = kRow + 256 * 8;                  // float2 [128]: max and sum
+    static constexpr int kSlots = kRing + kStages * kStage;     // two pieces
+    static constexpr int kMl = kSlots + 2 * PagedSlot<D>::kBytes;  // float2 [128]: max and sum
     static constexpr int kBars = kMl + 128 * 8;
-    static constexpr int kMisc = kBars + 32 * 8;                // flags, TMEM address, scan sums
-    static constexpr int kArrays = kMisc + 512;                 // start, stok: int [2][B + 1]
+    static constexpr int kMisc = kBars + 48 * 8;                // flags, TMEM address, scan sums
+    static constexpr int kFifo = kMisc + 256;                   // the address warp's entries
+    static constexpr int kArrays = kFifo + 4 * kPagedGroups * kPagedEntry * 4;  // start, stok: int [2][B + 1]
     static int bytes(int B) { return kArrays + 8 * (B + 1) + 1024; }
+};
+static_assert(sizeof(PagedPiece) <= 128, "a piece fits its slot");
+
+// The bounded wait behind a first poll that failed: out of line, because the kernel's
+// many waits would otherwise crowd its loops out of the instruction cache.
+static __device__ __noinline__ bool paged_wait_slow(uint32_t bar, uint32_t parity, unsigned long long timeout_ns,
+                                                    volatile int *timed_out, unsigned *status, unsigned site) {
+    return mbar_wait_bounded<false>(bar, parity, timeout_ns, timed_out, status, site);
+}
+
+template <bool V>
+struct PagedFlag {
+    static constexpr bool value = V;
 };
 
 __device__ __forceinline__ PagedRequest paged_request(const PagedAttnParams &p, int b) {
@@ -134,24 +205,31 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     const uint32_t ring = base + S::kRing;
     const uint32_t bar_full = base + S::kBars, bar_empty = bar_full + 8 * NS;
     const uint32_t bar_q = bar_empty + 8 * NS, bar_s = bar_q + 8, bar_p = bar_s + 16, bar_o = bar_p + 16,
-                   bar_drain = bar_o + 16;
+                   bar_drain = bar_o + 16, bar_piece = bar_drain + 8, bar_piece_free = bar_piece + 16,
+                   bar_entry = bar_piece_free + 16, bar_entry_free = bar_entry + 8 * kPagedGroups;
     int *misc = reinterpret_cast<int *>(smem + S::kMisc);
     volatile int *timed_out = misc;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 1);
     int *start = reinterpret_cast<int *>(smem + S::kArrays), *stok = start + p.B + 1;
-    int2 *row_at = reinterpret_cast<int2 *>(smem + S::kRow);
+    int *entries = reinterpret_cast<int *>(smem + S::kFifo);
     float2 *ml = reinterpret_cast<float2 *>(smem + S::kMl);
 
     if (tid == 0) {
-        for (int s = 0; s < NS; ++s) {
+        CFA_ROLLED for (int s = 0; s < NS; ++s) {
             mbar_init(bar_full + 8 * s, 1);
-            mbar_init(bar_empty + 8 * s, kComputeWarps);
+            mbar_init(bar_empty + 8 * s, 4);  // a warpgroup's warps, or three of these and a commit
+        }
+        for (int g = 0; g < kPagedGroups; ++g) {
+            mbar_init(bar_entry + 8 * g, 1);
+            mbar_init(bar_entry_free + 8 * g, 1);
         }
         mbar_init(bar_q, kComputeThreads);
         for (int w = 0; w < 2; ++w) {
             mbar_init(bar_s + 8 * w, 1);
             mbar_init(bar_p + 8 * w, 128);
             mbar_init(bar_o + 8 * w, 1);
+            mbar_init(bar_piece + 8 * w, 1);
+            mbar_init(bar_piece_free + 8 * w, kComputeWarps + 1);
         }
         mbar_init(bar_drain, 1);
         *timed_out = 0;
@@ -172,7 +250,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
         long long u = 0;
         int tk = 0, bad = 0, flags = 0;
-        for (int b = b0; b < b1; ++b) {
+        CFA_ROLLED for (int b = b0; b < b1; ++b) {
             PagedRequest r = paged_request(p, b);
             if (r.tok0 < 0 || r.n < 0 || r.n > p.T || r.tok0 > p.T - r.n) {
                 bad = 1;
@@ -186,7 +264,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         long long su = u;
         int st = tk;
-        for (int o = 1; o < 32; o <<= 1) {
+        CFA_ROLLED for (int o = 1; o < 32; o <<= 1) {
             const long long a = __shfl_up_sync(~0u, su, o);
             const int c = __shfl_up_sync(~0u, st, o);
             if (lane >= o) su += a, st += c;
@@ -198,12 +276,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         int all_t = 0;
         su -= u;
         st -= tk;
-        for (int w = 0; w < kPagedThreads / 32; ++w) {
+        CFA_ROLLED for (int w = 0; w < kPagedThreads / 32; ++w) {
             if (w < warp) su += sums_u[w], st += sums_t[w];
             all_u += sums_u[w];
             all_t += sums_t[w];
         }
-        for (int b = b0; b < b1; ++b) {
+        CFA_ROLLED for (int b = b0; b < b1; ++b) {
             PagedRequest r = paged_request(p, b);
             if (bad) r.n = 0;
             start[b] = static_cast<int>(su);
@@ -232,7 +310,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     const int u1 = static_cast<int>(min(first + plan.share, static_cast<long long>(plan.units)));
     auto get = [&](int b) { return paged_request(p, b); };
     auto wait = [&](uint32_t bar, uint32_t parity, unsigned site) {
-        mbar_wait_bounded<false>(bar, parity, p.timeout_ns, timed_out, p.status, site);
+        return mbar_try_wait(bar, parity) || paged_wait_slow(bar, parity, p.timeout_ns, timed_out, p.status, site);
     };
     // Stage `n` of the ring's life: slot n % NS, in the n / NS-th pass.
     auto slot_of = [&](uint32_t n) { return n % NS; };
@@ -247,49 +325,56 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     // blocks ahead K0 K1 V0 K2 V1 ... V_n-1).
     auto v_place = [&](bool split, int n, int i) { return !split ? 2 * i + 1 : i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
 
+    if (warp >= kComputeWarps) {
+    registers_for_issue();
     if (warp == kComputeWarps) {
         // -------------------------------------------------------------- load warp
         uint32_t n = 0;
-        const int box = p.box_rows;
-        const int all_rows = p.n_pages * p.n_kv * p.page_size;
-        for (int u = u0; u < u1;) {
-            const PagedPiece x = paged_piece(shape, plan, start, B, u, u1, get);
-            const int nb = x.b1 - x.b0;
-            const bool split = x.rows > kPagedSmallRows && x.rows <= 128;
-            for (int s = 0; s < 2 * nb; ++s, ++n) {
-                bool is_v = s & 1;
-                int i = s >> 1;
-                if (split && s > 0) {
-                    is_v = s == 2 * nb - 1 || (s > 1 && !(s & 1));
-                    i = s == 2 * nb - 1 ? nb - 1 : is_v ? (s - 2) >> 1 : (s + 1) >> 1;
-                }
-                int key0;
-                const int j = x.b0 + i, keys = block_keys(x, j, &key0);
-                const int *table = j < x.prefix_blocks ? p.prefix_table
-                                                       : p.tables + static_cast<size_t>(x.req) * p.width;
-                const int boxes = keys > 0 ? (keys + box - 1) / box : 0;
-                int y = all_rows;  // outside: reads as zeros
-                if (lane < boxes) {
-                    const int key = key0 + lane * box, pg = key / p.page_size;
-                    const int id = __ldcg(table + pg);
-                    if (id >= 0 && id < p.n_pages)
-                        y = (id * p.n_kv + x.h) * p.page_size + key - pg * p.page_size;
-                    else
-                        atomicOr(p.status, kStatusBadPageBit);
-                }
+        const uint32_t units = static_cast<uint32_t>(u1 - u0);
+        if (lane == 0) {
+            uint32_t known = 0;  // groups of entries seen
+            auto entry = [&](uint32_t q) -> const int * {
+                for (; known <= q / 4; ++known)
+                    if (!wait(bar_entry + 8 * (known % kPagedGroups), (known / kPagedGroups) & 1, kSiteStageFull))
+                        return nullptr;
+                return entries + q % (4 * kPagedGroups) * kPagedEntry;
+            };
+            auto stage_in = [&](uint32_t q, bool is_v) {
+                const int *e = entry(q);
+                if (!e) return false;
+                const int boxes = e[8];
                 const uint32_t full = bar_full + 8 * slot_of(n);
-                if (lane == 0) {
-                    if (n >= NS) wait(bar_empty + 8 * slot_of(n), (n / NS - 1) & 1, kSiteStageEmpty);
-                    mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * box * D * 2));
+                if (n >= NS && !wait(bar_empty + 8 * slot_of(n), (n / NS - 1) & 1, kSiteStageEmpty)) return false;
+                mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * p.box_rows * D * 2));
+                const CUtensorMap *tm = is_v ? &tm_v : &tm_k;
+                uint32_t dst = ring + slot_of(n) * S::kStage;
+                CFA_ROLLED for (int i = 0; i < boxes; ++i, dst += p.box_rows * 128) {
+                    const int y = e[i];
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h) tma_load_2d(dst + h * S::kHalf, tm, 64 * h, y, full);
                 }
-                __syncwarp();
-                if (lane < boxes) {
-                    const uint32_t dst = ring + slot_of(n) * S::kStage + lane * box * 128;
-                    for (int h = 0; h < D / 64; ++h)
-                        tma_load_2d(dst + h * S::kHalf, is_v ? &tm_v : &tm_k, 64 * h, y, full);
+                ++n;
+                // the values are a block's second stage: after the last block of a group its entries are free
+                if (is_v && (q % 4 == 3 || q + 1 == units)) mbar_arrive(bar_entry_free + 8 * (q / 4 % kPagedGroups));
+                return true;
+            };
+            for (uint32_t q = 0; q < units;) {
+                const int *e = entry(q);
+                if (!e) break;
+                const int nb = e[9], split = e[10];
+                int t = 0;
+                CFA_ROLLED for (; t < 2 * nb; ++t) {
+                    bool is_v = t & 1;
+                    int i = t >> 1;
+                    if (split && t > 0) {  // keys two blocks ahead of the values
+                        is_v = t == 2 * nb - 1 || (t > 1 && !(t & 1));
+                        i = t == 2 * nb - 1 ? nb - 1 : is_v ? (t - 2) >> 1 : (t + 1) >> 1;
+                    }
+                    if (!stage_in(q + i, is_v)) break;
                 }
+                if (t < 2 * nb) break;
+                q += nb;
             }
-            u += nb;
         }
         if (lane == 0 && *timed_out) {
             // a wait gave up: the copies in flight land before the block ends
@@ -308,21 +393,22 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             uint32_t n = 0, pieces = 0, probs[2] = {0, 0};
             auto scores = [&](int w, uint32_t q, uint32_t stage) {
                 const uint32_t k = ring + slot_of(stage) * S::kStage;
+                CFA_ROLLED for (int h = 0; h < D / 64; ++h) {
+                    const uint64_t qd = umma_smem_desc(q + h * S::kHalf, 16, 1024);
+                    const uint64_t kd = umma_smem_desc(k + h * S::kHalf, 16, 1024);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    umma_bf16(tmem + 128 * w,
-                              umma_smem_desc(q + (ks >> 2) * S::kHalf + (ks & 3) * 32, 16, 1024),
-                              umma_smem_desc(k + (ks >> 2) * S::kHalf + (ks & 3) * 32, 16, 1024),
-                              idesc_s, ks > 0);
+                    for (int ks = 0; ks < 4; ++ks)  // 32 bytes a step
+                        umma_bf16(tmem + 128 * w, qd + 2 * ks, kd + 2 * ks, idesc_s, h > 0 || ks > 0);
+                }
                 umma_commit(bar_s + 8 * w);
             };
             auto values = [&](int w, uint32_t stage, bool accumulate) {
-                const uint32_t v = ring + slot_of(stage) * S::kStage;
+                const uint64_t vd = umma_smem_desc(ring + slot_of(stage) * S::kStage, S::kHalf, 1024);
+                CFA_ROLLED for (int h = 0; h < kPagedKeys / 64; ++h)
 #pragma unroll
-                for (int ks = 0; ks < kPagedKeys / 16; ++ks)
-                    umma_bf16_ts(tmem + 256 + D * w, tmem + 128 * w + 8 * ks,
-                                 umma_smem_desc(v + ks * 2048, S::kHalf, 1024), idesc_o,
-                                 accumulate || ks > 0);
+                    for (int ks = 4 * h; ks < 4 * h + 4; ++ks)  // 16 rows of 128 bytes a step
+                        umma_bf16_ts(tmem + 256 + D * w, tmem + 128 * w + 8 * ks, vd + 128 * ks, idesc_o,
+                                     accumulate || ks > 0);
             };
             auto probs_ready = [&](int w) {
                 wait(bar_p + 8 * w, probs[w]++ & 1, kSiteSoftmaxExchange);
@@ -333,59 +419,44 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 tcgen05_fence_after();
             };
             auto release = [&](uint32_t stage) {  // once the MMAs issued so far have read it
-                mbar_arrive_n(bar_empty + 8 * slot_of(stage), kComputeWarps - 1);
+                mbar_arrive_n(bar_empty + 8 * slot_of(stage), 3);
                 umma_commit(bar_empty + 8 * slot_of(stage));
             };
-            for (int u = u0; u < u1;) {
-                const PagedPiece x = paged_piece(shape, plan, start, B, u, u1, get);
-                const int nb = x.b1 - x.b0;
+            uint32_t k_piece = 0;
+            for (int u = u0; u < u1; ++k_piece) {
+                const uint32_t at = k_piece & 1;
+                if (!wait(bar_piece + 8 * at, (k_piece >> 1) & 1, kSiteStageFull)) break;
+                const PagedPiece *x = reinterpret_cast<const PagedPiece *>(smem + S::kSlots + at * PagedSlot<D>::kBytes);
+                const int nb = x->b1 - x->b0, rows = x->rows;
+                mbar_arrive(bar_piece_free + 8 * at);
                 u += nb;
-                if (x.rows <= kPagedSmallRows) {
+                if (rows <= kPagedSmallRows) {
                     n += 2 * nb;
                     continue;
                 }
                 wait(bar_q, pieces++ & 1, kSiteQExchange);
                 tcgen05_fence_after();
                 const uint32_t q = base + S::kQ;
-                if (x.rows > 128) {
-                    keys_ready(n);
-                    scores(0, q, n);
-                    scores(1, q + S::kQTile, n);
-                    release(n);
-                    for (int j = 0; j < nb; ++j) {
-                        const uint32_t v = n + 2 * j + 1, k = v + 1;
-                        keys_ready(v);
-                        probs_ready(0);
-                        values(0, v, j > 0);
-                        if (j + 1 < nb) {
-                            keys_ready(k);
-                            scores(0, q, k);
-                        }
-                        probs_ready(1);
-                        values(1, v, j > 0);
-                        release(v);
-                        if (j + 1 < nb) {
-                            scores(1, q + S::kQTile, k);
-                            release(k);
-                        }
-                    }
-                } else {
-                    for (int j = 0; j < min(nb, 2); ++j) {
-                        keys_ready(n + j);
-                        scores(j, q, n + j);
-                        release(n + j);
-                    }
-                    for (int j = 0; j < nb; ++j) {
-                        const uint32_t v = n + v_place(true, nb, j);
-                        keys_ready(v);
-                        probs_ready(j & 1);
-                        values(j & 1, v, j > 1);
-                        release(v);
-                        if (j + 2 < nb) {
-                            keys_ready(v + 1);
-                            scores(j & 1, q, v + 1);
-                            release(v + 1);
-                        }
+                // steps: block j of the keys with query tile w (two tiles), or with the one
+                // tile in the scores and outputs of half w = j mod 2
+                const bool pair = rows > 128;
+                CFA_ROLLED for (int w = 0; w < (pair ? 2 : min(nb, 2)); ++w) {
+                    const uint32_t k = n + (pair ? 0 : w);
+                    keys_ready(k);
+                    scores(w, q + (pair ? w * S::kQTile : 0), k);
+                    if (!pair || w) release(k);
+                }
+                CFA_ROLLED for (int t = 0; t < (pair ? 2 * nb : nb); ++t) {
+                    const int j = pair ? t >> 1 : t, w = t & 1;
+                    const uint32_t v = n + v_place(!pair, nb, j);
+                    keys_ready(v);
+                    probs_ready(w);
+                    values(w, v, pair ? j > 0 : j > 1);
+                    if (!pair || w) release(v);
+                    if (j + (pair ? 1 : 2) < nb) {
+                        keys_ready(v + 1);
+                        scores(w, q + (pair ? w * S::kQTile : 0), v + 1);
+                        if (!pair || w) release(v + 1);
                     }
                 }
                 umma_commit(bar_o);
@@ -401,13 +472,116 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
         }
         __syncwarp();
+    } else if (warp == kComputeWarps + 2) {
+        // ----------------------------------------------------------- address warp
+        // Finds the cache rows of the run's blocks, four at a time (8 lanes each, a lane a
+        // box), ahead of the load warp: a table entry takes as long to arrive as the keys.
+        const int box = p.box_rows, sub = lane >> 3, i = lane & 7;
+        const int all_rows = p.n_pages * p.n_kv * p.page_size;
+        PagedPiece x;
+        int u = u0, at = u0;  // the next piece, the next block
+        x.b0 = x.b1 = 0;
+        for (uint32_t g = 0; at < u1; ++g) {
+            const int *id_at = nullptr;
+            int boxes = 0, add = 0, nb = 0, split = 0;
+            bool mine = false;
+            CFA_ROLLED for (int k = 0; k < 4 && at < u1; ++k, ++at) {
+                if (at == u) {
+                    x = paged_piece(shape, plan, start, B, u, u1, get);
+                    u += x.b1 - x.b0;
+                }
+                if (sub == k) {
+                    int key0;
+                    const int j = x.b1 - (u - at), keys = block_keys(x, j, &key0);
+                    boxes = keys > 0 ? (keys + box - 1) / box : 0;
+                    const int key = key0 + i * box, pg = key / p.page_size;
+                    if (i < boxes)
+                        id_at = (j < x.prefix_blocks ? p.prefix_table
+                                                     : p.tables + static_cast<size_t>(x.req) * p.width) + pg;
+                    add = x.h * p.page_size + key - pg * p.page_size;
+                    nb = x.b1 - x.b0;
+                    split = x.rows > kPagedSmallRows && x.rows <= 128;
+                    mine = true;
+                }
+            }
+            int y = all_rows;  // outside: reads as zeros
+            if (id_at) {
+                const int id = __ldcg(id_at);
+                if (id >= 0 && id < p.n_pages) y = id * p.n_kv * p.page_size + add;
+                else atomicOr(p.status, kStatusBadPageBit);
+            }
+            if (__any_sync(~0u, g >= kPagedGroups && !wait(bar_entry_free + 8 * (g % kPagedGroups),
+                                                           (g / kPagedGroups - 1) & 1, kSiteStageEmpty)))
+                break;
+            int *e = entries + (4 * (g % kPagedGroups) + sub) * kPagedEntry;
+            if (mine) {
+                e[i] = y;
+                if (i == 0) e[8] = boxes, e[9] = nb, e[10] = split;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_entry + 8 * (g % kPagedGroups));
+        }
+    } else {
+        // -------------------------------------------------------------- prep warp
+        // Lays the next piece out: its numbers, where each row's query and result lie, and
+        // the queries themselves where they are few.
+        uint32_t k = 0;
+        for (int u = u0; u < u1; ++k) {
+            const PagedPiece x = paged_piece(shape, plan, start, B, u, u1, get);
+            u += x.b1 - x.b0;
+            if (__any_sync(~0u, k >= 2 && !wait(bar_piece_free + 8 * (k & 1), (k / 2 - 1) & 1, kSiteStageEmpty)))
+                break;
+            uint8_t *slot = smem + S::kSlots + (k & 1) * PagedSlot<D>::kBytes;
+            if (lane == 0) *reinterpret_cast<PagedPiece *>(slot) = x;
+            int2 *row_at = reinterpret_cast<int2 *>(slot + PagedSlot<D>::kRow);
+            CFA_ROLLED for (int r = lane; r < x.rows; r += 32) {
+                const int i = (x.row0 + r) / G;
+                int t = x.r.tok0 + i;
+                if (x.req < 0) {
+                    const int b = paged_find(stok, B, i);
+                    t = __ldcg(p.cu + b) + i - stok[b];
+                }
+                row_at[r] = make_int2(t, t * p.n_heads + x.h * G + (x.row0 + r) - i * G);
+            }
+            __syncwarp();
+            if (x.rows <= kPagedSmallRows) {
+#pragma unroll
+                for (int c = lane; c < 16 * (D / 8); c += 32) {
+                    const int r = c / (D / 8), ch = c % (D / 8);
+                    uint8_t *dst = slot + PagedSlot<D>::kQ + (ch >> 3) * 2048 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                    if (r < x.rows) {
+                        const int2 at = row_at[r];
+                        cp_async_16(smem_addr(dst), p.q + at.x * p.q_stride + (at.y - at.x * p.n_heads) * D + 8 * ch);
+                    } else {
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                cp_async_wait_all();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_piece + 8 * (k & 1));
+        }
+    }
     } else {
         // ---------------------------------------------------------- compute warps
+        registers_for_compute();
         const int wg = warp >> 2;
         uint32_t n = 0, scored = 0, done = 0;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lanes of this warp
-        for (int u = u0; u < u1;) {
-            const PagedPiece x = paged_piece(shape, plan, start, B, u, u1, get);
+        uint32_t k_piece = 0;
+        for (int u = u0; u < u1; ++k_piece) {
+            // one thread's word for all of them: where its wait gave up, no warp goes on alone
+            const bool there = wait(bar_piece + 8 * (k_piece & 1), (k_piece >> 1) & 1, kSiteStageFull);
+            if (tid == 0) misc[2] = there;
+            compute_bar<kComputeThreads>();
+            if (!misc[2]) break;
+            const uint8_t *slot = smem + S::kSlots + (k_piece & 1) * PagedSlot<D>::kBytes;
+            const PagedPiece &x = *reinterpret_cast<const PagedPiece *>(slot);
+            const int2 *row_at = reinterpret_cast<const int2 *>(slot + PagedSlot<D>::kRow);
+            auto piece_done = [&]() {
+                compute_bar<kComputeThreads>();  // the scratch and the query tiles are free again
+                if (lane == 0) mbar_arrive(bar_piece_free + 8 * (k_piece & 1));
+            };
             const int nb = x.b1 - x.b0;
             u += nb;
             const bool final = paged_final(shape, x);
@@ -418,17 +592,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                           x.req < 0 ? 0 : stok[x.req], run);
             float *rec_o = p.rec_o + rec * D;
             float2 *rec_ml = p.rec_ml + rec;
-            // where each row's query and result lie
-            if (tid < x.rows) {
-                const int r = x.row0 + tid, i = r / G, g = r - i * G;
-                int t = x.r.tok0 + i;
-                if (x.req < 0) {
-                    const int b = paged_find(stok, B, i);
-                    t = __ldcg(p.cu + b) + i - stok[b];
-                }
-                row_at[tid] = make_int2(t, t * p.n_heads + x.h * G + g);
-            }
-            compute_bar<kComputeThreads>();
             auto query = [&](int row) {
                 const int2 at = row_at[row];
                 return p.q + at.x * p.q_stride + (at.y - at.x * p.n_heads) * D;
@@ -438,18 +601,15 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             };
 
             if (x.rows <= kPagedSmallRows) {
-                // ---- mma.sync: this warp's 16 keys of every block
-                const int r0 = lane >> 2, c2 = (lane & 3) * 2;
+                // ---- mma.sync: this warp's 32 keys of every other block
+                const int r0 = lane >> 2, c2 = (lane & 3) * 2, kw = 32 * (warp & 3);
                 uint32_t q[D / 16][4];
                 {
-                    const uint16_t *qa = r0 < x.rows ? query(r0) : nullptr;
-                    const uint16_t *qb = r0 + 8 < x.rows ? query(r0 + 8) : nullptr;
+                    const uint32_t qs = smem_addr(slot + PagedSlot<D>::kQ) + (lane & 15) * 128;
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        q[k][0] = qa ? *reinterpret_cast<const uint32_t *>(qa + 16 * k + c2) : 0u;
-                        q[k][1] = qb ? *reinterpret_cast<const uint32_t *>(qb + 16 * k + c2) : 0u;
-                        q[k][2] = qa ? *reinterpret_cast<const uint32_t *>(qa + 16 * k + 8 + c2) : 0u;
-                        q[k][3] = qb ? *reinterpret_cast<const uint32_t *>(qb + 16 * k + 8 + c2) : 0u;
+                        const uint32_t c = 2 * k + (lane >> 4);
+                        ldmatrix_x4(q[k], qs + (c >> 3) * 2048 + (((c & 7) ^ (lane & 7)) << 4));
                     }
                 }
                 float o[D / 8][4];
@@ -459,35 +619,40 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 // own keys that rows r0 and r0 + 8 see
                 const int see0 = paged_visible(x.r, (x.row0 + r0) / G);
                 const int see1 = paged_visible(x.r, (x.row0 + r0 + 8) / G);
-                const uint32_t kkey = 16 * warp + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
-                const uint32_t vkey = 16 * warp + (lane & 15), vc = lane >> 4;
-                for (int j = 0; j < nb; ++j, n += 2) {
+                const uint32_t kkey = kw + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+                const uint32_t vkey = kw + (lane & 15), vc = lane >> 4;
+                CFA_ROLLED for (int j = wg; j < nb; j += 2) {
+                    const uint32_t nk = n + 2 * j, nv = nk + 1;
                     int key0;
-                    const int keys = block_keys(x, x.b0 + j, &key0) - 16 * warp;
-                    key0 += 16 * warp;
-                    wait_full(n);
-                    float s[2][4] = {};
+                    const int keys = block_keys(x, x.b0 + j, &key0) - kw;
+                    key0 += kw;
+                    wait_full(nk);
+                    float s[4][4] = {};
                     if (keys > 0) {
-                        const uint32_t st = ring + slot_of(n) * S::kStage + kkey * 128;
+                        const uint32_t st = ring + slot_of(nk) * S::kStage + kkey * 128;
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
-                            uint32_t b[4];
+                            uint32_t b[4], d[4];
                             const uint32_t c = 2 * k + kc;
-                            ldmatrix_x4(b, st + (c >> 3) * S::kHalf + (((c & 7) ^ (kkey & 7)) << 4));
+                            const uint32_t at = st + (c >> 3) * S::kHalf + (((c & 7) ^ (kkey & 7)) << 4);
+                            ldmatrix_x4(b, at);
+                            ldmatrix_x4(d, at + 16 * 128);
                             mma_16x8x16(s[0], q[k], b[0], b[1]);
                             mma_16x8x16(s[1], q[k], b[2], b[3]);
+                            mma_16x8x16(s[2], q[k], d[0], d[1]);
+                            mma_16x8x16(s[3], q[k], d[2], d[3]);
                         }
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_empty + 8 * slot_of(n));
-                    uint32_t pr[4];
+                    if (lane == 0) mbar_arrive(bar_empty + 8 * slot_of(nk));
+                    uint32_t pr[2][4];
                     if (keys > 0) {
                         const bool own = x.b0 + j >= x.prefix_blocks;
                         const int lim0 = own ? min(keys, see0 - key0) : keys;
                         const int lim1 = own ? min(keys, see1 - key0) : keys;
                         float a0 = -INFINITY, a1 = -INFINITY;
 #pragma unroll
-                        for (int t = 0; t < 2; ++t)
+                        for (int t = 0; t < 4; ++t)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const int col = 8 * t + c2 + e;
@@ -515,7 +680,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                             m1 = n1;
                         }
 #pragma unroll
-                        for (int t = 0; t < 2; ++t)
+                        for (int t = 0; t < 4; ++t)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 s[t][e] = fast_exp2(s[t][e] - f0);
@@ -523,31 +688,46 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                 l0 += s[t][e];
                                 l1 += s[t][2 + e];
                             }
-                        pr[0] = pack2_bf16(s[0][0], s[0][1]);
-                        pr[1] = pack2_bf16(s[0][2], s[0][3]);
-                        pr[2] = pack2_bf16(s[1][0], s[1][1]);
-                        pr[3] = pack2_bf16(s[1][2], s[1][3]);
-                    }
-                    wait_full(n + 1);
-                    if (keys > 0) {
-                        // rows past the keys may hold anything, and 0 times NaN is NaN
-                        auto keep = [&](int k) {
-                            return (k < keys ? 0xffffu : 0u) | (k + 1 < keys ? 0xffff0000u : 0u);
-                        };
-                        const uint32_t keep0 = keep(c2), keep1 = keep(c2 + 8);
-                        const uint32_t st = ring + slot_of(n + 1) * S::kStage + vkey * 128;
 #pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            uint32_t b[4];
-                            const uint32_t c = 2 * i + vc;
-                            ldmatrix_x4_trans(b, st + (c >> 3) * S::kHalf + (((c & 7) ^ (vkey & 7)) << 4));
-                            mma_16x8x16(o[2 * i], pr, b[0] & keep0, b[1] & keep1);
-                            mma_16x8x16(o[2 * i + 1], pr, b[2] & keep0, b[3] & keep1);
+                        for (int t = 0; t < 2; ++t) {
+                            pr[t][0] = pack2_bf16_cvt(s[2 * t][0], s[2 * t][1]);
+                            pr[t][1] = pack2_bf16_cvt(s[2 * t][2], s[2 * t][3]);
+                            pr[t][2] = pack2_bf16_cvt(s[2 * t + 1][0], s[2 * t + 1][1]);
+                            pr[t][3] = pack2_bf16_cvt(s[2 * t + 1][2], s[2 * t + 1][3]);
                         }
                     }
+                    wait_full(nv);
+                    if (keys > 0) {
+                        const uint32_t st = ring + slot_of(nv) * S::kStage + vkey * 128;
+                        auto values = [&](auto whole) {
+                            // rows past the keys may hold anything, and 0 times NaN is NaN
+                            auto keep = [&](int k) {
+                                return (k < keys ? 0xffffu : 0u) | (k + 1 < keys ? 0xffff0000u : 0u);
+                            };
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                uint32_t b[4], d[4];
+                                const uint32_t c = 2 * i + vc;
+                                const uint32_t at = st + (c >> 3) * S::kHalf + (((c & 7) ^ (vkey & 7)) << 4);
+                                ldmatrix_x4_trans(b, at);
+                                ldmatrix_x4_trans(d, at + 16 * 128);
+                                if constexpr (!decltype(whole)::value) {
+                                    b[0] &= keep(c2); b[1] &= keep(c2 + 8); b[2] &= keep(c2); b[3] &= keep(c2 + 8);
+                                    d[0] &= keep(c2 + 16); d[1] &= keep(c2 + 24); d[2] &= keep(c2 + 16); d[3] &= keep(c2 + 24);
+                                }
+                                mma_16x8x16(o[2 * i], pr[0], b[0], b[1]);
+                                mma_16x8x16(o[2 * i + 1], pr[0], b[2], b[3]);
+                                mma_16x8x16(o[2 * i], pr[1], d[0], d[1]);
+                                mma_16x8x16(o[2 * i + 1], pr[1], d[2], d[3]);
+                            }
+                        };
+                        if (keys >= 32) values(PagedFlag<true>{});
+                        else values(PagedFlag<false>{});
+                    }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_empty + 8 * slot_of(n + 1));
+                    if (lane == 0) mbar_arrive(bar_empty + 8 * slot_of(nv));
                 }
+                n += 2 * nb;
                 // ---- join the eight warps
 #pragma unroll
                 for (int d = 1; d < 4; d <<= 1) {
@@ -568,7 +748,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         *reinterpret_cast<float2 *>(scr + (warp * 16 + r0 + 8) * D + 8 * i + c2) = make_float2(o[i][2], o[i][3]);
                 }
                 compute_bar<kComputeThreads>();
-                for (int i = tid; i < x.rows * (D / 4); i += kComputeThreads) {
+                CFA_ROLLED for (int i = tid; i < x.rows * (D / 4); i += kComputeThreads) {
                     // records are chunk major, results row major
                     const int row = final ? i / (D / 4) : i % x.rows, c = final ? i % (D / 4) : i / x.rows;
                     float m = -INFINITY;
@@ -595,18 +775,27 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         if (c == 0) rec_ml[row] = make_float2(m, l);
                     }
                 }
-                compute_bar<kComputeThreads>();
+                piece_done();
                 continue;
             }
 
             // ---- tcgen05
             const bool split = x.rows <= 128;
-            for (int i = tid; i < (split ? 128 : 256) * (D / 8); i += kComputeThreads) {
-                const int row = i / (D / 8), c = i % (D / 8);
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (row < x.rows) v = *reinterpret_cast<const uint4 *>(query(row) + 8 * c);
-                *reinterpret_cast<uint4 *>(smem + S::kQ + (row >> 7) * S::kQTile + (c >> 3) * S::kHalf +
-                                           (row & 127) * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+            CFA_ROLLED for (int t = 0; t < (split ? 1 : 2); ++t) {
+                constexpr int kPer = 128 * (D / 8) / kComputeThreads;
+                uint4 v[kPer];
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) {  // all the loads before the first store
+                    const int i = tid + k * kComputeThreads, row = 128 * t + i / (D / 8), c = i % (D / 8);
+                    v[k] = make_uint4(0u, 0u, 0u, 0u);
+                    if (row < x.rows) v[k] = *reinterpret_cast<const uint4 *>(query(row) + 8 * c);
+                }
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) {
+                    const int i = tid + k * kComputeThreads, row = i / (D / 8), c = i % (D / 8);
+                    *reinterpret_cast<uint4 *>(smem + S::kQ + t * S::kQTile + (c >> 3) * S::kHalf + row * 128 +
+                                               (((c & 7) ^ (row & 7)) << 4)) = v[k];
+                }
             }
             fence_proxy_async_smem();
             tcgen05_fence_before();
@@ -619,27 +808,39 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             const uint32_t t_s = tmem + lanes + 128 * wg, t_o = tmem + lanes + 256 + D * wg;
             float m = -INFINITY, l = 0.f;
             bool begun = false;
-            for (int j = split ? wg : 0; j < nb; j += split ? 2 : 1) {
+            CFA_ROLLED for (int j = split ? wg : 0; j < nb; j += split ? 2 : 1) {
                 int key0;
                 const int keys = block_keys(x, x.b0 + j, &key0);
                 const int lim = x.b0 + j < x.prefix_blocks ? keys : min(keys, see - key0);
                 wait(bar_s + 8 * wg, scored++ & 1, kSiteKvExchange);
                 tcgen05_fence_after();
                 if (warp_live) {
-                    uint32_t s[128];
+                    // two passes over the scores in TMEM, 32 columns at a time: keeping a row's 128 in
+                    // registers spills
+                    uint32_t s[2][32];
+                    if (!__all_sync(~0u, lim >= kPagedKeys)) {  // the hidden scores become -inf
+                        CFA_ROLLED for (int c = 0; c < kPagedKeys; c += 32) {
+                            tmem_ld_x32(t_s + c, s[0]);
+                            tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld_x32(t_s + 32 * c, s + 32 * c);
-                    tmem_wait_ld();
-                    if (!__all_sync(~0u, lim >= kPagedKeys)) {
-#pragma unroll
-                        for (int c = 0; c < 128; ++c) s[c] = c < lim ? s[c] : 0xff800000u;
+                            for (int e = 0; e < 32; ++e) s[0][e] = c + e < lim ? s[0][e] : 0xff800000u;
+                            tmem_st_x16(t_s + c, s[0]);
+                            tmem_st_x16(t_s + c + 16, s[0] + 16);
+                        }
+                        tmem_wait_st();
                     }
                     float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    tmem_ld_x32(t_s, s[0]);
 #pragma unroll
-                    for (int c = 0; c < 128; c += 8)
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_wait_ld();
+                        if (c < 3) tmem_ld_x32(t_s + 32 * (c + 1), s[(c + 1) & 1]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            a[e] = fmaxf(a[e], fmaxf(__uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1])));
+                        for (int e = 0; e < 32; e += 2)
+                            a[(e >> 1) & 3] = fmaxf(fmaxf(a[(e >> 1) & 3], __uint_as_float(s[c & 1][e])),
+                                                    __uint_as_float(s[c & 1][e + 1]));
+                    }
+                    tmem_ld_x32(t_s, s[0]);
                     const float top = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * p.scale_log2;
                     if (__any_sync(~0u, top > m + 8.f || (m == -INFINITY && top > m))) {
                         // rescale to the new maximum (m = -inf: nothing is there yet)
@@ -661,20 +862,26 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         }
                     }
                     const float f = m == -INFINITY ? 0.f : -m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint64_t scale2 = pair_f32(p.scale_log2, p.scale_log2), f2 = pair_f32(f, f);
+                    uint64_t sum[2] = {0, 0};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t w[16];
+                        tmem_wait_ld();
+                        if (c < 3) tmem_ld_x32(t_s + 32 * (c + 1), s[(c + 1) & 1]);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const float x0 = fast_exp2(fmaf(__uint_as_float(s[32 * c + 2 * e]), p.scale_log2, f));
-                            const float x1 = fast_exp2(fmaf(__uint_as_float(s[32 * c + 2 * e + 1]), p.scale_log2, f));
-                            sum[e & 3] += x0 + x1;
-                            w[e] = pack2_bf16(x0, x1);
+                            const float2 y = unpair_f32(fma_f32x2(
+                                pair_f32(__uint_as_float(s[c & 1][2 * e]), __uint_as_float(s[c & 1][2 * e + 1])),
+                                scale2, f2));
+                            const float x0 = fast_exp2(y.x), x1 = fast_exp2(y.y);
+                            sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(x0, x1));
+                            w[e] = pack2_bf16_cvt(x0, x1);
                         }
                         tmem_st_x16(t_s + 16 * c, w);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    const float2 both_sums = unpair_f32(add_f32x2(sum[0], sum[1]));
+                    l += both_sums.x + both_sums.y;
                     tmem_wait_st();
                 }
                 begun = true;
@@ -683,7 +890,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const uint32_t vn = n + v_place(split, nb, j);
                     wait_full(vn);
                     const int z = max(keys, 0);
-                    for (int i = tid & 127; i < (kPagedKeys - z) * (D / 8); i += 128) {
+                    CFA_ROLLED for (int i = tid & 127; i < (kPagedKeys - z) * (D / 8); i += 128) {
                         const int r = z + i / (D / 8), c = i % (D / 8);
                         *reinterpret_cast<uint4 *>(smem + S::kRing + slot_of(vn) * S::kStage + (c >> 3) * S::kHalf +
                                                    r * 128 + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
@@ -769,7 +976,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 }
             }
             tcgen05_fence_before();
-            compute_bar<kComputeThreads>();  // row_at, ml and the query tiles are free again
+            piece_done();
         }
     }
     tcgen05_fence_before();

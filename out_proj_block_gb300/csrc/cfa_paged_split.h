@@ -22,8 +22,10 @@
 
 #ifdef __CUDACC__
 #define CFA_HD __host__ __device__ __forceinline__
+#define CFA_ROLLED _Pragma("unroll 1")  // a loop that is not worth the instruction cache
 #else
 #define CFA_HD inline
+#define CFA_ROLLED
 #endif
 
 namespace cfa {
@@ -87,7 +89,7 @@ CFA_HD long long paged_request_units(const PagedShape &s, const PagedRequest &r)
     if (r.n == 0) return 0;
     if (!paged_alone(s, r.n)) return static_cast<long long>(s.nkv) * paged_cdiv(r.len, kPagedKeys);
     long long u = 0;
-    for (int t = 0; t * kPagedTile < r.n * s.G; ++t) u += paged_alone_blocks(s, r, t);
+    CFA_ROLLED for (int t = 0; t * kPagedTile < r.n * s.G; ++t) u += paged_alone_blocks(s, r, t);
     return u * s.nkv;
 }
 
@@ -110,7 +112,7 @@ CFA_HD PagedPlan paged_plan(const PagedShape &s, long long own_units, int shared
 // requests without units share their start with the next one and are passed over.
 CFA_HD int paged_find(const int *a, int B, int x) {
     int lo = 0, hi = B;
-    while (hi - lo > 1) {
+    CFA_ROLLED while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (a[mid] <= x) lo = mid; else hi = mid;
     }
@@ -149,7 +151,7 @@ CFA_HD PagedPiece paged_piece(const PagedShape &s, const PagedPlan &p, const int
             x.own_limit = x.r.len;
         } else {
             int t = 0, n = paged_alone_blocks(s, x.r, 0);
-            while (rem >= n) {
+            CFA_ROLLED while (rem >= n) {
                 rem -= n;
                 n = paged_alone_blocks(s, x.r, ++t);
             }
