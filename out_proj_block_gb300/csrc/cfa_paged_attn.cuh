@@ -131,6 +131,16 @@ __device__ __forceinline__ uint32_t pack2_bf16_cvt(float lo, float hi) {
     return r;
 }
 
+// True in one lane of the warp, the same one every time. A warp whose lanes all run an
+// issue loop keeps its operands in uniform registers; a loop inside "if (lane == 0)" moves
+// them there for every instruction (measured: 100 clocks a product, 250 a copy).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(~0u, v, 0); }
+
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
@@ -312,6 +322,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     auto wait = [&](uint32_t bar, uint32_t parity, unsigned site) {
         return mbar_try_wait(bar, parity) || paged_wait_slow(bar, parity, p.timeout_ns, timed_out, p.status, site);
     };
+    // The same for a warp as a whole.
+    auto wait_warp = [&](uint32_t bar, uint32_t parity, unsigned site) {
+        return __all_sync(~0u, mbar_try_wait(bar, parity)) ||
+               __all_sync(~0u, paged_wait_slow(bar, parity, p.timeout_ns, timed_out, p.status, site));
+    };
     // Stage `n` of the ring's life: slot n % NS, in the n / NS-th pass.
     auto slot_of = [&](uint32_t n) { return n % NS; };
     auto wait_full = [&](uint32_t n) { wait(bar_full + 8 * slot_of(n), (n / NS) & 1, kSiteStageFull); };
@@ -329,52 +344,52 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     registers_for_issue();
     if (warp == kComputeWarps) {
         // -------------------------------------------------------------- load warp
-        uint32_t n = 0;
-        const uint32_t units = static_cast<uint32_t>(u1 - u0);
-        if (lane == 0) {
-            uint32_t known = 0;  // groups of entries seen
-            auto entry = [&](uint32_t q) -> const int * {
-                for (; known <= q / 4; ++known)
-                    if (!wait(bar_entry + 8 * (known % kPagedGroups), (known / kPagedGroups) & 1, kSiteStageFull))
-                        return nullptr;
-                return entries + q % (4 * kPagedGroups) * kPagedEntry;
+        uint32_t n = 0, known = 0;  // stages issued, groups of entries seen
+        const uint32_t units = static_cast<uint32_t>(uniform(u1 - u0));
+        const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128;
+        for (uint32_t q = 0; q < units;) {
+            bool ok = true;
+            auto entry = [&](uint32_t e) {
+                for (; known <= e / 4 && ok; ++known)
+                    ok = wait_warp(bar_entry + 8 * (known % kPagedGroups), (known / kPagedGroups) & 1, kSiteStageFull);
+                return entries + e % (4 * kPagedGroups) * kPagedEntry;
             };
-            auto stage_in = [&](uint32_t q, bool is_v) {
-                const int *e = entry(q);
-                if (!e) return false;
-                const int boxes = e[8];
+            const int *first_entry = entry(q);
+            if (!ok) break;
+            const int nb = uniform(first_entry[9]), split = uniform(first_entry[10]);
+            CFA_ROLLED for (int t = 0; t < 2 * nb; ++t) {
+                bool is_v = t & 1;
+                int i = t >> 1;
+                if (split && t > 0) {  // keys two blocks ahead of the values
+                    is_v = t == 2 * nb - 1 || (t > 1 && !(t & 1));
+                    i = t == 2 * nb - 1 ? nb - 1 : is_v ? (t - 2) >> 1 : (t + 1) >> 1;
+                }
+                const uint32_t at = q + i;
+                const int *e = entry(at);
                 const uint32_t full = bar_full + 8 * slot_of(n);
-                if (n >= NS && !wait(bar_empty + 8 * slot_of(n), (n / NS - 1) & 1, kSiteStageEmpty)) return false;
-                mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * p.box_rows * D * 2));
-                const CUtensorMap *tm = is_v ? &tm_v : &tm_k;
-                uint32_t dst = ring + slot_of(n) * S::kStage;
-                CFA_ROLLED for (int i = 0; i < boxes; ++i, dst += p.box_rows * 128) {
-                    const int y = e[i];
+                if (ok && n >= NS) ok = wait_warp(bar_empty + 8 * slot_of(n), (n / NS - 1) & 1, kSiteStageEmpty);
+                if (!ok) break;
+                const int boxes = uniform(e[8]);
+                const uint32_t dst = ring + slot_of(n) * S::kStage;
+                if (elect_one()) mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes) * box_bytes * (D / 64));
+                __syncwarp();
+                CFA_ROLLED for (int k = 0; k < boxes; ++k) {
+                    const int y = uniform(e[k]);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int h = 0; h < D / 64; ++h) tma_load_2d(dst + h * S::kHalf, tm, 64 * h, y, full);
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_load_2d(dst + k * box_bytes + h * S::kHalf, is_v ? &tm_v : &tm_k, 64 * h, y, full);
+                    }
+                    __syncwarp();
                 }
                 ++n;
                 // the values are a block's second stage: after the last block of a group its entries are free
-                if (is_v && (q % 4 == 3 || q + 1 == units)) mbar_arrive(bar_entry_free + 8 * (q / 4 % kPagedGroups));
-                return true;
-            };
-            for (uint32_t q = 0; q < units;) {
-                const int *e = entry(q);
-                if (!e) break;
-                const int nb = e[9], split = e[10];
-                int t = 0;
-                CFA_ROLLED for (; t < 2 * nb; ++t) {
-                    bool is_v = t & 1;
-                    int i = t >> 1;
-                    if (split && t > 0) {  // keys two blocks ahead of the values
-                        is_v = t == 2 * nb - 1 || (t > 1 && !(t & 1));
-                        i = t == 2 * nb - 1 ? nb - 1 : is_v ? (t - 2) >> 1 : (t + 1) >> 1;
-                    }
-                    if (!stage_in(q + i, is_v)) break;
-                }
-                if (t < 2 * nb) break;
-                q += nb;
+                if (is_v && (at % 4 == 3 || at + 1 == units) && elect_one())
+                    mbar_arrive(bar_entry_free + 8 * (at / 4 % kPagedGroups));
+                __syncwarp();
             }
+            if (!ok) break;
+            q += nb;
         }
         if (lane == 0 && *timed_out) {
             // a wait gave up: the copies in flight land before the block ends
@@ -387,54 +402,63 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         __syncwarp();
     } else if (warp == kComputeWarps + 1) {
         // --------------------------------------------------------------- MMA warp
-        if (lane == 0) {
-            const uint32_t idesc_s = umma_idesc_bf16(128, kPagedKeys, false, false);
-            const uint32_t idesc_o = umma_idesc_bf16(128, D, false, true);
-            uint32_t n = 0, pieces = 0, probs[2] = {0, 0};
+        {
+            constexpr uint32_t idesc_s = umma_idesc_bf16(128, kPagedKeys, false, false);
+            constexpr uint32_t idesc_o = umma_idesc_bf16(128, D, false, true);
+            const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
+            const int end = uniform(u1);
+            uint32_t n = 0, pieces = 0, probs0 = 0, probs1 = 0;
             auto scores = [&](int w, uint32_t q, uint32_t stage) {
                 const uint32_t k = ring + slot_of(stage) * S::kStage;
-                CFA_ROLLED for (int h = 0; h < D / 64; ++h) {
-                    const uint64_t qd = umma_smem_desc(q + h * S::kHalf, 16, 1024);
-                    const uint64_t kd = umma_smem_desc(k + h * S::kHalf, 16, 1024);
+                if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)  // 32 bytes a step
-                        umma_bf16(tmem + 128 * w, qd + 2 * ks, kd + 2 * ks, idesc_s, h > 0 || ks > 0);
+                    for (int ks = 0; ks < D / 16; ++ks)  // 32 bytes a step
+                        umma_bf16(tm + 128 * w, umma_smem_desc(q + (ks >> 2) * S::kHalf, 16, 1024) + 2 * (ks & 3),
+                                  umma_smem_desc(k + (ks >> 2) * S::kHalf, 16, 1024) + 2 * (ks & 3), idesc_s, ks > 0);
+                    umma_commit(bar_s + 8 * w);
                 }
-                umma_commit(bar_s + 8 * w);
+                __syncwarp();
             };
             auto values = [&](int w, uint32_t stage, bool accumulate) {
                 const uint64_t vd = umma_smem_desc(ring + slot_of(stage) * S::kStage, S::kHalf, 1024);
-                CFA_ROLLED for (int h = 0; h < kPagedKeys / 64; ++h)
+                if (elect_one()) {
 #pragma unroll
-                    for (int ks = 4 * h; ks < 4 * h + 4; ++ks)  // 16 rows of 128 bytes a step
-                        umma_bf16_ts(tmem + 256 + D * w, tmem + 128 * w + 8 * ks, vd + 128 * ks, idesc_o,
+                    for (int ks = 0; ks < kPagedKeys / 16; ++ks)  // 16 rows of 128 bytes a step
+                        umma_bf16_ts(tm + 256 + D * w, tm + 128 * w + 8 * ks, vd + 128 * ks, idesc_o,
                                      accumulate || ks > 0);
+                }
+                __syncwarp();
             };
             auto probs_ready = [&](int w) {
-                wait(bar_p + 8 * w, probs[w]++ & 1, kSiteSoftmaxExchange);
+                const uint32_t c = w ? probs1++ : probs0++;
+                wait_warp(bar_p + 8 * w, c & 1, kSiteSoftmaxExchange);
                 tcgen05_fence_after();
             };
             auto keys_ready = [&](uint32_t stage) {
-                wait_full(stage);
+                wait_warp(bar_full + 8 * slot_of(stage), (stage / NS) & 1, kSiteStageFull);
                 tcgen05_fence_after();
             };
             auto release = [&](uint32_t stage) {  // once the MMAs issued so far have read it
-                mbar_arrive_n(bar_empty + 8 * slot_of(stage), 3);
-                umma_commit(bar_empty + 8 * slot_of(stage));
+                if (elect_one()) {
+                    mbar_arrive_n(bar_empty + 8 * slot_of(stage), 3);
+                    umma_commit(bar_empty + 8 * slot_of(stage));
+                }
+                __syncwarp();
             };
             uint32_t k_piece = 0;
-            for (int u = u0; u < u1; ++k_piece) {
+            for (int u = uniform(u0); u < end; ++k_piece) {
                 const uint32_t at = k_piece & 1;
-                if (!wait(bar_piece + 8 * at, (k_piece >> 1) & 1, kSiteStageFull)) break;
+                if (!wait_warp(bar_piece + 8 * at, (k_piece >> 1) & 1, kSiteStageFull)) break;
                 const PagedPiece *x = reinterpret_cast<const PagedPiece *>(smem + S::kSlots + at * PagedSlot<D>::kBytes);
-                const int nb = x->b1 - x->b0, rows = x->rows;
-                mbar_arrive(bar_piece_free + 8 * at);
+                const int nb = uniform(x->b1 - x->b0), rows = uniform(x->rows);
+                __syncwarp();
+                if (elect_one()) mbar_arrive(bar_piece_free + 8 * at);
                 u += nb;
                 if (rows <= kPagedSmallRows) {
                     n += 2 * nb;
                     continue;
                 }
-                wait(bar_q, pieces++ & 1, kSiteQExchange);
+                wait_warp(bar_q, pieces++ & 1, kSiteQExchange);
                 tcgen05_fence_after();
                 const uint32_t q = base + S::kQ;
                 // steps: block j of the keys with query tile w (two tiles), or with the one
@@ -459,11 +483,15 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         if (!pair || w) release(v + 1);
                     }
                 }
-                umma_commit(bar_o);
-                umma_commit(bar_o + 8);
+                if (elect_one()) {
+                    umma_commit(bar_o);
+                    umma_commit(bar_o + 8);
+                }
+                __syncwarp();
                 n += 2 * nb;
             }
-            if (*timed_out) {  // a wait gave up: the products in flight end before the block does
+            if (elect_one() && *timed_out) {
+                // a wait gave up: the products in flight end before the block does
                 umma_commit(bar_drain);
                 const uint64_t t0 = global_timer_ns();
                 while (!mbar_try_wait(bar_drain, 0) &&
@@ -534,7 +562,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             uint8_t *slot = smem + S::kSlots + (k & 1) * PagedSlot<D>::kBytes;
             if (lane == 0) *reinterpret_cast<PagedPiece *>(slot) = x;
             int2 *row_at = reinterpret_cast<int2 *>(slot + PagedSlot<D>::kRow);
-            CFA_ROLLED for (int r = lane; r < x.rows; r += 32) {
+#pragma unroll 2
+            for (int r = lane; r < x.rows; r += 32) {
                 const int i = (x.row0 + r) / G;
                 int t = x.r.tok0 + i;
                 if (x.req < 0) {
@@ -752,13 +781,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     // records are chunk major, results row major
                     const int row = final ? i / (D / 4) : i % x.rows, c = final ? i % (D / 4) : i / x.rows;
                     float m = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < 8; ++w) m = fmaxf(m, ml[w * 16 + row].x);
+                    CFA_ROLLED for (int w = 0; w < 8; ++w) m = fmaxf(m, ml[w * 16 + row].x);
                     const float f = m == -INFINITY ? 0.f : m;
                     float l = 0.f;
                     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int w = 0; w < 8; ++w) {
+                    CFA_ROLLED for (int w = 0; w < 8; ++w) {
                         const float2 s = ml[w * 16 + row];
                         const float g = fast_exp2(s.x - f);
                         const float4 v = *reinterpret_cast<const float4 *>(scr + (w * 16 + row) * D + 4 * c);
@@ -781,22 +808,16 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 
             // ---- tcgen05
             const bool split = x.rows <= 128;
-            CFA_ROLLED for (int t = 0; t < (split ? 1 : 2); ++t) {
-                constexpr int kPer = 128 * (D / 8) / kComputeThreads;
-                uint4 v[kPer];
-#pragma unroll
-                for (int k = 0; k < kPer; ++k) {  // all the loads before the first store
-                    const int i = tid + k * kComputeThreads, row = 128 * t + i / (D / 8), c = i % (D / 8);
-                    v[k] = make_uint4(0u, 0u, 0u, 0u);
-                    if (row < x.rows) v[k] = *reinterpret_cast<const uint4 *>(query(row) + 8 * c);
-                }
-#pragma unroll
-                for (int k = 0; k < kPer; ++k) {
-                    const int i = tid + k * kComputeThreads, row = i / (D / 8), c = i % (D / 8);
-                    *reinterpret_cast<uint4 *>(smem + S::kQ + t * S::kQTile + (c >> 3) * S::kHalf + row * 128 +
-                                               (((c & 7) ^ (row & 7)) << 4)) = v[k];
-                }
+            // asynchronous copies: all of them on their way before the first has landed
+#pragma unroll 4
+            for (int i = tid; i < (split ? 128 : 256) * (D / 8); i += kComputeThreads) {
+                const int row = i / (D / 8), c = i % (D / 8);
+                uint8_t *dst = smem + S::kQ + (row >> 7) * S::kQTile + (c >> 3) * S::kHalf + (row & 127) * 128 +
+                               (((c & 7) ^ (row & 7)) << 4);
+                if (row < x.rows) cp_async_16(smem_addr(dst), query(row) + 8 * c);
+                else *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
             }
+            cp_async_wait_all();
             fence_proxy_async_smem();
             tcgen05_fence_before();
             mbar_arrive(bar_q);
