@@ -8,7 +8,7 @@
 
 namespace cfa {
 
-constexpr int kPagedMaxSeqs = 2048;         // requests per call
+constexpr int kPagedMaxSeqs = 1024;         // requests per call
 constexpr int kPagedMaxTokens = 1 << 17;    // new tokens per call
 constexpr int kPagedMaxTableWidth = 1 << 18;
 
@@ -75,7 +75,7 @@ struct PagedAttnParams {
     unsigned long long timeout_ns;
 };
 
-constexpr int kPagedThreads = 384;    // 8 compute warps; load, MMA, address and prep warps
+constexpr int kPagedThreads = 384;    // 8 compute warps; two load warps, an address and a prep warp
 constexpr int kPagedPlanInts = 8;
 
 }  // namespace cfa

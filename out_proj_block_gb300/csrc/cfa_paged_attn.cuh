@@ -150,31 +150,28 @@ __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(n) : "memory");
 }
 
-// Blocks of keys whose cache rows the address warp finds ahead of the load warp, four
-// at a time: entries of 12 ints (up to 8 boxes' rows, their number, the piece's blocks
-// and order), groups of 4 entries.
+// Blocks of keys whose cache rows the address warp finds ahead of the load warps, four
+// at a time: entries of 12 ints (up to 8 boxes' rows, their number, and whether the run
+// ends here), groups of 4 entries.
 constexpr int kPagedGroups = 4;
 constexpr int kPagedEntry = 12;
-
-// A piece as the prep warp lays it out for the compute and MMA warps, one ahead.
-template <int D>
-struct PagedSlot {
-    static constexpr int kRow = 128;                 // after the PagedPiece: int2 [256] token, output row
-    static constexpr int kQ = kRow + 256 * 8;        // up to 16 query rows, [D / 64][16][64] swizzled
-    static constexpr int kBytes = kQ + 16 * D * 2;
-};
+// Pieces that the prep warp has laid out at most.
+constexpr int kPagedSlots = 3;
 
 // Shared memory of the attention kernel for head_dim D.
 template <int D>
 struct PagedSmem {
     static constexpr int kStage = kPagedKeys * D * 2;           // one block of K or V
     static constexpr int kHalf = kPagedKeys * 128;              // its 64-dim column halves
-    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kStages = D == 128 ? 2 : 4;            // of K, and as many of V
     static constexpr int kQTile = 128 * D * 2;
     static constexpr int kQ = 0;                                // two query tiles; scratch otherwise
     static constexpr int kRing = 2 * kQTile;
-    static constexpr int kSlots = kRing + kStages * kStage;     // two pieces
-    static constexpr int kMl = kSlots + 2 * PagedSlot<D>::kBytes;  // float2 [128]: max and sum
+    // a piece: its numbers, where its rows lie (int2 [256]: token and output row), then up to
+    // 16 query rows, [D / 64][16][64] swizzled
+    static constexpr int kSlots = kRing + 2 * kStages * kStage;
+    static constexpr int kSlotRows = 128, kSlotQ = kSlotRows + 256 * 8, kSlot = kSlotQ + 16 * D * 2;
+    static constexpr int kMl = kSlots + kPagedSlots * kSlot;    // float2 [128]: max and sum
     static constexpr int kBars = kMl + 128 * 8;
     static constexpr int kMisc = kBars + 48 * 8;                // flags, TMEM address, scan sums
     static constexpr int kFifo = kMisc + 256;                   // the address warp's entries
@@ -188,6 +185,29 @@ static_assert(sizeof(PagedPiece) <= 128, "a piece fits its slot");
 static __device__ __noinline__ bool paged_wait_slow(uint32_t bar, uint32_t parity, unsigned long long timeout_ns,
                                                     volatile int *timed_out, unsigned *status, unsigned site) {
     return mbar_wait_bounded<false>(bar, parity, timeout_ns, timed_out, status, site);
+}
+
+// A count that one thread raises and others wait for, within the same bound as a barrier.
+__device__ __forceinline__ void paged_publish(int *count, uint32_t v) {
+    asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" :: "r"(smem_addr(count)), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t paged_count(const int *count) {
+    uint32_t v;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(smem_addr(count)) : "memory");
+    return v;
+}
+static __device__ __noinline__ uint32_t paged_wait_count(const int *count, uint32_t least, unsigned long long timeout_ns,
+                                                         volatile int *timed_out, unsigned *status, unsigned site) {
+    uint32_t v = paged_count(count);
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t i = 1; v < least && !*timed_out; ++i) {
+        v = paged_count(count);
+        if ((i & 63u) == 0u && global_timer_ns() - t0 > timeout_ns) {
+            *timed_out = 1;
+            atomicOr(status, kStatusTimeoutBit | (site << kStatusSiteShift));
+        }
+    }
+    return v;
 }
 
 template <bool V>
@@ -213,10 +233,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = smem_addr(smem);
     const uint32_t ring = base + S::kRing;
-    const uint32_t bar_full = base + S::kBars, bar_empty = bar_full + 8 * NS;
-    const uint32_t bar_q = bar_empty + 8 * NS, bar_s = bar_q + 8, bar_p = bar_s + 16, bar_o = bar_p + 16,
-                   bar_drain = bar_o + 16, bar_piece = bar_drain + 8, bar_piece_free = bar_piece + 16,
-                   bar_entry = bar_piece_free + 16, bar_entry_free = bar_entry + 8 * kPagedGroups;
+    const uint32_t bar_full = base + S::kBars, bar_empty = bar_full + 16 * NS;  // K's stages, then V's
+    const uint32_t bar_both = bar_empty + 16 * NS, bar_s = bar_both + 8, bar_o = bar_s + 16,
+                   bar_drain = bar_o + 16, bar_piece = bar_drain + 16, bar_piece_free = bar_piece + 8 * kPagedSlots,
+                   bar_entry = bar_piece_free + 8 * kPagedSlots, bar_entry_free = bar_entry + 8 * kPagedGroups;
     int *misc = reinterpret_cast<int *>(smem + S::kMisc);
     volatile int *timed_out = misc;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 1);
@@ -225,24 +245,26 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     float2 *ml = reinterpret_cast<float2 *>(smem + S::kMl);
 
     if (tid == 0) {
-        CFA_ROLLED for (int s = 0; s < NS; ++s) {
+        CFA_ROLLED for (int s = 0; s < 2 * NS; ++s) {
             mbar_init(bar_full + 8 * s, 1);
-            mbar_init(bar_empty + 8 * s, 4);  // a warpgroup's warps, or three of these and a commit
+            mbar_init(bar_empty + 8 * s, 4);  // warps of a warpgroup, or arrivals and commits
         }
-        for (int g = 0; g < kPagedGroups; ++g) {
+        CFA_ROLLED for (int g = 0; g < kPagedGroups; ++g) {
             mbar_init(bar_entry + 8 * g, 1);
-            mbar_init(bar_entry_free + 8 * g, 1);
+            mbar_init(bar_entry_free + 8 * g, 2);
         }
-        mbar_init(bar_q, kComputeThreads);
+        CFA_ROLLED for (int g = 0; g < kPagedSlots; ++g) {
+            mbar_init(bar_piece + 8 * g, 1);
+            mbar_init(bar_piece_free + 8 * g, kComputeWarps);
+        }
+        mbar_init(bar_both, kComputeThreads);
         for (int w = 0; w < 2; ++w) {
             mbar_init(bar_s + 8 * w, 1);
-            mbar_init(bar_p + 8 * w, 128);
             mbar_init(bar_o + 8 * w, 1);
-            mbar_init(bar_piece + 8 * w, 1);
-            mbar_init(bar_piece_free + 8 * w, kComputeWarps + 1);
+            mbar_init(bar_drain + 8 * w, 1);
         }
-        mbar_init(bar_drain, 1);
         *timed_out = 0;
+        misc[4] = misc[5] = 0;
         fence_mbar_init();
     }
     if (warp == kComputeWarps) tmem_alloc(smem_addr(tmem_slot), 512);
@@ -327,292 +349,196 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         return __all_sync(~0u, mbar_try_wait(bar, parity)) ||
                __all_sync(~0u, paged_wait_slow(bar, parity, p.timeout_ns, timed_out, p.status, site));
     };
-    // Stage `n` of the ring's life: slot n % NS, in the n / NS-th pass.
-    auto slot_of = [&](uint32_t n) { return n % NS; };
-    auto wait_full = [&](uint32_t n) { wait(bar_full + 8 * slot_of(n), (n / NS) & 1, kSiteStageFull); };
+    // Block n of the run lies in stage n % NS of each ring (K: 0, V: 1), in its n / NS-th pass.
+    auto slot_of = [&](int v, uint32_t n) { return v * NS + n % NS; };
+    auto stage_at = [&](int v, uint32_t n) { return ring + slot_of(v, n) * S::kStage; };
+    auto wait_full = [&](int v, uint32_t n) { wait(bar_full + 8 * slot_of(v, n), (n / NS) & 1, kSiteStageFull); };
     // Keys of block j of a piece's item: where they lie and how many there are.
     auto block_keys = [&](const PagedPiece &x, int j, int *key0) {
         const bool pre = j < x.prefix_blocks;
         *key0 = (pre ? j : j - x.prefix_blocks) * kPagedKeys;
         return min(kPagedKeys, (pre ? p.prefix_len : x.own_limit) - *key0);
     };
-    // V_i's place among a piece's 2 n stages (K0 V0 K1 V1 ..., or with the keys of two
-    // blocks ahead K0 K1 V0 K2 V1 ... V_n-1).
-    auto v_place = [&](bool split, int n, int i) { return !split ? 2 * i + 1 : i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
-
     if (warp >= kComputeWarps) {
-    registers_for_issue();
-    if (warp == kComputeWarps) {
-        // -------------------------------------------------------------- load warp
-        uint32_t n = 0, known = 0;  // stages issued, groups of entries seen
-        const uint32_t units = static_cast<uint32_t>(uniform(u1 - u0));
-        const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128;
-        for (uint32_t q = 0; q < units;) {
-            bool ok = true;
-            auto entry = [&](uint32_t e) {
-                for (; known <= e / 4 && ok; ++known)
-                    ok = wait_warp(bar_entry + 8 * (known % kPagedGroups), (known / kPagedGroups) & 1, kSiteStageFull);
-                return entries + e % (4 * kPagedGroups) * kPagedEntry;
-            };
-            const int *first_entry = entry(q);
-            if (!ok) break;
-            const int nb = uniform(first_entry[9]), split = uniform(first_entry[10]);
-            CFA_ROLLED for (int t = 0; t < 2 * nb; ++t) {
-                bool is_v = t & 1;
-                int i = t >> 1;
-                if (split && t > 0) {  // keys two blocks ahead of the values
-                    is_v = t == 2 * nb - 1 || (t > 1 && !(t & 1));
-                    i = t == 2 * nb - 1 ? nb - 1 : is_v ? (t - 2) >> 1 : (t + 1) >> 1;
+        registers_for_issue();
+        if (warp < kComputeWarps + 2) {
+            // -------------------------------------------- load warps: one for K, one for V
+            const int v = warp - kComputeWarps;
+            uint32_t n = 0;
+            const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128;
+            for (;; ++n) {
+                const uint32_t group = n / 4;
+                if (n % 4 == 0 && !wait_warp(bar_entry + 8 * (group % kPagedGroups), (group / kPagedGroups) & 1, kSiteStageFull))
+                    break;
+                const int *e = entries + n % (4 * kPagedGroups) * kPagedEntry;
+                const int mine = lane < 10 ? e[lane] : 0;
+                if (__shfl_sync(~0u, mine, 9)) break;  // the run's end
+                const uint32_t full = bar_full + 8 * slot_of(v, n);
+                if (n >= NS && !wait_warp(bar_empty + 8 * slot_of(v, n), (n / NS - 1) & 1, kSiteStageEmpty)) break;
+                const int boxes = __shfl_sync(~0u, mine, 8);
+                const uint32_t dst = stage_at(v, n);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes) * box_bytes * (D / 64));
+                    paged_publish(misc + 4 + v, n + 1);
                 }
-                const uint32_t at = q + i;
-                const int *e = entry(at);
-                const uint32_t full = bar_full + 8 * slot_of(n);
-                if (ok && n >= NS) ok = wait_warp(bar_empty + 8 * slot_of(n), (n / NS - 1) & 1, kSiteStageEmpty);
-                if (!ok) break;
-                const int boxes = uniform(e[8]);
-                const uint32_t dst = ring + slot_of(n) * S::kStage;
-                if (elect_one()) mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes) * box_bytes * (D / 64));
                 __syncwarp();
                 CFA_ROLLED for (int k = 0; k < boxes; ++k) {
-                    const int y = uniform(e[k]);
+                    const int y = __shfl_sync(~0u, mine, k);
                     if (elect_one()) {
 #pragma unroll
                         for (int h = 0; h < D / 64; ++h)
-                            tma_load_2d(dst + k * box_bytes + h * S::kHalf, is_v ? &tm_v : &tm_k, 64 * h, y, full);
+                            tma_load_2d(dst + k * box_bytes + h * S::kHalf, v ? &tm_v : &tm_k, 64 * h, y, full);
                     }
                     __syncwarp();
                 }
-                ++n;
-                // the values are a block's second stage: after the last block of a group its entries are free
-                if (is_v && (at % 4 == 3 || at + 1 == units) && elect_one())
-                    mbar_arrive(bar_entry_free + 8 * (at / 4 % kPagedGroups));
+                if (n % 4 == 3 && elect_one()) mbar_arrive(bar_entry_free + 8 * (group % kPagedGroups));
                 __syncwarp();
             }
-            if (!ok) break;
-            q += nb;
-        }
-        if (lane == 0 && *timed_out) {
-            // a wait gave up: the copies in flight land before the block ends
-            const uint64_t t0 = global_timer_ns();
-            for (uint32_t k = n > NS ? n - NS : 0; k < n; ++k)
-                while (!mbar_try_wait(bar_full + 8 * slot_of(k), (k / NS) & 1) &&
-                       global_timer_ns() - t0 < kDrainTimeoutFactor * p.timeout_ns) {
-                }
-        }
-        __syncwarp();
-    } else if (warp == kComputeWarps + 1) {
-        // --------------------------------------------------------------- MMA warp
-        {
-            constexpr uint32_t idesc_s = umma_idesc_bf16(128, kPagedKeys, false, false);
-            constexpr uint32_t idesc_o = umma_idesc_bf16(128, D, false, true);
-            const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
-            const int end = uniform(u1);
-            uint32_t n = 0, pieces = 0, probs0 = 0, probs1 = 0;
-            auto scores = [&](int w, uint32_t q, uint32_t stage) {
-                const uint32_t k = ring + slot_of(stage) * S::kStage;
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)  // 32 bytes a step
-                        umma_bf16(tm + 128 * w, umma_smem_desc(q + (ks >> 2) * S::kHalf, 16, 1024) + 2 * (ks & 3),
-                                  umma_smem_desc(k + (ks >> 2) * S::kHalf, 16, 1024) + 2 * (ks & 3), idesc_s, ks > 0);
-                    umma_commit(bar_s + 8 * w);
-                }
-                __syncwarp();
-            };
-            auto values = [&](int w, uint32_t stage, bool accumulate) {
-                const uint64_t vd = umma_smem_desc(ring + slot_of(stage) * S::kStage, S::kHalf, 1024);
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = 0; ks < kPagedKeys / 16; ++ks)  // 16 rows of 128 bytes a step
-                        umma_bf16_ts(tm + 256 + D * w, tm + 128 * w + 8 * ks, vd + 128 * ks, idesc_o,
-                                     accumulate || ks > 0);
-                }
-                __syncwarp();
-            };
-            auto probs_ready = [&](int w) {
-                const uint32_t c = w ? probs1++ : probs0++;
-                wait_warp(bar_p + 8 * w, c & 1, kSiteSoftmaxExchange);
-                tcgen05_fence_after();
-            };
-            auto keys_ready = [&](uint32_t stage) {
-                wait_warp(bar_full + 8 * slot_of(stage), (stage / NS) & 1, kSiteStageFull);
-                tcgen05_fence_after();
-            };
-            auto release = [&](uint32_t stage) {  // once the MMAs issued so far have read it
-                if (elect_one()) {
-                    mbar_arrive_n(bar_empty + 8 * slot_of(stage), 3);
-                    umma_commit(bar_empty + 8 * slot_of(stage));
-                }
-                __syncwarp();
-            };
-            uint32_t k_piece = 0;
-            for (int u = uniform(u0); u < end; ++k_piece) {
-                const uint32_t at = k_piece & 1;
-                if (!wait_warp(bar_piece + 8 * at, (k_piece >> 1) & 1, kSiteStageFull)) break;
-                const PagedPiece *x = reinterpret_cast<const PagedPiece *>(smem + S::kSlots + at * PagedSlot<D>::kBytes);
-                const int nb = uniform(x->b1 - x->b0), rows = uniform(x->rows);
-                __syncwarp();
-                if (elect_one()) mbar_arrive(bar_piece_free + 8 * at);
-                u += nb;
-                if (rows <= kPagedSmallRows) {
-                    n += 2 * nb;
-                    continue;
-                }
-                wait_warp(bar_q, pieces++ & 1, kSiteQExchange);
-                tcgen05_fence_after();
-                const uint32_t q = base + S::kQ;
-                // steps: block j of the keys with query tile w (two tiles), or with the one
-                // tile in the scores and outputs of half w = j mod 2
-                const bool pair = rows > 128;
-                CFA_ROLLED for (int w = 0; w < (pair ? 2 : min(nb, 2)); ++w) {
-                    const uint32_t k = n + (pair ? 0 : w);
-                    keys_ready(k);
-                    scores(w, q + (pair ? w * S::kQTile : 0), k);
-                    if (!pair || w) release(k);
-                }
-                CFA_ROLLED for (int t = 0; t < (pair ? 2 * nb : nb); ++t) {
-                    const int j = pair ? t >> 1 : t, w = t & 1;
-                    const uint32_t v = n + v_place(!pair, nb, j);
-                    keys_ready(v);
-                    probs_ready(w);
-                    values(w, v, pair ? j > 0 : j > 1);
-                    if (!pair || w) release(v);
-                    if (j + (pair ? 1 : 2) < nb) {
-                        keys_ready(v + 1);
-                        scores(w, q + (pair ? w * S::kQTile : 0), v + 1);
-                        if (!pair || w) release(v + 1);
-                    }
-                }
-                if (elect_one()) {
-                    umma_commit(bar_o);
-                    umma_commit(bar_o + 8);
-                }
-                __syncwarp();
-                n += 2 * nb;
-            }
-            if (elect_one() && *timed_out) {
-                // a wait gave up: the products in flight end before the block does
-                umma_commit(bar_drain);
+            if (lane == 0 && *timed_out) {
+                // a wait gave up: the copies in flight land before the block ends
                 const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait(bar_drain, 0) &&
-                       global_timer_ns() - t0 < kDrainTimeoutFactor * p.timeout_ns) {
-                }
-            }
-        }
-        __syncwarp();
-    } else if (warp == kComputeWarps + 2) {
-        // ----------------------------------------------------------- address warp
-        // Finds the cache rows of the run's blocks, four at a time (8 lanes each, a lane a
-        // box), ahead of the load warp: a table entry takes as long to arrive as the keys.
-        const int box = p.box_rows, sub = lane >> 3, i = lane & 7;
-        const int all_rows = p.n_pages * p.n_kv * p.page_size;
-        PagedPiece x;
-        int u = u0, at = u0;  // the next piece, the next block
-        x.b0 = x.b1 = 0;
-        for (uint32_t g = 0; at < u1; ++g) {
-            const int *id_at = nullptr;
-            int boxes = 0, add = 0, nb = 0, split = 0;
-            bool mine = false;
-            CFA_ROLLED for (int k = 0; k < 4 && at < u1; ++k, ++at) {
-                if (at == u) {
-                    x = paged_piece(shape, plan, start, B, u, u1, get);
-                    u += x.b1 - x.b0;
-                }
-                if (sub == k) {
-                    int key0;
-                    const int j = x.b1 - (u - at), keys = block_keys(x, j, &key0);
-                    boxes = keys > 0 ? (keys + box - 1) / box : 0;
-                    const int key = key0 + i * box, pg = key / p.page_size;
-                    if (i < boxes)
-                        id_at = (j < x.prefix_blocks ? p.prefix_table
-                                                     : p.tables + static_cast<size_t>(x.req) * p.width) + pg;
-                    add = x.h * p.page_size + key - pg * p.page_size;
-                    nb = x.b1 - x.b0;
-                    split = x.rows > kPagedSmallRows && x.rows <= 128;
-                    mine = true;
-                }
-            }
-            int y = all_rows;  // outside: reads as zeros
-            if (id_at) {
-                const int id = __ldcg(id_at);
-                if (id >= 0 && id < p.n_pages) y = id * p.n_kv * p.page_size + add;
-                else atomicOr(p.status, kStatusBadPageBit);
-            }
-            if (__any_sync(~0u, g >= kPagedGroups && !wait(bar_entry_free + 8 * (g % kPagedGroups),
-                                                           (g / kPagedGroups - 1) & 1, kSiteStageEmpty)))
-                break;
-            int *e = entries + (4 * (g % kPagedGroups) + sub) * kPagedEntry;
-            if (mine) {
-                e[i] = y;
-                if (i == 0) e[8] = boxes, e[9] = nb, e[10] = split;
+                for (uint32_t k = n > NS ? n - NS : 0; k < n; ++k)
+                    while (!mbar_try_wait(bar_full + 8 * slot_of(v, k), (k / NS) & 1) &&
+                           global_timer_ns() - t0 < kDrainTimeoutFactor * p.timeout_ns) {
+                    }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_entry + 8 * (g % kPagedGroups));
-        }
-    } else {
-        // -------------------------------------------------------------- prep warp
-        // Lays the next piece out: its numbers, where each row's query and result lie, and
-        // the queries themselves where they are few.
-        uint32_t k = 0;
-        for (int u = u0; u < u1; ++k) {
-            const PagedPiece x = paged_piece(shape, plan, start, B, u, u1, get);
-            u += x.b1 - x.b0;
-            if (__any_sync(~0u, k >= 2 && !wait(bar_piece_free + 8 * (k & 1), (k / 2 - 1) & 1, kSiteStageEmpty)))
-                break;
-            uint8_t *slot = smem + S::kSlots + (k & 1) * PagedSlot<D>::kBytes;
-            if (lane == 0) *reinterpret_cast<PagedPiece *>(slot) = x;
-            int2 *row_at = reinterpret_cast<int2 *>(slot + PagedSlot<D>::kRow);
-#pragma unroll 2
-            for (int r = lane; r < x.rows; r += 32) {
-                const int i = (x.row0 + r) / G;
-                int t = x.r.tok0 + i;
-                if (x.req < 0) {
-                    const int b = paged_find(stok, B, i);
-                    t = __ldcg(p.cu + b) + i - stok[b];
-                }
-                row_at[r] = make_int2(t, t * p.n_heads + x.h * G + (x.row0 + r) - i * G);
-            }
-            __syncwarp();
-            if (x.rows <= kPagedSmallRows) {
-#pragma unroll
-                for (int c = lane; c < 16 * (D / 8); c += 32) {
-                    const int r = c / (D / 8), ch = c % (D / 8);
-                    uint8_t *dst = slot + PagedSlot<D>::kQ + (ch >> 3) * 2048 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-                    if (r < x.rows) {
-                        const int2 at = row_at[r];
-                        cp_async_16(smem_addr(dst), p.q + at.x * p.q_stride + (at.y - at.x * p.n_heads) * D + 8 * ch);
-                    } else {
-                        *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
+        } else if (warp == kComputeWarps + 2) {
+            // ------------------------------------------------------- address warp
+            // Finds the cache rows of the run's blocks, four at a time (8 lanes each, a lane a
+            // box), ahead of the load warps: a table entry takes as long to arrive as the keys.
+            const int box = p.box_rows, sub = lane >> 3, i = lane & 7;
+            const int all_rows = p.n_pages * p.n_kv * p.page_size;
+            PagedPiece x;
+            int u = u0, j = 0;  // the next piece, the next block of this one
+            x.b1 = 0;
+            bool more = true;
+            for (uint32_t g = 0; more; ++g) {
+                const int *id_at = nullptr;
+                int boxes = 0, add = 0;
+                bool mine = false, end = false;
+                CFA_ROLLED for (int k = 0; k < 4 && more; ++k, ++j) {
+                    if (j == x.b1) {
+                        more = paged_next(shape, plan, start, B, u, u1, get, x);
+                        j = x.b0;
+                    }
+                    if (sub == k) {
+                        mine = true;
+                        if (more) {
+                            int key0;
+                            const int keys = block_keys(x, j, &key0);
+                            boxes = keys > 0 ? (keys + box - 1) / box : 0;
+                            const int key = key0 + i * box, pg = key / p.page_size;
+                            if (i < boxes)
+                                id_at = (j < x.prefix_blocks ? p.prefix_table
+                                                             : p.tables + static_cast<size_t>(x.req) * p.width) + pg;
+                            add = x.h * p.page_size + key - pg * p.page_size;
+                        }
+                        end = !more;
                     }
                 }
-                cp_async_wait_all();
+                int y = all_rows;  // outside: reads as zeros
+                if (id_at) {
+                    const int id = __ldcg(id_at);
+                    if (id >= 0 && id < p.n_pages) y = id * p.n_kv * p.page_size + add;
+                    else atomicOr(p.status, kStatusBadPageBit);
+                }
+                if (__any_sync(~0u, g >= kPagedGroups && !wait(bar_entry_free + 8 * (g % kPagedGroups),
+                                                               (g / kPagedGroups - 1) & 1, kSiteStageEmpty)))
+                    break;
+                int *e = entries + (4 * (g % kPagedGroups) + sub) * kPagedEntry;
+                if (mine) {
+                    e[i] = y;
+                    if (i == 0) e[8] = boxes, e[9] = end;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_entry + 8 * (g % kPagedGroups));
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_piece + 8 * (k & 1));
+        } else {
+            // ---------------------------------------------------------- prep warp
+            // Lays pieces out ahead: their numbers, where each row's query and result lie,
+            // and the queries themselves where they are few. A piece without blocks ends the run.
+            bool more = true;
+            int u = u0;
+            for (uint32_t k = 0; more; ++k) {
+                PagedPiece x;
+                more = paged_next(shape, plan, start, B, u, u1, get, x);
+                if (!more) x.b0 = x.b1 = x.rows = 0;
+                if (__any_sync(~0u, k >= kPagedSlots && !wait(bar_piece_free + 8 * (k % kPagedSlots),
+                                                              (k / kPagedSlots - 1) & 1, kSiteStageEmpty)))
+                    break;
+                uint8_t *slot = smem + S::kSlots + k % kPagedSlots * S::kSlot;
+                if (lane == 0) *reinterpret_cast<PagedPiece *>(slot) = x;
+                const bool few = x.rows <= kPagedSmallRows;
+                int2 *row_at = reinterpret_cast<int2 *>(slot + S::kSlotRows);
+#pragma unroll 2
+                for (int r = lane; r < x.rows; r += 32) {
+                    const int i = (x.row0 + r) / G;
+                    int t = x.r.tok0 + i;
+                    if (x.req < 0) {
+                        const int b = paged_find(stok, B, i);
+                        t = __ldcg(p.cu + b) + i - stok[b];
+                    }
+                    row_at[r] = make_int2(t, t * p.n_heads + x.h * G + (x.row0 + r) - i * G);
+                }
+                __syncwarp();
+                if (few) {
+#pragma unroll
+                    for (int c = lane; c < 16 * (D / 8); c += 32) {
+                        const int r = c / (D / 8), ch = c % (D / 8);
+                        uint8_t *dst = slot + S::kSlotQ + (ch >> 3) * 2048 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                        if (r < x.rows) {
+                            const int2 at = row_at[r];
+                            cp_async_16(smem_addr(dst), p.q + at.x * p.q_stride + (at.y - at.x * p.n_heads) * D + 8 * ch);
+                        } else {
+                            *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    cp_async_wait_all();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_piece + 8 * (k % kPagedSlots));
+            }
         }
-    }
     } else {
         // ---------------------------------------------------------- compute warps
         registers_for_compute();
-        const int wg = warp >> 2;
-        uint32_t n = 0, scored = 0, done = 0;
+        const int wg = warp >> 2, wtid = tid & 127;
+        uint32_t n = 0, scored = 0, done = 0, met = 0;  // the piece's first block; phases
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lanes of this warp
-        uint32_t k_piece = 0;
-        for (int u = u0; u < u1; ++k_piece) {
-            // one thread's word for all of them: where its wait gave up, no warp goes on alone
-            const bool there = wait(bar_piece + 8 * (k_piece & 1), (k_piece >> 1) & 1, kSiteStageFull);
-            if (tid == 0) misc[2] = there;
-            compute_bar<kComputeThreads>();
-            if (!misc[2]) break;
-            const uint8_t *slot = smem + S::kSlots + (k_piece & 1) * PagedSlot<D>::kBytes;
+        const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
+        auto wg_bar = [&]() { asm volatile("bar.sync %0, 128;" :: "r"(2 + wg) : "memory"); };
+        // Both warpgroups meet; bounded, as one of them may have given up.
+        auto meet = [&]() {
+            mbar_arrive(bar_both);
+            wait(bar_both, met++ & 1, kSiteKvExchange);
+        };
+        auto release = [&](int v, uint32_t block, uint32_t arrivals) {  // once the products issued so far have read it
+            mbar_arrive_n(bar_empty + 8 * slot_of(v, block), arrivals);
+            umma_commit(bar_empty + 8 * slot_of(v, block));
+        };
+        for (uint32_t k_piece = 0;; ++k_piece) {
+            // one thread's word for its warpgroup: where its wait gave up, no warp goes on alone
+            const uint32_t at_slot = k_piece % kPagedSlots;
+            const bool there = wait(bar_piece + 8 * at_slot, (k_piece / kPagedSlots) & 1, kSiteStageFull);
+            if (wtid == 0) misc[2 + wg] = there;
+            wg_bar();
+            if (!misc[2 + wg]) break;
+            const uint8_t *slot = smem + S::kSlots + at_slot * S::kSlot;
             const PagedPiece &x = *reinterpret_cast<const PagedPiece *>(slot);
-            const int2 *row_at = reinterpret_cast<const int2 *>(slot + PagedSlot<D>::kRow);
-            auto piece_done = [&]() {
-                compute_bar<kComputeThreads>();  // the scratch and the query tiles are free again
-                if (lane == 0) mbar_arrive(bar_piece_free + 8 * (k_piece & 1));
-            };
             const int nb = x.b1 - x.b0;
-            u += nb;
+            if (nb == 0) break;
+            const bool few = x.rows <= kPagedSmallRows;
+            auto piece_done = [&]() {
+                n += nb;
+                wg_bar();  // (and misc is free again)
+                if (lane == 0) mbar_arrive(bar_piece_free + 8 * at_slot);
+            };
+            if (few && static_cast<int>(k_piece & 1) != wg) {  // the other warpgroup's
+                piece_done();
+                continue;
+            }
+            const int2 *row_at = reinterpret_cast<const int2 *>(slot + S::kSlotRows);
             const bool final = paged_final(shape, x);
             const long long rec =
                 x.req >= 0 && paged_alone(shape, x.r.n)
@@ -629,12 +555,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (p.lse) p.lse[row_at[row].y] = (m + log2f(l)) * 0.69314718055994531f;
             };
 
-            if (x.rows <= kPagedSmallRows) {
-                // ---- mma.sync: this warp's 32 keys of every other block
+            if (few) {
+                // ---- mma.sync: this warp's 32 keys of every block
                 const int r0 = lane >> 2, c2 = (lane & 3) * 2, kw = 32 * (warp & 3);
                 uint32_t q[D / 16][4];
                 {
-                    const uint32_t qs = smem_addr(slot + PagedSlot<D>::kQ) + (lane & 15) * 128;
+                    const uint32_t qs = smem_addr(slot + S::kSlotQ) + (lane & 15) * 128;
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t c = 2 * k + (lane >> 4);
@@ -645,20 +571,30 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
                 float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+                // The other warpgroup's blocks may lie between this one's last and these: a
+                // parity says nothing about a stage that is not yet this block's, so the load
+                // warps' counts come first.
+                uint32_t issued[2] = {0, 0};
+                auto wait_issued = [&](int v, uint32_t block) {
+                    if (issued[v] <= block)
+                        issued[v] = paged_wait_count(misc + 4 + v, block + 1, p.timeout_ns, timed_out, p.status, kSiteStageFull);
+                };
                 // own keys that rows r0 and r0 + 8 see
                 const int see0 = paged_visible(x.r, (x.row0 + r0) / G);
                 const int see1 = paged_visible(x.r, (x.row0 + r0 + 8) / G);
                 const uint32_t kkey = kw + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
                 const uint32_t vkey = kw + (lane & 15), vc = lane >> 4;
-                CFA_ROLLED for (int j = wg; j < nb; j += 2) {
-                    const uint32_t nk = n + 2 * j, nv = nk + 1;
+                CFA_ROLLED for (int j = 0; j < nb; ++j) {
+                    const uint32_t block = n + j;
                     int key0;
                     const int keys = block_keys(x, x.b0 + j, &key0) - kw;
                     key0 += kw;
-                    wait_full(nk);
+                    wait_issued(0, block);
+                    wait_full(0, block);
+                    __syncwarp();
                     float s[4][4] = {};
                     if (keys > 0) {
-                        const uint32_t st = ring + slot_of(nk) * S::kStage + kkey * 128;
+                        const uint32_t st = stage_at(0, block) + kkey * 128;
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
                             uint32_t b[4], d[4];
@@ -673,7 +609,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         }
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_empty + 8 * slot_of(nk));
+                    if (lane == 0) mbar_arrive(bar_empty + 8 * slot_of(0, block));
                     uint32_t pr[2][4];
                     if (keys > 0) {
                         const bool own = x.b0 + j >= x.prefix_blocks;
@@ -725,9 +661,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                             pr[t][3] = pack2_bf16_cvt(s[2 * t + 1][2], s[2 * t + 1][3]);
                         }
                     }
-                    wait_full(nv);
+                    wait_issued(1, block);
+                    wait_full(1, block);
+                    __syncwarp();
                     if (keys > 0) {
-                        const uint32_t st = ring + slot_of(nv) * S::kStage + vkey * 128;
+                        const uint32_t st = stage_at(1, block) + vkey * 128;
                         auto values = [&](auto whole) {
                             // rows past the keys may hold anything, and 0 times NaN is NaN
                             auto keep = [&](int k) {
@@ -754,43 +692,48 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         else values(PagedFlag<false>{});
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_empty + 8 * slot_of(nv));
+                    if (lane == 0) mbar_arrive(bar_empty + 8 * slot_of(1, block));
                 }
-                n += 2 * nb;
-                // ---- join the eight warps
+                // ---- join the warpgroup's four warps
 #pragma unroll
                 for (int d = 1; d < 4; d <<= 1) {
                     l0 += __shfl_xor_sync(~0u, l0, d);
                     l1 += __shfl_xor_sync(~0u, l1, d);
                 }
-                float *scr = reinterpret_cast<float *>(smem + S::kQ);  // [8][16][D]
-                if (r0 < x.rows) {
-                    if (c2 == 0) ml[warp * 16 + r0] = make_float2(m0, l0);
+                float *scr = reinterpret_cast<float *>(smem + S::kQ + wg * S::kQTile);  // [4][16][D]
+                float2 *wml = ml + 64 * wg;                                             // [4][16]
+                // column of a row in the scratch: rows 8 floats apart in the banks
+                auto col = [&](int row, int c) { return c ^ ((row & 7) << 3); };
+                auto leave = [&](int row, float m, float l, int e) {
+                    if (row >= x.rows) return;
+                    const int at = (warp & 3) * 16 + row;
+                    if (c2 == 0) wml[at] = make_float2(m, l);
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i)
-                        *reinterpret_cast<float2 *>(scr + (warp * 16 + r0) * D + 8 * i + c2) = make_float2(o[i][0], o[i][1]);
-                }
-                if (r0 + 8 < x.rows) {
-                    if (c2 == 0) ml[warp * 16 + r0 + 8] = make_float2(m1, l1);
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i)
-                        *reinterpret_cast<float2 *>(scr + (warp * 16 + r0 + 8) * D + 8 * i + c2) = make_float2(o[i][2], o[i][3]);
-                }
-                compute_bar<kComputeThreads>();
-                CFA_ROLLED for (int i = tid; i < x.rows * (D / 4); i += kComputeThreads) {
+                        *reinterpret_cast<float2 *>(scr + at * D + col(row, 8 * i + c2)) = make_float2(o[i][e], o[i][e + 1]);
+                };
+                leave(r0, m0, l0, 0);
+                leave(r0 + 8, m1, l1, 2);
+                wg_bar();
+                CFA_ROLLED for (int i = wtid; i < x.rows * (D / 4); i += 128) {
                     // records are chunk major, results row major
                     const int row = final ? i / (D / 4) : i % x.rows, c = final ? i % (D / 4) : i / x.rows;
-                    float m = -INFINITY;
-                    CFA_ROLLED for (int w = 0; w < 8; ++w) m = fmaxf(m, ml[w * 16 + row].x);
+                    float2 w[4];
+                    float4 v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        w[k] = wml[k * 16 + row];
+                        v[k] = *reinterpret_cast<const float4 *>(scr + (k * 16 + row) * D + col(row, 4 * c));
+                    }
+                    const float m = fmaxf(fmaxf(w[0].x, w[1].x), fmaxf(w[2].x, w[3].x));
                     const float f = m == -INFINITY ? 0.f : m;
                     float l = 0.f;
                     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-                    CFA_ROLLED for (int w = 0; w < 8; ++w) {
-                        const float2 s = ml[w * 16 + row];
-                        const float g = fast_exp2(s.x - f);
-                        const float4 v = *reinterpret_cast<const float4 *>(scr + (w * 16 + row) * D + 4 * c);
-                        l += g * s.y;
-                        a.x += g * v.x; a.y += g * v.y; a.z += g * v.z; a.w += g * v.w;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float g = fast_exp2(w[k].x - f);
+                        l += g * w[k].y;
+                        a.x += g * v[k].x; a.y += g * v[k].y; a.z += g * v[k].z; a.w += g * v[k].w;
                     }
                     if (final) {
                         const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -807,7 +750,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
 
             // ---- tcgen05
+            // a warpgroup's first warp issues its products: scores of the next block behind
+            // the values of this one, which read the weights that lie over the scores
             const bool split = x.rows <= 128;
+            meet();  // the scratch and the query tiles are free
             // asynchronous copies: all of them on their way before the first has landed
 #pragma unroll 4
             for (int i = tid; i < (split ? 128 : 256) * (D / 8); i += kComputeThreads) {
@@ -820,7 +766,25 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             cp_async_wait_all();
             fence_proxy_async_smem();
             tcgen05_fence_before();
-            mbar_arrive(bar_q);
+            meet();
+            const int step = split ? 2 : 1, first_block = split ? wg : 0;
+            const uint32_t q_tile = base + S::kQ + (split ? 0 : wg * S::kQTile);
+            auto scores = [&](int j) {
+                const uint32_t block = n + j, k = stage_at(0, block);
+                wait_warp(bar_full + 8 * slot_of(0, block), (block / NS) & 1, kSiteStageFull);
+                tcgen05_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)  // 32 bytes a step
+                        umma_bf16(tm + 128 * wg, umma_smem_desc(q_tile + (ks >> 2) * S::kHalf, 16, 1024) + 2 * (ks & 3),
+                                  umma_smem_desc(k + (ks >> 2) * S::kHalf, 16, 1024) + 2 * (ks & 3),
+                                  umma_idesc_bf16(128, kPagedKeys, false, false), ks > 0);
+                    umma_commit(bar_s + 8 * wg);
+                    release(0, block, split ? 3 : 1);
+                }
+                __syncwarp();
+            };
+            if ((warp & 3) == 0 && first_block < nb) scores(first_block);
 
             const int row = (split ? 0 : 128 * wg) + 32 * (warp & 3) + lane;
             const bool live = row < x.rows;
@@ -829,11 +793,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             const uint32_t t_s = tmem + lanes + 128 * wg, t_o = tmem + lanes + 256 + D * wg;
             float m = -INFINITY, l = 0.f;
             bool begun = false;
-            CFA_ROLLED for (int j = split ? wg : 0; j < nb; j += split ? 2 : 1) {
+            CFA_ROLLED for (int j = first_block; j < nb; j += step) {
                 int key0;
                 const int keys = block_keys(x, x.b0 + j, &key0);
                 const int lim = x.b0 + j < x.prefix_blocks ? keys : min(keys, see - key0);
-                wait(bar_s + 8 * wg, scored++ & 1, kSiteKvExchange);
+                wait(bar_s + 8 * wg, scored++ & 1, kSiteSoftmaxExchange);
+                __syncwarp();
                 tcgen05_fence_after();
                 if (warp_live) {
                     // two passes over the scores in TMEM, 32 columns at a time: keeping a row's 128 in
@@ -905,30 +870,46 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     l += both_sums.x + both_sums.y;
                     tmem_wait_st();
                 }
-                begun = true;
                 if (keys < kPagedKeys) {
                     // rows past the keys may hold anything, and 0 times NaN is NaN
-                    const uint32_t vn = n + v_place(split, nb, j);
-                    wait_full(vn);
+                    wait_full(1, n + j);
                     const int z = max(keys, 0);
                     CFA_ROLLED for (int i = tid & 127; i < (kPagedKeys - z) * (D / 8); i += 128) {
                         const int r = z + i / (D / 8), c = i % (D / 8);
-                        *reinterpret_cast<uint4 *>(smem + S::kRing + slot_of(vn) * S::kStage + (c >> 3) * S::kHalf +
+                        *reinterpret_cast<uint4 *>(smem + S::kRing + slot_of(1, n + j) * S::kStage + (c >> 3) * S::kHalf +
                                                    r * 128 + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
                 }
                 tcgen05_fence_before();
-                mbar_arrive(bar_p + 8 * wg);
+                wg_bar();
+                if ((warp & 3) == 0) {
+                    const uint32_t block = n + j;
+                    wait_warp(bar_full + 8 * slot_of(1, block), (block / NS) & 1, kSiteStageFull);
+                    tcgen05_fence_after();
+                    const uint64_t vd = umma_smem_desc(stage_at(1, block), S::kHalf, 1024);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ks = 0; ks < kPagedKeys / 16; ++ks)  // 16 rows of 128 bytes a step
+                            umma_bf16_ts(tm + 256 + D * wg, tm + 128 * wg + 8 * ks, vd + 128 * ks,
+                                         umma_idesc_bf16(128, D, false, true), begun || ks > 0);
+                        release(1, block, split ? 3 : 1);
+                        if (j + step >= nb) umma_commit(bar_o + 8 * wg);
+                    }
+                    __syncwarp();
+                    if (j + step < nb) scores(j + step);
+                }
+                begun = true;
             }
-            n += 2 * nb;
-            wait(bar_o + 8 * wg, done++ & 1, kSiteKvExchange);
+            if (begun) wait(bar_o + 8 * wg, done++ & 1, kSiteKvExchange);
+            __syncwarp();
             tcgen05_fence_after();
             // ---- the tile's results, or its record
             float mb = -INFINITY, lb = 0.f, ga = 1.f, gb = 0.f;
             // the other half's outputs
             auto at = [&](int c) { return smem + S::kQ + (row & 127) * (4 * D) + ((c ^ (row & 7)) << 4); };
             if (split) {
+                meet();  // no product reads the query tiles any more
                 if (wg == 1) {
                     ml[row] = make_float2(m, l);
                     if (warp_live && begun) {
@@ -944,7 +925,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         }
                     }
                 }
-                compute_bar<kComputeThreads>();
+                meet();
                 if (wg == 0) {
                     mb = ml[row].x;
                     lb = ml[row].y;
@@ -997,8 +978,18 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 }
             }
             tcgen05_fence_before();
+            meet();  // the scratch and the query tiles are free again
             piece_done();
         }
+        if ((warp & 3) == 0 && elect_one() && *timed_out) {
+            // a wait gave up: the products in flight end before the block does
+            umma_commit(bar_drain + 8 * wg);
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(bar_drain + 8 * wg, 0) &&
+                   global_timer_ns() - t0 < kDrainTimeoutFactor * p.timeout_ns) {
+            }
+        }
+        __syncwarp();
     }
     tcgen05_fence_before();
     __syncthreads();
@@ -1041,14 +1032,12 @@ paged_merge_kernel(const PagedAttnParams p, int grid, int shared_blocks) {
     bool live, skip = false;
     PagedPiece x;
     if (alone) {
-        x = paged_piece(shape, plan, start, B, static_cast<int>(end) - 1, static_cast<int>(end),
-                        [&](int b) { return paged_request(p, b); });
-        // cut here for the first time?
-        if (x.req < 0 || !paged_alone(shape, x.r.n) || x.b1 == x.blocks ||
-            x.first_unit < static_cast<long long>(run) * plan.share)
-            return;
+        paged_item(shape, plan, start, B, static_cast<int>(end) - 1, [&](int b) { return paged_request(p, b); }, x);
         c0 = run;
-        c1 = (x.first_unit + x.blocks - 1) / plan.share;
+        c1 = paged_last_run(plan, x.first_unit, x.blocks, x.cost);
+        // cut here for the first time?
+        if (x.req < 0 || !paged_alone(shape, x.r.n) || x.first_unit < static_cast<long long>(run) * plan.share || c1 == run)
+            return;
         h = x.h;
         row = (static_cast<int>(blockIdx.x) - shared_blocks) % 8 * 32 + lane;
         rows = x.rows;
@@ -1063,9 +1052,9 @@ paged_merge_kernel(const PagedAttnParams p, int grid, int shared_blocks) {
         row = r % kPagedTile;
         rows = paged_min(kPagedTile, plan.shared_rows - tile * kPagedTile);
         if (plan.prefix_blocks > 0) {
-            const int item = (h * plan.tiles + tile) * plan.prefix_blocks;
-            c0 = item / plan.share;
-            c1 = (item + plan.prefix_blocks - 1) / plan.share;
+            const int item = plan.prefix_units / p.n_kv * h + tile * plan.prefix_blocks * kPagedMaxCost;
+            c0 = paged_first_run(plan, item);
+            c1 = paged_last_run(plan, item, plan.prefix_blocks, paged_cost(rows));
         }
         if (live) {
             const int b = paged_find(stok, B, r / G);
@@ -1074,11 +1063,11 @@ paged_merge_kernel(const PagedAttnParams p, int grid, int shared_blocks) {
             own_row = r - stok[b] * G;
             out_row = (q.tok0 + own_row / G) * p.n_heads + h * G + own_row % G;
             own_rec = paged_shared_record(shape, plan, b, h, 0, own_rows, stok[b], 0);
-            const int nb = (start[b + 1] - start[b]) / p.n_kv;
+            const int nb = paged_cdiv(q.len, kPagedKeys), cost = paged_cost(own_rows);
             if (nb > 0) {
-                const int item = plan.prefix_units + start[b] + h * nb;
-                d0 = item / plan.share;
-                d1 = (item + nb - 1) / plan.share;
+                const int item = plan.prefix_units + start[b] + h * nb * cost;
+                d0 = paged_first_run(plan, item);
+                d1 = paged_last_run(plan, item, nb, cost);
             }
             skip = plan.prefix_blocks == 0 && d0 == d1;  // the piece wrote the result
         }

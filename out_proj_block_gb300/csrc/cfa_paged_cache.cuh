@@ -20,7 +20,7 @@ namespace cfa {
 // suffice, or a length is negative, nothing is granted (no table entry
 // changes, every cu is 0, every slot -1) and the status word says why.
 //
-// Every block scans all the lengths by itself (at most 16 KB, from L2), so that
+// Every block scans all the lengths by itself (at most 8 KB, from L2), so that
 // no block waits for another; its share of the tokens and of the new pages then
 // comes from two binary searches in shared memory. A page of this call is taken
 // from the free list directly, never read back from the table that other blocks
@@ -55,8 +55,8 @@ paged_tables_kernel(const TablesParams p) {
         tokens += f;
         pages += extra;
     }
-    // exclusive sums over the threads: at most 2048 * 2^17 tokens and
-    // 2048 * 2^18 pages, below 2^31
+    // exclusive sums over the threads: at most 1024 * 2^17 tokens and
+    // 1024 * 2^18 pages, below 2^31
     const int lane = tid & 31, warp = tid >> 5;
     int st = tokens, sp = pages;
     for (int o = 1; o < 32; o <<= 1) {

@@ -9,13 +9,14 @@
 // by itself: it is alone, and each of its tiles goes over the prefix's keys and
 // its own in one item, with nothing to merge.
 //
-// An item is cut into blocks of 128 keys, its units; prefix and own keys never
-// share a block. The units of all items, in a fixed order (shared prefix by
-// key head and tile; then requests in order, by key head and tile), are dealt
-// out to the grid's blocks in equal runs. A run's part of one item is a piece.
-// A piece that is a whole item, and the only item of its rows, writes its
-// result; every other piece leaves a record (max, sum and unnormalised output
-// of its rows), which are merged in the order of the runs.
+// An item is cut into blocks of 128 keys; prefix and own keys never share a
+// block. A block costs paged_cost() units, by how many rows its item has. The
+// units of all items, in a fixed order (shared prefix by key head and tile; then
+// requests in order, by key head and tile), are dealt out to the grid's blocks in
+// equal runs; a block of keys goes to the run in which its first unit lies. A
+// run's part of one item is a piece. A piece that is a whole item, and the only
+// item of its rows, writes its result; every other piece leaves a record (max, sum
+// and unnormalised output of its rows), which are merged in the order of the runs.
 #pragma once
 
 #include <cstdint>
@@ -34,6 +35,7 @@ constexpr int kPagedKeys = 128;       // keys of a block
 constexpr int kPagedTile = 256;       // rows of a tile
 constexpr int kPagedSmallRows = 16;   // rows that go through mma.sync
 constexpr int kPagedAloneRows = 128;  // rows up to which a request shares the prefix's tiles
+constexpr int kPagedMaxCost = 3;
 
 struct PagedShape {
     int G, nkv, prefix_len, grid;
@@ -63,12 +65,16 @@ struct PagedPiece {
     int own_limit;      // own keys that the last row sees
     int b0, b1;         // the piece: blocks [b0, b1) of the item
     int first_unit;     // the item's first unit
+    int cost;           // units of a block
     PagedRequest r;
 };
 
 CFA_HD int paged_min(int a, int b) { return a < b ? a : b; }
 CFA_HD int paged_max(int a, int b) { return a > b ? a : b; }
 CFA_HD int paged_cdiv(int a, int b) { return (a + b - 1) / b; }
+
+// Units of a block of keys for an item of so many rows.
+CFA_HD int paged_cost(int rows) { return rows <= 128 ? 2 : kPagedMaxCost; }
 
 // Own keys that token i of a request sees.
 CFA_HD int paged_visible(const PagedRequest &r, int i) {
@@ -87,9 +93,11 @@ CFA_HD int paged_alone_blocks(const PagedShape &s, const PagedRequest &r, int ti
 // Units of a request's own items.
 CFA_HD long long paged_request_units(const PagedShape &s, const PagedRequest &r) {
     if (r.n == 0) return 0;
-    if (!paged_alone(s, r.n)) return static_cast<long long>(s.nkv) * paged_cdiv(r.len, kPagedKeys);
+    if (!paged_alone(s, r.n))
+        return static_cast<long long>(s.nkv) * paged_cdiv(r.len, kPagedKeys) * paged_cost(r.n * s.G);
     long long u = 0;
-    CFA_ROLLED for (int t = 0; t * kPagedTile < r.n * s.G; ++t) u += paged_alone_blocks(s, r, t);
+    CFA_ROLLED for (int row = 0, t = 0; row < r.n * s.G; row += kPagedTile, ++t)
+        u += paged_alone_blocks(s, r, t) * paged_cost(r.n * s.G - row);
     return u * s.nkv;
 }
 
@@ -99,12 +107,17 @@ CFA_HD PagedPlan paged_plan(const PagedShape &s, long long own_units, int shared
     p.shared_rows = shared_tokens * s.G;
     p.prefix_blocks = paged_cdiv(s.prefix_len, kPagedKeys);
     p.tiles = paged_cdiv(p.shared_rows, kPagedTile);
-    const long long pu = static_cast<long long>(s.nkv) * p.tiles * p.prefix_blocks;
+    // every tile but the last is full
+    const int last_rows = p.shared_rows - (p.tiles - 1) * kPagedTile;
+    const long long pu = p.tiles == 0 ? 0
+                                      : static_cast<long long>(s.nkv) * p.prefix_blocks *
+                                            ((p.tiles - 1) * kPagedMaxCost + paged_cost(last_rows));
     const long long all = pu + own_units;
     p.valid = valid && all < (1ll << 31) - s.grid;
     p.prefix_units = p.valid ? static_cast<int>(pu) : 0;
     p.units = p.valid ? static_cast<int>(all) : 0;
-    p.share = paged_max(1, paged_cdiv(p.units, s.grid));
+    // at least a block, so that a run inside an item never comes away empty
+    p.share = paged_max(kPagedMaxCost, paged_cdiv(p.units, s.grid));
     return p;
 }
 
@@ -119,23 +132,23 @@ CFA_HD int paged_find(const int *a, int B, int x) {
     return lo;
 }
 
-// The piece of the run ending before unit `end` that starts at unit u. start[b]:
-// units of the requests before b; get(b): request b.
+// The item that holds unit u. start[b]: units of the requests before b; get(b): request b.
 template <typename Get>
-CFA_HD PagedPiece paged_piece(const PagedShape &s, const PagedPlan &p, const int *start, int B, int u,
-                              int end, Get get) {
-    PagedPiece x;
-    int rem;
+CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const int *start, int B, int u, Get get,
+                       PagedPiece &x) {
+    int rem;  // units of the item before u
     if (u < p.prefix_units) {
-        const int item = u / p.prefix_blocks;
+        const int head_units = p.prefix_units / s.nkv, full = p.prefix_blocks * kPagedMaxCost;
         x.req = -1;
-        x.h = item / p.tiles;
-        x.row0 = (item - x.h * p.tiles) * kPagedTile;
+        x.h = u / head_units;
+        rem = u - x.h * head_units;
+        const int tile = paged_min(rem / full, p.tiles - 1);
+        rem -= tile * full;
+        x.row0 = tile * kPagedTile;
         x.rows = paged_min(kPagedTile, p.shared_rows - x.row0);
         x.prefix_blocks = x.blocks = p.prefix_blocks;
         x.own_limit = 0;
         x.r = PagedRequest{0, 0, 0};
-        rem = u - item * p.prefix_blocks;
     } else {
         x.req = paged_find(start, B, u - p.prefix_units);
         x.r = get(x.req);
@@ -143,29 +156,43 @@ CFA_HD PagedPiece paged_piece(const PagedShape &s, const PagedPlan &p, const int
         const int per_head = (start[x.req + 1] - start[x.req]) / s.nkv;
         x.h = mine / per_head;
         rem = mine - x.h * per_head;
+        x.row0 = 0;
         if (!paged_alone(s, x.r.n)) {
-            x.row0 = 0;
             x.rows = x.r.n * s.G;
             x.prefix_blocks = 0;
-            x.blocks = per_head;
+            x.blocks = paged_cdiv(x.r.len, kPagedKeys);
             x.own_limit = x.r.len;
         } else {
-            int t = 0, n = paged_alone_blocks(s, x.r, 0);
-            CFA_ROLLED while (rem >= n) {
-                rem -= n;
-                n = paged_alone_blocks(s, x.r, ++t);
+            const int all = x.r.n * s.G;
+            int t = 0;
+            x.blocks = paged_alone_blocks(s, x.r, 0);
+            CFA_ROLLED while (rem >= x.blocks * paged_cost(all - x.row0)) {
+                rem -= x.blocks * paged_cost(all - x.row0);
+                x.row0 += kPagedTile;
+                x.blocks = paged_alone_blocks(s, x.r, ++t);
             }
-            x.row0 = t * kPagedTile;
-            x.rows = paged_min(kPagedTile, x.r.n * s.G - x.row0);
+            x.rows = paged_min(kPagedTile, all - x.row0);
             x.prefix_blocks = p.prefix_blocks;
-            x.blocks = n;
             x.own_limit = paged_visible(x.r, (x.row0 + x.rows - 1) / s.G);
         }
     }
+    x.cost = paged_cost(x.rows);
     x.first_unit = u - rem;
-    x.b0 = rem;
-    x.b1 = paged_min(x.blocks, rem + end - u);
-    return x;
+}
+
+// The next piece of the run that ends before unit `end`, from unit u on; u moves behind it.
+// False: the run has no more.
+template <typename Get>
+CFA_HD bool paged_next(const PagedShape &s, const PagedPlan &p, const int *start, int B, int &u, int end,
+                       Get get, PagedPiece &x) {
+    CFA_ROLLED while (u < end) {
+        paged_item(s, p, start, B, u, get, x);
+        x.b0 = paged_cdiv(u - x.first_unit, x.cost);
+        x.b1 = paged_min(x.blocks, paged_cdiv(end - x.first_unit, x.cost));
+        u = paged_min(end, x.first_unit + x.blocks * x.cost);
+        if (x.b0 < x.b1) return true;
+    }
+    return false;
 }
 
 // Whether a request's item holds all the keys its rows see.
@@ -175,6 +202,12 @@ CFA_HD bool paged_sole(const PagedShape &s, const PagedPiece &x) {
 // Whether a piece writes its rows' results itself.
 CFA_HD bool paged_final(const PagedShape &s, const PagedPiece &x) {
     return x.b0 == 0 && x.b1 == x.blocks && paged_sole(s, x);
+}
+
+// The runs of an item's first and last blocks.
+CFA_HD int paged_first_run(const PagedPlan &p, int first_unit) { return first_unit / p.share; }
+CFA_HD int paged_last_run(const PagedPlan &p, int first_unit, int blocks, int cost) {
+    return (first_unit + (blocks - 1) * cost) / p.share;
 }
 
 // First record row of a piece of run c. Items that share have room for their rows at every

@@ -85,7 +85,7 @@ def want_tables(c, ps, base=0):
 
 
 @pytest.mark.parametrize("B,ps,fresh", [(1, 16, 1), (3, 64, 5), (16, 16, 1), (33, 32, 90),
-                                        (513, 16, 2), (1025, 192, 1), (2048, 64, 3)])
+                                        (513, 16, 2), (1024, 192, 1), (1000, 64, 3)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_tables(cfa, B, ps, fresh, in_place):
     c = tables_case(B, ps, B, most_fresh=fresh)
@@ -355,6 +355,10 @@ ATTN = [
     (8, 2, 128, 16, 300, [20] * 70, [1] * 70),                # 280 rows a key head: two row tiles
     (4, 1, 64, 64, 130, [64 + i for i in range(150)], [1] * 150),
     (2, 1, 128, 4096, 100, [4000], [1]),                      # a whole cache as one page
+    (16, 16, 64, 64, 4000, [9000, 8500, 300], [1, 1, 1]),     # several long pieces to a block
+    (8, 8, 128, 64, 2500, [12000, 700, 11000, 40], [1, 1, 1, 1]),
+    (16, 4, 128, 64, 6000, [9000, 8000, 2000, 5000], [9, 1, 1, 6]),  # few rows and tiles in turn
+    (16, 4, 64, 32, 3000, [9000, 200, 7000, 5000], [1, 7, 40, 1]),
 ]
 
 

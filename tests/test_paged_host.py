@@ -32,7 +32,7 @@ def lib():
     ((1, 1, 32, 8, 128, 48), 2),
     ((1, 1, 32, 8, 128, 100), 2),
     ((1, 1, 32, 8, 128, (1 << 22) + 64), 2),
-    ((2049, 1, 32, 8, 128, 64), 2),
+    ((1025, 1, 32, 8, 128, 64), 2),
     ((1, (1 << 17) + 1, 32, 8, 128, 64), 2),
     ((1, 1, 2048, 8, 128, 64), 2),
 ])
