@@ -42,7 +42,7 @@ struct cfa_paged {
 
 namespace {
 
-constexpr unsigned long long kTimeoutNs = 2000000000ull;  // 2 s per device-side wait
+constexpr uint32_t kTimeoutNs = 2000000000u;  // 2 s per device-side wait
 
 cfa_status fail(cfa_status s) { return cfa::set_last_error(s); }
 
@@ -277,8 +277,8 @@ cfa_status launch_attention(cfa_paged *p, const AttnArgs &a, cudaStream_t stream
     int shared_blocks = static_cast<int>((shared + 31) / 32) * p->nkv;
     void *margs[3] = {&kp, &grid, &shared_blocks};
     const size_t pieces = static_cast<size_t>(grid) + 1;
-    return launch(cfa::paged_merge_kernel_ptr(p->D), shared_blocks + 8 * grid, 256,
-                  8u * (static_cast<size_t>(a.n_seqs) + 1) + pieces * 32 * 8, stream, margs);
+    return launch(cfa::paged_merge_kernel_ptr(p->D), shared_blocks + 8 * grid, 256, pieces * 32 * 8, stream,
+                  margs);
 }
 
 }  // namespace
@@ -325,19 +325,20 @@ cfa_paged *cfa_paged_create(int max_seqs, int max_tokens, int n_heads, int n_kv_
     p->device = device;
     p->num_sms = sms;
     const int G = n_heads / n_kv_heads;
-    p->rec_rows = cfa::paged_record_rows(
-        cfa::PagedShape{G, n_kv_heads, 0, sms},
-        std::min(static_cast<long long>(max_tokens) * G, static_cast<long long>(max_seqs) * cfa::kPagedAloneRows));
+    const long long shared = std::min(static_cast<long long>(max_tokens) * G,
+                                      static_cast<long long>(max_seqs) * cfa::kPagedAloneRows);
+    p->rec_rows = cfa::paged_record_rows(cfa::PagedShape{G, n_kv_heads, 0, sms}, shared);
+    // (the merge's blocks of 32 rows read whole)
+    const size_t plan_ints = cfa::kPagedPlanInts + 8 * (static_cast<size_t>(sms) + static_cast<size_t>(shared) + 31);
     if (cudaFuncSetAttribute(cfa::paged_tables_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(sizeof(int)) * (3 * cfa::kPagedMaxSeqs + 2)) != cudaSuccess ||
         cudaFuncSetAttribute(cfa::paged_attention_kernel_ptr(head_dim), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              cfa::paged_attention_smem(head_dim, cfa::kPagedMaxSeqs)) != cudaSuccess ||
         cudaFuncSetAttribute(cfa::paged_merge_kernel_ptr(head_dim), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             8 * (cfa::kPagedMaxSeqs + 1) + (sms + 1) * 32 * 8) != cudaSuccess ||
+                             (sms + 1) * 32 * 8) != cudaSuccess ||
         cudaMalloc(&p->words, 2 * sizeof(unsigned)) != cudaSuccess ||
         cudaMemset(p->words, 0, 2 * sizeof(unsigned)) != cudaSuccess ||
-        cudaMalloc(&p->plan_ws, sizeof(int) * (cfa::kPagedPlanInts + 2 * (static_cast<size_t>(max_seqs) + 1))) !=
-            cudaSuccess ||
+        cudaMalloc(&p->plan_ws, sizeof(int) * plan_ints) != cudaSuccess ||
         cudaMalloc(&p->rec_o, sizeof(float) * static_cast<size_t>(p->rec_rows) * head_dim) != cudaSuccess ||
         cudaMalloc(&p->rec_ml, sizeof(float2) * static_cast<size_t>(p->rec_rows)) != cudaSuccess) {
         cudaGetLastError();

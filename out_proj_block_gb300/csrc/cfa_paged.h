@@ -65,17 +65,34 @@ struct PagedAttnParams {
     uint16_t *out;              // [T][n_heads][d]
     float *lse;                 // [T][n_heads] or null
     unsigned *status;
-    int *plan_ws;               // the scan's totals (kPagedPlanInts) and arrays, for the merge
+    int *plan_ws;               // for the merge: the scan's totals, every run's PagedCut, every
+                                // shared row's PagedRow
     float *rec_o;               // records: unnormalised outputs, a piece's rows in 16-byte chunks,
                                 // [D / 4][rows][4]
     float2 *rec_ml;             // and each row's maximum (base 2) and sum
     int T, B, n_heads, n_kv, page_size, n_pages, width, prefix_len;
     int box_rows;               // cache rows of one TMA box
     float scale_log2;           // scale * log2(e)
-    unsigned long long timeout_ns;
+    uint32_t timeout_ns;
 };
 
-constexpr int kPagedThreads = 384;    // 8 compute warps; two load warps, an address and a prep warp
+// 8 compute warps; two load warps, an address, a prep, two MMA warps, a merge-rows warp, one idle
+constexpr int kPagedThreads = 512;
 constexpr int kPagedPlanInts = 8;
+
+// The tile of a request that is alone which a run's end cuts for the first time.
+struct PagedCut {
+    int rows;  // 0: none
+    int row0, tok0, h, last_run, unused[3];
+};
+
+// A shared row.
+struct PagedRow {
+    int out_row;           // output row with key head 0
+    int unit, head_units;  // first unit of its own keys' item, and units of a key head
+    int blocks;            // the item's blocks
+    int rec, head_rows;    // record row of the item (run 0, key head 0), and rows of a key head
+    int rows, row;         // rows of the item's tile, and this one among them
+};
 
 }  // namespace cfa

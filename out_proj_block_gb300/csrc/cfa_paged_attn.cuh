@@ -10,23 +10,26 @@
 //
 // One launch of one block per SM works through the runs of cfa_paged_split.h,
 // and a second one merges the records of rows whose keys several pieces hold.
-// A load warp streams K and V through one ring of 128-key stages (TMA boxes of
-// 64 dims with 128-byte swizzle, each inside one page); what the other warps do
-// with a stage depends on how many query rows the piece has:
-//   up to 16 rows   eight warps, 16 keys each, on mma.sync with a running max
-//                   and sum per warp, joined in shared memory at the piece's
-//                   end: the bytes of the keys bound it, and the 16-row
-//                   instruction wastes least on a few rows
+// Two load warps stream K and V through rings of 128-key stages (TMA boxes of
+// 64 dims with 128-byte swizzle, each inside one page); what the two compute
+// warpgroups do with a stage depends on how many query rows the piece has:
+//   up to 16 rows   the piece goes to one warpgroup, the next one to the other, so
+//                   that one streams while the other begins or ends a piece: four
+//                   warps, 32 keys of a block each, on mma.sync with a running max
+//                   and sum per warp, joined in shared memory at the piece's end.
+//                   The bytes of the keys bound it, and the 16-row instruction wastes
+//                   least on a few rows
 //   up to 128 rows  tcgen05, one tile of queries; even blocks of keys go to one
 //                   warpgroup and odd ones to the other, each with its own
-//                   scores and outputs in TMEM, so that one's softmax runs
-//                   under the other's products
+//                   scores and outputs in TMEM
 //   up to 256 rows  tcgen05, two tiles of queries, one to a warpgroup, on the
 //                   same keys
-// On tcgen05: S = Q K^T (M = 128 rows, N = 128 keys), a thread per row takes its
-// scores from TMEM, writes the weights back over them as bf16, and O += P V reads
-// them from there. A row's maximum is followed lazily: O is rescaled only when
-// it grew by more than 8 (a factor 2^8, far inside fp32), which is rare.
+// On tcgen05 a block's keys go in two halves: S = Q K^T (M = 128 rows, N = 64
+// keys) of the next half runs while a thread per row takes this half's scores from
+// TMEM and writes the weights back over them as bf16; O += P V reads them there. A
+// warpgroup has an MMA warp of its own. A row's maximum is followed lazily: O is
+// rescaled only when it grew by more than 8 (a factor 2^8, far inside fp32), which
+// is rare.
 //
 // Weights are rounded to bf16 for the product with V (tensor cores take both
 // operands in one type; 2^-8 each, the size of the result's own rounding); their
@@ -93,14 +96,22 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Register share of the calling warpgroup. The block is launched with 384 x 168 =
-// 64,512; the two compute warpgroups take 208 a thread and the third keeps 88:
-// 128 x (208 + 208 + 88) = 64,512.
+// Register share of the calling warpgroup. The block is launched with 512 x 128 =
+// 65,536; the two compute warpgroups take 176 a thread and the others keep 80:
+// 128 x (176 + 176 + 80 + 80) = 65,536.
 __device__ __forceinline__ void registers_for_compute() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
 }
 __device__ __forceinline__ void registers_for_issue() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+}
+
+// 2^x by the hardware's base-2 exponential (relative error about 2^-22), results below
+// 2^-126 flushed to 0: one instruction, where the form that keeps them takes four.
+__device__ __forceinline__ float exp2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // Two fp32 lanes in one instruction.
@@ -180,11 +191,28 @@ struct PagedSmem {
 };
 static_assert(sizeof(PagedPiece) <= 128, "a piece fits its slot");
 
-// The bounded wait behind a first poll that failed: out of line, because the kernel's
-// many waits would otherwise crowd its loops out of the instruction cache.
-static __device__ __noinline__ bool paged_wait_slow(uint32_t bar, uint32_t parity, unsigned long long timeout_ns,
-                                                    volatile int *timed_out, unsigned *status, unsigned site) {
-    return mbar_wait_bounded<false>(bar, parity, timeout_ns, timed_out, status, site);
+// The library's bounded wait in few instructions: the kernel's many waits would otherwise
+// crowd its loops out of the instruction cache, and a call in their place keeps the
+// compiler from giving the warpgroups different registers.
+__device__ __forceinline__ uint32_t timer_lo_ns() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+template <typename Done>
+__device__ __forceinline__ bool paged_wait(Done done, uint32_t timeout_ns, volatile int *timed_out, unsigned *status,
+                                           unsigned site) {
+    if (done()) return true;
+    const uint32_t t0 = timer_lo_ns();
+    CFA_ROLLED while (!done()) {
+        if (*timed_out) return false;
+        if (timer_lo_ns() - t0 > timeout_ns) {
+            *timed_out = 1;
+            atomicOr(status, kStatusTimeoutBit | (site << kStatusSiteShift));
+            return false;
+        }
+    }
+    return true;
 }
 
 // A count that one thread raises and others wait for, within the same bound as a barrier.
@@ -196,20 +224,6 @@ __device__ __forceinline__ uint32_t paged_count(const int *count) {
     asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(smem_addr(count)) : "memory");
     return v;
 }
-static __device__ __noinline__ uint32_t paged_wait_count(const int *count, uint32_t least, unsigned long long timeout_ns,
-                                                         volatile int *timed_out, unsigned *status, unsigned site) {
-    uint32_t v = paged_count(count);
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t i = 1; v < least && !*timed_out; ++i) {
-        v = paged_count(count);
-        if ((i & 63u) == 0u && global_timer_ns() - t0 > timeout_ns) {
-            *timed_out = 1;
-            atomicOr(status, kStatusTimeoutBit | (site << kStatusSiteShift));
-        }
-    }
-    return v;
-}
-
 template <bool V>
 struct PagedFlag {
     static constexpr bool value = V;
@@ -234,8 +248,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     const uint32_t base = smem_addr(smem);
     const uint32_t ring = base + S::kRing;
     const uint32_t bar_full = base + S::kBars, bar_empty = bar_full + 16 * NS;  // K's stages, then V's
-    const uint32_t bar_both = bar_empty + 16 * NS, bar_s = bar_both + 8, bar_o = bar_s + 16,
-                   bar_drain = bar_o + 16, bar_piece = bar_drain + 16, bar_piece_free = bar_piece + 8 * kPagedSlots,
+    const uint32_t bar_both = bar_empty + 16 * NS, bar_q = bar_both + 8, bar_s = bar_q + 8, bar_p = bar_s + 32,
+                   bar_drain = bar_p + 32, bar_piece = bar_drain + 16, bar_piece_free = bar_piece + 8 * kPagedSlots,
                    bar_entry = bar_piece_free + 8 * kPagedSlots, bar_entry_free = bar_entry + 8 * kPagedGroups;
     int *misc = reinterpret_cast<int *>(smem + S::kMisc);
     volatile int *timed_out = misc;
@@ -255,13 +269,14 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         CFA_ROLLED for (int g = 0; g < kPagedSlots; ++g) {
             mbar_init(bar_piece + 8 * g, 1);
-            mbar_init(bar_piece_free + 8 * g, kComputeWarps);
+            mbar_init(bar_piece_free + 8 * g, kComputeWarps + 2);
         }
         mbar_init(bar_both, kComputeThreads);
-        for (int w = 0; w < 2; ++w) {
+        mbar_init(bar_q, kComputeThreads);
+        for (int w = 0; w < 2; ++w) mbar_init(bar_drain + 8 * w, 1);
+        for (int w = 0; w < 4; ++w) {  // warpgroup and half
             mbar_init(bar_s + 8 * w, 1);
-            mbar_init(bar_o + 8 * w, 1);
-            mbar_init(bar_drain + 8 * w, 1);
+            mbar_init(bar_p + 8 * w, 4);
         }
         *timed_out = 0;
         misc[4] = misc[5] = 0;
@@ -276,8 +291,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     const int B = p.B, G = shape.G;
     PagedPlan plan;
     {
-        long long *sums_u = reinterpret_cast<long long *>(misc + 8);  // [10]
-        int *sums_t = misc + 32;                                      // [10]
+        long long *sums_u = reinterpret_cast<long long *>(misc + 8);  // a warp each
+        int *sums_t = misc + 40;
         const int per = (B + kPagedThreads - 1) / kPagedThreads;
         const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
         long long u = 0;
@@ -325,13 +340,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         plan = paged_plan(shape, all_u, all_t, !bad);
         tcgen05_fence_after();
         __syncthreads();
-        if (blockIdx.x == 0) {
-            int *ws = p.plan_ws;
-            if (tid == 0) {
-                *reinterpret_cast<PagedPlan *>(ws) = plan;
-                if (!plan.valid || flags) atomicOr(p.status, kStatusBadLengthBit);
-            }
-            for (int i = tid; i < 2 * (B + 1); i += kPagedThreads) ws[kPagedPlanInts + i] = start[i];
+        if (blockIdx.x == 0 && tid == 0) {
+            *reinterpret_cast<PagedPlan *>(p.plan_ws) = plan;
+            if (!plan.valid || flags) atomicOr(p.status, kStatusBadLengthBit);
         }
     }
     grid_dependents_launch();
@@ -342,12 +353,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     const int u1 = static_cast<int>(min(first + plan.share, static_cast<long long>(plan.units)));
     auto get = [&](int b) { return paged_request(p, b); };
     auto wait = [&](uint32_t bar, uint32_t parity, unsigned site) {
-        return mbar_try_wait(bar, parity) || paged_wait_slow(bar, parity, p.timeout_ns, timed_out, p.status, site);
+        return paged_wait([&]() { return mbar_try_wait(bar, parity); }, p.timeout_ns, timed_out, p.status, site);
     };
     // The same for a warp as a whole.
     auto wait_warp = [&](uint32_t bar, uint32_t parity, unsigned site) {
-        return __all_sync(~0u, mbar_try_wait(bar, parity)) ||
-               __all_sync(~0u, paged_wait_slow(bar, parity, p.timeout_ns, timed_out, p.status, site));
+        return __all_sync(~0u, wait(bar, parity, site));
     };
     // Block n of the run lies in stage n % NS of each ring (K: 0, V: 1), in its n / NS-th pass.
     auto slot_of = [&](int v, uint32_t n) { return v * NS + n % NS; };
@@ -454,16 +464,19 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_entry + 8 * (g % kPagedGroups));
             }
-        } else {
+        } else if (warp == kComputeWarps + 3) {
             // ---------------------------------------------------------- prep warp
             // Lays pieces out ahead: their numbers, where each row's query and result lie,
             // and the queries themselves where they are few. A piece without blocks ends the run.
             bool more = true;
             int u = u0;
+            PagedCut cut{};  // the tile that the run's end cuts, for the merge
             for (uint32_t k = 0; more; ++k) {
                 PagedPiece x;
                 more = paged_next(shape, plan, start, B, u, u1, get, x);
                 if (!more) x.b0 = x.b1 = x.rows = 0;
+                else if (x.req >= 0 && paged_alone(shape, x.r.n) && x.b0 == 0 && x.b1 < x.blocks)
+                    cut = PagedCut{x.rows, x.row0, x.r.tok0, x.h, paged_last_run(plan, x.first_unit, x.blocks, x.cost), {0, 0, 0}};
                 if (__any_sync(~0u, k >= kPagedSlots && !wait(bar_piece_free + 8 * (k % kPagedSlots),
                                                               (k / kPagedSlots - 1) & 1, kSiteStageEmpty)))
                     break;
@@ -499,23 +512,125 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_piece + 8 * (k % kPagedSlots));
             }
+            if (lane == 0) *reinterpret_cast<PagedCut *>(p.plan_ws + kPagedPlanInts + 8 * run) = cut;
+        } else if (warp < kComputeWarps + 6) {
+            // ------------------------------------------- MMA warps, one for a warpgroup
+            const int w = warp - (kComputeWarps + 4);
+            const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
+            const uint32_t d_s = tm + 128 * w, d_o = tm + 256 + D * w, bs = bar_s + 16 * w, bp = bar_p + 16 * w;
+            uint32_t n = 0, queries = 0, weights = 0;  // the piece's first block; phases
+            for (uint32_t k_piece = 0;; ++k_piece) {
+                const uint32_t at_slot = k_piece % kPagedSlots;
+                if (!wait_warp(bar_piece + 8 * at_slot, (k_piece / kPagedSlots) & 1, kSiteStageFull)) break;
+                const PagedPiece *x = reinterpret_cast<const PagedPiece *>(smem + S::kSlots + at_slot * S::kSlot);
+                const int nb = uniform(x->b1 - x->b0), rows = uniform(x->rows);
+                __syncwarp();
+                if (elect_one()) mbar_arrive(bar_piece_free + 8 * at_slot);
+                __syncwarp();
+                if (nb == 0) break;
+                if (rows > kPagedSmallRows) {
+                    wait_warp(bar_q, queries++ & 1, kSiteQExchange);
+                    tcgen05_fence_after();
+                    const bool split = rows <= 128;
+                    const int step = split ? 2 : 1, first_block = split ? w : 0;
+                    const uint32_t q = base + S::kQ + (split ? 0 : w * S::kQTile), arrivals = split ? 3 : 1;
+                    // scores of half h of block j (64 of the stage's rows: 8192 bytes on)
+                    auto scores = [&](int j, int h) {
+                        const uint32_t k = stage_at(0, n + j) + 8192 * h;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int ks = 0; ks < D / 16; ++ks)  // 32 bytes a step
+                                umma_bf16(d_s + 64 * h, umma_smem_desc(q + (ks >> 2) * S::kHalf, 16, 1024) + 2 * (ks & 3),
+                                          umma_smem_desc(k + (ks >> 2) * S::kHalf, 16, 1024) + 2 * (ks & 3),
+                                          umma_idesc_bf16(128, 64, false, false), ks > 0);
+                            umma_commit(bs + 8 * h);
+                            if (h == 1) {  // the keys are read
+                                mbar_arrive_n(bar_empty + 8 * slot_of(0, n + j), arrivals);
+                                umma_commit(bar_empty + 8 * slot_of(0, n + j));
+                            }
+                        }
+                        __syncwarp();
+                    };
+                    auto ready = [&](int v, int j) {
+                        wait_warp(bar_full + 8 * slot_of(v, n + j), ((n + j) / NS) & 1, kSiteStageFull);
+                        tcgen05_fence_after();
+                    };
+                    if (first_block < nb) {
+                        ready(0, first_block);
+                        scores(first_block, 0);
+                        scores(first_block, 1);
+                    }
+                    CFA_ROLLED for (int j = first_block; j < nb; j += step, ++weights) {
+                        ready(1, j);
+                        const bool more = j + step < nb;
+                        CFA_ROLLED for (int h = 0; h < 2; ++h) {
+                            wait_warp(bp + 8 * h, weights & 1, kSiteSoftmaxExchange);
+                            tcgen05_fence_after();
+                            const uint64_t vd = umma_smem_desc(stage_at(1, n + j) + 8192 * h, S::kHalf, 1024);
+                            if (elect_one()) {
+#pragma unroll
+                                for (int ks = 0; ks < 4; ++ks)  // 16 rows of 128 bytes a step
+                                    umma_bf16_ts(d_o, d_s + 64 * h + 8 * ks, vd + 128 * ks, umma_idesc_bf16(128, D, false, true),
+                                                 j > first_block || h > 0 || ks > 0);
+                                if (h == 1) {  // the values are read
+                                    mbar_arrive_n(bar_empty + 8 * slot_of(1, n + j), arrivals);
+                                    umma_commit(bar_empty + 8 * slot_of(1, n + j));
+                                }
+                                // behind the last blocks' values there are no more scores, but the
+                                // warpgroup still learns that the products are done
+                                if (!more) umma_commit(bs + 8 * h);
+                            }
+                            __syncwarp();
+                            if (more) {
+                                if (h == 0) ready(0, j + step);
+                                scores(j + step, h);
+                            }
+                        }
+                    }
+                }
+                n += nb;
+            }
+            if (elect_one() && *timed_out) {
+                // a wait gave up: the products in flight end before the block does
+                umma_commit(bar_drain + 8 * w);
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait(bar_drain + 8 * w, 0) &&
+                       global_timer_ns() - t0 < kDrainTimeoutFactor * p.timeout_ns) {
+                }
+            }
+            __syncwarp();
+        } else if (warp == kComputeWarps + 6) {
+            // --------------------------------------------------------- merge-rows warp
+            // For the merge: where each shared row's result goes and its own keys' item.
+            for (int r = run * 32 + lane; r < plan.shared_rows; r += shape.grid * 32) {
+                const int b = paged_find(stok, B, r / G);
+                const PagedRequest q = paged_request(p, b);
+                const int all = q.n * G, mine = r - stok[b] * G, tile = paged_own_tile(all);
+                const int row0 = mine / tile * tile, blocks = paged_cdiv(q.len, kPagedKeys);
+                const int cost = paged_cost(1), per_head = (start[b + 1] - start[b]) / p.n_kv;
+                PagedRow d;
+                d.out_row = (q.tok0 + mine / G) * p.n_heads + mine % G;
+                d.unit = plan.prefix_units + start[b] + row0 / tile * blocks * cost;
+                d.head_units = per_head;
+                d.blocks = blocks;
+                d.rec = static_cast<int>(paged_shared_record(shape, plan, b, 0, row0, q.n, stok[b], 0));
+                d.head_rows = all;
+                d.rows = min(tile, all - row0);
+                d.row = mine - row0;
+                reinterpret_cast<PagedRow *>(p.plan_ws + kPagedPlanInts + 8 * shape.grid)[r] = d;
+            }
         }
     } else {
         // ---------------------------------------------------------- compute warps
         registers_for_compute();
         const int wg = warp >> 2, wtid = tid & 127;
-        uint32_t n = 0, scored = 0, done = 0, met = 0;  // the piece's first block; phases
+        uint32_t n = 0, scored = 0, met = 0;  // the piece's first block; phases
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lanes of this warp
-        const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
         auto wg_bar = [&]() { asm volatile("bar.sync %0, 128;" :: "r"(2 + wg) : "memory"); };
         // Both warpgroups meet; bounded, as one of them may have given up.
         auto meet = [&]() {
             mbar_arrive(bar_both);
             wait(bar_both, met++ & 1, kSiteKvExchange);
-        };
-        auto release = [&](int v, uint32_t block, uint32_t arrivals) {  // once the products issued so far have read it
-            mbar_arrive_n(bar_empty + 8 * slot_of(v, block), arrivals);
-            umma_commit(bar_empty + 8 * slot_of(v, block));
         };
         for (uint32_t k_piece = 0;; ++k_piece) {
             // one thread's word for its warpgroup: where its wait gave up, no warp goes on alone
@@ -543,8 +658,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             const long long rec =
                 x.req >= 0 && paged_alone(shape, x.r.n)
                     ? paged_alone_record(shape, plan, x.b0, run)
-                    : paged_shared_record(shape, plan, x.req, x.h, x.row0, x.rows,
-                                          x.req < 0 ? 0 : stok[x.req], run);
+                    : paged_shared_record(shape, plan, x.req, x.h, x.row0, x.r.n, x.req < 0 ? 0 : stok[x.req], run);
             float *rec_o = p.rec_o + rec * D;
             float2 *rec_ml = p.rec_ml + rec;
             auto query = [&](int row) {
@@ -577,7 +691,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 uint32_t issued[2] = {0, 0};
                 auto wait_issued = [&](int v, uint32_t block) {
                     if (issued[v] <= block)
-                        issued[v] = paged_wait_count(misc + 4 + v, block + 1, p.timeout_ns, timed_out, p.status, kSiteStageFull);
+                        paged_wait([&]() { return (issued[v] = paged_count(misc + 4 + v)) > block; }, p.timeout_ns,
+                                   timed_out, p.status, kSiteStageFull);
                 };
                 // own keys that rows r0 and r0 + 8 see
                 const int see0 = paged_visible(x.r, (x.row0 + r0) / G);
@@ -634,7 +749,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
                         const float f0 = n0 == -INFINITY ? 0.f : n0, f1 = n1 == -INFINITY ? 0.f : n1;
                         if (__any_sync(~0u, n0 != m0 || n1 != m1)) {
-                            const float g0 = fast_exp2(m0 - f0), g1 = fast_exp2(m1 - f1);
+                            const float g0 = exp2_ftz(m0 - f0), g1 = exp2_ftz(m1 - f1);
                             l0 *= g0;
                             l1 *= g1;
 #pragma unroll
@@ -648,8 +763,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         for (int t = 0; t < 4; ++t)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                s[t][e] = fast_exp2(s[t][e] - f0);
-                                s[t][2 + e] = fast_exp2(s[t][2 + e] - f1);
+                                s[t][e] = exp2_ftz(s[t][e] - f0);
+                                s[t][2 + e] = exp2_ftz(s[t][2 + e] - f1);
                                 l0 += s[t][e];
                                 l1 += s[t][2 + e];
                             }
@@ -731,7 +846,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float g = fast_exp2(w[k].x - f);
+                        const float g = exp2_ftz(w[k].x - f);
                         l += g * w[k].y;
                         a.x += g * v[k].x; a.y += g * v[k].y; a.z += g * v[k].z; a.w += g * v[k].w;
                     }
@@ -750,8 +865,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
 
             // ---- tcgen05
-            // a warpgroup's first warp issues its products: scores of the next block behind
-            // the values of this one, which read the weights that lie over the scores
             const bool split = x.rows <= 128;
             meet();  // the scratch and the query tiles are free
             // asynchronous copies: all of them on their way before the first has landed
@@ -766,142 +879,105 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             cp_async_wait_all();
             fence_proxy_async_smem();
             tcgen05_fence_before();
-            meet();
-            const int step = split ? 2 : 1, first_block = split ? wg : 0;
-            const uint32_t q_tile = base + S::kQ + (split ? 0 : wg * S::kQTile);
-            auto scores = [&](int j) {
-                const uint32_t block = n + j, k = stage_at(0, block);
-                wait_warp(bar_full + 8 * slot_of(0, block), (block / NS) & 1, kSiteStageFull);
-                tcgen05_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)  // 32 bytes a step
-                        umma_bf16(tm + 128 * wg, umma_smem_desc(q_tile + (ks >> 2) * S::kHalf, 16, 1024) + 2 * (ks & 3),
-                                  umma_smem_desc(k + (ks >> 2) * S::kHalf, 16, 1024) + 2 * (ks & 3),
-                                  umma_idesc_bf16(128, kPagedKeys, false, false), ks > 0);
-                    umma_commit(bar_s + 8 * wg);
-                    release(0, block, split ? 3 : 1);
-                }
-                __syncwarp();
-            };
-            if ((warp & 3) == 0 && first_block < nb) scores(first_block);
+            mbar_arrive(bar_q);
 
+            const int step = split ? 2 : 1, first_block = split ? wg : 0;
             const int row = (split ? 0 : 128 * wg) + 32 * (warp & 3) + lane;
             const bool live = row < x.rows;
             const bool warp_live = (row & ~31) < x.rows;
             const int see = x.req < 0 ? 0 : paged_visible(x.r, (x.row0 + min(row, x.rows - 1)) / G);
             const uint32_t t_s = tmem + lanes + 128 * wg, t_o = tmem + lanes + 256 + D * wg;
+            const uint32_t bs = bar_s + 16 * wg, bp = bar_p + 16 * wg;
             float m = -INFINITY, l = 0.f;
             bool begun = false;
-            CFA_ROLLED for (int j = first_block; j < nb; j += step) {
+            CFA_ROLLED for (int j = first_block; j < nb; j += step, ++scored) {
                 int key0;
                 const int keys = block_keys(x, x.b0 + j, &key0);
-                const int lim = x.b0 + j < x.prefix_blocks ? keys : min(keys, see - key0);
-                wait(bar_s + 8 * wg, scored++ & 1, kSiteSoftmaxExchange);
-                __syncwarp();
-                tcgen05_fence_after();
-                if (warp_live) {
-                    // two passes over the scores in TMEM, 32 columns at a time: keeping a row's 128 in
-                    // registers spills
-                    uint32_t s[2][32];
-                    if (!__all_sync(~0u, lim >= kPagedKeys)) {  // the hidden scores become -inf
-                        CFA_ROLLED for (int c = 0; c < kPagedKeys; c += 32) {
-                            tmem_ld_x32(t_s + c, s[0]);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) s[0][e] = c + e < lim ? s[0][e] : 0xff800000u;
-                            tmem_st_x16(t_s + c, s[0]);
-                            tmem_st_x16(t_s + c + 16, s[0] + 16);
+                int lim = x.b0 + j < x.prefix_blocks ? keys : min(keys, see - key0);
+                CFA_ROLLED for (int h = 0; h < 2; ++h, lim -= 64) {
+                    wait(bs + 8 * h, scored & 1, kSiteSoftmaxExchange);
+                    __syncwarp();
+                    tcgen05_fence_after();
+                    if (h == 0 && keys < kPagedKeys) {
+                        // rows past the keys may hold anything, and 0 times NaN is NaN
+                        wait_full(1, n + j);
+                        const int z = max(keys, 0);
+                        CFA_ROLLED for (int i = wtid; i < (kPagedKeys - z) * (D / 8); i += 128) {
+                            const int r = z + i / (D / 8), c = i % (D / 8);
+                            *reinterpret_cast<uint4 *>(smem + S::kRing + slot_of(1, n + j) * S::kStage + (c >> 3) * S::kHalf +
+                                                       r * 128 + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
                         }
-                        tmem_wait_st();
+                        fence_proxy_async_smem();
                     }
-                    float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    tmem_ld_x32(t_s, s[0]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    if (warp_live) {
+                        uint32_t s[64];
+                        tmem_ld_x32(t_s + 64 * h, s);
+                        tmem_ld_x32(t_s + 64 * h + 32, s + 32);
                         tmem_wait_ld();
-                        if (c < 3) tmem_ld_x32(t_s + 32 * (c + 1), s[(c + 1) & 1]);
+                        if (!__all_sync(~0u, lim >= 64)) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            a[(e >> 1) & 3] = fmaxf(fmaxf(a[(e >> 1) & 3], __uint_as_float(s[c & 1][e])),
-                                                    __uint_as_float(s[c & 1][e + 1]));
-                    }
-                    tmem_ld_x32(t_s, s[0]);
-                    const float top = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * p.scale_log2;
-                    if (__any_sync(~0u, top > m + 8.f || (m == -INFINITY && top > m))) {
-                        // rescale to the new maximum (m = -inf: nothing is there yet)
-                        const float mn = fmaxf(m, top);
-                        const float g = m == mn ? 1.f : fast_exp2(m - mn);
-                        m = mn;
-                        l *= g;
-                        if (begun) {
+                            for (int c = 0; c < 64; ++c) s[c] = c < lim ? s[c] : 0xff800000u;
+                        }
+                        float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int c = 0; c < 64; c += 2)
+                            a[(c >> 1) & 3] = fmaxf(fmaxf(a[(c >> 1) & 3], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
+                        const float top = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * p.scale_log2;
+                        if (__any_sync(~0u, top > m + 8.f)) {
+                            // rescale to the new maximum (m = -inf: nothing is there yet)
+                            const float mn = fmaxf(m, top);
+                            const float g = m == mn ? 1.f : exp2_ftz(m - mn);
+                            m = mn;
+                            l *= g;
+                            if (begun) {
+                                // the other half's signal says that the last values' product is done
+                                wait(bs + 8 * (h ^ 1), (scored + h) & 1, kSiteSoftmaxExchange);
+                                __syncwarp();
+                                tcgen05_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t v[32];
-                                tmem_ld_x32(t_o + c, v);
-                                tmem_wait_ld();
+                                for (int c = 0; c < D; c += 32) {
+                                    uint32_t v[32];
+                                    tmem_ld_x32(t_o + c, v);
+                                    tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * g);
-                                tmem_st_x16(t_o + c, v);
-                                tmem_st_x16(t_o + c + 16, v + 16);
+                                    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * g);
+                                    tmem_st_x16(t_o + c, v);
+                                    tmem_st_x16(t_o + c + 16, v + 16);
+                                }
                             }
                         }
-                    }
-                    const float f = m == -INFINITY ? 0.f : -m;
-                    const uint64_t scale2 = pair_f32(p.scale_log2, p.scale_log2), f2 = pair_f32(f, f);
-                    uint64_t sum[2] = {0, 0};
+                        const float f = m == -INFINITY ? 0.f : -m;
+                        const uint64_t scale2 = pair_f32(p.scale_log2, p.scale_log2), f2 = pair_f32(f, f);
+                        uint64_t sum[2] = {0, 0};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t w[16];
-                        tmem_wait_ld();
-                        if (c < 3) tmem_ld_x32(t_s + 32 * (c + 1), s[(c + 1) & 1]);
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t w[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float2 y = unpair_f32(fma_f32x2(
-                                pair_f32(__uint_as_float(s[c & 1][2 * e]), __uint_as_float(s[c & 1][2 * e + 1])),
-                                scale2, f2));
-                            const float x0 = fast_exp2(y.x), x1 = fast_exp2(y.y);
-                            sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(x0, x1));
-                            w[e] = pack2_bf16_cvt(x0, x1);
+                            for (int e = 0; e < 16; ++e) {
+                                const float2 y = unpair_f32(fma_f32x2(
+                                    pair_f32(__uint_as_float(s[32 * c + 2 * e]), __uint_as_float(s[32 * c + 2 * e + 1])),
+                                    scale2, f2));
+                                const float x0 = exp2_ftz(y.x), x1 = exp2_ftz(y.y);
+                                sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(x0, x1));
+                                w[e] = pack2_bf16_cvt(x0, x1);
+                            }
+                            tmem_st_x16(t_s + 64 * h + 16 * c, w);
                         }
-                        tmem_st_x16(t_s + 16 * c, w);
+                        const float2 both_sums = unpair_f32(add_f32x2(sum[0], sum[1]));
+                        l += both_sums.x + both_sums.y;
+                        tmem_wait_st();
                     }
-                    const float2 both_sums = unpair_f32(add_f32x2(sum[0], sum[1]));
-                    l += both_sums.x + both_sums.y;
-                    tmem_wait_st();
-                }
-                if (keys < kPagedKeys) {
-                    // rows past the keys may hold anything, and 0 times NaN is NaN
-                    wait_full(1, n + j);
-                    const int z = max(keys, 0);
-                    CFA_ROLLED for (int i = tid & 127; i < (kPagedKeys - z) * (D / 8); i += 128) {
-                        const int r = z + i / (D / 8), c = i % (D / 8);
-                        *reinterpret_cast<uint4 *>(smem + S::kRing + slot_of(1, n + j) * S::kStage + (c >> 3) * S::kHalf +
-                                                   r * 128 + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();
-                }
-                tcgen05_fence_before();
-                wg_bar();
-                if ((warp & 3) == 0) {
-                    const uint32_t block = n + j;
-                    wait_warp(bar_full + 8 * slot_of(1, block), (block / NS) & 1, kSiteStageFull);
-                    tcgen05_fence_after();
-                    const uint64_t vd = umma_smem_desc(stage_at(1, block), S::kHalf, 1024);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int ks = 0; ks < kPagedKeys / 16; ++ks)  // 16 rows of 128 bytes a step
-                            umma_bf16_ts(tm + 256 + D * wg, tm + 128 * wg + 8 * ks, vd + 128 * ks,
-                                         umma_idesc_bf16(128, D, false, true), begun || ks > 0);
-                        release(1, block, split ? 3 : 1);
-                        if (j + step >= nb) umma_commit(bar_o + 8 * wg);
-                    }
+                    begun = true;
+                    tcgen05_fence_before();
                     __syncwarp();
-                    if (j + step < nb) scores(j + step);
+                    if (lane == 0) mbar_arrive(bp + 8 * h);
                 }
-                begun = true;
             }
-            if (begun) wait(bar_o + 8 * wg, done++ & 1, kSiteKvExchange);
+            if (begun) {
+                wait(bs, scored & 1, kSiteKvExchange);
+                wait(bs + 8, scored & 1, kSiteKvExchange);
+                ++scored;
+            }
             __syncwarp();
             tcgen05_fence_after();
             // ---- the tile's results, or its record
@@ -930,8 +1006,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     mb = ml[row].x;
                     lb = ml[row].y;
                     const float mn = fmaxf(m, mb), f = mn == -INFINITY ? 0.f : mn;
-                    ga = fast_exp2(m - f);
-                    gb = fast_exp2(mb - f);
+                    ga = exp2_ftz(m - f);
+                    gb = exp2_ftz(mb - f);
                     m = mn;
                     l = ga * l + gb * lb;
                 }
@@ -981,15 +1057,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             meet();  // the scratch and the query tiles are free again
             piece_done();
         }
-        if ((warp & 3) == 0 && elect_one() && *timed_out) {
-            // a wait gave up: the products in flight end before the block does
-            umma_commit(bar_drain + 8 * wg);
-            const uint64_t t0 = global_timer_ns();
-            while (!mbar_try_wait(bar_drain + 8 * wg, 0) &&
-                   global_timer_ns() - t0 < kDrainTimeoutFactor * p.timeout_ns) {
-            }
-        }
-        __syncwarp();
     }
     tcgen05_fence_before();
     __syncthreads();
@@ -1007,91 +1074,77 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 template <int D>
 __global__ void __launch_bounds__(256)
 paged_merge_kernel(const PagedAttnParams p, int grid, int shared_blocks) {
-    extern __shared__ int sh[];
-    constexpr int kPer = D / 32;  // chunks of a warp
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = p.B;
-    grid_dependency_wait();
-    const PagedPlan plan = *reinterpret_cast<const PagedPlan *>(p.plan_ws);
+    extern __shared__ float2 mls[];  // [pieces][32]
+    constexpr int kPer = D / 32;     // chunks of a warp
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int blk = static_cast<int>(blockIdx.x);
     const PagedShape shape{p.n_heads / p.n_kv, p.n_kv, p.prefix_len, grid};
-    const int G = shape.G;
-    const bool alone = static_cast<int>(blockIdx.x) >= shared_blocks;
-    if (!plan.valid) return;
-    if (!alone && static_cast<int>(blockIdx.x) / p.n_kv * 32 >= plan.shared_rows) return;
-    const int run = (static_cast<int>(blockIdx.x) - shared_blocks) / 8;
-    const long long end = static_cast<long long>(run + 1) * plan.share;
-    if (alone && end >= plan.units) return;
-    int *start = sh, *stok = sh + B + 1;
-    float2 *mls = reinterpret_cast<float2 *>(sh + 2 * (B + 1));  // [pieces][32]
-    for (int i = tid; i < 2 * (B + 1); i += 256) sh[i] = __ldcg(p.plan_ws + kPagedPlanInts + i);
-    __syncthreads();
-
+    const bool alone = blk >= shared_blocks;
     // pieces c0..c1 that all the lanes have, at record rows rec(c) + row, then the lane's own
-    int c0 = 0, c1 = -1, row = 0, rows = 1, h, out_row = 0;
+    int c0 = 0, c1 = -1, row = 0, rows = 1, h = 0, row0 = 0, out_row = 0;
     int d0 = 0, d1 = -1, own_row = 0, own_rows = 1;
     long long own_rec = 0;
-    bool live, skip = false;
-    PagedPiece x;
+    bool live = false, skip = false;
+    grid_dependency_wait();
+    const PagedPlan plan = *reinterpret_cast<const PagedPlan *>(p.plan_ws);
     if (alone) {
-        paged_item(shape, plan, start, B, static_cast<int>(end) - 1, [&](int b) { return paged_request(p, b); }, x);
-        c0 = run;
-        c1 = paged_last_run(plan, x.first_unit, x.blocks, x.cost);
-        // cut here for the first time?
-        if (x.req < 0 || !paged_alone(shape, x.r.n) || x.first_unit < static_cast<long long>(run) * plan.share || c1 == run)
-            return;
-        h = x.h;
-        row = (static_cast<int>(blockIdx.x) - shared_blocks) % 8 * 32 + lane;
-        rows = x.rows;
+        const int run = (blk - shared_blocks) / 8;
+        const PagedCut cut = *reinterpret_cast<const PagedCut *>(p.plan_ws + kPagedPlanInts + 8 * run);
+        row = (blk - shared_blocks) % 8 * 32 + lane;
+        rows = cut.rows;
         live = row < rows;
-        const int r = x.row0 + (live ? row : 0), i = r / G;
-        out_row = (x.r.tok0 + i) * p.n_heads + h * G + r - i * G;
+        c0 = run;
+        c1 = cut.last_run;
+        const int r = cut.row0 + row, i = r / shape.G;
+        out_row = (cut.tok0 + i) * p.n_heads + cut.h * shape.G + r - i * shape.G;
     } else {
-        h = static_cast<int>(blockIdx.x) % p.n_kv;
-        const int r = static_cast<int>(blockIdx.x) / p.n_kv * 32 + lane;
+        h = blk % p.n_kv;
+        const int r = blk / p.n_kv * 32 + lane;
+        const PagedRow d = reinterpret_cast<const PagedRow *>(p.plan_ws + kPagedPlanInts + 8 * grid)[r];
         live = r < plan.shared_rows;
-        const int tile = r / kPagedTile;
-        row = r % kPagedTile;
-        rows = paged_min(kPagedTile, plan.shared_rows - tile * kPagedTile);
+        row0 = r / kPagedTile * kPagedTile;
+        row = r - row0;
+        rows = paged_min(kPagedTile, plan.shared_rows - row0);
         if (plan.prefix_blocks > 0) {
-            const int item = plan.prefix_units / p.n_kv * h + tile * plan.prefix_blocks * kPagedMaxCost;
+            const int item = plan.prefix_units / p.n_kv * h + row0 / kPagedTile * plan.prefix_blocks * kPagedMaxCost;
             c0 = paged_first_run(plan, item);
             c1 = paged_last_run(plan, item, plan.prefix_blocks, paged_cost(rows));
         }
         if (live) {
-            const int b = paged_find(stok, B, r / G);
-            const PagedRequest q = paged_request(p, b);
-            own_rows = q.n * G;
-            own_row = r - stok[b] * G;
-            out_row = (q.tok0 + own_row / G) * p.n_heads + h * G + own_row % G;
-            own_rec = paged_shared_record(shape, plan, b, h, 0, own_rows, stok[b], 0);
-            const int nb = paged_cdiv(q.len, kPagedKeys), cost = paged_cost(own_rows);
-            if (nb > 0) {
-                const int item = plan.prefix_units + start[b] + h * nb * cost;
-                d0 = paged_first_run(plan, item);
-                d1 = paged_last_run(plan, item, nb, cost);
+            own_rows = d.rows;
+            own_row = d.row;
+            out_row = d.out_row + h * shape.G;
+            own_rec = d.rec + static_cast<long long>(h) * d.head_rows;
+            if (d.blocks > 0) {
+                d0 = paged_first_run(plan, d.unit + h * d.head_units);
+                d1 = paged_last_run(plan, d.unit + h * d.head_units, d.blocks, paged_cost(1));
             }
             skip = plan.prefix_blocks == 0 && d0 == d1;  // the piece wrote the result
         }
-        x.row0 = tile * kPagedTile;
     }
+    if (!plan.valid || !__syncthreads_or(live && !skip)) return;
     auto rec = [&](int c) {
         return alone ? paged_alone_record(shape, plan, c == c0 ? 0 : 1, c)
-                     : paged_shared_record(shape, plan, -1, h, x.row0, rows, 0, c);
+                     : paged_shared_record(shape, plan, -1, h, row0, 0, 0, c);
     };
-    if (!__syncthreads_or(live && !skip)) return;
     for (int c = c0 + warp; c <= c1; c += 8)
         mls[(c - c0) * 32 + lane] = live ? __ldcg(p.rec_ml + rec(c) + row) : make_float2(-INFINITY, 0.f);
+    float2 own = make_float2(-INFINITY, 0.f);  // the first own piece's, most often the only one
+    if (live && d0 <= d1) own = __ldcg(p.rec_ml + own_rec + static_cast<long long>(d0) * kPagedTile + own_row);
     __syncthreads();
     if (!live || skip) return;
+    auto own_ml = [&](int c) {
+        return c == d0 ? own : __ldcg(p.rec_ml + own_rec + static_cast<long long>(c) * kPagedTile + own_row);
+    };
     float m = -INFINITY, l = 0.f;
     for (int c = c0; c <= c1; ++c) m = fmaxf(m, mls[(c - c0) * 32 + lane].x);
-    for (int c = d0; c <= d1; ++c)
-        m = fmaxf(m, __ldcg(p.rec_ml + own_rec + static_cast<long long>(c) * kPagedTile + own_row).x);
+    for (int c = d0; c <= d1; ++c) m = fmaxf(m, own_ml(c).x);
     const float f = m == -INFINITY ? 0.f : m;
     float4 a[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float2 s, const float *o, int nrows, int r) {
-        const float g = fast_exp2(s.x - f);
+        const float g = exp2_ftz(s.x - f);
         l += g * s.y;
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
@@ -1102,10 +1155,8 @@ paged_merge_kernel(const PagedAttnParams p, int grid, int shared_blocks) {
     };
 #pragma unroll 4
     for (int c = c0; c <= c1; ++c) add(mls[(c - c0) * 32 + lane], p.rec_o + rec(c) * D, rows, row);
-    for (int c = d0; c <= d1; ++c) {
-        const long long at = own_rec + static_cast<long long>(c) * kPagedTile;
-        add(__ldcg(p.rec_ml + at + own_row), p.rec_o + at * D, own_rows, own_row);
-    }
+    for (int c = d0; c <= d1; ++c)
+        add(own_ml(c), p.rec_o + (own_rec + static_cast<long long>(c) * kPagedTile) * D, own_rows, own_row);
     const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
     for (int k = 0; k < kPer; ++k)

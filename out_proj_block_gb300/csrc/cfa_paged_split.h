@@ -4,10 +4,12 @@
 //
 // A request's query rows are its tokens times the G heads of a key head, token
 // major. A request with at most kPagedAloneRows rows shares: its rows join the
-// shared rows, whose tiles of 256 go over the prefix together, and one more
-// item goes over the request's own keys. A request with more rows fills tiles
-// by itself: it is alone, and each of its tiles goes over the prefix's keys and
-// its own in one item, with nothing to merge.
+// shared rows, whose tiles of 256 go over the prefix together, and further items
+// go over the request's own keys (one for all its rows, or, up to kPagedNarrowRows,
+// one for every 16: mma.sync takes 16 rows, and reads the keys again from L2
+// cheaper than a tensor-core tile is set up for a few blocks). A request with more
+// rows fills tiles by itself: it is alone, and each of its tiles goes over the
+// prefix's keys and its own in one item, with nothing to merge.
 //
 // An item is cut into blocks of 128 keys; prefix and own keys never share a
 // block. A block costs paged_cost() units, by how many rows its item has. The
@@ -35,6 +37,7 @@ constexpr int kPagedKeys = 128;       // keys of a block
 constexpr int kPagedTile = 256;       // rows of a tile
 constexpr int kPagedSmallRows = 16;   // rows that go through mma.sync
 constexpr int kPagedAloneRows = 128;  // rows up to which a request shares the prefix's tiles
+constexpr int kPagedNarrowRows = 64;  // rows up to which own keys go to tiles of 16
 constexpr int kPagedMaxCost = 3;
 
 struct PagedShape {
@@ -74,7 +77,7 @@ CFA_HD int paged_max(int a, int b) { return a > b ? a : b; }
 CFA_HD int paged_cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // Units of a block of keys for an item of so many rows.
-CFA_HD int paged_cost(int rows) { return rows <= 128 ? 2 : kPagedMaxCost; }
+CFA_HD int paged_cost(int rows) { return rows <= kPagedAloneRows ? 2 : kPagedMaxCost; }
 
 // Own keys that token i of a request sees.
 CFA_HD int paged_visible(const PagedRequest &r, int i) {
@@ -83,6 +86,8 @@ CFA_HD int paged_visible(const PagedRequest &r, int i) {
 CFA_HD bool paged_alone(const PagedShape &s, int n) {
     return static_cast<long long>(n) * s.G > kPagedAloneRows;
 }
+// Rows of the tiles in which a request that shares goes over its own keys.
+CFA_HD int paged_own_tile(int rows) { return rows <= kPagedNarrowRows ? kPagedSmallRows : kPagedAloneRows; }
 // Blocks of tile `tile` of a request that is alone; a tile whose rows see no key
 // still has one block, which finds none.
 CFA_HD int paged_alone_blocks(const PagedShape &s, const PagedRequest &r, int tile) {
@@ -94,7 +99,8 @@ CFA_HD int paged_alone_blocks(const PagedShape &s, const PagedRequest &r, int ti
 CFA_HD long long paged_request_units(const PagedShape &s, const PagedRequest &r) {
     if (r.n == 0) return 0;
     if (!paged_alone(s, r.n))
-        return static_cast<long long>(s.nkv) * paged_cdiv(r.len, kPagedKeys) * paged_cost(r.n * s.G);
+        return static_cast<long long>(s.nkv) * paged_cdiv(r.len, kPagedKeys) * paged_cost(1) *
+               paged_cdiv(r.n * s.G, paged_own_tile(r.n * s.G));
     long long u = 0;
     CFA_ROLLED for (int row = 0, t = 0; row < r.n * s.G; row += kPagedTile, ++t)
         u += paged_alone_blocks(s, r, t) * paged_cost(r.n * s.G - row);
@@ -158,9 +164,12 @@ CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const int *start
         rem = mine - x.h * per_head;
         x.row0 = 0;
         if (!paged_alone(s, x.r.n)) {
-            x.rows = x.r.n * s.G;
+            const int all = x.r.n * s.G, tile = paged_own_tile(all);
             x.prefix_blocks = 0;
             x.blocks = paged_cdiv(x.r.len, kPagedKeys);
+            x.row0 = rem / (x.blocks * paged_cost(1)) * tile;
+            rem %= x.blocks * paged_cost(1);
+            x.rows = paged_min(tile, all - x.row0);
             x.own_limit = x.r.len;
         } else {
             const int all = x.r.n * s.G;
@@ -214,12 +223,13 @@ CFA_HD int paged_last_run(const PagedPlan &p, int first_unit, int blocks, int co
 // run they meet: the rows of all the items before them plus a tile a run (so that neither the
 // next item nor the next run reaches back). Tiles of requests that are alone are cut at most at
 // a run's ends: two tiles a run, behind the others.
-CFA_HD long long paged_shared_record(const PagedShape &s, const PagedPlan &p, int req, int h, int row0,
-                                     int rows, int shared_tok0, int c) {
-    const long long before = req < 0 ? static_cast<long long>(h) * p.shared_rows + row0
+// shared_tok0: shared tokens before the request, n: its tokens (req >= 0).
+CFA_HD long long paged_shared_record(const PagedShape &s, const PagedPlan &p, int req, int h, int row0, int n,
+                                     int shared_tok0, int c) {
+    const long long before = req < 0 ? static_cast<long long>(h) * p.shared_rows
                                      : static_cast<long long>(s.nkv) * (p.shared_rows + static_cast<long long>(shared_tok0) * s.G) +
-                                           static_cast<long long>(h) * rows;
-    return before + static_cast<long long>(c) * kPagedTile;
+                                           static_cast<long long>(h) * n * s.G;
+    return before + row0 + static_cast<long long>(c) * kPagedTile;
 }
 CFA_HD long long paged_alone_record(const PagedShape &s, const PagedPlan &p, int b0, int c) {
     return 2ll * s.nkv * p.shared_rows + static_cast<long long>(s.grid) * kPagedTile +
