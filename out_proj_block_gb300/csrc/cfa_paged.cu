@@ -259,6 +259,8 @@ cfa_status launch_attention(cfa_paged *p, const AttnArgs &a, cudaStream_t stream
     kp.rec_o = p->rec_o;
     kp.rec_ml = p->rec_ml;
     kp.timeout_ns = kTimeoutNs;
+    kp.shape = cfa::PagedShape(p->nh / p->nkv, p->nkv, a.prefix_len, p->num_sms);
+    kp.by_page = cfa::FastDiv(static_cast<uint32_t>(p->ps));
     // a box of rows lies inside one page and divides a block of 128 keys
     kp.box_rows = p->ps % 128 == 0 ? 128 : p->ps % 64 == 0 ? 64 : p->ps;
     CUtensorMap tk, tv;
@@ -327,7 +329,7 @@ cfa_paged *cfa_paged_create(int max_seqs, int max_tokens, int n_heads, int n_kv_
     const int G = n_heads / n_kv_heads;
     const long long shared = std::min(static_cast<long long>(max_tokens) * G,
                                       static_cast<long long>(max_seqs) * cfa::kPagedAloneRows);
-    p->rec_rows = cfa::paged_record_rows(cfa::PagedShape{G, n_kv_heads, 0, sms}, shared);
+    p->rec_rows = cfa::paged_record_rows(cfa::PagedShape(G, n_kv_heads, 0, sms), shared);
     // (the merge's blocks of 32 rows read whole)
     const size_t plan_ints = cfa::kPagedPlanInts + 8 * (static_cast<size_t>(sms) + static_cast<size_t>(shared) + 31);
     if (cudaFuncSetAttribute(cfa::paged_tables_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,

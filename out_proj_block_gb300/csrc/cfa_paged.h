@@ -6,6 +6,8 @@
 
 #include <cuda_runtime.h>
 
+#include "cfa_paged_split.h"
+
 namespace cfa {
 
 constexpr int kPagedMaxSeqs = 1024;         // requests per call
@@ -71,6 +73,8 @@ struct PagedAttnParams {
                                 // [D / 4][rows][4]
     float2 *rec_ml;             // and each row's maximum (base 2) and sum
     int T, B, n_heads, n_kv, page_size, n_pages, width, prefix_len;
+    PagedShape shape;
+    FastDiv by_page;            // page_size
     int box_rows;               // cache rows of one TMA box
     float scale_log2;           // scale * log2(e)
     uint32_t timeout_ns;

@@ -155,6 +155,13 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(~0u, v, 0); }
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
+// Arrives on the barrier when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void prefetch_tensor_map(const void *tmap) {
+    asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
@@ -178,18 +185,19 @@ struct PagedSmem {
     static constexpr int kQTile = 128 * D * 2;
     static constexpr int kQ = 0;                                // two query tiles; scratch otherwise
     static constexpr int kRing = 2 * kQTile;
-    // a piece: its numbers, where its rows lie (int2 [256]: token and output row), then up to
-    // 16 query rows, [D / 64][16][64] swizzled
+    // a piece: its numbers, where its rows lie (int [256]: token and head of the group), then
+    // up to 16 query rows, [D / 64][16][64] swizzled
     static constexpr int kSlots = kRing + 2 * kStages * kStage;
-    static constexpr int kSlotRows = 128, kSlotQ = kSlotRows + 256 * 8, kSlot = kSlotQ + 16 * D * 2;
+    static constexpr int kSlotRows = 128, kSlotQ = kSlotRows + 256 * 4, kSlot = kSlotQ + 16 * D * 2;
     static constexpr int kMl = kSlots + kPagedSlots * kSlot;    // float2 [128]: max and sum
     static constexpr int kBars = kMl + 128 * 8;
     static constexpr int kMisc = kBars + 48 * 8;                // flags, TMEM address, scan sums
     static constexpr int kFifo = kMisc + 256;                   // the address warp's entries
-    static constexpr int kArrays = kFifo + 4 * kPagedGroups * kPagedEntry * 4;  // start, stok: int [2][B + 1]
-    static int bytes(int B) { return kArrays + 8 * (B + 1) + 1024; }
+    static constexpr int kArrays = kFifo + 4 * kPagedGroups * kPagedEntry * 4;  // PagedEntry [B + 1]
+    static int bytes(int B) { return kArrays + 16 * (B + 1) + 1024; }
 };
 static_assert(sizeof(PagedPiece) <= 128, "a piece fits its slot");
+constexpr int kPagedBars = 48;
 
 // The library's bounded wait in few instructions: the kernel's many waits would otherwise
 // crowd its loops out of the instruction cache, and a call in their place keeps the
@@ -224,16 +232,19 @@ __device__ __forceinline__ uint32_t paged_count(const int *count) {
     asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(smem_addr(count)) : "memory");
     return v;
 }
+// A row's entry in a piece's table: its token, and its head within the group above that.
+constexpr int kPagedTokenBits = 18;
+constexpr int kPagedTokenMask = (1 << kPagedTokenBits) - 1;
+static_assert(kPagedMaxTokens <= kPagedTokenMask, "a token fits its bits");
+template <int D>
+__device__ __forceinline__ const uint16_t *paged_query(const PagedAttnParams &p, int at, int h) {
+    return p.q + (at & kPagedTokenMask) * p.q_stride + (h * p.shape.G + (at >> kPagedTokenBits)) * D;
+}
+
 template <bool V>
 struct PagedFlag {
     static constexpr bool value = V;
 };
-
-__device__ __forceinline__ PagedRequest paged_request(const PagedAttnParams &p, int b) {
-    const int c0 = __ldcg(p.cu + b), c1 = __ldcg(p.cu + b + 1), len = __ldcg(p.lens + b);
-    const bool ok = len >= 0 && len <= static_cast<long long>(p.width) * p.page_size;
-    return PagedRequest{c0, c1 - c0, ok ? len : 0};
-}
 
 template <int D>
 __global__ void __launch_bounds__(kPagedThreads, 1)
@@ -254,95 +265,87 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     int *misc = reinterpret_cast<int *>(smem + S::kMisc);
     volatile int *timed_out = misc;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 1);
-    int *start = reinterpret_cast<int *>(smem + S::kArrays), *stok = start + p.B + 1;
+    PagedEntry *req = reinterpret_cast<PagedEntry *>(smem + S::kArrays);
     int *entries = reinterpret_cast<int *>(smem + S::kFifo);
     float2 *ml = reinterpret_cast<float2 *>(smem + S::kMl);
 
-    if (tid == 0) {
-        CFA_ROLLED for (int s = 0; s < 2 * NS; ++s) {
-            mbar_init(bar_full + 8 * s, 1);
-            mbar_init(bar_empty + 8 * s, 4);  // warps of a warpgroup, or arrivals and commits
-        }
-        CFA_ROLLED for (int g = 0; g < kPagedGroups; ++g) {
-            mbar_init(bar_entry + 8 * g, 1);
-            mbar_init(bar_entry_free + 8 * g, 2);
-        }
-        CFA_ROLLED for (int g = 0; g < kPagedSlots; ++g) {
-            mbar_init(bar_piece + 8 * g, 1);
-            mbar_init(bar_piece_free + 8 * g, kComputeWarps + 2);
-        }
-        mbar_init(bar_both, kComputeThreads);
-        mbar_init(bar_q, kComputeThreads);
-        for (int w = 0; w < 2; ++w) mbar_init(bar_drain + 8 * w, 1);
-        for (int w = 0; w < 4; ++w) {  // warpgroup and half
-            mbar_init(bar_s + 8 * w, 1);
-            mbar_init(bar_p + 8 * w, 4);
-        }
-        *timed_out = 0;
-        misc[4] = misc[5] = 0;
+    // a thread a barrier, with the arrivals it expects
+    if (tid < kPagedBars) {
+        const uint32_t bar = base + S::kBars + 8 * tid;
+        uint32_t count = 1;
+        if (bar >= bar_empty && bar < bar_both) count = 4;  // warps of a warpgroup, or arrivals and commits
+        if (bar == bar_both || bar == bar_q) count = kComputeThreads;
+        if (bar >= bar_p && bar < bar_drain) count = 4;
+        if (bar >= bar_piece && bar < bar_piece_free) count = 33;  // the prep warp's lanes, and their word
+        if (bar >= bar_piece_free && bar < bar_entry) count = kComputeWarps + 2;
+        if (bar >= bar_entry_free) count = 2;
+        mbar_init(bar, count);
+        if (tid < 8 && tid != 1) misc[tid] = 0;  // (misc[1]: the TMEM address)
         fence_mbar_init();
     }
     if (warp == kComputeWarps) tmem_alloc(smem_addr(tmem_slot), 512);
+    if (warp == kComputeWarps + 1 && elect_one()) {
+        prefetch_tensor_map(&tm_k);
+        prefetch_tensor_map(&tm_v);
+    }
     tcgen05_fence_before();
     grid_dependency_wait();
 
-    // ---- every block scans the requests
-    const PagedShape shape{p.n_heads / p.n_kv, p.n_kv, p.prefix_len, static_cast<int>(gridDim.x)};
+    // ---- every block scans the requests, a thread a request
+    const PagedShape &shape = p.shape;
     const int B = p.B, G = shape.G;
     PagedPlan plan;
     {
-        long long *sums_u = reinterpret_cast<long long *>(misc + 8);  // a warp each
-        int *sums_t = misc + 40;
-        const int per = (B + kPagedThreads - 1) / kPagedThreads;
-        const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
-        long long u = 0;
-        int tk = 0, bad = 0, flags = 0;
-        CFA_ROLLED for (int b = b0; b < b1; ++b) {
-            PagedRequest r = paged_request(p, b);
-            if (r.tok0 < 0 || r.n < 0 || r.n > p.T || r.tok0 > p.T - r.n) {
-                bad = 1;
-                r.n = 0;
+        int *sums = misc + 16;  // units and tokens of each warp
+        int units = 0, tokens = 0;
+        bool bad = false;
+        CFA_ROLLED for (int first = 0; first < B; first += kPagedThreads) {
+            const int b = first + tid;
+            PagedRequest r{0, 0, 0};
+            int u = 0, t = 0;
+            if (b < B) {
+                r.tok0 = __ldcg(p.cu + b);
+                r.n = __ldcg(p.cu + b + 1) - r.tok0;
+                r.len = __ldcg(p.lens + b);
+                if (r.len < 0 || r.len > static_cast<long long>(p.width) * p.page_size) {
+                    r.len = 0;
+                    if (blockIdx.x == 0) atomicOr(p.status, kStatusBadLengthBit);
+                }
+                if (r.tok0 < 0 || r.n < 0 || r.n > p.T || r.tok0 > p.T - r.n) {
+                    bad = true;
+                } else {
+                    const long long all = paged_request_units(shape, r);
+                    bad |= all > kPagedMostUnits;
+                    u = static_cast<int>(min(all, static_cast<long long>(kPagedMostUnits)));
+                    t = paged_alone(shape, r.n) ? 0 : r.n;
+                }
             }
-            if (r.len != __ldcg(p.lens + b)) flags = 1;
-            const long long ub = paged_request_units(shape, r);
-            const int tb = paged_alone(shape, r.n) ? 0 : r.n;
-            u += ub;
-            tk += tb;
+            int su = u, st = t;
+            CFA_ROLLED for (int o = 1; o < 32; o <<= 1) {
+                const int a = __shfl_up_sync(~0u, su, o), c = __shfl_up_sync(~0u, st, o);
+                if (lane >= o) su += a, st += c;
+            }
+            if (lane == 31) sums[warp] = su, sums[16 + warp] = st;
+            __syncthreads();
+            int wu = lane < 16 ? sums[lane] : 0, wt = lane < 16 ? sums[16 + lane] : 0;
+            CFA_ROLLED for (int o = 1; o < 16; o <<= 1) {
+                const int a = __shfl_up_sync(~0u, wu, o), c = __shfl_up_sync(~0u, wt, o);
+                if (lane >= o) wu += a, wt += c;
+            }
+            const int before_u = __shfl_sync(~0u, wu, (warp + 31) & 31), before_t = __shfl_sync(~0u, wt, (warp + 31) & 31);
+            if (b < B)
+                req[b] = PagedEntry{units + su - u + (warp ? before_u : 0), tokens + st - t + (warp ? before_t : 0), r.tok0, r.len};
+            units += __shfl_sync(~0u, wu, 15);
+            tokens += __shfl_sync(~0u, wt, 15);
+            if (first + kPagedThreads < B) __syncthreads();  // the sums are read
         }
-        long long su = u;
-        int st = tk;
-        CFA_ROLLED for (int o = 1; o < 32; o <<= 1) {
-            const long long a = __shfl_up_sync(~0u, su, o);
-            const int c = __shfl_up_sync(~0u, st, o);
-            if (lane >= o) su += a, st += c;
-        }
-        if (lane == 31) sums_u[warp] = su, sums_t[warp] = st;
+        if (tid == 0) req[B] = PagedEntry{units, tokens, __ldcg(p.cu + B), 0};
         bad = __syncthreads_or(bad);
-        flags = __syncthreads_or(flags);
-        long long all_u = 0;
-        int all_t = 0;
-        su -= u;
-        st -= tk;
-        CFA_ROLLED for (int w = 0; w < kPagedThreads / 32; ++w) {
-            if (w < warp) su += sums_u[w], st += sums_t[w];
-            all_u += sums_u[w];
-            all_t += sums_t[w];
-        }
-        CFA_ROLLED for (int b = b0; b < b1; ++b) {
-            PagedRequest r = paged_request(p, b);
-            if (bad) r.n = 0;
-            start[b] = static_cast<int>(su);
-            stok[b] = st;
-            su += paged_request_units(shape, r);
-            st += paged_alone(shape, r.n) ? 0 : r.n;
-        }
-        if (tid == 0) start[B] = static_cast<int>(all_u), stok[B] = all_t;
-        plan = paged_plan(shape, all_u, all_t, !bad);
+        plan = paged_plan(shape, units, tokens, !bad);
         tcgen05_fence_after();
-        __syncthreads();
         if (blockIdx.x == 0 && tid == 0) {
             *reinterpret_cast<PagedPlan *>(p.plan_ws) = plan;
-            if (!plan.valid || flags) atomicOr(p.status, kStatusBadLengthBit);
+            if (!plan.valid) atomicOr(p.status, kStatusBadLengthBit);
         }
     }
     grid_dependents_launch();
@@ -351,7 +354,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     const long long first = static_cast<long long>(run) * plan.share;
     const int u0 = static_cast<int>(min(first, static_cast<long long>(plan.units)));
     const int u1 = static_cast<int>(min(first + plan.share, static_cast<long long>(plan.units)));
-    auto get = [&](int b) { return paged_request(p, b); };
     auto wait = [&](uint32_t bar, uint32_t parity, unsigned site) {
         return paged_wait([&]() { return mbar_try_wait(bar, parity); }, p.timeout_ns, timed_out, p.status, site);
     };
@@ -429,7 +431,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 bool mine = false, end = false;
                 CFA_ROLLED for (int k = 0; k < 4 && more; ++k, ++j) {
                     if (j == x.b1) {
-                        more = paged_next(shape, plan, start, B, u, u1, get, x);
+                        more = paged_next(shape, plan, req, B, u, u1, x);
                         j = x.b0;
                     }
                     if (sub == k) {
@@ -438,7 +440,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                             int key0;
                             const int keys = block_keys(x, j, &key0);
                             boxes = keys > 0 ? (keys + box - 1) / box : 0;
-                            const int key = key0 + i * box, pg = key / p.page_size;
+                            const int key = key0 + i * box, pg = key / p.by_page;
                             if (i < boxes)
                                 id_at = (j < x.prefix_blocks ? p.prefix_table
                                                              : p.tables + static_cast<size_t>(x.req) * p.width) + pg;
@@ -473,45 +475,49 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             PagedCut cut{};  // the tile that the run's end cuts, for the merge
             for (uint32_t k = 0; more; ++k) {
                 PagedPiece x;
-                more = paged_next(shape, plan, start, B, u, u1, get, x);
+                more = paged_next(shape, plan, req, B, u, u1, x);
                 if (!more) x.b0 = x.b1 = x.rows = 0;
                 else if (x.req >= 0 && paged_alone(shape, x.r.n) && x.b0 == 0 && x.b1 < x.blocks)
                     cut = PagedCut{x.rows, x.row0, x.r.tok0, x.h, paged_last_run(plan, x.first_unit, x.blocks, x.cost), {0, 0, 0}};
+                x.final = more && paged_final(shape, x);
+                x.rec = !more ? 0
+                        : x.req >= 0 && paged_alone(shape, x.r.n)
+                            ? paged_alone_record(shape, plan, x.b0, run)
+                            : paged_shared_record(shape, plan, x.req, x.h, x.row0, x.r.n, x.req < 0 ? 0 : req[x.req].tok, run);
                 if (__any_sync(~0u, k >= kPagedSlots && !wait(bar_piece_free + 8 * (k % kPagedSlots),
                                                               (k / kPagedSlots - 1) & 1, kSiteStageEmpty)))
                     break;
                 uint8_t *slot = smem + S::kSlots + k % kPagedSlots * S::kSlot;
                 if (lane == 0) *reinterpret_cast<PagedPiece *>(slot) = x;
                 const bool few = x.rows <= kPagedSmallRows;
-                int2 *row_at = reinterpret_cast<int2 *>(slot + S::kSlotRows);
+                int *row_at = reinterpret_cast<int *>(slot + S::kSlotRows);
 #pragma unroll 2
                 for (int r = lane; r < x.rows; r += 32) {
-                    const int i = (x.row0 + r) / G;
+                    const int i = (x.row0 + r) / shape.by_G;
                     int t = x.r.tok0 + i;
                     if (x.req < 0) {
-                        const int b = paged_find(stok, B, i);
-                        t = __ldcg(p.cu + b) + i - stok[b];
+                        const int b = paged_find(B, i, [&](int k) { return req[k].tok; });
+                        t = req[b].tok0 + i - req[b].tok;
                     }
-                    row_at[r] = make_int2(t, t * p.n_heads + x.h * G + (x.row0 + r) - i * G);
+                    row_at[r] = t | ((x.row0 + r) - i * G) << kPagedTokenBits;
                 }
                 __syncwarp();
                 if (few) {
-#pragma unroll
-                    for (int c = lane; c < 16 * (D / 8); c += 32) {
+                    CFA_ROLLED for (int c = lane; c < 16 * (D / 8); c += 32) {
                         const int r = c / (D / 8), ch = c % (D / 8);
                         uint8_t *dst = slot + S::kSlotQ + (ch >> 3) * 2048 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-                        if (r < x.rows) {
-                            const int2 at = row_at[r];
-                            cp_async_16(smem_addr(dst), p.q + at.x * p.q_stride + (at.y - at.x * p.n_heads) * D + 8 * ch);
-                        } else {
+                        if (r < x.rows)
+                            cp_async_16(smem_addr(dst), paged_query<D>(p, row_at[r], x.h) + 8 * ch);
+                        else
                             *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
-                        }
                     }
-                    cp_async_wait_all();
                 }
+                // every lane's arrival follows its copies; the next piece need not wait for them
+                cp_async_arrive(bar_piece + 8 * (k % kPagedSlots));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_piece + 8 * (k % kPagedSlots));
             }
+            cp_async_wait_all();
             if (lane == 0) *reinterpret_cast<PagedCut *>(p.plan_ws + kPagedPlanInts + 8 * run) = cut;
         } else if (warp < kComputeWarps + 6) {
             // ------------------------------------------- MMA warps, one for a warpgroup
@@ -603,17 +609,16 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             // --------------------------------------------------------- merge-rows warp
             // For the merge: where each shared row's result goes and its own keys' item.
             for (int r = run * 32 + lane; r < plan.shared_rows; r += shape.grid * 32) {
-                const int b = paged_find(stok, B, r / G);
-                const PagedRequest q = paged_request(p, b);
-                const int all = q.n * G, mine = r - stok[b] * G, tile = paged_own_tile(all);
-                const int row0 = mine / tile * tile, blocks = paged_cdiv(q.len, kPagedKeys);
-                const int cost = paged_cost(1), per_head = (start[b + 1] - start[b]) / p.n_kv;
+                const int tok = r / shape.by_G, b = paged_find(B, tok, [&](int k) { return req[k].tok; });
+                const PagedRequest q = paged_request_at(req, b);
+                const int all = q.n * G, mine = r - req[b].tok * G, tile = paged_own_tile(all);
+                const int own = all > tile ? mine / tile : 0, row0 = own * tile, blocks = paged_cdiv(q.len, kPagedKeys);
                 PagedRow d;
-                d.out_row = (q.tok0 + mine / G) * p.n_heads + mine % G;
-                d.unit = plan.prefix_units + start[b] + row0 / tile * blocks * cost;
-                d.head_units = per_head;
+                d.out_row = (q.tok0 + tok - req[b].tok) * p.n_heads + r - tok * G;
+                d.unit = plan.prefix_units + req[b].unit + own * blocks * paged_cost(1);
+                d.head_units = (req[b + 1].unit - req[b].unit) / shape.by_nkv;
                 d.blocks = blocks;
-                d.rec = static_cast<int>(paged_shared_record(shape, plan, b, 0, row0, q.n, stok[b], 0));
+                d.rec = static_cast<int>(paged_shared_record(shape, plan, b, 0, row0, q.n, req[b].tok, 0));
                 d.head_rows = all;
                 d.rows = min(tile, all - row0);
                 d.row = mine - row0;
@@ -653,20 +658,16 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 piece_done();
                 continue;
             }
-            const int2 *row_at = reinterpret_cast<const int2 *>(slot + S::kSlotRows);
-            const bool final = paged_final(shape, x);
-            const long long rec =
-                x.req >= 0 && paged_alone(shape, x.r.n)
-                    ? paged_alone_record(shape, plan, x.b0, run)
-                    : paged_shared_record(shape, plan, x.req, x.h, x.row0, x.r.n, x.req < 0 ? 0 : stok[x.req], run);
-            float *rec_o = p.rec_o + rec * D;
-            float2 *rec_ml = p.rec_ml + rec;
-            auto query = [&](int row) {
-                const int2 at = row_at[row];
-                return p.q + at.x * p.q_stride + (at.y - at.x * p.n_heads) * D;
+            const int *row_at = reinterpret_cast<const int *>(slot + S::kSlotRows);
+            const bool final = x.final;
+            float *rec_o = p.rec_o + x.rec * D;
+            float2 *rec_ml = p.rec_ml + x.rec;
+            auto result_row = [&](int row) {
+                const int at = row_at[row];
+                return (at & kPagedTokenMask) * p.n_heads + x.h * G + (at >> kPagedTokenBits);
             };
             auto write_lse = [&](int row, float m, float l) {
-                if (p.lse) p.lse[row_at[row].y] = (m + log2f(l)) * 0.69314718055994531f;
+                if (p.lse) p.lse[result_row(row)] = (m + log2f(l)) * 0.69314718055994531f;
             };
 
             if (few) {
@@ -695,8 +696,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                    timed_out, p.status, kSiteStageFull);
                 };
                 // own keys that rows r0 and r0 + 8 see
-                const int see0 = paged_visible(x.r, (x.row0 + r0) / G);
-                const int see1 = paged_visible(x.r, (x.row0 + r0 + 8) / G);
+                const int see0 = paged_visible(x.r, (x.row0 + r0) / shape.by_G);
+                const int see1 = paged_visible(x.r, (x.row0 + r0 + 8) / shape.by_G);
                 const uint32_t kkey = kw + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
                 const uint32_t vkey = kw + (lane & 15), vc = lane >> 4;
                 CFA_ROLLED for (int j = 0; j < nb; ++j) {
@@ -830,9 +831,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 leave(r0, m0, l0, 0);
                 leave(r0 + 8, m1, l1, 2);
                 wg_bar();
-                CFA_ROLLED for (int i = wtid; i < x.rows * (D / 4); i += 128) {
-                    // records are chunk major, results row major
-                    const int row = final ? i / (D / 4) : i % x.rows, c = final ? i % (D / 4) : i / x.rows;
+                const int row = wtid & 15;
+                CFA_ROLLED for (int c = wtid >> 4; c < D / 4 && row < x.rows; c += 8) {
                     float2 w[4];
                     float4 v[4];
 #pragma unroll
@@ -852,7 +852,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
                     if (final) {
                         const float inv = l > 0.f ? 1.f / l : 0.f;
-                        *reinterpret_cast<uint2 *>(p.out + static_cast<size_t>(row_at[row].y) * D + 4 * c) =
+                        *reinterpret_cast<uint2 *>(p.out + static_cast<size_t>(result_row(row)) * D + 4 * c) =
                             make_uint2(pack2_bf16(a.x * inv, a.y * inv), pack2_bf16(a.z * inv, a.w * inv));
                         if (c == 0) write_lse(row, m, l);
                     } else {
@@ -873,7 +873,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const int row = i / (D / 8), c = i % (D / 8);
                 uint8_t *dst = smem + S::kQ + (row >> 7) * S::kQTile + (c >> 3) * S::kHalf + (row & 127) * 128 +
                                (((c & 7) ^ (row & 7)) << 4);
-                if (row < x.rows) cp_async_16(smem_addr(dst), query(row) + 8 * c);
+                if (row < x.rows) cp_async_16(smem_addr(dst), paged_query<D>(p, row_at[row], x.h) + 8 * c);
                 else *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
             }
             cp_async_wait_all();
@@ -885,7 +885,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             const int row = (split ? 0 : 128 * wg) + 32 * (warp & 3) + lane;
             const bool live = row < x.rows;
             const bool warp_live = (row & ~31) < x.rows;
-            const int see = x.req < 0 ? 0 : paged_visible(x.r, (x.row0 + min(row, x.rows - 1)) / G);
+            const int see = x.req < 0 ? 0 : paged_visible(x.r, (x.row0 + min(row, x.rows - 1)) / shape.by_G);
             const uint32_t t_s = tmem + lanes + 128 * wg, t_o = tmem + lanes + 256 + D * wg;
             const uint32_t bs = bar_s + 16 * wg, bp = bar_p + 16 * wg;
             float m = -INFINITY, l = 0.f;
@@ -1014,7 +1014,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
             if (warp_live && !(split && wg == 1)) {
                 const float inv = !final ? 1.f : l > 0.f ? 1.f / l : 0.f;
-                const size_t out_row = live ? static_cast<size_t>(row_at[row].y) * D : 0;
+                const size_t out_row = live ? static_cast<size_t>(result_row(row)) * D : 0;
                 if (live) {
                     if (final) write_lse(row, m, l);
                     else rec_ml[row] = make_float2(m, l);
@@ -1078,7 +1078,7 @@ paged_merge_kernel(const PagedAttnParams p, int grid, int shared_blocks) {
     constexpr int kPer = D / 32;     // chunks of a warp
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int blk = static_cast<int>(blockIdx.x);
-    const PagedShape shape{p.n_heads / p.n_kv, p.n_kv, p.prefix_len, grid};
+    const PagedShape &shape = p.shape;
     const bool alone = blk >= shared_blocks;
     // pieces c0..c1 that all the lanes have, at record rows rec(c) + row, then the lane's own
     int c0 = 0, c1 = -1, row = 0, rows = 1, h = 0, row0 = 0, out_row = 0;
@@ -1095,18 +1095,18 @@ paged_merge_kernel(const PagedAttnParams p, int grid, int shared_blocks) {
         live = row < rows;
         c0 = run;
         c1 = cut.last_run;
-        const int r = cut.row0 + row, i = r / shape.G;
+        const int r = cut.row0 + row, i = r / shape.by_G;
         out_row = (cut.tok0 + i) * p.n_heads + cut.h * shape.G + r - i * shape.G;
     } else {
-        h = blk % p.n_kv;
-        const int r = blk / p.n_kv * 32 + lane;
+        const int group = blk / shape.by_nkv, r = group * 32 + lane;
+        h = blk - group * p.n_kv;
         const PagedRow d = reinterpret_cast<const PagedRow *>(p.plan_ws + kPagedPlanInts + 8 * grid)[r];
         live = r < plan.shared_rows;
         row0 = r / kPagedTile * kPagedTile;
         row = r - row0;
         rows = paged_min(kPagedTile, plan.shared_rows - row0);
         if (plan.prefix_blocks > 0) {
-            const int item = plan.prefix_units / p.n_kv * h + row0 / kPagedTile * plan.prefix_blocks * kPagedMaxCost;
+            const int item = plan.prefix_units / shape.by_nkv * h + row0 / kPagedTile * plan.prefix_blocks * kPagedMaxCost;
             c0 = paged_first_run(plan, item);
             c1 = paged_last_run(plan, item, plan.prefix_blocks, paged_cost(rows));
         }

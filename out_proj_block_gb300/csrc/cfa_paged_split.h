@@ -40,8 +40,38 @@ constexpr int kPagedAloneRows = 128;  // rows up to which a request shares the p
 constexpr int kPagedNarrowRows = 64;  // rows up to which own keys go to tiles of 16
 constexpr int kPagedMaxCost = 3;
 
+// Division of 0 <= n < 2^31 by a divisor that the host knows: n / d = (n mul) >> (32 + shift)
+// with mul = 2^(31 + l) / d rounded up, l = ceil(log2 d), shift = l - 1; the rounding adds less
+// than n / 2^(31 + l) < 1 / d to the quotient. An integer division takes some 30 instructions.
+struct FastDiv {
+    uint32_t d = 1, mul = 0;
+    int shift = 0;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t divisor) : d(divisor) {
+        int l = 0;
+        while ((1ull << l) < divisor) ++l;
+        if (l > 0) {
+            mul = static_cast<uint32_t>(((1ull << (31 + l)) + divisor - 1) / divisor);
+            shift = l - 1;
+        }
+    }
+};
+CFA_HD int operator/(int n, const FastDiv &f) {
+    if (f.d == 1) return n;
+#ifdef __CUDA_ARCH__
+    return static_cast<int>(__umulhi(static_cast<uint32_t>(n), f.mul) >> f.shift);
+#else
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * f.mul >> 32) >> f.shift);
+#endif
+}
+
 struct PagedShape {
     int G, nkv, prefix_len, grid;
+    FastDiv by_G, by_nkv;
+    PagedShape() = default;
+    PagedShape(int G_, int nkv_, int prefix, int grid_)
+        : G(G_), nkv(nkv_), prefix_len(prefix), grid(grid_), by_G(static_cast<uint32_t>(G_)),
+          by_nkv(static_cast<uint32_t>(nkv_)) {}
 };
 
 // What one scan over the requests finds.
@@ -59,6 +89,18 @@ struct PagedRequest {
     int tok0, n, len;  // first token row, tokens, own keys
 };
 
+// A request as the scan leaves it; entry B holds the totals.
+struct alignas(16) PagedEntry {
+    int unit;  // units of the requests before it, behind the shared prefix's
+    int tok;   // tokens that share of the requests before it
+    int tok0, len;
+};
+CFA_HD PagedRequest paged_request_at(const PagedEntry *e, int b) {
+    return PagedRequest{e[b].tok0, e[b + 1].tok0 - e[b].tok0, e[b].len};
+}
+// Units that one request may have, so that 1024 of them stay below 2^31.
+constexpr int kPagedMostUnits = (1 << 21) - 1;
+
 struct PagedPiece {
     int req;            // request, or -1: the shared rows over the prefix
     int h;              // key head
@@ -69,6 +111,8 @@ struct PagedPiece {
     int b0, b1;         // the piece: blocks [b0, b1) of the item
     int first_unit;     // the item's first unit
     int cost;           // units of a block
+    int final;          // the piece writes its rows' results
+    long long rec;      // else: its first record row
     PagedRequest r;
 };
 
@@ -93,7 +137,7 @@ CFA_HD int paged_own_tile(int rows) { return rows <= kPagedNarrowRows ? kPagedSm
 CFA_HD int paged_alone_blocks(const PagedShape &s, const PagedRequest &r, int tile) {
     const int last = paged_min(r.n * s.G, (tile + 1) * kPagedTile) - 1;
     return paged_max(1, paged_cdiv(s.prefix_len, kPagedKeys) +
-                            paged_cdiv(paged_visible(r, last / s.G), kPagedKeys));
+                            paged_cdiv(paged_visible(r, last / s.by_G), kPagedKeys));
 }
 // Units of a request's own items.
 CFA_HD long long paged_request_units(const PagedShape &s, const PagedRequest &r) {
@@ -127,28 +171,27 @@ CFA_HD PagedPlan paged_plan(const PagedShape &s, long long own_units, int shared
     return p;
 }
 
-// Index of the last entry of a[0..B] (ascending, a[0] = 0) that is at most x, below B:
-// requests without units share their start with the next one and are passed over.
-CFA_HD int paged_find(const int *a, int B, int x) {
+// The last request b whose `at(b)` (ascending, at(0) = 0) is at most x: requests that add
+// nothing share theirs with the next one and are passed over.
+template <typename At>
+CFA_HD int paged_find(int B, int x, At at) {
     int lo = 0, hi = B;
     CFA_ROLLED while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a[mid] <= x) lo = mid; else hi = mid;
+        if (at(mid) <= x) lo = mid; else hi = mid;
     }
     return lo;
 }
 
-// The item that holds unit u. start[b]: units of the requests before b; get(b): request b.
-template <typename Get>
-CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const int *start, int B, int u, Get get,
-                       PagedPiece &x) {
+// The item that holds unit u, of the requests e[0..B].
+CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const PagedEntry *e, int B, int u, PagedPiece &x) {
     int rem;  // units of the item before u
     if (u < p.prefix_units) {
-        const int head_units = p.prefix_units / s.nkv, full = p.prefix_blocks * kPagedMaxCost;
+        const int head_units = p.prefix_units / s.by_nkv, full = p.prefix_blocks * kPagedMaxCost;
         x.req = -1;
         x.h = u / head_units;
         rem = u - x.h * head_units;
-        const int tile = paged_min(rem / full, p.tiles - 1);
+        const int tile = p.tiles == 1 ? 0 : paged_min(rem / full, p.tiles - 1);
         rem -= tile * full;
         x.row0 = tile * kPagedTile;
         x.rows = paged_min(kPagedTile, p.shared_rows - x.row0);
@@ -156,10 +199,10 @@ CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const int *start
         x.own_limit = 0;
         x.r = PagedRequest{0, 0, 0};
     } else {
-        x.req = paged_find(start, B, u - p.prefix_units);
-        x.r = get(x.req);
-        const int mine = u - p.prefix_units - start[x.req];
-        const int per_head = (start[x.req + 1] - start[x.req]) / s.nkv;
+        x.req = paged_find(B, u - p.prefix_units, [&](int b) { return e[b].unit; });
+        x.r = paged_request_at(e, x.req);
+        const int mine = u - p.prefix_units - e[x.req].unit;
+        const int per_head = (e[x.req + 1].unit - e[x.req].unit) / s.by_nkv;
         x.h = mine / per_head;
         rem = mine - x.h * per_head;
         x.row0 = 0;
@@ -167,8 +210,10 @@ CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const int *start
             const int all = x.r.n * s.G, tile = paged_own_tile(all);
             x.prefix_blocks = 0;
             x.blocks = paged_cdiv(x.r.len, kPagedKeys);
-            x.row0 = rem / (x.blocks * paged_cost(1)) * tile;
-            rem %= x.blocks * paged_cost(1);
+            if (all > tile) {
+                x.row0 = rem / (x.blocks * paged_cost(1)) * tile;
+                rem %= x.blocks * paged_cost(1);
+            }
             x.rows = paged_min(tile, all - x.row0);
             x.own_limit = x.r.len;
         } else {
@@ -182,22 +227,24 @@ CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const int *start
             }
             x.rows = paged_min(kPagedTile, all - x.row0);
             x.prefix_blocks = p.prefix_blocks;
-            x.own_limit = paged_visible(x.r, (x.row0 + x.rows - 1) / s.G);
+            x.own_limit = paged_visible(x.r, (x.row0 + x.rows - 1) / s.by_G);
         }
     }
     x.cost = paged_cost(x.rows);
     x.first_unit = u - rem;
 }
 
+// Blocks whose first unit lies before `units` of an item.
+CFA_HD int paged_blocks_before(int units, int cost) { return cost == 2 ? (units + 1) >> 1 : paged_cdiv(units, kPagedMaxCost); }
+
 // The next piece of the run that ends before unit `end`, from unit u on; u moves behind it.
 // False: the run has no more.
-template <typename Get>
-CFA_HD bool paged_next(const PagedShape &s, const PagedPlan &p, const int *start, int B, int &u, int end,
-                       Get get, PagedPiece &x) {
+CFA_HD bool paged_next(const PagedShape &s, const PagedPlan &p, const PagedEntry *e, int B, int &u, int end,
+                       PagedPiece &x) {
     CFA_ROLLED while (u < end) {
-        paged_item(s, p, start, B, u, get, x);
-        x.b0 = paged_cdiv(u - x.first_unit, x.cost);
-        x.b1 = paged_min(x.blocks, paged_cdiv(end - x.first_unit, x.cost));
+        paged_item(s, p, e, B, u, x);
+        x.b0 = paged_blocks_before(u - x.first_unit, x.cost);
+        x.b1 = paged_min(x.blocks, paged_blocks_before(end - x.first_unit, x.cost));
         u = paged_min(end, x.first_unit + x.blocks * x.cost);
         if (x.b0 < x.b1) return true;
     }
