@@ -786,6 +786,7 @@ class Paged:
         self.handle = cfa_paged_create(max_seqs, max_tokens, n_heads, n_kv_heads, head_dim,
                                        page_size)
         self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
 
     def close(self):
         if getattr(self, "handle", None):
@@ -825,19 +826,20 @@ class Paged:
         if st != CFA_OK:
             raise CfaError(st, "cfa_paged_set_rope")
 
-    # Argument checks; each is a few attribute reads, since the smallest calls
-    # take the GPU only microseconds.
+    # Argument checks: one expression for what is right, since the smallest calls take
+    # the GPU only microseconds; what is wrong is looked for afterwards.
 
     def _dense(self, name, t, shape, dtype):
+        if (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                and t.get_device() == self._index):
+            return t.data_ptr()
         if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if t.device != self.device:
-            raise ValueError(f"{name} must be on {self.device}")
-        return t.data_ptr()
+        raise ValueError(f"{name} must be on {self.device}")
 
     def _rows(self, name, t, n, heads):
         """Pointer and row stride of [n, heads, head_dim] with dense rows."""
@@ -849,7 +851,7 @@ class Paged:
         s = t.stride()
         if s[2] != 1 or (heads > 1 and s[1] != self.head_dim):
             raise ValueError(f"{name} must be dense within a row")
-        if t.device != self.device:
+        if t.get_device() != self._index:
             raise ValueError(f"{name} must be on {self.device}")
         return t.data_ptr(), (s[0] if n > 1 else heads * self.head_dim)
 
@@ -861,7 +863,7 @@ class Paged:
 
     def _stream(self, stream):
         if stream is None:
-            return torch._C._cuda_getCurrentRawStream(self.device.index)
+            return torch._C._cuda_getCurrentRawStream(self._index)
         return _stream(stream)
 
     def build_tables(self, lens, fresh, free_pages, pool, tables, lens_out, pool_out, cu, positions,
@@ -870,20 +872,18 @@ class Paged:
         lens, fresh, lens_out [B]; free_pages [n]; pool, pool_out [2]; tables
         [B, width]; cu [B + 1]; positions, slots [rows]. base is the prefix's
         length. Returns (cu, positions, slots)."""
-        B = lens.shape[0]
-        n = slots.shape[0]
-        if tables.dim() != 2:
-            raise ValueError("tables must be [requests, width]")
+        one, n, free = lens.shape, slots.shape, free_pages.shape
+        if len(one) != 1 or len(n) != 1 or len(free) != 1 or tables.dim() != 2:
+            raise ValueError("lens, slots and free_pages have one dimension, tables two")
+        B, width = tables.shape
+        dense = self._dense
         st = _lib.cfa_paged_tables(
-            self.handle, B, base, self._dense("lens", lens, (B,), _I32),
-            self._dense("fresh", fresh, (B,), _I32),
-            self._dense("free_pages", free_pages, (free_pages.numel(),), _I32),
-            free_pages.numel(), self._dense("pool", pool, (2,), _I32),
-            self._dense("tables", tables, (B, tables.shape[1]), _I32), tables.shape[1],
-            self._dense("lens_out", lens_out, (B,), _I32),
-            self._dense("pool_out", pool_out, (2,), _I32), self._dense("cu", cu, (B + 1,), _I32),
-            self._dense("positions", positions, (n,), _I32), self._dense("slots", slots, (n,), _I32),
-            n, self._stream(stream))
+            self.handle, B, base, dense("lens", lens, (B,), _I32), dense("fresh", fresh, one, _I32),
+            dense("free_pages", free_pages, free, _I32), free[0], dense("pool", pool, (2,), _I32),
+            dense("tables", tables, (B, width), _I32), width, dense("lens_out", lens_out, one, _I32),
+            dense("pool_out", pool_out, (2,), _I32), dense("cu", cu, (B + 1,), _I32),
+            dense("positions", positions, n, _I32), dense("slots", slots, n, _I32), n[0],
+            self._stream(stream))
         if st != CFA_OK:
             raise CfaError(st, "cfa_paged_tables")
         return cu, positions, slots

@@ -269,18 +269,12 @@ cfa_status launch_attention(cfa_paged *p, const AttnArgs &a, cudaStream_t stream
         cfa::encode_bf16_2d_ex(&tv, a.vp, d, rows, d, 64, static_cast<uint32_t>(kp.box_rows), true) != CFA_OK)
         return CFA_ERR_CUDA;
     void *args[3] = {&tk, &tv, &kp};
-    int grid = p->num_sms;
-    cfa_status st = launch(cfa::paged_attention_kernel_ptr(p->D), grid, cfa::kPagedThreads,
+    const int grid = p->num_sms;
+    const cfa_status st = launch(cfa::paged_attention_kernel_ptr(p->D), grid, cfa::kPagedThreads,
                            static_cast<size_t>(cfa::paged_attention_smem(p->D, a.n_seqs)), stream, args);
     if (st != CFA_OK) return st;
-    // rows that can share: all of them, or every request's most
-    const long long shared = std::min(static_cast<long long>(a.n_tokens) * (p->nh / p->nkv),
-                                      static_cast<long long>(a.n_seqs) * cfa::kPagedAloneRows);
-    int shared_blocks = static_cast<int>((shared + 31) / 32) * p->nkv;
-    void *margs[3] = {&kp, &grid, &shared_blocks};
-    const size_t pieces = static_cast<size_t>(grid) + 1;
-    return launch(cfa::paged_merge_kernel_ptr(p->D), shared_blocks + 8 * grid, 256, pieces * 32 * 8, stream,
-                  margs);
+    void *margs[1] = {&kp};
+    return launch(cfa::paged_merge_kernel_ptr(p->D), 3 * grid, cfa::kPagedMergeThreads, 0, stream, margs);
 }
 
 }  // namespace
@@ -325,19 +319,16 @@ cfa_paged *cfa_paged_create(int max_seqs, int max_tokens, int n_heads, int n_kv_
     p->D = head_dim;
     p->ps = page_size;
     p->device = device;
-    p->num_sms = sms;
+    p->num_sms = std::min(sms, cfa::kPagedMaxGrid);
     const int G = n_heads / n_kv_heads;
     const long long shared = std::min(static_cast<long long>(max_tokens) * G,
                                       static_cast<long long>(max_seqs) * cfa::kPagedAloneRows);
-    p->rec_rows = cfa::paged_record_rows(cfa::PagedShape(G, n_kv_heads, 0, sms), shared);
-    // (the merge's blocks of 32 rows read whole)
-    const size_t plan_ints = cfa::kPagedPlanInts + 8 * (static_cast<size_t>(sms) + static_cast<size_t>(shared) + 31);
+    p->rec_rows = cfa::paged_record_rows(cfa::PagedShape(G, n_kv_heads, 0, p->num_sms), shared);
+    const size_t plan_ints = cfa::kPagedPlanInts + 8 * (static_cast<size_t>(p->num_sms) + static_cast<size_t>(shared));
     if (cudaFuncSetAttribute(cfa::paged_tables_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(sizeof(int)) * (3 * cfa::kPagedMaxSeqs + 2)) != cudaSuccess ||
         cudaFuncSetAttribute(cfa::paged_attention_kernel_ptr(head_dim), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              cfa::paged_attention_smem(head_dim, cfa::kPagedMaxSeqs)) != cudaSuccess ||
-        cudaFuncSetAttribute(cfa::paged_merge_kernel_ptr(head_dim), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (sms + 1) * 32 * 8) != cudaSuccess ||
         cudaMalloc(&p->words, 2 * sizeof(unsigned)) != cudaSuccess ||
         cudaMemset(p->words, 0, 2 * sizeof(unsigned)) != cudaSuccess ||
         cudaMalloc(&p->plan_ws, sizeof(int) * plan_ints) != cudaSuccess ||

@@ -83,6 +83,8 @@ struct PagedAttnParams {
 // 8 compute warps; two load warps, an address, a prep, two MMA warps, a merge-rows warp, one idle
 constexpr int kPagedThreads = 512;
 constexpr int kPagedPlanInts = 8;
+constexpr int kPagedMaxGrid = 256;    // blocks of the attention kernel, one per SM
+constexpr int kPagedMergeThreads = 256;
 
 // The tile of a request that is alone which a run's end cuts for the first time.
 struct PagedCut {

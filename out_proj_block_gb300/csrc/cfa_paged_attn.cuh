@@ -1066,103 +1066,138 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
 }
 
-// Merges the records: a block for 32 rows of one key head (a lane per row), its
-// warps taking the row's 16-byte chunks in turn, pieces in the order of the
-// runs. The first blocks take the shared rows (the prefix's pieces, then the
-// request's own), the others the tiles of requests that are alone and were cut
-// at the end of run (block / 8).
+// Merges the records, a warp for 32 rows of one key head (a lane a row) and CH of
+// the row's 16-byte chunks: the shared rows (the prefix's pieces, then the
+// request's own) a chunk at a time, then the tiles of requests that are alone and
+// that a run's end cut, four at a time. Pieces are taken in the order of the runs,
+// eight at a time, so that their loads, maxima and sums among them, are on their way
+// together: the kernel is a chain of three loads (plan, row, records), and what counts
+// is that nothing else waits in between.
+template <int CH>
+struct PagedMerge {
+    float m = -INFINITY, l = 0.f;
+    float4 a[CH];
+    __device__ __forceinline__ PagedMerge() {
+#pragma unroll
+        for (int k = 0; k < CH; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    // Pieces c0..c1, whose record row for this lane is at(c), in records of `rows` rows
+    // beginning at base(c); N at a time.
+    template <int D, int N, typename Base>
+    __device__ __forceinline__ void add(const PagedAttnParams &p, int c0, int c1, int chunk, int rows, int row, Base base) {
+        for (int c = c0; c <= c1; c += N) {
+            float2 s[N];
+            float4 v[N][CH];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const bool there = c + i <= c1;
+                const long long at = base(there ? c + i : c1);
+                s[i] = __ldcg(p.rec_ml + at + row);
+                if (!there) s[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int k = 0; k < CH; ++k)
+                    v[i][k] = there ? __ldcg(reinterpret_cast<const float4 *>(
+                                          p.rec_o + at * D + (static_cast<size_t>(chunk + k) * rows + row) * 4))
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < N; ++i) top = fmaxf(top, s[i].x);
+            const float f = top == -INFINITY ? 0.f : top, g0 = exp2_ftz(m - f);
+            m = top;
+            l *= g0;
+#pragma unroll
+            for (int k = 0; k < CH; ++k) a[k].x *= g0, a[k].y *= g0, a[k].z *= g0, a[k].w *= g0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float g = exp2_ftz(s[i].x - f);
+                l += g * s[i].y;
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    a[k].x += g * v[i][k].x; a[k].y += g * v[i][k].y;
+                    a[k].z += g * v[i][k].z; a[k].w += g * v[i][k].w;
+                }
+            }
+        }
+    }
+    template <int D>
+    __device__ __forceinline__ void write(const PagedAttnParams &p, int out_row, int chunk) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+            *reinterpret_cast<uint2 *>(p.out + static_cast<size_t>(out_row) * D + 4 * (chunk + k)) =
+                make_uint2(pack2_bf16(a[k].x * inv, a[k].y * inv), pack2_bf16(a[k].z * inv, a[k].w * inv));
+        if (p.lse && chunk == 0) p.lse[out_row] = (m + log2f(l)) * 0.69314718055994531f;
+    }
+};
+
 template <int D>
-__global__ void __launch_bounds__(256)
-paged_merge_kernel(const PagedAttnParams p, int grid, int shared_blocks) {
-    extern __shared__ float2 mls[];  // [pieces][32]
-    constexpr int kPer = D / 32;     // chunks of a warp
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int blk = static_cast<int>(blockIdx.x);
+__global__ void __launch_bounds__(kPagedMergeThreads)
+paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
+    __shared__ int cuts[kPagedMaxGrid], cut_warps[kPagedMergeThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31;
     const PagedShape &shape = p.shape;
-    const bool alone = blk >= shared_blocks;
-    // pieces c0..c1 that all the lanes have, at record rows rec(c) + row, then the lane's own
-    int c0 = 0, c1 = -1, row = 0, rows = 1, h = 0, row0 = 0, out_row = 0;
-    int d0 = 0, d1 = -1, own_row = 0, own_rows = 1;
-    long long own_rec = 0;
-    bool live = false, skip = false;
     grid_dependency_wait();
     const PagedPlan plan = *reinterpret_cast<const PagedPlan *>(p.plan_ws);
-    if (alone) {
-        const int run = (blk - shared_blocks) / 8;
-        const PagedCut cut = *reinterpret_cast<const PagedCut *>(p.plan_ws + kPagedPlanInts + 8 * run);
-        row = (blk - shared_blocks) % 8 * 32 + lane;
-        rows = cut.rows;
-        live = row < rows;
-        c0 = run;
-        c1 = cut.last_run;
-        const int r = cut.row0 + row, i = r / shape.by_G;
-        out_row = (cut.tok0 + i) * p.n_heads + cut.h * shape.G + r - i * shape.G;
-    } else {
-        const int group = blk / shape.by_nkv, r = group * 32 + lane;
-        h = blk - group * p.n_kv;
-        const PagedRow d = reinterpret_cast<const PagedRow *>(p.plan_ws + kPagedPlanInts + 8 * grid)[r];
-        live = r < plan.shared_rows;
-        row0 = r / kPagedTile * kPagedTile;
-        row = r - row0;
-        rows = paged_min(kPagedTile, plan.shared_rows - row0);
+    const PagedCut *cut_of = reinterpret_cast<const PagedCut *>(p.plan_ws + kPagedPlanInts);
+    const PagedRow *row_of = reinterpret_cast<const PagedRow *>(p.plan_ws + kPagedPlanInts + 8 * shape.grid);
+    static_assert(kPagedMaxGrid <= kPagedMergeThreads, "a thread looks at a run");
+    const bool is_cut = tid < shape.grid && cut_of[tid].rows > 0;
+    const unsigned in_warp = __ballot_sync(~0u, is_cut);
+    if (lane == 0) cut_warps[tid >> 5] = __popc(in_warp);
+    if (!plan.valid) return;
+    const int groups = (plan.shared_rows + 31) / 32;
+    const int shared_tasks = groups * p.n_kv * (D / 4);
+    const int warps = static_cast<int>(gridDim.x) * (kPagedMergeThreads / 32);
+    const int first = static_cast<int>(blockIdx.x) * (kPagedMergeThreads / 32) + (tid >> 5);
+    CFA_ROLLED for (int task = first; task < shared_tasks; task += warps) {
+        // chunks of a row group and key head lie together, so that its warps share its lines
+        const int chunk = task % (D / 4), rest = task / (D / 4);
+        const int group = rest / shape.by_nkv, h = rest - group * p.n_kv, r = group * 32 + lane;
+        if (r >= plan.shared_rows) continue;
+        const PagedRow d = row_of[r];
+        int c0 = 0, c1 = -1;
+        const int row0 = r / kPagedTile * kPagedTile, rows = paged_min(kPagedTile, plan.shared_rows - row0);
         if (plan.prefix_blocks > 0) {
             const int item = plan.prefix_units / shape.by_nkv * h + row0 / kPagedTile * plan.prefix_blocks * kPagedMaxCost;
             c0 = paged_first_run(plan, item);
             c1 = paged_last_run(plan, item, plan.prefix_blocks, paged_cost(rows));
         }
-        if (live) {
-            own_rows = d.rows;
-            own_row = d.row;
-            out_row = d.out_row + h * shape.G;
-            own_rec = d.rec + static_cast<long long>(h) * d.head_rows;
-            if (d.blocks > 0) {
-                d0 = paged_first_run(plan, d.unit + h * d.head_units);
-                d1 = paged_last_run(plan, d.unit + h * d.head_units, d.blocks, paged_cost(1));
-            }
-            skip = plan.prefix_blocks == 0 && d0 == d1;  // the piece wrote the result
+        int d0 = 0, d1 = -1;
+        if (d.blocks > 0) {
+            d0 = paged_first_run(plan, d.unit + h * d.head_units);
+            d1 = paged_last_run(plan, d.unit + h * d.head_units, d.blocks, paged_cost(1));
         }
+        if (plan.prefix_blocks == 0 && d0 == d1) continue;  // the piece wrote the result
+        const long long own = d.rec + static_cast<long long>(h) * d.head_rows;
+        PagedMerge<1> acc;
+        acc.template add<D, 8>(p, c0, c1, chunk, rows, r - row0,
+                               [&](int c) { return paged_shared_record(shape, plan, -1, h, row0, 0, 0, c); });
+        acc.template add<D, 2>(p, d0, d1, chunk, d.rows, d.row,
+                               [&](int c) { return own + static_cast<long long>(c) * kPagedTile; });
+        acc.template write<D>(p, d.out_row + h * shape.G, chunk);
     }
-    if (!plan.valid || !__syncthreads_or(live && !skip)) return;
-    auto rec = [&](int c) {
-        return alone ? paged_alone_record(shape, plan, c == c0 ? 0 : 1, c)
-                     : paged_shared_record(shape, plan, -1, h, row0, 0, 0, c);
-    };
-    for (int c = c0 + warp; c <= c1; c += 8)
-        mls[(c - c0) * 32 + lane] = live ? __ldcg(p.rec_ml + rec(c) + row) : make_float2(-INFINITY, 0.f);
-    float2 own = make_float2(-INFINITY, 0.f);  // the first own piece's, most often the only one
-    if (live && d0 <= d1) own = __ldcg(p.rec_ml + own_rec + static_cast<long long>(d0) * kPagedTile + own_row);
+    // the cut runs in order, the same list in every block
     __syncthreads();
-    if (!live || skip) return;
-    auto own_ml = [&](int c) {
-        return c == d0 ? own : __ldcg(p.rec_ml + own_rec + static_cast<long long>(c) * kPagedTile + own_row);
-    };
-    float m = -INFINITY, l = 0.f;
-    for (int c = c0; c <= c1; ++c) m = fmaxf(m, mls[(c - c0) * 32 + lane].x);
-    for (int c = d0; c <= d1; ++c) m = fmaxf(m, own_ml(c).x);
-    const float f = m == -INFINITY ? 0.f : m;
-    float4 a[kPer];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float2 s, const float *o, int nrows, int r) {
-        const float g = exp2_ftz(s.x - f);
-        l += g * s.y;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-                o + (static_cast<size_t>(warp + 8 * k) * nrows + r) * 4));
-            a[k].x += g * v.x; a[k].y += g * v.y; a[k].z += g * v.z; a[k].w += g * v.w;
-        }
-    };
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) add(mls[(c - c0) * 32 + lane], p.rec_o + rec(c) * D, rows, row);
-    for (int c = d0; c <= d1; ++c)
-        add(own_ml(c), p.rec_o + (own_rec + static_cast<long long>(c) * kPagedTile) * D, own_rows, own_row);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-        *reinterpret_cast<uint2 *>(p.out + static_cast<size_t>(out_row) * D + 4 * (warp + 8 * k)) =
-            make_uint2(pack2_bf16(a[k].x * inv, a[k].y * inv), pack2_bf16(a[k].z * inv, a[k].w * inv));
-    if (p.lse && warp == 0) p.lse[out_row] = (m + log2f(l)) * 0.69314718055994531f;
+    int before = 0, n_cuts = 0;
+    CFA_ROLLED for (int w = 0; w < kPagedMergeThreads / 32; ++w) {
+        if (w < tid >> 5) before += cut_warps[w];
+        n_cuts += cut_warps[w];
+    }
+    if (is_cut) cuts[before + __popc(in_warp & ((1u << lane) - 1))] = tid;
+    __syncthreads();
+    const int cut_tasks = n_cuts * (kPagedTile / 32) * (D / 16);
+    CFA_ROLLED for (int task = first; task < cut_tasks; task += warps) {
+        const int chunk = task % (D / 16) * 4, rest = task / (D / 16);
+        const int run = cuts[rest / (kPagedTile / 32)], row = rest % (kPagedTile / 32) * 32 + lane;
+        const PagedCut cut = cut_of[run];
+        if (row >= cut.rows) continue;
+        const int r = cut.row0 + row, i = r / shape.by_G;
+        PagedMerge<4> acc;
+        acc.template add<D, 2>(p, run, cut.last_run, chunk, cut.rows, row,
+                               [&](int c) { return paged_alone_record(shape, plan, c == run ? 0 : 1, c); });
+        acc.template write<D>(p, (cut.tok0 + i) * p.n_heads + cut.h * shape.G + r - i * shape.G, chunk);
+    }
 }
 
 }  // namespace cfa
