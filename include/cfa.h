@@ -623,8 +623,8 @@ cfa_status cfa_paged_append(cfa_paged *paged, int n_tokens, const void *q, long 
  * that no row of the request sees may hold anything, NaN included; a value there
  * that is not finite where some row sees it may spoil the request's other rows
  * too. Flagged in the status word as CFA_ERR_INVALID_ARG: offsets cu that
- * are not ascending within [0, n_tokens], or more than 2^29 blocks of 128
- * keys over all key heads (nothing is written then); a
+ * are not ascending within [0, n_tokens], or more than some 2^27 blocks of
+ * 128 keys over all key heads and tiles of 256 rows (nothing is written then); a
  * length outside [0, table_width * page_size] (taken as 0); a page id outside
  * [0, n_pages) where a key is read (its keys and values count as zeros).
  * out and lse must not overlap an input or each other.

@@ -76,13 +76,15 @@ struct PagedAttnParams {
     PagedShape shape;
     FastDiv by_page;            // page_size
     int box_rows;               // cache rows of one TMA box
+    int block_clocks;           // of paged_plan
     float scale_log2;           // scale * log2(e)
     uint32_t timeout_ns;
 };
 
 // 8 compute warps; two load warps, an address, a prep, two MMA warps, a merge-rows warp, one idle
 constexpr int kPagedThreads = 512;
-constexpr int kPagedPlanInts = 8;
+constexpr int kPagedPlanInts = 16;
+static_assert(sizeof(PagedPlan) <= 4 * kPagedPlanInts, "the totals fit");
 constexpr int kPagedMaxGrid = 256;    // blocks of the attention kernel, one per SM
 constexpr int kPagedMergeThreads = 256;
 
@@ -97,7 +99,7 @@ struct PagedRow {
     int out_row;           // output row with key head 0
     int unit, head_units;  // first unit of its own keys' item, and units of a key head
     int blocks;            // the item's blocks
-    int rec, head_rows;    // record row of the item (run 0, key head 0), and rows of a key head
+    int rec, head_rows;    // record row of its later pieces (run 0, key head 0), and rows of a key head
     int rows, row;         // rows of the item's tile, and this one among them
 };
 

@@ -296,13 +296,16 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
     const int B = p.B, G = shape.G;
     PagedPlan plan;
     {
-        int *sums = misc + 16;  // units and tokens of each warp
-        int units = 0, tokens = 0;
+        // sums of each warp: units of blocks, items, tokens that share; sums of units and items
+        // stop at the limit, which makes the plan invalid
+        int *sums = reinterpret_cast<int *>(smem + S::kQ), *items_before = sums + 64;  // (free until the first piece)
+        int units = 0, items = 0, tokens = 0;
         bool bad = false;
+        auto more = [](int a, int b) { return min(a + b, kPagedMaxUnits); };
         CFA_ROLLED for (int first = 0; first < B; first += kPagedThreads) {
             const int b = first + tid;
             PagedRequest r{0, 0, 0};
-            int u = 0, t = 0;
+            int u = 0, k = 0, t = 0;
             if (b < B) {
                 r.tok0 = __ldcg(p.cu + b);
                 r.n = __ldcg(p.cu + b + 1) - r.tok0;
@@ -314,37 +317,47 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (r.tok0 < 0 || r.n < 0 || r.n > p.T || r.tok0 > p.T - r.n) {
                     bad = true;
                 } else {
-                    const long long all = paged_request_units(shape, r);
-                    bad |= all > kPagedMostUnits;
-                    u = static_cast<int>(min(all, static_cast<long long>(kPagedMostUnits)));
+                    const PagedCost cost = paged_request_cost(shape, r);
+                    u = static_cast<int>(min(cost.blocks, static_cast<long long>(kPagedMaxUnits)));
+                    k = static_cast<int>(min(cost.items, static_cast<long long>(kPagedMaxUnits)));
                     t = paged_alone(shape, r.n) ? 0 : r.n;
                 }
             }
-            int su = u, st = t;
+            int su = u, sk = k, st = t;
             CFA_ROLLED for (int o = 1; o < 32; o <<= 1) {
-                const int a = __shfl_up_sync(~0u, su, o), c = __shfl_up_sync(~0u, st, o);
-                if (lane >= o) su += a, st += c;
+                const int a = __shfl_up_sync(~0u, su, o), c = __shfl_up_sync(~0u, sk, o), d = __shfl_up_sync(~0u, st, o);
+                if (lane >= o) su = more(su, a), sk = more(sk, c), st += d;
             }
-            if (lane == 31) sums[warp] = su, sums[16 + warp] = st;
+            if (lane == 31) sums[warp] = su, sums[16 + warp] = sk, sums[32 + warp] = st;
             __syncthreads();
-            int wu = lane < 16 ? sums[lane] : 0, wt = lane < 16 ? sums[16 + lane] : 0;
+            int wu = 0, wk = 0, wt = 0;
+            if (lane < 16) wu = sums[lane], wk = sums[16 + lane], wt = sums[32 + lane];
             CFA_ROLLED for (int o = 1; o < 16; o <<= 1) {
-                const int a = __shfl_up_sync(~0u, wu, o), c = __shfl_up_sync(~0u, wt, o);
-                if (lane >= o) wu += a, wt += c;
+                const int a = __shfl_up_sync(~0u, wu, o), c = __shfl_up_sync(~0u, wk, o), d = __shfl_up_sync(~0u, wt, o);
+                if (lane >= o) wu = more(wu, a), wk = more(wk, c), wt += d;
             }
-            const int before_u = __shfl_sync(~0u, wu, (warp + 31) & 31), before_t = __shfl_sync(~0u, wt, (warp + 31) & 31);
-            if (b < B)
-                req[b] = PagedEntry{units + su - u + (warp ? before_u : 0), tokens + st - t + (warp ? before_t : 0), r.tok0, r.len};
-            units += __shfl_sync(~0u, wu, 15);
+            const int left = (warp + 31) & 31;
+            const int bu = __shfl_sync(~0u, wu, left), bk = __shfl_sync(~0u, wk, left), bt = __shfl_sync(~0u, wt, left);
+            if (b < B) {
+                req[b] = PagedEntry{more(units, su - u + (warp ? bu : 0)), tokens + st - t + (warp ? bt : 0), r.tok0, r.len};
+                items_before[b] = more(items, sk - k + (warp ? bk : 0));
+            }
+            units = more(units, __shfl_sync(~0u, wu, 15));
+            items = more(items, __shfl_sync(~0u, wk, 15));
             tokens += __shfl_sync(~0u, wt, 15);
             if (first + kPagedThreads < B) __syncthreads();  // the sums are read
         }
         if (tid == 0) req[B] = PagedEntry{units, tokens, __ldcg(p.cu + B), 0};
-        bad = __syncthreads_or(bad);
-        plan = paged_plan(shape, units, tokens, !bad);
+        plan = paged_plan(shape, PagedCost{units, items}, tokens, p.block_clocks, true);
+        CFA_ROLLED for (int b = tid; b < B; b += kPagedThreads) req[b].unit += items_before[b] * plan.item_units;
+        if (tid == 0) req[B].unit += items * plan.item_units;
+        if (__syncthreads_or(bad)) plan.valid = plan.units = plan.prefix_units = 0;
         tcgen05_fence_after();
         if (blockIdx.x == 0 && tid == 0) {
-            *reinterpret_cast<PagedPlan *>(p.plan_ws) = plan;
+            PagedPlan told = plan;
+            told.alone_tokens = req[B].tok0 - req[0].tok0 - tokens;
+            told.by_share = FastDiv(static_cast<uint32_t>(plan.share));
+            *reinterpret_cast<PagedPlan *>(p.plan_ws) = told;
             if (!plan.valid) atomicOr(p.status, kStatusBadLengthBit);
         }
     }
@@ -480,10 +493,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 else if (x.req >= 0 && paged_alone(shape, x.r.n) && x.b0 == 0 && x.b1 < x.blocks)
                     cut = PagedCut{x.rows, x.row0, x.r.tok0, x.h, paged_last_run(plan, x.first_unit, x.blocks, x.cost), {0, 0, 0}};
                 x.final = more && paged_final(shape, x);
-                x.rec = !more ? 0
-                        : x.req >= 0 && paged_alone(shape, x.r.n)
-                            ? paged_alone_record(shape, plan, x.b0, run)
-                            : paged_shared_record(shape, plan, x.req, x.h, x.row0, x.r.n, x.req < 0 ? 0 : req[x.req].tok, run);
+                if (more) paged_record(shape, plan, x.req < 0 ? 0 : req[x.req].tok, run, x);
                 if (__any_sync(~0u, k >= kPagedSlots && !wait(bar_piece_free + 8 * (k % kPagedSlots),
                                                               (k / kPagedSlots - 1) & 1, kSiteStageEmpty)))
                     break;
@@ -615,7 +625,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const int own = all > tile ? mine / tile : 0, row0 = own * tile, blocks = paged_cdiv(q.len, kPagedKeys);
                 PagedRow d;
                 d.out_row = (q.tok0 + tok - req[b].tok) * p.n_heads + r - tok * G;
-                d.unit = plan.prefix_units + req[b].unit + own * blocks * paged_cost(1);
+                d.unit = plan.prefix_units + req[b].unit + own * paged_item_units(plan, tile, paged_cost(tile), blocks);
                 d.head_units = (req[b + 1].unit - req[b].unit) / shape.by_nkv;
                 d.blocks = blocks;
                 d.rec = static_cast<int>(paged_shared_record(shape, plan, b, 0, row0, q.n, req[b].tok, 0));
@@ -660,8 +670,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
             const int *row_at = reinterpret_cast<const int *>(slot + S::kSlotRows);
             const bool final = x.final;
-            float *rec_o = p.rec_o + x.rec * D;
-            float2 *rec_ml = p.rec_ml + x.rec;
+            float *rec_o = p.rec_o + x.rec * D + x.rec_row * 4;
+            float2 *rec_ml = p.rec_ml + x.rec + x.rec_row;
+            const int rec_stride = x.rec_stride;
             auto result_row = [&](int row) {
                 const int at = row_at[row];
                 return (at & kPagedTokenMask) * p.n_heads + x.h * G + (at >> kPagedTokenBits);
@@ -856,7 +867,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                             make_uint2(pack2_bf16(a.x * inv, a.y * inv), pack2_bf16(a.z * inv, a.w * inv));
                         if (c == 0) write_lse(row, m, l);
                     } else {
-                        *reinterpret_cast<float4 *>(rec_o + (static_cast<size_t>(c) * x.rows + row) * 4) = a;
+                        *reinterpret_cast<float4 *>(rec_o + (static_cast<size_t>(c) * rec_stride + row) * 4) = a;
                         if (c == 0) rec_ml[row] = make_float2(m, l);
                     }
                 }
@@ -1048,7 +1059,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     } else {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<float4 *>(rec_o + (static_cast<size_t>(c / 4 + e) * x.rows + row) * 4) =
+                            *reinterpret_cast<float4 *>(rec_o + (static_cast<size_t>(c / 4 + e) * rec_stride + row) * 4) =
                                 make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
                     }
                 }
@@ -1069,10 +1080,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 // Merges the records, a warp for 32 rows of one key head (a lane a row) and CH of
 // the row's 16-byte chunks: the shared rows (the prefix's pieces, then the
 // request's own) a chunk at a time, then the tiles of requests that are alone and
-// that a run's end cut, four at a time. Pieces are taken in the order of the runs,
-// eight at a time, so that their loads, maxima and sums among them, are on their way
-// together: the kernel is a chain of three loads (plan, row, records), and what counts
-// is that nothing else waits in between.
+// that a run's end cut, four at a time. The prefix's pieces are taken in the order of
+// the runs, several at a time, then the request's own, so that their loads, maxima and
+// sums among them, are on their way together with the row's: the kernel is a chain of
+// two loads (the plan, then rows and records), and what counts is that nothing else waits
+// in between.
 template <int CH>
 struct PagedMerge {
     float m = -INFINITY, l = 0.f;
@@ -1081,43 +1093,48 @@ struct PagedMerge {
 #pragma unroll
         for (int k = 0; k < CH; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    // Pieces c0..c1, whose record row for this lane is at(c), in records of `rows` rows
-    // beginning at base(c); N at a time.
-    template <int D, int N, typename Base>
-    __device__ __forceinline__ void add(const PagedAttnParams &p, int c0, int c1, int chunk, int rows, int row, Base base) {
-        for (int c = c0; c <= c1; c += N) {
-            float2 s[N];
+    // One piece's chunks with weight 2^(s.x - f).
+    __device__ __forceinline__ void fold(float2 s, const float4 *v, float f) {
+        const float g = exp2_ftz(s.x - f);
+        l += g * s.y;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            a[k].x += g * v[k].x; a[k].y += g * v[k].y; a[k].z += g * v[k].z; a[k].w += g * v[k].w;
+        }
+    }
+    // Takes the maximum on to `top`; returns what weights refer to.
+    __device__ __forceinline__ float raise(float top) {
+        const float f = top == -INFINITY ? 0.f : top, g = exp2_ftz(m - f);
+        m = top;
+        l *= g;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) a[k].x *= g, a[k].y *= g, a[k].z *= g, a[k].w *= g;
+        return f;
+    }
+    // n pieces a run apart each: their maxima and sums at s, their chunks at o, `rows` rows a
+    // chunk; N at a time.
+    template <int D, int N>
+    __device__ __forceinline__ void add(const float2 *s, const float4 *o, int rows, int n) {
+        CFA_ROLLED for (; n > 0; n -= N, s += N * kPagedTile, o += static_cast<size_t>(N) * kPagedTile * (D / 4)) {
+            float2 t[N];
             float4 v[N][CH];
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const bool there = c + i <= c1;
-                const long long at = base(there ? c + i : c1);
-                s[i] = __ldcg(p.rec_ml + at + row);
-                if (!there) s[i] = make_float2(-INFINITY, 0.f);
+                t[i] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-                for (int k = 0; k < CH; ++k)
-                    v[i][k] = there ? __ldcg(reinterpret_cast<const float4 *>(
-                                          p.rec_o + at * D + (static_cast<size_t>(chunk + k) * rows + row) * 4))
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < CH; ++k) v[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < n) {
+                    t[i] = __ldcg(s + i * kPagedTile);
+#pragma unroll
+                    for (int k = 0; k < CH; ++k) v[i][k] = __ldcg(o + i * kPagedTile * (D / 4) + k * rows);
+                }
             }
             float top = m;
 #pragma unroll
-            for (int i = 0; i < N; ++i) top = fmaxf(top, s[i].x);
-            const float f = top == -INFINITY ? 0.f : top, g0 = exp2_ftz(m - f);
-            m = top;
-            l *= g0;
+            for (int i = 0; i < N; ++i) top = fmaxf(top, t[i].x);
+            const float f = raise(top);
 #pragma unroll
-            for (int k = 0; k < CH; ++k) a[k].x *= g0, a[k].y *= g0, a[k].z *= g0, a[k].w *= g0;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float g = exp2_ftz(s[i].x - f);
-                l += g * s[i].y;
-#pragma unroll
-                for (int k = 0; k < CH; ++k) {
-                    a[k].x += g * v[i][k].x; a[k].y += g * v[i][k].y;
-                    a[k].z += g * v[i][k].z; a[k].w += g * v[i][k].w;
-                }
-            }
+            for (int i = 0; i < N; ++i) fold(t[i], v[i], f);
         }
     }
     template <int D>
@@ -1126,58 +1143,65 @@ struct PagedMerge {
 #pragma unroll
         for (int k = 0; k < CH; ++k)
             *reinterpret_cast<uint2 *>(p.out + static_cast<size_t>(out_row) * D + 4 * (chunk + k)) =
-                make_uint2(pack2_bf16(a[k].x * inv, a[k].y * inv), pack2_bf16(a[k].z * inv, a[k].w * inv));
+                make_uint2(pack2_bf16_cvt(a[k].x * inv, a[k].y * inv), pack2_bf16_cvt(a[k].z * inv, a[k].w * inv));
         if (p.lse && chunk == 0) p.lse[out_row] = (m + log2f(l)) * 0.69314718055994531f;
     }
 };
 
 template <int D>
-__global__ void __launch_bounds__(kPagedMergeThreads)
+__global__ void __launch_bounds__(kPagedMergeThreads, 3)
 paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
     __shared__ int cuts[kPagedMaxGrid], cut_warps[kPagedMergeThreads / 32];
+    constexpr int C = D / 4;  // chunks of a row
     const int tid = threadIdx.x, lane = tid & 31;
     const PagedShape &shape = p.shape;
+    const float4 *rec_o = reinterpret_cast<const float4 *>(p.rec_o);
     grid_dependency_wait();
     const PagedPlan plan = *reinterpret_cast<const PagedPlan *>(p.plan_ws);
     const PagedCut *cut_of = reinterpret_cast<const PagedCut *>(p.plan_ws + kPagedPlanInts);
     const PagedRow *row_of = reinterpret_cast<const PagedRow *>(p.plan_ws + kPagedPlanInts + 8 * shape.grid);
-    static_assert(kPagedMaxGrid <= kPagedMergeThreads, "a thread looks at a run");
-    const bool is_cut = tid < shape.grid && cut_of[tid].rows > 0;
-    const unsigned in_warp = __ballot_sync(~0u, is_cut);
-    if (lane == 0) cut_warps[tid >> 5] = __popc(in_warp);
     if (!plan.valid) return;
-    const int groups = (plan.shared_rows + 31) / 32;
-    const int shared_tasks = groups * p.n_kv * (D / 4);
+    const int shared_tasks = (plan.shared_rows + 31) / 32 * p.n_kv * C;
     const int warps = static_cast<int>(gridDim.x) * (kPagedMergeThreads / 32);
     const int first = static_cast<int>(blockIdx.x) * (kPagedMergeThreads / 32) + (tid >> 5);
     CFA_ROLLED for (int task = first; task < shared_tasks; task += warps) {
         // chunks of a row group and key head lie together, so that its warps share its lines
-        const int chunk = task % (D / 4), rest = task / (D / 4);
+        const int chunk = task % C, rest = task / C;
         const int group = rest / shape.by_nkv, h = rest - group * p.n_kv, r = group * 32 + lane;
         if (r >= plan.shared_rows) continue;
         const PagedRow d = row_of[r];
-        int c0 = 0, c1 = -1;
-        const int row0 = r / kPagedTile * kPagedTile, rows = paged_min(kPagedTile, plan.shared_rows - row0);
-        if (plan.prefix_blocks > 0) {
-            const int item = plan.prefix_units / shape.by_nkv * h + row0 / kPagedTile * plan.prefix_blocks * kPagedMaxCost;
-            c0 = paged_first_run(plan, item);
-            c1 = paged_last_run(plan, item, plan.prefix_blocks, paged_cost(rows));
-        }
-        int d0 = 0, d1 = -1;
-        if (d.blocks > 0) {
-            d0 = paged_first_run(plan, d.unit + h * d.head_units);
-            d1 = paged_last_run(plan, d.unit + h * d.head_units, d.blocks, paged_cost(1));
-        }
-        if (plan.prefix_blocks == 0 && d0 == d1) continue;  // the piece wrote the result
-        const long long own = d.rec + static_cast<long long>(h) * d.head_rows;
+        // its first own piece's record, wherever that piece ran
+        const long long first_rec = paged_first_record(plan, h);
+        const float2 own_ml = __ldcg(p.rec_ml + first_rec + r);
+        const float4 own = __ldcg(rec_o + first_rec * C + chunk * plan.shared_rows + r);
         PagedMerge<1> acc;
-        acc.template add<D, 8>(p, c0, c1, chunk, rows, r - row0,
-                               [&](int c) { return paged_shared_record(shape, plan, -1, h, row0, 0, 0, c); });
-        acc.template add<D, 2>(p, d0, d1, chunk, d.rows, d.row,
-                               [&](int c) { return own + static_cast<long long>(c) * kPagedTile; });
+        if (plan.prefix_blocks > 0) {
+            const int tile = r / kPagedTile, row0 = tile * kPagedTile, rows = paged_min(kPagedTile, plan.shared_rows - row0);
+            const int item = plan.prefix_units / shape.by_nkv * h + tile * plan.full_units;
+            const int c0 = item / plan.by_share;
+            const int c1 = (item + (plan.prefix_blocks - 1) * paged_prefix_cost(plan.by_bytes, rows)) / plan.by_share;
+            const long long rec = paged_shared_record(shape, plan, -1, h, row0, 0, 0, c0);
+            acc.template add<D, 4>(p.rec_ml + rec + r - row0, rec_o + rec * C + chunk * rows + r - row0, rows, c1 - c0 + 1);
+        }
+        if (d.blocks > 0) {
+            const int item = d.unit + h * d.head_units;
+            const int d0 = item / plan.by_share;
+            const int more = (item + (d.blocks - 1) * paged_cost(d.rows)) / plan.by_share - d0;
+            if (plan.prefix_blocks == 0 && more == 0) continue;  // the piece wrote the result
+            acc.fold(own_ml, &own, acc.raise(fmaxf(acc.m, own_ml.x)));
+            if (more > 0) {
+                const long long rec = d.rec + static_cast<long long>(h) * d.head_rows + static_cast<long long>(d0 + 1) * kPagedTile;
+                acc.template add<D, 1>(p.rec_ml + rec + d.row, rec_o + rec * C + chunk * d.rows + d.row, d.rows, more);
+            }
+        }
         acc.template write<D>(p, d.out_row + h * shape.G, chunk);
     }
+    if (plan.alone_tokens == 0) return;
     // the cut runs in order, the same list in every block
+    static_assert(kPagedMaxGrid <= kPagedMergeThreads, "a thread looks at a run");
+    const bool is_cut = tid < shape.grid && cut_of[tid].rows > 0;
+    const unsigned in_warp = __ballot_sync(~0u, is_cut);
+    if (lane == 0) cut_warps[tid >> 5] = __popc(in_warp);
     __syncthreads();
     int before = 0, n_cuts = 0;
     CFA_ROLLED for (int w = 0; w < kPagedMergeThreads / 32; ++w) {
@@ -1186,16 +1210,32 @@ paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
     }
     if (is_cut) cuts[before + __popc(in_warp & ((1u << lane) - 1))] = tid;
     __syncthreads();
-    const int cut_tasks = n_cuts * (kPagedTile / 32) * (D / 16);
+    const int cut_tasks = n_cuts * (kPagedTile / 32) * (C / 4);
     CFA_ROLLED for (int task = first; task < cut_tasks; task += warps) {
-        const int chunk = task % (D / 16) * 4, rest = task / (D / 16);
+        const int chunk = task % (C / 4) * 4, rest = task / (C / 4);
         const int run = cuts[rest / (kPagedTile / 32)], row = rest % (kPagedTile / 32) * 32 + lane;
         const PagedCut cut = cut_of[run];
         if (row >= cut.rows) continue;
         const int r = cut.row0 + row, i = r / shape.by_G;
         PagedMerge<4> acc;
-        acc.template add<D, 2>(p, run, cut.last_run, chunk, cut.rows, row,
-                               [&](int c) { return paged_alone_record(shape, plan, c == run ? 0 : 1, c); });
+        // the run's own piece and the next run's, then what further runs have
+        long long rec = paged_alone_record(shape, plan, 1, run + 1);
+        const long long recs[2] = {paged_alone_record(shape, plan, 0, run), rec};
+        float2 t[2];
+        float4 v[2][4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            t[k] = __ldcg(p.rec_ml + recs[k] + row);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[k][e] = __ldcg(rec_o + recs[k] * C + (chunk + e) * cut.rows + row);
+        }
+        const float f = acc.raise(fmaxf(t[0].x, t[1].x));
+        acc.fold(t[0], v[0], f);
+        acc.fold(t[1], v[1], f);
+        CFA_ROLLED for (int c = run + 2; c <= cut.last_run; ++c) {
+            rec += 2 * kPagedTile;
+            acc.template add<D, 1>(p.rec_ml + rec + row, rec_o + rec * C + chunk * cut.rows + row, cut.rows, 1);
+        }
         acc.template write<D>(p, (cut.tok0 + i) * p.n_heads + cut.h * shape.G + r - i * shape.G, chunk);
     }
 }

@@ -12,10 +12,11 @@
 // prefix's keys and its own in one item, with nothing to merge.
 //
 // An item is cut into blocks of 128 keys; prefix and own keys never share a
-// block. A block costs paged_cost() units, by how many rows its item has. The
-// units of all items, in a fixed order (shared prefix by key head and tile; then
-// requests in order, by key head and tile), are dealt out to the grid's blocks in
-// equal runs; a block of keys goes to the run in which its first unit lies. A
+// block. A block costs so many units by how many rows its item has, and an item some more
+// behind its blocks (paged_plan says how many). The units of all items, in a fixed order
+// (shared prefix by key head and tile; then requests in order, by key head and tile),
+// are dealt out to the grid's blocks in equal runs; a block of keys goes to the run in
+// which its first unit lies. A
 // run's part of one item is a piece. A piece that is a whole item, and the only
 // item of its rows, writes its result; every other piece leaves a record (max, sum
 // and unnormalised output of its rows), which are merged in the order of the runs.
@@ -38,18 +39,19 @@ constexpr int kPagedTile = 256;       // rows of a tile
 constexpr int kPagedSmallRows = 16;   // rows that go through mma.sync
 constexpr int kPagedAloneRows = 128;  // rows up to which a request shares the prefix's tiles
 constexpr int kPagedNarrowRows = 64;  // rows up to which own keys go to tiles of 16
-constexpr int kPagedMaxCost = 3;
+constexpr int kPagedMaxCost = 9;
+constexpr int kPagedMaxUnits = (1 << 30) - 1;  // two of them added stay below 2^31
 
 // Division of 0 <= n < 2^31 by a divisor that the host knows: n / d = (n mul) >> (32 + shift)
 // with mul = 2^(31 + l) / d rounded up, l = ceil(log2 d), shift = l - 1; the rounding adds less
 // than n / 2^(31 + l) < 1 / d to the quotient. An integer division takes some 30 instructions.
 struct FastDiv {
-    uint32_t d = 1, mul = 0;
-    int shift = 0;
+    uint32_t d, mul;
+    int shift;
     FastDiv() = default;
-    explicit FastDiv(uint32_t divisor) : d(divisor) {
+    CFA_HD explicit FastDiv(uint32_t divisor) : d(divisor), mul(0), shift(0) {
         int l = 0;
-        while ((1ull << l) < divisor) ++l;
+        CFA_ROLLED while ((1ull << l) < divisor) ++l;
         if (l > 0) {
             mul = static_cast<uint32_t>(((1ull << (31 + l)) + divisor - 1) / divisor);
             shift = l - 1;
@@ -76,12 +78,17 @@ struct PagedShape {
 
 // What one scan over the requests finds.
 struct PagedPlan {
+    int by_bytes;       // the bytes of the keys bound the whole
+    int item_units;     // units of an item whose paged_item_cost() is 1
     int shared_rows;    // of one key head
     int prefix_blocks;  // blocks of the prefix
     int tiles;          // tiles of the shared rows
+    int full_units;     // units of a full tile's item
     int prefix_units;   // units of the shared prefix
     int units;          // of everything
     int share;          // units of one run
+    int alone_tokens;   // tokens of the requests that are alone
+    FastDiv by_share;   // (set by whoever divides by it)
     int valid;
 };
 
@@ -98,9 +105,6 @@ struct alignas(16) PagedEntry {
 CFA_HD PagedRequest paged_request_at(const PagedEntry *e, int b) {
     return PagedRequest{e[b].tok0, e[b + 1].tok0 - e[b].tok0, e[b].len};
 }
-// Units that one request may have, so that 1024 of them stay below 2^31.
-constexpr int kPagedMostUnits = (1 << 21) - 1;
-
 struct PagedPiece {
     int req;            // request, or -1: the shared rows over the prefix
     int h;              // key head
@@ -110,9 +114,10 @@ struct PagedPiece {
     int own_limit;      // own keys that the last row sees
     int b0, b1;         // the piece: blocks [b0, b1) of the item
     int first_unit;     // the item's first unit
-    int cost;           // units of a block
+    int cost, units;    // units of a block, and of the item
     int final;          // the piece writes its rows' results
-    long long rec;      // else: its first record row
+    long long rec;      // else its record (paged_record)
+    int rec_row, rec_stride;
     PagedRequest r;
 };
 
@@ -120,8 +125,19 @@ CFA_HD int paged_min(int a, int b) { return a < b ? a : b; }
 CFA_HD int paged_max(int a, int b) { return a > b ? a : b; }
 CFA_HD int paged_cdiv(int a, int b) { return (a + b - 1) / b; }
 
-// Units of a block of keys for an item of so many rows.
-CFA_HD int paged_cost(int rows) { return rows <= kPagedAloneRows ? 2 : kPagedMaxCost; }
+// Clocks by 400 of a block of keys, and of beginning and ending an item by kPagedItemClocks
+// times 400, as measured where the warps' work bounds them: 16 rows 1600 a block (the other
+// warpgroup's block beside it), a tile of 128 rows 2800, of 256 rows 3560.
+CFA_HD int paged_cost(int rows) { return rows <= kPagedSmallRows ? 4 : rows <= kPagedAloneRows ? 7 : kPagedMaxCost; }
+CFA_HD int paged_item_cost(int rows) { return rows <= kPagedSmallRows ? 1 : 3; }
+#ifndef kPagedItemClocks
+constexpr int kPagedItemClocks = 8;
+#endif
+// Where the bytes of the keys bound the whole, blocks cost nearly alike, and an item next to
+// nothing: what the warps do goes on under the loads.
+CFA_HD int paged_prefix_cost(bool by_bytes, int rows) {
+    return rows <= kPagedSmallRows ? 4 : rows <= kPagedAloneRows ? (by_bytes ? 5 : 7) : by_bytes ? 6 : kPagedMaxCost;
+}
 
 // Own keys that token i of a request sees.
 CFA_HD int paged_visible(const PagedRequest &r, int i) {
@@ -139,35 +155,63 @@ CFA_HD int paged_alone_blocks(const PagedShape &s, const PagedRequest &r, int ti
     return paged_max(1, paged_cdiv(s.prefix_len, kPagedKeys) +
                             paged_cdiv(paged_visible(r, last / s.by_G), kPagedKeys));
 }
-// Units of a request's own items.
-CFA_HD long long paged_request_units(const PagedShape &s, const PagedRequest &r) {
-    if (r.n == 0) return 0;
-    if (!paged_alone(s, r.n))
-        return static_cast<long long>(s.nkv) * paged_cdiv(r.len, kPagedKeys) * paged_cost(1) *
-               paged_cdiv(r.n * s.G, paged_own_tile(r.n * s.G));
-    long long u = 0;
-    CFA_ROLLED for (int row = 0, t = 0; row < r.n * s.G; row += kPagedTile, ++t)
-        u += paged_alone_blocks(s, r, t) * paged_cost(r.n * s.G - row);
-    return u * s.nkv;
+// What a request's own items cost: units of their blocks, and items.
+struct PagedCost {
+    long long blocks, items;
+};
+CFA_HD PagedCost paged_request_cost(const PagedShape &s, const PagedRequest &r) {
+    if (r.n == 0) return PagedCost{0, 0};
+    const int all = r.n * s.G;
+    if (!paged_alone(s, r.n)) {
+        if (r.len == 0) return PagedCost{0, 0};
+        const int tile = paged_own_tile(all);  // (a last tile of fewer rows costs the same)
+        const long long items = static_cast<long long>(s.nkv) * paged_cdiv(all, tile);
+        return PagedCost{items * paged_cdiv(r.len, kPagedKeys) * paged_cost(paged_min(all, tile)),
+                         items * paged_item_cost(paged_min(all, tile))};
+    }
+    PagedCost c{0, 0};
+    CFA_ROLLED for (int row = 0, t = 0; row < all; row += kPagedTile, ++t) {
+        c.blocks += paged_alone_blocks(s, r, t) * paged_cost(all - row);
+        c.items += paged_item_cost(all - row);
+    }
+    return PagedCost{c.blocks * s.nkv, c.items * s.nkv};
 }
 
-// The totals: `own_units` of all requests and `shared_tokens` of those that share.
-CFA_HD PagedPlan paged_plan(const PagedShape &s, long long own_units, int shared_tokens, bool valid) {
+CFA_HD int paged_item_units(const PagedPlan &p, int rows, int cost, int blocks) {
+    return blocks * cost + paged_item_cost(rows) * p.item_units;
+}
+
+// The totals: what all requests' own items cost, and shared_tokens of those that share.
+// block_bytes_clocks: clocks by 400 that the device's memory takes to deliver a block's keys
+// and values to one of its SMs while it serves them all.
+CFA_HD PagedPlan paged_plan(const PagedShape &s, const PagedCost &own, int shared_tokens, int block_bytes_clocks,
+                            bool valid) {
     PagedPlan p;
     p.shared_rows = shared_tokens * s.G;
     p.prefix_blocks = paged_cdiv(s.prefix_len, kPagedKeys);
-    p.tiles = paged_cdiv(p.shared_rows, kPagedTile);
-    // every tile but the last is full
-    const int last_rows = p.shared_rows - (p.tiles - 1) * kPagedTile;
-    const long long pu = p.tiles == 0 ? 0
-                                      : static_cast<long long>(s.nkv) * p.prefix_blocks *
-                                            ((p.tiles - 1) * kPagedMaxCost + paged_cost(last_rows));
-    const long long all = pu + own_units;
-    p.valid = valid && all < (1ll << 31) - s.grid;
-    p.prefix_units = p.valid ? static_cast<int>(pu) : 0;
+    p.tiles = p.prefix_blocks == 0 ? 0 : paged_cdiv(p.shared_rows, kPagedTile);
+    const int last_rows = p.shared_rows - (p.tiles - 1) * kPagedTile;  // every tile but the last is full
+    long long all = 0;
+    CFA_ROLLED for (int by_bytes = 0; by_bytes < 2; ++by_bytes) {
+        p.by_bytes = by_bytes;
+        p.item_units = by_bytes ? 1 : kPagedItemClocks;
+        p.full_units = paged_item_units(p, kPagedTile, paged_prefix_cost(by_bytes, kPagedTile), p.prefix_blocks);
+        const long long pu =
+            p.tiles == 0 ? 0
+                         : s.nkv * ((p.tiles - 1ll) * p.full_units +
+                                    paged_item_units(p, last_rows, paged_prefix_cost(by_bytes, last_rows), p.prefix_blocks));
+        all = pu + own.blocks + own.items * p.item_units;
+        p.prefix_units = pu < kPagedMaxUnits ? static_cast<int>(pu) : 0;
+        // every block of own keys counts four units at least, and the prefix's keys are read once
+        const long long bytes = (own.blocks / 4 + static_cast<long long>(s.nkv) * (p.tiles ? p.prefix_blocks : 0)) * block_bytes_clocks;
+        if (bytes <= all) break;
+    }
+    p.valid = valid && all < kPagedMaxUnits;
+    if (!p.valid) p.prefix_units = 0;
     p.units = p.valid ? static_cast<int>(all) : 0;
     // at least a block, so that a run inside an item never comes away empty
     p.share = paged_max(kPagedMaxCost, paged_cdiv(p.units, s.grid));
+    p.alone_tokens = 0;
     return p;
 }
 
@@ -187,7 +231,7 @@ CFA_HD int paged_find(int B, int x, At at) {
 CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const PagedEntry *e, int B, int u, PagedPiece &x) {
     int rem;  // units of the item before u
     if (u < p.prefix_units) {
-        const int head_units = p.prefix_units / s.by_nkv, full = p.prefix_blocks * kPagedMaxCost;
+        const int head_units = p.prefix_units / s.by_nkv, full = p.full_units;
         x.req = -1;
         x.h = u / head_units;
         rem = u - x.h * head_units;
@@ -197,6 +241,7 @@ CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const PagedEntry
         x.rows = paged_min(kPagedTile, p.shared_rows - x.row0);
         x.prefix_blocks = x.blocks = p.prefix_blocks;
         x.own_limit = 0;
+        x.cost = paged_prefix_cost(p.by_bytes, x.rows);
         x.r = PagedRequest{0, 0, 0};
     } else {
         x.req = paged_find(B, u - p.prefix_units, [&](int b) { return e[b].unit; });
@@ -211,8 +256,9 @@ CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const PagedEntry
             x.prefix_blocks = 0;
             x.blocks = paged_cdiv(x.r.len, kPagedKeys);
             if (all > tile) {
-                x.row0 = rem / (x.blocks * paged_cost(1)) * tile;
-                rem %= x.blocks * paged_cost(1);
+                const int each = paged_item_units(p, tile, paged_cost(tile), x.blocks);
+                x.row0 = rem / each * tile;
+                rem %= each;
             }
             x.rows = paged_min(tile, all - x.row0);
             x.own_limit = x.r.len;
@@ -220,8 +266,10 @@ CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const PagedEntry
             const int all = x.r.n * s.G;
             int t = 0;
             x.blocks = paged_alone_blocks(s, x.r, 0);
-            CFA_ROLLED while (rem >= x.blocks * paged_cost(all - x.row0)) {
-                rem -= x.blocks * paged_cost(all - x.row0);
+            CFA_ROLLED for (;;) {
+                const int each = paged_item_units(p, all - x.row0, paged_cost(all - x.row0), x.blocks);
+                if (rem < each) break;
+                rem -= each;
                 x.row0 += kPagedTile;
                 x.blocks = paged_alone_blocks(s, x.r, ++t);
             }
@@ -230,12 +278,10 @@ CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const PagedEntry
             x.own_limit = paged_visible(x.r, (x.row0 + x.rows - 1) / s.by_G);
         }
     }
-    x.cost = paged_cost(x.rows);
+    if (x.req >= 0) x.cost = paged_cost(x.rows);
+    x.units = paged_item_units(p, x.rows, x.cost, x.blocks);
     x.first_unit = u - rem;
 }
-
-// Blocks whose first unit lies before `units` of an item.
-CFA_HD int paged_blocks_before(int units, int cost) { return cost == 2 ? (units + 1) >> 1 : paged_cdiv(units, kPagedMaxCost); }
 
 // The next piece of the run that ends before unit `end`, from unit u on; u moves behind it.
 // False: the run has no more.
@@ -243,9 +289,9 @@ CFA_HD bool paged_next(const PagedShape &s, const PagedPlan &p, const PagedEntry
                        PagedPiece &x) {
     CFA_ROLLED while (u < end) {
         paged_item(s, p, e, B, u, x);
-        x.b0 = paged_blocks_before(u - x.first_unit, x.cost);
-        x.b1 = paged_min(x.blocks, paged_blocks_before(end - x.first_unit, x.cost));
-        u = paged_min(end, x.first_unit + x.blocks * x.cost);
+        x.b0 = paged_cdiv(u - x.first_unit, x.cost);
+        x.b1 = paged_min(x.blocks, paged_cdiv(end - x.first_unit, x.cost));
+        u = paged_min(end, x.first_unit + x.units);
         if (x.b0 < x.b1) return true;
     }
     return false;
@@ -266,24 +312,43 @@ CFA_HD int paged_last_run(const PagedPlan &p, int first_unit, int blocks, int co
     return (first_unit + (blocks - 1) * cost) / p.share;
 }
 
-// First record row of a piece of run c. Items that share have room for their rows at every
-// run they meet: the rows of all the items before them plus a tile a run (so that neither the
-// next item nor the next run reaches back). Tiles of requests that are alone are cut at most at
-// a run's ends: two tiles a run, behind the others.
-// shared_tok0: shared tokens before the request, n: its tokens (req >= 0).
+// Where a piece leaves its record: rows of the record arrays. A shared request's first
+// piece over its own keys has its place by key head and shared row, so that the merge finds
+// it without looking the request up. The other pieces of shared rows have room for their rows at
+// every run they meet: the rows of all the items before them plus a tile a run (so that
+// neither the next item nor the next run reaches back). Tiles of requests that are alone are
+// cut at most at a run's ends: two tiles a run, behind the others. shared_tok0: shared tokens
+// before the request, n: its tokens.
+CFA_HD long long paged_first_record(const PagedPlan &p, int h) { return static_cast<long long>(h) * p.shared_rows; }
 CFA_HD long long paged_shared_record(const PagedShape &s, const PagedPlan &p, int req, int h, int row0, int n,
                                      int shared_tok0, int c) {
+    const long long head = static_cast<long long>(s.nkv) * p.shared_rows;
     const long long before = req < 0 ? static_cast<long long>(h) * p.shared_rows
-                                     : static_cast<long long>(s.nkv) * (p.shared_rows + static_cast<long long>(shared_tok0) * s.G) +
+                                     : head + static_cast<long long>(s.nkv) * shared_tok0 * s.G +
                                            static_cast<long long>(h) * n * s.G;
-    return before + row0 + static_cast<long long>(c) * kPagedTile;
+    return head + before + row0 + static_cast<long long>(c) * kPagedTile;
 }
 CFA_HD long long paged_alone_record(const PagedShape &s, const PagedPlan &p, int b0, int c) {
-    return 2ll * s.nkv * p.shared_rows + static_cast<long long>(s.grid) * kPagedTile +
+    return 3ll * s.nkv * p.shared_rows + static_cast<long long>(s.grid) * kPagedTile +
            (2ll * c + (b0 > 0 ? 0 : 1)) * kPagedTile;
 }
 CFA_HD long long paged_record_rows(const PagedShape &s, long long shared_rows) {
-    return 2 * s.nkv * shared_rows + 3ll * s.grid * kPagedTile;
+    return 3 * s.nkv * shared_rows + 3ll * s.grid * kPagedTile;
+}
+// A piece's record: outputs at rec D + (chunk stride + row) 4, maximum and sum at rec + row,
+// for rows from rec_row on.
+CFA_HD void paged_record(const PagedShape &s, const PagedPlan &p, int shared_tok0, int run, PagedPiece &x) {
+    x.rec_row = 0;
+    x.rec_stride = x.rows;
+    if (x.req >= 0 && paged_alone(s, x.r.n)) {
+        x.rec = paged_alone_record(s, p, x.b0, run);
+    } else if (x.req >= 0 && x.b0 == 0) {
+        x.rec = paged_first_record(p, x.h);
+        x.rec_row = shared_tok0 * s.G + x.row0;
+        x.rec_stride = p.shared_rows;
+    } else {
+        x.rec = paged_shared_record(s, p, x.req, x.h, x.row0, x.r.n, shared_tok0, run);
+    }
 }
 
 }  // namespace cfa
