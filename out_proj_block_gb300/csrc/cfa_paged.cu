@@ -259,8 +259,9 @@ cfa_status launch_attention(cfa_paged *p, const AttnArgs &a, cudaStream_t stream
     kp.rec_o = p->rec_o;
     kp.rec_ml = p->rec_ml;
     kp.timeout_ns = kTimeoutNs;
-    // 512 D bytes at 6.8 TB/s over 152 SMs of 1.9 GHz: 2780 clocks at D = 128
-    kp.block_clocks = p->D == 128 ? 7 : 4;
+    // 512 D bytes at 6.8 TB/s over 152 SMs of 1.9 GHz: 2780 clocks at head_dim 128; at 64, 1390,
+    // beside 1350 of work instead of 1900 (paged_cost)
+    kp.block_clocks = p->D == 128 ? 7 : 6;
     kp.shape = cfa::PagedShape(p->nh / p->nkv, p->nkv, a.prefix_len, p->num_sms);
     kp.by_page = cfa::FastDiv(static_cast<uint32_t>(p->ps));
     // a box of rows lies inside one page and divides a block of 128 keys

@@ -348,14 +348,14 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             if (first + kPagedThreads < B) __syncthreads();  // the sums are read
         }
         if (tid == 0) req[B] = PagedEntry{units, tokens, __ldcg(p.cu + B), 0};
-        plan = paged_plan(shape, PagedCost{units, items}, tokens, p.block_clocks, true);
+        const int all_tokens = __ldcg(p.cu + B) - __ldcg(p.cu);
+        plan = paged_plan(shape, PagedCost{units, items}, tokens, all_tokens - tokens, p.block_clocks, true);
         CFA_ROLLED for (int b = tid; b < B; b += kPagedThreads) req[b].unit += items_before[b] * plan.item_units;
         if (tid == 0) req[B].unit += items * plan.item_units;
         if (__syncthreads_or(bad)) plan.valid = plan.units = plan.prefix_units = 0;
         tcgen05_fence_after();
         if (blockIdx.x == 0 && tid == 0) {
             PagedPlan told = plan;
-            told.alone_tokens = req[B].tok0 - req[0].tok0 - tokens;
             told.by_share = FastDiv(static_cast<uint32_t>(plan.share));
             *reinterpret_cast<PagedPlan *>(p.plan_ws) = told;
             if (!plan.valid) atomicOr(p.status, kStatusBadLengthBit);
@@ -1179,7 +1179,7 @@ paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
             const int tile = r / kPagedTile, row0 = tile * kPagedTile, rows = paged_min(kPagedTile, plan.shared_rows - row0);
             const int item = plan.prefix_units / shape.by_nkv * h + tile * plan.full_units;
             const int c0 = item / plan.by_share;
-            const int c1 = (item + (plan.prefix_blocks - 1) * paged_prefix_cost(plan.by_bytes, rows)) / plan.by_share;
+            const int c1 = (item + (plan.prefix_blocks - 1) * paged_cost(rows)) / plan.by_share;
             const long long rec = paged_shared_record(shape, plan, -1, h, row0, 0, 0, c0);
             acc.template add<D, 4>(p.rec_ml + rec + r - row0, rec_o + rec * C + chunk * rows + r - row0, rows, c1 - c0 + 1);
         }

@@ -39,7 +39,7 @@ constexpr int kPagedTile = 256;       // rows of a tile
 constexpr int kPagedSmallRows = 16;   // rows that go through mma.sync
 constexpr int kPagedAloneRows = 128;  // rows up to which a request shares the prefix's tiles
 constexpr int kPagedNarrowRows = 64;  // rows up to which own keys go to tiles of 16
-constexpr int kPagedMaxCost = 9;
+constexpr int kPagedMaxCost = 8;
 constexpr int kPagedMaxUnits = (1 << 30) - 1;  // two of them added stay below 2^31
 
 // Division of 0 <= n < 2^31 by a divisor that the host knows: n / d = (n mul) >> (32 + shift)
@@ -125,19 +125,15 @@ CFA_HD int paged_min(int a, int b) { return a < b ? a : b; }
 CFA_HD int paged_max(int a, int b) { return a > b ? a : b; }
 CFA_HD int paged_cdiv(int a, int b) { return (a + b - 1) / b; }
 
-// Clocks by 400 of a block of keys, and of beginning and ending an item by kPagedItemClocks
-// times 400, as measured where the warps' work bounds them: 16 rows 1600 a block (the other
-// warpgroup's block beside it), a tile of 128 rows 2800, of 256 rows 3560.
-CFA_HD int paged_cost(int rows) { return rows <= kPagedSmallRows ? 4 : rows <= kPagedAloneRows ? 7 : kPagedMaxCost; }
-CFA_HD int paged_item_cost(int rows) { return rows <= kPagedSmallRows ? 1 : 3; }
-#ifndef kPagedItemClocks
-constexpr int kPagedItemClocks = 8;
-#endif
-// Where the bytes of the keys bound the whole, blocks cost nearly alike, and an item next to
-// nothing: what the warps do goes on under the loads.
-CFA_HD int paged_prefix_cost(bool by_bytes, int rows) {
-    return rows <= kPagedSmallRows ? 4 : rows <= kPagedAloneRows ? (by_bytes ? 5 : 7) : by_bytes ? 6 : kPagedMaxCost;
-}
+// Clocks by 400 of a block of keys, and by 400 kPagedItemClocks of beginning and ending an
+// item, as fitted to the runs' times of batches whose work bounds them (head_dim 128: 16 rows
+// 1900 a block, with the other warpgroup's block beside it, and 2400 an item; tiles of
+// 128 and 256 rows 1700 and 3200 a block, 12000 an item).
+CFA_HD int paged_cost(int rows) { return rows <= kPagedAloneRows ? 5 : kPagedMaxCost; }
+CFA_HD int paged_item_cost(int rows) { return rows <= kPagedSmallRows ? 1 : 5; }
+constexpr int kPagedItemClocks = 6;
+// Where the bytes of the keys bound the whole, an item costs next to nothing: what the warps
+// do at its ends goes on under the loads.
 
 // Own keys that token i of a request sees.
 CFA_HD int paged_visible(const PagedRequest &r, int i) {
@@ -181,11 +177,11 @@ CFA_HD int paged_item_units(const PagedPlan &p, int rows, int cost, int blocks) 
     return blocks * cost + paged_item_cost(rows) * p.item_units;
 }
 
-// The totals: what all requests' own items cost, and shared_tokens of those that share.
-// block_bytes_clocks: clocks by 400 that the device's memory takes to deliver a block's keys
-// and values to one of its SMs while it serves them all.
-CFA_HD PagedPlan paged_plan(const PagedShape &s, const PagedCost &own, int shared_tokens, int block_bytes_clocks,
-                            bool valid) {
+// The totals: what all requests' own items cost, and the tokens of those that share and of
+// those that are alone. block_bytes_clocks: clocks by 400 that the device's memory takes to
+// deliver a block's keys and values to one of its SMs while it serves them all.
+CFA_HD PagedPlan paged_plan(const PagedShape &s, const PagedCost &own, int shared_tokens, int alone_tokens,
+                            int block_bytes_clocks, bool valid) {
     PagedPlan p;
     p.shared_rows = shared_tokens * s.G;
     p.prefix_blocks = paged_cdiv(s.prefix_len, kPagedKeys);
@@ -195,15 +191,15 @@ CFA_HD PagedPlan paged_plan(const PagedShape &s, const PagedCost &own, int share
     CFA_ROLLED for (int by_bytes = 0; by_bytes < 2; ++by_bytes) {
         p.by_bytes = by_bytes;
         p.item_units = by_bytes ? 1 : kPagedItemClocks;
-        p.full_units = paged_item_units(p, kPagedTile, paged_prefix_cost(by_bytes, kPagedTile), p.prefix_blocks);
+        p.full_units = paged_item_units(p, kPagedTile, paged_cost(kPagedTile), p.prefix_blocks);
         const long long pu =
             p.tiles == 0 ? 0
                          : s.nkv * ((p.tiles - 1ll) * p.full_units +
-                                    paged_item_units(p, last_rows, paged_prefix_cost(by_bytes, last_rows), p.prefix_blocks));
+                                    paged_item_units(p, last_rows, paged_cost(last_rows), p.prefix_blocks));
         all = pu + own.blocks + own.items * p.item_units;
         p.prefix_units = pu < kPagedMaxUnits ? static_cast<int>(pu) : 0;
-        // every block of own keys counts four units at least, and the prefix's keys are read once
-        const long long bytes = (own.blocks / 4 + static_cast<long long>(s.nkv) * (p.tiles ? p.prefix_blocks : 0)) * block_bytes_clocks;
+        // (requests that are alone have more work than bytes)
+        const long long bytes = alone_tokens > 0 ? 0 : (own.blocks / paged_cost(1) + static_cast<long long>(s.nkv) * (p.tiles ? p.prefix_blocks : 0)) * block_bytes_clocks;
         if (bytes <= all) break;
     }
     p.valid = valid && all < kPagedMaxUnits;
@@ -211,7 +207,7 @@ CFA_HD PagedPlan paged_plan(const PagedShape &s, const PagedCost &own, int share
     p.units = p.valid ? static_cast<int>(all) : 0;
     // at least a block, so that a run inside an item never comes away empty
     p.share = paged_max(kPagedMaxCost, paged_cdiv(p.units, s.grid));
-    p.alone_tokens = 0;
+    p.alone_tokens = alone_tokens;
     return p;
 }
 
@@ -241,7 +237,7 @@ CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const PagedEntry
         x.rows = paged_min(kPagedTile, p.shared_rows - x.row0);
         x.prefix_blocks = x.blocks = p.prefix_blocks;
         x.own_limit = 0;
-        x.cost = paged_prefix_cost(p.by_bytes, x.rows);
+        x.cost = paged_cost(x.rows);
         x.r = PagedRequest{0, 0, 0};
     } else {
         x.req = paged_find(B, u - p.prefix_units, [&](int b) { return e[b].unit; });
