@@ -18,7 +18,7 @@
 
 namespace cfa {
 const void *paged_tables_kernel_ptr();
-const void *paged_append_kernel_ptr();
+const void *paged_append_kernel_ptr(bool interleaved);
 const void *paged_attention_kernel_ptr(int d);
 const void *paged_merge_kernel_ptr(int d);
 int paged_attention_smem(int d, int seqs);
@@ -225,10 +225,13 @@ cfa_status launch_append(cfa_paged *p, const AppendArgs &a, cudaStream_t stream)
     kp.n_rows = a.n_pages * p->ps;
     kp.rd = p->rd;
     kp.interleaved = p->interleaved;
+    kp.by_units = cfa::FastDiv(static_cast<uint32_t>((p->interleaved ? p->rd / 8 : p->rd / 16) + (p->D - p->rd) / 8));
+    kp.heads_a_pass = cfa::kAppendThreads / static_cast<int>(kp.by_units.d);
+    kp.by_page = cfa::FastDiv(static_cast<uint32_t>(p->ps));
     kp.magnitude = p->magnitude;
     std::memcpy(kp.turns, p->turns, sizeof kp.turns);
     void *args[1] = {&kp};
-    return launch(cfa::paged_append_kernel_ptr(), a.n_tokens, cfa::kAppendThreads, 0, stream, args);
+    return launch(cfa::paged_append_kernel_ptr(p->interleaved != 0), a.n_tokens, cfa::kAppendThreads, 0, stream, args);
 }
 
 cfa_status launch_attention(cfa_paged *p, const AttnArgs &a, cudaStream_t stream) {

@@ -47,6 +47,9 @@ struct AppendParams {
     int n_rows;        // slots there are: n_pages * page_size
     int rd;            // rotated dims of a head; 0: none
     int interleaved;   // pairs (2i, 2i+1) instead of (i, i + rd/2)
+    FastDiv by_units;  // 16-byte chunks (or pairs) of a head's q or k
+    int heads_a_pass;  // heads that a block's threads take at a time
+    FastDiv by_page;
     float magnitude;   // factor on cos and sin
     // turns per position of pair i as a fraction of 2^64
     unsigned long long turns[64];

@@ -142,76 +142,116 @@ paged_tables_kernel(const TablesParams p) {
 // fp32 angle at position 2^22 would be off by 0.25 rad), and the reduction
 // that the sine needs is the wrap-around of the integer product.
 //
-// One block per token: the cosines and sines of its position are made once in
-// shared memory for all the heads; then every thread moves 16-byte chunks.
-__global__ void __launch_bounds__(kAppendThreads)
+// One block per token. A thread keeps one chunk of a head's dims (16 bytes, or a pair of
+// chunks where the layout pairs halves) and goes through the heads, so that its cosines and
+// sines stay in registers; they are made once for the block in shared memory while the first
+// chunks of q, k and v are already on their way (several of each: they would otherwise wait for
+// memory one after the other). What bounds it at many tokens is instructions: choosing head and
+// chunk anew for every 16 bytes took 24 us at 4096 tokens of 32/8 heads x 128 (100.7 MB).
+__device__ __forceinline__ uint32_t pack2_bf16_one(float lo, float hi) {  // one conversion, to nearest even
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <bool kInterleaved>
+__global__ void __launch_bounds__(kAppendThreads, 4)
 paged_append_kernel(const __grid_constant__ AppendParams p) {
     __shared__ float2 cs[64];
-    const int t = blockIdx.x, tid = threadIdx.x;
-    const int d = p.d, half = p.rd / 2;
+    constexpr int U = kInterleaved ? 4 : 2, kPairs = kInterleaved ? 4 : 8;  // loads ahead; pairs of a unit
+    const int t = blockIdx.x, tid = threadIdx.x, d = p.d, half = p.rd / 2;
     grid_dependency_wait();
-    const int pos = p.positions[t], slot = p.slots[t];
+    const int slot = __ldcg(p.slots + t);
+    const int pos = __ldcg(p.positions + t);
+    // units of a head: the rotated ones first, then 8 dims each that pass through
+    const int rot = kInterleaved ? p.rd / 8 : p.rd / 16, units = rot + (d - p.rd) / 8;
+    const int first = tid / p.by_units, unit = tid - first * units, step = p.heads_a_pass;
+    const bool turns = unit < rot;
+    const int at = turns ? 8 * unit : p.rd + 8 * (unit - rot);
+    const int heads = first < step ? p.n_heads + p.n_kv : 0;
+    const uint16_t *q = p.q + t * p.q_stride + at, *k = p.k + t * p.k_stride + at;
+    const uint16_t *v = p.v + t * p.v_stride + 8 * tid;
+    const int v_chunks = p.n_kv * d / 8;
+    uint4 a[U], b[U], c[U];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int h = h0 + j * step;
+            if (h >= heads) continue;
+            const uint16_t *src = h < p.n_heads ? q + h * d : k + (h - p.n_heads) * d;
+            a[j] = *reinterpret_cast<const uint4 *>(src);
+            if (!kInterleaved && turns) b[j] = *reinterpret_cast<const uint4 *>(src + half);
+        }
+    };
+    auto load_v = [&](int i0) {
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (tid + i0 + j * kAppendThreads < v_chunks)
+                c[j] = *reinterpret_cast<const uint4 *>(v + 8 * (i0 + j * kAppendThreads));
+    };
+    load(first);
+    load_v(0);
     if (tid < half) {
-        const unsigned long long a =
-            static_cast<unsigned long long>(static_cast<long long>(pos)) * p.turns[tid];
+        const unsigned long long turn = static_cast<unsigned long long>(static_cast<long long>(pos)) * p.turns[tid];
         // the signed upper half counts half turns in units of 2^-31
-        float s, c;
-        sincospif(static_cast<float>(static_cast<int>(a >> 32)) * 0x1p-31f, &s, &c);
-        cs[tid] = make_float2(c * p.magnitude, s * p.magnitude);
+        float sn, cn;
+        sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &sn, &cn);
+        cs[tid] = make_float2(cn * p.magnitude, sn * p.magnitude);
     }
     if (slot >= p.n_rows && tid == 0) atomicOr(p.status, kStatusBadPageBit);
-    const bool live = slot >= 0 && slot < p.n_rows;
     __syncthreads();
-    if (!live) {
-        grid_dependents_launch();
-        return;
-    }
-    const int page = slot / p.page_size, off = slot - page * p.page_size;
-    // chunks of a head: rotated units first, then 8 dims each that pass through
-    const int rot = p.interleaved ? p.rd / 8 : p.rd / 16;
-    const int units = rot + (d - p.rd) / 8;
-    const int n_rot = (p.n_heads + p.n_kv) * units, n = n_rot + p.n_kv * (d / 8);
-    auto cache_row = [&](uint16_t *pages, int h) {
-        return pages + ((static_cast<size_t>(page) * p.n_kv + h) * p.page_size + off) * d;
-    };
-    for (int i = tid; i < n; i += kAppendThreads) {
-        if (i >= n_rot) {
-            const int h = (i - n_rot) / (d / 8), c = (i - n_rot) % (d / 8);
-            *reinterpret_cast<uint4 *>(cache_row(p.v_pages, h) + 8 * c) =
-                *reinterpret_cast<const uint4 *>(p.v + t * p.v_stride + h * d + 8 * c);
-            continue;
+    if (slot >= 0 && slot < p.n_rows) {
+        float2 r[kPairs];
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) r[e] = turns ? cs[kPairs * unit + e] : make_float2(1.f, 0.f);
+        const int page = slot / p.by_page, off = slot - page * p.page_size;
+        const size_t row = (static_cast<size_t>(page) * p.n_kv * p.page_size + off) * d;
+        const size_t head_rows = static_cast<size_t>(p.page_size) * d;
+        uint16_t *q_out = p.q_out + static_cast<size_t>(t) * p.n_heads * d + at, *k_out = p.k_pages + row + at;
+        for (int h0 = first; h0 < heads; h0 += U * step) {
+            if (h0 > first) load(h0);
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int h = h0 + j * step;
+                if (h >= heads) continue;
+                uint16_t *dst = h < p.n_heads ? q_out + h * d : k_out + (h - p.n_heads) * head_rows;
+                if (turns) {
+                    float x[8], y[8];
+                    unpack8_bf16(a[j], x);
+                    if constexpr (kInterleaved) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            y[2 * e] = x[2 * e] * r[e].x - x[2 * e + 1] * r[e].y;
+                            y[2 * e + 1] = x[2 * e + 1] * r[e].x + x[2 * e] * r[e].y;
+                        }
+                    } else {
+                        float z[8];
+                        unpack8_bf16(b[j], z);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            y[e] = x[e] * r[e].x - z[e] * r[e].y;
+                            z[e] = z[e] * r[e].x + x[e] * r[e].y;
+                        }
+                        *reinterpret_cast<uint4 *>(dst + half) =
+                            make_uint4(pack2_bf16_one(z[0], z[1]), pack2_bf16_one(z[2], z[3]),
+                                       pack2_bf16_one(z[4], z[5]), pack2_bf16_one(z[6], z[7]));
+                    }
+                    a[j] = make_uint4(pack2_bf16_one(y[0], y[1]), pack2_bf16_one(y[2], y[3]),
+                                      pack2_bf16_one(y[4], y[5]), pack2_bf16_one(y[6], y[7]));
+                }
+                *reinterpret_cast<uint4 *>(dst) = a[j];
+            }
         }
-        const int h = i / units, u = i % units;
-        const uint16_t *src = h < p.n_heads ? p.q + t * p.q_stride + h * d
-                                            : p.k + t * p.k_stride + (h - p.n_heads) * d;
-        uint16_t *dst = h < p.n_heads ? p.q_out + (static_cast<size_t>(t) * p.n_heads + h) * d
-                                      : cache_row(p.k_pages, h - p.n_heads);
-        if (u >= rot) {
-            const int c = p.rd + 8 * (u - rot);
-            *reinterpret_cast<uint4 *>(dst + c) = *reinterpret_cast<const uint4 *>(src + c);
-        } else if (p.interleaved) {
-            float x[8];
-            unpack8_bf16(*reinterpret_cast<const uint4 *>(src + 8 * u), x);
-            uint32_t y[4];
+        const int shift = d == 128 ? 4 : 3;  // chunks of a head
+        uint16_t *v_out = p.v_pages + row;
+        for (int i0 = 0; tid + i0 < v_chunks; i0 += U * kAppendThreads) {
+            if (i0 > 0) load_v(i0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 r = cs[4 * u + e];
-                y[e] = pack2_bf16(x[2 * e] * r.x - x[2 * e + 1] * r.y, x[2 * e + 1] * r.x + x[2 * e] * r.y);
+            for (int j = 0; j < U; ++j) {
+                const int i = tid + i0 + j * kAppendThreads;
+                if (i < v_chunks)
+                    *reinterpret_cast<uint4 *>(v_out + (i >> shift) * head_rows + 8 * (i & ((1 << shift) - 1))) = c[j];
             }
-            *reinterpret_cast<uint4 *>(dst + 8 * u) = make_uint4(y[0], y[1], y[2], y[3]);
-        } else {
-            float x[8], z[8];
-            unpack8_bf16(*reinterpret_cast<const uint4 *>(src + 8 * u), x);
-            unpack8_bf16(*reinterpret_cast<const uint4 *>(src + half + 8 * u), z);
-            uint32_t y[4], w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 r = cs[8 * u + 2 * e], s = cs[8 * u + 2 * e + 1];
-                y[e] = pack2_bf16(x[2 * e] * r.x - z[2 * e] * r.y, x[2 * e + 1] * s.x - z[2 * e + 1] * s.y);
-                w[e] = pack2_bf16(z[2 * e] * r.x + x[2 * e] * r.y, z[2 * e + 1] * s.x + x[2 * e + 1] * s.y);
-            }
-            *reinterpret_cast<uint4 *>(dst + 8 * u) = make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4 *>(dst + half + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
     grid_dependents_launch();

@@ -5,7 +5,10 @@
 namespace cfa {
 
 const void *paged_tables_kernel_ptr() { return reinterpret_cast<const void *>(&paged_tables_kernel); }
-const void *paged_append_kernel_ptr() { return reinterpret_cast<const void *>(&paged_append_kernel); }
+const void *paged_append_kernel_ptr(bool interleaved) {
+    return interleaved ? reinterpret_cast<const void *>(&paged_append_kernel<true>)
+                       : reinterpret_cast<const void *>(&paged_append_kernel<false>);
+}
 const void *paged_attention_kernel_ptr(int d) {
     return d == 128 ? reinterpret_cast<const void *>(&paged_attention_kernel<128>)
                     : reinterpret_cast<const void *>(&paged_attention_kernel<64>);
