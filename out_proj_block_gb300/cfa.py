@@ -787,6 +787,7 @@ class Paged:
                                        page_size)
         self.device = torch.device("cuda", torch.cuda.current_device())
         self._index = self.device.index
+        self._page_shape = (n_kv_heads, page_size, head_dim)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -826,23 +827,21 @@ class Paged:
         if st != CFA_OK:
             raise CfaError(st, "cfa_paged_set_rope")
 
-    # Argument checks: one expression for what is right, since the smallest calls take
-    # the GPU only microseconds; what is wrong is looked for afterwards.
+    # Argument checks. The smallest calls take the GPU only microseconds, so each method
+    # asks in one expression whether everything is right, and looks for what is wrong
+    # (these two) only where it is not.
 
-    def _dense(self, name, t, shape, dtype):
-        if (t.dtype is dtype and t.shape == shape and t.is_contiguous()
-                and t.get_device() == self._index):
-            return t.data_ptr()
+    def _check(self, name, t, shape, dtype):
         if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        raise ValueError(f"{name} must be on {self.device}")
+        if t.get_device() != self._index:
+            raise ValueError(f"{name} must be on {self.device}")
 
-    def _rows(self, name, t, n, heads):
-        """Pointer and row stride of [n, heads, head_dim] with dense rows."""
+    def _check_rows(self, name, t, n, heads):
         if t.dtype is not _BF16:
             raise TypeError(f"{name} must be {_BF16}")
         if t.shape != (n, heads, self.head_dim):
@@ -853,13 +852,26 @@ class Paged:
             raise ValueError(f"{name} must be dense within a row")
         if t.get_device() != self._index:
             raise ValueError(f"{name} must be on {self.device}")
-        return t.data_ptr(), (s[0] if n > 1 else heads * self.head_dim)
+
+    def _rows(self, name, t, n, heads):
+        """Pointer and row stride of [n, heads, head_dim] with dense rows."""
+        d = self.head_dim
+        row, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+        if not (t.dtype is _BF16 and t.shape == (n, heads, d) and one == 1
+                and (head == d or heads == 1) and t.get_device() == self._index):
+            self._check_rows(name, t, n, heads)
+        return t.data_ptr(), (row if n > 1 else heads * d)
 
     def _pages(self, k_pages, v_pages):
-        n = k_pages.shape[0]
-        shape = (n, self.n_kv_heads, self.page_size, self.head_dim)
-        return n, self._dense("k_pages", k_pages, shape, _BF16), \
-            self._dense("v_pages", v_pages, shape, _BF16)
+        shape = k_pages.shape
+        i = self._index
+        if not (k_pages.dtype is v_pages.dtype is _BF16 and shape == v_pages.shape
+                and shape[1:] == self._page_shape and k_pages.is_contiguous()
+                and v_pages.is_contiguous() and k_pages.get_device() == i == v_pages.get_device()):
+            shape = (shape[0],) + self._page_shape
+            self._check("k_pages", k_pages, shape, _BF16)
+            self._check("v_pages", v_pages, shape, _BF16)
+        return shape[0], k_pages.data_ptr(), v_pages.data_ptr()
 
     def _stream(self, stream):
         if stream is None:
@@ -872,18 +884,33 @@ class Paged:
         lens, fresh, lens_out [B]; free_pages [n]; pool, pool_out [2]; tables
         [B, width]; cu [B + 1]; positions, slots [rows]. base is the prefix's
         length. Returns (cu, positions, slots)."""
-        one, n, free = lens.shape, slots.shape, free_pages.shape
+        one, n, free, i = lens.shape, slots.shape, free_pages.shape, self._index
         if len(one) != 1 or len(n) != 1 or len(free) != 1 or tables.dim() != 2:
             raise ValueError("lens, slots and free_pages have one dimension, tables two")
         B, width = tables.shape
-        dense = self._dense
+        if not (lens.dtype is fresh.dtype is free_pages.dtype is pool.dtype is tables.dtype
+                is lens_out.dtype is pool_out.dtype is cu.dtype is positions.dtype is slots.dtype
+                is _I32 and one[0] == B and fresh.shape == one == lens_out.shape
+                and positions.shape == n and pool.shape == (2,) == pool_out.shape
+                and cu.shape == (B + 1,)
+                and lens.is_contiguous() and fresh.is_contiguous() and free_pages.is_contiguous()
+                and pool.is_contiguous() and tables.is_contiguous() and lens_out.is_contiguous()
+                and pool_out.is_contiguous() and cu.is_contiguous() and positions.is_contiguous()
+                and slots.is_contiguous()
+                and lens.get_device() == i == fresh.get_device() == free_pages.get_device()
+                == pool.get_device() == tables.get_device() == lens_out.get_device()
+                == pool_out.get_device() == cu.get_device() == positions.get_device()
+                == slots.get_device()):
+            for name, t, shape in (("lens", lens, (B,)), ("fresh", fresh, (B,)),
+                                   ("free_pages", free_pages, free), ("pool", pool, (2,)),
+                                   ("tables", tables, (B, width)), ("lens_out", lens_out, (B,)),
+                                   ("pool_out", pool_out, (2,)), ("cu", cu, (B + 1,)),
+                                   ("positions", positions, n), ("slots", slots, n)):
+                self._check(name, t, shape, _I32)
         st = _lib.cfa_paged_tables(
-            self.handle, B, base, dense("lens", lens, (B,), _I32), dense("fresh", fresh, one, _I32),
-            dense("free_pages", free_pages, free, _I32), free[0], dense("pool", pool, (2,), _I32),
-            dense("tables", tables, (B, width), _I32), width, dense("lens_out", lens_out, one, _I32),
-            dense("pool_out", pool_out, (2,), _I32), dense("cu", cu, (B + 1,), _I32),
-            dense("positions", positions, n, _I32), dense("slots", slots, n, _I32), n[0],
-            self._stream(stream))
+            self.handle, B, base, lens.data_ptr(), fresh.data_ptr(), free_pages.data_ptr(), free[0],
+            pool.data_ptr(), tables.data_ptr(), width, lens_out.data_ptr(), pool_out.data_ptr(),
+            cu.data_ptr(), positions.data_ptr(), slots.data_ptr(), n[0], self._stream(stream))
         if st != CFA_OK:
             raise CfaError(st, "cfa_paged_tables")
         return cu, positions, slots
@@ -892,35 +919,62 @@ class Paged:
         """Rotate q into q_out and k into its page, put v into its page
         (cfa_paged_append). Returns q_out."""
         T = q.shape[0]
-        qp, qs = self._rows("q", q, T, self.n_heads)
-        kp, ks = self._rows("k", k, T, self.n_kv_heads)
-        vp, vs = self._rows("v", v, T, self.n_kv_heads)
         n, kc, vc = self._pages(k_pages, v_pages)
         st = _lib.cfa_paged_append(
-            self.handle, T, qp, qs, kp, ks, vp, vs, self._dense("positions", positions, (T,), _I32),
-            self._dense("slots", slots, (T,), _I32), n, kc, vc,
-            self._dense("q_out", q_out, (T, self.n_heads, self.head_dim), _BF16),
-            self._stream(stream))
+            self.handle, T, *self._rows("q", q, T, self.n_heads), *self._rows("k", k, T, self.n_kv_heads),
+            *self._rows("v", v, T, self.n_kv_heads), *self._tokens(T, positions, slots), n, kc, vc,
+            self._turned(T, q_out), self._stream(stream))
         if st != CFA_OK:
             raise CfaError(st, "cfa_paged_append")
         return q_out
 
-    def _attn(self, T, cu, lens, tables, prefix_table, prefix_len, out, lse):
-        B = lens.shape[0]
-        if tables.dim() != 2:
-            raise ValueError("tables must be [requests, width]")
+    def _tokens(self, T, positions, slots):
+        i = self._index
+        if not (positions.dtype is slots.dtype is _I32 and positions.shape == (T,) == slots.shape
+                and positions.is_contiguous() and slots.is_contiguous()
+                and positions.get_device() == i == slots.get_device()):
+            self._check("positions", positions, (T,), _I32)
+            self._check("slots", slots, (T,), _I32)
+        return positions.data_ptr(), slots.data_ptr()
+
+    def _turned(self, T, q_out):
+        shape = (T, self.n_heads, self.head_dim)
+        if not (q_out.dtype is _BF16 and q_out.shape == shape and q_out.is_contiguous()
+                and q_out.get_device() == self._index):
+            self._check("q_out", q_out, shape, _BF16)
+        return q_out.data_ptr()
+
+    def _attn(self, T, cu, lens, tables, prefix_table, prefix_len, scale, out, lse):
+        one, i = lens.shape, self._index
+        if len(one) != 1 or tables.dim() != 2:
+            raise ValueError("lens has one dimension, tables two")
         if prefix_len < 0:
             raise ValueError("prefix_len must not be negative")
+        if scale is not None and not scale > 0.0:
+            raise ValueError("scale must be positive")
+        B, width = tables.shape
+        shape = (T, self.n_heads, self.head_dim)
+        if not (lens.dtype is cu.dtype is tables.dtype is _I32 and out.dtype is _BF16
+                and one[0] == B and cu.shape == (B + 1,) and out.shape == shape
+                and lens.is_contiguous() and cu.is_contiguous() and tables.is_contiguous()
+                and out.is_contiguous()
+                and lens.get_device() == i == cu.get_device() == tables.get_device() == out.get_device()):
+            self._check("lens", lens, one, _I32)
+            self._check("cu", cu, one[:0] + (one[0] + 1,), _I32)
+            self._check("tables", tables, (one[0], width), _I32)
+            self._check("out", out, shape, _BF16)
         pt = None
         if prefix_len:
             if prefix_table is None or prefix_table.numel() * self.page_size < prefix_len:
                 raise ValueError("prefix_table does not hold prefix_len positions")
-            pt = self._dense("prefix_table", prefix_table, (prefix_table.numel(),), _I32)
-        return (B, self._dense("cu", cu, (B + 1,), _I32), pt,
-                self._dense("tables", tables, (B, tables.shape[1]), _I32), tables.shape[1],
-                self._dense("lens", lens, (B,), _I32),
-                self._dense("out", out, (T, self.n_heads, self.head_dim), _BF16),
-                None if lse is None else self._dense("lse", lse, (T, self.n_heads), _F32))
+            if not (prefix_table.dtype is _I32 and prefix_table.is_contiguous()
+                    and prefix_table.get_device() == i):
+                self._check("prefix_table", prefix_table, prefix_table.shape, _I32)
+            pt = prefix_table.data_ptr()
+        if lse is not None:
+            self._check("lse", lse, shape[:2], _F32)
+        return (B, cu.data_ptr(), pt, tables.data_ptr(), width, lens.data_ptr(), out.data_ptr(),
+                None if lse is None else lse.data_ptr(), scale or 0.0)
 
     def attend(self, q, cu, lens, tables, k_pages, v_pages, out, prefix_table=None,
                prefix_len: int = 0, scale: Optional[float] = None, lse=None, stream=None):
@@ -929,12 +983,10 @@ class Paged:
         T = q.shape[0]
         qp, qs = self._rows("q", q, T, self.n_heads)
         n, kc, vc = self._pages(k_pages, v_pages)
-        B, cup, pt, tp, width, lp, op, sp = self._attn(T, cu, lens, tables, prefix_table,
-                                                       prefix_len, out, lse)
-        if scale is not None and not scale > 0.0:
-            raise ValueError("scale must be positive")
-        st = _lib.cfa_paged_attention(self.handle, T, B, qp, qs, cup, pt, prefix_len, tp, width,
-                                      lp, n, kc, vc, scale or 0.0, op, sp, self._stream(stream))
+        B, cup, pt, tp, width, lp, op, sp, scale = self._attn(T, cu, lens, tables, prefix_table,
+                                                              prefix_len, scale, out, lse)
+        st = _lib.cfa_paged_attention(self.handle, T, B, qp, qs, cup, pt, prefix_len, tp, width, lp,
+                                      n, kc, vc, scale, op, sp, self._stream(stream))
         if st != CFA_OK:
             raise CfaError(st, "cfa_paged_attention")
         return out
@@ -944,20 +996,14 @@ class Paged:
               stream=None):
         """append, then attend on q_out (cfa_paged_layer). Returns out."""
         T = q.shape[0]
-        qp, qs = self._rows("q", q, T, self.n_heads)
-        kp, ks = self._rows("k", k, T, self.n_kv_heads)
-        vp, vs = self._rows("v", v, T, self.n_kv_heads)
         n, kc, vc = self._pages(k_pages, v_pages)
-        B, cup, pt, tp, width, lp, op, sp = self._attn(T, cu, lens, tables, prefix_table,
-                                                       prefix_len, out, lse)
-        if scale is not None and not scale > 0.0:
-            raise ValueError("scale must be positive")
-        st = _lib.cfa_paged_layer(self.handle, T, B, qp, qs, kp, ks, vp, vs,
-                                  self._dense("positions", positions, (T,), _I32),
-                                  self._dense("slots", slots, (T,), _I32), cup, pt, prefix_len, tp,
-                                  width, lp, n, kc, vc, scale or 0.0,
-                                  self._dense("q_out", q_out, (T, self.n_heads, self.head_dim),
-                                              _BF16), op, sp, self._stream(stream))
+        B, cup, pt, tp, width, lp, op, sp, scale = self._attn(T, cu, lens, tables, prefix_table,
+                                                              prefix_len, scale, out, lse)
+        st = _lib.cfa_paged_layer(
+            self.handle, T, B, *self._rows("q", q, T, self.n_heads),
+            *self._rows("k", k, T, self.n_kv_heads), *self._rows("v", v, T, self.n_kv_heads),
+            *self._tokens(T, positions, slots), cup, pt, prefix_len, tp, width, lp, n, kc, vc, scale,
+            self._turned(T, q_out), op, sp, self._stream(stream))
         if st != CFA_OK:
             raise CfaError(st, "cfa_paged_layer")
         return out
