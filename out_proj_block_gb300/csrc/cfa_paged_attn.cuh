@@ -721,12 +721,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     __syncwarp();
                     float s[4][4] = {};
                     if (keys > 0) {
-                        const uint32_t st = stage_at(0, block) + kkey * 128;
+                        // chunk 2 k + kc of the row, swizzled: bits 5 and 6 of its address turn with k
+                        const uint32_t st = stage_at(0, block) + kkey * 128 + ((kc ^ (kkey & 7)) << 4);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
                             uint32_t b[4], d[4];
-                            const uint32_t c = 2 * k + kc;
-                            const uint32_t at = st + (c >> 3) * S::kHalf + (((c & 7) ^ (kkey & 7)) << 4);
+                            const uint32_t at = (st ^ ((k & 3) << 5)) + (k >> 2) * S::kHalf;
                             ldmatrix_x4(b, at);
                             ldmatrix_x4(d, at + 16 * 128);
                             mma_16x8x16(s[0], q[k], b[0], b[1]);
@@ -792,7 +792,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     wait_full(1, block);
                     __syncwarp();
                     if (keys > 0) {
-                        const uint32_t st = stage_at(1, block) + vkey * 128;
+                        const uint32_t st = stage_at(1, block) + vkey * 128 + ((vc ^ (vkey & 7)) << 4);
                         auto values = [&](auto whole) {
                             // rows past the keys may hold anything, and 0 times NaN is NaN
                             auto keep = [&](int k) {
@@ -801,8 +801,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                             for (int i = 0; i < D / 16; ++i) {
                                 uint32_t b[4], d[4];
-                                const uint32_t c = 2 * i + vc;
-                                const uint32_t at = st + (c >> 3) * S::kHalf + (((c & 7) ^ (vkey & 7)) << 4);
+                                const uint32_t at = (st ^ ((i & 3) << 5)) + (i >> 2) * S::kHalf;
                                 ldmatrix_x4_trans(b, at);
                                 ldmatrix_x4_trans(d, at + 16 * 128);
                                 if constexpr (!decltype(whole)::value) {
@@ -904,8 +903,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             CFA_ROLLED for (int j = first_block; j < nb; j += step, ++scored) {
                 int key0;
                 const int keys = block_keys(x, x.b0 + j, &key0);
-                int lim = x.b0 + j < x.prefix_blocks ? keys : min(keys, see - key0);
-                CFA_ROLLED for (int h = 0; h < 2; ++h, lim -= 64) {
+                const int lim = x.b0 + j < x.prefix_blocks ? keys : min(keys, see - key0);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
                     wait(bs + 8 * h, scored & 1, kSiteSoftmaxExchange);
                     __syncwarp();
                     tcgen05_fence_after();
@@ -925,9 +925,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                         tmem_ld_x32(t_s + 64 * h, s);
                         tmem_ld_x32(t_s + 64 * h + 32, s + 32);
                         tmem_wait_ld();
-                        if (!__all_sync(~0u, lim >= 64)) {
+                        if (!__all_sync(~0u, lim - 64 * h >= 64)) {
 #pragma unroll
-                            for (int c = 0; c < 64; ++c) s[c] = c < lim ? s[c] : 0xff800000u;
+                            for (int c = 0; c < 64; ++c) s[c] = c < lim - 64 * h ? s[c] : 0xff800000u;
                         }
                         float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
