@@ -98,11 +98,10 @@ struct PagedCut {
 };
 
 // A shared row.
-struct PagedRow {
+struct alignas(16) PagedRow {
     int out_row;           // output row with key head 0
     int unit, head_units;  // first unit of its own keys' item, and units of a key head
     int blocks;            // the item's blocks
-    int rec, head_rows;    // record row of its later pieces (run 0, key head 0), and rows of a key head
     int rows, row;         // rows of the item's tile, and this one among them
 };
 

@@ -628,8 +628,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 d.unit = plan.prefix_units + req[b].unit + own * paged_item_units(plan, tile, paged_cost(tile), blocks);
                 d.head_units = (req[b + 1].unit - req[b].unit) / shape.by_nkv;
                 d.blocks = blocks;
-                d.rec = static_cast<int>(paged_shared_record(shape, plan, b, 0, row0, q.n, req[b].tok, 0));
-                d.head_rows = all;
                 d.rows = min(tile, all - row0);
                 d.row = mine - row0;
                 reinterpret_cast<PagedRow *>(p.plan_ws + kPagedPlanInts + 8 * shape.grid)[r] = d;
@@ -1111,11 +1109,12 @@ struct PagedMerge {
         for (int k = 0; k < CH; ++k) a[k].x *= g, a[k].y *= g, a[k].z *= g, a[k].w *= g;
         return f;
     }
-    // n pieces a run apart each: their maxima and sums at s, their chunks at o, `rows` rows a
-    // chunk; N at a time.
+    // n pieces, the first of a run each: their maxima and sums at s, their chunks at o, `rows`
+    // rows a chunk; N at a time.
     template <int D, int N>
     __device__ __forceinline__ void add(const float2 *s, const float4 *o, int rows, int n) {
-        CFA_ROLLED for (; n > 0; n -= N, s += N * kPagedTile, o += static_cast<size_t>(N) * kPagedTile * (D / 4)) {
+        constexpr int kRun = 2 * kPagedTile;  // record rows of a run
+        CFA_ROLLED for (; n > 0; n -= N, s += N * kRun, o += static_cast<size_t>(N) * kRun * (D / 4)) {
             float2 t[N];
             float4 v[N][CH];
 #pragma unroll
@@ -1124,9 +1123,9 @@ struct PagedMerge {
 #pragma unroll
                 for (int k = 0; k < CH; ++k) v[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (i < n) {
-                    t[i] = __ldcg(s + i * kPagedTile);
+                    t[i] = __ldcg(s + i * kRun);
 #pragma unroll
-                    for (int k = 0; k < CH; ++k) v[i][k] = __ldcg(o + i * kPagedTile * (D / 4) + k * rows);
+                    for (int k = 0; k < CH; ++k) v[i][k] = __ldcg(o + i * kRun * (D / 4) + k * rows);
                 }
             }
             float top = m;
@@ -1170,18 +1169,20 @@ paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
         const int group = rest / shape.by_nkv, h = rest - group * p.n_kv, r = group * 32 + lane;
         if (r >= plan.shared_rows) continue;
         const PagedRow d = row_of[r];
-        // its first own piece's record, wherever that piece ran
-        const long long first_rec = paged_first_record(plan, h);
-        const float2 own_ml = __ldcg(p.rec_ml + first_rec + r);
-        const float4 own = __ldcg(rec_o + first_rec * C + chunk * plan.shared_rows + r);
+        // the records of its first pieces, wherever those ran
+        const long long pre_rec = paged_first_record(shape, plan, false, h), own_rec = paged_first_record(shape, plan, true, h);
+        const int at = chunk * plan.shared_rows + r;
+        const float2 pre_ml = __ldcg(p.rec_ml + pre_rec + r), own_ml = __ldcg(p.rec_ml + own_rec + r);
+        const float4 pre = __ldcg(rec_o + pre_rec * C + at), own = __ldcg(rec_o + own_rec * C + at);
         PagedMerge<1> acc;
         if (plan.prefix_blocks > 0) {
             const int tile = r / kPagedTile, row0 = tile * kPagedTile, rows = paged_min(kPagedTile, plan.shared_rows - row0);
             const int item = plan.prefix_units / shape.by_nkv * h + tile * plan.full_units;
             const int c0 = item / plan.by_share;
-            const int c1 = (item + (plan.prefix_blocks - 1) * paged_cost(rows)) / plan.by_share;
-            const long long rec = paged_shared_record(shape, plan, -1, h, row0, 0, 0, c0);
-            acc.template add<D, 4>(p.rec_ml + rec + r - row0, rec_o + rec * C + chunk * rows + r - row0, rows, c1 - c0 + 1);
+            const int more = (item + (plan.prefix_blocks - 1) * paged_cost(rows)) / plan.by_share - c0;
+            const long long rec = paged_run_record(shape, plan, true, c0 + 1);
+            acc.fold(pre_ml, &pre, acc.raise(pre_ml.x));
+            acc.template add<D, 4>(p.rec_ml + rec + r - row0, rec_o + rec * C + chunk * rows + r - row0, rows, more);
         }
         if (d.blocks > 0) {
             const int item = d.unit + h * d.head_units;
@@ -1190,7 +1191,7 @@ paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
             if (plan.prefix_blocks == 0 && more == 0) continue;  // the piece wrote the result
             acc.fold(own_ml, &own, acc.raise(fmaxf(acc.m, own_ml.x)));
             if (more > 0) {
-                const long long rec = d.rec + static_cast<long long>(h) * d.head_rows + static_cast<long long>(d0 + 1) * kPagedTile;
+                const long long rec = paged_run_record(shape, plan, true, d0 + 1);
                 acc.template add<D, 1>(p.rec_ml + rec + d.row, rec_o + rec * C + chunk * d.rows + d.row, d.rows, more);
             }
         }
@@ -1219,8 +1220,8 @@ paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
         const int r = cut.row0 + row, i = r / shape.by_G;
         PagedMerge<4> acc;
         // the run's own piece and the next run's, then what further runs have
-        long long rec = paged_alone_record(shape, plan, 1, run + 1);
-        const long long recs[2] = {paged_alone_record(shape, plan, 0, run), rec};
+        long long rec = paged_run_record(shape, plan, true, run + 1);
+        const long long recs[2] = {paged_run_record(shape, plan, false, run), rec};
         float2 t[2];
         float4 v[2][4];
 #pragma unroll

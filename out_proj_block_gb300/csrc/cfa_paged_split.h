@@ -308,42 +308,31 @@ CFA_HD int paged_last_run(const PagedPlan &p, int first_unit, int blocks, int co
     return (first_unit + (blocks - 1) * cost) / p.share;
 }
 
-// Where a piece leaves its record: rows of the record arrays. A shared request's first
-// piece over its own keys has its place by key head and shared row, so that the merge finds
-// it without looking the request up. The other pieces of shared rows have room for their rows at
-// every run they meet: the rows of all the items before them plus a tile a run (so that
-// neither the next item nor the next run reaches back). Tiles of requests that are alone are
-// cut at most at a run's ends: two tiles a run, behind the others. shared_tok0: shared tokens
-// before the request, n: its tokens.
-CFA_HD long long paged_first_record(const PagedPlan &p, int h) { return static_cast<long long>(h) * p.shared_rows; }
-CFA_HD long long paged_shared_record(const PagedShape &s, const PagedPlan &p, int req, int h, int row0, int n,
-                                     int shared_tok0, int c) {
-    const long long head = static_cast<long long>(s.nkv) * p.shared_rows;
-    const long long before = req < 0 ? static_cast<long long>(h) * p.shared_rows
-                                     : head + static_cast<long long>(s.nkv) * shared_tok0 * s.G +
-                                           static_cast<long long>(h) * n * s.G;
-    return head + before + row0 + static_cast<long long>(c) * kPagedTile;
+// Where a piece leaves its record: rows of the record arrays. An item's first piece over the
+// prefix and its first over a shared request's own keys have their places by key head and
+// shared row, where the merge finds them without looking anything up. A run's first piece, where
+// it goes on with an item, has the run's own place; so has a tile of a request that is alone
+// and that the run's end cuts (a request that is alone has no place by shared row).
+CFA_HD long long paged_first_record(const PagedShape &s, const PagedPlan &p, bool own, int h) {
+    return (static_cast<long long>(own ? s.nkv : 0) + h) * p.shared_rows;
 }
-CFA_HD long long paged_alone_record(const PagedShape &s, const PagedPlan &p, int b0, int c) {
-    return 3ll * s.nkv * p.shared_rows + static_cast<long long>(s.grid) * kPagedTile +
-           (2ll * c + (b0 > 0 ? 0 : 1)) * kPagedTile;
+CFA_HD long long paged_run_record(const PagedShape &s, const PagedPlan &p, bool first_of_run, int run) {
+    return 2ll * s.nkv * p.shared_rows + (2ll * run + (first_of_run ? 0 : 1)) * kPagedTile;
 }
 CFA_HD long long paged_record_rows(const PagedShape &s, long long shared_rows) {
-    return 3 * s.nkv * shared_rows + 3ll * s.grid * kPagedTile;
+    return 2 * s.nkv * shared_rows + 2ll * s.grid * kPagedTile;
 }
 // A piece's record: outputs at rec D + (chunk stride + row) 4, maximum and sum at rec + row,
-// for rows from rec_row on.
+// for rows from rec_row on. shared_tok0: shared tokens before the request.
 CFA_HD void paged_record(const PagedShape &s, const PagedPlan &p, int shared_tok0, int run, PagedPiece &x) {
-    x.rec_row = 0;
-    x.rec_stride = x.rows;
-    if (x.req >= 0 && paged_alone(s, x.r.n)) {
-        x.rec = paged_alone_record(s, p, x.b0, run);
-    } else if (x.req >= 0 && x.b0 == 0) {
-        x.rec = paged_first_record(p, x.h);
+    if (x.b0 > 0 || (x.req >= 0 && paged_alone(s, x.r.n))) {
+        x.rec = paged_run_record(s, p, x.b0 > 0, run);
+        x.rec_row = 0;
+        x.rec_stride = x.rows;
+    } else {
+        x.rec = paged_first_record(s, p, x.req >= 0, x.h);
         x.rec_row = shared_tok0 * s.G + x.row0;
         x.rec_stride = p.shared_rows;
-    } else {
-        x.rec = paged_shared_record(s, p, x.req, x.h, x.row0, x.r.n, shared_tok0, run);
     }
 }
 
