@@ -237,6 +237,33 @@ def test_append_in_place_and_bad_slots(cfa):
         assert plan.status() == cfa.CFA_OK
 
 
+def test_append_most_tokens_far_apart(cfa):
+    """The most tokens a plan takes, in rows that lie beyond 2^32 elements."""
+    T, d, ps = 1 << 17, 64, 64
+    rows = torch.empty(T, 1 << 15, dtype=torch.bfloat16, device="cuda")[:, :3 * d]
+    rows.copy_(normal(1, T, 3 * d))
+    dense = rows.contiguous()
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    slots = torch.flip(pos, (0,)).contiguous()
+    got = []
+    with cfa.Paged(1, T, 1, 1, d, ps) as plan:
+        plan.set_rope()
+        for x in (rows, dense):
+            kp, vp = (torch.zeros(T // ps, 1, ps, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+            q = torch.zeros(T, 1, d, dtype=torch.bfloat16, device="cuda")
+            plan.append(x[:, :d].unsqueeze(1), x[:, d:2 * d].unsqueeze(1), x[:, 2 * d:].unsqueeze(1), pos, slots,
+                        kp, vp, q)
+            got.append((q, kp, vp))
+        assert plan.status() == cfa.CFA_OK
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    assert torch.equal(got[0][2].view(T, d), torch.flip(dense[:, 2 * d:], (0,)))
+    some = [0, 1, T // 2, T - 1]
+    x = f64(dense[some])
+    want = ref.rotate(x[:, None, d:2 * d], some, ref.frequencies(10000.0, d), False)[:, 0]
+    k = f64(got[0][1].view(T, d)[[T - 1 - t for t in some]])
+    assert np.all(np.abs(k - want) <= H8 * np.abs(want) + 1e-6 * 2 * np.abs(x).max())
+
+
 def test_append_checks_arguments(cfa):
     T, nh, d = 4, 4, 64
     q, k, v = normal(1, T, nh, d), normal(2, T, 2, d), normal(3, T, 2, d)
@@ -389,6 +416,82 @@ def test_attention_random_shapes(cfa, seed):
         out, lse = attend(plan, c, scale=scale)
         assert plan.status() == cfa.CFA_OK
     check_attn(c, out, lse, scale)
+
+
+TILES = [
+    # nh, nkv, d, ps, prefix, lens, new tokens
+    (8, 1, 128, 64, 200, [300, 150], [12, 9]),                # 96 and 72 rows: one tile over own keys
+    (8, 1, 64, 32, 0, [500, 77, 40, 9], [16, 3, 7, 17]),      # 128, 24, 56, and 136 rows
+    (3, 1, 128, 16, 90, [64, 65, 20], [21, 20, 22]),          # 63, 60 and 66 rows
+    (16, 2, 128, 64, 300, [700, 513], [100, 65]),             # 800 and 520 rows: several tiles each
+    (16, 1, 64, 16, 0, [70, 300], [70, 17]),                  # the same without a prefix
+    (4, 4, 64, 64, 700, [i % 5 for i in range(600)], [1] * 600),         # three tiles over the prefix
+    (2, 1, 64, 16, 33, [i % 40 for i in range(1024)], [i % 3 for i in range(1024)]),
+    (2, 1, 128, 32, 0, [1 + i % 70 for i in range(1024)], [1] * 1024),
+    (128, 1, 128, 64, 150, [70, 1], [1, 1]),                  # a group of 128: the most that shares
+    (129, 1, 64, 64, 150, [70, 1], [1, 1]),                   # and one more
+    (1024, 2, 64, 64, 20, [9], [1]),
+]
+
+
+@pytest.mark.parametrize("case", range(len(TILES)))
+def test_attention_tiles(cfa, case):
+    nh, nkv, d, ps, prefix, lens, news = TILES[case]
+    c = attn_case(300 + case, nh, nkv, d, ps, prefix, lens, news)
+    with cfa.Paged(len(lens), sum(news), nh, nkv, d, ps) as plan:
+        out, lse = attend(plan, c)
+        assert plan.status() == cfa.CFA_OK
+    check_attn(c, out, lse)
+
+
+def test_attention_far_pages_and_rows(cfa):
+    """Pages beyond 2^32 elements of their cache, query rows as far behind the first."""
+    nh, nkv, d, ps, pages = 8, 8, 128, 64, 70000
+    c = attn_case(12, nh, nkv, d, ps, 100, [130, 70, 3], [2, 1, 1])
+    n, T = c["kp"].shape[0], c["q"].shape[0]
+    kp, vp = (torch.empty(pages, nkv, ps, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kp[pages - n:], vp[pages - n:] = c["kp"], c["vp"]
+    far = dict(c, kp=kp, vp=vp, tables=(c["tables"] + (pages - n)).astype(np.int32),
+               prefix_table=[i + pages - n for i in c["prefix_table"]])
+    q = torch.empty(T, 1 << 31, dtype=torch.bfloat16, device="cuda")[:, :nh * d].unflatten(1, (nh, d))
+    q.copy_(c["q"])
+    with cfa.Paged(3, T, nh, nkv, d, ps) as plan:
+        out, lse = attend(plan, far, q=q)
+        assert plan.status() == cfa.CFA_OK
+        check_attn(c, out, lse)
+        k, v = normal(1, T, nkv, d), normal(2, T, nkv, d)
+        slots = [pages * ps - 1, (pages - n) * ps, pages * ps - 2, -1]
+        plan.append(q, k, v, ints([0] * T), ints(slots), kp, vp, torch.empty_like(out))
+        assert plan.status() == cfa.CFA_OK
+        for t, s in enumerate(slots[:3]):
+            assert torch.equal(kp[s // ps, :, s % ps], k[t]) and torch.equal(vp[s // ps, :, s % ps], v[t])
+
+
+def test_two_graphs_of_one_plan(cfa):
+    """Graphs of different batches take turns in the plan's workspace."""
+    cases = [attn_case(13, 8, 2, 64, 32, 400, [300, 10, 99], [1, 3, 40]),
+             attn_case(14, 8, 2, 64, 32, 0, [900] * 4, [1] * 4),
+             attn_case(15, 8, 2, 64, 32, 1300, [1], [1])]
+    with cfa.Paged(4, 44, 8, 2, 64, 32) as plan:
+        want = [attend(plan, c) for c in cases]
+        graphs, got = [], []
+        for c in cases:
+            a = (c["q"], ints(c["cu"]), ints(c["lens"]), torch.from_numpy(c["tables"]).cuda(), c["kp"], c["vp"])
+            out, lse = torch.zeros_like(c["q"]), torch.zeros(c["q"].shape[:2], device="cuda")
+            pt = ints(c["prefix_table"]) if c["prefix"] else None
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                plan.attend(*a, out, prefix_table=pt, prefix_len=c["prefix"], lse=lse)
+            graphs.append((g, a, pt))
+            got.append((out, lse))
+        for turn in (0, 1, 2, 2, 1, 0, 2, 0):
+            for x in got[turn]:
+                x.zero_()
+            graphs[turn][0].replay()
+            attend(plan, cases[(turn + 1) % 3])
+            assert all(torch.equal(x, y) for x, y in zip(got[turn], want[turn]))
+        assert plan.status() == cfa.CFA_OK
 
 
 def test_attention_extreme_scores(cfa):

@@ -2,6 +2,8 @@
 device call, the frequencies and tables of the oracle against closed forms."""
 import ctypes
 import math
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -121,3 +123,15 @@ def test_oracle_attention_of_equal_keys_is_the_mean():
     assert lse[1, 0] == pytest.approx(2.0 + math.log(8))
     out, lse, _ = ref.attention(q, [0, 2], [1], [[1]], k, v)
     assert np.all(out[0] == 0) and lse[0, 0] == -math.inf and np.allclose(out[1, 0], v[1, 0, 0])
+
+
+# ------------------------------------------------------------------ how the attention is cut
+
+
+def test_split_covers_every_block_once(tmp_path):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = str(tmp_path / "paged_split_check")
+    subprocess.run(["g++", "-std=c++17", "-O2", "-I", os.path.join(root, "out_proj_block_gb300", "csrc"),
+                    os.path.join(root, "tests", "paged_split_check.cpp"), "-o", exe], check=True)
+    out = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "ok", out.stdout
