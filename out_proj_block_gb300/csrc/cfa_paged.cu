@@ -203,6 +203,11 @@ cfa_status check_attention(const cfa_paged *p, const AttnArgs &a) {
     return overlaps(a.out, no, a.lse, nl) ? CFA_ERR_INVALID_ARG : CFA_OK;
 }
 
+// Threads of an append block, which takes a token's rows of q, k and v: 64 up to 16 KB of
+// them, 128 above (60 MB of rows, read and written: 6 KB a token 21.3 and 23.9 us, 12 KB 20.7
+// and 21.8, 16 KB 20.4 and 20.6, 18 KB 22.1 and 20.6, 24 KB 23.6 and 20.9).
+int append_threads(const cfa_paged *p) { return (p->nh + 2 * p->nkv) * p->D * 2 <= 16384 ? 64 : cfa::kAppendThreads; }
+
 cfa_status launch_append(cfa_paged *p, const AppendArgs &a, cudaStream_t stream) {
     if (a.n_tokens == 0) return CFA_OK;
     cfa::AppendParams kp{};
@@ -226,12 +231,12 @@ cfa_status launch_append(cfa_paged *p, const AppendArgs &a, cudaStream_t stream)
     kp.rd = p->rd;
     kp.interleaved = p->interleaved;
     kp.by_units = cfa::FastDiv(static_cast<uint32_t>((p->interleaved ? p->rd / 8 : p->rd / 16) + (p->D - p->rd) / 8));
-    kp.heads_a_pass = cfa::kAppendThreads / static_cast<int>(kp.by_units.d);
+    kp.heads_a_pass = append_threads(p) / static_cast<int>(kp.by_units.d);
     kp.by_page = cfa::FastDiv(static_cast<uint32_t>(p->ps));
     kp.magnitude = p->magnitude;
     std::memcpy(kp.turns, p->turns, sizeof kp.turns);
     void *args[1] = {&kp};
-    return launch(cfa::paged_append_kernel_ptr(p->interleaved != 0), a.n_tokens, cfa::kAppendThreads, 0, stream, args);
+    return launch(cfa::paged_append_kernel_ptr(p->interleaved != 0), a.n_tokens, append_threads(p), 0, stream, args);
 }
 
 cfa_status launch_attention(cfa_paged *p, const AttnArgs &a, cudaStream_t stream) {

@@ -55,7 +55,7 @@ struct AppendParams {
     unsigned long long turns[64];
 };
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;  // at most (append_threads)
 
 // ----------------------------------------- attention over a shared prefix
 

@@ -146,8 +146,10 @@ paged_tables_kernel(const TablesParams p) {
 // chunks where the layout pairs halves) and goes through the heads, so that its cosines and
 // sines stay in registers; they are made once for the block in shared memory while the first
 // chunks of q, k and v are already on their way (several of each: they would otherwise wait for
-// memory one after the other). What bounds it at many tokens is instructions: choosing head and
-// chunk anew for every 16 bytes took 24 us at 4096 tokens of 32/8 heads x 128 (100.7 MB).
+// memory one after the other). Instructions count: choosing head and chunk anew for every 16
+// bytes took 24 us at 4096 tokens of 32/8 heads x 128 (100.7 MB). So does that some blocks of
+// an SM load while others store, which small blocks do best: 256 threads took 21.3 us there,
+// 128 18.9, 64 17.3 (5.8 TB/s). The bytes bound it at many tokens, the launch at few.
 __device__ __forceinline__ uint32_t pack2_bf16_one(float lo, float hi) {  // one conversion, to nearest even
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -155,11 +157,11 @@ __device__ __forceinline__ uint32_t pack2_bf16_one(float lo, float hi) {  // one
 }
 
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kAppendThreads, 4)
+__global__ void __launch_bounds__(kAppendThreads, 8)
 paged_append_kernel(const __grid_constant__ AppendParams p) {
     __shared__ float2 cs[64];
     constexpr int U = kInterleaved ? 4 : 2, kPairs = kInterleaved ? 4 : 8;  // loads ahead; pairs of a unit
-    const int t = blockIdx.x, tid = threadIdx.x, d = p.d, half = p.rd / 2;
+    const int t = blockIdx.x, tid = threadIdx.x, threads = blockDim.x, d = p.d, half = p.rd / 2;
     grid_dependency_wait();
     const int slot = __ldcg(p.slots + t);
     const int pos = __ldcg(p.positions + t);
@@ -186,8 +188,8 @@ paged_append_kernel(const __grid_constant__ AppendParams p) {
     auto load_v = [&](int i0) {
 #pragma unroll
         for (int j = 0; j < U; ++j)
-            if (tid + i0 + j * kAppendThreads < v_chunks)
-                c[j] = *reinterpret_cast<const uint4 *>(v + 8 * (i0 + j * kAppendThreads));
+            if (tid + i0 + j * threads < v_chunks)
+                c[j] = *reinterpret_cast<const uint4 *>(v + 8 * (i0 + j * threads));
     };
     load(first);
     load_v(0);
@@ -244,11 +246,11 @@ paged_append_kernel(const __grid_constant__ AppendParams p) {
         }
         const int shift = d == 128 ? 4 : 3;  // chunks of a head
         uint16_t *v_out = p.v_pages + row;
-        for (int i0 = 0; tid + i0 < v_chunks; i0 += U * kAppendThreads) {
+        for (int i0 = 0; tid + i0 < v_chunks; i0 += U * threads) {
             if (i0 > 0) load_v(i0);
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                const int i = tid + i0 + j * kAppendThreads;
+                const int i = tid + i0 + j * threads;
                 if (i < v_chunks)
                     *reinterpret_cast<uint4 *>(v_out + (i >> shift) * head_rows + 8 * (i & ((1 << shift) - 1))) = c[j];
             }
