@@ -529,7 +529,9 @@ typedef struct cfa_paged cfa_paged; /* opaque */
  * 1024, page_size 16, 32 or a multiple of 64 up to 1<<22
  * (CFA_ERR_UNSUPPORTED otherwise; CFA_ERR_INVALID_ARG for non-positive values
  * or n_heads not a multiple of n_kv_heads). No rotation until
- * cfa_paged_set_rope. NULL on failure; cfa_last_error() says why.
+ * cfa_paged_set_rope. The workspace holds 2 n_kv_heads min(max_tokens G,
+ * 128 max_seqs) + 512 SMs rows of head_dim + 2 floats (G = n_heads /
+ * n_kv_heads). NULL on failure; cfa_last_error() says why.
  */
 cfa_paged *cfa_paged_create(int max_seqs, int max_tokens, int n_heads, int n_kv_heads,
                             int head_dim, int page_size);
@@ -554,7 +556,7 @@ enum {
  * by parts, with r = original_ctx f_i / 2 pi turns over the original context
  * and g = clamp((r - low_turns) / (high_turns - low_turns), 0, 1), the
  * frequency is g f_i + (1 - g) f_i / factor. Needs theta >= 1, factor >= 1,
- * magnitude > 0, all finite, and by parts 0 <= low_turns < high_turns and
+ * 0 < magnitude <= 1e6, all finite, and by parts 0 <= low_turns < high_turns and
  * original_ctx >= 1 (CFA_ERR_INVALID_ARG; a rotary_dim that is no multiple of
  * 16 or above head_dim: CFA_ERR_UNSUPPORTED). Held on the host: a recorded
  * graph keeps the rotation it was recorded with.
@@ -577,7 +579,10 @@ cfa_status cfa_paged_set_rope(cfa_paged *paged, double theta, int rotary_dim, in
  *     page; rows from the total up to n_slots get position 0 and slot -1;
  *   - lens_out [n_seqs] = lens + fresh, pool_out = {pool[0] + pages taken, pool[1]}
  *     (lens_out may be lens and pool_out may be pool; no other overlap).
- * tables is [n_seqs, table_width] (table_width <= 1<<18). All or nothing: a
+ * A page id below 0 or with slots above 2^31 - 1 gives slot -1 and is flagged
+ * (CFA_ERR_INVALID_ARG from cfa_paged_status). tables is [n_seqs, table_width]
+ * (table_width <= 1<<18, table_width * page_size and base <= 1<<30, here and
+ * below). All or nothing: a
  * negative length, a total above n_slots, a request longer than
  * table_width * page_size (then cfa_paged_status returns CFA_ERR_INVALID_ARG) or too few
  * free pages (CFA_ERR_NO_PAGES) leave the tables as they were, lens_out = lens,
@@ -600,8 +605,8 @@ cfa_status cfa_paged_tables(cfa_paged *paged, int n_seqs, int base, const int *l
  * overlap q otherwise, nor k, v or the pages. Rows with a negative slot are
  * skipped: their q_out row stays as it was. A slot of n_pages * page_size or
  * more is skipped too and flagged (CFA_ERR_INVALID_ARG from cfa_paged_status).
- * Two tokens with the same slot leave either's row there. With n_tokens 0
- * this call and the next two do nothing (pointers may then be NULL).
+ * Two tokens with the same slot leave in its row pieces of either. With
+ * n_tokens 0 this call and the next two do nothing (pointers may then be NULL).
  */
 cfa_status cfa_paged_append(cfa_paged *paged, int n_tokens, const void *q, long long q_stride,
                             const void *k, long long k_stride, const void *v, long long v_stride,
@@ -653,7 +658,8 @@ cfa_status cfa_paged_layer(cfa_paged *paged, int n_tokens, int n_seqs, const voi
  * cfa_plan_status; CFA_ERR_NO_PAGES after a refused cfa_paged_tables). */
 cfa_status cfa_paged_status(cfa_paged *paged);
 
-/* One-line JSON description (shape, rotation, grid, shared memory, workspace). */
+/* One-line JSON description (shape, rotation, SMs used, shared memory and
+ * workspace bytes). */
 cfa_status cfa_paged_describe(const cfa_paged *paged, char *buf, int len);
 
 #ifdef __cplusplus

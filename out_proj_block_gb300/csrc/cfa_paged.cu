@@ -405,7 +405,7 @@ cfa_status cfa_paged_tables(cfa_paged *p, int n_seqs, int base, const int *lens,
     if (!p || n_seqs < 1 || n_seqs > p->max_seqs || base < 0 || !lens || !fresh || n_free < 0 ||
         (n_free > 0 && !free_pages) || !pool || !tables || table_width < 1 ||
         table_width > cfa::kPagedMaxTableWidth ||
-        static_cast<long long>(table_width) * p->ps + base > (1ll << 31) - 1 || !lens_out ||
+        static_cast<long long>(table_width) * p->ps > (1 << 30) || base > (1 << 30) || !lens_out ||
         !pool_out || !cu || !positions || !slots || n_slots < 1 || n_slots > p->max_tokens)
         return fail(CFA_ERR_INVALID_ARG);
     const size_t B4 = 4u * static_cast<size_t>(n_seqs), S4 = 4u * static_cast<size_t>(n_slots);
@@ -445,6 +445,7 @@ cfa_status cfa_paged_tables(cfa_paged *p, int n_seqs, int base, const int *lens,
     kp.n_free = n_free;
     kp.n_slots = n_slots;
     kp.base = base;
+    kp.max_page = static_cast<int>(((1ll << 31) - 1) / p->ps) - 1;
     const int grid = std::min(p->num_sms, (n_slots + cfa::kTablesThreads - 1) / cfa::kTablesThreads);
     void *args[1] = {&kp};
     const cfa_status st = launch(cfa::paged_tables_kernel_ptr(), grid, cfa::kTablesThreads,
@@ -528,9 +529,10 @@ cfa_status cfa_paged_describe(const cfa_paged *p, char *buf, int len) {
     std::snprintf(buf, static_cast<size_t>(len),
                   "{\"max_seqs\": %d, \"max_tokens\": %d, \"n_heads\": %d, \"n_kv_heads\": %d, "
                   "\"head_dim\": %d, \"page_size\": %d, \"rotary_dim\": %d, \"interleaved\": %d, "
-                  "\"scaling\": %d, \"num_sms\": %d}",
+                  "\"scaling\": %d, \"num_sms\": %d, \"smem_bytes\": %d, \"workspace_bytes\": %lld}",
                   p->max_seqs, p->max_tokens, p->nh, p->nkv, p->D, p->ps, p->rd, p->interleaved,
-                  p->scaling, p->num_sms);
+                  p->scaling, p->num_sms, cfa::paged_attention_smem(p->D, p->max_seqs),
+                  p->rec_rows * (4ll * p->D + 8));
     return CFA_OK;
 }
 

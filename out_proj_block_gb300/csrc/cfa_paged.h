@@ -30,6 +30,7 @@ struct TablesParams {
     unsigned *ticket;       // arrivals of the grid's blocks; 0 between calls
     unsigned *status;
     int B, width, page_size, n_free, n_slots, base;
+    int max_page;           // the last page whose slots an int holds
 };
 
 constexpr int kTablesThreads = 512;

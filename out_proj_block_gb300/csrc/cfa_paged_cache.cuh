@@ -102,7 +102,8 @@ paged_tables_kernel(const TablesParams p) {
             const int page = j < have ? p.tables[static_cast<size_t>(b) * p.width + j]
                                       : p.free_pages[taken + rank[b] + j - have];
             pos = p.base + at_b;
-            slot = page * ps + at_b - j * ps;
+            if (page >= 0 && page <= p.max_page) slot = page * ps + at_b - j * ps;
+            else atomicOr(p.status, kStatusBadPageBit);
         }
         p.positions[t] = pos;
         p.slots[t] = slot;

@@ -157,6 +157,29 @@ def test_tables_checks_arguments(cfa):
         assert plan.status() == cfa.CFA_OK
 
 
+@pytest.mark.parametrize("bad", [-1, -(1 << 31), (1 << 31) - 1, 1 << 27])
+def test_tables_bad_page_ids(cfa, bad):
+    """A held page or a free one that no slot can name: slot -1, flagged, the rest as ever."""
+    with cfa.Paged(2, 8, 2, 1, 64, 16) as plan:
+        tables = ints([[bad, -7, -7], [3, -7, -7]])
+        cu, pos, slots, lens, pool = ints([0] * 3), ints([7] * 8), ints([7] * 8), ints([14, 16]), ints([0, 2])
+        plan.build_tables(lens, ints([4, 2]), ints([bad, 5]), pool, tables, lens, pool, cu, pos, slots)
+        assert plan.status() == cfa.CFA_ERR_INVALID_ARG
+        # the first request's tokens 14 and 15 lie in its held page, 16 and 17 in the first free one
+        assert slots.tolist() == [-1, -1, -1, -1, 5 * 16, 5 * 16 + 1, -1, -1]
+        assert pos.tolist() == [14, 15, 16, 17, 16, 17, 0, 0] and cu.tolist() == [0, 4, 6]
+        assert tables.tolist() == [[bad, bad, -7], [3, 5, -7]]
+        assert lens.tolist() == [18, 18] and pool.tolist() == [2, 2]
+        assert plan.status() == cfa.CFA_OK
+
+
+def test_describe(cfa):
+    with cfa.Paged(2, 8, 4, 2, 64, 16) as plan:
+        d = plan.describe()
+        rows = 2 * 2 * 16 + 512 * d["num_sms"]
+        assert d["workspace_bytes"] == rows * 4 * 66 and d["smem_bytes"] > 0 and d["page_size"] == 16
+
+
 # --------------------------------------------------------------------- append
 
 
