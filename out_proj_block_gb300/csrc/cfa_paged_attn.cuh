@@ -398,6 +398,16 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         *key0 = (pre ? j : j - x.prefix_blocks) * kPagedKeys;
         return min(kPagedKeys, (pre ? p.prefix_len : x.own_limit) - *key0);
     };
+    // Where a row of a piece's tile lies: its token and its head of the group.
+    auto find_row = [&](const PagedPiece &x, int r) {
+        const int i = (x.row0 + r) / shape.by_G;
+        int t = x.r.tok0 + i;
+        if (x.req < 0) {
+            const int b = paged_find(B, i, [&](int k) { return req[k].tok; });
+            t = req[b].tok0 + i - req[b].tok;
+        }
+        return t | (x.row0 + r - i * G) << kPagedTokenBits;
+    };
     if (warp >= kComputeWarps) {
         registers_for_issue();
         if (warp < kComputeWarps + 2) {
@@ -515,18 +525,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (lane == 0) *reinterpret_cast<PagedPiece *>(slot) = x;
                 const bool few = x.rows <= kPagedSmallRows;
                 int *row_at = reinterpret_cast<int *>(slot + S::kSlotRows);
-#pragma unroll 2
-                for (int r = lane; r < x.rows; r += 32) {
-                    const int i = (x.row0 + r) / shape.by_G;
-                    int t = x.r.tok0 + i;
-                    if (x.req < 0) {
-                        const int b = paged_find(B, i, [&](int k) { return req[k].tok; });
-                        t = req[b].tok0 + i - req[b].tok;
-                    }
-                    row_at[r] = t | ((x.row0 + r) - i * G) << kPagedTokenBits;
-                }
-                __syncwarp();
-                if (few) {
+                if (few) {  // (of a tile the compute warps do it, a thread a row)
+                    if (lane < x.rows) row_at[lane] = find_row(x, lane);
+                    __syncwarp();
                     CFA_ROLLED for (int c = lane; c < 16 * (D / 8); c += 32) {
                         const int r = c / (D / 8), ch = c % (D / 8);
                         uint8_t *dst = slot + S::kSlotQ + (ch >> 3) * 2048 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
@@ -680,7 +681,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 piece_done();
                 continue;
             }
-            const int *row_at = reinterpret_cast<const int *>(slot + S::kSlotRows);
+            int *row_at = reinterpret_cast<int *>(smem + S::kSlots + at_slot * S::kSlot + S::kSlotRows);
             const bool final = x.final;
             float *rec_o = p.rec_o + x.rec * D + x.rec_row * 4;
             float2 *rec_ml = p.rec_ml + x.rec + x.rec_row;
@@ -888,6 +889,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 
             // ---- tcgen05
             const bool split = x.rows <= 128;
+            if (tid < x.rows) row_at[tid] = find_row(x, tid);
             meet();  // the scratch and the query tiles are free
             // asynchronous copies: all of them on their way before the first has landed
 #pragma unroll 4
