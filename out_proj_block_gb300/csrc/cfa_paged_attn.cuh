@@ -664,9 +664,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             // one thread's word for its warpgroup: where its wait gave up, no warp goes on alone
             const uint32_t at_slot = k_piece % kPagedSlots;
             const bool there = wait(bar_piece + 8 * at_slot, (k_piece / kPagedSlots) & 1, kSiteStageFull);
-            if (wtid == 0) misc[2 + wg] = there;
+            volatile int *word = misc + 8 + 2 * wg + (k_piece & 1);  // (read before the next but one is written)
+            if (wtid == 0) *word = there;
             wg_bar();
-            if (!misc[2 + wg]) break;
+            if (!*word) break;
             const uint8_t *slot = smem + S::kSlots + at_slot * S::kSlot;
             const PagedPiece &x = *reinterpret_cast<const PagedPiece *>(slot);
             const int nb = x.b1 - x.b0;
@@ -674,7 +675,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             const bool few = x.rows <= kPagedSmallRows;
             auto piece_done = [&]() {
                 n += nb;
-                wg_bar();  // (and misc is free again)
+                __syncwarp();
                 if (lane == 0) mbar_arrive(bar_piece_free + 8 * at_slot);
             };
             if (few && static_cast<int>(k_piece & 1) != wg) {  // the other warpgroup's
@@ -854,8 +855,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 leave(r0, m0, l0, 0);
                 leave(r0 + 8, m1, l1, 2);
                 wg_bar();
-                const int row = wtid & 15;
-                CFA_ROLLED for (int c = wtid >> 4; c < D / 4 && row < x.rows; c += 8) {
+                // (threads for 2, 4, 8 or 16 rows)
+                const int bits = x.rows <= 2 ? 1 : x.rows <= 4 ? 2 : x.rows <= 8 ? 3 : 4, row = wtid & ((1 << bits) - 1);
+                CFA_ROLLED for (int c = wtid >> bits; c < D / 4 && row < x.rows; c += 128 >> bits) {
                     float2 w[4];
                     float4 v[4];
 #pragma unroll
