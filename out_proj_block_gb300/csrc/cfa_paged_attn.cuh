@@ -315,6 +315,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         int *sums = reinterpret_cast<int *>(smem + S::kQ), *items_before = sums + 64;  // (free until the first piece)
         int units = 0, items = 0, tokens = 0;
         bool bad = false;
+        const int cu_first = __ldcg(p.cu), cu_end = __ldcg(p.cu + B);
         auto more = [](int a, int b) { return min(a + b, kPagedMaxUnits); };
         CFA_ROLLED for (int first = 0; first < B; first += kPagedThreads) {
             const int b = first + tid;
@@ -361,8 +362,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             tokens += __shfl_sync(~0u, wt, 15);
             if (first + kPagedThreads < B) __syncthreads();  // the sums are read
         }
-        if (tid == 0) req[B] = PagedEntry{units, tokens, __ldcg(p.cu + B), 0};
-        const int all_tokens = __ldcg(p.cu + B) - __ldcg(p.cu);
+        if (tid == 0) req[B] = PagedEntry{units, tokens, cu_end, 0};
+        const int all_tokens = cu_end - cu_first;
         plan = paged_plan(shape, PagedCost{units, items}, tokens, all_tokens - tokens, p.block_clocks, true);
         CFA_ROLLED for (int b = tid; b < B; b += kPagedThreads) req[b].unit += items_before[b] * plan.item_units;
         if (tid == 0) req[B].unit += items * plan.item_units;

@@ -69,11 +69,11 @@ CFA_HD int operator/(int n, const FastDiv &f) {
 
 struct PagedShape {
     int G, nkv, prefix_len, grid;
-    FastDiv by_G, by_nkv;
+    FastDiv by_G, by_nkv, by_grid;
     PagedShape() = default;
     PagedShape(int G_, int nkv_, int prefix, int grid_)
         : G(G_), nkv(nkv_), prefix_len(prefix), grid(grid_), by_G(static_cast<uint32_t>(G_)),
-          by_nkv(static_cast<uint32_t>(nkv_)) {}
+          by_nkv(static_cast<uint32_t>(nkv_)), by_grid(static_cast<uint32_t>(grid_)) {}
 };
 
 // What one scan over the requests finds.
@@ -187,26 +187,25 @@ CFA_HD PagedPlan paged_plan(const PagedShape &s, const PagedCost &own, int share
     p.prefix_blocks = paged_cdiv(s.prefix_len, kPagedKeys);
     p.tiles = p.prefix_blocks == 0 ? 0 : paged_cdiv(p.shared_rows, kPagedTile);
     const int last_rows = p.shared_rows - (p.tiles - 1) * kPagedTile;  // every tile but the last is full
-    long long all = 0;
-    CFA_ROLLED for (int by_bytes = 0; by_bytes < 2; ++by_bytes) {
-        p.by_bytes = by_bytes;
-        p.item_units = by_bytes ? 1 : kPagedItemClocks;
-        p.full_units = paged_item_units(p, kPagedTile, paged_cost(kPagedTile), p.prefix_blocks);
-        const long long pu =
-            p.tiles == 0 ? 0
-                         : s.nkv * ((p.tiles - 1ll) * p.full_units +
-                                    paged_item_units(p, last_rows, paged_cost(last_rows), p.prefix_blocks));
-        all = pu + own.blocks + own.items * p.item_units;
-        p.prefix_units = pu < kPagedMaxUnits ? static_cast<int>(pu) : 0;
-        // (requests that are alone have more work than bytes)
-        const long long bytes = alone_tokens > 0 ? 0 : (own.blocks / paged_cost(1) + static_cast<long long>(s.nkv) * (p.tiles ? p.prefix_blocks : 0)) * block_bytes_clocks;
-        if (bytes <= all) break;
-    }
+    const bool some = p.tiles > 0;
+    // units of a block of all the prefix's items, and their paged_item_cost()s
+    const int block = some ? s.nkv * ((p.tiles - 1) * kPagedMaxCost + paged_cost(last_rows)) : 0;
+    const int items = some ? s.nkv * ((p.tiles - 1) * paged_item_cost(kPagedTile) + paged_item_cost(last_rows)) : 0;
+    const long long prefix = static_cast<long long>(block) * p.prefix_blocks;
+    // (requests that are alone have more work than bytes)
+    const int own_blocks = static_cast<int>(own.blocks < kPagedMaxUnits ? own.blocks : kPagedMaxUnits) / paged_cost(1);
+    const long long bytes =
+        alone_tokens > 0 ? 0 : (own_blocks + (some ? static_cast<long long>(s.nkv) * p.prefix_blocks : 0)) * block_bytes_clocks;
+    p.by_bytes = bytes > prefix + own.blocks + (items + own.items) * kPagedItemClocks;
+    p.item_units = p.by_bytes ? 1 : kPagedItemClocks;
+    p.full_units = paged_item_units(p, kPagedTile, kPagedMaxCost, p.prefix_blocks);
+    const long long pu = prefix + static_cast<long long>(items) * p.item_units;
+    const long long all = pu + own.blocks + own.items * p.item_units;
     p.valid = valid && all < kPagedMaxUnits;
-    if (!p.valid) p.prefix_units = 0;
+    p.prefix_units = p.valid ? static_cast<int>(pu) : 0;
     p.units = p.valid ? static_cast<int>(all) : 0;
     // at least a block, so that a run inside an item never comes away empty
-    p.share = paged_max(kPagedMaxCost, paged_cdiv(p.units, s.grid));
+    p.share = paged_max(kPagedMaxCost, (p.units + s.grid - 1) / s.by_grid);
     p.alone_tokens = alone_tokens;
     return p;
 }
