@@ -106,4 +106,7 @@ struct alignas(16) PagedRow {
     int rows, row;         // rows of the item's tile, and this one among them
 };
 
+// (the merge finds them by 8 ints each)
+static_assert(sizeof(PagedCut) == 32 && sizeof(PagedRow) == 32, "their places in plan_ws");
+
 }  // namespace cfa

@@ -39,7 +39,7 @@
 //   16 requests, 4096 shared keys and some 1024 own ones, no groups: 46.2 us, 213 MB (4.6 TB/s)
 //   64 requests, 32768 and 2048, 8 key heads: 84 us, 431 MB (5.1 TB/s)
 //   256 requests, 8192 and 512, 8 key heads, pages of 16: 93 us, 315 MB
-//   8 requests of up to 512 new tokens, 4096 and 1500, 8 key heads: 230 us (1.13 PFLOP/s)
+//   8 requests of up to 512 new tokens, 4096 and 1500, 8 key heads: 228 us (1.14 PFLOP/s)
 //   one request, 64 and 64 keys: 10.7 us
 // What bounds it: many keys, the memory, with some 4 us before the first copy (the plan, and
 // instructions that arrive one line after the other) and 4 us of the merge; small pieces over
@@ -47,7 +47,7 @@
 // products and the softmax alike: a half of 64 keys and 256 rows takes 1500 clocks of products
 // (the 64-key scores read their 128 query rows from shared memory for 59 clocks where the
 // arithmetic takes 34) and 1575 of softmax with its waits. Scores of 128 keys at once spend
-// fewer clocks but find no second buffer in TMEM: 249 us instead of 229. The loops' code has to
+// fewer clocks but find no second buffer in TMEM: 249 us instead of 229 then. The loops' code has to
 // stay in the instruction cache: versions above some 7600 instructions lost 5%.
 #pragma once
 
@@ -1102,8 +1102,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
 // the runs, several at a time, then the request's own, so that their loads, maxima and
 // sums among them, are on their way together with the row's: the kernel is a chain of
 // two loads (the plan, then rows and records), and what counts is that nothing else waits
-// in between. 3 to 5 us behind the attention at up to 2048 shared rows; 12 us (40 MB of
-// records, 3.3 TB/s) behind the 151 cut tiles of 8 prompt chunks. Four blocks an SM, of 64
+// in between. 3 to 5 us behind the attention at up to 2048 shared rows; 11 us (40 MB of
+// records) behind the 151 cut tiles of 8 prompt chunks. Four blocks an SM, of 64
 // registers a thread, were no faster than three.
 template <int CH>
 struct PagedMerge {
