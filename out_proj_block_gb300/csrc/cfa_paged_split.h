@@ -127,11 +127,11 @@ CFA_HD int paged_cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // Clocks by 400 of a block of keys, and by 400 kPagedItemClocks of beginning and ending an
 // item, as fitted to the runs' times of batches whose work bounds them (head_dim 128: 16 rows
-// 1900 a block, with the other warpgroup's block beside it, and 2400 an item; tiles of
+// 1900 a block, with the other warpgroup's block beside it, and 2000 an item; tiles of
 // 128 and 256 rows 1700 and 3200 a block, 12000 an item).
 CFA_HD int paged_cost(int rows) { return rows <= kPagedAloneRows ? 5 : kPagedMaxCost; }
-CFA_HD int paged_item_cost(int rows) { return rows <= kPagedSmallRows ? 1 : 5; }
-constexpr int kPagedItemClocks = 6;
+CFA_HD int paged_item_cost(int rows) { return rows <= kPagedSmallRows ? 1 : 6; }
+constexpr int kPagedItemClocks = 5;
 // Where the bytes of the keys bound the whole, an item costs next to nothing: what the warps
 // do at its ends goes on under the loads.
 
