@@ -467,6 +467,36 @@ def test_attention_tiles(cfa, case):
     check_attn(c, out, lse)
 
 
+@pytest.mark.parametrize("n,own,prefix,nh,nkv,d", [
+    (5000, 6001, 300, 8, 2, 128),          # a long prompt: many tiles, each cut by a run's end at most once
+    (1, 1 << 20, 0, 4, 1, 64),             # one row over a million keys: every run has a piece of it
+    (2, 70, 1 << 19, 2, 1, 128),           # and over a long prefix
+    (1 << 17, 40, 9, 1, 1, 64),            # the most tokens, most of them without own keys
+])
+def test_attention_long(cfa, n, own, prefix, nh, nkv, d):
+    """The largest calls, a few rows of each against 64 bits."""
+    ps, np_ = 64, -(-prefix // 64)
+    pages = np_ + -(-own // ps)
+    kp, vp = normal(1, pages, nkv, ps, d), normal(2, pages, nkv, ps, d)
+    c = dict(q=normal(3, n, nh, d), kp=kp, vp=vp, tables=np.arange(np_, pages, dtype=np.int32)[None].copy(),
+             lens=[own], cu=[0, n], prefix_table=list(range(np_)), prefix=prefix)
+    with cfa.Paged(1, n, nh, nkv, d, ps) as plan:
+        out, lse = attend(plan, c)
+        assert plan.status() == cfa.CFA_OK
+    for i in {0, 1 % n, n // 3, max(0, n - own), n - 1}:
+        see = min(own, max(0, own - n + i + 1))
+        for h in {0, nh - 1}:
+            g = h * nkv // nh
+            k, v = (torch.cat((x[:np_, g].reshape(-1, d)[:prefix], x[np_:, g].reshape(-1, d)[:see])).double()
+                    for x in (kp, vp))
+            s = k @ c["q"][i, h].double() / math.sqrt(d)
+            w = torch.softmax(s, 0)
+            want, size = w @ v, w @ v.abs()
+            tol = (1 + 2.0 ** -4) * H8 * (want.abs() + size) + 1e-6
+            assert torch.all((out[i, h].double() - want).abs() <= tol)
+            assert abs(float(lse[i, h]) - float(torch.logsumexp(s, 0))) <= 1e-4
+
+
 def test_attention_far_pages_and_rows(cfa):
     """Pages beyond 2^32 elements of their cache, query rows as far behind the first."""
     nh, nkv, d, ps, pages = 8, 8, 128, 64, 70000
