@@ -315,7 +315,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         // stop at the limit, which makes the plan invalid
         int *sums = reinterpret_cast<int *>(smem + S::kQ), *items_before = sums + 64;  // (free until the first piece)
         int units = 0, items = 0, tokens = 0;
-        bool bad = false;
+        bool bad = false, refused = false;
         const int cu_first = __ldcg(p.cu), cu_end = __ldcg(p.cu + B);
         auto more = [](int a, int b) { return min(a + b, kPagedMaxUnits); };
         CFA_ROLLED for (int first = 0; first < B; first += kPagedThreads) {
@@ -345,7 +345,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (lane >= o) su = more(su, a), sk = more(sk, c), st += d;
             }
             if (lane == 31) sums[warp] = su, sums[16 + warp] = sk, sums[32 + warp] = st;
-            __syncthreads();
+            refused |= __syncthreads_or(bad) != 0;
             int wu = 0, wk = 0, wt = 0;
             if (lane < 16) wu = sums[lane], wk = sums[16 + lane], wt = sums[32 + lane];
             CFA_ROLLED for (int o = 1; o < 16; o <<= 1) {
@@ -365,10 +365,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         if (tid == 0) req[B] = PagedEntry{units, tokens, cu_end, 0};
         const int all_tokens = cu_end - cu_first;
-        plan = paged_plan(shape, PagedCost{units, items}, tokens, all_tokens - tokens, p.block_clocks, true);
+        plan = paged_plan(shape, PagedCost{units, items}, tokens, all_tokens - tokens, p.block_clocks, !refused);
         CFA_ROLLED for (int b = tid; b < B; b += kPagedThreads) req[b].unit += items_before[b] * plan.item_units;
         if (tid == 0) req[B].unit += items * plan.item_units;
-        if (__syncthreads_or(bad)) plan.valid = plan.units = plan.prefix_units = 0;
+        __syncthreads();
         tcgen05_fence_after();
         if (blockIdx.x == 0 && tid == 0) {
             PagedPlan told = plan;

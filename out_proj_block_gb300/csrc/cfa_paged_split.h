@@ -179,7 +179,8 @@ CFA_HD int paged_item_units(const PagedPlan &p, int rows, int cost, int blocks) 
 
 // The totals: what all requests' own items cost, and the tokens of those that share and of
 // those that are alone. block_bytes_clocks: clocks by 400 that the device's memory takes to
-// deliver a block's keys and values to one of its SMs while it serves them all.
+// deliver a block's keys and values to one of its SMs while it serves them all. valid: the
+// offsets are in order.
 CFA_HD PagedPlan paged_plan(const PagedShape &s, const PagedCost &own, int shared_tokens, int alone_tokens,
                             int block_bytes_clocks, bool valid) {
     PagedPlan p;
@@ -207,6 +208,9 @@ CFA_HD PagedPlan paged_plan(const PagedShape &s, const PagedCost &own, int share
     // at least a block, so that a run inside an item never comes away empty
     p.share = paged_max(kPagedMaxCost, (p.units + s.grid - 1) / s.by_grid);
     p.alone_tokens = alone_tokens;
+    // A refused batch has no rows either: offsets that go up and down count tokens more than
+    // once, beyond what the workspace has room for.
+    if (!p.valid) p.shared_rows = p.tiles = p.alone_tokens = 0;
     return p;
 }
 

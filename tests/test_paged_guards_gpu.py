@@ -1,0 +1,52 @@
+"""What the paged-cache operators do on the GPU with device data out of range: refused or
+skipped as a whole, flagged in the status word, and nothing else changed."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def cfa():
+    from out_proj_block_gb300 import build
+    build.build()
+    from out_proj_block_gb300 import cfa
+    return cfa
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def normal(seed, *shape):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("B,T,each,prefix", [(64, 32, 32, 0), (64, 32, 32, 100), (600, 100, 3, 70)])
+def test_attention_offsets_up_and_down(cfa, B, T, each, prefix):
+    """Every second request looks right by itself, and together they count the same tokens many
+    times over: refused, with no row touched. The plan has room for all that are counted."""
+    nh, nkv, d, ps = 8, 2, 64, 64
+    pages = 8
+    cu = [each * (b % 2) for b in range(B + 1)]
+    q, kp, vp = normal(1, T, nh, d), normal(2, pages, nkv, ps, d), normal(3, pages, nkv, ps, d)
+    out = torch.full((T, nh, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, nh), 7.0, device="cuda")
+    lens, tables = ints([40] * B), torch.zeros(B, 2, dtype=torch.int32, device="cuda")
+    good = ints([min(b, T) for b in range(B + 1)])
+    kw = dict(prefix_table=ints([1, 2]), prefix_len=prefix) if prefix else {}
+    with cfa.Paged(B, 4096, nh, nkv, d, ps) as plan:
+        for _ in range(2):
+            plan.attend(q, ints(cu), lens, tables, kp, vp, out, lse=lse, **kw)
+            assert torch.all(out == 7.0) and torch.all(lse == 7.0)
+            assert plan.status() == cfa.CFA_ERR_INVALID_ARG
+        first, again = torch.empty_like(out), torch.empty_like(out)
+        plan.attend(q, good, lens, tables, kp, vp, first, lse=lse, **kw)
+        plan.attend(q, ints(cu), lens, tables, kp, vp, out, **kw)
+        assert plan.status() == cfa.CFA_ERR_INVALID_ARG
+        plan.attend(q, good, lens, tables, kp, vp, again, lse=lse, **kw)
+        n = min(B, T)
+        assert torch.equal(first[:n], again[:n]) and torch.all(out == 7.0)
+        assert plan.status() == cfa.CFA_OK

@@ -1,0 +1,19 @@
+"""What the paged-cache operators make of values out of range, without a GPU: the rules that
+their kernels share with the host."""
+import os
+import subprocess
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def run_check(tmp_path, name, *args, timeout=120):
+    """Compiles tests/<name>.cpp with the host compiler and runs it."""
+    exe = str(tmp_path / name)
+    subprocess.run(["g++", "-std=c++17", "-O2", "-I", os.path.join(ROOT, "out_proj_block_gb300", "csrc"),
+                    *args, os.path.join(ROOT, "tests", name + ".cpp"), "-o", exe], check=True)
+    out = subprocess.run([exe], capture_output=True, text=True, timeout=timeout)
+    assert out.returncode == 0 and out.stdout.strip() == "ok", out.stdout
+
+
+def test_refused_batches_have_no_rows(tmp_path):
+    run_check(tmp_path, "paged_guards_check")
