@@ -582,11 +582,11 @@ cfa_status cfa_paged_set_rope(cfa_paged *paged, double theta, int rotary_dim, in
  * A page id below 0 or with slots above 2^31 - 1 gives slot -1 and is flagged
  * (CFA_ERR_INVALID_ARG from cfa_paged_status). tables is [n_seqs, table_width]
  * (table_width <= 1<<18, table_width * page_size and base <= 1<<30, here and
- * below). All or nothing: a
- * negative length, a total above n_slots, a request longer than
- * table_width * page_size (then cfa_paged_status returns CFA_ERR_INVALID_ARG) or too few
- * free pages (CFA_ERR_NO_PAGES) leave the tables as they were, lens_out = lens,
- * pool_out = pool, every cu 0, every slot -1 and every position 0.
+ * below). All or nothing: a negative length or pool counter, a total above n_slots,
+ * a request longer than table_width * page_size (then cfa_paged_status returns
+ * CFA_ERR_INVALID_ARG) or too few free pages (CFA_ERR_NO_PAGES) leave the tables as
+ * they were, lens_out = lens, pool_out = pool, every cu 0, every slot -1 and every
+ * position 0.
  * Errors: CFA_ERR_INVALID_ARG (NULL, sizes out of the plan's range, overlaps),
  * CFA_ERR_ALIGNMENT, CFA_ERR_CUDA.
  */

@@ -35,6 +35,12 @@ struct TablesParams {
 
 constexpr int kTablesThreads = 512;
 
+// Free pages that a pool has left, by its two counters; -1 where one of them is below zero.
+CFA_HD int paged_pool_left(int taken, int there, int n_free) {
+    if (taken < 0 || there < 0) return -1;
+    return paged_max(0, paged_min(there, n_free) - taken);
+}
+
 // ------------------------------------------------------------ rotary append
 
 struct AppendParams {

@@ -17,7 +17,7 @@ namespace cfa {
 //   token i of request b: position base + lens_b + i, slot = page * ps + offset
 //
 // All or nothing: where the pages, the token rows or the table's width do not
-// suffice, or a length is negative, nothing is granted (no table entry
+// suffice, or a length or a counter of the pool is negative, nothing is granted (no table entry
 // changes, every cu is 0, every slot -1) and the status word says why.
 //
 // Every block scans all the lengths by itself (at most 8 KB, from L2), so that
@@ -80,9 +80,9 @@ paged_tables_kernel(const TablesParams p) {
     if (b0 < b1 && b1 == B) cu[B] = at, rank[B] = ar;
     __syncthreads();
     const int total = cu[B], grant = rank[B];
-    const int taken = p.pool[0], there = min(p.pool[1], p.n_free);
-    const bool invalid = bad != 0 || total > p.n_slots || taken < 0;
-    const bool none = !invalid && grant > max(there - taken, 0);
+    const int taken = p.pool[0], left = paged_pool_left(taken, p.pool[1], p.n_free);
+    const bool invalid = bad != 0 || total > p.n_slots || left < 0;
+    const bool none = !invalid && grant > left;
     const bool ok = !invalid && !none;
 
     const int nthreads = gridDim.x * kTablesThreads, gid = blockIdx.x * kTablesThreads + tid;

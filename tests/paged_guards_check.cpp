@@ -1,8 +1,10 @@
 // Checks of what the paged kernels make of device data that is out of range, by the rules they
-// share with the host (csrc/cfa_paged_split.h). Prints "ok" or what is wrong.
+// share with the host (csrc/cfa_paged.h, csrc/cfa_paged_split.h). Prints "ok" or what is wrong.
+#include "cfa_paged.h"
 #include "cfa_paged_split.h"
 
 #include <algorithm>
+#include <climits>
 #include <cstdio>
 #include <vector>
 
@@ -40,6 +42,23 @@ const char *offsets(int max_seqs, int max_tokens, int G, int prefix, int each) {
     return nullptr;
 }
 
+// Pages that a pool can give: never more than lie between its first counter and the list's end.
+const char *pools() {
+    const int counts[] = {INT_MIN, INT_MIN + 1, -5, -2, -1, 0, 1, 3, 4, 5, 100, 1 << 30, INT_MAX - 1, INT_MAX};
+    for (int taken : counts)
+        for (int there : counts)
+            for (int n_free : {0, 1, 4, 5, INT_MAX}) {
+                const int left = paged_pool_left(taken, there, n_free);
+                if (taken < 0 || there < 0) {
+                    if (left != -1) return "a counter below zero was taken";
+                    continue;
+                }
+                const long long end = std::min(there, n_free);
+                if (left != std::max(0ll, end - taken)) return "pages that are not there";
+            }
+    return nullptr;
+}
+
 }  // namespace
 
 int main() {
@@ -48,6 +67,7 @@ int main() {
     for (const auto &b : batches)
         if (const char *wrong = offsets(b.seqs, b.tokens, b.G, b.prefix, b.each))
             return std::printf("%d requests: %s\n", b.seqs, wrong), 1;
+    if (const char *wrong = pools()) return std::puts(wrong), 1;
     // more work than its units can count is refused in the same way
     const PagedShape big(1024, 1, 1 << 28, 152);
     const PagedPlan p = paged_plan(big, PagedCost{0, 0}, 128, 0, 5, true);

@@ -50,3 +50,23 @@ def test_attention_offsets_up_and_down(cfa, B, T, each, prefix):
         n = min(B, T)
         assert torch.equal(first[:n], again[:n]) and torch.all(out == 7.0)
         assert plan.status() == cfa.CFA_OK
+
+
+@pytest.mark.parametrize("pool", [[1, -1], [0, -(1 << 31)], [(1 << 31) - 1, -2], [-2, (1 << 31) - 1], [-3, -2]])
+@pytest.mark.parametrize("fresh", [[5, 0, 9], [1, 0, 0]])
+def test_tables_pool_counters_below_zero(cfa, pool, fresh):
+    """Refused whole, also where no page is wanted."""
+    lens, tables, n = [16, 4, 30], [[3, -7, -7], [2, -7, -7], [4, 5, -7]], 20
+    if fresh[0] == 1:
+        lens = [15, 4, 30]
+    t, new_lens, new_pool = ints(tables), ints([-9] * 3), ints([-9] * 2)
+    cu, pos, slots = ints([-9] * 4), ints([-9] * n), ints([-9] * n)
+    with cfa.Paged(3, 32, 8, 2, 64, 16) as plan:
+        plan.build_tables(ints(lens), ints(fresh), ints([9, 8, 7]), ints(pool), t, new_lens, new_pool, cu, pos, slots)
+        assert plan.status() == cfa.CFA_ERR_INVALID_ARG
+        assert t.tolist() == tables and new_lens.tolist() == lens and new_pool.tolist() == pool
+        assert cu.tolist() == [0] * 4 and pos.tolist() == [0] * n and slots.tolist() == [-1] * n
+        good = ints([0, 3])
+        plan.build_tables(ints(lens), ints(fresh), ints([9, 8, 7]), good, t, new_lens, good, cu, pos, slots)
+        assert plan.status() == cfa.CFA_OK
+        assert new_lens.tolist() == [a + b for a, b in zip(lens, fresh)] and cu.tolist()[-1] == sum(fresh)

@@ -6,14 +6,19 @@ import subprocess
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
+def cuda_include():
+    from out_proj_block_gb300 import build
+    return os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build.nvcc()))), "include")
+
+
 def run_check(tmp_path, name, *args, timeout=120):
     """Compiles tests/<name>.cpp with the host compiler and runs it."""
     exe = str(tmp_path / name)
     subprocess.run(["g++", "-std=c++17", "-O2", "-I", os.path.join(ROOT, "out_proj_block_gb300", "csrc"),
-                    *args, os.path.join(ROOT, "tests", name + ".cpp"), "-o", exe], check=True)
+                    "-I", cuda_include(), *args, os.path.join(ROOT, "tests", name + ".cpp"), "-o", exe], check=True)
     out = subprocess.run([exe], capture_output=True, text=True, timeout=timeout)
     assert out.returncode == 0 and out.stdout.strip() == "ok", out.stdout
 
 
-def test_refused_batches_have_no_rows(tmp_path):
+def test_refused_batches_and_pools(tmp_path):
     run_check(tmp_path, "paged_guards_check")
