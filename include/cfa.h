@@ -645,6 +645,8 @@ cfa_status cfa_paged_attention(cfa_paged *paged, int n_tokens, int n_seqs, const
  * The attention half of one layer: cfa_paged_append (q rotated into q_out,
  * which may be q), then cfa_paged_attention on q_out. Arguments as theirs; the
  * requests' rows and slots as cfa_paged_tables made them, once per step for all layers.
+ * Nothing that the call writes may overlap cu, lens, tables or prefix_table, and out and
+ * lse not positions or slots either.
  */
 cfa_status cfa_paged_layer(cfa_paged *paged, int n_tokens, int n_seqs, const void *q,
                            long long q_stride, const void *k, long long k_stride, const void *v,

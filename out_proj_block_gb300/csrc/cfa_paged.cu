@@ -174,6 +174,23 @@ cfa_status check_append(const cfa_paged *p, const AppendArgs &a) {
     return CFA_OK;
 }
 
+struct Span {
+    const void *at;
+    size_t n;
+};
+
+// Whether n bytes at `out` lie over the arrays that say what the batch is.
+bool over_batch(const cfa_paged *p, const AttnArgs &a, const void *out, size_t n) {
+    const Span in[] = {
+        {a.cu, 4u * (static_cast<size_t>(a.n_seqs) + 1)},
+        {a.lens, 4u * static_cast<size_t>(a.n_seqs)},
+        {a.tables, 4u * static_cast<size_t>(a.n_seqs) * a.width},
+        {a.prefix_table, a.prefix_len ? 4u * ((static_cast<size_t>(a.prefix_len) + p->ps - 1) / p->ps) : 0}};
+    for (const Span &b : in)
+        if (overlaps(out, n, b.at, b.n)) return true;
+    return false;
+}
+
 cfa_status check_attention(const cfa_paged *p, const AttnArgs &a) {
     if (a.n_tokens == 0) return CFA_OK;  // nothing to do
     if (!a.q || !a.cu || !a.tables || !a.lens || !a.kp || !a.vp || !a.out || a.n_tokens < 0 ||
@@ -190,17 +207,28 @@ cfa_status check_attention(const cfa_paged *p, const AttnArgs &a) {
     const size_t no = span(p, a.n_tokens, p->nh, static_cast<long long>(p->nh) * p->D);
     const size_t nl = a.lse ? 4u * static_cast<size_t>(a.n_tokens) * p->nh : 0;
     const size_t pages = 2u * static_cast<size_t>(cache_rows(p, a.n_pages)) * p->D;
-    const struct { const void *at; size_t n; } in[] = {
-        {a.q, span(p, a.n_tokens, p->nh, a.qs)},
-        {a.kp, pages},
-        {a.vp, pages},
-        {a.cu, 4u * (static_cast<size_t>(a.n_seqs) + 1)},
-        {a.lens, 4u * static_cast<size_t>(a.n_seqs)},
-        {a.tables, 4u * static_cast<size_t>(a.n_seqs) * a.width},
-        {a.prefix_table, a.prefix_len ? 4u * ((static_cast<size_t>(a.prefix_len) + p->ps - 1) / p->ps) : 0}};
-    for (const auto &b : in)
+    const Span q_and_cache[] = {{a.q, span(p, a.n_tokens, p->nh, a.qs)}, {a.kp, pages}, {a.vp, pages}};
+    for (const Span &b : q_and_cache)
         if (overlaps(a.out, no, b.at, b.n) || overlaps(a.lse, nl, b.at, b.n)) return CFA_ERR_INVALID_ARG;
+    if (over_batch(p, a, a.out, no) || over_batch(p, a, a.lse, nl)) return CFA_ERR_INVALID_ARG;
     return overlaps(a.out, no, a.lse, nl) ? CFA_ERR_INVALID_ARG : CFA_OK;
+}
+
+// Both calls' checks, and what neither sees: the append writes before the attention reads its
+// offsets and tables, and the next layer's call reads the positions and slots again.
+cfa_status check_layer(const cfa_paged *p, const AppendArgs &a, const AttnArgs &b) {
+    cfa_status st = check_append(p, a);
+    if (st == CFA_OK) st = check_attention(p, b);
+    if (st != CFA_OK || a.n_tokens == 0) return st;
+    const size_t no = span(p, a.n_tokens, p->nh, static_cast<long long>(p->nh) * p->D);
+    const size_t pages = 2u * static_cast<size_t>(cache_rows(p, a.n_pages)) * p->D;
+    if (over_batch(p, b, a.q_out, no) || over_batch(p, b, a.kp, pages) || over_batch(p, b, a.vp, pages))
+        return CFA_ERR_INVALID_ARG;
+    const size_t nl = b.lse ? 4u * static_cast<size_t>(a.n_tokens) * p->nh : 0;
+    const size_t ints = 4u * static_cast<size_t>(a.n_tokens);
+    for (const int *t : {a.positions, a.slots})
+        if (overlaps(b.out, no, t, ints) || overlaps(b.lse, nl, t, ints)) return CFA_ERR_INVALID_ARG;
+    return CFA_OK;
 }
 
 // Threads of an append block, which takes a token's rows of q, k and v: 64 up to 16 KB of
@@ -498,8 +526,7 @@ cfa_status cfa_paged_layer(cfa_paged *p, int n_tokens, int n_seqs, const void *q
     const AttnArgs b{n_tokens, n_seqs, q_out, static_cast<long long>(p->nh) * p->D, cu,
                      prefix_table, prefix_len, tables, table_width, lens, n_pages, k_pages, v_pages,
                      scale, out, lse};
-    cfa_status st = check_append(p, a);
-    if (st == CFA_OK) st = check_attention(p, b);
+    cfa_status st = check_layer(p, a, b);
     if (st != CFA_OK) return fail(st);
     OnDevice on(p->device);
     if (!on.ok()) return fail(CFA_ERR_CUDA);

@@ -1,0 +1,106 @@
+// Checks of the paged-cache entry points' host code with a stand-in for the CUDA runtime that
+// writes down what is called: which calls are refused, and in which order the device's work is
+// asked for. The argument names the check. Prints "ok" or what is wrong.
+#include "cfa_paged.cu"
+
+#include <cstdlib>
+#include <string>
+#include <vector>
+
+namespace {
+std::vector<std::string> calls;
+cudaError_t note(const char *what) {
+    calls.push_back(what);
+    return cudaSuccess;
+}
+char kernels[4];
+}  // namespace
+
+extern "C" {
+cudaError_t CUDARTAPI cudaGetDevice(int *d) { return *d = 0, cudaSuccess; }
+cudaError_t CUDARTAPI cudaSetDevice(int) { return cudaSuccess; }
+cudaError_t CUDARTAPI cudaGetLastError(void) { return cudaSuccess; }
+cudaError_t CUDARTAPI cudaDeviceGetAttribute(int *v, cudaDeviceAttr a, int) {
+    *v = a == cudaDevAttrComputeCapabilityMajor ? 10 : a == cudaDevAttrComputeCapabilityMinor ? 3 : 152;
+    return cudaSuccess;
+}
+cudaError_t CUDARTAPI cudaFuncSetAttribute(const void *, cudaFuncAttribute, int) { return cudaSuccess; }
+cudaError_t CUDARTAPI cudaMalloc(void **p, size_t) { return *p = std::malloc(64), cudaSuccess; }
+cudaError_t CUDARTAPI cudaFree(void *p) { return std::free(p), cudaSuccess; }
+cudaError_t CUDARTAPI cudaMemset(void *, int, size_t) { return note("set"); }
+cudaError_t CUDARTAPI cudaMemcpy(void *to, const void *, size_t n, cudaMemcpyKind) {
+    return std::memset(to, 0, n), note("copy");
+}
+cudaError_t CUDARTAPI cudaStreamSynchronize(cudaStream_t) { return note("wait"); }
+cudaError_t CUDARTAPI cudaDeviceSynchronize(void) { return note("wait"); }
+cudaError_t CUDARTAPI cudaLaunchKernelExC(const cudaLaunchConfig_t *, const void *, void **) { return note("launch"); }
+}
+
+namespace cfa {
+const void *paged_tables_kernel_ptr() { return kernels; }
+const void *paged_append_kernel_ptr(bool) { return kernels + 1; }
+const void *paged_attention_kernel_ptr(int) { return kernels + 2; }
+const void *paged_merge_kernel_ptr(int) { return kernels + 3; }
+int paged_attention_smem(int, int) { return 1 << 17; }
+cfa_status encode_bf16_2d_ex(CUtensorMap *, const void *, uint64_t, uint64_t, uint64_t, uint32_t, uint32_t, bool) {
+    return CFA_OK;
+}
+cfa_status set_last_error(cfa_status s) { return s; }
+}  // namespace cfa
+
+namespace {
+
+// A layer call whose arrays lie apart, at addresses that nobody reads.
+struct Layer {
+    static constexpr int T = 8, B = 3, H = 4, KV = 2, D = 64, PS = 16, PAGES = 4, W = 2, P = 20;
+    uintptr_t q = 0x1000000, k = 0x2000000, v = 0x3000000, pos = 0x4000000, slots = 0x5000000, cu = 0x6000000,
+              prefix = 0x7000000, tables = 0x8000000, lens = 0x9000000, kp = 0xa000000, vp = 0xb000000,
+              q_out = 0xc000000, out = 0xd000000, lse = 0xe000000;
+    static const int *ints(uintptr_t a) { return reinterpret_cast<const int *>(a); }
+    static void *at(uintptr_t a) { return reinterpret_cast<void *>(a); }
+    cfa_status operator()(cfa_paged *p, float scale = 0.f) const {
+        return cfa_paged_layer(p, T, B, at(q), H * D, at(k), KV * D, at(v), KV * D, ints(pos), ints(slots), ints(cu),
+                               ints(prefix), P, ints(tables), W, ints(lens), PAGES, at(kp), at(vp), scale, at(q_out),
+                               at(out), static_cast<float *>(at(lse)), nullptr);
+    }
+};
+
+// What the append writes must not be what the attention reads its offsets and tables from.
+const char *overlaps() {
+    cfa_paged *p = cfa_paged_create(Layer::B, Layer::T, Layer::H, Layer::KV, Layer::D, Layer::PS);
+    if (!p) return "no plan";
+    const uintptr_t pages = 2 * Layer::PAGES * Layer::KV * Layer::PS * Layer::D, turned = 2 * Layer::T * Layer::H * Layer::D;
+    calls.clear();
+    if (Layer{}(p) != CFA_OK || calls != std::vector<std::string>(3, "launch")) return "a good call was refused";
+    Layer in_place;
+    in_place.q_out = in_place.q;
+    if (in_place(p) != CFA_OK) return "rotation in place was refused";
+    calls.clear();
+    struct { uintptr_t Layer::*array; uintptr_t bytes; } read[] = {
+        {&Layer::cu, 4 * (Layer::B + 1)}, {&Layer::lens, 4 * Layer::B}, {&Layer::tables, 4 * Layer::B * Layer::W},
+        {&Layer::prefix, 4 * ((Layer::P + Layer::PS - 1) / Layer::PS)}, {&Layer::pos, 4 * Layer::T}, {&Layer::slots, 4 * Layer::T}};
+    struct { uintptr_t Layer::*array; uintptr_t bytes; } written[] = {
+        {&Layer::kp, pages}, {&Layer::vp, pages}, {&Layer::q_out, turned}, {&Layer::out, turned}, {&Layer::lse, 4 * Layer::T * Layer::H}};
+    for (const auto &r : read)
+        for (const auto &w : written)
+            for (const uintptr_t off : {uintptr_t(0), w.bytes - 4, w.bytes, uintptr_t(0) - r.bytes, uintptr_t(4) - r.bytes}) {
+                Layer c;
+                c.*r.array = c.*w.array + off;
+                const bool apart = off == w.bytes || off == uintptr_t(0) - r.bytes;
+                const cfa_status st = c(p);
+                if (apart ? st != CFA_OK : st != CFA_ERR_INVALID_ARG) return apart ? "arrays side by side were refused" : "an overlap was taken";
+                if (!apart && !calls.empty()) return "a refused call launched";
+                calls.clear();
+            }
+    cfa_paged_destroy(p);
+    return nullptr;
+}
+
+}  // namespace
+
+int main(int argc, char **argv) {
+    const std::string which = argc > 1 ? argv[1] : "";
+    const char *wrong = which == "overlaps" ? overlaps() : "which check?";
+    std::puts(wrong ? wrong : "ok");
+    return wrong != nullptr;
+}

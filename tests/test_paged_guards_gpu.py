@@ -70,3 +70,23 @@ def test_tables_pool_counters_below_zero(cfa, pool, fresh):
         plan.build_tables(ints(lens), ints(fresh), ints([9, 8, 7]), good, t, new_lens, good, cu, pos, slots)
         assert plan.status() == cfa.CFA_OK
         assert new_lens.tolist() == [a + b for a, b in zip(lens, fresh)] and cu.tolist()[-1] == sum(fresh)
+
+
+@pytest.mark.parametrize("over", ["cu", "lens", "tables", "prefix_table"])
+def test_layer_refuses_writing_over_what_it_reads(cfa, over):
+    T, nh, nkv, d, ps = 4, 4, 2, 64, 16
+    q, k, v = normal(1, T, nh, d), normal(2, T, nkv, d), normal(3, T, nkv, d)
+    kp, vp, q_out, out = normal(4, 8, nkv, ps, d), normal(5, 8, nkv, ps, d), normal(6, T, nh, d), normal(7, T, nh, d)
+    a = dict(q=q, k=k, v=v, positions=ints([5] * T), slots=ints([16, 17, 32, 48]), cu=ints([0, 2, 3, 4]),
+             lens=ints([2, 1, 1]), tables=ints([[1], [2], [3]]), k_pages=kp, v_pages=vp, q_out=q_out, out=out,
+             prefix_table=ints([5]), prefix_len=9)
+    with cfa.Paged(3, T, nh, nkv, d, ps) as plan:
+        plan.layer(**a)
+        assert plan.status() == cfa.CFA_OK
+        before = [x.clone() for x in (kp, vp, q_out, out)]
+        for t in (kp, vp, q_out, out):
+            there = t.view(-1).view(torch.int32)[8:8 + a[over].numel()].view(a[over].shape)
+            with pytest.raises(cfa.CfaError):
+                plan.layer(**{**a, over: there})
+        assert all(torch.equal(x, y) for x, y in zip(before, (kp, vp, q_out, out)))
+        assert plan.status() == cfa.CFA_OK

@@ -12,13 +12,17 @@ def cuda_include():
 
 
 def run_check(tmp_path, name, *args, timeout=120):
-    """Compiles tests/<name>.cpp with the host compiler and runs it."""
+    """Compiles tests/<name>.cpp with the host compiler and runs it with these arguments."""
     exe = str(tmp_path / name)
     subprocess.run(["g++", "-std=c++17", "-O2", "-I", os.path.join(ROOT, "out_proj_block_gb300", "csrc"),
-                    "-I", cuda_include(), *args, os.path.join(ROOT, "tests", name + ".cpp"), "-o", exe], check=True)
-    out = subprocess.run([exe], capture_output=True, text=True, timeout=timeout)
+                    "-I", cuda_include(), "-I", os.path.join(ROOT, "include"), os.path.join(ROOT, "tests", name + ".cpp"), "-o", exe], check=True)
+    out = subprocess.run([exe, *args], capture_output=True, text=True, timeout=timeout)
     assert out.returncode == 0 and out.stdout.strip() == "ok", out.stdout
 
 
 def test_refused_batches_and_pools(tmp_path):
     run_check(tmp_path, "paged_guards_check")
+
+
+def test_layer_refuses_writing_over_what_it_reads(tmp_path):
+    run_check(tmp_path, "paged_calls_check", "overlaps")
