@@ -102,6 +102,12 @@ void paged_free(cfa_paged *p) {
     p->rec_ml = nullptr;
 }
 
+// Clears words of a plan. A memset may run after the call that asks for it has returned, and
+// streams that do not wait for the legacy one would launch on what the words held before.
+bool clear_words(unsigned *words, int n) {
+    return cudaMemset(words, 0, sizeof(unsigned) * n) == cudaSuccess && cudaStreamSynchronize(nullptr) == cudaSuccess;
+}
+
 // Rows of a cache of n_pages pages, or -1 where they pass the kernels' 32-bit
 // row index.
 long long cache_rows(const cfa_paged *p, int n_pages) {
@@ -369,7 +375,7 @@ cfa_paged *cfa_paged_create(int max_seqs, int max_tokens, int n_heads, int n_kv_
         cudaFuncSetAttribute(cfa::paged_attention_kernel_ptr(head_dim), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              cfa::paged_attention_smem(head_dim, cfa::kPagedMaxSeqs)) != cudaSuccess ||
         cudaMalloc(&p->words, 2 * sizeof(unsigned)) != cudaSuccess ||
-        cudaMemset(p->words, 0, 2 * sizeof(unsigned)) != cudaSuccess ||
+        !clear_words(p->words, 2) ||
         cudaMalloc(&p->plan_ws, sizeof(int) * plan_ints) != cudaSuccess ||
         cudaMalloc(&p->rec_o, sizeof(float) * static_cast<size_t>(p->rec_rows) * head_dim) != cudaSuccess ||
         cudaMalloc(&p->rec_ml, sizeof(float2) * static_cast<size_t>(p->rec_rows)) != cudaSuccess) {
@@ -541,7 +547,7 @@ cfa_status cfa_paged_status(cfa_paged *p) {
     unsigned v = 0;
     if (!on.ok() || cudaDeviceSynchronize() != cudaSuccess ||
         cudaMemcpy(&v, p->words, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess ||
-        cudaMemset(p->words, 0, sizeof v) != cudaSuccess) {
+        !clear_words(p->words, 1)) {
         cudaGetLastError();
         return fail(CFA_ERR_CUDA);
     }

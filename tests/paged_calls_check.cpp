@@ -96,11 +96,28 @@ const char *overlaps() {
     return nullptr;
 }
 
+// A memset runs in the legacy stream after the call that asks for it has returned, and a kernel
+// on a stream that does not wait for that one may come first: the plan's words are cleared
+// before create and status return.
+const char *order() {
+    using Calls = std::vector<std::string>;
+    calls.clear();
+    cfa_paged *p = cfa_paged_create(Layer::B, Layer::T, Layer::H, Layer::KV, Layer::D, Layer::PS);
+    if (!p) return "no plan";
+    if (calls != Calls{"set", "wait"}) return "create leaves its words to be cleared later";
+    calls.clear();
+    if (cfa_paged_status(p) != CFA_OK) return "status";
+    if (calls != Calls{"wait", "copy", "set", "wait"}) return "status leaves its word to be cleared later";
+    calls.clear();
+    cfa_paged_destroy(p);
+    return nullptr;
+}
+
 }  // namespace
 
 int main(int argc, char **argv) {
     const std::string which = argc > 1 ? argv[1] : "";
-    const char *wrong = which == "overlaps" ? overlaps() : "which check?";
+    const char *wrong = which == "overlaps" ? overlaps() : which == "order" ? order() : "which check?";
     std::puts(wrong ? wrong : "ok");
     return wrong != nullptr;
 }

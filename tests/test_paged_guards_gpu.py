@@ -90,3 +90,24 @@ def test_layer_refuses_writing_over_what_it_reads(cfa, over):
                 plan.layer(**{**a, over: there})
         assert all(torch.equal(x, y) for x, y in zip(before, (kp, vp, q_out, out)))
         assert plan.status() == cfa.CFA_OK
+
+
+def test_a_new_plan_behind_a_busy_default_stream(cfa):
+    """The plan's words are zero when create returns, and stay what later kernels make them, for
+    streams that do not wait for the default one too."""
+    side = torch.cuda.Stream()
+    lens, fresh, n = ints([0] * 5), ints([300] * 5), 2048
+    tables = torch.full((5, 20), -1, dtype=torch.int32, device="cuda")
+    free, pool, cu = ints(range(100)), ints([0, 100]), ints([0] * 6)
+    pos, slots = ints([0] * n), ints([0] * n)
+    torch.cuda.synchronize()
+    for turn in range(4):
+        torch.cuda._sleep(200_000_000)
+        with cfa.Paged(5, n, 8, 2, 64, 16) as plan:
+            with torch.cuda.stream(side):
+                lens.zero_()
+                pool.copy_(ints([0, 100] if turn % 2 else [0, 90]))
+                plan.build_tables(lens, fresh, free, pool, tables, lens, pool, cu, pos, slots)
+                side.synchronize()
+                assert lens.tolist() == ([300] * 5 if turn % 2 else [0] * 5)
+                assert plan.status() == (cfa.CFA_OK if turn % 2 else cfa.CFA_ERR_NO_PAGES)

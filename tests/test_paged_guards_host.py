@@ -26,3 +26,7 @@ def test_refused_batches_and_pools(tmp_path):
 
 def test_layer_refuses_writing_over_what_it_reads(tmp_path):
     run_check(tmp_path, "paged_calls_check", "overlaps")
+
+
+def test_words_are_cleared_before_the_call_returns(tmp_path):
+    run_check(tmp_path, "paged_calls_check", "order")
