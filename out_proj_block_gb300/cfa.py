@@ -950,8 +950,8 @@ class Paged:
             raise ValueError("lens has one dimension, tables two")
         if prefix_len < 0:
             raise ValueError("prefix_len must not be negative")
-        if scale is not None and not scale > 0.0:
-            raise ValueError("scale must be positive")
+        if scale is not None and not ctypes.c_float(scale).value > 0.0:
+            raise ValueError("scale must be positive, in 32 bits too")
         B, width = tables.shape
         shape = (T, self.n_heads, self.head_dim)
         if not (lens.dtype is cu.dtype is tables.dtype is _I32 and out.dtype is _BF16

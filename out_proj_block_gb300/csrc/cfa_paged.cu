@@ -180,6 +180,12 @@ cfa_status check_append(const cfa_paged *p, const AppendArgs &a) {
     return CFA_OK;
 }
 
+// The scale (0: the default one) with the exponential's change to base 2.
+float scale_log2(const cfa_paged *p, float scale) {
+    const double s = scale > 0.0f ? scale : 1.0 / std::sqrt(static_cast<double>(p->D));
+    return static_cast<float>(s * 1.4426950408889634);
+}
+
 struct Span {
     const void *at;
     size_t n;
@@ -204,7 +210,8 @@ cfa_status check_attention(const cfa_paged *p, const AttnArgs &a) {
         cache_rows(p, a.n_pages) < 0 || !stride_ok(p, p->nh, a.qs) || a.prefix_len < 0 ||
         a.prefix_len > (1 << 30) || (a.prefix_len > 0 && !a.prefix_table) || a.width < 1 ||
         a.width > cfa::kPagedMaxTableWidth ||
-        static_cast<long long>(a.width) * p->ps > (1 << 30) || !(a.scale >= 0.0f) || !std::isfinite(a.scale))
+        static_cast<long long>(a.width) * p->ps > (1 << 30) || !(a.scale >= 0.0f) ||
+        !std::isfinite(scale_log2(p, a.scale)))
         return CFA_ERR_INVALID_ARG;
     if (!aligned(a.q, 16) || !aligned(a.kp, 16) || !aligned(a.vp, 16) || !aligned(a.out, 16) ||
         !aligned(a.cu, 4) || !aligned(a.prefix_table, 4) || !aligned(a.tables, 4) ||
@@ -295,8 +302,7 @@ cfa_status launch_attention(cfa_paged *p, const AttnArgs &a, cudaStream_t stream
     kp.n_pages = a.n_pages;
     kp.width = a.width;
     kp.prefix_len = a.prefix_len;
-    const double scale = a.scale > 0.0f ? a.scale : 1.0 / std::sqrt(static_cast<double>(p->D));
-    kp.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    kp.scale_log2 = scale_log2(p, a.scale);
     kp.plan_ws = p->plan_ws;
     kp.rec_o = p->rec_o;
     kp.rec_ml = p->rec_ml;

@@ -113,11 +113,23 @@ const char *order() {
     return nullptr;
 }
 
+// A scale counts in 32 bits and times log2 e: neither may become infinite on the way.
+const char *scales() {
+    cfa_paged *p = cfa_paged_create(Layer::B, Layer::T, Layer::H, Layer::KV, Layer::D, Layer::PS);
+    if (!p) return "no plan";
+    for (const float good : {0.f, 1e-45f, 1e-38f, 0.125f, 1e10f, 2.3e38f})
+        if (Layer{}(p, good) != CFA_OK) return "a scale was refused";
+    for (const float bad : {-1.f, 2.4e38f, 3.4e38f, HUGE_VALF, NAN})
+        if (Layer{}(p, bad) != CFA_ERR_INVALID_ARG) return "a scale was taken";
+    cfa_paged_destroy(p);
+    return nullptr;
+}
+
 }  // namespace
 
 int main(int argc, char **argv) {
     const std::string which = argc > 1 ? argv[1] : "";
-    const char *wrong = which == "overlaps" ? overlaps() : which == "order" ? order() : "which check?";
+    const char *wrong = which == "overlaps" ? overlaps() : which == "order" ? order() : which == "scales" ? scales() : "which check?";
     std::puts(wrong ? wrong : "ok");
     return wrong != nullptr;
 }

@@ -111,3 +111,22 @@ def test_a_new_plan_behind_a_busy_default_stream(cfa):
                 side.synchronize()
                 assert lens.tolist() == ([300] * 5 if turn % 2 else [0] * 5)
                 assert plan.status() == (cfa.CFA_OK if turn % 2 else cfa.CFA_ERR_NO_PAGES)
+
+
+def test_scales_that_32_bits_do_not_hold(cfa):
+    """A scale that rounds to 0 would be taken as the default, one near the largest number
+    becomes infinite when it is turned to base 2. The smallest one makes the mean of the values."""
+    nh, d, n = 2, 64, 40
+    q, kp, vp = normal(1, 1, nh, d), normal(2, 1, nh, 64, d), normal(3, 1, nh, 64, d)
+    out, lse = torch.empty_like(q), torch.empty(1, nh, device="cuda")
+    a = dict(q=q, cu=ints([0, 1]), lens=ints([n]), tables=ints([[0]]), k_pages=kp, v_pages=vp, out=out, lse=lse)
+    with cfa.Paged(1, 1, nh, nh, d, 64) as plan:
+        for scale, error in ((1e-50, ValueError), (5e-324, ValueError), (3e38, cfa.CfaError), (1e39, cfa.CfaError)):
+            with pytest.raises(error):
+                plan.attend(**a, scale=scale)
+        plan.attend(**a, scale=1e-45)
+        assert plan.status() == cfa.CFA_OK
+    want = vp[0, :, :n].double().mean(1)
+    # 40 weights of one, exact in bf16: only the result is rounded
+    assert torch.all((out[0].double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-6)
+    assert torch.all((lse.double() - torch.log(torch.tensor(float(n)))).abs() <= 1e-5)

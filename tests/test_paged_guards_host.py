@@ -30,3 +30,7 @@ def test_layer_refuses_writing_over_what_it_reads(tmp_path):
 
 def test_words_are_cleared_before_the_call_returns(tmp_path):
     run_check(tmp_path, "paged_calls_check", "order")
+
+
+def test_scales_that_pass_32_bits(tmp_path):
+    run_check(tmp_path, "paged_calls_check", "scales")
