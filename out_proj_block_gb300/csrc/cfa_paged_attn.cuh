@@ -512,8 +512,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             bool more = true;
             int u = u0;
             PagedCut cut{};  // the tile that the run's end cuts, for the merge
+            PagedPiece x;
             for (uint32_t k = 0; more; ++k) {
-                PagedPiece x;
                 more = paged_next(shape, plan, req, B, u, u1, x);
                 if (!more) x.b0 = x.b1 = x.rows = 0;
                 else if (x.req >= 0 && paged_alone(shape, x.r.n) && x.b0 == 0 && x.b1 < x.blocks)

@@ -113,8 +113,8 @@ struct PagedPiece {
     int blocks;         // the item's blocks
     int own_limit;      // own keys that the last row sees
     int b0, b1;         // the piece: blocks [b0, b1) of the item
-    int first_unit;     // the item's first unit
-    int cost, units;    // units of a block, and of the item
+    int first_unit = 0; // the item's first unit
+    int cost, units = 0;  // units of a block, and of the item
     int final;          // the piece writes its rows' results
     long long rec;      // else its record (paged_record)
     int rec_row, rec_stride;
@@ -151,6 +151,13 @@ CFA_HD int paged_alone_blocks(const PagedShape &s, const PagedRequest &r, int ti
     return paged_max(1, paged_cdiv(s.prefix_len, kPagedKeys) +
                             paged_cdiv(paged_visible(r, last / s.by_G), kPagedKeys));
 }
+// How many tiles from `tile` on, which has so many blocks, are full and have as many (itself
+// in any case): those of the tokens that see no more keys than these blocks hold. A request
+// has up to 2^19 tiles, but only some n / 128 numbers of blocks.
+CFA_HD int paged_alike(const PagedShape &s, const PagedRequest &r, int tile, int blocks) {
+    const int keys = (blocks - paged_cdiv(s.prefix_len, kPagedKeys)) * kPagedKeys;
+    return paged_max(1, paged_min(r.n, keys - r.len + r.n) * s.G / kPagedTile - tile);
+}
 // What a request's own items cost: units of their blocks, and items.
 struct PagedCost {
     long long blocks, items;
@@ -166,9 +173,12 @@ CFA_HD PagedCost paged_request_cost(const PagedShape &s, const PagedRequest &r) 
                          items * paged_item_cost(paged_min(all, tile))};
     }
     PagedCost c{0, 0};
-    CFA_ROLLED for (int row = 0, t = 0; row < all; row += kPagedTile, ++t) {
-        c.blocks += paged_alone_blocks(s, r, t) * paged_cost(all - row);
-        c.items += paged_item_cost(all - row);
+    int n = 1;
+    CFA_ROLLED for (int row = 0, t = 0; row < all; row += n * kPagedTile, t += n) {
+        const int blocks = paged_alone_blocks(s, r, t);
+        n = paged_alike(s, r, t, blocks);
+        c.blocks += static_cast<long long>(n) * blocks * paged_cost(all - row);
+        c.items += static_cast<long long>(n) * paged_item_cost(all - row);
     }
     return PagedCost{c.blocks * s.nkv, c.items * s.nkv};
 }
@@ -226,7 +236,7 @@ CFA_HD int paged_find(int B, int x, At at) {
     return lo;
 }
 
-// The item that holds unit u, of the requests e[0..B].
+// The item that holds unit u, of the requests e[0..B]; x: the item found before, if any.
 CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const PagedEntry *e, int B, int u, PagedPiece &x) {
     int rem;  // units of the item before u
     if (u < p.prefix_units) {
@@ -249,8 +259,8 @@ CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const PagedEntry
         const int per_head = (e[x.req + 1].unit - e[x.req].unit) / s.by_nkv;
         x.h = mine / per_head;
         rem = mine - x.h * per_head;
-        x.row0 = 0;
         if (!paged_alone(s, x.r.n)) {
+            x.row0 = 0;
             const int all = x.r.n * s.G, tile = paged_own_tile(all);
             x.prefix_blocks = 0;
             x.blocks = paged_cdiv(x.r.len, kPagedKeys);
@@ -264,14 +274,24 @@ CFA_HD void paged_item(const PagedShape &s, const PagedPlan &p, const PagedEntry
         } else {
             const int all = x.r.n * s.G;
             int t = 0;
-            x.blocks = paged_alone_blocks(s, x.r, 0);
-            CFA_ROLLED for (;;) {
-                const int each = paged_item_units(p, all - x.row0, paged_cost(all - x.row0), x.blocks);
-                if (rem < each) break;
-                rem -= each;
-                x.row0 += kPagedTile;
-                x.blocks = paged_alone_blocks(s, x.r, ++t);
+            if (rem > 0 && u == x.first_unit + x.units) {  // the tile behind the last one
+                t = x.row0 / kPagedTile + 1;
+                rem = 0;
             }
+            CFA_ROLLED for (;;) {
+                x.blocks = paged_alone_blocks(s, x.r, t);
+                const int each = paged_item_units(p, all - t * kPagedTile, paged_cost(all - t * kPagedTile), x.blocks);
+                const int n = paged_alike(s, x.r, t, x.blocks);
+                if (rem < n * each) {
+                    const int at = n > 1 ? rem / each : 0;
+                    t += at;
+                    rem -= at * each;
+                    break;
+                }
+                rem -= n * each;
+                t += n;
+            }
+            x.row0 = t * kPagedTile;
             x.rows = paged_min(kPagedTile, all - x.row0);
             x.prefix_blocks = p.prefix_blocks;
             x.own_limit = paged_visible(x.r, (x.row0 + x.rows - 1) / s.by_G);

@@ -130,3 +130,30 @@ def test_scales_that_32_bits_do_not_hold(cfa):
     # 40 weights of one, exact in bf16: only the result is rounded
     assert torch.all((out[0].double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-6)
     assert torch.all((lse.double() - torch.log(torch.tensor(float(n)))).abs() <= 1e-5)
+
+
+@pytest.mark.parametrize("n,own,prefix", [(32768, 40, 9), (16384, 16384, 0)])
+def test_attention_of_some_hundred_thousand_tiles(cfa, n, own, prefix):
+    """1024 query heads on one key head: tiles of a quarter of a token. A few rows against 64
+    bits (as in the other attention tests: the weights and the result rounded to bf16)."""
+    nh, d, ps = 1024, 64, 64
+    pages = 1 + -(-own // ps)
+    kp, vp = normal(1, pages, 1, ps, d), normal(2, pages, 1, ps, d)
+    q = torch.empty(n, nh, d, dtype=torch.bfloat16, device="cuda")
+    q.copy_(normal(3, 64, nh, d).repeat(n // 64, 1, 1))
+    out, lse = torch.full_like(q, 7.0), torch.empty(n, nh, device="cuda")
+    kw = dict(prefix_table=ints([0]), prefix_len=prefix) if prefix else {}
+    with cfa.Paged(1, n, nh, 1, d, ps) as plan:
+        plan.attend(q, ints([0, n]), ints([own]), ints([list(range(1, pages))]), kp, vp, out, lse=lse, **kw)
+        assert plan.status() == cfa.CFA_OK
+    for i in (0, 1, n // 3, n - own, n - 1):
+        see = max(0, own - n + i + 1)
+        k, v = (torch.cat((x[0, 0, :prefix], x[1:, 0].reshape(-1, d)[:see])).double() for x in (kp, vp))
+        for h in (0, 255, 256, 1023):
+            s = k @ q[i, h].double() / 8.0
+            w = torch.softmax(s, 0)
+            want, size = w @ v, w @ v.abs()
+            tol = (1 + 2.0 ** -4) * 2.0 ** -8 * (want.abs() + size) + 1e-6
+            assert torch.all((out[i, h].double() - want).abs() <= tol)
+            assert abs(float(lse[i, h]) - float(torch.logsumexp(s, 0))) <= 1e-4
+    assert torch.all(torch.isfinite(out.view(-1)[:: 997]))

@@ -34,3 +34,7 @@ def test_words_are_cleared_before_the_call_returns(tmp_path):
 
 def test_scales_that_pass_32_bits(tmp_path):
     run_check(tmp_path, "paged_calls_check", "scales")
+
+
+def test_walk_through_long_requests(tmp_path):
+    run_check(tmp_path, "paged_walk_check")
