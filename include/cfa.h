@@ -529,9 +529,9 @@ typedef struct cfa_paged cfa_paged; /* opaque */
  * 1024, page_size 16, 32 or a multiple of 64 up to 1<<22
  * (CFA_ERR_UNSUPPORTED otherwise; CFA_ERR_INVALID_ARG for non-positive values
  * or n_heads not a multiple of n_kv_heads). No rotation until
- * cfa_paged_set_rope. The workspace holds 2 n_kv_heads min(max_tokens G,
- * 128 max_seqs) + 512 SMs rows of head_dim + 2 floats (G = n_heads /
- * n_kv_heads). NULL on failure; cfa_last_error() says why.
+ * cfa_paged_set_rope. With R = min(max_tokens G, 128 max_seqs) and G = n_heads /
+ * n_kv_heads the workspace holds 2 n_kv_heads R + 512 SMs rows of head_dim + 2
+ * floats, and the plan of a call 64 + 32 (SMs + R) bytes. NULL on failure; cfa_last_error() says why.
  */
 cfa_paged *cfa_paged_create(int max_seqs, int max_tokens, int n_heads, int n_kv_heads,
                             int head_dim, int page_size);
@@ -660,8 +660,8 @@ cfa_status cfa_paged_layer(cfa_paged *paged, int n_tokens, int n_seqs, const voi
  * cfa_plan_status; CFA_ERR_NO_PAGES after a refused cfa_paged_tables). */
 cfa_status cfa_paged_status(cfa_paged *paged);
 
-/* One-line JSON description (shape, rotation, SMs used, shared memory and
- * workspace bytes). */
+/* One-line JSON description (shape, rotation, SMs used, shared memory; on the
+ * device, workspace_bytes of records and plan_bytes of a call's plan). */
 cfa_status cfa_paged_describe(const cfa_paged *paged, char *buf, int len);
 
 #ifdef __cplusplus

@@ -38,6 +38,7 @@ struct cfa_paged {
     float *rec_o = nullptr;     // records of the attention's pieces
     float2 *rec_ml = nullptr;
     long long rec_rows = 0;
+    size_t plan_ints = 0;
 };
 
 namespace {
@@ -375,14 +376,14 @@ cfa_paged *cfa_paged_create(int max_seqs, int max_tokens, int n_heads, int n_kv_
     const long long shared = std::min(static_cast<long long>(max_tokens) * G,
                                       static_cast<long long>(max_seqs) * cfa::kPagedAloneRows);
     p->rec_rows = cfa::paged_record_rows(cfa::PagedShape(G, n_kv_heads, 0, p->num_sms), shared);
-    const size_t plan_ints = cfa::kPagedPlanInts + 8 * (static_cast<size_t>(p->num_sms) + static_cast<size_t>(shared));
+    p->plan_ints = cfa::kPagedPlanInts + 8 * (static_cast<size_t>(p->num_sms) + static_cast<size_t>(shared));
     if (cudaFuncSetAttribute(cfa::paged_tables_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(sizeof(int)) * (3 * cfa::kPagedMaxSeqs + 2)) != cudaSuccess ||
         cudaFuncSetAttribute(cfa::paged_attention_kernel_ptr(head_dim), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              cfa::paged_attention_smem(head_dim, cfa::kPagedMaxSeqs)) != cudaSuccess ||
         cudaMalloc(&p->words, 2 * sizeof(unsigned)) != cudaSuccess ||
         !clear_words(p->words, 2) ||
-        cudaMalloc(&p->plan_ws, sizeof(int) * plan_ints) != cudaSuccess ||
+        cudaMalloc(&p->plan_ws, sizeof(int) * p->plan_ints) != cudaSuccess ||
         cudaMalloc(&p->rec_o, sizeof(float) * static_cast<size_t>(p->rec_rows) * head_dim) != cudaSuccess ||
         cudaMalloc(&p->rec_ml, sizeof(float2) * static_cast<size_t>(p->rec_rows)) != cudaSuccess) {
         cudaGetLastError();
@@ -568,10 +569,11 @@ cfa_status cfa_paged_describe(const cfa_paged *p, char *buf, int len) {
     std::snprintf(buf, static_cast<size_t>(len),
                   "{\"max_seqs\": %d, \"max_tokens\": %d, \"n_heads\": %d, \"n_kv_heads\": %d, "
                   "\"head_dim\": %d, \"page_size\": %d, \"rotary_dim\": %d, \"interleaved\": %d, "
-                  "\"scaling\": %d, \"num_sms\": %d, \"smem_bytes\": %d, \"workspace_bytes\": %lld}",
+                  "\"scaling\": %d, \"num_sms\": %d, \"smem_bytes\": %d, \"workspace_bytes\": %lld, "
+                  "\"plan_bytes\": %lld}",
                   p->max_seqs, p->max_tokens, p->nh, p->nkv, p->D, p->ps, p->rd, p->interleaved,
                   p->scaling, p->num_sms, cfa::paged_attention_smem(p->D, p->max_seqs),
-                  p->rec_rows * (4ll * p->D + 8));
+                  p->rec_rows * (4ll * p->D + 8), static_cast<long long>(sizeof(int) * p->plan_ints));
     return CFA_OK;
 }
 

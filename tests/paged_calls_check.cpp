@@ -13,6 +13,7 @@ cudaError_t note(const char *what) {
     calls.push_back(what);
     return cudaSuccess;
 }
+size_t allocated;
 char kernels[4];
 }  // namespace
 
@@ -25,7 +26,7 @@ cudaError_t CUDARTAPI cudaDeviceGetAttribute(int *v, cudaDeviceAttr a, int) {
     return cudaSuccess;
 }
 cudaError_t CUDARTAPI cudaFuncSetAttribute(const void *, cudaFuncAttribute, int) { return cudaSuccess; }
-cudaError_t CUDARTAPI cudaMalloc(void **p, size_t) { return *p = std::malloc(64), cudaSuccess; }
+cudaError_t CUDARTAPI cudaMalloc(void **p, size_t n) { return allocated += n, *p = std::malloc(64), cudaSuccess; }
 cudaError_t CUDARTAPI cudaFree(void *p) { return std::free(p), cudaSuccess; }
 cudaError_t CUDARTAPI cudaMemset(void *, int, size_t) { return note("set"); }
 cudaError_t CUDARTAPI cudaMemcpy(void *to, const void *, size_t n, cudaMemcpyKind) {
@@ -125,11 +126,32 @@ const char *scales() {
     return nullptr;
 }
 
+// describe tells of every byte that a plan keeps on the device (and two words).
+const char *bytes() {
+    const struct { int seqs, tokens, heads, kv, d; } plans[] = {
+        {1, 1, 1, 1, 64}, {2, 8, 4, 2, 64}, {64, 512, 32, 8, 128}, {1024, 1 << 17, 32, 32, 128}, {1024, 1 << 17, 1024, 1, 64}};
+    for (const auto &s : plans) {
+        allocated = 0;
+        cfa_paged *p = cfa_paged_create(s.seqs, s.tokens, s.heads, s.kv, s.d, 64);
+        char text[1024];
+        if (!p || cfa_paged_describe(p, text, sizeof text) != CFA_OK) return "no plan";
+        long long told = 0;
+        for (const char *name : {"\"workspace_bytes\": ", "\"plan_bytes\": "}) {
+            const char *at = std::strstr(text, name);
+            if (!at) return "a field is missing";
+            told += std::atoll(at + std::strlen(name));
+        }
+        if (told + 8 != static_cast<long long>(allocated)) return "bytes that describe leaves out";
+        cfa_paged_destroy(p);
+    }
+    return nullptr;
+}
+
 }  // namespace
 
 int main(int argc, char **argv) {
     const std::string which = argc > 1 ? argv[1] : "";
-    const char *wrong = which == "overlaps" ? overlaps() : which == "order" ? order() : which == "scales" ? scales() : "which check?";
+    const char *wrong = which == "overlaps" ? overlaps() : which == "order" ? order() : which == "scales" ? scales() : which == "bytes" ? bytes() : "which check?";
     std::puts(wrong ? wrong : "ok");
     return wrong != nullptr;
 }

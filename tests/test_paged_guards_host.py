@@ -38,3 +38,7 @@ def test_scales_that_pass_32_bits(tmp_path):
 
 def test_walk_through_long_requests(tmp_path):
     run_check(tmp_path, "paged_walk_check")
+
+
+def test_describe_counts_every_byte(tmp_path):
+    run_check(tmp_path, "paged_calls_check", "bytes")
