@@ -531,7 +531,8 @@ typedef struct cfa_paged cfa_paged; /* opaque */
  * or n_heads not a multiple of n_kv_heads). No rotation until
  * cfa_paged_set_rope. With R = min(max_tokens G, 128 max_seqs) and G = n_heads /
  * n_kv_heads the workspace holds 2 n_kv_heads R + 512 SMs rows of head_dim + 2
- * floats, and the plan of a call 64 + 32 (SMs + R) bytes. NULL on failure; cfa_last_error() says why.
+ * floats, and the plan of a call 64 + 32 (SMs + R) bytes. NULL on failure;
+ * cfa_last_error() says why.
  */
 cfa_paged *cfa_paged_create(int max_seqs, int max_tokens, int n_heads, int n_kv_heads,
                             int head_dim, int page_size);

@@ -29,7 +29,6 @@ struct cfa_paged {
     int device = -1, num_sms = 0;
     // rotation
     int rd = 0, interleaved = 0, scaling = CFA_ROPE_PLAIN;
-    double theta = 0.0;
     float magnitude = 1.0f;
     unsigned long long turns[64] = {};
     // workspace
@@ -431,7 +430,6 @@ cfa_status cfa_paged_set_rope(cfa_paged *p, double theta, int rotary_dim, int in
         // f <= 1, so below 1/6 of a turn: the product stays far below 2^64
         p->turns[i] = static_cast<unsigned long long>(std::ldexp(f / two_pi, 64));
     }
-    p->theta = theta;
     p->rd = rotary_dim;
     p->interleaved = interleaved ? 1 : 0;
     p->scaling = scaling;

@@ -56,6 +56,7 @@
 
 #include "cfa_device.cuh"
 #include "cfa_paged.h"
+#include "cfa_paged_device.cuh"
 #include "cfa_paged_split.h"
 #include "cfa_tile.cuh"
 
@@ -150,13 +151,6 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-// Two fp32 to packed bf16, rounded to nearest even, in one conversion.
-__device__ __forceinline__ uint32_t pack2_bf16_cvt(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // True in one lane of the warp, the same one every time. A warp whose lanes all run an
 // issue loop keeps its operands in uniform registers; a loop inside "if (lane == 0)" moves
 // them there for every instruction (measured: 100 clocks a product, 250 a copy).

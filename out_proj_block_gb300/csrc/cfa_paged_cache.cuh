@@ -5,6 +5,7 @@
 
 #include "cfa_device.cuh"
 #include "cfa_paged.h"
+#include "cfa_paged_device.cuh"
 #include "cfa_tile.cuh"
 
 namespace cfa {
@@ -153,12 +154,6 @@ paged_tables_kernel(const TablesParams p) {
 // bytes took 24 us at 4096 tokens of 32/8 heads x 128 (100.7 MB). So does that some blocks of
 // an SM load while others store, which small blocks do best: 256 threads took 21.3 us there,
 // 128 18.9, 64 17.3 (5.8 TB/s). The bytes bound it at many tokens, the launch at few.
-__device__ __forceinline__ uint32_t pack2_bf16_one(float lo, float hi) {  // one conversion, to nearest even
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 template <bool kInterleaved>
 __global__ void __launch_bounds__(kAppendThreads, 8)
 paged_append_kernel(const __grid_constant__ AppendParams p) {
@@ -238,11 +233,11 @@ paged_append_kernel(const __grid_constant__ AppendParams p) {
                             z[e] = z[e] * r[e].x + x[e] * r[e].y;
                         }
                         *reinterpret_cast<uint4 *>(dst + half) =
-                            make_uint4(pack2_bf16_one(z[0], z[1]), pack2_bf16_one(z[2], z[3]),
-                                       pack2_bf16_one(z[4], z[5]), pack2_bf16_one(z[6], z[7]));
+                            make_uint4(pack2_bf16_cvt(z[0], z[1]), pack2_bf16_cvt(z[2], z[3]),
+                                       pack2_bf16_cvt(z[4], z[5]), pack2_bf16_cvt(z[6], z[7]));
                     }
-                    a[j] = make_uint4(pack2_bf16_one(y[0], y[1]), pack2_bf16_one(y[2], y[3]),
-                                      pack2_bf16_one(y[4], y[5]), pack2_bf16_one(y[6], y[7]));
+                    a[j] = make_uint4(pack2_bf16_cvt(y[0], y[1]), pack2_bf16_cvt(y[2], y[3]),
+                                      pack2_bf16_cvt(y[4], y[5]), pack2_bf16_cvt(y[6], y[7]));
                 }
                 *reinterpret_cast<uint4 *>(dst) = a[j];
             }
