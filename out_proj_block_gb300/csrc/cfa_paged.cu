@@ -307,9 +307,12 @@ cfa_status launch_attention(cfa_paged *p, const AttnArgs &a, cudaStream_t stream
     kp.rec_o = p->rec_o;
     kp.rec_ml = p->rec_ml;
     kp.timeout_ns = kTimeoutNs;
-    // 512 D bytes at 6.8 TB/s over 152 SMs of 1.9 GHz: 2780 clocks at head_dim 128; at 64, 1390,
-    // beside 1350 of work instead of 1900 (paged_cost)
-    kp.block_clocks = p->D == 128 ? 7 : 6;
+    // 512 D bytes at 6.8 TB/s over 152 SMs of 1.9 GHz, by 400 clocks: 2780 at head_dim 128. At 64
+    // 1390, beside some 1350 of work on a block of few rows that counts as 5 (paged_cost): 5, so
+    // that there the bytes never bound the whole. 6 there took 52.1 us instead of 40.0 for 16
+    // requests of some 550 keys without a prefix (64 heads) and 68.8 instead of 56.6 for 4 of
+    // some 4000, and was nowhere more than 0.7% faster (8 of some 1100 behind 2048).
+    kp.block_clocks = p->D == 128 ? 7 : 5;
     kp.shape = cfa::PagedShape(p->nh / p->nkv, p->nkv, a.prefix_len, p->num_sms);
     kp.by_page = cfa::FastDiv(static_cast<uint32_t>(p->ps));
     // a box of rows lies inside one page and divides a block of 128 keys

@@ -14,6 +14,7 @@ cudaError_t note(const char *what) {
     return cudaSuccess;
 }
 size_t allocated;
+cfa::PagedAttnParams merged;
 char kernels[4];
 }  // namespace
 
@@ -34,7 +35,10 @@ cudaError_t CUDARTAPI cudaMemcpy(void *to, const void *, size_t n, cudaMemcpyKin
 }
 cudaError_t CUDARTAPI cudaStreamSynchronize(cudaStream_t) { return note("wait"); }
 cudaError_t CUDARTAPI cudaDeviceSynchronize(void) { return note("wait"); }
-cudaError_t CUDARTAPI cudaLaunchKernelExC(const cudaLaunchConfig_t *, const void *, void **) { return note("launch"); }
+cudaError_t CUDARTAPI cudaLaunchKernelExC(const cudaLaunchConfig_t *, const void *kernel, void **args) {
+    if (kernel == kernels + 3) merged = *static_cast<const cfa::PagedAttnParams *>(args[0]);
+    return note("launch");
+}
 }
 
 namespace cfa {
@@ -147,11 +151,28 @@ const char *bytes() {
     return nullptr;
 }
 
+// The clocks of a block's bytes are those that its head_dim's comment derives.
+const char *clocks() {
+    for (const int d : {64, 128}) {
+        cfa_paged *p = cfa_paged_create(Layer::B, Layer::T, Layer::H, Layer::KV, d, Layer::PS);
+        const Layer a;
+        if (cfa_paged_attention(p, 1, 1, Layer::at(a.q), Layer::H * d, Layer::ints(a.cu), nullptr, 0, Layer::ints(a.tables),
+                                1, Layer::ints(a.lens), 1, Layer::at(a.kp), Layer::at(a.vp), 0.f, Layer::at(a.out), nullptr,
+                                nullptr) != CFA_OK)
+            return "a good call was refused";
+        const double clk = 512.0 * d * 152 / 6.8e12 * 1.9e9;
+        const double unit = d == 128 ? 400 : 1350.0 / cfa::paged_cost(1);
+        if (merged.block_clocks != std::lround(clk / unit)) return "other clocks than derived";
+        cfa_paged_destroy(p);
+    }
+    return nullptr;
+}
+
 }  // namespace
 
 int main(int argc, char **argv) {
     const std::string which = argc > 1 ? argv[1] : "";
-    const char *wrong = which == "overlaps" ? overlaps() : which == "order" ? order() : which == "scales" ? scales() : which == "bytes" ? bytes() : "which check?";
+    const char *wrong = which == "overlaps" ? overlaps() : which == "order" ? order() : which == "scales" ? scales() : which == "bytes" ? bytes() : which == "clocks" ? clocks() : "which check?";
     std::puts(wrong ? wrong : "ok");
     return wrong != nullptr;
 }

@@ -42,3 +42,7 @@ def test_walk_through_long_requests(tmp_path):
 
 def test_describe_counts_every_byte(tmp_path):
     run_check(tmp_path, "paged_calls_check", "bytes")
+
+
+def test_clocks_of_a_blocks_bytes(tmp_path):
+    run_check(tmp_path, "paged_calls_check", "clocks")
