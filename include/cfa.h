@@ -626,9 +626,9 @@ cfa_status cfa_paged_append(cfa_paged *paged, int n_tokens, const void *q, long 
  *        exp(scale q . k), or NULL
  * A row that sees no key gets 0 and lse -inf. Rows outside [cu[0], cu[n_seqs])
  * stay as they were. scale 0 means 1/sqrt(head_dim); scale times log2 e must be
- * finite in 32 bits. Cache rows at positions that no row of the request sees may
- * hold anything, NaN included; a value that is not finite where some row
- * sees it may spoil the request's other rows too. Flagged in the status word as CFA_ERR_INVALID_ARG: offsets cu that
+ * finite in 32 bits. Keys and values that a row does not see do not change it,
+ * whatever they hold, NaN included (values that are not finite and that only some of a
+ * request's rows see take a slow pass behind the call). Flagged in the status word as CFA_ERR_INVALID_ARG: offsets cu that
  * are not ascending within [0, n_tokens], or more than some 2^27 blocks of
  * 128 keys over all key heads and tiles of 256 rows (nothing is written then); a
  * length outside [0, table_width * page_size] (taken as 0); a page id outside

@@ -32,7 +32,7 @@ struct cfa_paged {
     float magnitude = 1.0f;
     unsigned long long turns[64] = {};
     // workspace
-    unsigned *words = nullptr;  // [0] status, [1] arrivals of the tables' blocks
+    unsigned *words = nullptr;  // [0] status, [1] arrivals of the tables' blocks, [2..3] the merge's (odd)
     int *plan_ws = nullptr;     // the attention's scan, for its merge
     float *rec_o = nullptr;     // records of the attention's pieces
     float2 *rec_ml = nullptr;
@@ -285,7 +285,7 @@ cfa_status launch_attention(cfa_paged *p, const AttnArgs &a, cudaStream_t stream
     cfa::PagedAttnParams kp{};
     kp.q = static_cast<const uint16_t *>(a.q);
     kp.q_stride = a.qs;
-    kp.k_pages = static_cast<const uint16_t *>(a.kp);
+    kp.v_pages = static_cast<const uint16_t *>(a.vp);
     kp.v_pages = static_cast<const uint16_t *>(a.vp);
     kp.cu = a.cu;
     kp.lens = a.lens;
@@ -294,6 +294,7 @@ cfa_status launch_attention(cfa_paged *p, const AttnArgs &a, cudaStream_t stream
     kp.out = static_cast<uint16_t *>(a.out);
     kp.lse = a.lse;
     kp.status = p->words;
+    kp.odd = p->words + 2;
     kp.T = a.n_tokens;
     kp.B = a.n_seqs;
     kp.n_heads = p->nh;
@@ -383,8 +384,8 @@ cfa_paged *cfa_paged_create(int max_seqs, int max_tokens, int n_heads, int n_kv_
                              static_cast<int>(sizeof(int)) * (3 * cfa::kPagedMaxSeqs + 2)) != cudaSuccess ||
         cudaFuncSetAttribute(cfa::paged_attention_kernel_ptr(head_dim), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              cfa::paged_attention_smem(head_dim, cfa::kPagedMaxSeqs)) != cudaSuccess ||
-        cudaMalloc(&p->words, 2 * sizeof(unsigned)) != cudaSuccess ||
-        !clear_words(p->words, 2) ||
+        cudaMalloc(&p->words, 4 * sizeof(unsigned)) != cudaSuccess ||
+        !clear_words(p->words, 4) ||
         cudaMalloc(&p->plan_ws, sizeof(int) * p->plan_ints) != cudaSuccess ||
         cudaMalloc(&p->rec_o, sizeof(float) * static_cast<size_t>(p->rec_rows) * head_dim) != cudaSuccess ||
         cudaMalloc(&p->rec_ml, sizeof(float2) * static_cast<size_t>(p->rec_rows)) != cudaSuccess) {

@@ -69,7 +69,7 @@ constexpr int kAppendThreads = 128;  // at most (append_threads)
 struct PagedAttnParams {
     const uint16_t *q;          // [T][n_heads][d], row stride q_stride elements
     long long q_stride;
-    const uint16_t *k_pages, *v_pages;
+    const uint16_t *v_pages;    // (the attention reads keys and values by tensor maps)
     const int *cu;              // [B + 1]
     const int *lens;            // [B]
     const int *tables;          // [B][width]
@@ -77,6 +77,8 @@ struct PagedAttnParams {
     uint16_t *out;              // [T][n_heads][d]
     float *lse;                 // [T][n_heads] or null
     unsigned *status;
+    unsigned *odd;              // {a value that is not finite was cleared, arrivals of the merge's
+                                // blocks}; 0 between calls
     int *plan_ws;               // for the merge: the scan's totals, every run's PagedCut, every
                                 // shared row's PagedRow
     float *rec_o;               // records: unnormalised outputs, a piece's rows in 16-byte chunks,

@@ -130,6 +130,12 @@ __device__ __forceinline__ float exp2_ftz(float x) {
     return y;
 }
 
+// All bits of those of two bf16 that are infinite or NaN: an exponent of ones and the 1 added to
+// it carry into the sign's place.
+__device__ __forceinline__ uint32_t odd_bf16x2(uint32_t v) {
+    return ((((v & 0x7f807f80u) + 0x00800080u) >> 15) & 0x00010001u) * 0xffffu;
+}
+
 // Two fp32 lanes in one instruction.
 __device__ __forceinline__ uint64_t pair_f32(float a, float b) {
     uint64_t r;
@@ -248,6 +254,29 @@ static_assert(kPagedMaxTokens <= kPagedTokenMask, "a token fits its bits");
 template <int D>
 __device__ __forceinline__ const uint16_t *paged_query(const PagedAttnParams &p, int at, int h) {
     return p.q + (at & kPagedTokenMask) * p.q_stride + (h * p.shape.G + (at >> kPagedTokenBits)) * D;
+}
+
+// What of a stage's values must not meet masked weights, which are 0, and 0 times NaN is NaN: rows
+// [keys, end), past the keys, may hold anything and become 0; of rows [begin, keys), which some
+// query rows see and others do not, what is not finite becomes 0, and the merge is told to add
+// it to the rows that see it. By `threads` threads, of which this is the t-th.
+template <int D>
+__device__ __forceinline__ void paged_clear(const PagedAttnParams &p, uint8_t *rows, int begin, int keys, int end, int t,
+                                            int threads) {
+    CFA_ROLLED for (int i = t; i < (end - begin) * (D / 8); i += threads) {
+        const int r = begin + i / (D / 8), c = i % (D / 8);  // (of a row's chunks any order will do)
+        uint4 *at = reinterpret_cast<uint4 *>(rows + (c >> 3) * PagedSmem<D>::kHalf + r * 128 + ((c & 7) << 4));
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (r < keys) {
+            v = *at;
+            const uint32_t a = odd_bf16x2(v.x), b = odd_bf16x2(v.y), d = odd_bf16x2(v.z), e = odd_bf16x2(v.w);
+            if ((a | b | d | e) == 0u) continue;
+            *p.odd = 1u;
+            v = make_uint4(v.x & ~a, v.y & ~b, v.z & ~d, v.w & ~e);
+        }
+        *at = v;
+        if (r < keys) fence_proxy_async_smem();  // (the stage's next copy comes after)
+    }
 }
 
 template <bool V>
@@ -748,10 +777,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_empty + 8 * slot_of(0, block));
                     uint32_t pr[2][4];
+                    int seen = 32;  // of the warp's keys, by every row
                     if (keys > 0) {
                         const bool own = x.b0 + j >= x.prefix_blocks;
                         const int lim0 = own ? min(keys, see0 - key0) : keys;
                         const int lim1 = own ? min(keys, see1 - key0) : keys;
+                        seen = uniform(lim0);  // (lane 0 has the first row)
                         float a0 = -INFINITY, a1 = -INFINITY;
 #pragma unroll
                         for (int t = 0; t < 4; ++t)
@@ -824,8 +855,16 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
                                 mma_16x8x16(o[2 * i + 1], pr[1], d[2], d[3]);
                             }
                         };
-                        if (keys >= 32) values(PagedFlag<true>{});
-                        else values(PagedFlag<false>{});
+                        if (seen >= 32) {
+                            values(PagedFlag<true>{});
+                        } else {
+                            if (seen < min(keys, 32)) {
+                                paged_clear<D>(p, smem + S::kRing + slot_of(1, block) * S::kStage + kw * 128, max(seen, 0),
+                                               min(keys, 32), min(keys, 32), lane, 32);
+                                __syncwarp();
+                            }
+                            values(PagedFlag<false>{});
+                        }
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_empty + 8 * slot_of(1, block));
@@ -908,6 +947,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             const bool live = row < x.rows;
             const bool warp_live = (row & ~31) < x.rows;
             const int see = x.req < 0 ? 0 : paged_visible(x.r, (x.row0 + min(row, x.rows - 1)) / shape.by_G);
+            const int all_see = paged_visible(x.r, x.row0 / shape.by_G);  // what the first row sees, every row does
             const uint32_t t_s = tmem + lanes + 128 * wg, t_o = tmem + lanes + 256 + D * wg;
             const uint32_t bs = bar_s + 16 * wg, bp = bar_p + 16 * wg;
             float m = -INFINITY, l = 0.f;
@@ -915,21 +955,20 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
             CFA_ROLLED for (int j = first_block; j < nb; j += step, ++scored) {
                 int key0;
                 const int keys = block_keys(x, x.b0 + j, &key0);
-                const int lim = x.b0 + j < x.prefix_blocks ? keys : min(keys, see - key0);
+                const bool own = x.b0 + j >= x.prefix_blocks;
+                const int lim = own ? min(keys, see - key0) : keys;
+                const int some = own ? max(0, all_see - key0) : kPagedKeys;  // keys from here on some rows do not see
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     wait(bs + 8 * h, scored & 1, kSiteSoftmaxExchange);
                     __syncwarp();
                     tcgen05_fence_after();
-                    if (h == 0 && keys < kPagedKeys) {
-                        // rows past the keys may hold anything, and 0 times NaN is NaN
+                    if (h == 0 && (keys < kPagedKeys || some < keys)) {
+                        // (not before these scores: with them the stage's last values are known to
+                        // have landed, and its barrier's parity to speak of these)
                         wait_full(1, n + j);
-                        const int z = max(keys, 0);
-                        CFA_ROLLED for (int i = wtid; i < (kPagedKeys - z) * (D / 8); i += 128) {
-                            const int r = z + i / (D / 8), c = i % (D / 8);
-                            *reinterpret_cast<uint4 *>(smem + S::kRing + slot_of(1, n + j) * S::kStage + (c >> 3) * S::kHalf +
-                                                       r * 128 + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                        }
+                        paged_clear<D>(p, smem + S::kRing + slot_of(1, n + j) * S::kStage, min(some, max(keys, 0)),
+                                       max(keys, 0), kPagedKeys, wtid, 128);
                         fence_proxy_async_smem();
                     }
                     if (warp_live) {
@@ -1190,6 +1229,52 @@ struct PagedMerge {
     }
 };
 
+// Adds the values that are not finite to the rows that see them, where paged_clear has met one (rows
+// that have them already do not change). The last block does it, when all rows are written: a
+// thread goes through a request's new tokens with 8 dims of a key head and holds what they
+// have seen so far. Rare, so it need only end in time: a load a token.
+template <int D>
+__device__ __noinline__ void paged_add_odd(const PagedAttnParams &p) {
+    __shared__ bool last;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomic_add_acq_rel_gpu(p.odd + 1, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    if (threadIdx.x < 2) p.odd[threadIdx.x] = 0;
+    const int G = p.shape.G;
+    for (int task = threadIdx.x; task < p.B * p.n_kv * (D / 8); task += kPagedMergeThreads) {
+        const int c = task % (D / 8), b = task / (D / 8) / p.n_kv, h = task / (D / 8) - b * p.n_kv;
+        const int tok0 = p.cu[b], n = p.cu[b + 1] - tok0, len = p.lens[b];
+        if (len < 0 || len > static_cast<long long>(p.width) * p.page_size) continue;
+        bool some = false;
+        float seen[8] = {};
+        // token i is the first that sees key len - n + i (the first token's keys all see)
+        for (int i = max(1, n - len); i < n; ++i) {
+            const int key = len - n + i, pg = key / p.by_page;
+            const int id = p.tables[static_cast<size_t>(b) * p.width + pg];
+            if (id >= 0 && id < p.n_pages) {
+                const size_t row = static_cast<size_t>(id * p.n_kv + h) * p.page_size + key - pg * p.page_size;
+                float v[8];
+                unpack8_bf16(*reinterpret_cast<const uint4 *>(p.v_pages + row * D + 8 * c), v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (!(fabsf(v[e]) < INFINITY)) seen[e] += v[e], some = true;
+            }
+            if (!some) continue;
+            for (int g = 0; g < G; ++g) {
+                uint4 *at = reinterpret_cast<uint4 *>(p.out + (static_cast<size_t>(tok0 + i) * p.n_heads + h * G + g) * D + 8 * c);
+                float y[8];
+                unpack8_bf16(*at, y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = seen[e] == 0.f ? y[e] : y[e] + seen[e];
+                *at = make_uint4(pack2_bf16_cvt(y[0], y[1]), pack2_bf16_cvt(y[2], y[3]), pack2_bf16_cvt(y[4], y[5]),
+                                 pack2_bf16_cvt(y[6], y[7]));
+            }
+        }
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPagedMergeThreads, 3)
 paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
@@ -1202,6 +1287,7 @@ paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
     const PagedPlan plan = *reinterpret_cast<const PagedPlan *>(p.plan_ws);
     const PagedCut *cut_of = reinterpret_cast<const PagedCut *>(p.plan_ws + kPagedPlanInts);
     const PagedRow *row_of = reinterpret_cast<const PagedRow *>(p.plan_ws + kPagedPlanInts + 8 * shape.grid);
+    const unsigned odd = __ldcg(p.odd);
     if (!plan.valid) return;
     const int shared_tasks = (plan.shared_rows + 31) / 32 * p.n_kv * C;
     const int warps = static_cast<int>(gridDim.x) * (kPagedMergeThreads / 32);
@@ -1240,7 +1326,10 @@ paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
         }
         acc.template write<D>(p, d.out_row + h * shape.G, chunk);
     }
-    if (plan.alone_tokens == 0) return;
+    if (plan.alone_tokens == 0) {
+        if (odd) paged_add_odd<D>(p);
+        return;
+    }
     // the cut runs in order, the same list in every block
     static_assert(kPagedMaxGrid <= kPagedMergeThreads, "a thread looks at a run");
     const bool is_cut = tid < shape.grid && cut_of[tid].rows > 0;
@@ -1282,6 +1371,7 @@ paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
         }
         acc.template write_pairs<D>(p, at < cut.rows ? (cut.tok0 + i) * p.n_heads + cut.h * shape.G + r - i * shape.G : -1, chunk);
     }
+    if (odd) paged_add_odd<D>(p);
 }
 
 }  // namespace cfa

@@ -130,7 +130,7 @@ const char *scales() {
     return nullptr;
 }
 
-// describe tells of every byte that a plan keeps on the device (and two words).
+// describe tells of every byte that a plan keeps on the device (and four words).
 const char *bytes() {
     const struct { int seqs, tokens, heads, kv, d; } plans[] = {
         {1, 1, 1, 1, 64}, {2, 8, 4, 2, 64}, {64, 512, 32, 8, 128}, {1024, 1 << 17, 32, 32, 128}, {1024, 1 << 17, 1024, 1, 64}};
@@ -145,7 +145,7 @@ const char *bytes() {
             if (!at) return "a field is missing";
             told += std::atoll(at + std::strlen(name));
         }
-        if (told + 8 != static_cast<long long>(allocated)) return "bytes that describe leaves out";
+        if (told + 16 != static_cast<long long>(allocated)) return "bytes that describe leaves out";
         cfa_paged_destroy(p);
     }
     return nullptr;
