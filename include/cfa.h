@@ -518,7 +518,8 @@ cfa_status cfa_mla_set_row_splits(cfa_mla *mla, int splits);
  * 4-byte aligned, the bf16 ones 16-byte aligned.
  *
  * A plan owns a workspace: one plan must not run on two streams at once, nor
- * in two graphs that may run at the same time.
+ * in two graphs that may run at the same time. Calls are asynchronous: arrays live
+ * until the stream has passed the call.
  * ========================================================================== */
 
 typedef struct cfa_paged cfa_paged; /* opaque */
@@ -621,7 +622,9 @@ cfa_status cfa_paged_append(cfa_paged *paged, int n_tokens, const void *q, long 
  * the pages prefix_table lists; may be 0) and, of the lens[b] keys in the pages
  * of tables[b] (its new tokens' own keys among them), those up to its own
  * position: row cu[b] + i sees lens[b] - (cu[b + 1] - cu[b]) + i + 1 of them.
- *   out  bf16 [n_tokens, n_heads, head_dim] = softmax(scale q . k) v
+ *   out  bf16 [n_tokens, n_heads, head_dim] = softmax(scale q . k) v; the weights
+ *        are rounded to bf16 (to nearest) for the product with v, everything else
+ *        up to the result is held in 32 bits
  *   lse  fp32 [n_tokens, n_heads], the natural logarithm of the sum of
  *        exp(scale q . k), or NULL
  * A row that sees no key gets 0 and lse -inf. Rows outside [cu[0], cu[n_seqs])

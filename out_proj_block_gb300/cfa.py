@@ -776,7 +776,9 @@ class Paged:
 
     k_pages and v_pages are bf16 [n_pages, n_kv_heads, page_size, head_dim];
     q, k, v [tokens, heads, head_dim] may be slices of a fused projection (dense
-    within a row); every integer tensor is int32 on the plan's device."""
+    within a row); every integer tensor is int32 on the plan's device. Calls go to the
+    current stream of that device, or to ``stream``; the tensors of a call on a stream
+    other than their own have to be kept (or ``record_stream``-ed) until it has run."""
 
     def __init__(self, max_seqs: int, max_tokens: int, n_heads: int, n_kv_heads: int,
                  head_dim: int, page_size: int):

@@ -27,9 +27,9 @@
 // On tcgen05 a block's keys go in two halves: S = Q K^T (M = 128 rows, N = 64
 // keys) of the next half runs while a thread per row takes this half's scores from
 // TMEM and writes the weights back over them as bf16; O += P V reads them there. A
-// warpgroup has an MMA warp of its own. A row's maximum is followed lazily: O is
-// rescaled only when it grew by more than 8 (a factor 2^8, far inside fp32), which
-// is rare.
+// warpgroup has an MMA warp of its own. A row's maximum is followed lazily, a
+// published method: O is rescaled only when it grew by more than 8 (a factor 2^8, far
+// inside fp32), which is rare.
 //
 // Weights are rounded to bf16 for the product with V (tensor cores take both
 // operands in one type; 2^-8 each, the size of the result's own rounding); their
