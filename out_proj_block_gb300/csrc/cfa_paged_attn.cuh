@@ -37,7 +37,7 @@
 //
 // Measured, with the merge (one GB300, 32 heads x 128 where not said):
 //   16 requests, 4096 shared keys and some 1024 own ones, no groups: 46.2 us, 213 MB (4.6 TB/s)
-//   64 requests, 32768 and 2048, 8 key heads: 84 us, 431 MB (5.1 TB/s)
+//   64 requests, 32768 and 2048, 8 key heads: 85 us, 431 MB (5.1 TB/s)
 //   256 requests, 8192 and 512, 8 key heads, pages of 16: 92 us, 315 MB
 //   8 requests of up to 512 new tokens, 4096 and 1500, 8 key heads: 228 us (1.14 PFLOP/s)
 //   one request, 64 and 64 keys: 10.7 us
