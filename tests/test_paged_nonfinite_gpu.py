@@ -162,3 +162,47 @@ def test_a_query_that_is_nan(cfa, case):
         got, lse2 = run(plan, q=q)
     assert torch.equal(got[~spoiled], base[~spoiled]) and torch.equal(lse[~spoiled], lse2[~spoiled])
     assert torch.all(torch.isnan(got[spoiled])) and torch.all(torch.isnan(lse2[spoiled]))
+
+
+@pytest.mark.parametrize("case", [0, 4, 5])
+def test_a_recorded_call_meets_them_in_turn(cfa, case):
+    """Replays of one graph, with values that are finite, are not, and are again."""
+    nh, nkv, d, ps, prefix, lens, news = CASES[case]
+    c, run, plan_of = setup(case)
+    v = c["v"].clone()
+    key, out = lens[0] - 1, torch.zeros_like(c["q"])
+    page, off = int(c["tables"][0, key // ps]), key % ps
+    a = (c["q"], ints(c["cu"]), ints(lens), c["tables"].cuda(), c["k"], v, out)
+    kw = dict(prefix_table=ints(list(range(c["pp"]))), prefix_len=prefix) if prefix else {}
+    with plan_of(cfa) as plan:
+        zero = c["v"].clone()
+        zero[page, :, off, 9] = 0.0
+        base, _ = run(plan, v=zero)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            plan.attend(*a, **kw)
+        for x in (0.0, math.inf, 0.0, math.nan, -math.inf, -math.inf, 0.0):
+            v[page, :, off, 9] = x
+            g.replay()
+            want = base.clone()
+            if x != 0.0:
+                want[rows_that_see(case, 0, key), :, 9] = x
+            assert torch.equal(torch.nan_to_num(out, nan=5.0), torch.nan_to_num(want, nan=5.0))
+        assert plan.status() == cfa.CFA_OK
+
+
+def test_many_rows_meet_them(cfa):
+    """A long prompt: the pass behind the call is one load a token, not one a pair of tokens."""
+    nh, nkv, d, ps, n = 8, 2, 128, 64, 20000
+    pages = -(-n // ps)
+    q, k, v = normal(1, n, nh, d), normal(2, pages, nkv, ps, d), normal(3, pages, nkv, ps, d)
+    out, tables = torch.empty_like(q), ints([list(range(pages))])
+    key = 12345
+    v[key // ps, 1, key % ps, 100] = math.inf
+    with cfa.Paged(1, n, nh, nkv, d, ps) as plan:
+        plan.attend(q, ints([0, n]), ints([n]), tables, k, v, out)
+        assert plan.status() == cfa.CFA_OK
+    want = torch.zeros(n, nh, d, dtype=torch.bool, device="cuda")
+    want[key:, 4:, 100] = True
+    assert torch.equal(~torch.isfinite(out), want) and torch.all(out[want] == math.inf)
