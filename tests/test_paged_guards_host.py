@@ -14,8 +14,9 @@ def cuda_include():
 def run_check(tmp_path, name, *args, timeout=120):
     """Compiles tests/<name>.cpp with the host compiler and runs it with these arguments."""
     exe = str(tmp_path / name)
-    subprocess.run(["g++", "-std=c++17", "-O2", "-I", os.path.join(ROOT, "out_proj_block_gb300", "csrc"),
-                    "-I", cuda_include(), "-I", os.path.join(ROOT, "include"), os.path.join(ROOT, "tests", name + ".cpp"), "-o", exe], check=True)
+    csrc = os.path.join(ROOT, "out_proj_block_gb300", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O2", "-I", csrc, "-I", cuda_include(), "-I", os.path.join(ROOT, "include"),
+                    os.path.join(ROOT, "tests", name + ".cpp"), "-o", exe], check=True)
     out = subprocess.run([exe, *args], capture_output=True, text=True, timeout=timeout)
     assert out.returncode == 0 and out.stdout.strip() == "ok", out.stdout
 
