@@ -668,6 +668,144 @@ cfa_status cfa_paged_status(cfa_paged *paged);
  * device, workspace_bytes of records and plan_bytes of a call's plan). */
 cfa_status cfa_paged_describe(const cfa_paged *paged, char *buf, int len);
 
+/* ==========================================================================
+ * Paged latent caches: multi-head latent attention (the formulas and widths of
+ * cfa_mla: latent 512, per head 128 unrotated + 64 rotated query dims, 128 value dims) for the
+ * ragged batches of the paged caches. A cache row is a token's normed latent and
+ * rotated key, 576 bf16, which all heads share:
+ *   pages bf16 [n_pages, page_size, 576]; row `off` of page `id` is slot id * page_size + off,
+ * so cfa_paged_tables of a plan with the same page_size makes tables, offsets, positions and
+ * slots for it too. Per layer and step:
+ *   cfa_latent_append     norm, rotation, rows into their slots; queries rotated
+ *   decode, drafted tokens (absorbed form: a head's products with W_kvb on the query's side)
+ *     cfa_latent_fold       queries into the latent space
+ *     cfa_latent_attention  over the cached rows
+ *     cfa_latent_unfold     results back to the value dims
+ *   prompts (expanded form)
+ *     cfa_latent_expanded   over keys and values that the caller has expanded (latents . W_kvb)
+ * W_kvb is cfa_mla's: [512, n_heads * 256], per head [W_k (128) | W_v (128)]. Device arrays,
+ * values out of range, alignment and streams as in the paged caches above (a plan's workspace
+ * serves cfa_latent_attention alone).
+ * ========================================================================== */
+
+typedef struct cfa_latent cfa_latent; /* opaque */
+
+/*
+ * Plan on the current device for at most max_seqs (1..1024) requests and max_tokens
+ * (1..131072) new tokens per call, n_heads 1..1024, page_size 16, 32 or a multiple of 64 up
+ * to 1<<22 (CFA_ERR_UNSUPPORTED otherwise; CFA_ERR_INVALID_ARG for non-positive values). No
+ * rotation until cfa_latent_set_rope. The workspace holds the records of cut tiles, SMs x 128
+ * rows of 512 + 2 floats. NULL on failure; cfa_last_error() says why.
+ */
+cfa_latent *cfa_latent_create(int max_seqs, int max_tokens, int n_heads, int page_size);
+
+/* Release the plan (synchronizes its device first). NULL is a no-op. */
+void cfa_latent_destroy(cfa_latent *latent);
+
+/*
+ * The rotation of the following cfa_latent_append and cfa_latent_layer calls, over the 64
+ * rotated dims; arguments as cfa_paged_set_rope. theta 0 turns it off.
+ */
+cfa_status cfa_latent_set_rope(cfa_latent *latent, double theta, int interleaved, int scaling,
+                               double factor, double low_turns, double high_turns,
+                               int original_ctx, double magnitude);
+
+/*
+ * A token's cache row from the down projection's row a (576 bf16: latent, then the key to
+ * rotate; rows a_stride elements apart) and its rotated queries:
+ *   row = [bf16(rmsnorm(a[:512]; g_kv)) | bf16(rope(a[512:], positions[t]))] to slots[t]
+ *   q_out[t, h] = [q[t, h, :128] | bf16(rope(q[t, h, 128:], positions[t]))]
+ * q rows of n_heads * 192, q_stride elements apart (both strides multiples of 8); q_out
+ * [n_tokens, n_heads, 192] may be q where q_stride = n_heads * 192 (then only the rotated
+ * dims are touched), and must not overlap q otherwise. rmsnorm as cfa_rmsnorm; g_kv [512]; eps >= 0, finite.
+ * Rows with a negative slot are skipped: their q_out row stays as it was. A slot of
+ * n_pages * page_size or more is skipped too and flagged (CFA_ERR_INVALID_ARG from
+ * cfa_latent_status). Two tokens with the same slot leave in its row pieces of either. With
+ * n_tokens 0 this call and the next ones do nothing (pointers may then be NULL).
+ */
+cfa_status cfa_latent_append(cfa_latent *latent, int n_tokens, const void *a, long long a_stride,
+                             const void *g_kv, float eps, const void *q, long long q_stride,
+                             const int *positions, const int *slots, int n_pages, void *pages,
+                             void *q_out, void *stream);
+
+/*
+ * Queries into the latent space: q_lat [n_tokens, n_heads, 576],
+ *   q_lat[t, h] = [bf16(W_k,h . q[t, h, :128]) | q[t, h, 128:]]
+ * q as cfa_latent_append wrote it (q_stride elements between tokens, a multiple of 8). fp32 sums.
+ */
+cfa_status cfa_latent_fold(cfa_latent *latent, int n_tokens, const void *q, long long q_stride,
+                           const void *W_kvb, void *q_lat, void *stream);
+
+/*
+ * Results out of the latent space: out [n_tokens, n_heads, 128],
+ *   out[t, h] = bf16(o_lat[t, h] . W_v,h), o_lat [n_tokens, n_heads, 512].
+ */
+cfa_status cfa_latent_unfold(cfa_latent *latent, int n_tokens, const void *o_lat,
+                             const void *W_kvb, void *out, void *stream);
+
+/*
+ * Attention of folded queries q_lat [n_tokens, n_heads, 576] of n_seqs requests over their
+ * cached rows: tokens [cu[b], cu[b + 1]) are the last of request b, whose lens[b] rows (its
+ * new tokens' own among them) lie in the pages of tables[b]. Token cu[b] + i sees the first
+ * lens[b] - (cu[b + 1] - cu[b]) + i + 1 of them.
+ *   o_lat bf16 [n_tokens, n_heads, 512] = sum_j softmax_j(scale q_lat . row_j) row_j[:512];
+ *         the weights are rounded to bf16 for the product with the rows, everything else up to the
+ *         result is held in 32 bits
+ *   lse   fp32 [n_tokens, n_heads], the natural logarithm of the sum of exp(scale q_lat . row_j),
+ *         or NULL
+ * A token that sees no row gets 0 and lse -inf. Tokens outside [cu[0], cu[n_seqs]) stay as
+ * they were. scale 0 means 1/sqrt(192); scale times log2 e must be finite in 32 bits. Rows
+ * that a token does not see do not change it, whatever they hold. Flagged in the status word
+ * as CFA_ERR_INVALID_ARG: offsets cu that are not ascending within [0, n_tokens], or more than
+ * 2^29 blocks of 128 rows over all tiles of 128 token heads (nothing is written then); a length outside
+ * [0, table_width * page_size] (taken as 0); a page id outside [0, n_pages) where a row is read
+ * (it counts as zeros). o_lat and lse must not overlap an input or each other.
+ */
+cfa_status cfa_latent_attention(cfa_latent *latent, int n_tokens, int n_seqs, const void *q_lat,
+                                const int *cu, const int *tables, int table_width,
+                                const int *lens, int n_pages, const void *pages, float scale,
+                                void *o_lat, float *lse, void *stream);
+
+/*
+ * Attention of prompts over expanded keys and values: request b has query tokens
+ * [cu[b], cu[b + 1]) of q (n_heads * 192 a token, q_stride elements apart) and keys
+ * [cu_k[b], cu_k[b + 1]) of kv [n_keys, n_heads, 256] (per head [key (128) | value (128)], rows
+ * kv_stride elements apart: the product of normed latents with W_kvb) and k_rope (64 a key, shared by the
+ * heads, rows k_rope_stride apart: cache rows from dim 512 on, for instance). Its query tokens
+ * are the last of its keys' tokens: with n query tokens and L keys, token i sees the first
+ * L - n + i + 1 keys.
+ *   out bf16 [n_tokens, n_heads, 128], lse fp32 [n_tokens, n_heads] or NULL, as cfa_latent_attention
+ *   computes them from k = [key | k_rope] and value, scale and unseen keys as there.
+ * q_stride a multiple of 8, kv_stride and k_rope_stride too. A token that sees no key gets 0 and lse
+ * -inf; tokens outside the requests stay as they were. Flagged (CFA_ERR_INVALID_ARG from
+ * cfa_latent_status, nothing written): cu or cu_k that are not ascending within [0, n_tokens]
+ * and [0, n_keys]. n_keys up to 1<<30; with 0 kv and k_rope may be NULL.
+ */
+cfa_status cfa_latent_expanded(cfa_latent *latent, int n_tokens, int n_keys, int n_seqs,
+                               const void *q, long long q_stride, const void *kv,
+                               long long kv_stride, const void *k_rope, long long k_rope_stride,
+                               const int *cu, const int *cu_k, float scale, void *out, float *lse,
+                               void *stream);
+
+/*
+ * The attention of one layer's decode step: cfa_latent_append (queries rotated into q_out,
+ * which may be q), cfa_latent_fold to q_lat, cfa_latent_attention to o_lat, cfa_latent_unfold
+ * to out [n_tokens, n_heads, 128]. Arguments as theirs. Nothing that the call writes may overlap what
+ * a later part of it reads, but for these four arrays' own part.
+ */
+cfa_status cfa_latent_layer(cfa_latent *latent, int n_tokens, int n_seqs, const void *a,
+                            long long a_stride, const void *g_kv, float eps, const void *q,
+                            long long q_stride, const int *positions, const int *slots,
+                            const int *cu, const int *tables, int table_width, const int *lens,
+                            int n_pages, void *pages, const void *W_kvb, float scale, void *q_out,
+                            void *q_lat, void *o_lat, float *lse, void *out, void *stream);
+
+/* Synchronizes, reads and clears the plan's device status word (as cfa_plan_status). */
+cfa_status cfa_latent_status(cfa_latent *latent);
+
+/* One-line JSON description (shape, rotation, grid, shared memory, workspace_bytes). */
+cfa_status cfa_latent_describe(const cfa_latent *latent, char *buf, int len);
+
 #ifdef __cplusplus
 }
 #endif

@@ -133,6 +133,34 @@ _lib.cfa_paged_status.argtypes = [_vp]
 _lib.cfa_paged_describe.restype = _i
 _lib.cfa_paged_describe.argtypes = [_vp, ctypes.c_char_p, _i]
 
+_lib.cfa_latent_create.restype = _vp
+_lib.cfa_latent_create.argtypes = [_i] * 4
+_lib.cfa_latent_destroy.restype = None
+_lib.cfa_latent_destroy.argtypes = [_vp]
+_lib.cfa_latent_set_rope.restype = _i
+_lib.cfa_latent_set_rope.argtypes = [_vp, ctypes.c_double, _i, _i, ctypes.c_double, ctypes.c_double,
+                                     ctypes.c_double, _i, ctypes.c_double]
+_lib.cfa_latent_append.restype = _i
+_lib.cfa_latent_append.argtypes = [_vp, _i, _vp, _ll, _vp, ctypes.c_float, _vp, _ll, _vp, _vp, _i, _vp,
+                                   _vp, _vp]
+_lib.cfa_latent_fold.restype = _i
+_lib.cfa_latent_fold.argtypes = [_vp, _i, _vp, _ll, _vp, _vp, _vp]
+_lib.cfa_latent_unfold.restype = _i
+_lib.cfa_latent_unfold.argtypes = [_vp, _i, _vp, _vp, _vp, _vp]
+_lib.cfa_latent_attention.restype = _i
+_lib.cfa_latent_attention.argtypes = [_vp, _i, _i, _vp, _vp, _vp, _i, _vp, _i, _vp, ctypes.c_float, _vp,
+                                      _vp, _vp]
+_lib.cfa_latent_expanded.restype = _i
+_lib.cfa_latent_expanded.argtypes = [_vp, _i, _i, _i, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp,
+                                     ctypes.c_float, _vp, _vp, _vp]
+_lib.cfa_latent_layer.restype = _i
+_lib.cfa_latent_layer.argtypes = [_vp, _i, _i, _vp, _ll, _vp, ctypes.c_float, _vp, _ll, _vp, _vp, _vp, _vp,
+                                  _i, _vp, _i, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp]
+_lib.cfa_latent_status.restype = _i
+_lib.cfa_latent_status.argtypes = [_vp]
+_lib.cfa_latent_describe.restype = _i
+_lib.cfa_latent_describe.argtypes = [_vp, ctypes.c_char_p, _i]
+
 CFA_OK = 0
 CFA_ERR_INVALID_ARG = 1
 CFA_ERR_UNSUPPORTED = 2
@@ -160,6 +188,9 @@ EXPORTED_SYMBOLS = (
     "cfa_paged_create", "cfa_paged_destroy", "cfa_paged_set_rope", "cfa_paged_tables",
     "cfa_paged_append", "cfa_paged_attention", "cfa_paged_layer", "cfa_paged_status",
     "cfa_paged_describe",
+    "cfa_latent_create", "cfa_latent_destroy", "cfa_latent_set_rope", "cfa_latent_append",
+    "cfa_latent_fold", "cfa_latent_unfold", "cfa_latent_attention", "cfa_latent_expanded",
+    "cfa_latent_layer", "cfa_latent_status", "cfa_latent_describe",
 )
 
 
@@ -1008,4 +1039,226 @@ class Paged:
             self._turned(T, q_out), op, sp, self._stream(stream))
         if st != CFA_OK:
             raise CfaError(st, "cfa_paged_layer")
+        return out
+
+
+# --------------------------------------------------------- paged latent caches
+
+
+def cfa_latent_create(max_seqs: int, max_tokens: int, n_heads: int, page_size: int) -> int:
+    h = _lib.cfa_latent_create(max_seqs, max_tokens, n_heads, page_size)
+    if not h:
+        raise CfaError(cfa_last_error(), "cfa_latent_create")
+    return h
+
+
+def cfa_latent_destroy(latent: int) -> None:
+    _lib.cfa_latent_destroy(latent)
+
+
+def cfa_latent_status(latent) -> int:
+    return int(_lib.cfa_latent_status(latent))
+
+
+def cfa_latent_describe(latent) -> dict:
+    buf = ctypes.create_string_buffer(1024)
+    st = _lib.cfa_latent_describe(latent, buf, len(buf))
+    if st != CFA_OK:
+        raise CfaError(st, "cfa_latent_describe")
+    return json.loads(buf.value.decode())
+
+
+class Latent:
+    """Owns a cfa_latent: latent attention over paged caches, for ragged batches.
+
+    pages are bf16 [n_pages, page_size, 576] (normed latent 512 | rotated key 64); tables,
+    offsets, positions and slots as ``Paged.build_tables`` of the same page_size makes them. W_kvb
+    [512, n_heads * 256] is the ``Mla`` step's. Decode: append, fold, attend, unfold (or layer,
+    which runs the four); prompts: append, then attend_expanded on keys and values the caller has
+    expanded. Integer tensors are int32 on the plan's device; streams as in ``Paged``."""
+
+    def __init__(self, max_seqs: int, max_tokens: int, n_heads: int, page_size: int):
+        self.max_seqs, self.max_tokens, self.n_heads, self.page_size = (
+            max_seqs, max_tokens, n_heads, page_size)
+        self.handle = cfa_latent_create(max_seqs, max_tokens, n_heads, page_size)
+        self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
+        self._w_shape = (MLA_KV, n_heads * (MLA_NOPE + MLA_V))
+
+    def close(self):
+        if getattr(self, "handle", None):
+            cfa_latent_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def describe(self) -> dict:
+        return cfa_latent_describe(self.handle)
+
+    def status(self) -> int:
+        return cfa_latent_status(self.handle)
+
+    def set_rope(self, theta: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                 factor: float = 1.0, low_turns: float = 1.0, high_turns: float = 32.0,
+                 original_ctx: int = 4096, magnitude: float = 1.0) -> None:
+        """The rotation of the following append and layer calls (cfa_latent_set_rope);
+        theta 0: no rotation."""
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+        st = _lib.cfa_latent_set_rope(self.handle, float(theta), 1 if interleaved else 0,
+                                      ROPE_SCALINGS[scaling], float(factor), float(low_turns),
+                                      float(high_turns), int(original_ctx), float(magnitude))
+        if st != CFA_OK:
+            raise CfaError(st, "cfa_latent_set_rope")
+
+    # Argument checks: one expression a tensor, what is wrong is said only where it is not true.
+
+    def _dense(self, name, t, shape, dtype=_BF16):
+        """Pointer of a contiguous tensor of this shape."""
+        if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == self._index):
+            if t.dtype is not dtype:
+                raise TypeError(f"{name} must be {dtype}")
+            if t.shape != shape:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            raise ValueError(f"{name} must be on {self.device}")
+        return t.data_ptr()
+
+    def _rows(self, name, t, n, *dims):
+        """Pointer and row stride of bf16 [n, *dims] with dense rows."""
+        s, width, ok = t.stride(), 1, t.dtype is _BF16 and t.shape == (n, *dims)
+        for i in range(len(dims), 0, -1):
+            ok = ok and (s[i] == width or dims[i - 1] == 1)
+            width *= dims[i - 1]
+        if not (ok and t.get_device() == self._index):
+            if t.dtype is not _BF16:
+                raise TypeError(f"{name} must be {_BF16}")
+            if t.shape != (n, *dims):
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, *dims)}")
+            if not ok:
+                raise ValueError(f"{name} must be dense within a row")
+            raise ValueError(f"{name} must be on {self.device}")
+        return t.data_ptr(), (s[0] if n > 1 else width)
+
+    def _pages(self, pages):
+        return pages.shape[0], self._dense("pages", pages, (pages.shape[0], self.page_size, MLA_ROW))
+
+    def _heads(self, name, t, T, d):
+        return self._dense(name, t, (T, self.n_heads, d))
+
+    def _stream(self, stream):
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self._index)
+        return _stream(stream)
+
+    def _scale(self, scale):
+        if scale is not None and not ctypes.c_float(scale).value > 0.0:
+            raise ValueError("scale must be positive, in 32 bits too")
+        return scale or 0.0
+
+    def _append(self, a, g_kv, eps, q, positions, slots, pages, q_out):
+        T = q.shape[0]
+        n, pp = self._pages(pages)
+        return (*self._rows("a", a, T, MLA_ROW), self._dense("g_kv", g_kv, (MLA_KV,)), eps,
+                *self._rows("q", q, T, self.n_heads, MLA_NOPE + MLA_ROPE),
+                self._dense("positions", positions, (T,), _I32), self._dense("slots", slots, (T,), _I32),
+                n, pp, self._heads("q_out", q_out, T, MLA_NOPE + MLA_ROPE))
+
+    def _batch(self, T, cu, lens, tables):
+        if lens.dim() != 1 or tables.dim() != 2:
+            raise ValueError("lens has one dimension, tables two")
+        B, width = lens.shape[0], tables.shape[1]
+        return (B, self._dense("cu", cu, (B + 1,), _I32), self._dense("tables", tables, (B, width), _I32), width,
+                self._dense("lens", lens, (B,), _I32))
+
+    def _lse(self, lse, T):
+        return None if lse is None else self._dense("lse", lse, (T, self.n_heads), _F32)
+
+    def append(self, a, g_kv, q, positions, slots, pages, q_out, eps: float = 1e-6, stream=None):
+        """Cache rows of a [T, 576] (a slice of the down projection) into their slots, q
+        [T, heads, 192] rotated into q_out, which may be q (cfa_latent_append). Returns q_out."""
+        st = _lib.cfa_latent_append(self.handle, q.shape[0],
+                                    *self._append(a, g_kv, eps, q, positions, slots, pages, q_out),
+                                    self._stream(stream))
+        if st != CFA_OK:
+            raise CfaError(st, "cfa_latent_append")
+        return q_out
+
+    def fold(self, q, W_kvb, q_lat, stream=None):
+        """q [T, heads, 192] into the latent space: q_lat [T, heads, 576] (cfa_latent_fold)."""
+        T = q.shape[0]
+        st = _lib.cfa_latent_fold(self.handle, T, *self._rows("q", q, T, self.n_heads, MLA_NOPE + MLA_ROPE),
+                                  self._dense("W_kvb", W_kvb, self._w_shape),
+                                  self._heads("q_lat", q_lat, T, MLA_ROW), self._stream(stream))
+        if st != CFA_OK:
+            raise CfaError(st, "cfa_latent_fold")
+        return q_lat
+
+    def unfold(self, o_lat, W_kvb, out, stream=None):
+        """o_lat [T, heads, 512] out of the latent space: out [T, heads, 128] (cfa_latent_unfold)."""
+        T = o_lat.shape[0]
+        st = _lib.cfa_latent_unfold(self.handle, T, self._heads("o_lat", o_lat, T, MLA_KV),
+                                    self._dense("W_kvb", W_kvb, self._w_shape),
+                                    self._heads("out", out, T, MLA_V), self._stream(stream))
+        if st != CFA_OK:
+            raise CfaError(st, "cfa_latent_unfold")
+        return out
+
+    def attend(self, q_lat, cu, lens, tables, pages, o_lat, scale: Optional[float] = None, lse=None,
+               stream=None):
+        """Attention of folded queries over the cached rows (cfa_latent_attention). scale None:
+        1/sqrt(192). Returns o_lat [T, heads, 512]."""
+        T = q_lat.shape[0]
+        B, cup, tp, width, lp = self._batch(T, cu, lens, tables)
+        n, pp = self._pages(pages)
+        st = _lib.cfa_latent_attention(self.handle, T, B, self._heads("q_lat", q_lat, T, MLA_ROW), cup, tp,
+                                       width, lp, n, pp, self._scale(scale),
+                                       self._heads("o_lat", o_lat, T, MLA_KV), self._lse(lse, T),
+                                       self._stream(stream))
+        if st != CFA_OK:
+            raise CfaError(st, "cfa_latent_attention")
+        return o_lat
+
+    def attend_expanded(self, q, kv, k_rope, cu, cu_k, out, scale: Optional[float] = None, lse=None,
+                        stream=None):
+        """Attention of prompts: q [T, heads, 192] over kv [S, heads, 256] (key 128 | value 128)
+        and k_rope [S, 64], requests' rows by cu and cu_k (cfa_latent_expanded). Returns out
+        [T, heads, 128]."""
+        T, S = q.shape[0], kv.shape[0]
+        if cu.dim() != 1:
+            raise ValueError("cu has one dimension")
+        B = cu.shape[0] - 1
+        st = _lib.cfa_latent_expanded(
+            self.handle, T, S, B, *self._rows("q", q, T, self.n_heads, MLA_NOPE + MLA_ROPE),
+            *self._rows("kv", kv, S, self.n_heads, MLA_NOPE + MLA_V), *self._rows("k_rope", k_rope, S, MLA_ROPE),
+            self._dense("cu", cu, (B + 1,), _I32), self._dense("cu_k", cu_k, (B + 1,), _I32), self._scale(scale),
+            self._heads("out", out, T, MLA_V), self._lse(lse, T), self._stream(stream))
+        if st != CFA_OK:
+            raise CfaError(st, "cfa_latent_expanded")
+        return out
+
+    def layer(self, a, g_kv, q, positions, slots, cu, lens, tables, pages, W_kvb, q_out, q_lat, o_lat, out,
+              eps: float = 1e-6, scale: Optional[float] = None, lse=None, stream=None):
+        """append, fold, attend, unfold in one call (cfa_latent_layer). Returns out."""
+        T = q.shape[0]
+        ap, ast, gp, eps, qp, qs, pos, sl, n, pp, qo = self._append(a, g_kv, eps, q, positions, slots, pages, q_out)
+        B, cup, tp, width, lp = self._batch(T, cu, lens, tables)
+        st = _lib.cfa_latent_layer(
+            self.handle, T, B, ap, ast, gp, eps, qp, qs, pos, sl, cup, tp, width, lp, n, pp,
+            self._dense("W_kvb", W_kvb, self._w_shape), self._scale(scale), qo,
+            self._heads("q_lat", q_lat, T, MLA_ROW), self._heads("o_lat", o_lat, T, MLA_KV), self._lse(lse, T),
+            self._heads("out", out, T, MLA_V), self._stream(stream))
+        if st != CFA_OK:
+            raise CfaError(st, "cfa_latent_layer")
         return out

@@ -12,6 +12,7 @@
 
 #include "cfa.h"
 #include "cfa_host.h"
+#include "cfa_host_util.h"
 #include "cfa_internal.h"
 #include "cfa_paged.h"
 #include "cfa_paged_split.h"
@@ -46,49 +47,15 @@ constexpr uint32_t kTimeoutNs = 2000000000u;  // 2 s per device-side wait
 
 cfa_status fail(cfa_status s) { return cfa::set_last_error(s); }
 
-bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
-bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return na && nb && x < y + nb && y < x + na;
-}
-
-// The plan's device is the current one for the length of a call.
-class OnDevice {
-  public:
-    explicit OnDevice(int device) {
-        if (cudaGetDevice(&was_) != cudaSuccess) was_ = -1;
-        ok_ = was_ == device || cudaSetDevice(device) == cudaSuccess;
-        if (was_ == device) was_ = -1;
-        if (!ok_) cudaGetLastError();
-    }
-    ~OnDevice() {
-        if (was_ >= 0) cudaSetDevice(was_);
-    }
-    bool ok() const { return ok_; }
-
-  private:
-    int was_ = -1;
-    bool ok_ = false;
-};
+using cfa::OnDevice;
+using cfa::Span;
+using cfa::aligned;
+using cfa::clear_words;
+using cfa::overlaps;
 
 cfa_status launch(const void *kernel, int grid, int threads, size_t smem, cudaStream_t stream,
                   void **args) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelExC(&cfg, kernel, args) != cudaSuccess) {
-        cudaGetLastError();
-        return CFA_ERR_CUDA;
-    }
-    return CFA_OK;
+    return cfa::launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), threads, smem, stream, args);
 }
 
 void paged_free(cfa_paged *p) {
@@ -100,12 +67,6 @@ void paged_free(cfa_paged *p) {
     p->plan_ws = nullptr;
     p->rec_o = nullptr;
     p->rec_ml = nullptr;
-}
-
-// Clears words of a plan. A memset may run after the call that asks for it has returned, and
-// streams that do not wait for the legacy one would launch on what the words held before.
-bool clear_words(unsigned *words, int n) {
-    return cudaMemset(words, 0, sizeof(unsigned) * n) == cudaSuccess && cudaStreamSynchronize(nullptr) == cudaSuccess;
 }
 
 // Rows of a cache of n_pages pages, or -1 where they pass the kernels' 32-bit
@@ -185,11 +146,6 @@ float scale_log2(const cfa_paged *p, float scale) {
     const double s = scale > 0.0f ? scale : 1.0 / std::sqrt(static_cast<double>(p->D));
     return static_cast<float>(s * 1.4426950408889634);
 }
-
-struct Span {
-    const void *at;
-    size_t n;
-};
 
 // Whether n bytes at `out` lie over the arrays that say what the batch is.
 bool over_batch(const cfa_paged *p, const AttnArgs &a, const void *out, size_t n) {
@@ -415,25 +371,11 @@ cfa_status cfa_paged_set_rope(cfa_paged *p, double theta, int rotary_dim, int in
         p->rd = 0;
         return CFA_OK;
     }
-    if (!(theta >= 1.0) || !std::isfinite(theta) || !(factor >= 1.0) || !std::isfinite(factor) ||
-        !(magnitude > 0.0) || !std::isfinite(magnitude) || magnitude > 1e6 ||
-        scaling < CFA_ROPE_PLAIN || scaling > CFA_ROPE_BY_PARTS)
-        return fail(CFA_ERR_INVALID_ARG);
-    if (scaling == CFA_ROPE_BY_PARTS &&
-        (!(low_turns >= 0.0) || !(high_turns > low_turns) || !std::isfinite(high_turns) || original_ctx < 1))
-        return fail(CFA_ERR_INVALID_ARG);
-    const double two_pi = 6.283185307179586476925287;
-    for (int i = 0; i < rotary_dim / 2; ++i) {
-        double f = std::pow(theta, -2.0 * i / rotary_dim);
-        if (scaling == CFA_ROPE_LINEAR) f /= factor;
-        if (scaling == CFA_ROPE_BY_PARTS) {
-            const double r = original_ctx * f / two_pi;
-            const double g = std::min(1.0, std::max(0.0, (r - low_turns) / (high_turns - low_turns)));
-            f = g * f + (1.0 - g) * f / factor;
-        }
-        // f <= 1, so below 1/6 of a turn: the product stays far below 2^64
-        p->turns[i] = static_cast<unsigned long long>(std::ldexp(f / two_pi, 64));
-    }
+    unsigned long long turns[64] = {};
+    const cfa_status st = cfa::rope_turns(theta, rotary_dim, scaling, factor, low_turns, high_turns, original_ctx,
+                                          magnitude, turns);
+    if (st != CFA_OK) return fail(st);
+    std::memcpy(p->turns, turns, sizeof turns);
     p->rd = rotary_dim;
     p->interleaved = interleaved ? 1 : 0;
     p->scaling = scaling;
