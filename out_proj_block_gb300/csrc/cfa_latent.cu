@@ -16,6 +16,7 @@
 #include "cfa_host_util.h"
 #include "cfa_internal.h"
 #include "cfa_latent.h"
+#include "cfa_latent_split.h"
 #include "cfa_paged.h"
 
 namespace cfa {
@@ -23,7 +24,9 @@ const void *latent_append_kernel_ptr(bool interleaved);
 const void *latent_fold_kernel_ptr();
 const void *latent_unfold_kernel_ptr();
 const void *latent_attention_kernel_ptr();
+const void *latent_merge_kernel_ptr();
 const void *latent_expanded_kernel_ptr();
+int latent_attention_smem();
 }  // namespace cfa
 
 struct cfa_latent {
@@ -33,7 +36,12 @@ struct cfa_latent {
     int rope = 0, interleaved = 0, scaling = CFA_ROPE_PLAIN;
     float magnitude = 1.0f;
     unsigned long long turns[cfa::kLatR / 2] = {};
+    // workspace
     unsigned *words = nullptr;  // [0] status
+    float *rec_o = nullptr;     // records of the attention's pieces
+    float2 *rec_ml = nullptr;
+    int4 *cuts = nullptr;
+    int runs = 0;
 };
 
 namespace {
@@ -55,8 +63,9 @@ constexpr uint32_t kTimeoutNs = 2000000000u;  // 2 s per device-side wait
 cfa_status fail(cfa_status s) { return cfa::set_last_error(s); }
 
 void latent_free(cfa_latent *p) {
-    if (p->words) cudaFree(p->words);
-    p->words = nullptr;
+    void *all[] = {p->words, p->rec_o, p->rec_ml, p->cuts};
+    for (void *a : all)
+        if (a) cudaFree(a);
 }
 
 // Rows of a cache of n_pages pages, or -1 where they pass the kernels' 32-bit row index.
@@ -212,8 +221,6 @@ cfa_status launch_unfold(cfa_latent *p, int T, const void *o, const void *w, voi
 
 cfa_status launch_attention(cfa_latent *p, const AttnArgs &a, void *stream) {
     cfa::LatentAttnParams kp{};
-    kp.q = static_cast<const uint16_t *>(a.q);
-    kp.pages = static_cast<const uint16_t *>(a.pages);
     kp.cu = a.cu;
     kp.lens = a.lens;
     kp.tables = a.tables;
@@ -228,9 +235,26 @@ cfa_status launch_attention(cfa_latent *p, const AttnArgs &a, void *stream) {
     kp.width = a.width;
     kp.scale_log2 = scale_log2(a.scale);
     kp.timeout_ns = kTimeoutNs;
-    void *args[1] = {&kp};
-    return launch(cfa::latent_attention_kernel_ptr(),
-                  dim3(static_cast<unsigned>(a.n_tokens), static_cast<unsigned>((p->nh + 7) / 8)), 256, 0, stream, args);
+    kp.rec_o = p->rec_o;
+    kp.rec_ml = p->rec_ml;
+    kp.cuts = p->cuts;
+    kp.runs = p->runs;
+    kp.by_H = cfa::FastDiv(static_cast<uint32_t>(p->nh));
+    kp.by_page = cfa::FastDiv(static_cast<uint32_t>(p->ps));
+    kp.box_rows = std::min(p->ps, 64);  // a box lies inside one page and divides 64 keys
+    CUtensorMap tq, tr;
+    if (cfa::encode_bf16_2d_ex(&tq, a.q, kLatRow, static_cast<uint64_t>(a.n_tokens) * p->nh, kLatRow, 64, 64, true) !=
+            CFA_OK ||
+        cfa::encode_bf16_2d_ex(&tr, a.pages, kLatRow, static_cast<uint64_t>(cache_rows(p, a.n_pages)), kLatRow, 64,
+                               static_cast<uint32_t>(kp.box_rows), true) != CFA_OK)
+        return CFA_ERR_CUDA;
+    void *args[3] = {&tq, &tr, &kp};
+    const cfa_status st = launch(cfa::latent_attention_kernel_ptr(), dim3(2u * static_cast<unsigned>(p->runs)),
+                                 cfa::kLatAttnThreads, static_cast<size_t>(cfa::latent_attention_smem()), stream, args);
+    if (st != CFA_OK) return st;
+    void *margs[1] = {&kp};
+    return launch(cfa::latent_merge_kernel_ptr(), dim3(cfa::kLatMergeBlocks, static_cast<unsigned>(p->runs)),
+                  cfa::kLatMergeThreads, 0, stream, margs);
 }
 
 }  // namespace
@@ -271,7 +295,14 @@ cfa_latent *cfa_latent_create(int max_seqs, int max_tokens, int n_heads, int pag
     p->ps = page_size;
     p->device = device;
     p->num_sms = sms;
-    if (cudaMalloc(&p->words, sizeof(unsigned)) != cudaSuccess || !clear_words(p->words, 1)) {
+    p->runs = sms / 2;
+    const size_t rec_rows = 2u * static_cast<size_t>(p->runs) * cfa::kLatTile;
+    if (cudaFuncSetAttribute(cfa::latent_attention_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             cfa::latent_attention_smem()) != cudaSuccess ||
+        cudaMalloc(&p->words, sizeof(unsigned)) != cudaSuccess || !clear_words(p->words, 1) ||
+        cudaMalloc(&p->rec_o, sizeof(float) * rec_rows * kLatC) != cudaSuccess ||
+        cudaMalloc(&p->rec_ml, sizeof(float2) * rec_rows) != cudaSuccess ||
+        cudaMalloc(&p->cuts, sizeof(int4) * static_cast<size_t>(p->runs)) != cudaSuccess) {
         cudaGetLastError();
         latent_free(p);
         delete p;
@@ -462,8 +493,10 @@ cfa_status cfa_latent_describe(const cfa_latent *p, char *buf, int len) {
     if (!p || !buf || len < 1) return fail(CFA_ERR_INVALID_ARG);
     std::snprintf(buf, static_cast<size_t>(len),
                   "{\"max_seqs\": %d, \"max_tokens\": %d, \"n_heads\": %d, \"page_size\": %d, \"rope\": %d, "
-                  "\"interleaved\": %d, \"scaling\": %d, \"num_sms\": %d}",
-                  p->max_seqs, p->max_tokens, p->nh, p->ps, p->rope, p->interleaved, p->scaling, p->num_sms);
+                  "\"interleaved\": %d, \"scaling\": %d, \"num_sms\": %d, \"runs\": %d, \"smem_bytes\": %d, "
+                  "\"workspace_bytes\": %lld}",
+                  p->max_seqs, p->max_tokens, p->nh, p->ps, p->rope, p->interleaved, p->scaling, p->num_sms, p->runs,
+                  cfa::latent_attention_smem(), 2ll * p->runs * cfa::kLatTile * (4 * kLatC + 8) + 16ll * p->runs);
     return CFA_OK;
 }
 

@@ -52,16 +52,29 @@ struct LatentHeadsParams {
 // ------------------------------------------------------- attention over rows
 
 struct LatentAttnParams {
-    const uint16_t *q;    // [T][H][576]
-    const uint16_t *pages;
-    const int *cu, *lens, *tables;
+    const int *cu;        // [B + 1]
+    const int *lens;      // [B]
+    const int *tables;    // [B][width]
     uint16_t *out;        // [T][H][512]
     float *lse;           // [T][H] or null
     unsigned *status;
+    float *rec_o;         // records, two a run: unnormalised outputs in 16-byte chunks [128][128 rows][4]
+    float2 *rec_ml;       // and each row's maximum (base 2) and sum
+    int4 *cuts;           // for the merge: the tile that each run's end cuts
     int T, B, H, page_size, n_pages, width;
+    int runs;             // clusters of the attention kernel
+    int box_rows;         // cache rows of one TMA box
+    FastDiv by_H, by_page;
     float scale_log2;     // scale * log2(e)
     uint32_t timeout_ns;
 };
+
+// four compute warps; a load warp for queries and keys and one for values, a relay, one that
+// issues the products (with a ninth warp an SM's quarter would hold three, of 168 registers a thread)
+constexpr int kLatLoadWarp = 4, kLatMmaWarp = 7;
+constexpr int kLatAttnThreads = 256;
+constexpr int kLatMergeThreads = 256;
+constexpr int kLatMergeBlocks = 16;  // blocks of the merge for one tile: a warp for 32 of its rows and 16 of 512 dims
 
 // ------------------------------------------- attention over expanded keys and values
 

@@ -8,10 +8,30 @@
 
 #include "cfa_device.cuh"
 #include "cfa_latent.h"
-#include "cfa_latent_attn.cuh"
 #include "cfa_tile.cuh"
 
 namespace cfa {
+
+// Offsets that are in order within [0, n]; by all threads of the block.
+__device__ __forceinline__ bool latent_offsets_ok(const int *cu, int B, int n) {
+    bool bad = false;
+    for (int b = threadIdx.x; b <= B; b += blockDim.x) {
+        const int c = __ldcg(cu + b), before = b > 0 ? __ldcg(cu + b - 1) : 0;
+        bad |= c < before || c > n;
+    }
+    return !__syncthreads_or(bad);
+}
+
+// The request of token t, or -1.
+__device__ __forceinline__ int latent_request(const int *cu, int B, int t) {
+    int lo = 0, hi = B;  // first request whose end is above t
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (__ldcg(cu + mid + 1) > t) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo < B && t >= __ldcg(cu + lo) ? lo : -1;
+}
 
 __global__ void __launch_bounds__(256) latent_expanded_kernel(const __grid_constant__ LatentExpandedParams p) {
     const int t = blockIdx.x, h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;

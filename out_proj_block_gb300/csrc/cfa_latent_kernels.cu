@@ -13,6 +13,8 @@ const void *latent_append_kernel_ptr(bool interleaved) {
 const void *latent_fold_kernel_ptr() { return reinterpret_cast<const void *>(&latent_fold_kernel); }
 const void *latent_unfold_kernel_ptr() { return reinterpret_cast<const void *>(&latent_unfold_kernel); }
 const void *latent_attention_kernel_ptr() { return reinterpret_cast<const void *>(&latent_attention_kernel); }
+const void *latent_merge_kernel_ptr() { return reinterpret_cast<const void *>(&latent_merge_kernel); }
+int latent_attention_smem() { return LatSmem::kBytes; }
 const void *latent_expanded_kernel_ptr() { return reinterpret_cast<const void *>(&latent_expanded_kernel); }
 
 }  // namespace cfa
