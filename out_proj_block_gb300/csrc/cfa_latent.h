@@ -74,7 +74,7 @@ struct LatentAttnParams {
 constexpr int kLatLoadWarp = 4, kLatMmaWarp = 7;
 constexpr int kLatAttnThreads = 256;
 constexpr int kLatMergeThreads = 256;
-constexpr int kLatMergeBlocks = 16;  // blocks of the merge for one tile: a warp for 32 of its rows and 16 of 512 dims
+constexpr int kLatMergeBlocks = 32;  // blocks of the merge for one tile: a warp for 32 of its rows and 8 of 512 dims
 
 // ------------------------------------------- attention over expanded keys and values
 

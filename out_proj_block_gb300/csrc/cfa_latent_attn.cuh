@@ -46,7 +46,10 @@
 namespace cfa {
 
 constexpr int kLatChunk = 64 * 128;        // 64 rows of 64 dims
-constexpr int kLatKSlots = 8, kLatVSlots = 4;
+// a block of keys takes three slots of three chunks of keys and two slots of four chunks of values
+// (both key halves of 128 dims): each wait, arrival and commit costs its warp 100 clocks or more, which slots of
+// single chunks could not hide (5000 clocks a block instead of NNNN)
+constexpr int kLatKSlots = 3, kLatKSlot = 3 * kLatChunk, kLatVSlots = 2, kLatVSlot = 4 * kLatChunk;
 constexpr int kLatQChunks = kLatRow / 64;  // 9
 constexpr int kLatShare = 1;                // least units of a run
 constexpr int kLatWarps = kLatAttnThreads / 32;
@@ -56,9 +59,9 @@ constexpr int kLatWarps = kLatAttnThreads / 32;
 struct LatSmem {
     static constexpr int kQ = 0;                                 // [9][64 rows][128 bytes]
     static constexpr int kP = kQ + kLatQChunks * kLatChunk;      // [2 key halves][64 rows][128 bytes]
-    static constexpr int kK = kP + 2 * kLatChunk;                // ring of chunks
-    static constexpr int kV = kK + kLatKSlots * kLatChunk;       // ring of pairs of chunks
-    static constexpr int kBars = kV + kLatVSlots * 2 * kLatChunk;
+    static constexpr int kK = kP + 2 * kLatChunk;                // ring of [3][64 keys][128 bytes]
+    static constexpr int kV = kK + kLatKSlots * kLatKSlot;       // ring of [2 key halves][2][64 keys][128 bytes]
+    static constexpr int kBars = kV + kLatVSlots * kLatVSlot;
     static constexpr int kFullK = kBars, kEmptyK = kFullK + 8 * kLatKSlots, kReadyK = kEmptyK + 8 * kLatKSlots;
     static constexpr int kFullV = kReadyK + 8 * kLatKSlots, kEmptyV = kFullV + 8 * kLatVSlots,
                          kReadyV = kEmptyV + 8 * kLatVSlots;
@@ -84,6 +87,13 @@ __device__ __forceinline__ void umma2_bf16(uint32_t d_tmem, uint64_t a_desc, uin
                  "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
                  :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
                  : "memory");
+}
+// Arrives on a barrier of either block (an address from map_to_rank). What it tells of are writes of the
+// asynchronous proxy, or ones that a proxy fence has put in front of it, to the arriving
+// block's own shared memory, which that block's own tensor core reads. The form that releases at cluster scope
+// takes 1100 clocks each time: 16,000 for a block of keys that should take 3000.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t remote_bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(remote_bar) : "memory");
 }
 // By one warp of each block.
 __device__ __forceinline__ void tmem2_alloc(uint32_t slot_smem_addr, uint32_t ncols) {
@@ -196,7 +206,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     auto next = [&]() { return walk.next(p.B, p.H, p.by_H, request); };
     const LatentPiece &x = walk.x;
     auto wait = [&](int bar, uint32_t parity, unsigned site) {
-        return bounded_wait([&]() { return mbar_try_wait_cluster(base + bar, parity); }, p.timeout_ns, timed_out,
+        return bounded_wait([&]() { return mbar_try_wait(base + bar, parity); }, p.timeout_ns, timed_out,
                             p.status, site);
     };
     // The same for a warp as a whole.
@@ -208,11 +218,12 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     if (warp == kLatLoadWarp || warp == kLatLoadWarp + 1) {
         // ------------------------------------------------ load warps: keys (and queries), values
         const bool values = warp != kLatLoadWarp;
-        const int box = p.box_rows, per_half = 64 / box;  // boxes of 64 keys
+        // boxes of 64 keys: 1, 2 or 4 (shifts: a division takes 150 clocks, and a chunk has no more than 350)
+        const int box = p.box_rows, bits = box == 64 ? 0 : box == 32 ? 1 : 2, per_half = 1 << bits;
         const int all_rows = p.n_pages * p.page_size;     // outside: reads as zeros
         uint32_t n = 0, pieces = 0;
         bool ok = true;
-        // Where box i of the piece's key halves from b0 on lies, 32 / per_half halves at a time: a lane a box.
+        // Where the boxes of the tile's 64-key halves lie is found 32 boxes at a time, a lane a box.
         while (ok && next()) {
             if (x.b0 == x.b1) continue;
             if (!values) {
@@ -230,12 +241,13 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             ++pieces;
             const int keys = seen_by_last();
             const int *table = p.tables + static_cast<size_t>(x.req) * p.width;
-            int rows = 0, cached = -1;  // this lane's box, of the halves from `cached` on
-            auto box_row = [&](int half, int i) {  // of 64-key half number `half` of the tile's rows
-                const int group = half / (32 / per_half);
+            int rows = 0, cached = -1;  // this lane's box, of group `cached`
+            // cache rows of a half's boxes
+            auto boxes = [&](int half, int (&y)[4]) {
+                const int group = half >> (5 - bits);
                 if (group != cached) {
                     cached = group;
-                    const int key = (group * (32 / per_half) + lane / per_half) * 64 + lane % per_half * box;
+                    const int key = (group * 32 + lane) * box;
                     rows = all_rows;
                     if (key < keys) {
                         const int pg = key / p.by_page, id = __ldcg(table + pg);
@@ -243,42 +255,50 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                         else atomicOr(p.status, kStatusBadPageBit);
                     }
                 }
-                return __shfl_sync(~0u, rows, (half % (32 / per_half)) * per_half + i);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = __shfl_sync(~0u, rows, ((half << bits) + i) & 31);
             };
             CFA_ROLLED for (int b = x.b0; ok && b < x.b1; ++b) {
                 if (!values) {
-                    CFA_ROLLED for (int c = 0; c < kLatQChunks; ++c, ++n) {
-                        const uint32_t slot = n % kLatKSlots, full = base + S::kFullK + 8 * slot;
-                        if (n >= kLatKSlots)
-                            ok = wait_warp(S::kEmptyK + 8 * slot, (n / kLatKSlots - 1) & 1, kSiteStageEmpty);
+                    int y[4];
+                    boxes(2 * b + rank, y);
+                    CFA_ROLLED for (int c = 0; c < kLatKSlots; ++c, ++n) {
+                        const int full = S::kFullK + 8 * c;
+                        if (n >= kLatKSlots) ok = wait_warp(S::kEmptyK + 8 * c, (n / kLatKSlots - 1) & 1, kSiteStageEmpty);
                         if (!ok) break;
-                        if (elect_one()) mbar_arrive_expect_tx(full, kLatChunk);
-                        __syncwarp();
-                        CFA_ROLLED for (int i = 0; i < per_half; ++i) {
-                            const int y = box_row(2 * b + rank, i);
-                            if (elect_one())
-                                tma_load_2d(base + S::kK + slot * kLatChunk + i * box * 128, &tm_rows, 64 * c, y, full);
-                            __syncwarp();
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(base + full, kLatKSlot);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (i >= per_half) break;
+#pragma unroll
+                                for (int k = 0; k < 3; ++k)
+                                    tma_load_2d(base + S::kK + c * kLatKSlot + k * kLatChunk + i * box * 128, &tm_rows,
+                                                64 * (3 * c + k), y[i], base + full);
+                            }
                         }
+                        __syncwarp();
                     }
                 } else {
-                    CFA_ROLLED for (int c = 0; c < 4; ++c, ++n) {  // (dims, keys): (0, 0), (0, 1), (1, 0), (1, 1)
-                        const uint32_t slot = n % kLatVSlots, full = base + S::kFullV + 8 * slot;
-                        if (n >= kLatVSlots)
-                            ok = wait_warp(S::kEmptyV + 8 * slot, (n / kLatVSlots - 1) & 1, kSiteStageEmpty);
+                    int y[2][4];
+                    boxes(2 * b, y[0]);
+                    boxes(2 * b + 1, y[1]);
+                    CFA_ROLLED for (int c = 0; c < kLatVSlots; ++c, ++n) {
+                        const int full = S::kFullV + 8 * c, dim = 256 * rank + 128 * c;
+                        if (n >= kLatVSlots) ok = wait_warp(S::kEmptyV + 8 * c, (n / kLatVSlots - 1) & 1, kSiteStageEmpty);
                         if (!ok) break;
-                        if (elect_one()) mbar_arrive_expect_tx(full, 2 * kLatChunk);
-                        __syncwarp();
-                        CFA_ROLLED for (int i = 0; i < per_half; ++i) {
-                            const int y = box_row(2 * b + (c & 1), i);
-                            if (elect_one()) {
-                                const uint32_t dst = base + S::kV + slot * 2 * kLatChunk + i * box * 128;
-                                const int dim = 256 * rank + 128 * (c >> 1);
-                                tma_load_2d(dst, &tm_rows, dim, y, full);
-                                tma_load_2d(dst + kLatChunk, &tm_rows, dim + 64, y, full);
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(base + full, kLatVSlot);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (i >= per_half) break;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    tma_load_2d(base + S::kV + c * kLatVSlot + k * kLatChunk + i * box * 128, &tm_rows,
+                                                dim + 64 * (k & 1), y[k >> 1][i], base + full);
                             }
-                            __syncwarp();
                         }
+                        __syncwarp();
                     }
                 }
             }
@@ -299,39 +319,39 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     } else if (warp == kLatLoadWarp + 2) {
         // ------------------------------------------------------------------- relay warp
         // in the order in which the products take them: queries, keys of a block ahead, values
-        uint32_t nk = 0, nv = 0, pieces = 0;
+        uint32_t nk = 0, nv = 0, pieces = 0;  // blocks and pieces so far
         const uint32_t ready_k = map_to_rank(base + S::kReadyK, 0), ready_v = map_to_rank(base + S::kReadyV, 0),
                        ready_q = map_to_rank(base + S::kReadyQ, 0);
         bool ok = true;
         auto keys = [&]() {
-            CFA_ROLLED for (int c = 0; ok && c < kLatQChunks; ++c, ++nk) {
-                const uint32_t slot = nk % kLatKSlots;
-                ok = wait_warp(S::kFullK + 8 * slot, (nk / kLatKSlots) & 1, kSiteStageFull);
-                if (ok && elect_one()) mbar_arrive_remote(ready_k + 8 * slot);
+            CFA_ROLLED for (int c = 0; ok && c < kLatKSlots; ++c) {
+                ok = wait_warp(S::kFullK + 8 * c, nk & 1, kSiteStageFull);
+                if (ok && elect_one()) mbar_arrive_pair(ready_k + 8 * c);
                 __syncwarp();
             }
+            ++nk;
         };
         while (ok && next()) {
             if (x.b0 == x.b1) continue;
             ok = wait_warp(S::kFullQ, pieces++ & 1, kSiteStageFull);
-            if (ok && elect_one()) mbar_arrive_remote(ready_q);
+            if (ok && elect_one()) mbar_arrive_pair(ready_q);
             __syncwarp();
             const int all = seen_by_last(), some = seen_by_first();
             keys();
-            CFA_ROLLED for (int b = x.b0; ok && b < x.b1; ++b) {
+            CFA_ROLLED for (int b = x.b0; ok && b < x.b1; ++b, ++nv) {
                 if (b + 1 < x.b1) keys();
-                CFA_ROLLED for (int c = 0; ok && c < 4; ++c, ++nv) {
-                    const uint32_t slot = nv % kLatVSlots;
-                    ok = wait_warp(S::kFullV + 8 * slot, (nv / kLatVSlots) & 1, kSiteStageFull);
-                    const int key0 = b * kLatKeys + 64 * (c & 1), begin = max(0, some - key0);
-                    if (ok && begin < 64) {
+                const int begin = max(0, some - b * kLatKeys);
+                CFA_ROLLED for (int c = 0; ok && c < kLatVSlots; ++c) {
+                    ok = wait_warp(S::kFullV + 8 * c, nv & 1, kSiteStageFull);
+                    if (ok && begin < kLatKeys) {
                         // keys from `some` on are not seen by every row, from `all` on by none
-                        uint8_t *v = smem + S::kV + slot * 2 * kLatChunk;
-                        CFA_ROLLED for (int i = lane; i < (64 - begin) * 16; i += 32) {
+                        uint8_t *v = smem + S::kV + c * kLatVSlot;
+                        CFA_ROLLED for (int i = lane; i < (kLatKeys - begin) * 16; i += 32) {
                             const int r = begin + (i >> 4);
-                            uint4 *at = reinterpret_cast<uint4 *>(v + ((i >> 3) & 1) * kLatChunk + r * 128 + ((i & 7) << 4));
+                            uint4 *at = reinterpret_cast<uint4 *>(v + ((r >> 6) * 2 + ((i >> 3) & 1)) * kLatChunk +
+                                                                  (r & 63) * 128 + ((i & 7) << 4));
                             uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                            if (key0 + r < all) {
+                            if (b * kLatKeys + r < all) {
                                 w = *at;
                                 const uint32_t f = odd_bf16x2(w.x), g = odd_bf16x2(w.y), h = odd_bf16x2(w.z), k = odd_bf16x2(w.w);
                                 if ((f | g | h | k) == 0u) continue;
@@ -342,7 +362,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                         fence_proxy_async_smem();
                         __syncwarp();
                     }
-                    if (ok && elect_one()) mbar_arrive_remote(ready_v + 8 * slot);
+                    if (ok && elect_one()) mbar_arrive_pair(ready_v + 8 * c);
                     __syncwarp();
                 }
             }
@@ -352,21 +372,21 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         if (rank == 0) {
             const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
             const uint32_t idesc_s = umma_idesc_bf16(128, 128, false, false), idesc_o = umma_idesc_bf16(128, 256, false, true);
-            uint32_t nk = 0, nv = 0, g = 0, pieces = 0;  // chunks, value slots, blocks, pieces so far
+            uint32_t g = 0, pieces = 0;  // blocks and pieces so far
             bool ok = true;
             auto scores = [&](uint32_t block, bool last) {
-                CFA_ROLLED for (int c = 0; ok && c < kLatQChunks; ++c, ++nk) {
-                    const uint32_t slot = nk % kLatKSlots;
-                    ok = wait_warp(S::kReadyK + 8 * slot, (nk / kLatKSlots) & 1, kSiteStageFull);
+                const uint64_t q0 = umma_smem_desc(base + S::kQ, 16, 1024), k0 = umma_smem_desc(base + S::kK, 16, 1024);
+                CFA_ROLLED for (int c = 0; ok && c < kLatKSlots; ++c) {
+                    ok = wait_warp(S::kReadyK + 8 * c, block & 1, kSiteStageFull);
                     tcgen05_fence_after();
                     if (ok && elect_one()) {
-                        const uint64_t a = umma_smem_desc(base + S::kQ + c * kLatChunk, 16, 1024);
-                        const uint64_t b = umma_smem_desc(base + S::kK + slot * kLatChunk, 16, 1024);
+                        const uint64_t a = q0 + c * (kLatKSlot >> 4), b = k0 + c * (kLatKSlot >> 4);
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            umma2_bf16(tm + 64 * (block & 1), a + 2 * ks, b + 2 * ks, idesc_s, c > 0 || ks > 0);
-                        umma2_commit(base + S::kEmptyK + 8 * slot);
-                        if (c == kLatQChunks - 1) {
+                        for (int ks = 0; ks < 12; ++ks)  // 32 bytes a step
+                            umma2_bf16(tm + 64 * (block & 1), a + (ks >> 2) * (kLatChunk >> 4) + 2 * (ks & 3),
+                                       b + (ks >> 2) * (kLatChunk >> 4) + 2 * (ks & 3), idesc_s, c > 0 || ks > 0);
+                        umma2_commit(base + S::kEmptyK + 8 * c);
+                        if (c == kLatKSlots - 1) {
                             umma2_commit(base + S::kScores + 8 * (block & 1));
                             if (last) umma2_commit(base + S::kEmptyQ);
                         }
@@ -382,19 +402,18 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 CFA_ROLLED for (int j = 0; ok && j < nb; ++j, ++g) {
                     if (j + 1 < nb) scores(g + 1, j + 2 == nb);
                     ok = ok && wait_warp(S::kWeights, g & 1, kSiteSoftmaxExchange);
-                    CFA_ROLLED for (int c = 0; ok && c < 4; ++c, ++nv) {
-                        const uint32_t slot = nv % kLatVSlots;
-                        ok = wait_warp(S::kReadyV + 8 * slot, (nv / kLatVSlots) & 1, kSiteStageFull);
+                    const uint64_t p0 = umma_smem_desc(base + S::kP, 16, 1024), v0 = umma_smem_desc(base + S::kV, kLatChunk, 1024);
+                    CFA_ROLLED for (int c = 0; ok && c < kLatVSlots; ++c) {
+                        ok = wait_warp(S::kReadyV + 8 * c, g & 1, kSiteStageFull);
                         tcgen05_fence_after();
                         if (ok && elect_one()) {
-                            const uint64_t a = umma_smem_desc(base + S::kP + (c & 1) * kLatChunk, 16, 1024);
-                            const uint64_t b = umma_smem_desc(base + S::kV + slot * 2 * kLatChunk, kLatChunk, 1024);
+                            const uint64_t v = v0 + c * (kLatVSlot >> 4);
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)  // 16 keys of 128 bytes a step
-                                umma2_bf16(tm + 128 + 128 * (c >> 1), a + 2 * ks, b + 128 * ks, idesc_o,
-                                           j > 0 || (c & 1) || ks > 0);
-                            umma2_commit(base + S::kEmptyV + 8 * slot);
-                            if (c == 3) umma2_commit(base + S::kSum);
+                            for (int ks = 0; ks < 8; ++ks)  // 16 keys of 128 bytes a step
+                                umma2_bf16(tm + 128 + 128 * c, p0 + (ks >> 2) * (kLatChunk >> 4) + 2 * (ks & 3),
+                                           v + (ks >> 2) * (2 * kLatChunk >> 4) + 128 * (ks & 3), idesc_o, j > 0 || ks > 0);
+                            umma2_commit(base + S::kEmptyV + 8 * c);
+                            if (c == kLatVSlots - 1) umma2_commit(base + S::kSum);
                         }
                         __syncwarp();
                     }
@@ -504,7 +523,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 fence_proxy_async_smem();
                 tcgen05_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(weights);
+                if (lane == 0) mbar_arrive_pair(weights);
             }
             // ---- the tile's results, or its record
             const bool any = x.b1 > x.b0, final = x.b0 == 0 && x.b1 == x.blocks, begins = x.b0 == 0;
@@ -580,43 +599,61 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
 }
 
 // Merges the records of the tiles that runs' ends cut: blockIdx.y is the run in which such a tile
-// begins; a warp takes 32 rows (a lane a row) and 16 of their dims.
+// begins; a warp takes 32 rows (a lane a row) and 8 of their dims, eight records at a time, so that their loads
+// are on their way together.
 __global__ void __launch_bounds__(kLatMergeThreads) latent_merge_kernel(const __grid_constant__ LatentAttnParams p) {
+    constexpr int N = 8, CH = 2;
     grid_dependency_wait();
     const int run = blockIdx.y, lane = threadIdx.x & 31;
     const int4 cut = __ldcg(p.cuts + run);  // rows, the first one's place, the tile's last run
     const int task = blockIdx.x * (kLatMergeThreads / 32) + (threadIdx.x >> 5);
-    const int row = task % (kLatTile / 32) * 32 + lane, chunk = task / (kLatTile / 32) * 4;
+    const int row = task % (kLatTile / 32) * 32 + lane, chunk = task / (kLatTile / 32) * CH;
     if (row < cut.x) {
         const float2 *ml = p.rec_ml + row;
         const float4 *o = reinterpret_cast<const float4 *>(p.rec_o) + static_cast<size_t>(chunk) * kLatTile + row;
         constexpr int kRec = kLatTile * (kLatC / 4);
         float m = -INFINITY, l = 0.f;
-        CFA_ROLLED for (int k = run; k <= cut.z; ++k) m = fmaxf(m, __ldcg(ml + (2 * k + (k == run)) * kLatTile).x);
-        const float f = m == -INFINITY ? 0.f : m;
-        float a[16] = {};
-#pragma unroll 2
-        for (int k = run; k <= cut.z; ++k) {
-            const int rec = 2 * k + (k == run);
-            const float2 s = __ldcg(ml + rec * kLatTile);
-            const float g = exp2_ftz(s.x - f);
-            l += g * s.y;
+        float a[4 * CH] = {};
+        CFA_ROLLED for (int k = run; k <= cut.z; k += N) {
+            float2 s[N];
+            float4 v[N][CH];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float4 v = __ldcg(o + static_cast<size_t>(rec) * kRec + c * kLatTile);
-                a[4 * c] += g * v.x; a[4 * c + 1] += g * v.y; a[4 * c + 2] += g * v.z; a[4 * c + 3] += g * v.w;
+            for (int i = 0; i < N; ++i) {
+                s[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) v[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k + i <= cut.z) {
+                    const int rec = 2 * (k + i) + (k + i == run);  // the first run's second record, the others' first
+                    s[i] = __ldcg(ml + rec * kLatTile);
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) v[i][c] = __ldcg(o + static_cast<size_t>(rec) * kRec + c * kLatTile);
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < N; ++i) top = fmaxf(top, s[i].x);
+            const float f = top == -INFINITY ? 0.f : top, g0 = exp2_ftz(m - f);
+            m = top;
+            l *= g0;
+#pragma unroll
+            for (int e = 0; e < 4 * CH; ++e) a[e] *= g0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float g = exp2_ftz(s[i].x - f);
+                l += g * s[i].y;
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    a[4 * c] += g * v[i][c].x; a[4 * c + 1] += g * v[i][c].y;
+                    a[4 * c + 2] += g * v[i][c].z; a[4 * c + 3] += g * v[i][c].w;
+                }
             }
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
         uint16_t *out = p.out + (static_cast<size_t>(cut.y) + row) * kLatC + 4 * chunk;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            *reinterpret_cast<uint4 *>(out + 8 * e) =
-                l == 0.f ? make_uint4(0u, 0u, 0u, 0u)
-                         : make_uint4(pack2_bf16_cvt(a[8 * e] * inv, a[8 * e + 1] * inv),
-                                      pack2_bf16_cvt(a[8 * e + 2] * inv, a[8 * e + 3] * inv),
-                                      pack2_bf16_cvt(a[8 * e + 4] * inv, a[8 * e + 5] * inv),
-                                      pack2_bf16_cvt(a[8 * e + 6] * inv, a[8 * e + 7] * inv));
+        static_assert(CH == 2, "16 bytes");
+        *reinterpret_cast<uint4 *>(out) = l == 0.f ? make_uint4(0u, 0u, 0u, 0u)
+                                                   : make_uint4(pack2_bf16_cvt(a[0] * inv, a[1] * inv), pack2_bf16_cvt(a[2] * inv, a[3] * inv),
+                                                                pack2_bf16_cvt(a[4] * inv, a[5] * inv), pack2_bf16_cvt(a[6] * inv, a[7] * inv));
         if (p.lse && chunk == 0) p.lse[static_cast<size_t>(cut.y) + row] = (m + log2f(l)) * 0.69314718055994531f;
     }
     grid_dependents_launch();
