@@ -224,6 +224,8 @@ cfa_status launch_attention(cfa_latent *p, const AttnArgs &a, void *stream) {
     kp.cu = a.cu;
     kp.lens = a.lens;
     kp.tables = a.tables;
+    kp.q = static_cast<const uint16_t *>(a.q);
+    kp.pages = static_cast<const uint16_t *>(a.pages);
     kp.out = static_cast<uint16_t *>(a.out);
     kp.lse = a.lse;
     kp.status = p->words;
@@ -253,7 +255,7 @@ cfa_status launch_attention(cfa_latent *p, const AttnArgs &a, void *stream) {
                                  cfa::kLatAttnThreads, static_cast<size_t>(cfa::latent_attention_smem()), stream, args);
     if (st != CFA_OK) return st;
     void *margs[1] = {&kp};
-    return launch(cfa::latent_merge_kernel_ptr(), dim3(cfa::kLatMergeBlocks, static_cast<unsigned>(p->runs)),
+    return launch(cfa::latent_merge_kernel_ptr(), dim3(3u * static_cast<unsigned>(p->num_sms)),
                   cfa::kLatMergeThreads, 0, stream, margs);
 }
 
@@ -295,7 +297,7 @@ cfa_latent *cfa_latent_create(int max_seqs, int max_tokens, int n_heads, int pag
     p->ps = page_size;
     p->device = device;
     p->num_sms = sms;
-    p->runs = sms / 2;
+    p->runs = std::min(sms / 2, cfa::kLatMaxRuns);
     const size_t rec_rows = 2u * static_cast<size_t>(p->runs) * cfa::kLatTile;
     if (cudaFuncSetAttribute(cfa::latent_attention_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              cfa::latent_attention_smem()) != cudaSuccess ||

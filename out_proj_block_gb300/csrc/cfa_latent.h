@@ -55,6 +55,7 @@ struct LatentAttnParams {
     const int *cu;        // [B + 1]
     const int *lens;      // [B]
     const int *tables;    // [B][width]
+    const uint16_t *q, *pages;  // [T][H][576], rows of 576 (but for prefetches, read by tensor maps)
     uint16_t *out;        // [T][H][512]
     float *lse;           // [T][H] or null
     unsigned *status;
@@ -74,7 +75,8 @@ struct LatentAttnParams {
 constexpr int kLatLoadWarp = 4, kLatMmaWarp = 7;
 constexpr int kLatAttnThreads = 256;
 constexpr int kLatMergeThreads = 256;
-constexpr int kLatMergeBlocks = 32;  // blocks of the merge for one tile: a warp for 32 of its rows and 8 of 512 dims
+constexpr int kLatMaxRuns = 256;     // a thread of the merge looks at a run
+static_assert(kLatMaxRuns <= kLatMergeThreads, "it does");
 
 // ------------------------------------------- attention over expanded keys and values
 

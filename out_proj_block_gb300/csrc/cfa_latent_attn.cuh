@@ -20,9 +20,9 @@
 // TMEM holds O (256 columns) and two S (64 each), so that the next block's scores run under this
 // one's softmax. Warps: four for the softmax (a thread for half the keys of a row), one to issue
 // the products, two to load keys and values (TMA boxes of 64 dims with 128-byte swizzle, each
-// inside one page), and one that passes on what has landed: the issuing block waits for both blocks'
-// copies, and values that some or all rows do not see are cleared before the product, because a masked
-// weight is 0 and 0 times NaN is NaN.
+// inside one page), and one that passes on what has landed, as the issuing block waits for both blocks' copies.
+// Values that some or all rows do not see are cleared before the product, by the compute warps: a masked
+// weight is 0, and 0 times NaN is NaN.
 //
 // Tiles are cut into runs of blocks of keys, one to a cluster (cfa_latent_split.h); what the
 // runs' ends cut leaves records, which a second kernel merges in the order of the runs, so results
@@ -51,6 +51,7 @@ constexpr int kLatChunk = 64 * 128;        // 64 rows of 64 dims
 // single chunks could not hide (5000 clocks a block instead of NNNN)
 constexpr int kLatKSlots = 3, kLatKSlot = 3 * kLatChunk, kLatVSlots = 2, kLatVSlot = 4 * kLatChunk;
 constexpr int kLatQChunks = kLatRow / 64;  // 9
+constexpr int kLatAhead = 3;                // blocks before a tile's end that the next one's data are asked for in L2
 constexpr int kLatShare = 1;                // least units of a run
 constexpr int kLatWarps = kLatAttnThreads / 32;
 
@@ -94,6 +95,10 @@ __device__ __forceinline__ void umma2_bf16(uint32_t d_tmem, uint64_t a_desc, uin
 // takes 1100 clocks each time: 16,000 for a block of keys that should take 3000.
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t remote_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(remote_bar) : "memory");
+}
+// Asks for contiguous bytes in L2 (address and size multiples of 16).
+__device__ __forceinline__ void bulk_prefetch_l2(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(src), "r"(bytes) : "memory");
 }
 // By one warp of each block.
 __device__ __forceinline__ void tmem2_alloc(uint32_t slot_smem_addr, uint32_t ncols) {
@@ -155,8 +160,9 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         auto more = [](int a, int b) { return min(a + b, kLatMaxUnits); };
         int units = 0;
         bool bad = false;
+        LatentRequest r{};  // (with no more requests than threads read once)
         CFA_ROLLED for (int b = first; b < last; ++b) {
-            LatentRequest r = request(b);
+            r = request(b);
             if (r.tok0 < 0 || r.n < 0 || r.n > p.T || r.tok0 > p.T - r.n) bad = true;
             else units = more(units, latent_units(r, p.H, p.by_H));
             if (blockIdx.x == 0) {
@@ -187,18 +193,22 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         int at = more(before, scan - units);
         if (u0 < u1 && u0 >= at && u0 < at + units) {
             int b = first;
-            CFA_ROLLED for (; b < last; ++b) {
-                const int c = latent_units(request(b), p.H, p.by_H);
+            CFA_ROLLED for (; per > 1 && b < last; ++b) {
+                r = request(b);
+                const int c = latent_units(r, p.H, p.by_H);
                 if (u0 < at + c) break;
                 at += c;
             }
             misc[2] = b;
             misc[3] = at;
+            misc[5] = r.tok0;
+            misc[6] = r.n;
+            misc[7] = r.len;
         }
         if (tid == 0) misc[4] = share;
         __syncthreads();
         tcgen05_fence_after();
-        walk.begin(u0, misc[2] < 0 ? u0 : u1, misc[2], misc[3], p.H, p.by_H, request);
+        walk.begin(u0, misc[2] < 0 ? u0 : u1, misc[2], LatentRequest{misc[5], misc[6], misc[7]}, misc[3], p.H, p.by_H);
     }
     grid_dependents_launch();
     cluster_wait();
@@ -211,9 +221,8 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     };
     // The same for a warp as a whole.
     auto wait_warp = [&](int bar, uint32_t parity, unsigned site) { return __all_sync(~0u, wait(bar, parity, site)); };
-    // cache rows that the last token of the piece's tile sees, and the first
+    // cache rows that the last token of the piece's tile sees
     auto seen_by_last = [&]() { return latent_visible(x.r, min(x.r.n - 1, (x.tile * kLatTile + kLatTile - 1) / p.by_H)); };
-    auto seen_by_first = [&]() { return latent_visible(x.r, (x.tile * kLatTile) / p.by_H); };
 
     if (warp == kLatLoadWarp || warp == kLatLoadWarp + 1) {
         // ------------------------------------------------ load warps: keys (and queries), values
@@ -223,26 +232,16 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const int all_rows = p.n_pages * p.page_size;     // outside: reads as zeros
         uint32_t n = 0, pieces = 0;
         bool ok = true;
+        auto first_row = [&](const LatentPiece &z) {  // of this block's queries
+            return z.r.tok0 * p.H + z.tile * kLatTile + rank * latent_split(latent_rows(z.r, p.H, z.tile));
+        };
         // Where the boxes of the tile's 64-key halves lie is found 32 boxes at a time, a lane a box.
         while (ok && next()) {
             if (x.b0 == x.b1) continue;
-            if (!values) {
-                if (pieces > 0) ok = wait_warp(S::kEmptyQ, (pieces - 1) & 1, kSiteStageEmpty);
-                if (!ok) break;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(base + S::kFullQ, kLatQChunks * kLatChunk);
-                    const int row = x.r.tok0 * p.H + x.tile * kLatTile + 64 * rank;
-#pragma unroll 1
-                    for (int c = 0; c < kLatQChunks; ++c)
-                        tma_load_2d(base + S::kQ + c * kLatChunk, &tm_q, 64 * c, row, base + S::kFullQ);
-                }
-                __syncwarp();
-            }
-            ++pieces;
             const int keys = seen_by_last();
             const int *table = p.tables + static_cast<size_t>(x.req) * p.width;
             int rows = 0, cached = -1;  // this lane's box, of group `cached`
-            // cache rows of a half's boxes
+            // cache rows of a 64-key half's boxes
             auto boxes = [&](int half, int (&y)[4]) {
                 const int group = half >> (5 - bits);
                 if (group != cached) {
@@ -276,6 +275,36 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                                     tma_load_2d(base + S::kK + c * kLatKSlot + k * kLatChunk + i * box * 128, &tm_rows,
                                                 64 * (3 * c + k), y[i], base + full);
                             }
+                        }
+                        __syncwarp();
+                    }
+                    if (b == x.b0 && ok) {  // (behind the keys: the last tile's scores free them first)
+                        if (pieces > 0) ok = wait_warp(S::kEmptyQ, (pieces - 1) & 1, kSiteStageEmpty);
+                        if (!ok) break;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(base + S::kFullQ, kLatQChunks * kLatChunk);
+#pragma unroll 1
+                            for (int c = 0; c < kLatQChunks; ++c)
+                                tma_load_2d(base + S::kQ + c * kLatChunk, &tm_q, 64 * c, first_row(x), base + S::kFullQ);
+                        }
+                        __syncwarp();
+                        ++pieces;
+                    }
+                    if (b == max(x.b0, x.b1 - kLatAhead)) {
+                        // the next tile's queries and first keys, in L2 by the time they are loaded
+                        LatentWalk peek = walk;
+                        if (peek.next(p.B, p.H, p.by_H, request) && peek.x.b0 < peek.x.b1) {
+                            const LatentPiece &z = peek.x;
+                            const int key = (2 * z.b0 + rank) * 64 + lane * box;
+                            if (lane < per_half && key < latent_visible(z.r, z.r.n - 1)) {
+                                const int pg = key / p.by_page, id = __ldcg(p.tables + static_cast<size_t>(z.req) * p.width + pg);
+                                if (id >= 0 && id < p.n_pages)
+                                    bulk_prefetch_l2(p.pages + (static_cast<size_t>(id) * p.page_size + key - pg * p.page_size) * kLatRow,
+                                                     static_cast<uint32_t>(box) * kLatRow * 2);
+                            }
+                            const int rows = min(64, latent_rows(z.r, p.H, z.tile) - rank * latent_split(latent_rows(z.r, p.H, z.tile)));
+                            if (lane == 31 && rows > 0)
+                                bulk_prefetch_l2(p.q + static_cast<size_t>(first_row(z)) * kLatRow, static_cast<uint32_t>(rows) * kLatRow * 2);
                         }
                         __syncwarp();
                     }
@@ -336,32 +365,11 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             ok = wait_warp(S::kFullQ, pieces++ & 1, kSiteStageFull);
             if (ok && elect_one()) mbar_arrive_pair(ready_q);
             __syncwarp();
-            const int all = seen_by_last(), some = seen_by_first();
             keys();
             CFA_ROLLED for (int b = x.b0; ok && b < x.b1; ++b, ++nv) {
                 if (b + 1 < x.b1) keys();
-                const int begin = max(0, some - b * kLatKeys);
                 CFA_ROLLED for (int c = 0; ok && c < kLatVSlots; ++c) {
                     ok = wait_warp(S::kFullV + 8 * c, nv & 1, kSiteStageFull);
-                    if (ok && begin < kLatKeys) {
-                        // keys from `some` on are not seen by every row, from `all` on by none
-                        uint8_t *v = smem + S::kV + c * kLatVSlot;
-                        CFA_ROLLED for (int i = lane; i < (kLatKeys - begin) * 16; i += 32) {
-                            const int r = begin + (i >> 4);
-                            uint4 *at = reinterpret_cast<uint4 *>(v + ((r >> 6) * 2 + ((i >> 3) & 1)) * kLatChunk +
-                                                                  (r & 63) * 128 + ((i & 7) << 4));
-                            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                            if (b * kLatKeys + r < all) {
-                                w = *at;
-                                const uint32_t f = odd_bf16x2(w.x), g = odd_bf16x2(w.y), h = odd_bf16x2(w.z), k = odd_bf16x2(w.w);
-                                if ((f | g | h | k) == 0u) continue;
-                                w = make_uint4(w.x & ~f, w.y & ~g, w.z & ~h, w.w & ~k);
-                            }
-                            *at = w;
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
                     if (ok && elect_one()) mbar_arrive_pair(ready_v + 8 * c);
                     __syncwarp();
                 }
@@ -439,14 +447,19 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         int4 cut = make_int4(0, 0, 0, 0);  // the tile that the run's end cuts, for the merge
         // the other half of a row's thread, 64 threads on
         auto meet = [&]() { compute_bar<128>(); };
-        while (next()) {
-            const int in_request = x.tile * kLatTile + 64 * rank + row;  // the query row
-            const int all = x.r.n * p.H;
-            const bool live = in_request < all;
-            const bool warp_live = in_request - lane < all;
-            const int see = live ? latent_visible(x.r, in_request / p.by_H) : 0;
+        bool more = next();
+        while (more) {
+            const LatentPiece z = x;
+            const int tile_rows = latent_rows(z.r, p.H, z.tile), split = latent_split(tile_rows);
+            const int here = rank ? tile_rows - split : split;         // rows of this block
+            const int in_tile = rank * split + row;
+            const int in_request = z.tile * kLatTile + in_tile;        // the query row
+            const bool live = row < here, warp_live = row - lane < here;
+            const int see = live ? latent_visible(z.r, in_request / p.by_H) : 0;
+            const int some = latent_visible(z.r, (z.tile * kLatTile) / p.by_H);  // keys that every row sees
+            const int all = latent_visible(z.r, (z.tile * kLatTile + tile_rows - 1) / p.by_H);  // and any
             float m = -INFINITY, l = 0.f;
-            CFA_ROLLED for (int b = x.b0; b < x.b1; ++b, ++g) {
+            CFA_ROLLED for (int b = z.b0; b < z.b1; ++b, ++g) {
                 wait(S::kScores + 8 * (g & 1), (g >> 1) & 1, kSiteSoftmaxExchange);
                 __syncwarp();
                 tcgen05_fence_after();
@@ -501,7 +514,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 __syncwarp();
                 tcgen05_fence_after();
                 if (warp_live) {
-                    if (raise && b > x.b0) {
+                    if (raise && b > z.b0) {
 #pragma unroll 1
                         for (int c = 0; c < 256; c += 32) {
                             uint32_t v[32];
@@ -520,13 +533,35 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                         *reinterpret_cast<uint4 *>(to + ((c ^ (row & 7)) << 4)) =
                             make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
                 }
+                if (some < (b + 1) * kLatKeys) {
+                    // keys from `some` on are not seen by every row, from `all` on by none: what is not
+                    // finite of the first, and all of the others, becomes 0
+                    CFA_ROLLED for (int c = 0; c < kLatVSlots; ++c) {
+                        wait(S::kFullV + 8 * c, g & 1, kSiteStageFull);
+                        __syncwarp();
+                        uint8_t *v = smem + S::kV + c * kLatVSlot + ((tid >> 3) & 1) * kLatChunk + ((tid & 7) << 4);
+                        // (of a row's 16-byte chunks any order will do; the key halves lie 2 chunks apart)
+                        CFA_ROLLED for (int r = max(0, some - b * kLatKeys) + (tid >> 4); r < kLatKeys; r += 8) {
+                            uint4 *at = reinterpret_cast<uint4 *>(v + r * 128 + (r >> 6) * kLatChunk);
+                            uint4 d = make_uint4(0u, 0u, 0u, 0u);
+                            if (b * kLatKeys + r < all) {
+                                d = *at;
+                                const uint32_t f = odd_bf16x2(d.x), h = odd_bf16x2(d.y), i = odd_bf16x2(d.z), k = odd_bf16x2(d.w);
+                                if ((f | h | i | k) == 0u) continue;
+                                d = make_uint4(d.x & ~f, d.y & ~h, d.z & ~i, d.w & ~k);
+                            }
+                            *at = d;
+                        }
+                    }
+                }
                 fence_proxy_async_smem();
                 tcgen05_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_pair(weights);
             }
             // ---- the tile's results, or its record
-            const bool any = x.b1 > x.b0, final = x.b0 == 0 && x.b1 == x.blocks, begins = x.b0 == 0;
+            const bool any = z.b1 > z.b0, final = z.b0 == 0 && z.b1 == z.blocks, begins = z.b0 == 0;
+            more = next();  // (its loads are on their way meanwhile)
             if (any) wait(S::kSum, (g - 1) & 1, kSiteKvExchange);
             __syncwarp();
             tcgen05_fence_after();
@@ -535,53 +570,61 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             meet();
             l += sums[64 * (half ^ 1) + row];
             meet();  // the next block's maxima go to the same place
-            const long long out_row = static_cast<long long>(x.r.tok0) * p.H + in_request;
-            const int rec = 2 * run + (begins ? 1 : 0);
-            float *rec_o = p.rec_o + static_cast<size_t>(rec) * kLatTile * kLatC;
-            if (!final && begins && rank == 0 && tid == 0) {
-                const int share = misc[4], tile_rows = min(kLatTile, all - x.tile * kLatTile);
-                cut = make_int4(tile_rows, static_cast<int>(out_row), (x.unit + x.blocks + kLatItem - 1) / share, 0);
-            }
-            if (warp_live) {
-                if (half == 0 && live) {
-                    if (!final) p.rec_ml[rec * kLatTile + 64 * rank + row] = make_float2(m, l);
-                    else if (p.lse) p.lse[out_row] = (m + log2f(l)) * 0.69314718055994531f;
-                }
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+            const long long tile_row = static_cast<long long>(z.r.tok0) * p.H + z.tile * kLatTile;
+            const long long out_row = tile_row + in_tile;
+            const int row_group = row - lane;  // the warp's first row
+            if (!final && begins && rank == 0 && tid == 0)
+                cut = make_int4(tile_rows, static_cast<int>(tile_row), (z.unit + z.blocks + kLatItem - 1) / misc[4], 0);
+            if (!warp_live) continue;
+            if (!final) {
+                // a piece's record: the run's second where the tile begins in it, else its first
+                const int rec = 2 * run + (begins ? 1 : 0);
+                if (half == 0 && live) p.rec_ml[rec * kLatTile + in_tile] = make_float2(m, l);
+                float *rec_o = p.rec_o + static_cast<size_t>(rec) * kLatTile * kLatC + 4 * in_tile;
 #pragma unroll 1
                 for (int c = 0; c < 256; c += 32) {
                     uint32_t v[32];
                     __syncwarp();
+                    tmem_ld_x32(tmem + lanes + 128 + c, v);
+                    tmem_wait_ld();
+                    if (!live) continue;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<uint4 *>(rec_o + static_cast<size_t>(64 * half + c / 4 + e) * (4 * kLatTile)) =
+                            make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                }
+            } else {
+                if (p.lse && half == 0 && live) p.lse[out_row] = (m + log2f(l)) * 0.69314718055994531f;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                // through the warp's rows of P (32 of 128 bytes), so that a row's 128 bytes are written
+                // together: a thread's own 16 bytes, in 32 rows at once, take a transaction each
+                uint8_t *stage = smem + S::kP + half * kLatChunk + row_group * 128;
+#pragma unroll 1
+                for (int c = 0; c < 256; c += 32) {
+                    uint32_t v[32];
+                    float f[32];
+                    __syncwarp();
                     if (any) {
                         tmem_ld_x32(tmem + lanes + 128 + c, v);
                         tmem_wait_ld();
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = 0u;
                     }
-                    if (!live) continue;
-                    float f[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
-                    const int dim = 256 * half + c;
-                    if (final) {
-                        if (see == 0) {
+                    for (int e = 0; e < 32; ++e) f[e] = see > 0 ? __uint_as_float(v[e]) * inv : 0.f;
+                    const int at = c / 8 & 7;  // 16-byte chunks of the staged 128
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) f[e] = 0.f;
-                        }
-                        uint16_t *out = p.out + static_cast<size_t>(out_row) * kLatC + dim;
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4 *>(stage + lane * 128 + (((at + e) ^ (lane & 7)) << 4)) =
+                            make_uint4(pack2_bf16_cvt(f[8 * e], f[8 * e + 1]), pack2_bf16_cvt(f[8 * e + 2], f[8 * e + 3]),
+                                       pack2_bf16_cvt(f[8 * e + 4], f[8 * e + 5]), pack2_bf16_cvt(f[8 * e + 6], f[8 * e + 7]));
+                    if ((c & 32) == 0) continue;
+                    __syncwarp();
+                    uint16_t *out = p.out + (out_row - lane) * kLatC + 256 * half + (c - 32) + 8 * (lane & 7);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            *reinterpret_cast<uint4 *>(out + 8 * e) =
-                                make_uint4(pack2_bf16_cvt(f[8 * e] * inv, f[8 * e + 1] * inv),
-                                           pack2_bf16_cvt(f[8 * e + 2] * inv, f[8 * e + 3] * inv),
-                                           pack2_bf16_cvt(f[8 * e + 4] * inv, f[8 * e + 5] * inv),
-                                           pack2_bf16_cvt(f[8 * e + 6] * inv, f[8 * e + 7] * inv));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<float4 *>(rec_o + (static_cast<size_t>(dim / 4 + e) * kLatTile + 64 * rank + row) * 4) =
-                                make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = 4 * e + (lane >> 3);
+                        if (row_group + r < here)
+                            *reinterpret_cast<uint4 *>(out + r * kLatC) =
+                                *reinterpret_cast<const uint4 *>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
                     }
                 }
             }
@@ -598,62 +641,104 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     }
 }
 
-// Merges the records of the tiles that runs' ends cut: blockIdx.y is the run in which such a tile
-// begins; a warp takes 32 rows (a lane a row) and 8 of their dims, eight records at a time, so that their loads
-// are on their way together.
-__global__ void __launch_bounds__(kLatMergeThreads) latent_merge_kernel(const __grid_constant__ LatentAttnParams p) {
-    constexpr int N = 8, CH = 2;
+// Merges the records of the tiles that runs' ends cut. A warp takes 32 rows (a lane a row) of a tile, and 16 of
+// their dims where the tile has two pieces, 4 where it has more, whose records are read eight at a time: what
+// counts is that enough loads are on their way.
+__global__ void __launch_bounds__(kLatMergeThreads, 3) latent_merge_kernel(const __grid_constant__ LatentAttnParams p) {
+    constexpr int kWarps = kLatMergeThreads / 32, kRec = kLatTile * (kLatC / 4);
+    __shared__ int4 cuts[kLatMergeThreads];
+    __shared__ int before[kLatMergeThreads + 1], sums[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();
-    const int run = blockIdx.y, lane = threadIdx.x & 31;
-    const int4 cut = __ldcg(p.cuts + run);  // rows, the first one's place, the tile's last run
-    const int task = blockIdx.x * (kLatMergeThreads / 32) + (threadIdx.x >> 5);
-    const int row = task % (kLatTile / 32) * 32 + lane, chunk = task / (kLatTile / 32) * CH;
-    if (row < cut.x) {
+    // every block lists the tasks: a run's tile, by rows and dims
+    int4 cut = make_int4(0, 0, 0, 0);  // rows, the first one's place, the tile's last run
+    if (tid < p.runs) cut = __ldcg(p.cuts + tid);
+    const int tasks = (cut.x + 31) / 32 * (cut.z == tid + 1 ? kLatC / 16 : kLatC / 4);
+    int scan = tasks;
+    CFA_ROLLED for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(~0u, scan, o);
+        if (lane >= o) scan += v;
+    }
+    if (lane == 31) sums[warp] = scan;
+    cuts[tid] = cut;
+    __syncthreads();
+    CFA_ROLLED for (int w = 0; w < warp; ++w) scan += sums[w];
+    before[tid + 1] = scan;
+    if (tid == 0) before[0] = 0;
+    __syncthreads();
+    const int all = before[kLatMergeThreads];
+    CFA_ROLLED for (int task = static_cast<int>(blockIdx.x) * kWarps + warp; task < all; task += static_cast<int>(gridDim.x) * kWarps) {
+        int lo = 0, hi = kLatMergeThreads;  // the last run whose tasks begin no later
+        CFA_ROLLED while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (before[mid] <= task) lo = mid;
+            else hi = mid;
+        }
+        cut = cuts[lo];
+        const int run = lo, last = cut.z, groups = (cut.x + 31) / 32, at = task - before[lo];
+        const bool two = last == run + 1;
+        const int row = at % groups * 32 + lane, chunk = at / groups * (two ? 4 : 1);
+        if (row >= cut.x) continue;
         const float2 *ml = p.rec_ml + row;
         const float4 *o = reinterpret_cast<const float4 *>(p.rec_o) + static_cast<size_t>(chunk) * kLatTile + row;
-        constexpr int kRec = kLatTile * (kLatC / 4);
-        float m = -INFINITY, l = 0.f;
-        float a[4 * CH] = {};
-        CFA_ROLLED for (int k = run; k <= cut.z; k += N) {
-            float2 s[N];
-            float4 v[N][CH];
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                s[i] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-                for (int c = 0; c < CH; ++c) v[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (k + i <= cut.z) {
-                    const int rec = 2 * (k + i) + (k + i == run);  // the first run's second record, the others' first
-                    s[i] = __ldcg(ml + rec * kLatTile);
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) v[i][c] = __ldcg(o + static_cast<size_t>(rec) * kRec + c * kLatTile);
-                }
-            }
-            float top = m;
-#pragma unroll
-            for (int i = 0; i < N; ++i) top = fmaxf(top, s[i].x);
-            const float f = top == -INFINITY ? 0.f : top, g0 = exp2_ftz(m - f);
-            m = top;
-            l *= g0;
-#pragma unroll
-            for (int e = 0; e < 4 * CH; ++e) a[e] *= g0;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float g = exp2_ftz(s[i].x - f);
-                l += g * s[i].y;
-#pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    a[4 * c] += g * v[i][c].x; a[4 * c + 1] += g * v[i][c].y;
-                    a[4 * c + 2] += g * v[i][c].z; a[4 * c + 3] += g * v[i][c].w;
-                }
-            }
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
         uint16_t *out = p.out + (static_cast<size_t>(cut.y) + row) * kLatC + 4 * chunk;
-        static_assert(CH == 2, "16 bytes");
-        *reinterpret_cast<uint4 *>(out) = l == 0.f ? make_uint4(0u, 0u, 0u, 0u)
-                                                   : make_uint4(pack2_bf16_cvt(a[0] * inv, a[1] * inv), pack2_bf16_cvt(a[2] * inv, a[3] * inv),
-                                                                pack2_bf16_cvt(a[4] * inv, a[5] * inv), pack2_bf16_cvt(a[6] * inv, a[7] * inv));
+        float m = -INFINITY, l = 0.f;
+        if (two) {
+            const int r0 = 2 * run + 1, r1 = 2 * run + 2;
+            const float2 s0 = __ldcg(ml + r0 * kLatTile), s1 = __ldcg(ml + r1 * kLatTile);
+            float4 v[2][4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                v[0][c] = __ldcg(o + static_cast<size_t>(r0) * kRec + c * kLatTile);
+                v[1][c] = __ldcg(o + static_cast<size_t>(r1) * kRec + c * kLatTile);
+            }
+            m = fmaxf(s0.x, s1.x);
+            const float f = m == -INFINITY ? 0.f : m, g0 = exp2_ftz(s0.x - f), g1 = exp2_ftz(s1.x - f);
+            l = g0 * s0.y + g1 * s1.y;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            uint32_t w[8];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                w[2 * c] = pack2_bf16_cvt((g0 * v[0][c].x + g1 * v[1][c].x) * inv, (g0 * v[0][c].y + g1 * v[1][c].y) * inv);
+                w[2 * c + 1] = pack2_bf16_cvt((g0 * v[0][c].z + g1 * v[1][c].z) * inv, (g0 * v[0][c].w + g1 * v[1][c].w) * inv);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                *reinterpret_cast<uint4 *>(out + 8 * c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        } else {
+            constexpr int N = 8;
+            float a[4] = {};
+            CFA_ROLLED for (int k = run; k <= last; k += N) {
+                float2 s[N];
+                float4 v[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    s[i] = make_float2(-INFINITY, 0.f);
+                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k + i <= last) {
+                        const int rec = 2 * (k + i) + (k + i == run);  // the first run's second record, the others' first
+                        s[i] = __ldcg(ml + rec * kLatTile);
+                        v[i] = __ldcg(o + static_cast<size_t>(rec) * kRec);
+                    }
+                }
+                float top = m;
+#pragma unroll
+                for (int i = 0; i < N; ++i) top = fmaxf(top, s[i].x);
+                const float f = top == -INFINITY ? 0.f : top, g0 = exp2_ftz(m - f);
+                m = top;
+                l *= g0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a[e] *= g0;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float g = exp2_ftz(s[i].x - f);
+                    l += g * s[i].y;
+                    a[0] += g * v[i].x; a[1] += g * v[i].y; a[2] += g * v[i].z; a[3] += g * v[i].w;
+                }
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            *reinterpret_cast<uint2 *>(out) = make_uint2(pack2_bf16_cvt(a[0] * inv, a[1] * inv), pack2_bf16_cvt(a[2] * inv, a[3] * inv));
+        }
         if (p.lse && chunk == 0) p.lse[static_cast<size_t>(cut.y) + row] = (m + log2f(l)) * 0.69314718055994531f;
     }
     grid_dependents_launch();

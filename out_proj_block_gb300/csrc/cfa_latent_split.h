@@ -28,6 +28,11 @@ CFA_HD int latent_visible(const LatentRequest &r, int i) {
     return paged_max(0, paged_min(r.len, r.len - r.n + i + 1));
 }
 
+// Rows of a tile, and how many of them the first block of a cluster takes: half, so that few rows are
+// spread over both.
+CFA_HD int latent_rows(const LatentRequest &r, int H, int tile) { return paged_min(kLatTile, r.n * H - tile * kLatTile); }
+CFA_HD int latent_split(int rows) { return (rows + 1) / 2; }
+
 CFA_HD int latent_tiles(int n, int H) { return (n * H + kLatTile - 1) / kLatTile; }
 
 // Blocks of a tile: those its last token sees.
@@ -75,15 +80,14 @@ struct LatentWalk {
     LatentPiece x;
     bool fresh;  // the piece that x holds has not been given out
 
-    // At the run's begin: request b's first unit is `unit`, and u0 lies in it or before it.
-    template <typename Request>
-    CFA_HD void begin(int from, int to, int b, int unit, int H, const FastDiv &by_H, const Request &request) {
+    // At the run's begin, which lies in request b, r, whose first unit is `unit`.
+    CFA_HD void begin(int from, int to, int b, const LatentRequest &r, int unit, int H, const FastDiv &by_H) {
         u0 = from;
         u1 = to;
         fresh = false;
         if (u0 >= u1) return;
         x.req = b;
-        x.r = request(b);
+        x.r = r;
         x.tile = 0;
         x.unit = unit;
         fresh = true;

@@ -48,12 +48,14 @@ int check(const std::vector<LatentRequest> &reqs, int H, int runs, int least) {
         int b = 0;
         while (b < B && first[b + 1] <= u0) ++b;
         if (u0 < u1 && b >= B) return failed("start", run, u0, u1);
-        w.begin(u0, u1, b < B ? b : 0, b < B ? first[b] : 0, H, by_H, request);
+        w.begin(u0, u1, b < B ? b : 0, reqs[b < B ? b : 0], b < B ? first[b] : 0, H, by_H);
         int cut = 0, went_on = 0;
         while (w.next(B, H, by_H, request)) {
             const LatentPiece &x = w.x;
             Tile &t = seen[{x.req, x.tile}];
-            const int blocks = latent_blocks(reqs[x.req], by_H, x.tile);
+            const int blocks = latent_blocks(reqs[x.req], by_H, x.tile), rows = latent_rows(x.r, H, x.tile);
+            if (rows < 1 || rows > kLatTile || latent_split(rows) > 64 || rows - latent_split(rows) > 64)
+                return failed("rows", run, x.req, rows);
             if (x.blocks != blocks || x.tile >= tiles[x.req]) return failed("piece", run, x.req, x.tile);
             if (x.b0 == x.b1) {
                 ++t.zeros;
