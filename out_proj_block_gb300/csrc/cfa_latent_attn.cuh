@@ -51,8 +51,9 @@ constexpr int kLatChunk = 64 * 128;        // 64 rows of 64 dims
 // single chunks could not hide (5000 clocks a block instead of NNNN)
 constexpr int kLatKSlots = 3, kLatKSlot = 3 * kLatChunk, kLatVSlots = 2, kLatVSlot = 4 * kLatChunk;
 constexpr int kLatQChunks = kLatRow / 64;  // 9
-constexpr int kLatAhead = 3;                // blocks before a tile's end that the next one's data are asked for in L2
-constexpr int kLatShare = 1;                // least units of a run
+constexpr int kLatAhead = 1;                // blocks of keys that are asked for in L2 ahead of their copies
+constexpr int kLatPeek = 3;                 // blocks before a tile's end that the next one's data are
+constexpr int kLatShare = 2;                // least units of a run
 constexpr int kLatWarps = kLatAttnThreads / 32;
 
 // Shared memory, the same in both blocks of a cluster (an instruction that spans them has one
@@ -179,7 +180,8 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         if (tid == 0) misc[2] = -1;
         const bool refused = __syncthreads_or(bad) != 0;
         int before = 0, all = 0;
-        CFA_ROLLED for (int w = 0; w < kLatWarps; ++w) {
+#pragma unroll
+        for (int w = 0; w < kLatWarps; ++w) {
             if (w < warp) before = more(before, sums[w]);
             all = more(all, sums[w]);
         }
@@ -240,23 +242,40 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             if (x.b0 == x.b1) continue;
             const int keys = seen_by_last();
             const int *table = p.tables + static_cast<size_t>(x.req) * p.width;
-            int rows = 0, cached = -1;  // this lane's box, of group `cached`
-            // cache rows of a 64-key half's boxes
-            auto boxes = [&](int half, int (&y)[4]) {
+            // cache rows of a 64-key half's boxes; `at` and `ahead` hold this lane's box of a group of 32
+            struct Boxes {
+                int group = -1, row;
+            } at, ahead;
+            auto find = [&](Boxes &f, int half) {
                 const int group = half >> (5 - bits);
-                if (group != cached) {
-                    cached = group;
-                    const int key = (group * 32 + lane) * box;
-                    rows = all_rows;
-                    if (key < keys) {
-                        const int pg = key / p.by_page, id = __ldcg(table + pg);
-                        if (id >= 0 && id < p.n_pages) rows = id * p.page_size + key - pg * p.page_size;
-                        else atomicOr(p.status, kStatusBadPageBit);
-                    }
+                if (group == f.group) return;
+                const int found = at.group;
+                f.group = group;
+                if (group == found) {  // (the copies' group, already found)
+                    f.row = at.row;
+                    return;
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = __shfl_sync(~0u, rows, ((half << bits) + i) & 31);
+                const int key = (group * 32 + lane) * box;
+                f.row = all_rows;
+                if (key < keys) {
+                    const int pg = key / p.by_page, id = __ldcg(table + pg);
+                    if (id >= 0 && id < p.n_pages) f.row = id * p.page_size + key - pg * p.page_size;
+                    else atomicOr(p.status, kStatusBadPageBit);
+                }
             };
+            auto boxes = [&](int half, int (&y)[4]) {
+                find(at, half);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = __shfl_sync(~0u, at.row, ((half << bits) + i) & 31);
+            };
+            // asks for a half's rows in L2, a lane a box
+            auto prefetch = [&](int half) {
+                find(ahead, half);
+                if (lane >> bits == (half & ((32 >> bits) - 1)) && ahead.row < all_rows)
+                    bulk_prefetch_l2(p.pages + static_cast<size_t>(ahead.row) * kLatRow, static_cast<uint32_t>(box) * kLatRow * 2);
+                __syncwarp();
+            };
+            int asked = x.b0;  // the last block that L2 has been asked for
             CFA_ROLLED for (int b = x.b0; ok && b < x.b1; ++b) {
                 if (!values) {
                     int y[4];
@@ -290,7 +309,8 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                         __syncwarp();
                         ++pieces;
                     }
-                    if (b == max(x.b0, x.b1 - kLatAhead)) {
+                    CFA_ROLLED for (int k = 0; ok && k < 2 && asked < min(b + kLatAhead, x.b1 - 1); ++k) prefetch(2 * ++asked + rank);
+                    if (b == max(x.b0, x.b1 - kLatPeek)) {
                         // the next tile's queries and first keys, in L2 by the time they are loaded
                         LatentWalk peek = walk;
                         if (peek.next(p.B, p.H, p.by_H, request) && peek.x.b0 < peek.x.b1) {
@@ -600,31 +620,37 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 // together: a thread's own 16 bytes, in 32 rows at once, take a transaction each
                 uint8_t *stage = smem + S::kP + half * kLatChunk + row_group * 128;
 #pragma unroll 1
-                for (int c = 0; c < 256; c += 32) {
-                    uint32_t v[32];
-                    float f[32];
+                for (int c = 0; c < 256; c += 64) {
+                    uint32_t v[64];
                     __syncwarp();
                     if (any) {
                         tmem_ld_x32(tmem + lanes + 128 + c, v);
+                        tmem_ld_x32(tmem + lanes + 128 + c + 32, v + 32);
                         tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) v[e] = 0u;
                     }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] = see > 0 ? __uint_as_float(v[e]) * inv : 0.f;
-                    const int at = c / 8 & 7;  // 16-byte chunks of the staged 128
+                    for (int e = 0; e < 8; ++e) {
+                        uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<uint4 *>(stage + lane * 128 + (((at + e) ^ (lane & 7)) << 4)) =
-                            make_uint4(pack2_bf16_cvt(f[8 * e], f[8 * e + 1]), pack2_bf16_cvt(f[8 * e + 2], f[8 * e + 3]),
-                                       pack2_bf16_cvt(f[8 * e + 4], f[8 * e + 5]), pack2_bf16_cvt(f[8 * e + 6], f[8 * e + 7]));
-                    if ((c & 32) == 0) continue;
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = pack2_bf16_cvt(__uint_as_float(v[8 * e + 2 * k]) * inv, __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
                     __syncwarp();
-                    uint16_t *out = p.out + (out_row - lane) * kLatC + 256 * half + (c - 32) + 8 * (lane & 7);
+                    uint4 y[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int r = 4 * e + (lane >> 3);
-                        if (row_group + r < here)
-                            *reinterpret_cast<uint4 *>(out + r * kLatC) =
-                                *reinterpret_cast<const uint4 *>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                        y[e] = *reinterpret_cast<const uint4 *>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                    }
+                    uint16_t *out = p.out + (out_row - lane) * kLatC + 256 * half + c + 8 * (lane & 7);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = 4 * e + (lane >> 3);
+                        if (row_group + r < here) *reinterpret_cast<uint4 *>(out + r * kLatC) = y[e];
                     }
                 }
             }
