@@ -685,7 +685,7 @@ cfa_status cfa_paged_describe(const cfa_paged *paged, char *buf, int len);
  *     cfa_latent_expanded   over keys and values that the caller has expanded (latents . W_kvb)
  * W_kvb is cfa_mla's: [512, n_heads * 256], per head [W_k (128) | W_v (128)]. Device arrays,
  * values out of range, alignment and streams as in the paged caches above (a plan's workspace
- * serves cfa_latent_attention alone).
+ * serves cfa_latent_attention and cfa_latent_expanded).
  * ========================================================================== */
 
 typedef struct cfa_latent cfa_latent; /* opaque */
@@ -695,7 +695,7 @@ typedef struct cfa_latent cfa_latent; /* opaque */
  * (1..131072) new tokens per call, n_heads 1..1024, page_size 16, 32 or a multiple of 64 up
  * to 1<<22 (CFA_ERR_UNSUPPORTED otherwise; CFA_ERR_INVALID_ARG for non-positive values). No
  * rotation until cfa_latent_set_rope. The workspace holds the records of cut tiles, SMs x 128
- * rows of 512 + 2 floats. NULL on failure; cfa_last_error() says why.
+ * rows of 512 + 4 floats. NULL on failure; cfa_last_error() says why.
  */
 cfa_latent *cfa_latent_create(int max_seqs, int max_tokens, int n_heads, int page_size);
 

@@ -26,6 +26,8 @@ const void *latent_unfold_kernel_ptr();
 const void *latent_attention_kernel_ptr();
 const void *latent_merge_kernel_ptr();
 const void *latent_expanded_kernel_ptr();
+const void *latent_expanded_merge_kernel_ptr();
+int latent_expanded_smem();
 int latent_attention_smem();
 }  // namespace cfa
 
@@ -37,7 +39,7 @@ struct cfa_latent {
     float magnitude = 1.0f;
     unsigned long long turns[cfa::kLatR / 2] = {};
     // workspace
-    unsigned *words = nullptr;  // [0] status
+    unsigned *words = nullptr;  // [0] status, [1..2] the expanded form's merge (odd)
     float *rec_o = nullptr;     // records of the attention's pieces
     float2 *rec_ml = nullptr;
     int4 *cuts = nullptr;
@@ -301,9 +303,12 @@ cfa_latent *cfa_latent_create(int max_seqs, int max_tokens, int n_heads, int pag
     const size_t rec_rows = 2u * static_cast<size_t>(p->runs) * cfa::kLatTile;
     if (cudaFuncSetAttribute(cfa::latent_attention_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              cfa::latent_attention_smem()) != cudaSuccess ||
-        cudaMalloc(&p->words, sizeof(unsigned)) != cudaSuccess || !clear_words(p->words, 1) ||
+        cudaFuncSetAttribute(cfa::latent_expanded_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             cfa::latent_expanded_smem()) != cudaSuccess ||
+        cudaMalloc(&p->words, 3 * sizeof(unsigned)) != cudaSuccess || !clear_words(p->words, 3) ||
         cudaMalloc(&p->rec_o, sizeof(float) * rec_rows * kLatC) != cudaSuccess ||
-        cudaMalloc(&p->rec_ml, sizeof(float2) * rec_rows) != cudaSuccess ||
+        // (twice the rows: the expanded form's records are 256 rows of 128 dims, one a block)
+        cudaMalloc(&p->rec_ml, 2 * sizeof(float2) * rec_rows) != cudaSuccess ||
         cudaMalloc(&p->cuts, sizeof(int4) * static_cast<size_t>(p->runs)) != cudaSuccess) {
         cudaGetLastError();
         latent_free(p);
@@ -420,27 +425,41 @@ cfa_status cfa_latent_expanded(cfa_latent *p, int n_tokens, int n_keys, int n_se
     OnDevice on(p->device);
     if (!on.ok()) return fail(CFA_ERR_CUDA);
     cfa::LatentExpandedParams kp{};
-    kp.q = static_cast<const uint16_t *>(q);
-    kp.q_stride = q_stride;
     kp.kv = static_cast<const uint16_t *>(kv);
     kp.kv_stride = kv_stride;
-    kp.k_rope = static_cast<const uint16_t *>(k_rope);
-    kp.k_rope_stride = k_rope_stride;
     kp.cu = cu;
     kp.cu_k = cu_k;
     kp.out = static_cast<uint16_t *>(out);
     kp.lse = lse;
     kp.status = p->words;
+    kp.odd = p->words + 1;
+    kp.rec_o = p->rec_o;
+    kp.rec_ml = p->rec_ml;
     kp.T = n_tokens;
     kp.S = n_keys;
     kp.B = n_seqs;
     kp.H = p->nh;
+    kp.grid = 2 * p->runs;
+    kp.by_H = cfa::FastDiv(static_cast<uint32_t>(p->nh));
     kp.scale_log2 = scale_log2(scale);
     kp.timeout_ns = kTimeoutNs;
-    void *args[1] = {&kp};
-    const cfa_status st =
-        launch(cfa::latent_expanded_kernel_ptr(),
-               dim3(static_cast<unsigned>(n_tokens), static_cast<unsigned>((p->nh + 7) / 8)), 256, 0, stream, args);
+    // without keys the kernel loads none: any map will do
+    const uint64_t rows = static_cast<uint64_t>(std::max(n_keys, 1));
+    CUtensorMap tq, tk, tr;
+    if (cfa::encode_bf16_2d_ex(&tq, q, static_cast<uint64_t>(wide), static_cast<uint64_t>(n_tokens),
+                               static_cast<uint64_t>(q_stride), 64, 128, true) != CFA_OK ||
+        cfa::encode_bf16_2d_ex(&tk, n_keys ? kv : q, static_cast<uint64_t>(n_keys ? kwide : 64), rows,
+                               static_cast<uint64_t>(n_keys ? kv_stride : 64), 64, 128, true) != CFA_OK ||
+        cfa::encode_bf16_2d_ex(&tr, n_keys ? k_rope : q, kLatR, rows, static_cast<uint64_t>(n_keys ? k_rope_stride : 64),
+                               64, 128, true) != CFA_OK)
+        return fail(CFA_ERR_CUDA);
+    void *args[4] = {&tq, &tk, &tr, &kp};
+    cfa_status st = launch(cfa::latent_expanded_kernel_ptr(), dim3(static_cast<unsigned>(kp.grid)), cfa::kExpThreads,
+                           static_cast<size_t>(cfa::latent_expanded_smem()), stream, args);
+    void *margs[1] = {&kp};
+    if (st == CFA_OK)
+        st = launch(cfa::latent_expanded_merge_kernel_ptr(), dim3(2u * static_cast<unsigned>(p->num_sms)),
+                    cfa::kLatMergeThreads, 0, stream, margs);
     return st == CFA_OK ? CFA_OK : fail(st);
 }
 
@@ -498,7 +517,7 @@ cfa_status cfa_latent_describe(const cfa_latent *p, char *buf, int len) {
                   "\"interleaved\": %d, \"scaling\": %d, \"num_sms\": %d, \"runs\": %d, \"smem_bytes\": %d, "
                   "\"workspace_bytes\": %lld}",
                   p->max_seqs, p->max_tokens, p->nh, p->ps, p->rope, p->interleaved, p->scaling, p->num_sms, p->runs,
-                  cfa::latent_attention_smem(), 2ll * p->runs * cfa::kLatTile * (4 * kLatC + 8) + 16ll * p->runs);
+                  cfa::latent_attention_smem(), 2ll * p->runs * cfa::kLatTile * (4 * kLatC + 16) + 16ll * p->runs);
     return CFA_OK;
 }
 

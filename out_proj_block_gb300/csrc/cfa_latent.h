@@ -81,19 +81,25 @@ static_assert(kLatMaxRuns <= kLatMergeThreads, "it does");
 // ------------------------------------------- attention over expanded keys and values
 
 struct LatentExpandedParams {
-    const uint16_t *q;       // rows of H * 192
-    long long q_stride;
-    const uint16_t *kv;      // rows of H * 256
+    const uint16_t *kv;      // rows of H * 256 (but for one rare pass, read by a tensor map)
     long long kv_stride;
-    const uint16_t *k_rope;  // rows of 64
-    long long k_rope_stride;
     const int *cu, *cu_k;
     uint16_t *out;           // [T][H][128]
     float *lse;              // [T][H] or null
     unsigned *status;
-    int T, S, B, H;
+    unsigned *odd;           // {a value that is not finite was cleared, arrivals of the merge's blocks}; 0 between calls
+    float *rec_o;            // records of parts: unnormalised outputs in 16-byte chunks [32][256 rows][4]
+    float2 *rec_ml;          // and each row's maximum (base 2) and sum
+    int T, S, B, H, grid;
+    FastDiv by_H;
     float scale_log2;
     uint32_t timeout_ns;
 };
+
+// eight softmax warps; a load warp for keys and queries and one for values, one that issues the products, one idle
+constexpr int kExpLoadWarp = 8, kExpMmaWarp = 10;
+constexpr int kExpThreads = 384;
+constexpr int kExpMaxParts = 8;  // of a task of the last round
+constexpr int kExpLeast = 3;     // least blocks of a part
 
 }  // namespace cfa

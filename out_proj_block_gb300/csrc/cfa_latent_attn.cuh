@@ -508,7 +508,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 const bool raise = __any_sync(~0u, top > m + 8.f);
                 float scale = 1.f;
                 if (raise) {
-                    const float mn = fmaxf(m, top);
+                    const float mn = top > m + 8.f ? top : m;  // (each row by itself: others must not change it)
                     scale = m == mn ? 1.f : exp2_ftz(m - mn);
                     m = mn;
                     l *= scale;

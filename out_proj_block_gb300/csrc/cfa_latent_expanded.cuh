@@ -3,72 +3,621 @@
 //   o = sum_j w_j v_j / sum_j w_j,  w_j = 2^(s_j - m),  m = max_j s_j,
 //   s_j = scale log2(e) (q_nope . k_j + q_rope . k_rope_j);  lse = (m + log2 sum_j w_j) ln 2
 //
-// A warp for a token's head goes over its keys one by one.
+// for each query token and head over the keys that the token sees. A row without any is 0 with lse -inf.
+//
+// A task is a head of a request and 256 of its tokens, as two tiles of 128: 192 dims of scores and 128
+// of values are 640 operations a query and key, so products bound it. On tcgen05 a block of 128 keys
+// takes S = Q K^T (12 instructions of 128 x 128 x 16) and O += P V (8) for either tile. TMEM holds S and O
+// of both tiles (4 x 128 columns), the weights P as bf16 in place of the scores. A tile's next scores
+// need its weights' product to have ended, so while one tile's softmax runs (a thread a row), the other's
+// products do: the tiles take turns. The last commit that a tile's scores wait for covers the product before
+// them, so O may be rescaled then; that is done lazily, when a row's maximum grew by more than 8 (a factor 2^8,
+// far inside fp32), a published method. Keys come in chunks of 64 dims through a ring of four,
+// the queries and values whole.
+//
+// Tasks are dealt out in turn to one block per SM, a request's tiles one behind the other (they read the same
+// keys at the same time, out of L2), each round in the other direction. What does not fill the last
+// round is split along the keys; its parts leave records, which a second kernel merges in order, so results
+// are bitwise reproducible.
+//
+// Weights are rounded to bf16 for their product with the values (2^-8 each, the size of the result's own
+// rounding); their sum, the maxima, the outputs and the records are fp32.
 #pragma once
+
+#include <cuda.h>
 
 #include "cfa_device.cuh"
 #include "cfa_latent.h"
+#include "cfa_paged.h"
+#include "cfa_paged_device.cuh"
+#include "cfa_tensor.cuh"
 #include "cfa_tile.cuh"
 
 namespace cfa {
 
-// Offsets that are in order within [0, n]; by all threads of the block.
-__device__ __forceinline__ bool latent_offsets_ok(const int *cu, int B, int n) {
+constexpr int kExpChunk = 128 * 128;  // 128 rows of 64 dims
+constexpr int kExpKSlots = 4, kExpVSlots = 2;
+constexpr int kExpRows = 256;         // tokens of a task
+constexpr int kExpWarps = kExpThreads / 32;
+
+struct ExpSmem {
+    static constexpr int kQ = 0;                              // [2 tiles][3][128 rows][128 bytes]
+    static constexpr int kK = kQ + 6 * kExpChunk;             // ring of chunks
+    static constexpr int kV = kK + kExpKSlots * kExpChunk;    // ring of [2][128 keys][128 bytes]
+    static constexpr int kBars = kV + kExpVSlots * 2 * kExpChunk;
+    static constexpr int kFullK = kBars, kEmptyK = kFullK + 8 * kExpKSlots;
+    static constexpr int kFullV = kEmptyK + 8 * kExpKSlots, kEmptyV = kFullV + 8 * kExpVSlots;
+    static constexpr int kFullQ = kEmptyV + 8 * kExpVSlots, kEmptyQ = kFullQ + 16;  // a tile each
+    static constexpr int kScores = kEmptyQ + 16, kWeights = kScores + 16, kDrain = kWeights + 16;
+    static constexpr int kBarsEnd = kDrain + 8;
+    static constexpr int kMisc = kBarsEnd;                    // flags, TMEM address
+    static constexpr int kSums = kMisc + 16;                  // int [12]: the scan's sums
+    static constexpr int kTiles = kSums + 64;                 // uint16 [B + 1]: tasks of a head before a request
+    static constexpr int kBytes = kTiles + 2 * (kPagedMaxSeqs + 2);
+};
+static_assert(ExpSmem::kBytes <= 227 * 1024, "it fits");
+static_assert(kPagedMaxTokens / kExpRows + kPagedMaxSeqs < 65536, "tasks of a head fit 16 bits");
+
+// Tasks and how they are dealt out to `grid` blocks, from what a scan over the requests finds.
+struct ExpPlan {
+    int full;   // rounds in which every block has a task
+    int rest;   // tasks behind them
+    int parts;  // that each of those is split into at most
+};
+CFA_HD ExpPlan latent_expanded_plan(int tasks, int grid) {
+    ExpPlan p;
+    p.full = tasks / grid;
+    p.rest = tasks - p.full * grid;
+    p.parts = p.rest > 0 ? paged_min(kExpMaxParts, grid / p.rest) : 1;
+    return p;
+}
+
+// A task's part.
+struct ExpItem {
+    int req, h, tile;          // request, head, tile of 256 tokens
+    int tok0, n, k0, len;      // the request's tokens and keys
+    int part, parts;           // which of how many parts of its blocks
+    int b0, end0, end1;        // first block of keys, and behind the last one that each tile of 128 sees
+    int rec;                   // its record's number
+    __device__ __forceinline__ int end(int t) const { return t ? end1 : end0; }
+    __device__ __forceinline__ int last() const { return max(end0, end1); }
+    __device__ __forceinline__ int rows(int t) const { return max(0, min(128, n - tile * kExpRows - 128 * t)); }
+    // keys that token i of the request sees
+    __device__ __forceinline__ int visible(int i) const { return max(0, min(len, len - n + i + 1)); }
+};
+
+// Fills smem with the tasks of a head before each request; the number of all, or -1 where the offsets are not in order.
+// By all threads of the block.
+template <int kThreads>
+__device__ __forceinline__ int latent_expanded_scan(const LatentExpandedParams &p, uint16_t *tiles, int *sums) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.B + kThreads - 1) / kThreads, first = tid * per, last = min(p.B, first + per);
+    int mine = 0;
     bool bad = false;
-    for (int b = threadIdx.x; b <= B; b += blockDim.x) {
-        const int c = __ldcg(cu + b), before = b > 0 ? __ldcg(cu + b - 1) : 0;
-        bad |= c < before || c > n;
+    CFA_ROLLED for (int b = first; b < last; ++b) {
+        const int a = __ldcg(p.cu + b), e = __ldcg(p.cu + b + 1), ka = __ldcg(p.cu_k + b), ke = __ldcg(p.cu_k + b + 1);
+        if (a < 0 || e < a || e > p.T || ka < 0 || ke < ka || ke > p.S) bad = true;
+        else mine += (e - a + kExpRows - 1) / kExpRows;
     }
-    return !__syncthreads_or(bad);
+    int scan = mine;
+    CFA_ROLLED for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(~0u, scan, o);
+        if (lane >= o) scan += v;
+    }
+    if (lane == 31) sums[warp] = scan;
+    const bool refused = __syncthreads_or(bad) != 0;
+    int at = scan - mine, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) at += sums[w];
+        all += sums[w];
+    }
+    if (refused) return -1;
+    CFA_ROLLED for (int b = first; b < last; ++b) {
+        tiles[b] = static_cast<uint16_t>(at);
+        at += (__ldcg(p.cu + b + 1) - __ldcg(p.cu + b) + kExpRows - 1) / kExpRows;
+    }
+    if (tid == 0) tiles[p.B] = static_cast<uint16_t>(all);
+    __syncthreads();
+    return all * p.H;
 }
 
-// The request of token t, or -1.
-__device__ __forceinline__ int latent_request(const int *cu, int B, int t) {
-    int lo = 0, hi = B;  // first request whose end is above t
-    while (lo < hi) {
+// Task number `task`, part `part` of at most `parts`; false where it has fewer.
+__device__ __forceinline__ bool latent_expanded_item(const LatentExpandedParams &p, const uint16_t *tiles, int task, int part,
+                                                     int parts, ExpItem &x) {
+    const int at = task / p.by_H;
+    int lo = 0, hi = p.B;  // the last request whose tasks begin no later (and that has any)
+    CFA_ROLLED while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (__ldcg(cu + mid + 1) > t) hi = mid;
-        else lo = mid + 1;
+        if (tiles[mid] <= at) lo = mid;
+        else hi = mid;
     }
-    return lo < B && t >= __ldcg(cu + lo) ? lo : -1;
+    const int own = tiles[lo + 1] - tiles[lo], in = task - tiles[lo] * p.H;
+    x.req = lo;
+    x.h = in / own;
+    x.tile = own - 1 - (in - x.h * own);  // the longest first
+    x.tok0 = __ldcg(p.cu + lo);
+    x.n = __ldcg(p.cu + lo + 1) - x.tok0;
+    x.k0 = __ldcg(p.cu_k + lo);
+    x.len = __ldcg(p.cu_k + lo + 1) - x.k0;
+    auto blocks_of = [&](int t) {
+        const int rows = x.rows(t);
+        return rows > 0 ? (x.visible(x.tile * kExpRows + 128 * t + rows - 1) + 127) / 128 : 0;
+    };
+    const int e0 = blocks_of(0), e1 = blocks_of(1), blocks = max(e0, e1);
+    x.part = part;
+    x.parts = max(1, min(parts, blocks / kExpLeast));
+    if (part >= x.parts) return false;
+    x.b0 = blocks * part / x.parts;
+    const int b1 = blocks * (part + 1) / x.parts;
+    x.end0 = max(x.b0, min(b1, e0));
+    x.end1 = max(x.b0, min(b1, e1));
+    return true;
 }
 
-__global__ void __launch_bounds__(256) latent_expanded_kernel(const __grid_constant__ LatentExpandedParams p) {
-    const int t = blockIdx.x, h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+__device__ __forceinline__ void registers_of_softmax() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+__device__ __forceinline__ void registers_of_loads() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+
+__global__ void __launch_bounds__(kExpThreads, 1)
+latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                       const __grid_constant__ CUtensorMap tm_rope, const __grid_constant__ LatentExpandedParams p) {
+    using S = ExpSmem;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = smem_addr(smem);
+    int *misc = reinterpret_cast<int *>(smem + S::kMisc);
+    volatile int *timed_out = misc;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 1);
+    const uint16_t *tiles = reinterpret_cast<const uint16_t *>(smem + S::kTiles);
+
+    // a thread a barrier, with the arrivals it expects
+    if (tid < (S::kBarsEnd - S::kBars) / 8) {
+        const int at = S::kBars + 8 * tid;
+        mbar_init(base + at, (at >= S::kEmptyQ && at < S::kScores) || (at >= S::kWeights && at < S::kDrain) ? 4 : 1);
+        fence_mbar_init();
+    }
+    if (tid == 0) misc[0] = 0;
+    if (warp == kExpMmaWarp) tmem_alloc(smem_addr(tmem_slot), 512);
+    if (warp == kExpLoadWarp && elect_one()) {
+        prefetch_tensor_map(&tm_q);
+        prefetch_tensor_map(&tm_kv);
+        prefetch_tensor_map(&tm_rope);
+    }
+    tcgen05_fence_before();
     grid_dependency_wait();
-    const bool a = latent_offsets_ok(p.cu, p.B, p.T), c = latent_offsets_ok(p.cu_k, p.B, p.S);
-    if (!(a && c) && t == 0 && threadIdx.x == 0) atomicOr(p.status, kStatusBadLengthBit);
-    const int b = a && c ? latent_request(p.cu, p.B, t) : -1;
-    if (b >= 0 && h < p.H) {
-        const int k0 = __ldcg(p.cu_k + b), len = __ldcg(p.cu_k + b + 1) - k0;
-        const int see = min(len, len - (__ldcg(p.cu + b + 1) - t) + 1);
-        float q[kLatQ / 32], o[kLatV / 32] = {}, m = -INFINITY, l = 0.f;
-        const uint16_t *qp = p.q + t * p.q_stride + h * kLatQ;
+    const int tasks = latent_expanded_scan<kExpThreads>(p, reinterpret_cast<uint16_t *>(smem + S::kTiles),
+                                                        reinterpret_cast<int *>(smem + S::kSums));
+    tcgen05_fence_after();
+    if (blockIdx.x == 0 && tid == 0 && tasks < 0) atomicOr(p.status, kStatusBadLengthBit);
+    grid_dependents_launch();
+    const uint32_t tmem = *tmem_slot;
+    const int grid = static_cast<int>(gridDim.x);
+    const ExpPlan plan = latent_expanded_plan(max(0, tasks), grid);
+    // The block's item of round r; false where it has none.
+    auto item = [&](int r, ExpItem &x) {
+        const int at = r & 1 ? grid - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
+        if (r < plan.full) return latent_expanded_item(p, tiles, r * grid + at, 0, 1, x);
+        const int task = at / plan.parts, part = at - task * plan.parts;
+        x.rec = at;
+        return task < plan.rest && latent_expanded_item(p, tiles, plan.full * grid + task, part, plan.parts, x);
+    };
+    const int rounds = plan.full + (plan.rest > 0);
+    auto wait = [&](int bar, uint32_t parity, unsigned site) {
+        return bounded_wait([&]() { return mbar_try_wait(base + bar, parity); }, p.timeout_ns, timed_out, p.status, site);
+    };
+    // The same for a warp as a whole.
+    auto wait_warp = [&](int bar, uint32_t parity, unsigned site) { return __all_sync(~0u, wait(bar, parity, site)); };
+
+    if (warp >= kExpLoadWarp) {
+        registers_of_loads();
+        if (warp == kExpLoadWarp || warp == kExpLoadWarp + 1) {
+            // -------------------------------------- load warps: keys and queries, values
+            const bool values = warp != kExpLoadWarp;
+            uint32_t n = 0, queried = 0, queries = 0;  // slots; tiles whose queries were ever loaded, and phases, a bit a tile
+            bool ok = true;
+            CFA_ROLLED for (int r = 0; ok && r < rounds; ++r) {
+                ExpItem x;
+                if (!item(r, x)) continue;
+                const int last = x.last();
+                if (!values) {
+                    CFA_ROLLED for (int t = 0; ok && t < 2; ++t) {
+                        if (x.end(t) == x.b0) continue;
+                        if (queried >> t & 1) ok = wait_warp(S::kEmptyQ + 8 * t, ~queries >> t & 1, kSiteStageEmpty);
+                        if (!ok) break;
+                        if (elect_one()) {
+                            const uint32_t full = base + S::kFullQ + 8 * t;
+                            mbar_arrive_expect_tx(full, 3 * kExpChunk);
 #pragma unroll
-        for (int i = 0; i < kLatQ / 32; ++i) q[i] = bf16_bits(qp[lane + 32 * i]);
-        for (int j = 0; j < see; ++j) {
-            const uint16_t *kv = p.kv + (k0 + j) * p.kv_stride + h * kLatKv;
-            const uint16_t *kr = p.k_rope + (k0 + j) * p.k_rope_stride;
-            float s = 0.f;
+                            for (int c = 0; c < 3; ++c)
+                                tma_load_2d(base + S::kQ + (3 * t + c) * kExpChunk, &tm_q, x.h * kLatQ + 64 * c,
+                                            x.tok0 + x.tile * kExpRows + 128 * t, full);
+                        }
+                        __syncwarp();
+                        queried |= 1u << t;
+                        queries ^= 1u << t;
+                    }
+                    CFA_ROLLED for (int b = x.b0; ok && b < last; ++b)
+                        CFA_ROLLED for (int c = 0; c < 3; ++c, ++n) {
+                            const uint32_t slot = n % kExpKSlots, full = base + S::kFullK + 8 * slot;
+                            if (n >= kExpKSlots) ok = wait_warp(S::kEmptyK + 8 * slot, (n / kExpKSlots - 1) & 1, kSiteStageEmpty);
+                            if (!ok) break;
+                            if (elect_one()) {
+                                mbar_arrive_expect_tx(full, kExpChunk);
+                                if (c < 2) tma_load_2d(base + S::kK + slot * kExpChunk, &tm_kv, x.h * kLatKv + 64 * c, x.k0 + 128 * b, full);
+                                else tma_load_2d(base + S::kK + slot * kExpChunk, &tm_rope, 0, x.k0 + 128 * b, full);
+                            }
+                            __syncwarp();
+                        }
+                } else {
+                    CFA_ROLLED for (int b = x.b0; ok && b < last; ++b, ++n) {
+                        const uint32_t slot = n % kExpVSlots, full = base + S::kFullV + 8 * slot;
+                        if (n >= kExpVSlots) ok = wait_warp(S::kEmptyV + 8 * slot, (n / kExpVSlots - 1) & 1, kSiteStageEmpty);
+                        if (!ok) break;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(full, 2 * kExpChunk);
 #pragma unroll
-            for (int i = 0; i < kLatN / 32; ++i) s = fmaf(q[i], bf16_bits(kv[lane + 32 * i]), s);
+                            for (int c = 0; c < 2; ++c)
+                                tma_load_2d(base + S::kV + (2 * slot + c) * kExpChunk, &tm_kv, x.h * kLatKv + kLatN + 64 * c,
+                                            x.k0 + 128 * b, full);
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (lane == 0 && *timed_out) {
+                // a wait gave up: the copies in flight land before the block ends
+                const uint64_t t0 = global_timer_ns();
+                auto land = [&](uint32_t bar, uint32_t parity) {
+                    while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kDrainTimeoutFactor * p.timeout_ns) {
+                    }
+                };
+                const uint32_t slots = values ? kExpVSlots : kExpKSlots;
+                for (uint32_t k = n > slots ? n - slots : 0; k < n; ++k)
+                    land(base + (values ? S::kFullV : S::kFullK) + 8 * (k % slots), (k / slots) & 1);
+                for (int t = 0; !values && t < 2; ++t)
+                    if (queried >> t & 1) land(base + S::kFullQ + 8 * t, ~queries >> t & 1);
+            }
+            __syncwarp();
+        } else if (warp == kExpMmaWarp) {
+            // ------------------------------------------------------------------- products
+            const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
+            const uint32_t idesc_s = umma_idesc_bf16(128, 128, false, false), idesc_o = umma_idesc_bf16(128, 128, false, true);
+            const uint64_t q0 = umma_smem_desc(base + S::kQ, 16, 1024), k0 = umma_smem_desc(base + S::kK, 16, 1024),
+                           v0 = umma_smem_desc(base + S::kV, kExpChunk, 1024);
+            uint32_t nk = 0, nv = 0, queries = 0, weights = 0;  // chunks and blocks before the item's; phases, a bit a tile
+            bool ok = true;
+            CFA_ROLLED for (int r = 0; ok && r < rounds; ++r) {
+                ExpItem x;
+                if (!item(r, x)) continue;
+                const int last = x.last(), b0 = x.b0;
+                // scores of tile t and block b; `frees`: nobody reads the keys after
+                auto scores = [&](int t, int b, bool frees) {
+                    CFA_ROLLED for (int c = 0; ok && c < 3; ++c) {
+                        const uint32_t k = nk + 3 * (b - b0) + c, slot = k % kExpKSlots;
+                        ok = wait_warp(S::kFullK + 8 * slot, (k / kExpKSlots) & 1, kSiteStageFull);
+                        tcgen05_fence_after();
+                        if (ok && elect_one()) {
+                            const uint64_t a = q0 + (3 * t + c) * (kExpChunk >> 4), bd = k0 + slot * (kExpChunk >> 4);
 #pragma unroll
-            for (int i = 0; i < kLatR / 32; ++i) s = fmaf(q[kLatN / 32 + i], bf16_bits(kr[lane + 32 * i]), s);
+                            for (int ks = 0; ks < 4; ++ks)  // 32 bytes a step
+                                umma_bf16(tm + 128 * t, a + 2 * ks, bd + 2 * ks, idesc_s, c > 0 || ks > 0);
+                            if (frees) umma_commit(base + S::kEmptyK + 8 * slot);
+                            if (c == 2) umma_commit(base + S::kScores + 8 * t);
+                        }
+                        __syncwarp();
+                    }
+                };
+                CFA_ROLLED for (int t = 0; ok && t < 2; ++t) {
+                    if (x.end(t) == b0) continue;
+                    ok = wait_warp(S::kFullQ + 8 * t, queries >> t & 1, kSiteQExchange);
+                    queries ^= 1u << t;
+                    if (ok) scores(t, b0, t == 1 || x.end1 == b0);
+                }
+                CFA_ROLLED for (int b = b0; ok && b < last; ++b)
+                    CFA_ROLLED for (int t = 0; ok && t < 2; ++t) {
+                        if (b >= x.end(t)) continue;
+                        const uint32_t v = nv + b - b0, slot = v % kExpVSlots;
+                        ok = wait_warp(S::kFullV + 8 * slot, (v / kExpVSlots) & 1, kSiteStageFull) &&
+                             wait_warp(S::kWeights + 8 * t, weights >> t & 1, kSiteSoftmaxExchange);
+                        weights ^= 1u << t;
+                        tcgen05_fence_after();
+                        const bool more = b + 1 < x.end(t);
+                        if (ok && elect_one()) {
+                            const uint64_t vd = v0 + slot * (2 * kExpChunk >> 4);
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-            s *= p.scale_log2;
-            const float n = fmaxf(m, s), f = n == -INFINITY ? 0.f : n;
-            const float g = fast_exp2(m - f), w = fast_exp2(s - f);
-            m = n;
-            l = l * g + w;
-#pragma unroll
-            for (int i = 0; i < kLatV / 32; ++i) o[i] = fmaf(w, bf16_bits(kv[kLatN + lane + 32 * i]), o[i] * g);
+                            for (int ks = 0; ks < 8; ++ks)  // 16 keys of 128 bytes a step
+                                umma_bf16_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * ks, vd + 128 * ks, idesc_o, b > b0 || ks > 0);
+                            if (t == 1 || b >= x.end1) umma_commit(base + S::kEmptyV + 8 * slot);
+                            // behind the last product there are no more scores, but the tile's warps learn that it ended
+                            if (!more) umma_commit(base + S::kScores + 8 * t);
+                        }
+                        __syncwarp();
+                        if (ok && more) scores(t, b + 1, t == 1 || b + 1 >= x.end1);
+                    }
+                nk += 3 * (last - b0);
+                nv += last - b0;
+            }
+            if (elect_one() && *timed_out) {
+                // a wait gave up: the products in flight end before the block does
+                umma_commit(base + S::kDrain);
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait(base + S::kDrain, 0) && global_timer_ns() - t0 < kDrainTimeoutFactor * p.timeout_ns) {
+                }
+            }
+            __syncwarp();
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint16_t *out = p.out + (static_cast<size_t>(t) * p.H + h) * kLatV;
+    } else {
+        // ---------------------------------------------- softmax warps, a warpgroup a tile
+        registers_of_softmax();
+        const int t = warp >> 2, row = tid & 127;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lanes of this warp
+        const uint32_t t_s = tmem + lanes + 128 * t, t_o = tmem + lanes + 256 + 128 * t;
+        const int scores = S::kScores + 8 * t;
+        const uint32_t weights = base + S::kWeights + 8 * t;
+        uint32_t scored = 0, nv = 0;  // phases; blocks before the item's
+        CFA_ROLLED for (int r = 0; r < rounds; ++r) {
+            ExpItem x;
+            if (!item(r, x)) continue;
+            const int rows = x.rows(t), first = x.tile * kExpRows + 128 * t;
+            const bool live = row < rows, warp_live = row - lane < rows;
+            const int see = live ? x.visible(first + row) : 0;
+            const int some = x.visible(first);  // keys that every row of the tile sees
+            const int all = x.visible(min(x.n, x.tile * kExpRows + kExpRows) - 1);  // and any row of the task
+            float m = -INFINITY, l = 0.f;
+            CFA_ROLLED for (int b = x.b0; b < x.end(t); ++b, ++scored) {
+                wait(scores, scored & 1, kSiteSoftmaxExchange);
+                __syncwarp();
+                tcgen05_fence_after();
+                if (warp_live) {
+                    uint32_t s[128];
 #pragma unroll
-        for (int i = 0; i < kLatV / 32; ++i) out[lane + 32 * i] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv));
-        if (p.lse && lane == 0) p.lse[static_cast<size_t>(t) * p.H + h] = (m + log2f(l)) * 0.69314718055994531f;
+                    for (int c = 0; c < 128; c += 32) tmem_ld_x32(t_s + c, s + c);
+                    tmem_wait_ld();
+                    const int lim = see - 128 * b;
+                    if (!__all_sync(~0u, lim >= 128)) {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c) s[c] = c < lim ? s[c] : 0xff800000u;
+                    }
+                    float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < 128; c += 2)
+                        a[(c >> 1) & 3] = fmaxf(fmaxf(a[(c >> 1) & 3], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
+                    const float top = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * p.scale_log2;
+                    if (__any_sync(~0u, top > m + 8.f)) {
+                        // rescale to the new maximum (m = -inf: nothing is there yet)
+                        const float mn = top > m + 8.f ? top : m;  // (each row by itself: others must not change it)
+                        const float g = m == mn ? 1.f : exp2_ftz(m - mn);
+                        m = mn;
+                        l *= g;
+                        if (b > x.b0) {
+#pragma unroll 1
+                            for (int c = 0; c < kLatV; c += 32) {
+                                uint32_t v[32];
+                                tmem_ld_x32(t_o + c, v);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * g);
+                                tmem_st_x16(t_o + c, v);
+                                tmem_st_x16(t_o + c + 16, v + 16);
+                            }
+                        }
+                    }
+                    const float f = m == -INFINITY ? 0.f : -m;
+                    const uint64_t scale2 = pair_f32(p.scale_log2, p.scale_log2), f2 = pair_f32(f, f);
+                    uint64_t sum[2] = {0, 0};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 y = unpair_f32(fma_f32x2(
+                                pair_f32(__uint_as_float(s[32 * c + 2 * e]), __uint_as_float(s[32 * c + 2 * e + 1])), scale2, f2));
+                            const float x0 = exp2_ftz(y.x), x1 = exp2_ftz(y.y);
+                            sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(x0, x1));
+                            w[e] = pack2_bf16_cvt(x0, x1);
+                        }
+                        tmem_st_x16(t_s + 16 * c, w);
+                    }
+                    const float2 both = unpair_f32(add_f32x2(sum[0], sum[1]));
+                    l += both.x + both.y;
+                    tmem_wait_st();
+                }
+                if (some < 128 * (b + 1)) {
+                    // keys from `some` on are not seen by every row, from `all` on by none. A masked weight is 0, and
+                    // 0 times NaN is NaN: what is not finite of the first becomes 0 here, and the merge adds it to the rows
+                    // that see it; the others become 0. (Where the other tile's product runs meanwhile, either way does.)
+                    const uint32_t v = nv + b - x.b0, slot = v % kExpVSlots;
+                    wait(S::kFullV + 8 * slot, (v / kExpVSlots) & 1, kSiteStageFull);
+                    __syncwarp();
+                    uint8_t *vals = smem + S::kV + 2 * slot * kExpChunk + ((row >> 3) & 1) * kExpChunk + ((row & 7) << 4);
+                    CFA_ROLLED for (int k = max(0, some - 128 * b) + (row >> 4); k < 128; k += 8) {
+                        uint4 *at = reinterpret_cast<uint4 *>(vals + k * 128);  // (of a row's chunks any order will do)
+                        uint4 d = make_uint4(0u, 0u, 0u, 0u);
+                        if (128 * b + k < all) {
+                            d = *at;
+                            const uint32_t e = odd_bf16x2(d.x), f = odd_bf16x2(d.y), g = odd_bf16x2(d.z), h = odd_bf16x2(d.w);
+                            if ((e | f | g | h) == 0u) continue;
+                            *p.odd = 1u;
+                            d = make_uint4(d.x & ~e, d.y & ~f, d.z & ~g, d.w & ~h);
+                        }
+                        *at = d;
+                    }
+                    fence_proxy_async_smem();
+                }
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(weights);
+            }
+            const bool any = x.end(t) > x.b0;
+            if (any) {
+                wait(scores, scored & 1, kSiteKvExchange);
+                ++scored;
+            }
+            __syncwarp();
+            tcgen05_fence_after();
+            // ---- the tile's results, or its record
+            nv += x.last() - x.b0;
+            if (warp_live) {
+                const size_t tok = static_cast<size_t>(x.tok0 + first + row);
+                if (x.parts > 1) {
+                    if (live) p.rec_ml[x.rec * kExpRows + 128 * t + row] = make_float2(m, l);
+                    float *rec_o = p.rec_o + static_cast<size_t>(x.rec) * kExpRows * kLatV + 4 * (128 * t + row);
+#pragma unroll 1
+                    for (int c = 0; any && c < kLatV; c += 32) {  // (without keys: m says that nothing is there)
+                        uint32_t v[32];
+                        __syncwarp();
+                        tmem_ld_x32(t_o + c, v);
+                        tmem_wait_ld();
+                        if (!live) continue;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<uint4 *>(rec_o + static_cast<size_t>(c / 4 + e) * (4 * kExpRows)) =
+                                make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    }
+                } else {
+                    if (p.lse && live) p.lse[tok * p.H + x.h] = (m + log2f(l)) * 0.69314718055994531f;
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    // through the tile's first chunk of queries, which nobody reads any more, so that a row's 128 bytes
+                    // are written together
+                    uint8_t *stage = smem + S::kQ + 3 * t * kExpChunk + (row - lane) * 128;
+#pragma unroll 1
+                    for (int c = 0; c < kLatV; c += 64) {
+                        uint32_t v[64];
+                        __syncwarp();
+                        if (any) {
+                            tmem_ld_x32(t_o + c, v);
+                            tmem_ld_x32(t_o + c + 32, v + 32);
+                            tmem_wait_ld();
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 64; ++e) v[e] = 0u;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = pack2_bf16_cvt(__uint_as_float(v[8 * e + 2 * k]) * inv, __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
+                            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                        __syncwarp();
+                        uint4 y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int k = 4 * e + (lane >> 3);
+                            y[e] = *reinterpret_cast<const uint4 *>(stage + k * 128 + (((lane & 7) ^ (k & 7)) << 4));
+                        }
+                        uint16_t *out = p.out + ((tok - lane) * p.H + x.h) * kLatV + c + 8 * (lane & 7);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int k = 4 * e + (lane >> 3);
+                            if (row - lane + k < rows) *reinterpret_cast<uint4 *>(out + static_cast<size_t>(k) * p.H * kLatV) = y[e];
+                        }
+                    }
+                    fence_proxy_async_smem();  // (the next queries come by the asynchronous proxy)
+                }
+            }
+            tcgen05_fence_before();
+            __syncwarp();
+            if (any && lane == 0) mbar_arrive(base + S::kEmptyQ + 8 * t);
+        }
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    if (warp == kExpMmaWarp) {
+        tcgen05_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Adds the values that are not finite to the rows that see them, where the attention has met one that some rows
+// see and others do not (rows that have them already do not change). The last block does it, when
+// all rows are written: a thread goes through a request's new tokens with 8 dims of a head and holds what they
+// have seen so far. Rare, so it need only end in time: a load a token.
+__device__ __noinline__ void latent_expanded_add_odd(const LatentExpandedParams &p) {
+    __shared__ bool last;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomic_add_acq_rel_gpu(p.odd + 1, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    if (threadIdx.x < 2) p.odd[threadIdx.x] = 0;
+    constexpr int C = kLatV / 8;
+    for (int task = threadIdx.x; task < p.B * p.H * C; task += kLatMergeThreads) {
+        const int c = task % C, b = task / C / p.H, h = task / C - b * p.H;
+        const int tok0 = p.cu[b], n = p.cu[b + 1] - tok0, k0 = p.cu_k[b], len = p.cu_k[b + 1] - k0;
+        bool some = false;
+        float seen[8] = {};
+        // token i is the first that sees key len - n + i (the first token's keys all see)
+        for (int i = max(1, n - len); i < n; ++i) {
+            float v[8];
+            unpack8_bf16(*reinterpret_cast<const uint4 *>(p.kv + (k0 + len - n + i) * p.kv_stride + h * kLatKv + kLatN + 8 * c), v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (!(fabsf(v[e]) < INFINITY)) seen[e] += v[e], some = true;
+            if (!some) continue;
+            uint4 *at = reinterpret_cast<uint4 *>(p.out + (static_cast<size_t>(tok0 + i) * p.H + h) * kLatV + 8 * c);
+            float y[8];
+            unpack8_bf16(*at, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = seen[e] == 0.f ? y[e] : y[e] + seen[e];
+            *at = make_uint4(pack2_bf16_cvt(y[0], y[1]), pack2_bf16_cvt(y[2], y[3]), pack2_bf16_cvt(y[4], y[5]), pack2_bf16_cvt(y[6], y[7]));
+        }
+    }
+}
+
+// Merges the records of the split tasks, a warp for 32 rows (a lane a row) and 16 dims.
+__global__ void __launch_bounds__(kLatMergeThreads, 3) latent_expanded_merge_kernel(const __grid_constant__ LatentExpandedParams p) {
+    __shared__ uint16_t tiles[kPagedMaxSeqs + 1];
+    __shared__ int sums[kLatMergeThreads / 32];
+    grid_dependency_wait();
+    const unsigned odd = __ldcg(p.odd);
+    const int tasks = latent_expanded_scan<kLatMergeThreads>(p, tiles, sums);
+    if (tasks > 0) {
+        const ExpPlan plan = latent_expanded_plan(tasks, p.grid);
+        const int lane = threadIdx.x & 31, warps = static_cast<int>(gridDim.x) * (kLatMergeThreads / 32);
+        constexpr int kRec = kExpRows * (kLatV / 4);
+        CFA_ROLLED for (int i = static_cast<int>(blockIdx.x) * (kLatMergeThreads / 32) + (threadIdx.x >> 5);
+                        plan.parts > 1 && i < plan.rest * 64; i += warps) {
+            const int task = i >> 6, row = (i & 7) * 32 + lane, chunk = (i >> 3 & 7) * 4;
+            ExpItem x;
+            latent_expanded_item(p, tiles, plan.full * p.grid + task, 0, plan.parts, x);
+            const int tok = x.tile * kExpRows + row;
+            if (x.parts == 1 || tok >= x.n) continue;
+            const int rec = task * plan.parts;
+            const float2 *ml = p.rec_ml + rec * kExpRows + row;
+            const float4 *o = reinterpret_cast<const float4 *>(p.rec_o) + static_cast<size_t>(rec) * kRec + chunk * kExpRows + row;
+            float m = -INFINITY, l = 0.f;
+            float2 s[kExpMaxParts];
+#pragma unroll
+            for (int k = 0; k < kExpMaxParts; ++k) {
+                s[k] = k < x.parts ? __ldcg(ml + k * kExpRows) : make_float2(-INFINITY, 0.f);
+                m = fmaxf(m, s[k].x);
+            }
+            const float f = m == -INFINITY ? 0.f : m;
+            float a[16] = {};
+#pragma unroll
+            for (int k = 0; k < kExpMaxParts; ++k) {
+                if (k >= x.parts) break;
+                const float g = exp2_ftz(s[k].x - f);
+                l += g * s[k].y;
+                if (s[k].x == -INFINITY && s[k].y == 0.f) continue;  // no keys: there may be no outputs
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float4 v = __ldcg(o + static_cast<size_t>(k) * kRec + c * kExpRows);
+                    a[4 * c] += g * v.x; a[4 * c + 1] += g * v.y; a[4 * c + 2] += g * v.z; a[4 * c + 3] += g * v.w;
+                }
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const size_t at = static_cast<size_t>(x.tok0 + tok) * p.H + x.h;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                *reinterpret_cast<uint4 *>(p.out + at * kLatV + 4 * chunk + 8 * c) =
+                    make_uint4(pack2_bf16_cvt(a[8 * c] * inv, a[8 * c + 1] * inv), pack2_bf16_cvt(a[8 * c + 2] * inv, a[8 * c + 3] * inv),
+                               pack2_bf16_cvt(a[8 * c + 4] * inv, a[8 * c + 5] * inv), pack2_bf16_cvt(a[8 * c + 6] * inv, a[8 * c + 7] * inv));
+            if (p.lse && chunk == 0) p.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
+        }
+        if (odd) latent_expanded_add_odd(p);
     }
     grid_dependents_launch();
 }

@@ -16,5 +16,7 @@ const void *latent_attention_kernel_ptr() { return reinterpret_cast<const void *
 const void *latent_merge_kernel_ptr() { return reinterpret_cast<const void *>(&latent_merge_kernel); }
 int latent_attention_smem() { return LatSmem::kBytes; }
 const void *latent_expanded_kernel_ptr() { return reinterpret_cast<const void *>(&latent_expanded_kernel); }
+const void *latent_expanded_merge_kernel_ptr() { return reinterpret_cast<const void *>(&latent_expanded_merge_kernel); }
+int latent_expanded_smem() { return ExpSmem::kBytes; }
 
 }  // namespace cfa
