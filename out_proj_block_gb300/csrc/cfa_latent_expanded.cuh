@@ -290,20 +290,24 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 ExpItem x;
                 if (!item(r, x)) continue;
                 const int last = x.last(), b0 = x.b0;
-                // scores of tile t and block b; `frees`: nobody reads the keys after
-                auto scores = [&](int t, int b, bool frees) {
-                    CFA_ROLLED for (int c = 0; ok && c < 3; ++c) {
-                        const uint32_t k = nk + 3 * (b - b0) + c, slot = k % kExpKSlots;
-                        ok = wait_warp(S::kFullK + 8 * slot, (k / kExpKSlots) & 1, kSiteStageFull);
-                        tcgen05_fence_after();
-                        if (ok && elect_one()) {
-                            const uint64_t a = q0 + (3 * t + c) * (kExpChunk >> 4), bd = k0 + slot * (kExpChunk >> 4);
+                // Chunk c of block b's keys: its slot, and whether it has landed.
+                auto slot_of = [&](int b, int c) { return (nk + 3 * (b - b0) + c) % kExpKSlots; };
+                auto parity_of = [&](int b, int c) { return (nk + 3 * (b - b0) + c) / kExpKSlots & 1; };
+                // By one thread: the products of chunk c for tile t's scores. `frees`: nobody reads the keys after.
+                auto score_chunk = [&](int t, int b, int c, bool frees) {
+                    const uint32_t slot = slot_of(b, c);
+                    const uint64_t a = q0 + (3 * t + c) * (kExpChunk >> 4), bd = k0 + slot * (kExpChunk >> 4);
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)  // 32 bytes a step
-                                umma_bf16(tm + 128 * t, a + 2 * ks, bd + 2 * ks, idesc_s, c > 0 || ks > 0);
-                            if (frees) umma_commit(base + S::kEmptyK + 8 * slot);
-                            if (c == 2) umma_commit(base + S::kScores + 8 * t);
-                        }
+                    for (int ks = 0; ks < 4; ++ks)  // 32 bytes a step
+                        umma_bf16(tm + 128 * t, a + 2 * ks, bd + 2 * ks, idesc_s, c > 0 || ks > 0);
+                    if (frees) umma_commit(base + S::kEmptyK + 8 * slot);
+                    if (c == 2) umma_commit(base + S::kScores + 8 * t);
+                };
+                auto scores = [&](int t, int b, bool frees, bool landed) {
+                    CFA_ROLLED for (int c = 0; ok && c < 3; ++c) {
+                        if (!landed) ok = wait_warp(S::kFullK + 8 * slot_of(b, c), parity_of(b, c), kSiteStageFull);
+                        tcgen05_fence_after();
+                        if (ok && elect_one()) score_chunk(t, b, c, frees);
                         __syncwarp();
                     }
                 };
@@ -311,17 +315,25 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     if (x.end(t) == b0) continue;
                     ok = wait_warp(S::kFullQ + 8 * t, queries >> t & 1, kSiteQExchange);
                     queries ^= 1u << t;
-                    if (ok) scores(t, b0, t == 1 || x.end1 == b0);
+                    if (ok) scores(t, b0, t == 1 || x.end1 == b0, t == 1 && x.end0 > b0);
                 }
                 CFA_ROLLED for (int b = b0; ok && b < last; ++b)
                     CFA_ROLLED for (int t = 0; ok && t < 2; ++t) {
                         if (b >= x.end(t)) continue;
                         const uint32_t v = nv + b - b0, slot = v % kExpVSlots;
-                        ok = wait_warp(S::kFullV + 8 * slot, (v / kExpVSlots) & 1, kSiteStageFull) &&
-                             wait_warp(S::kWeights + 8 * t, weights >> t & 1, kSiteSoftmaxExchange);
+                        const bool more = b + 1 < x.end(t);
+                        // what the first tile waited for need not be asked for again
+                        if (t == 0 || b >= x.end0) ok = wait_warp(S::kFullV + 8 * slot, (v / kExpVSlots) & 1, kSiteStageFull);
+                        bool landed = t == 1 && b + 1 < x.end0;
+                        if (more && !landed) {
+                            landed = true;
+#pragma unroll
+                            for (int c = 0; c < 3; ++c) landed = landed && mbar_try_wait(base + S::kFullK + 8 * slot_of(b + 1, c), parity_of(b + 1, c));
+                            landed = __all_sync(~0u, landed);
+                        }
+                        ok = ok && wait_warp(S::kWeights + 8 * t, weights >> t & 1, kSiteSoftmaxExchange);
                         weights ^= 1u << t;
                         tcgen05_fence_after();
-                        const bool more = b + 1 < x.end(t);
                         if (ok && elect_one()) {
                             const uint64_t vd = v0 + slot * (2 * kExpChunk >> 4);
 #pragma unroll
@@ -330,9 +342,15 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                             if (t == 1 || b >= x.end1) umma_commit(base + S::kEmptyV + 8 * slot);
                             // behind the last product there are no more scores, but the tile's warps learn that it ended
                             if (!more) umma_commit(base + S::kScores + 8 * t);
+                            // both products in one go where the keys are there: between two goes the tensor core runs dry
+                            // for some 400 clocks
+                            if (more && landed) {
+#pragma unroll
+                                for (int c = 0; c < 3; ++c) score_chunk(t, b + 1, c, t == 1 || b + 1 >= x.end1);
+                            }
                         }
                         __syncwarp();
-                        if (ok && more) scores(t, b + 1, t == 1 || b + 1 >= x.end1);
+                        if (ok && more && !landed) scores(t, b + 1, t == 1 || b + 1 >= x.end1, false);
                     }
                 nk += 3 * (last - b0);
                 nv += last - b0;
