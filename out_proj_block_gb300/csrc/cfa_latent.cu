@@ -307,7 +307,7 @@ cfa_latent *cfa_latent_create(int max_seqs, int max_tokens, int n_heads, int pag
                              cfa::latent_expanded_smem()) != cudaSuccess ||
         cudaMalloc(&p->words, 3 * sizeof(unsigned)) != cudaSuccess || !clear_words(p->words, 3) ||
         cudaMalloc(&p->rec_o, sizeof(float) * rec_rows * kLatC) != cudaSuccess ||
-        // (twice the rows: the expanded form's records are 256 rows of 128 dims, one a block)
+        // (twice the rows: the expanded form's records are 512 rows of 128 dims, one a cluster)
         cudaMalloc(&p->rec_ml, 2 * sizeof(float2) * rec_rows) != cudaSuccess ||
         cudaMalloc(&p->cuts, sizeof(int4) * static_cast<size_t>(p->runs)) != cudaSuccess) {
         cudaGetLastError();
@@ -439,7 +439,7 @@ cfa_status cfa_latent_expanded(cfa_latent *p, int n_tokens, int n_keys, int n_se
     kp.S = n_keys;
     kp.B = n_seqs;
     kp.H = p->nh;
-    kp.grid = 2 * p->runs;
+    kp.grid = p->runs;
     kp.by_H = cfa::FastDiv(static_cast<uint32_t>(p->nh));
     kp.scale_log2 = scale_log2(scale);
     kp.timeout_ns = kTimeoutNs;
@@ -449,12 +449,12 @@ cfa_status cfa_latent_expanded(cfa_latent *p, int n_tokens, int n_keys, int n_se
     if (cfa::encode_bf16_2d_ex(&tq, q, static_cast<uint64_t>(wide), static_cast<uint64_t>(n_tokens),
                                static_cast<uint64_t>(q_stride), 64, 128, true) != CFA_OK ||
         cfa::encode_bf16_2d_ex(&tk, n_keys ? kv : q, static_cast<uint64_t>(n_keys ? kwide : 64), rows,
-                               static_cast<uint64_t>(n_keys ? kv_stride : 64), 64, 128, true) != CFA_OK ||
+                               static_cast<uint64_t>(n_keys ? kv_stride : 64), 64, 64, true) != CFA_OK ||
         cfa::encode_bf16_2d_ex(&tr, n_keys ? k_rope : q, kLatR, rows, static_cast<uint64_t>(n_keys ? k_rope_stride : 64),
-                               64, 128, true) != CFA_OK)
+                               64, 64, true) != CFA_OK)
         return fail(CFA_ERR_CUDA);
     void *args[4] = {&tq, &tk, &tr, &kp};
-    cfa_status st = launch(cfa::latent_expanded_kernel_ptr(), dim3(static_cast<unsigned>(kp.grid)), cfa::kExpThreads,
+    cfa_status st = launch(cfa::latent_expanded_kernel_ptr(), dim3(2u * static_cast<unsigned>(kp.grid)), cfa::kExpThreads,
                            static_cast<size_t>(cfa::latent_expanded_smem()), stream, args);
     void *margs[1] = {&kp};
     if (st == CFA_OK)

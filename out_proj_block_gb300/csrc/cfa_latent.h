@@ -88,16 +88,17 @@ struct LatentExpandedParams {
     float *lse;              // [T][H] or null
     unsigned *status;
     unsigned *odd;           // {a value that is not finite was cleared, arrivals of the merge's blocks}; 0 between calls
-    float *rec_o;            // records of parts: unnormalised outputs in 16-byte chunks [32][256 rows][4]
+    float *rec_o;            // records of parts: unnormalised outputs in 16-byte chunks [32][512 rows][4]
     float2 *rec_ml;          // and each row's maximum (base 2) and sum
-    int T, S, B, H, grid;
+    int T, S, B, H;
+    int grid;                // clusters
     FastDiv by_H;
     float scale_log2;
     uint32_t timeout_ns;
 };
 
-// eight softmax warps; a load warp for keys and queries and one for values, one that issues the products, one idle
-constexpr int kExpLoadWarp = 8, kExpMmaWarp = 10;
+// eight softmax warps; a load warp for keys and queries and one for values, one that issues the products, a relay
+constexpr int kExpLoadWarp = 8, kExpMmaWarp = 10, kExpRelayWarp = 11;
 constexpr int kExpThreads = 384;
 constexpr int kExpMaxParts = 8;  // of a task of the last round
 constexpr int kExpLeast = 3;     // least blocks of a part

@@ -5,19 +5,21 @@
 //
 // for each query token and head over the keys that the token sees. A row without any is 0 with lse -inf.
 //
-// A task is a head of a request and 256 of its tokens, as two tiles of 128: 192 dims of scores and 128
-// of values are 640 operations a query and key, so products bound it. On tcgen05 a block of 128 keys
-// takes S = Q K^T (12 instructions of 128 x 128 x 16) and O += P V (8) for either tile. TMEM holds S and O
-// of both tiles (4 x 128 columns), the weights P as bf16 in place of the scores. A tile's next scores
-// need its weights' product to have ended, so while one tile's softmax runs (a thread a row), the other's
-// products do: the tiles take turns. The last commit that a tile's scores wait for covers the product before
-// them, so O may be rescaled then; that is done lazily, when a row's maximum grew by more than 8 (a factor 2^8,
-// far inside fp32), a published method. Keys come in chunks of 64 dims through a ring of four,
-// the queries and values whole.
+// A task is a head of a request and 512 of its tokens; 192 dims of scores and 128 of values are 640
+// operations a query and key, so products bound it. A cluster of two blocks takes a task as two tiles of
+// 256 rows (128 to either block) with the tcgen05 instructions that span both: a block of 128 keys is S = Q K^T
+// (12 instructions of 256 x 128 x 16) and O += P V (8) for either tile, and either block holds half of it, 64 keys
+// for the scores and 64 dims for the values. In one block's own instructions (128 x 128 x 16) the
+// scores' two operands kept shared memory busy for 92 clocks each, where the arithmetic takes 64, and left room
+// for little more than one block of keys. TMEM holds S and O of both tiles (4 x 128 columns), the weights P as
+// bf16 in place of the scores. A tile's next scores need its weights' product to have ended, so while one tile's
+// softmax runs (a thread a row), the other's products do: the tiles take turns. The last commit that a
+// tile's scores wait for covers the product before them, so O may be rescaled then; that is done lazily, when a
+// row's maximum grew by more than 8 (a factor 2^8, far inside fp32), a published method.
 //
-// Tasks are dealt out in turn to one block per SM, a request's tiles one behind the other (they read the same
-// keys at the same time, out of L2), each round in the other direction. What does not fill the last
-// round is split along the keys; its parts leave records, which a second kernel merges in order, so results
+// Tasks are dealt out in turn to one cluster per pair of SMs, a request's tiles one behind the other (they
+// read the same keys at the same time, out of L2), each round in the other direction. What does not fill the
+// last round is split along the keys; its parts leave records, which a second kernel merges in order, so results
 // are bitwise reproducible.
 //
 // Weights are rounded to bf16 for their product with the values (2^-8 each, the size of the result's own
@@ -31,24 +33,27 @@
 #include "cfa_paged.h"
 #include "cfa_paged_device.cuh"
 #include "cfa_tensor.cuh"
+#include "cfa_tensor_pair.cuh"
 #include "cfa_tile.cuh"
 
 namespace cfa {
 
-constexpr int kExpChunk = 128 * 128;  // 128 rows of 64 dims
-constexpr int kExpKSlots = 4, kExpVSlots = 2;
-constexpr int kExpRows = 256;         // tokens of a task
-constexpr int kExpWarps = kExpThreads / 32;
+constexpr int kExpChunk = 128 * 128;   // 128 rows of 64 dims
+constexpr int kExpSlots = 3;           // blocks of keys and of values in flight
+constexpr int kExpKSlot = 3 * 64 * 128, kExpVSlot = 128 * 128;
+constexpr int kExpTile = 256;          // tokens of a tile, half of them to either block
+constexpr int kExpRows = 2 * kExpTile; // tokens of a task
 
+// Shared memory, the same in both blocks of a cluster.
 struct ExpSmem {
     static constexpr int kQ = 0;                              // [2 tiles][3][128 rows][128 bytes]
-    static constexpr int kK = kQ + 6 * kExpChunk;             // ring of chunks
-    static constexpr int kV = kK + kExpKSlots * kExpChunk;    // ring of [2][128 keys][128 bytes]
-    static constexpr int kBars = kV + kExpVSlots * 2 * kExpChunk;
-    static constexpr int kFullK = kBars, kEmptyK = kFullK + 8 * kExpKSlots;
-    static constexpr int kFullV = kEmptyK + 8 * kExpKSlots, kEmptyV = kFullV + 8 * kExpVSlots;
-    static constexpr int kFullQ = kEmptyV + 8 * kExpVSlots, kEmptyQ = kFullQ + 16;  // a tile each
-    static constexpr int kScores = kEmptyQ + 16, kWeights = kScores + 16, kDrain = kWeights + 16;
+    static constexpr int kK = kQ + 6 * kExpChunk;             // ring of [3][64 keys][128 bytes]
+    static constexpr int kV = kK + kExpSlots * kExpKSlot;     // ring of [128 keys][128 bytes]
+    static constexpr int kBars = kV + kExpSlots * kExpVSlot;
+    static constexpr int kFullK = kBars, kEmptyK = kFullK + 8 * kExpSlots, kReadyK = kEmptyK + 8 * kExpSlots;
+    static constexpr int kFullV = kReadyK + 8 * kExpSlots, kEmptyV = kFullV + 8 * kExpSlots, kReadyV = kEmptyV + 8 * kExpSlots;
+    static constexpr int kFullQ = kReadyV + 8 * kExpSlots, kEmptyQ = kFullQ + 16, kReadyQ = kEmptyQ + 16;  // a tile each
+    static constexpr int kScores = kReadyQ + 16, kWeights = kScores + 16, kDrain = kWeights + 16;
     static constexpr int kBarsEnd = kDrain + 8;
     static constexpr int kMisc = kBarsEnd;                    // flags, TMEM address
     static constexpr int kSums = kMisc + 16;                  // int [12]: the scan's sums
@@ -58,9 +63,9 @@ struct ExpSmem {
 static_assert(ExpSmem::kBytes <= 227 * 1024, "it fits");
 static_assert(kPagedMaxTokens / kExpRows + kPagedMaxSeqs < 65536, "tasks of a head fit 16 bits");
 
-// Tasks and how they are dealt out to `grid` blocks, from what a scan over the requests finds.
+// Tasks and how they are dealt out to `grid` clusters, from what a scan over the requests finds.
 struct ExpPlan {
-    int full;   // rounds in which every block has a task
+    int full;   // rounds in which every cluster has a task
     int rest;   // tasks behind them
     int parts;  // that each of those is split into at most
 };
@@ -74,14 +79,14 @@ CFA_HD ExpPlan latent_expanded_plan(int tasks, int grid) {
 
 // A task's part.
 struct ExpItem {
-    int req, h, tile;          // request, head, tile of 256 tokens
+    int req, h, tile;          // request, head, which 512 of its tokens
     int tok0, n, k0, len;      // the request's tokens and keys
     int part, parts;           // which of how many parts of its blocks
-    int b0, end0, end1;        // first block of keys, and behind the last one that each tile of 128 sees
+    int b0, end0, end1;        // first block of keys, and behind the last one that each tile sees
     int rec;                   // its record's number
     __device__ __forceinline__ int end(int t) const { return t ? end1 : end0; }
     __device__ __forceinline__ int last() const { return max(end0, end1); }
-    __device__ __forceinline__ int rows(int t) const { return max(0, min(128, n - tile * kExpRows - 128 * t)); }
+    __device__ __forceinline__ int rows(int t) const { return max(0, min(kExpTile, n - tile * kExpRows - kExpTile * t)); }
     // keys that token i of the request sees
     __device__ __forceinline__ int visible(int i) const { return max(0, min(len, len - n + i + 1)); }
 };
@@ -142,7 +147,7 @@ __device__ __forceinline__ bool latent_expanded_item(const LatentExpandedParams 
     x.len = __ldcg(p.cu_k + lo + 1) - x.k0;
     auto blocks_of = [&](int t) {
         const int rows = x.rows(t);
-        return rows > 0 ? (x.visible(x.tile * kExpRows + 128 * t + rows - 1) + 127) / 128 : 0;
+        return rows > 0 ? (x.visible(x.tile * kExpRows + kExpTile * t + rows - 1) + 127) / 128 : 0;
     };
     const int e0 = blocks_of(0), e1 = blocks_of(1), blocks = max(e0, e1);
     x.part = part;
@@ -158,13 +163,14 @@ __device__ __forceinline__ bool latent_expanded_item(const LatentExpandedParams 
 __device__ __forceinline__ void registers_of_softmax() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
 __device__ __forceinline__ void registers_of_loads() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
 
-__global__ void __launch_bounds__(kExpThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
 latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                        const __grid_constant__ CUtensorMap tm_rope, const __grid_constant__ LatentExpandedParams p) {
     using S = ExpSmem;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = smem_addr(smem);
+    const int rank = static_cast<int>(cluster_ctarank()), cluster = static_cast<int>(blockIdx.x) >> 1;
     int *misc = reinterpret_cast<int *>(smem + S::kMisc);
     volatile int *timed_out = misc;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 1);
@@ -173,29 +179,38 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     // a thread a barrier, with the arrivals it expects
     if (tid < (S::kBarsEnd - S::kBars) / 8) {
         const int at = S::kBars + 8 * tid;
-        mbar_init(base + at, (at >= S::kEmptyQ && at < S::kScores) || (at >= S::kWeights && at < S::kDrain) ? 4 : 1);
+        uint32_t count = 1;
+        if ((at >= S::kReadyK && at < S::kFullV) || (at >= S::kReadyV && at < S::kFullQ) || (at >= S::kReadyQ && at < S::kScores))
+            count = 2;  // the relays of both blocks
+        if (at >= S::kEmptyQ && at < S::kReadyQ) count = 4;   // a tile's warps
+        if (at >= S::kWeights && at < S::kDrain) count = 8;   // and those of both blocks
+        mbar_init(base + at, count);
         fence_mbar_init();
     }
     if (tid == 0) misc[0] = 0;
-    if (warp == kExpMmaWarp) tmem_alloc(smem_addr(tmem_slot), 512);
+    if (warp == kExpMmaWarp) tmem2_alloc(smem_addr(tmem_slot), 512);
     if (warp == kExpLoadWarp && elect_one()) {
         prefetch_tensor_map(&tm_q);
         prefetch_tensor_map(&tm_kv);
         prefetch_tensor_map(&tm_rope);
     }
+    __syncwarp();
     tcgen05_fence_before();
+    cluster_arrive();  // (the other block's barriers are ready behind the wait below)
     grid_dependency_wait();
     const int tasks = latent_expanded_scan<kExpThreads>(p, reinterpret_cast<uint16_t *>(smem + S::kTiles),
                                                         reinterpret_cast<int *>(smem + S::kSums));
     tcgen05_fence_after();
     if (blockIdx.x == 0 && tid == 0 && tasks < 0) atomicOr(p.status, kStatusBadLengthBit);
     grid_dependents_launch();
+    __syncwarp();
+    cluster_wait();
     const uint32_t tmem = *tmem_slot;
-    const int grid = static_cast<int>(gridDim.x);
+    const int grid = static_cast<int>(gridDim.x) >> 1;
     const ExpPlan plan = latent_expanded_plan(max(0, tasks), grid);
-    // The block's item of round r; false where it has none.
+    // The cluster's item of round r; false where it has none.
     auto item = [&](int r, ExpItem &x) {
-        const int at = r & 1 ? grid - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
+        const int at = r & 1 ? grid - 1 - cluster : cluster;
         if (r < plan.full) return latent_expanded_item(p, tiles, r * grid + at, 0, 1, x);
         const int task = at / plan.parts, part = at - task * plan.parts;
         x.rec = at;
@@ -213,54 +228,51 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         if (warp == kExpLoadWarp || warp == kExpLoadWarp + 1) {
             // -------------------------------------- load warps: keys and queries, values
             const bool values = warp != kExpLoadWarp;
-            uint32_t n = 0, queried = 0, queries = 0;  // slots; tiles whose queries were ever loaded, and phases, a bit a tile
+            uint32_t n = 0, queried = 0, queries = 0;  // blocks; tiles whose queries were ever loaded, and phases, a bit a tile
             bool ok = true;
             CFA_ROLLED for (int r = 0; ok && r < rounds; ++r) {
                 ExpItem x;
                 if (!item(r, x)) continue;
                 const int last = x.last();
-                if (!values) {
+                CFA_ROLLED for (int b = x.b0; ok && b < last; ++b, ++n) {
+                    const uint32_t slot = n % kExpSlots, again = n / kExpSlots;
+                    const int full = (values ? S::kFullV : S::kFullK) + 8 * slot;
+                    if (again > 0) ok = wait_warp((values ? S::kEmptyV : S::kEmptyK) + 8 * slot, (again - 1) & 1, kSiteStageEmpty);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        if (!values) {  // 64 of the keys
+                            const uint32_t dst = base + S::kK + slot * kExpKSlot;
+                            const int y = x.k0 + 128 * b + 64 * rank;
+                            mbar_arrive_expect_tx(base + full, kExpKSlot);
+                            tma_load_2d(dst, &tm_kv, x.h * kLatKv, y, base + full);
+                            tma_load_2d(dst + 64 * 128, &tm_kv, x.h * kLatKv + 64, y, base + full);
+                            tma_load_2d(dst + 2 * 64 * 128, &tm_rope, 0, y, base + full);
+                        } else {        // 64 of the dims
+                            const uint32_t dst = base + S::kV + slot * kExpVSlot;
+                            const int dim = x.h * kLatKv + kLatN + 64 * rank, y = x.k0 + 128 * b;
+                            mbar_arrive_expect_tx(base + full, kExpVSlot);
+                            tma_load_2d(dst, &tm_kv, dim, y, base + full);
+                            tma_load_2d(dst + 64 * 128, &tm_kv, dim, y + 64, base + full);
+                        }
+                    }
+                    __syncwarp();
+                    if (values || b > x.b0) continue;
+                    // the queries behind the first keys, which find room earlier
                     CFA_ROLLED for (int t = 0; ok && t < 2; ++t) {
                         if (x.end(t) == x.b0) continue;
                         if (queried >> t & 1) ok = wait_warp(S::kEmptyQ + 8 * t, ~queries >> t & 1, kSiteStageEmpty);
                         if (!ok) break;
                         if (elect_one()) {
-                            const uint32_t full = base + S::kFullQ + 8 * t;
-                            mbar_arrive_expect_tx(full, 3 * kExpChunk);
+                            const uint32_t full_q = base + S::kFullQ + 8 * t;
+                            mbar_arrive_expect_tx(full_q, 3 * kExpChunk);
 #pragma unroll
                             for (int c = 0; c < 3; ++c)
                                 tma_load_2d(base + S::kQ + (3 * t + c) * kExpChunk, &tm_q, x.h * kLatQ + 64 * c,
-                                            x.tok0 + x.tile * kExpRows + 128 * t, full);
+                                            x.tok0 + x.tile * kExpRows + kExpTile * t + 128 * rank, full_q);
                         }
                         __syncwarp();
                         queried |= 1u << t;
                         queries ^= 1u << t;
-                    }
-                    CFA_ROLLED for (int b = x.b0; ok && b < last; ++b)
-                        CFA_ROLLED for (int c = 0; c < 3; ++c, ++n) {
-                            const uint32_t slot = n % kExpKSlots, full = base + S::kFullK + 8 * slot;
-                            if (n >= kExpKSlots) ok = wait_warp(S::kEmptyK + 8 * slot, (n / kExpKSlots - 1) & 1, kSiteStageEmpty);
-                            if (!ok) break;
-                            if (elect_one()) {
-                                mbar_arrive_expect_tx(full, kExpChunk);
-                                if (c < 2) tma_load_2d(base + S::kK + slot * kExpChunk, &tm_kv, x.h * kLatKv + 64 * c, x.k0 + 128 * b, full);
-                                else tma_load_2d(base + S::kK + slot * kExpChunk, &tm_rope, 0, x.k0 + 128 * b, full);
-                            }
-                            __syncwarp();
-                        }
-                } else {
-                    CFA_ROLLED for (int b = x.b0; ok && b < last; ++b, ++n) {
-                        const uint32_t slot = n % kExpVSlots, full = base + S::kFullV + 8 * slot;
-                        if (n >= kExpVSlots) ok = wait_warp(S::kEmptyV + 8 * slot, (n / kExpVSlots - 1) & 1, kSiteStageEmpty);
-                        if (!ok) break;
-                        if (elect_one()) {
-                            mbar_arrive_expect_tx(full, 2 * kExpChunk);
-#pragma unroll
-                            for (int c = 0; c < 2; ++c)
-                                tma_load_2d(base + S::kV + (2 * slot + c) * kExpChunk, &tm_kv, x.h * kLatKv + kLatN + 64 * c,
-                                            x.k0 + 128 * b, full);
-                        }
-                        __syncwarp();
                     }
                 }
             }
@@ -271,93 +283,107 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kDrainTimeoutFactor * p.timeout_ns) {
                     }
                 };
-                const uint32_t slots = values ? kExpVSlots : kExpKSlots;
-                for (uint32_t k = n > slots ? n - slots : 0; k < n; ++k)
-                    land(base + (values ? S::kFullV : S::kFullK) + 8 * (k % slots), (k / slots) & 1);
+                for (uint32_t k = n > kExpSlots ? n - kExpSlots : 0; k < n; ++k)
+                    land(base + (values ? S::kFullV : S::kFullK) + 8 * (k % kExpSlots), (k / kExpSlots) & 1);
                 for (int t = 0; !values && t < 2; ++t)
                     if (queried >> t & 1) land(base + S::kFullQ + 8 * t, ~queries >> t & 1);
             }
             __syncwarp();
-        } else if (warp == kExpMmaWarp) {
-            // ------------------------------------------------------------------- products
+        } else if (warp == kExpRelayWarp) {
+            // ----------------------------------------------------------------- relay warp
+            // tells the issuing block what has landed, in the order in which the products take it: keys of a
+            // block ahead, values
+            uint32_t nk = 0, nv = 0, queries = 0;
+            const uint32_t ready_k = map_to_rank(base + S::kReadyK, 0), ready_v = map_to_rank(base + S::kReadyV, 0),
+                           ready_q = map_to_rank(base + S::kReadyQ, 0);
+            bool ok = true;
+            auto pass_on = [&](int full, uint32_t ready, uint32_t parity) {
+                ok = ok && wait_warp(full, parity, kSiteStageFull);
+                if (ok && elect_one()) mbar_arrive_pair(ready);
+                __syncwarp();
+            };
+            auto keys = [&]() {
+                pass_on(S::kFullK + 8 * (nk % kExpSlots), ready_k + 8 * (nk % kExpSlots), (nk / kExpSlots) & 1);
+                ++nk;
+            };
+            CFA_ROLLED for (int r = 0; ok && r < rounds; ++r) {
+                ExpItem x;
+                if (!item(r, x) || x.last() == x.b0) continue;
+                keys();
+                CFA_ROLLED for (int t = 0; t < 2; ++t) {
+                    if (x.end(t) == x.b0) continue;
+                    pass_on(S::kFullQ + 8 * t, ready_q + 8 * t, queries >> t & 1);
+                    queries ^= 1u << t;
+                }
+                CFA_ROLLED for (int b = x.b0; ok && b < x.last(); ++b, ++nv) {
+                    if (b + 1 < x.last()) keys();
+                    pass_on(S::kFullV + 8 * (nv % kExpSlots), ready_v + 8 * (nv % kExpSlots), (nv / kExpSlots) & 1);
+                }
+            }
+        } else if (warp == kExpMmaWarp && rank == 0) {
+            // -------------------------------------------------- products, by the first block
             const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
-            const uint32_t idesc_s = umma_idesc_bf16(128, 128, false, false), idesc_o = umma_idesc_bf16(128, 128, false, true);
+            const uint32_t idesc_s = umma_idesc_bf16(256, 128, false, false), idesc_o = umma_idesc_bf16(256, 128, false, true);
             const uint64_t q0 = umma_smem_desc(base + S::kQ, 16, 1024), k0 = umma_smem_desc(base + S::kK, 16, 1024),
-                           v0 = umma_smem_desc(base + S::kV, kExpChunk, 1024);
-            uint32_t nk = 0, nv = 0, queries = 0, weights = 0;  // chunks and blocks before the item's; phases, a bit a tile
+                           v0 = umma_smem_desc(base + S::kV, kExpVSlot, 1024);
+            uint32_t n = 0, queries = 0, weights = 0;  // blocks before the item's; phases, a bit a tile
             bool ok = true;
             CFA_ROLLED for (int r = 0; ok && r < rounds; ++r) {
                 ExpItem x;
                 if (!item(r, x)) continue;
                 const int last = x.last(), b0 = x.b0;
-                // Chunk c of block b's keys: its slot, and whether it has landed.
-                auto slot_of = [&](int b, int c) { return (nk + 3 * (b - b0) + c) % kExpKSlots; };
-                auto parity_of = [&](int b, int c) { return (nk + 3 * (b - b0) + c) / kExpKSlots & 1; };
-                // By one thread: the products of chunk c for tile t's scores. `frees`: nobody reads the keys after.
-                auto score_chunk = [&](int t, int b, int c, bool frees) {
-                    const uint32_t slot = slot_of(b, c);
-                    const uint64_t a = q0 + (3 * t + c) * (kExpChunk >> 4), bd = k0 + slot * (kExpChunk >> 4);
+                // By one thread: scores of tile t and block b. `frees`: nobody reads the keys after.
+                auto scores = [&](int t, int b, bool frees) {
+                    const uint32_t slot = (n + b - b0) % kExpSlots;
+                    const uint64_t a = q0 + 3 * t * (kExpChunk >> 4), bd = k0 + slot * (kExpKSlot >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)  // 32 bytes a step
-                        umma_bf16(tm + 128 * t, a + 2 * ks, bd + 2 * ks, idesc_s, c > 0 || ks > 0);
-                    if (frees) umma_commit(base + S::kEmptyK + 8 * slot);
-                    if (c == 2) umma_commit(base + S::kScores + 8 * t);
+                    for (int ks = 0; ks < 12; ++ks)  // 32 bytes a step
+                        umma2_bf16(tm + 128 * t, a + (ks >> 2) * (kExpChunk >> 4) + 2 * (ks & 3),
+                                   bd + (ks >> 2) * (64 * 128 >> 4) + 2 * (ks & 3), idesc_s, ks > 0);
+                    if (frees) umma2_commit(base + S::kEmptyK + 8 * slot);
+                    umma2_commit(base + S::kScores + 8 * t);
                 };
-                auto scores = [&](int t, int b, bool frees, bool landed) {
-                    CFA_ROLLED for (int c = 0; ok && c < 3; ++c) {
-                        if (!landed) ok = wait_warp(S::kFullK + 8 * slot_of(b, c), parity_of(b, c), kSiteStageFull);
-                        tcgen05_fence_after();
-                        if (ok && elect_one()) score_chunk(t, b, c, frees);
-                        __syncwarp();
-                    }
+                auto keys = [&](int b) {
+                    const uint32_t k = n + b - b0;
+                    ok = ok && wait_warp(S::kReadyK + 8 * (k % kExpSlots), (k / kExpSlots) & 1, kSiteStageFull);
                 };
+                if (last > b0) keys(b0);
                 CFA_ROLLED for (int t = 0; ok && t < 2; ++t) {
                     if (x.end(t) == b0) continue;
-                    ok = wait_warp(S::kFullQ + 8 * t, queries >> t & 1, kSiteQExchange);
+                    ok = wait_warp(S::kReadyQ + 8 * t, queries >> t & 1, kSiteQExchange);
                     queries ^= 1u << t;
-                    if (ok) scores(t, b0, t == 1 || x.end1 == b0, t == 1 && x.end0 > b0);
+                    tcgen05_fence_after();
+                    if (ok && elect_one()) scores(t, b0, t == 1 || x.end1 == b0);
+                    __syncwarp();
                 }
-                CFA_ROLLED for (int b = b0; ok && b < last; ++b)
+                CFA_ROLLED for (int b = b0; ok && b < last; ++b) {
+                    const uint32_t slot = (n + b - b0) % kExpSlots;
+                    if (b + 1 < last) keys(b + 1);
+                    ok = ok && wait_warp(S::kReadyV + 8 * slot, ((n + b - b0) / kExpSlots) & 1, kSiteStageFull);
                     CFA_ROLLED for (int t = 0; ok && t < 2; ++t) {
                         if (b >= x.end(t)) continue;
-                        const uint32_t v = nv + b - b0, slot = v % kExpVSlots;
-                        const bool more = b + 1 < x.end(t);
-                        // what the first tile waited for need not be asked for again
-                        if (t == 0 || b >= x.end0) ok = wait_warp(S::kFullV + 8 * slot, (v / kExpVSlots) & 1, kSiteStageFull);
-                        bool landed = t == 1 && b + 1 < x.end0;
-                        if (more && !landed) {
-                            landed = true;
-#pragma unroll
-                            for (int c = 0; c < 3; ++c) landed = landed && mbar_try_wait(base + S::kFullK + 8 * slot_of(b + 1, c), parity_of(b + 1, c));
-                            landed = __all_sync(~0u, landed);
-                        }
-                        ok = ok && wait_warp(S::kWeights + 8 * t, weights >> t & 1, kSiteSoftmaxExchange);
+                        ok = wait_warp(S::kWeights + 8 * t, weights >> t & 1, kSiteSoftmaxExchange);
                         weights ^= 1u << t;
                         tcgen05_fence_after();
+                        // the product and the next scores in one go: between two goes the tensor core runs dry for some 400 clocks
                         if (ok && elect_one()) {
-                            const uint64_t vd = v0 + slot * (2 * kExpChunk >> 4);
 #pragma unroll
                             for (int ks = 0; ks < 8; ++ks)  // 16 keys of 128 bytes a step
-                                umma_bf16_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * ks, vd + 128 * ks, idesc_o, b > b0 || ks > 0);
-                            if (t == 1 || b >= x.end1) umma_commit(base + S::kEmptyV + 8 * slot);
+                                umma2_bf16_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * ks, v0 + slot * (kExpVSlot >> 4) + 128 * ks,
+                                              idesc_o, b > b0 || ks > 0);
+                            if (t == 1 || b >= x.end1) umma2_commit(base + S::kEmptyV + 8 * slot);
                             // behind the last product there are no more scores, but the tile's warps learn that it ended
-                            if (!more) umma_commit(base + S::kScores + 8 * t);
-                            // both products in one go where the keys are there: between two goes the tensor core runs dry
-                            // for some 400 clocks
-                            if (more && landed) {
-#pragma unroll
-                                for (int c = 0; c < 3; ++c) score_chunk(t, b + 1, c, t == 1 || b + 1 >= x.end1);
-                            }
+                            if (b + 1 < x.end(t)) scores(t, b + 1, t == 1 || b + 1 >= x.end1);
+                            else umma2_commit(base + S::kScores + 8 * t);
                         }
                         __syncwarp();
-                        if (ok && more && !landed) scores(t, b + 1, t == 1 || b + 1 >= x.end1, false);
                     }
-                nk += 3 * (last - b0);
-                nv += last - b0;
+                }
+                n += last - b0;
             }
             if (elect_one() && *timed_out) {
-                // a wait gave up: the products in flight end before the block does
-                umma_commit(base + S::kDrain);
+                // a wait gave up: the products in flight end before the blocks do
+                umma2_commit(base + S::kDrain);
                 const uint64_t t0 = global_timer_ns();
                 while (!mbar_try_wait(base + S::kDrain, 0) && global_timer_ns() - t0 < kDrainTimeoutFactor * p.timeout_ns) {
                 }
@@ -371,15 +397,16 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lanes of this warp
         const uint32_t t_s = tmem + lanes + 128 * t, t_o = tmem + lanes + 256 + 128 * t;
         const int scores = S::kScores + 8 * t;
-        const uint32_t weights = base + S::kWeights + 8 * t;
+        const uint32_t weights = map_to_rank(base + S::kWeights, 0) + 8 * t;
         uint32_t scored = 0, nv = 0;  // phases; blocks before the item's
         CFA_ROLLED for (int r = 0; r < rounds; ++r) {
             ExpItem x;
             if (!item(r, x)) continue;
-            const int rows = x.rows(t), first = x.tile * kExpRows + 128 * t;
+            const int first = x.tile * kExpRows + kExpTile * t + 128 * rank;  // this block's first token of the tile
+            const int rows = max(0, min(128, x.rows(t) - 128 * rank));
             const bool live = row < rows, warp_live = row - lane < rows;
             const int see = live ? x.visible(first + row) : 0;
-            const int some = x.visible(first);  // keys that every row of the tile sees
+            const int some = x.visible(x.tile * kExpRows + kExpTile * t);  // keys that every row of the tile sees
             const int all = x.visible(min(x.n, x.tile * kExpRows + kExpRows) - 1);  // and any row of the task
             float m = -INFINITY, l = 0.f;
             CFA_ROLLED for (int b = x.b0; b < x.end(t); ++b, ++scored) {
@@ -444,11 +471,11 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     // keys from `some` on are not seen by every row, from `all` on by none. A masked weight is 0, and
                     // 0 times NaN is NaN: what is not finite of the first becomes 0 here, and the merge adds it to the rows
                     // that see it; the others become 0. (Where the other tile's product runs meanwhile, either way does.)
-                    const uint32_t v = nv + b - x.b0, slot = v % kExpVSlots;
-                    wait(S::kFullV + 8 * slot, (v / kExpVSlots) & 1, kSiteStageFull);
+                    const uint32_t v = nv + b - x.b0, slot = v % kExpSlots;
+                    wait(S::kFullV + 8 * slot, (v / kExpSlots) & 1, kSiteStageFull);
                     __syncwarp();
-                    uint8_t *vals = smem + S::kV + 2 * slot * kExpChunk + ((row >> 3) & 1) * kExpChunk + ((row & 7) << 4);
-                    CFA_ROLLED for (int k = max(0, some - 128 * b) + (row >> 4); k < 128; k += 8) {
+                    uint8_t *vals = smem + S::kV + slot * kExpVSlot + ((row & 7) << 4);
+                    CFA_ROLLED for (int k = max(0, some - 128 * b) + (row >> 3); k < 128; k += 16) {
                         uint4 *at = reinterpret_cast<uint4 *>(vals + k * 128);  // (of a row's chunks any order will do)
                         uint4 d = make_uint4(0u, 0u, 0u, 0u);
                         if (128 * b + k < all) {
@@ -464,7 +491,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 }
                 tcgen05_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(weights);
+                if (lane == 0) mbar_arrive_pair(weights);
             }
             const bool any = x.end(t) > x.b0;
             if (any) {
@@ -476,10 +503,11 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             // ---- the tile's results, or its record
             nv += x.last() - x.b0;
             if (warp_live) {
+                const int in_task = kExpTile * t + 128 * rank + row;
                 const size_t tok = static_cast<size_t>(x.tok0 + first + row);
                 if (x.parts > 1) {
-                    if (live) p.rec_ml[x.rec * kExpRows + 128 * t + row] = make_float2(m, l);
-                    float *rec_o = p.rec_o + static_cast<size_t>(x.rec) * kExpRows * kLatV + 4 * (128 * t + row);
+                    if (live) p.rec_ml[x.rec * kExpRows + in_task] = make_float2(m, l);
+                    float *rec_o = p.rec_o + static_cast<size_t>(x.rec) * kExpRows * kLatV + 4 * in_task;
 #pragma unroll 1
                     for (int c = 0; any && c < kLatV; c += 32) {  // (without keys: m says that nothing is there)
                         uint32_t v[32];
@@ -542,9 +570,10 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     }
     tcgen05_fence_before();
     __syncthreads();
+    cluster_sync_all();  // nothing of either block reaches into the other any more
     if (warp == kExpMmaWarp) {
         tcgen05_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem2_dealloc(tmem, 512);
     }
 }
 
@@ -596,8 +625,8 @@ __global__ void __launch_bounds__(kLatMergeThreads, 3) latent_expanded_merge_ker
         const int lane = threadIdx.x & 31, warps = static_cast<int>(gridDim.x) * (kLatMergeThreads / 32);
         constexpr int kRec = kExpRows * (kLatV / 4);
         CFA_ROLLED for (int i = static_cast<int>(blockIdx.x) * (kLatMergeThreads / 32) + (threadIdx.x >> 5);
-                        plan.parts > 1 && i < plan.rest * 64; i += warps) {
-            const int task = i >> 6, row = (i & 7) * 32 + lane, chunk = (i >> 3 & 7) * 4;
+                        plan.parts > 1 && i < plan.rest * 128; i += warps) {
+            const int task = i >> 7, row = (i & 15) * 32 + lane, chunk = (i >> 4 & 7) * 4;
             ExpItem x;
             latent_expanded_item(p, tiles, plan.full * p.grid + task, 0, plan.parts, x);
             const int tok = x.tile * kExpRows + row;
