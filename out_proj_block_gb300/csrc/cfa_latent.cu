@@ -21,8 +21,10 @@
 
 namespace cfa {
 const void *latent_append_kernel_ptr(bool interleaved);
-const void *latent_fold_kernel_ptr();
-const void *latent_unfold_kernel_ptr();
+const void *latent_fold_kernel_ptr(int tm);
+const void *latent_unfold_kernel_ptr(int tm);
+int latent_fold_smem(int tm);
+int latent_unfold_smem(int tm);
 const void *latent_attention_kernel_ptr();
 const void *latent_merge_kernel_ptr();
 const void *latent_expanded_kernel_ptr();
@@ -205,20 +207,42 @@ cfa_status launch_append(cfa_latent *p, const AppendArgs &a, void *stream) {
                   cfa::kLatAppendThreads, 0, stream, args);
 }
 
-cfa_status launch_fold(cfa_latent *p, int T, const void *q, long long qs, const void *w, void *y, void *stream) {
-    cfa::LatentHeadsParams kp{static_cast<const uint16_t *>(q), qs, static_cast<const uint16_t *>(w),
-                              static_cast<uint16_t *>(y), T, p->nh};
+// Tokens of a block of the folding kernels.
+int heads_tokens(int T) { return T <= 32 ? 16 : T <= 256 ? 64 : 128; }
+
+cfa_status launch_heads(const void *kernel, int smem, int tm, unsigned split, cfa::LatentHeadsParams kp, void *stream) {
     void *args[1] = {&kp};
-    return launch(cfa::latent_fold_kernel_ptr(),
-                  dim3(static_cast<unsigned>((T + 63) / 64), static_cast<unsigned>(p->nh)), 256, 0, stream, args);
+    return launch(kernel, dim3(static_cast<unsigned>((kp.T + tm - 1) / tm), static_cast<unsigned>(kp.H), split),
+                  tm > 64 ? 256 : 128, static_cast<size_t>(smem), stream, args);
+}
+
+cfa_status launch_fold(cfa_latent *p, int T, const void *q, long long qs, const void *w, void *y, void *stream) {
+    const int tm = heads_tokens(T);
+    return launch_heads(cfa::latent_fold_kernel_ptr(tm), cfa::latent_fold_smem(tm), tm, 4,
+                        {static_cast<const uint16_t *>(q), qs, static_cast<const uint16_t *>(w),
+                         static_cast<uint16_t *>(y), T, p->nh},
+                        stream);
 }
 
 cfa_status launch_unfold(cfa_latent *p, int T, const void *o, const void *w, void *y, void *stream) {
-    cfa::LatentHeadsParams kp{static_cast<const uint16_t *>(o), static_cast<long long>(p->nh) * kLatC,
-                              static_cast<const uint16_t *>(w), static_cast<uint16_t *>(y), T, p->nh};
-    void *args[1] = {&kp};
-    return launch(cfa::latent_unfold_kernel_ptr(),
-                  dim3(static_cast<unsigned>((T + 63) / 64), static_cast<unsigned>(p->nh)), 256, 0, stream, args);
+    const int tm = heads_tokens(T);
+    return launch_heads(cfa::latent_unfold_kernel_ptr(tm), cfa::latent_unfold_smem(tm), tm, tm == 16 ? 4 : 1,
+                        {static_cast<const uint16_t *>(o), static_cast<long long>(p->nh) * kLatC,
+                         static_cast<const uint16_t *>(w), static_cast<uint16_t *>(y), T, p->nh},
+                        stream);
+}
+
+// Lets the kernels have the shared memory that they ask for.
+bool allow_smem() {
+    auto allow = [](const void *kernel, int bytes) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+    };
+    bool ok = allow(cfa::latent_attention_kernel_ptr(), cfa::latent_attention_smem()) &&
+              allow(cfa::latent_expanded_kernel_ptr(), cfa::latent_expanded_smem());
+    for (const int tm : {16, 64, 128})
+        ok = ok && allow(cfa::latent_fold_kernel_ptr(tm), cfa::latent_fold_smem(tm)) &&
+             allow(cfa::latent_unfold_kernel_ptr(tm), cfa::latent_unfold_smem(tm));
+    return ok;
 }
 
 cfa_status launch_attention(cfa_latent *p, const AttnArgs &a, void *stream) {
@@ -301,10 +325,7 @@ cfa_latent *cfa_latent_create(int max_seqs, int max_tokens, int n_heads, int pag
     p->num_sms = sms;
     p->runs = std::min(sms / 2, cfa::kLatMaxRuns);
     const size_t rec_rows = 2u * static_cast<size_t>(p->runs) * cfa::kLatTile;
-    if (cudaFuncSetAttribute(cfa::latent_attention_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             cfa::latent_attention_smem()) != cudaSuccess ||
-        cudaFuncSetAttribute(cfa::latent_expanded_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             cfa::latent_expanded_smem()) != cudaSuccess ||
+    if (!allow_smem() ||
         cudaMalloc(&p->words, 3 * sizeof(unsigned)) != cudaSuccess || !clear_words(p->words, 3) ||
         cudaMalloc(&p->rec_o, sizeof(float) * rec_rows * kLatC) != cudaSuccess ||
         // (twice the rows: the expanded form's records are 512 rows of 128 dims, one a cluster)
