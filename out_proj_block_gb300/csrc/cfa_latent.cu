@@ -21,10 +21,10 @@
 
 namespace cfa {
 const void *latent_append_kernel_ptr(bool interleaved);
-const void *latent_fold_kernel_ptr(int tm);
-const void *latent_unfold_kernel_ptr(int tm);
-int latent_fold_smem(int tm);
-int latent_unfold_smem(int tm);
+const void *latent_heads_kernel_ptr(bool fold);
+int latent_heads_smem(bool fold);
+const void *latent_heads_mma_kernel_ptr(bool fold);
+int latent_heads_mma_smem(bool fold);
 const void *latent_attention_kernel_ptr();
 const void *latent_merge_kernel_ptr();
 const void *latent_expanded_kernel_ptr();
@@ -207,29 +207,41 @@ cfa_status launch_append(cfa_latent *p, const AppendArgs &a, void *stream) {
                   cfa::kLatAppendThreads, 0, stream, args);
 }
 
-// Tokens of a block of the folding kernels.
-int heads_tokens(int T) { return T <= 32 ? 16 : T <= 256 ? 64 : 128; }
-
-cfa_status launch_heads(const void *kernel, int smem, int tm, unsigned split, cfa::LatentHeadsParams kp, void *stream) {
-    void *args[1] = {&kp};
-    return launch(kernel, dim3(static_cast<unsigned>((kp.T + tm - 1) / tm), static_cast<unsigned>(kp.H), split),
-                  tm > 64 ? 256 : 128, static_cast<size_t>(smem), stream, args);
+// The folding product: x rows of each head, xs elements between tokens.
+cfa_status launch_heads(cfa_latent *p, bool fold, int T, const void *x, long long xs, const void *w, void *y, void *stream) {
+    cfa::LatentHeadsParams kp{static_cast<const uint16_t *>(x), xs, static_cast<const uint16_t *>(w),
+                              static_cast<uint16_t *>(y), T, p->nh, p->words, kTimeoutNs};
+    // Few tokens go to many small blocks, which read the weights once for 16 of them; many to tcgen05, which reads
+    // them once but takes 1 us more to begin. By 16 tokens times heads, in us, in (few, many): 32 heads, 128 tokens
+    // (256) 6.1 and 6.9, 200 (416) 7.6 and 6.5; 128 heads, 48 (384) 7.9 and 8.9, 100 (896) 12.4 and 9.3. Out: 32 heads,
+    // 64 (128) 4.6 and 6.4, 100 (224) 7.2 and 6.6; 128 heads, 16 (128) 6.1 and 7.8, 32 (256) 8.9 and 7.9.
+    const long long work = (T + cfa::kHeadsTokens - 1ll) / cfa::kHeadsTokens * p->nh;
+    if (work <= (fold ? 384 : 160)) {
+        void *args[1] = {&kp};
+        return launch(cfa::latent_heads_kernel_ptr(fold),
+                      dim3(static_cast<unsigned>((T + cfa::kHeadsTokens - 1) / cfa::kHeadsTokens), static_cast<unsigned>(p->nh), 4),
+                      128, static_cast<size_t>(cfa::latent_heads_smem(fold)), stream, args);
+    }
+    const uint64_t H = static_cast<uint64_t>(p->nh), in = H * (fold ? kLatQ : kLatC), out = H * (fold ? kLatRow : kLatV),
+                   rows = static_cast<uint64_t>(T);
+    CUtensorMap tx, tw, ty;
+    if (cfa::encode_bf16_2d_ex(&tx, x, in, rows, static_cast<uint64_t>(xs), 64, 128, true) != CFA_OK ||
+        cfa::encode_bf16_2d_ex(&tw, w, H * kLatKv, kLatC, H * kLatKv, 64, 64, true) != CFA_OK ||
+        cfa::encode_bf16_2d_ex(&ty, y, out, rows, out, 64, 128, true) != CFA_OK)
+        return CFA_ERR_CUDA;
+    void *args[4] = {&tx, &tw, &ty, &kp};
+    const long long jobs = static_cast<long long>(p->nh) * (fold ? 2 : 1) * ((T + 127) / 128);
+    return launch(cfa::latent_heads_mma_kernel_ptr(fold),
+                  dim3(static_cast<unsigned>(std::min<long long>(jobs, p->num_sms))), cfa::kHeadsMmaThreads,
+                  static_cast<size_t>(cfa::latent_heads_mma_smem(fold)), stream, args);
 }
 
 cfa_status launch_fold(cfa_latent *p, int T, const void *q, long long qs, const void *w, void *y, void *stream) {
-    const int tm = heads_tokens(T);
-    return launch_heads(cfa::latent_fold_kernel_ptr(tm), cfa::latent_fold_smem(tm), tm, 4,
-                        {static_cast<const uint16_t *>(q), qs, static_cast<const uint16_t *>(w),
-                         static_cast<uint16_t *>(y), T, p->nh},
-                        stream);
+    return launch_heads(p, true, T, q, qs, w, y, stream);
 }
 
 cfa_status launch_unfold(cfa_latent *p, int T, const void *o, const void *w, void *y, void *stream) {
-    const int tm = heads_tokens(T);
-    return launch_heads(cfa::latent_unfold_kernel_ptr(tm), cfa::latent_unfold_smem(tm), tm, tm == 16 ? 4 : 1,
-                        {static_cast<const uint16_t *>(o), static_cast<long long>(p->nh) * kLatC,
-                         static_cast<const uint16_t *>(w), static_cast<uint16_t *>(y), T, p->nh},
-                        stream);
+    return launch_heads(p, false, T, o, static_cast<long long>(p->nh) * kLatC, w, y, stream);
 }
 
 // Lets the kernels have the shared memory that they ask for.
@@ -239,9 +251,9 @@ bool allow_smem() {
     };
     bool ok = allow(cfa::latent_attention_kernel_ptr(), cfa::latent_attention_smem()) &&
               allow(cfa::latent_expanded_kernel_ptr(), cfa::latent_expanded_smem());
-    for (const int tm : {16, 64, 128})
-        ok = ok && allow(cfa::latent_fold_kernel_ptr(tm), cfa::latent_fold_smem(tm)) &&
-             allow(cfa::latent_unfold_kernel_ptr(tm), cfa::latent_unfold_smem(tm));
+    for (const bool fold : {false, true})
+        ok = ok && allow(cfa::latent_heads_kernel_ptr(fold), cfa::latent_heads_smem(fold)) &&
+             allow(cfa::latent_heads_mma_kernel_ptr(fold), cfa::latent_heads_mma_smem(fold));
     return ok;
 }
 

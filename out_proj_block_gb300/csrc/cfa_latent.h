@@ -47,7 +47,12 @@ struct LatentHeadsParams {
     const uint16_t *w;    // W_kvb
     uint16_t *y;          // fold: [T][H][576]; unfold: [T][H][128]
     int T, H;
+    unsigned *status;
+    uint32_t timeout_ns;
 };
+
+constexpr int kHeadsTokens = 16;       // of a block, where there are few
+constexpr int kHeadsMmaThreads = 192;  // four warps for the results, a load warp, one that issues the products
 
 // ------------------------------------------------------- attention over rows
 

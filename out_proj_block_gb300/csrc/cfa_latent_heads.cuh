@@ -3,12 +3,14 @@
 //   unfold   y[t, h, d] = sum_c x[t, h, c] W[c, h * 256 + 128 + d]    512 -> 128
 // in fp32, each result rounded to bf16 once.
 //
-// A token's head is 131,072 operations for 1.3 to 1.5 KB read and written: memory bounds them, the
-// weights (128 KB a head) for few tokens, the tokens' rows for many, so mma.sync is enough. What counts is
-// that enough loads are on their way: a block asks for everything it needs, or three stages of it, before it
-// waits, and few tokens are split into many small blocks (over the result's columns; unfold's four warps
-// each take a quarter of the sum, joined in their order). Results go through shared memory, so that whole
-// rows are written.
+// These are the kernels for few tokens (many: cfa_latent_heads_mma.cuh): the weights, 128 KB a head, bound
+// them, and the latency of getting them. So a block asks for everything it needs before it waits, and the work
+// is split into many small blocks, over the result's columns; unfold's four warps each take a quarter of the sum,
+// joined in their order. mma.sync is enough.
+//
+// Measured (one GB300, calls back to back from Python, which itself takes 4.5 us): 4 tokens of 128 heads in 5.6 us
+// (17.6 MB, floor 2.6); 1 token out 4.6 us (floor 2.5). The rule between the two forms is in
+// cfa_latent.cu.
 #pragma once
 
 #include "cfa_device.cuh"
@@ -18,172 +20,77 @@
 
 namespace cfa {
 
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
-}
 // 16 bytes, or zeros where there is no source.
 __device__ __forceinline__ void cp_async_16_or_0(uint8_t *dst, const void *src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0)
                  : "memory");
 }
 
-constexpr int kHeadsWarpRows = 64;  // tokens of a warp at most
-constexpr int kHeadsCols = 128;     // columns of a block's result
-// Threads of a block of TM tokens: a warp takes 64 tokens (or all) and 32 columns.
-__host__ __device__ constexpr int heads_threads(int TM) { return TM > kHeadsWarpRows ? 256 : 128; }
+constexpr int kHeadsCols = 128;   // columns of a fold block's result
 // Rows of 256 bytes as 16-byte chunks, rows of a group of eight apart in the banks.
 __device__ __forceinline__ int heads_at(int row, int chunk) { return row * 256 + ((chunk ^ (row & 7)) << 4); }
 
-// A block's [TM][128] results (fragments of mma.sync) to rows of y, `stride` elements apart.
-template <int TM, int MF>
-__device__ __forceinline__ void heads_write(float (&acc)[MF][4][4], uint8_t *stage, uint16_t *y, size_t stride, int tokens) {
+// A block takes 16 tokens and 128 of the 512 latent dims. Shared memory: 128 rows of W, 16 of x.
+__global__ void __launch_bounds__(128) latent_fold_kernel(const __grid_constant__ LatentHeadsParams p) {
+    __shared__ __align__(128) uint8_t w[kHeadsCols * 256], x[kHeadsTokens * 256];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int m0 = warp / 4 * kHeadsWarpRows + (lane >> 2), n0 = warp % 4 * 32;
-#pragma unroll
-    for (int i = 0; i < MF; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<uint32_t *>(stage + heads_at(m0 + 16 * i + 8 * e, n0 / 8 + j) + 4 * (lane & 3)) =
-                    pack2_bf16_cvt(acc[i][j][2 * e], acc[i][j][2 * e + 1]);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < TM * 16 / heads_threads(TM); ++i) {
-        const int at = tid + i * heads_threads(TM), row = at >> 4, chunk = at & 15;
-        if (row < tokens)
-            *reinterpret_cast<uint4 *>(y + row * stride + 8 * chunk) = *reinterpret_cast<const uint4 *>(stage + heads_at(row, chunk));
-    }
-}
-
-// Shared memory: 128 rows of W, TM of x.
-template <int TM>
-__global__ void __launch_bounds__(heads_threads(TM)) latent_fold_kernel(const __grid_constant__ LatentHeadsParams p) {
-    extern __shared__ __align__(1024) uint8_t smem[];
-    constexpr int kThreads = heads_threads(TM), MF = (TM < kHeadsWarpRows ? TM : kHeadsWarpRows) / 16;
-    uint8_t *w = smem, *x = smem + kHeadsCols * 256;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int t0 = blockIdx.x * TM, h = blockIdx.y, c0 = blockIdx.z * kHeadsCols, tokens = min(TM, p.T - t0);
+    const int t0 = blockIdx.x * kHeadsTokens, h = blockIdx.y, c0 = blockIdx.z * kHeadsCols, tokens = min(kHeadsTokens, p.T - t0);
     const size_t row_w = static_cast<size_t>(p.H) * kLatKv;
     grid_dependency_wait();
     const uint16_t *src_w = p.w + c0 * row_w + h * kLatKv, *src_x = p.x + t0 * p.x_stride + h * kLatQ;
 #pragma unroll
-    for (int i = 0; i < kHeadsCols * 16 / kThreads; ++i) {
-        const int at = tid + i * kThreads, row = at >> 4, chunk = at & 15;
+    for (int i = 0; i < kHeadsCols * 16 / 128; ++i) {
+        const int at = tid + i * 128, row = at >> 4, chunk = at & 15;
         cp_async_16(smem_addr(w + heads_at(row, chunk)), src_w + row * row_w + 8 * chunk);
     }
 #pragma unroll
-    for (int i = 0; i < TM * 16 / kThreads; ++i) {
-        const int at = tid + i * kThreads, row = at >> 4, chunk = at & 15;
+    for (int i = 0; i < kHeadsTokens * 16 / 128; ++i) {
+        const int at = tid + i * 128, row = at >> 4, chunk = at & 15;
         cp_async_16_or_0(x + heads_at(row, chunk), row < tokens ? src_x + row * p.x_stride + 8 * chunk : src_x, row < tokens);
     }
     uint16_t *y = p.y + (static_cast<size_t>(t0) * p.H + h) * kLatRow;
     const size_t row_y = static_cast<size_t>(p.H) * kLatRow;
-    if (c0 == 0)  // the rotated dims pass through
-        for (int i = tid; i < tokens * 8; i += kThreads)
-            *reinterpret_cast<uint4 *>(y + (i >> 3) * row_y + kLatC + 8 * (i & 7)) =
-                *reinterpret_cast<const uint4 *>(src_x + (i >> 3) * p.x_stride + kLatN + 8 * (i & 7));
+    if (c0 == 0 && tid < tokens * 8)  // the rotated dims pass through
+        *reinterpret_cast<uint4 *>(y + (tid >> 3) * row_y + kLatC + 8 * (tid & 7)) =
+            *reinterpret_cast<const uint4 *>(src_x + (tid >> 3) * p.x_stride + kLatN + 8 * (tid & 7));
     cp_async_wait_all();
     __syncthreads();
-    float acc[MF][4][4] = {};
-    const int m0 = warp / 4 * kHeadsWarpRows, n0 = warp % 4 * 32;
+    float acc[4][4] = {};
+    const int n0 = warp * 32;
 #pragma unroll
     for (int k = 0; k < kLatN / 16; ++k) {
-        uint32_t b[2][4];
+        uint32_t a[4], b[2][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             ldmatrix_x4(b[j], smem_addr(w + heads_at(n0 + 16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1))));
+        ldmatrix_x4(a, smem_addr(x + heads_at(lane & 15, 2 * k + (lane >> 4))));
 #pragma unroll
-        for (int i = 0; i < MF; ++i) {
-            uint32_t a[4];
-            ldmatrix_x4(a, smem_addr(x + heads_at(m0 + 16 * i + (lane & 15), 2 * k + (lane >> 4))));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mma_16x8x16(acc[i][j], a, b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
-        }
+        for (int j = 0; j < 4; ++j) mma_16x8x16(acc[j], a, b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
     }
     __syncthreads();
-    heads_write<TM, MF>(acc, smem, y + c0, row_y, tokens);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<uint32_t *>(x + heads_at((lane >> 2) + 8 * e, n0 / 8 + j) + 4 * (lane & 3)) =
+                pack2_bf16_cvt(acc[j][2 * e], acc[j][2 * e + 1]);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kHeadsTokens * 16 / 128; ++i) {
+        const int at = tid + i * 128, row = at >> 4, chunk = at & 15;
+        if (row < tokens) *reinterpret_cast<uint4 *>(y + row * row_y + c0 + 8 * chunk) = *reinterpret_cast<const uint4 *>(x + heads_at(row, chunk));
+    }
     grid_dependents_launch();
 }
 
-// Many tokens: a block takes TM of them and a head's 128 dims, over stages of 64 latent dims.
-constexpr int kUnfoldStages = 3;
-template <int TM>
+// A block takes 16 tokens and 32 dims, each of its warps a quarter of the latent dims.
 struct UnfoldSmem {
-    static constexpr int kX = TM * 128, kStage = kX + 64 * 256;  // [TM][64] of x, [64][128] of W
-    static constexpr int kBytes = kUnfoldStages * kStage;
-    static_assert(kBytes >= TM * 256, "the results fit");
-};
-template <int TM>
-__global__ void __launch_bounds__(heads_threads(TM)) latent_unfold_kernel(const __grid_constant__ LatentHeadsParams p) {
-    extern __shared__ __align__(1024) uint8_t smem[];
-    using S = UnfoldSmem<TM>;
-    constexpr int kThreads = heads_threads(TM), MF = (TM < kHeadsWarpRows ? TM : kHeadsWarpRows) / 16, kSteps = kLatC / 64;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int t0 = blockIdx.x * TM, h = blockIdx.y, tokens = min(TM, p.T - t0);
-    const size_t row_w = static_cast<size_t>(p.H) * kLatKv;
-    grid_dependency_wait();
-    const uint16_t *src_w = p.w + h * kLatKv + kLatN, *src_x = p.x + t0 * p.x_stride + h * kLatC;
-    auto load = [&](int step) {
-        uint8_t *x = smem + step % kUnfoldStages * S::kStage, *w = x + S::kX;
-#pragma unroll
-        for (int i = 0; i < TM * 8 / kThreads; ++i) {
-            const int at = tid + i * kThreads, row = at >> 3, chunk = at & 7;
-            cp_async_16_or_0(x + row * 128 + ((chunk ^ (row & 7)) << 4),
-                             row < tokens ? src_x + row * p.x_stride + 64 * step + 8 * chunk : src_x, row < tokens);
-        }
-#pragma unroll
-        for (int i = 0; i < 64 * 16 / kThreads; ++i) {
-            const int at = tid + i * kThreads, row = at >> 4, chunk = at & 15;
-            cp_async_16(smem_addr(w + heads_at(row, chunk)), src_w + (64 * step + row) * row_w + 8 * chunk);
-        }
-    };
-#pragma unroll
-    for (int s = 0; s < kUnfoldStages - 1; ++s) {
-        load(s);
-        cp_async_commit();
-    }
-    float acc[MF][4][4] = {};
-    const int m0 = warp / 4 * kHeadsWarpRows, n0 = warp % 4 * 32;
-#pragma unroll 1
-    for (int step = 0; step < kSteps; ++step) {
-        cp_async_wait<kUnfoldStages - 2>();
-        __syncthreads();
-        if (step + kUnfoldStages - 1 < kSteps) load(step + kUnfoldStages - 1);
-        cp_async_commit();
-        const uint8_t *x = smem + step % kUnfoldStages * S::kStage, *w = x + S::kX;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t b[2][4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                ldmatrix_x4_trans(b[j], smem_addr(w + heads_at(16 * k + (lane & 15), n0 / 8 + 2 * j + (lane >> 4))));
-#pragma unroll
-            for (int i = 0; i < MF; ++i) {
-                uint32_t a[4];
-                const int row = m0 + 16 * i + (lane & 15);
-                ldmatrix_x4(a, smem_addr(x + row * 128 + (((2 * k + (lane >> 4)) ^ (row & 7)) << 4)));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mma_16x8x16(acc[i][j], a, b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
-            }
-        }
-    }
-    cp_async_wait_all();
-    __syncthreads();
-    heads_write<TM, MF>(acc, smem, p.y + (static_cast<size_t>(t0) * p.H + h) * kLatV, static_cast<size_t>(p.H) * kLatV, tokens);
-    grid_dependents_launch();
-}
-
-// Few tokens: a block takes 16 of them and 32 dims, each of its warps a quarter of the latent dims.
-struct UnfoldFewSmem {
     static constexpr int kW = 0, kX = kLatC * 64, kSum = kX + 16 * kLatC * 2;  // [512][32], [16][512], [4][16][32] floats
     static constexpr int kBytes = kSum + 4 * 16 * 32 * 4;
 };
-__global__ void __launch_bounds__(128) latent_unfold_few_kernel(const __grid_constant__ LatentHeadsParams p) {
+__global__ void __launch_bounds__(128) latent_unfold_kernel(const __grid_constant__ LatentHeadsParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    using S = UnfoldFewSmem;
+    using S = UnfoldSmem;
     uint8_t *w = smem + S::kW, *x = smem + S::kX;
     float *sum = reinterpret_cast<float *>(smem + S::kSum);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

@@ -150,7 +150,10 @@ def test_append_of_zeros_and_not_finite(cfa):
 
 
 @pytest.mark.parametrize("T,H", [(1, 1), (1, 128), (2, 3), (4, 20), (15, 7), (16, 8), (17, 33), (63, 2), (65, 5),
-                                 (129, 4), (300, 3)])
+                                 (129, 4), (300, 3),
+                                 # many tokens by heads, and either side of where the form changes
+                                 (33, 128), (48, 128), (49, 128), (20, 80), (21, 96), (128, 50), (129, 64), (257, 33),
+                                 (1000, 7), (2500, 3), (385, 20)])
 def test_fold_unfold(cfa, T, H):
     W = weights(1, H)
     wide = normal(2, T, H * QK + 24)
@@ -158,7 +161,7 @@ def test_fold_unfold(cfa, T, H):
     o = normal(3, T, H, C)
     q_lat = torch.full((T + 1, H, ROW), 3.0, dtype=torch.bfloat16, device="cuda")
     out = torch.full((T + 1, H, V), 3.0, dtype=torch.bfloat16, device="cuda")
-    with cfa.Latent(1, 512, H, 64) as plan:
+    with cfa.Latent(1, 2500, H, 64) as plan:
         plan.fold(q, W, q_lat[:T])
         plan.unfold(o, W, out[:T])
         assert plan.status() == cfa.CFA_OK
@@ -171,9 +174,9 @@ def test_fold_unfold(cfa, T, H):
     assert torch.all(q_lat[T] == 3.0) and torch.all(out[T] == 3.0)
 
 
-def test_fold_keeps_tokens_and_heads_apart(cfa):
+@pytest.mark.parametrize("T,H", [(20, 3), (300, 40)])
+def test_fold_keeps_tokens_and_heads_apart(cfa, T, H):
     """What is not finite in one token's head stays there."""
-    T, H = 20, 3
     W, q, o = weights(1, H), normal(2, T, H, QK), normal(3, T, H, C)
     q[7, 1, 3], o[9, 2, 400] = float("nan"), float("inf")
     q_lat, out = normal(4, T, H, ROW), normal(5, T, H, V)
