@@ -17,10 +17,16 @@
 // tile's scores wait for covers the product before them, so O may be rescaled then; that is done lazily, when a
 // row's maximum grew by more than 8 (a factor 2^8, far inside fp32), a published method.
 //
-// Tasks are dealt out in turn to one cluster per pair of SMs, a request's tiles one behind the other (they
-// read the same keys at the same time, out of L2), each round in the other direction. What does not fill the
-// last round is split along the keys; its parts leave records, which a second kernel merges in order, so results
-// are bitwise reproducible.
+// Tasks are dealt out in turn to one cluster per pair of SMs, those of most keys first and each round in
+// the other direction; in the order of requests instead, five prompts of 763 to 1500 tokens took the last cluster
+// 20% longer than the mean. What does not fill the last round is split along the keys; its parts leave records,
+// which a second kernel merges in order, so results are bitwise reproducible.
+//
+// Measured, with the merge (one GB300): 1024 tokens behind 2500 keys, 128 heads: 192 us (1.32 PFLOP/s); five
+// prompts of up to 1500 tokens, 32 heads: 114 us (0.65). A block of keys takes 2950 clocks of 512 rows, of
+// which products are 2560; a task's begin and end 7000, its last blocks, which one tile alone sees or
+// whose keys are masked, 5000 each. Tiles that go through the tasks each by itself, so that one's last
+// blocks run beside the other's next task, took more in the middle (3200 to 3500 clocks a block) than they saved.
 //
 // Weights are rounded to bf16 for their product with the values (2^-8 each, the size of the result's own
 // rounding); their sum, the maxima, the outputs and the records are fp32.
@@ -41,6 +47,7 @@ namespace cfa {
 constexpr int kExpChunk = 128 * 128;   // 128 rows of 64 dims
 constexpr int kExpSlots = 3;           // blocks of keys and of values in flight
 constexpr int kExpKSlot = 3 * 64 * 128, kExpVSlot = 128 * 128;
+constexpr int kExpPeek = 3;            // blocks before an item's end that the next one's queries are asked for in L2
 constexpr int kExpTile = 256;          // tokens of a tile, half of them to either block
 constexpr int kExpRows = 2 * kExpTile; // tokens of a task
 
@@ -57,11 +64,14 @@ struct ExpSmem {
     static constexpr int kBarsEnd = kDrain + 8;
     static constexpr int kMisc = kBarsEnd;                    // flags, TMEM address
     static constexpr int kSums = kMisc + 16;                  // int [12]: the scan's sums
-    static constexpr int kTiles = kSums + 64;                 // uint16 [B + 1]: tasks of a head before a request
-    static constexpr int kBytes = kTiles + 2 * (kPagedMaxSeqs + 2);
+    static constexpr int kTasks = kSums + 64;                 // int [kExpMaxTasks]: a head's tasks, the dearest first
+    static constexpr int kBytes = kTasks + 4 * (kPagedMaxTokens / kExpRows + kPagedMaxSeqs);
 };
 static_assert(ExpSmem::kBytes <= 227 * 1024, "it fits");
-static_assert(kPagedMaxTokens / kExpRows + kPagedMaxSeqs < 65536, "tasks of a head fit 16 bits");
+// Tasks of a head at most, and how the list names one.
+constexpr int kExpMaxTasks = kPagedMaxTokens / kExpRows + kPagedMaxSeqs;
+constexpr int kExpTaskBits = 12;
+static_assert(kPagedMaxTokens / kExpRows < 1 << kExpTaskBits, "a request's task fits its bits");
 
 // Tasks and how they are dealt out to `grid` clusters, from what a scan over the requests finds.
 struct ExpPlan {
@@ -91,10 +101,11 @@ struct ExpItem {
     __device__ __forceinline__ int visible(int i) const { return max(0, min(len, len - n + i + 1)); }
 };
 
-// Fills smem with the tasks of a head before each request; the number of all, or -1 where the offsets are not in order.
-// By all threads of the block.
+// Lists a head's tasks in smem, (request << 12 | which 512 tokens), those of most blocks first: dealt out in turn
+// and back, they come out even, and what is left for the last round is cheap. The number of all
+// heads', or -1 where the offsets are not in order. `work` holds 8 kExpMaxTasks bytes. By all threads of the block.
 template <int kThreads>
-__device__ __forceinline__ int latent_expanded_scan(const LatentExpandedParams &p, uint16_t *tiles, int *sums) {
+__device__ __forceinline__ int latent_expanded_list(const LatentExpandedParams &p, int *list, int2 *work, int *sums) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + kThreads - 1) / kThreads, first = tid * per, last = min(p.B, first + per);
     int mine = 0;
@@ -119,28 +130,29 @@ __device__ __forceinline__ int latent_expanded_scan(const LatentExpandedParams &
     }
     if (refused) return -1;
     CFA_ROLLED for (int b = first; b < last; ++b) {
-        tiles[b] = static_cast<uint16_t>(at);
-        at += (__ldcg(p.cu + b + 1) - __ldcg(p.cu + b) + kExpRows - 1) / kExpRows;
+        const int tok0 = __ldcg(p.cu + b), n = __ldcg(p.cu + b + 1) - tok0;
+        const int len = __ldcg(p.cu_k + b + 1) - __ldcg(p.cu_k + b);
+        CFA_ROLLED for (int i = 0; i * kExpRows < n; ++i)  // (named by its keys: half of them more or less is no matter)
+            work[at++] = make_int2(min(len, max(0, len - n + (i + 1) * kExpRows)), b << kExpTaskBits | i);
     }
-    if (tid == 0) tiles[p.B] = static_cast<uint16_t>(all);
+    __syncthreads();
+    CFA_ROLLED for (int i = tid; i < all; i += kThreads) {
+        const int2 x = work[i];
+        int rank = 0;
+        CFA_ROLLED for (int j = 0; j < all; ++j) rank += work[j].x > x.x || (work[j].x == x.x && j < i);
+        list[rank] = x.y;
+    }
     __syncthreads();
     return all * p.H;
 }
 
 // Task number `task`, part `part` of at most `parts`; false where it has fewer.
-__device__ __forceinline__ bool latent_expanded_item(const LatentExpandedParams &p, const uint16_t *tiles, int task, int part,
+__device__ __forceinline__ bool latent_expanded_item(const LatentExpandedParams &p, const int *list, int task, int part,
                                                      int parts, ExpItem &x) {
-    const int at = task / p.by_H;
-    int lo = 0, hi = p.B;  // the last request whose tasks begin no later (and that has any)
-    CFA_ROLLED while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (tiles[mid] <= at) lo = mid;
-        else hi = mid;
-    }
-    const int own = tiles[lo + 1] - tiles[lo], in = task - tiles[lo] * p.H;
+    const int at = task / p.by_H, lo = list[at] >> kExpTaskBits;
     x.req = lo;
-    x.h = in / own;
-    x.tile = own - 1 - (in - x.h * own);  // the longest first
+    x.h = task - at * p.H;
+    x.tile = list[at] & ((1 << kExpTaskBits) - 1);
     x.tok0 = __ldcg(p.cu + lo);
     x.n = __ldcg(p.cu + lo + 1) - x.tok0;
     x.k0 = __ldcg(p.cu_k + lo);
@@ -174,7 +186,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     int *misc = reinterpret_cast<int *>(smem + S::kMisc);
     volatile int *timed_out = misc;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 1);
-    const uint16_t *tiles = reinterpret_cast<const uint16_t *>(smem + S::kTiles);
+    int *list = reinterpret_cast<int *>(smem + S::kTasks);
 
     // a thread a barrier, with the arrivals it expects
     if (tid < (S::kBarsEnd - S::kBars) / 8) {
@@ -198,12 +210,13 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     tcgen05_fence_before();
     cluster_arrive();  // (the other block's barriers are ready behind the wait below)
     grid_dependency_wait();
-    const int tasks = latent_expanded_scan<kExpThreads>(p, reinterpret_cast<uint16_t *>(smem + S::kTiles),
+    const int tasks = latent_expanded_list<kExpThreads>(p, list, reinterpret_cast<int2 *>(smem + S::kQ),  // (free yet)
                                                         reinterpret_cast<int *>(smem + S::kSums));
     tcgen05_fence_after();
     if (blockIdx.x == 0 && tid == 0 && tasks < 0) atomicOr(p.status, kStatusBadLengthBit);
     grid_dependents_launch();
-    __syncwarp();
+    fence_proxy_async_smem();  // (the queries go where the list was made)
+    __syncthreads();
     cluster_wait();
     const uint32_t tmem = *tmem_slot;
     const int grid = static_cast<int>(gridDim.x) >> 1;
@@ -211,12 +224,18 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     // The cluster's item of round r; false where it has none.
     auto item = [&](int r, ExpItem &x) {
         const int at = r & 1 ? grid - 1 - cluster : cluster;
-        if (r < plan.full) return latent_expanded_item(p, tiles, r * grid + at, 0, 1, x);
+        if (r < plan.full) return latent_expanded_item(p, list, r * grid + at, 0, 1, x);
         const int task = at / plan.parts, part = at - task * plan.parts;
         x.rec = at;
-        return task < plan.rest && latent_expanded_item(p, tiles, plan.full * grid + task, part, plan.parts, x);
+        return task < plan.rest && latent_expanded_item(p, list, plan.full * grid + task, part, plan.parts, x);
     };
     const int rounds = plan.full + (plan.rest > 0);
+    // The first item from round r on, r becomes the round behind it; false at the end.
+    auto next = [&](int &r, ExpItem &x) {
+        CFA_ROLLED while (r < rounds)
+            if (item(r++, x)) return true;
+        return false;
+    };
     auto wait = [&](int bar, uint32_t parity, unsigned site) {
         return bounded_wait([&]() { return mbar_try_wait(base + bar, parity); }, p.timeout_ns, timed_out, p.status, site);
     };
@@ -230,10 +249,12 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             const bool values = warp != kExpLoadWarp;
             uint32_t n = 0, queried = 0, queries = 0;  // blocks; tiles whose queries were ever loaded, and phases, a bit a tile
             bool ok = true;
-            CFA_ROLLED for (int r = 0; ok && r < rounds; ++r) {
-                ExpItem x;
-                if (!item(r, x)) continue;
+            int r = 0;
+            ExpItem x, ahead;
+            bool have = next(r, x);
+            for (; ok && have; x = ahead) {
                 const int last = x.last();
+                have = next(r, ahead);
                 CFA_ROLLED for (int b = x.b0; ok && b < last; ++b, ++n) {
                     const uint32_t slot = n % kExpSlots, again = n / kExpSlots;
                     const int full = (values ? S::kFullV : S::kFullK) + 8 * slot;
@@ -253,6 +274,14 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                             mbar_arrive_expect_tx(base + full, kExpVSlot);
                             tma_load_2d(dst, &tm_kv, dim, y, base + full);
                             tma_load_2d(dst + 64 * 128, &tm_kv, dim, y + 64, base + full);
+                            if (have && b == max(x.b0, last - kExpPeek)) {
+                                // the next item's queries, in L2 by the time they are loaded
+#pragma unroll 1
+                                for (int i = 0; i < 6; ++i)
+                                    if (ahead.end(i / 3) > ahead.b0)
+                                        tma_prefetch_2d(&tm_q, ahead.h * kLatQ + 64 * (i % 3),
+                                                        ahead.tok0 + ahead.tile * kExpRows + kExpTile * (i / 3) + 128 * rank);
+                            }
                         }
                     }
                     __syncwarp();
@@ -306,9 +335,13 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 pass_on(S::kFullK + 8 * (nk % kExpSlots), ready_k + 8 * (nk % kExpSlots), (nk / kExpSlots) & 1);
                 ++nk;
             };
-            CFA_ROLLED for (int r = 0; ok && r < rounds; ++r) {
-                ExpItem x;
-                if (!item(r, x) || x.last() == x.b0) continue;
+            int r = 0;
+            ExpItem x;
+            while (ok && next(r, x)) {
+                if (x.last() == x.b0) continue;
+                // keys that every row of a tile sees, and that any row of the task does
+                const int some0 = x.visible(x.tile * kExpRows), some1 = x.visible(x.tile * kExpRows + kExpTile);
+                const int all = x.visible(min(x.n, x.tile * kExpRows + kExpRows) - 1);
                 keys();
                 CFA_ROLLED for (int t = 0; t < 2; ++t) {
                     if (x.end(t) == x.b0) continue;
@@ -317,7 +350,39 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 }
                 CFA_ROLLED for (int b = x.b0; ok && b < x.last(); ++b, ++nv) {
                     if (b + 1 < x.last()) keys();
-                    pass_on(S::kFullV + 8 * (nv % kExpSlots), ready_v + 8 * (nv % kExpSlots), (nv / kExpSlots) & 1);
+                    const uint32_t slot = nv % kExpSlots;
+                    ok = ok && wait_warp(S::kFullV + 8 * slot, (nv / kExpSlots) & 1, kSiteStageFull);
+                    const int begin = (b < x.end0 ? some0 : some1) - 128 * b, end = all - 128 * b;
+                    if (ok && begin < 128) {
+                        // Keys from `begin` on are not seen by every row, from `end` on by none. A masked weight is 0, and 0
+                        // times NaN is NaN: what is not finite of the first becomes 0, and the merge adds it to the rows that
+                        // see it; the others become 0. (A lane 16 bytes of every fourth row; of a row's chunks any order will do.)
+                        uint8_t *v = smem + S::kV + slot * kExpVSlot + (lane >> 3) * 128 + ((lane & 7) << 4);
+                        CFA_ROLLED for (int k0 = max(0, begin) & ~31; k0 < 128; k0 += 32) {
+                            uint4 d[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) d[i] = *reinterpret_cast<const uint4 *>(v + k0 * 128 + i * 512);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int k = k0 + 4 * i + (lane >> 3);
+                                // an exponent of ones and the 1 added to it carry into the sign's place
+                                auto carry = [](uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; };
+                                const uint32_t odd = (carry(d[i].x) | carry(d[i].y) | carry(d[i].z) | carry(d[i].w)) & 0x80008000u;
+                                if (k < begin || (k < end && odd == 0u)) continue;
+                                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                                if (k < end) {
+                                    *p.odd = 1u;
+                                    w = make_uint4(d[i].x & ~odd_bf16x2(d[i].x), d[i].y & ~odd_bf16x2(d[i].y),
+                                                   d[i].z & ~odd_bf16x2(d[i].z), d[i].w & ~odd_bf16x2(d[i].w));
+                                }
+                                *reinterpret_cast<uint4 *>(v + k0 * 128 + i * 512) = w;
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (ok && elect_one()) mbar_arrive_pair(ready_v + 8 * slot);
+                    __syncwarp();
                 }
             }
         } else if (warp == kExpMmaWarp && rank == 0) {
@@ -328,9 +393,10 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                            v0 = umma_smem_desc(base + S::kV, kExpVSlot, 1024);
             uint32_t n = 0, queries = 0, weights = 0;  // blocks before the item's; phases, a bit a tile
             bool ok = true;
-            CFA_ROLLED for (int r = 0; ok && r < rounds; ++r) {
-                ExpItem x;
-                if (!item(r, x)) continue;
+            int r = 0;
+            ExpItem x, ahead;
+            bool have = next(r, x);
+            for (; ok && have; x = ahead) {
                 const int last = x.last(), b0 = x.b0;
                 // By one thread: scores of tile t and block b. `frees`: nobody reads the keys after.
                 auto scores = [&](int t, int b, bool frees) {
@@ -356,6 +422,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     if (ok && elect_one()) scores(t, b0, t == 1 || x.end1 == b0);
                     __syncwarp();
                 }
+                have = next(r, ahead);  // (beside the first softmax)
                 CFA_ROLLED for (int b = b0; ok && b < last; ++b) {
                     const uint32_t slot = (n + b - b0) % kExpSlots;
                     if (b + 1 < last) keys(b + 1);
@@ -398,16 +465,15 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         const uint32_t t_s = tmem + lanes + 128 * t, t_o = tmem + lanes + 256 + 128 * t;
         const int scores = S::kScores + 8 * t;
         const uint32_t weights = map_to_rank(base + S::kWeights, 0) + 8 * t;
-        uint32_t scored = 0, nv = 0;  // phases; blocks before the item's
-        CFA_ROLLED for (int r = 0; r < rounds; ++r) {
-            ExpItem x;
-            if (!item(r, x)) continue;
+        uint32_t scored = 0;  // phases
+        int r = 0;
+        ExpItem x, ahead;
+        bool have = next(r, x);
+        for (; have; x = ahead) {
             const int first = x.tile * kExpRows + kExpTile * t + 128 * rank;  // this block's first token of the tile
             const int rows = max(0, min(128, x.rows(t) - 128 * rank));
             const bool live = row < rows, warp_live = row - lane < rows;
             const int see = live ? x.visible(first + row) : 0;
-            const int some = x.visible(x.tile * kExpRows + kExpTile * t);  // keys that every row of the tile sees
-            const int all = x.visible(min(x.n, x.tile * kExpRows + kExpRows) - 1);  // and any row of the task
             float m = -INFINITY, l = 0.f;
             CFA_ROLLED for (int b = x.b0; b < x.end(t); ++b, ++scored) {
                 wait(scores, scored & 1, kSiteSoftmaxExchange);
@@ -420,8 +486,13 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     tmem_wait_ld();
                     const int lim = see - 128 * b;
                     if (!__all_sync(~0u, lim >= 128)) {
+                        const int least = __reduce_min_sync(~0u, lim);
 #pragma unroll
-                        for (int c = 0; c < 128; ++c) s[c] = c < lim ? s[c] : 0xff800000u;
+                        for (int g = 0; g < 128; g += 32)
+                            if (least < g + 32) {
+#pragma unroll
+                                for (int c = g; c < g + 32; ++c) s[c] = c < lim ? s[c] : 0xff800000u;
+                            }
                     }
                     float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -467,33 +538,12 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     l += both.x + both.y;
                     tmem_wait_st();
                 }
-                if (some < 128 * (b + 1)) {
-                    // keys from `some` on are not seen by every row, from `all` on by none. A masked weight is 0, and
-                    // 0 times NaN is NaN: what is not finite of the first becomes 0 here, and the merge adds it to the rows
-                    // that see it; the others become 0. (Where the other tile's product runs meanwhile, either way does.)
-                    const uint32_t v = nv + b - x.b0, slot = v % kExpSlots;
-                    wait(S::kFullV + 8 * slot, (v / kExpSlots) & 1, kSiteStageFull);
-                    __syncwarp();
-                    uint8_t *vals = smem + S::kV + slot * kExpVSlot + ((row & 7) << 4);
-                    CFA_ROLLED for (int k = max(0, some - 128 * b) + (row >> 3); k < 128; k += 16) {
-                        uint4 *at = reinterpret_cast<uint4 *>(vals + k * 128);  // (of a row's chunks any order will do)
-                        uint4 d = make_uint4(0u, 0u, 0u, 0u);
-                        if (128 * b + k < all) {
-                            d = *at;
-                            const uint32_t e = odd_bf16x2(d.x), f = odd_bf16x2(d.y), g = odd_bf16x2(d.z), h = odd_bf16x2(d.w);
-                            if ((e | f | g | h) == 0u) continue;
-                            *p.odd = 1u;
-                            d = make_uint4(d.x & ~e, d.y & ~f, d.z & ~g, d.w & ~h);
-                        }
-                        *at = d;
-                    }
-                    fence_proxy_async_smem();
-                }
                 tcgen05_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_pair(weights);
             }
             const bool any = x.end(t) > x.b0;
+            have = next(r, ahead);  // (its loads are on their way meanwhile)
             if (any) {
                 wait(scores, scored & 1, kSiteKvExchange);
                 ++scored;
@@ -501,7 +551,6 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             __syncwarp();
             tcgen05_fence_after();
             // ---- the tile's results, or its record
-            nv += x.last() - x.b0;
             if (warp_live) {
                 const int in_task = kExpTile * t + 128 * rank + row;
                 const size_t tok = static_cast<size_t>(x.tok0 + first + row);
@@ -615,11 +664,12 @@ __device__ __noinline__ void latent_expanded_add_odd(const LatentExpandedParams 
 
 // Merges the records of the split tasks, a warp for 32 rows (a lane a row) and 16 dims.
 __global__ void __launch_bounds__(kLatMergeThreads, 3) latent_expanded_merge_kernel(const __grid_constant__ LatentExpandedParams p) {
-    __shared__ uint16_t tiles[kPagedMaxSeqs + 1];
+    __shared__ int list[kExpMaxTasks];
+    __shared__ int2 work[kExpMaxTasks];
     __shared__ int sums[kLatMergeThreads / 32];
     grid_dependency_wait();
     const unsigned odd = __ldcg(p.odd);
-    const int tasks = latent_expanded_scan<kLatMergeThreads>(p, tiles, sums);
+    const int tasks = latent_expanded_list<kLatMergeThreads>(p, list, work, sums);
     if (tasks > 0) {
         const ExpPlan plan = latent_expanded_plan(tasks, p.grid);
         const int lane = threadIdx.x & 31, warps = static_cast<int>(gridDim.x) * (kLatMergeThreads / 32);
@@ -628,7 +678,7 @@ __global__ void __launch_bounds__(kLatMergeThreads, 3) latent_expanded_merge_ker
                         plan.parts > 1 && i < plan.rest * 128; i += warps) {
             const int task = i >> 7, row = (i & 15) * 32 + lane, chunk = (i >> 4 & 7) * 4;
             ExpItem x;
-            latent_expanded_item(p, tiles, plan.full * p.grid + task, 0, plan.parts, x);
+            latent_expanded_item(p, list, plan.full * p.grid + task, 0, plan.parts, x);
             const int tok = x.tile * kExpRows + row;
             if (x.parts == 1 || tok >= x.n) continue;
             const int rec = task * plan.parts;
