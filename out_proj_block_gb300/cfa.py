@@ -680,6 +680,7 @@ class Stack:
 
 MLA_KV, MLA_NOPE, MLA_ROPE, MLA_V = 512, 128, 64, 128
 MLA_ROW = MLA_KV + MLA_ROPE
+MLA_QK = MLA_NOPE + MLA_ROPE
 
 
 def cfa_mla_create(B: int, hidden: int, n_heads: int, q_lora: int, max_ctx: int) -> int:
@@ -1083,7 +1084,11 @@ class Latent:
         self.handle = cfa_latent_create(max_seqs, max_tokens, n_heads, page_size)
         self.device = torch.device("cuda", torch.cuda.current_device())
         self._index = self.device.index
-        self._w_shape = (MLA_KV, n_heads * (MLA_NOPE + MLA_V))
+        # shapes behind the tokens, keys or pages
+        self._q_shape, self._lat_shape, self._o_shape = (n_heads, MLA_QK), (n_heads, MLA_ROW), (n_heads, MLA_KV)
+        self._out_shape, self._kv_shape = (n_heads, MLA_V), (n_heads, MLA_NOPE + MLA_V)
+        self._page_shape, self._w_shape = (page_size, MLA_ROW), (MLA_KV, n_heads * (MLA_NOPE + MLA_V))
+        self._q_width, self._kv_width = n_heads * MLA_QK, n_heads * (MLA_NOPE + MLA_V)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -1121,41 +1126,38 @@ class Latent:
         if st != CFA_OK:
             raise CfaError(st, "cfa_latent_set_rope")
 
-    # Argument checks: one expression a tensor, what is wrong is said only where it is not true.
+    # Argument checks. The smallest calls take the GPU only microseconds, so each method asks in one
+    # expression whether everything is right, and looks for what is wrong (these) only where it is not.
 
     def _dense(self, name, t, shape, dtype=_BF16):
-        """Pointer of a contiguous tensor of this shape."""
-        if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == self._index):
-            if t.dtype is not dtype:
-                raise TypeError(f"{name} must be {dtype}")
-            if t.shape != shape:
-                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.get_device() != self._index:
             raise ValueError(f"{name} must be on {self.device}")
-        return t.data_ptr()
 
     def _rows(self, name, t, n, *dims):
-        """Pointer and row stride of bf16 [n, *dims] with dense rows."""
-        s, width, ok = t.stride(), 1, t.dtype is _BF16 and t.shape == (n, *dims)
-        for i in range(len(dims), 0, -1):
-            ok = ok and (s[i] == width or dims[i - 1] == 1)
-            width *= dims[i - 1]
-        if not (ok and t.get_device() == self._index):
-            if t.dtype is not _BF16:
-                raise TypeError(f"{name} must be {_BF16}")
-            if t.shape != (n, *dims):
-                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, *dims)}")
-            if not ok:
-                raise ValueError(f"{name} must be dense within a row")
+        """bf16 [n, *dims] with dense rows."""
+        if t.dtype is not _BF16:
+            raise TypeError(f"{name} must be {_BF16}")
+        if t.shape != (n, *dims):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, *dims)}")
+        if not self._dense_rows(t.stride(), dims):
+            raise ValueError(f"{name} must be dense within a row")
+        if t.get_device() != self._index:
             raise ValueError(f"{name} must be on {self.device}")
-        return t.data_ptr(), (s[0] if n > 1 else width)
 
-    def _pages(self, pages):
-        return pages.shape[0], self._dense("pages", pages, (pages.shape[0], self.page_size, MLA_ROW))
-
-    def _heads(self, name, t, T, d):
-        return self._dense(name, t, (T, self.n_heads, d))
+    @staticmethod
+    def _dense_rows(stride, dims):
+        width = 1
+        for i in range(len(dims), 0, -1):
+            if stride[i] != width and dims[i - 1] != 1:
+                return False
+            width *= dims[i - 1]
+        return True
 
     def _stream(self, stream):
         if stream is None:
@@ -1163,27 +1165,60 @@ class Latent:
         return _stream(stream)
 
     def _scale(self, scale):
-        if scale is not None and not ctypes.c_float(scale).value > 0.0:
+        if scale is None:
+            return 0.0
+        if not ctypes.c_float(scale).value > 0.0:
             raise ValueError("scale must be positive, in 32 bits too")
-        return scale or 0.0
+        return scale
 
     def _append(self, a, g_kv, eps, q, positions, slots, pages, q_out):
-        T = q.shape[0]
-        n, pp = self._pages(pages)
-        return (*self._rows("a", a, T, MLA_ROW), self._dense("g_kv", g_kv, (MLA_KV,)), eps,
-                *self._rows("q", q, T, self.n_heads, MLA_NOPE + MLA_ROPE),
-                self._dense("positions", positions, (T,), _I32), self._dense("slots", slots, (T,), _I32),
-                n, pp, self._heads("q_out", q_out, T, MLA_NOPE + MLA_ROPE))
+        shape, one, page, i = q.shape, positions.shape, pages.shape, self._index
+        T = shape[0]
+        sa, sq = a.stride(), q.stride()
+        if not (a.dtype is q.dtype is g_kv.dtype is pages.dtype is q_out.dtype is _BF16
+                and positions.dtype is slots.dtype is _I32
+                and shape[1:] == self._q_shape and q_out.shape == shape and a.shape == (T, MLA_ROW)
+                and one == (T,) == slots.shape and page[1:] == self._page_shape and g_kv.shape == (MLA_KV,)
+                and sa[1] == 1 == sq[2] and sq[1] == MLA_QK
+                and q_out.is_contiguous() and pages.is_contiguous() and g_kv.is_contiguous()
+                and positions.is_contiguous() and slots.is_contiguous()
+                and a.get_device() == i == q.get_device() == g_kv.get_device() == pages.get_device()
+                == q_out.get_device() == positions.get_device() == slots.get_device()):
+            self._rows("q", q, T, *self._q_shape)
+            self._rows("a", a, T, MLA_ROW)
+            for name, t, shape, dtype in (("g_kv", g_kv, (MLA_KV,), _BF16), ("positions", positions, (T,), _I32),
+                                          ("slots", slots, (T,), _I32),
+                                          ("pages", pages, (page[0], *self._page_shape), _BF16),
+                                          ("q_out", q_out, (T, *self._q_shape), _BF16)):
+                self._dense(name, t, shape, dtype)
+        return (a.data_ptr(), sa[0] if T > 1 else MLA_ROW, g_kv.data_ptr(), eps, q.data_ptr(),
+                sq[0] if T > 1 else self._q_width, positions.data_ptr(), slots.data_ptr(), page[0],
+                pages.data_ptr(), q_out.data_ptr())
 
-    def _batch(self, T, cu, lens, tables):
-        if lens.dim() != 1 or tables.dim() != 2:
+    def _attn(self, q_lat, cu, lens, tables, pages, o_lat, lse):
+        shape, one, page, i = q_lat.shape, lens.shape, pages.shape, self._index
+        if len(one) != 1 or tables.dim() != 2:
             raise ValueError("lens has one dimension, tables two")
-        B, width = lens.shape[0], tables.shape[1]
-        return (B, self._dense("cu", cu, (B + 1,), _I32), self._dense("tables", tables, (B, width), _I32), width,
-                self._dense("lens", lens, (B,), _I32))
-
-    def _lse(self, lse, T):
-        return None if lse is None else self._dense("lse", lse, (T, self.n_heads), _F32)
+        T = shape[0]
+        B, width = tables.shape
+        if not (q_lat.dtype is pages.dtype is o_lat.dtype is _BF16
+                and cu.dtype is lens.dtype is tables.dtype is _I32
+                and shape[1:] == self._lat_shape and o_lat.shape == (T, *self._o_shape)
+                and page[1:] == self._page_shape and one[0] == B and cu.shape == (B + 1,)
+                and q_lat.is_contiguous() and pages.is_contiguous() and o_lat.is_contiguous()
+                and cu.is_contiguous() and lens.is_contiguous() and tables.is_contiguous()
+                and q_lat.get_device() == i == pages.get_device() == o_lat.get_device() == cu.get_device()
+                == lens.get_device() == tables.get_device()):
+            for name, t, shape, dtype in (("q_lat", q_lat, (T, *self._lat_shape), _BF16),
+                                          ("lens", lens, one, _I32), ("cu", cu, (one[0] + 1,), _I32),
+                                          ("tables", tables, (one[0], width), _I32),
+                                          ("pages", pages, (page[0], *self._page_shape), _BF16),
+                                          ("o_lat", o_lat, (T, *self._o_shape), _BF16)):
+                self._dense(name, t, shape, dtype)
+        if lse is not None:
+            self._dense("lse", lse, (T, self.n_heads), _F32)
+        return (B, q_lat.data_ptr(), cu.data_ptr(), tables.data_ptr(), width, lens.data_ptr(), page[0],
+                pages.data_ptr(), o_lat.data_ptr(), None if lse is None else lse.data_ptr())
 
     def append(self, a, g_kv, q, positions, slots, pages, q_out, eps: float = 1e-6, stream=None):
         """Cache rows of a [T, 576] (a slice of the down projection) into their slots, q
@@ -1197,20 +1232,34 @@ class Latent:
 
     def fold(self, q, W_kvb, q_lat, stream=None):
         """q [T, heads, 192] into the latent space: q_lat [T, heads, 576] (cfa_latent_fold)."""
-        T = q.shape[0]
-        st = _lib.cfa_latent_fold(self.handle, T, *self._rows("q", q, T, self.n_heads, MLA_NOPE + MLA_ROPE),
-                                  self._dense("W_kvb", W_kvb, self._w_shape),
-                                  self._heads("q_lat", q_lat, T, MLA_ROW), self._stream(stream))
+        shape, sq, i = q.shape, q.stride(), self._index
+        T = shape[0]
+        if not (q.dtype is W_kvb.dtype is q_lat.dtype is _BF16 and shape[1:] == self._q_shape and sq[2] == 1
+                and sq[1] == MLA_QK and W_kvb.shape == self._w_shape and q_lat.shape == (T, *self._lat_shape)
+                and W_kvb.is_contiguous() and q_lat.is_contiguous()
+                and q.get_device() == i == W_kvb.get_device() == q_lat.get_device()):
+            self._rows("q", q, T, *self._q_shape)
+            self._dense("W_kvb", W_kvb, self._w_shape)
+            self._dense("q_lat", q_lat, (T, *self._lat_shape))
+        st = _lib.cfa_latent_fold(self.handle, T, q.data_ptr(), sq[0] if T > 1 else self._q_width,
+                                  W_kvb.data_ptr(), q_lat.data_ptr(), self._stream(stream))
         if st != CFA_OK:
             raise CfaError(st, "cfa_latent_fold")
         return q_lat
 
     def unfold(self, o_lat, W_kvb, out, stream=None):
         """o_lat [T, heads, 512] out of the latent space: out [T, heads, 128] (cfa_latent_unfold)."""
-        T = o_lat.shape[0]
-        st = _lib.cfa_latent_unfold(self.handle, T, self._heads("o_lat", o_lat, T, MLA_KV),
-                                    self._dense("W_kvb", W_kvb, self._w_shape),
-                                    self._heads("out", out, T, MLA_V), self._stream(stream))
+        shape, i = o_lat.shape, self._index
+        T = shape[0]
+        if not (o_lat.dtype is W_kvb.dtype is out.dtype is _BF16 and shape[1:] == self._o_shape
+                and W_kvb.shape == self._w_shape and out.shape == (T, *self._out_shape)
+                and o_lat.is_contiguous() and W_kvb.is_contiguous() and out.is_contiguous()
+                and o_lat.get_device() == i == W_kvb.get_device() == out.get_device()):
+            self._dense("o_lat", o_lat, (T, *self._o_shape))
+            self._dense("W_kvb", W_kvb, self._w_shape)
+            self._dense("out", out, (T, *self._out_shape))
+        st = _lib.cfa_latent_unfold(self.handle, T, o_lat.data_ptr(), W_kvb.data_ptr(), out.data_ptr(),
+                                    self._stream(stream))
         if st != CFA_OK:
             raise CfaError(st, "cfa_latent_unfold")
         return out
@@ -1219,13 +1268,9 @@ class Latent:
                stream=None):
         """Attention of folded queries over the cached rows (cfa_latent_attention). scale None:
         1/sqrt(192). Returns o_lat [T, heads, 512]."""
-        T = q_lat.shape[0]
-        B, cup, tp, width, lp = self._batch(T, cu, lens, tables)
-        n, pp = self._pages(pages)
-        st = _lib.cfa_latent_attention(self.handle, T, B, self._heads("q_lat", q_lat, T, MLA_ROW), cup, tp,
-                                       width, lp, n, pp, self._scale(scale),
-                                       self._heads("o_lat", o_lat, T, MLA_KV), self._lse(lse, T),
-                                       self._stream(stream))
+        B, qp, cup, tp, width, lp, n, pp, op, sp = self._attn(q_lat, cu, lens, tables, pages, o_lat, lse)
+        st = _lib.cfa_latent_attention(self.handle, q_lat.shape[0], B, qp, cup, tp, width, lp, n, pp,
+                                       self._scale(scale), op, sp, self._stream(stream))
         if st != CFA_OK:
             raise CfaError(st, "cfa_latent_attention")
         return o_lat
@@ -1235,15 +1280,31 @@ class Latent:
         """Attention of prompts: q [T, heads, 192] over kv [S, heads, 256] (key 128 | value 128)
         and k_rope [S, 64], requests' rows by cu and cu_k (cfa_latent_expanded). Returns out
         [T, heads, 128]."""
-        T, S = q.shape[0], kv.shape[0]
-        if cu.dim() != 1:
+        shape, many, one, i = q.shape, kv.shape, cu.shape, self._index
+        if len(one) != 1:
             raise ValueError("cu has one dimension")
-        B = cu.shape[0] - 1
+        T, S, B = shape[0], many[0], one[0] - 1
+        sq, sk, sr = q.stride(), kv.stride(), k_rope.stride()
+        if not (q.dtype is kv.dtype is k_rope.dtype is out.dtype is _BF16 and cu.dtype is cu_k.dtype is _I32
+                and shape[1:] == self._q_shape and many[1:] == self._kv_shape and k_rope.shape == (S, MLA_ROPE)
+                and out.shape == (T, *self._out_shape) and cu_k.shape == one
+                and sq[2] == 1 == sk[2] == sr[1] and sq[1] == MLA_QK and sk[1] == MLA_NOPE + MLA_V
+                and out.is_contiguous() and cu.is_contiguous() and cu_k.is_contiguous()
+                and q.get_device() == i == kv.get_device() == k_rope.get_device() == out.get_device()
+                == cu.get_device() == cu_k.get_device()):
+            self._rows("q", q, T, *self._q_shape)
+            self._rows("kv", kv, S, *self._kv_shape)
+            self._rows("k_rope", k_rope, S, MLA_ROPE)
+            self._dense("cu", cu, (B + 1,), _I32)
+            self._dense("cu_k", cu_k, (B + 1,), _I32)
+            self._dense("out", out, (T, *self._out_shape))
+        if lse is not None:
+            self._dense("lse", lse, (T, self.n_heads), _F32)
         st = _lib.cfa_latent_expanded(
-            self.handle, T, S, B, *self._rows("q", q, T, self.n_heads, MLA_NOPE + MLA_ROPE),
-            *self._rows("kv", kv, S, self.n_heads, MLA_NOPE + MLA_V), *self._rows("k_rope", k_rope, S, MLA_ROPE),
-            self._dense("cu", cu, (B + 1,), _I32), self._dense("cu_k", cu_k, (B + 1,), _I32), self._scale(scale),
-            self._heads("out", out, T, MLA_V), self._lse(lse, T), self._stream(stream))
+            self.handle, T, S, B, q.data_ptr(), sq[0] if T > 1 else self._q_width, kv.data_ptr(),
+            sk[0] if S > 1 else self._kv_width, k_rope.data_ptr(), sr[0] if S > 1 else MLA_ROPE, cu.data_ptr(),
+            cu_k.data_ptr(), self._scale(scale), out.data_ptr(), None if lse is None else lse.data_ptr(),
+            self._stream(stream))
         if st != CFA_OK:
             raise CfaError(st, "cfa_latent_expanded")
         return out
@@ -1253,12 +1314,14 @@ class Latent:
         """append, fold, attend, unfold in one call (cfa_latent_layer). Returns out."""
         T = q.shape[0]
         ap, ast, gp, eps, qp, qs, pos, sl, n, pp, qo = self._append(a, g_kv, eps, q, positions, slots, pages, q_out)
-        B, cup, tp, width, lp = self._batch(T, cu, lens, tables)
+        if q_lat.shape[0] != T:
+            raise ValueError(f"q_lat has {q_lat.shape[0]} tokens, expected {T}")
+        B, qlp, cup, tp, width, lp, _, _, op, sp = self._attn(q_lat, cu, lens, tables, pages, o_lat, lse)
+        self._dense("W_kvb", W_kvb, self._w_shape)
+        self._dense("out", out, (T, *self._out_shape))
         st = _lib.cfa_latent_layer(
-            self.handle, T, B, ap, ast, gp, eps, qp, qs, pos, sl, cup, tp, width, lp, n, pp,
-            self._dense("W_kvb", W_kvb, self._w_shape), self._scale(scale), qo,
-            self._heads("q_lat", q_lat, T, MLA_ROW), self._heads("o_lat", o_lat, T, MLA_KV), self._lse(lse, T),
-            self._heads("out", out, T, MLA_V), self._stream(stream))
+            self.handle, T, B, ap, ast, gp, eps, qp, qs, pos, sl, cup, tp, width, lp, n, pp, W_kvb.data_ptr(),
+            self._scale(scale), qo, qlp, op, sp, out.data_ptr(), self._stream(stream))
         if st != CFA_OK:
             raise CfaError(st, "cfa_latent_layer")
         return out

@@ -41,7 +41,7 @@ struct cfa_latent {
     float magnitude = 1.0f;
     unsigned long long turns[cfa::kLatR / 2] = {};
     // workspace
-    unsigned *words = nullptr;  // [0] status, [1..2] the expanded form's merge (odd)
+    unsigned *words = nullptr;  // [0] status, [1..3] the expanded form's merge (odd, rest)
     float *rec_o = nullptr;     // records of the attention's pieces
     float2 *rec_ml = nullptr;
     int4 *cuts = nullptr;
@@ -338,7 +338,7 @@ cfa_latent *cfa_latent_create(int max_seqs, int max_tokens, int n_heads, int pag
     p->runs = std::min(sms / 2, cfa::kLatMaxRuns);
     const size_t rec_rows = 2u * static_cast<size_t>(p->runs) * cfa::kLatTile;
     if (!allow_smem() ||
-        cudaMalloc(&p->words, 3 * sizeof(unsigned)) != cudaSuccess || !clear_words(p->words, 3) ||
+        cudaMalloc(&p->words, 4 * sizeof(unsigned)) != cudaSuccess || !clear_words(p->words, 4) ||
         cudaMalloc(&p->rec_o, sizeof(float) * rec_rows * kLatC) != cudaSuccess ||
         // (twice the rows: the expanded form's records are 512 rows of 128 dims, one a cluster)
         cudaMalloc(&p->rec_ml, 2 * sizeof(float2) * rec_rows) != cudaSuccess ||
@@ -472,7 +472,8 @@ cfa_status cfa_latent_expanded(cfa_latent *p, int n_tokens, int n_keys, int n_se
     kp.S = n_keys;
     kp.B = n_seqs;
     kp.H = p->nh;
-    kp.grid = p->runs;
+    kp.rest = reinterpret_cast<int *>(p->words + 3);
+    kp.splits = p->cuts;
     kp.by_H = cfa::FastDiv(static_cast<uint32_t>(p->nh));
     kp.scale_log2 = scale_log2(scale);
     kp.timeout_ns = kTimeoutNs;
@@ -487,7 +488,7 @@ cfa_status cfa_latent_expanded(cfa_latent *p, int n_tokens, int n_keys, int n_se
                                64, 64, true) != CFA_OK)
         return fail(CFA_ERR_CUDA);
     void *args[4] = {&tq, &tk, &tr, &kp};
-    cfa_status st = launch(cfa::latent_expanded_kernel_ptr(), dim3(2u * static_cast<unsigned>(kp.grid)), cfa::kExpThreads,
+    cfa_status st = launch(cfa::latent_expanded_kernel_ptr(), dim3(2u * static_cast<unsigned>(p->runs)), cfa::kExpThreads,
                            static_cast<size_t>(cfa::latent_expanded_smem()), stream, args);
     void *margs[1] = {&kp};
     if (st == CFA_OK)

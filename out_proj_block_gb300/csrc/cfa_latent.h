@@ -95,8 +95,9 @@ struct LatentExpandedParams {
     unsigned *odd;           // {a value that is not finite was cleared, arrivals of the merge's blocks}; 0 between calls
     float *rec_o;            // records of parts: unnormalised outputs in 16-byte chunks [32][512 rows][4]
     float2 *rec_ml;          // and each row's maximum (base 2) and sum
+    int *rest;               // for the merge: how many tasks are split,
+    int4 *splits;            // and of each its first row's place, rows, parts and first record
     int T, S, B, H;
-    int grid;                // clusters
     FastDiv by_H;
     float scale_log2;
     uint32_t timeout_ns;

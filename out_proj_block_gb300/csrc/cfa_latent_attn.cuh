@@ -527,21 +527,22 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 if (some < (b + 1) * kLatKeys) {
                     // keys from `some` on are not seen by every row, from `all` on by none: what is not
                     // finite of the first, and all of the others, becomes 0
+                    const int begin = max(0, some - b * kLatKeys), end = min(kLatKeys, all - b * kLatKeys);
                     CFA_ROLLED for (int c = 0; c < kLatVSlots; ++c) {
                         wait(S::kFullV + 8 * c, g & 1, kSiteStageFull);
                         __syncwarp();
                         uint8_t *v = smem + S::kV + c * kLatVSlot + ((tid >> 3) & 1) * kLatChunk + ((tid & 7) << 4);
                         // (of a row's 16-byte chunks any order will do; the key halves lie 2 chunks apart)
-                        CFA_ROLLED for (int r = max(0, some - b * kLatKeys) + (tid >> 4); r < kLatKeys; r += 8) {
-                            uint4 *at = reinterpret_cast<uint4 *>(v + r * 128 + (r >> 6) * kLatChunk);
-                            uint4 d = make_uint4(0u, 0u, 0u, 0u);
-                            if (b * kLatKeys + r < all) {
-                                d = *at;
-                                const uint32_t f = odd_bf16x2(d.x), h = odd_bf16x2(d.y), i = odd_bf16x2(d.z), k = odd_bf16x2(d.w);
-                                if ((f | h | i | k) == 0u) continue;
-                                d = make_uint4(d.x & ~f, d.y & ~h, d.z & ~i, d.w & ~k);
-                            }
-                            *at = d;
+                        auto at = [&](int r) { return reinterpret_cast<uint4 *>(v + r * 128 + (r >> 6) * kLatChunk); };
+                        CFA_ROLLED for (int r = begin + (tid >> 4); r < end; r += 8) {
+                            const uint4 d = *at(r);
+                            const uint32_t f = odd_bf16x2(d.x), h = odd_bf16x2(d.y), i = odd_bf16x2(d.z), k = odd_bf16x2(d.w);
+                            if ((f | h | i | k) != 0u) *at(r) = make_uint4(d.x & ~f, d.y & ~h, d.z & ~i, d.w & ~k);
+                        }
+#pragma unroll
+                        for (int i = 0; i < kLatKeys / 8; ++i) {
+                            const int r = 8 * i + (tid >> 4);
+                            if (r >= end) *at(r) = make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
                 }

@@ -221,6 +221,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     const uint32_t tmem = *tmem_slot;
     const int grid = static_cast<int>(gridDim.x) >> 1;
     const ExpPlan plan = latent_expanded_plan(max(0, tasks), grid);
+    if (blockIdx.x == 0 && tid == 0) *p.rest = plan.parts > 1 ? plan.rest : 0;
     // The cluster's item of round r; false where it has none.
     auto item = [&](int r, ExpItem &x) {
         const int at = r & 1 ? grid - 1 - cluster : cluster;
@@ -470,6 +471,10 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         ExpItem x, ahead;
         bool have = next(r, x);
         for (; have; x = ahead) {
+            // of a split task, for the merge: where its rows are and how many parts it has
+            if (r > plan.full && plan.parts > 1 && x.part == 0 && rank == 0 && tid == 0)
+                p.splits[x.rec / plan.parts] = make_int4((x.tok0 + x.tile * kExpRows) * p.H + x.h, min(kExpRows, x.n - x.tile * kExpRows),
+                                                         x.parts, x.rec);
             const int first = x.tile * kExpRows + kExpTile * t + 128 * rank;  // this block's first token of the tile
             const int rows = max(0, min(128, x.rows(t) - 128 * rank));
             const bool live = row < rows, warp_live = row - lane < rows;
@@ -664,58 +669,48 @@ __device__ __noinline__ void latent_expanded_add_odd(const LatentExpandedParams 
 
 // Merges the records of the split tasks, a warp for 32 rows (a lane a row) and 16 dims.
 __global__ void __launch_bounds__(kLatMergeThreads, 3) latent_expanded_merge_kernel(const __grid_constant__ LatentExpandedParams p) {
-    __shared__ int list[kExpMaxTasks];
-    __shared__ int2 work[kExpMaxTasks];
-    __shared__ int sums[kLatMergeThreads / 32];
     grid_dependency_wait();
     const unsigned odd = __ldcg(p.odd);
-    const int tasks = latent_expanded_list<kLatMergeThreads>(p, list, work, sums);
-    if (tasks > 0) {
-        const ExpPlan plan = latent_expanded_plan(tasks, p.grid);
-        const int lane = threadIdx.x & 31, warps = static_cast<int>(gridDim.x) * (kLatMergeThreads / 32);
-        constexpr int kRec = kExpRows * (kLatV / 4);
-        CFA_ROLLED for (int i = static_cast<int>(blockIdx.x) * (kLatMergeThreads / 32) + (threadIdx.x >> 5);
-                        plan.parts > 1 && i < plan.rest * 128; i += warps) {
-            const int task = i >> 7, row = (i & 15) * 32 + lane, chunk = (i >> 4 & 7) * 4;
-            ExpItem x;
-            latent_expanded_item(p, list, plan.full * p.grid + task, 0, plan.parts, x);
-            const int tok = x.tile * kExpRows + row;
-            if (x.parts == 1 || tok >= x.n) continue;
-            const int rec = task * plan.parts;
-            const float2 *ml = p.rec_ml + rec * kExpRows + row;
-            const float4 *o = reinterpret_cast<const float4 *>(p.rec_o) + static_cast<size_t>(rec) * kRec + chunk * kExpRows + row;
-            float m = -INFINITY, l = 0.f;
-            float2 s[kExpMaxParts];
+    const int rest = __ldcg(p.rest);
+    const int lane = threadIdx.x & 31, warps = static_cast<int>(gridDim.x) * (kLatMergeThreads / 32);
+    constexpr int kRec = kExpRows * (kLatV / 4);
+    CFA_ROLLED for (int i = static_cast<int>(blockIdx.x) * (kLatMergeThreads / 32) + (threadIdx.x >> 5); i < rest * 128; i += warps) {
+        const int4 x = __ldcg(p.splits + (i >> 7));  // the first row's place, rows, parts, the first record
+        const int row = (i & 15) * 32 + lane, chunk = (i >> 4 & 7) * 4, parts = x.z;
+        if (parts == 1 || row >= x.y) continue;
+        const float2 *ml = p.rec_ml + x.w * kExpRows + row;
+        const float4 *o = reinterpret_cast<const float4 *>(p.rec_o) + static_cast<size_t>(x.w) * kRec + chunk * kExpRows + row;
+        float m = -INFINITY, l = 0.f;
+        float2 s[kExpMaxParts];
 #pragma unroll
-            for (int k = 0; k < kExpMaxParts; ++k) {
-                s[k] = k < x.parts ? __ldcg(ml + k * kExpRows) : make_float2(-INFINITY, 0.f);
-                m = fmaxf(m, s[k].x);
-            }
-            const float f = m == -INFINITY ? 0.f : m;
-            float a[16] = {};
-#pragma unroll
-            for (int k = 0; k < kExpMaxParts; ++k) {
-                if (k >= x.parts) break;
-                const float g = exp2_ftz(s[k].x - f);
-                l += g * s[k].y;
-                if (s[k].x == -INFINITY && s[k].y == 0.f) continue;  // no keys: there may be no outputs
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float4 v = __ldcg(o + static_cast<size_t>(k) * kRec + c * kExpRows);
-                    a[4 * c] += g * v.x; a[4 * c + 1] += g * v.y; a[4 * c + 2] += g * v.z; a[4 * c + 3] += g * v.w;
-                }
-            }
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const size_t at = static_cast<size_t>(x.tok0 + tok) * p.H + x.h;
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                *reinterpret_cast<uint4 *>(p.out + at * kLatV + 4 * chunk + 8 * c) =
-                    make_uint4(pack2_bf16_cvt(a[8 * c] * inv, a[8 * c + 1] * inv), pack2_bf16_cvt(a[8 * c + 2] * inv, a[8 * c + 3] * inv),
-                               pack2_bf16_cvt(a[8 * c + 4] * inv, a[8 * c + 5] * inv), pack2_bf16_cvt(a[8 * c + 6] * inv, a[8 * c + 7] * inv));
-            if (p.lse && chunk == 0) p.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
+        for (int k = 0; k < kExpMaxParts; ++k) {
+            s[k] = k < parts ? __ldcg(ml + k * kExpRows) : make_float2(-INFINITY, 0.f);
+            m = fmaxf(m, s[k].x);
         }
-        if (odd) latent_expanded_add_odd(p);
+        const float f = m == -INFINITY ? 0.f : m;
+        float a[16] = {};
+#pragma unroll
+        for (int k = 0; k < kExpMaxParts; ++k) {
+            if (k >= parts) break;
+            const float g = exp2_ftz(s[k].x - f);
+            l += g * s[k].y;
+            if (s[k].x == -INFINITY && s[k].y == 0.f) continue;  // no keys: there may be no outputs
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float4 v = __ldcg(o + static_cast<size_t>(k) * kRec + c * kExpRows);
+                a[4 * c] += g * v.x; a[4 * c + 1] += g * v.y; a[4 * c + 2] += g * v.z; a[4 * c + 3] += g * v.w;
+            }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t at = static_cast<size_t>(x.x) + static_cast<size_t>(row) * p.H;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<uint4 *>(p.out + at * kLatV + 4 * chunk + 8 * c) =
+                make_uint4(pack2_bf16_cvt(a[8 * c] * inv, a[8 * c + 1] * inv), pack2_bf16_cvt(a[8 * c + 2] * inv, a[8 * c + 3] * inv),
+                           pack2_bf16_cvt(a[8 * c + 4] * inv, a[8 * c + 5] * inv), pack2_bf16_cvt(a[8 * c + 6] * inv, a[8 * c + 7] * inv));
+        if (p.lse && chunk == 0) p.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
     }
+    if (odd) latent_expanded_add_odd(p);
     grid_dependents_launch();
 }
 
