@@ -446,7 +446,8 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             const int in_tile = rank * split + row;
             const int in_request = z.tile * kLatTile + in_tile;        // the query row
             const bool live = row < here, warp_live = row - lane < here;
-            const int see = live ? latent_visible(z.r, in_request / p.by_H) : 0;
+            // (rows past the last see what that one sees, so that their warp takes no masked blocks for them)
+            const int see = latent_visible(z.r, (z.tile * kLatTile + rank * split + min(row, max(here, 1) - 1)) / p.by_H);
             const int some = latent_visible(z.r, (z.tile * kLatTile) / p.by_H);  // keys that every row sees
             const int all = latent_visible(z.r, (z.tile * kLatTile + tile_rows - 1) / p.by_H);  // and any
             float m = -INFINITY, l = 0.f;
