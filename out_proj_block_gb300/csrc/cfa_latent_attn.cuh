@@ -444,7 +444,6 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             const int tile_rows = latent_rows(z.r, p.H, z.tile), split = latent_split(tile_rows);
             const int here = rank ? tile_rows - split : split;         // rows of this block
             const int in_tile = rank * split + row;
-            const int in_request = z.tile * kLatTile + in_tile;        // the query row
             const bool live = row < here, warp_live = row - lane < here;
             // (rows past the last see what that one sees, so that their warp takes no masked blocks for them)
             const int see = latent_visible(z.r, (z.tile * kLatTile + rank * split + min(row, max(here, 1) - 1)) / p.by_H);
@@ -677,9 +676,10 @@ __global__ void __launch_bounds__(kLatMergeThreads, 3) latent_merge_kernel(const
         const int run = lo, last = cut.z, groups = (cut.x + 31) / 32, at = task - before[lo];
         const bool two = last == run + 1;
         const int row = at % groups * 32 + lane, chunk = at / groups * (two ? 4 : 1);
-        if (row >= cut.x) continue;
-        const float2 *ml = p.rec_ml + row;
-        const float4 *o = reinterpret_cast<const float4 *>(p.rec_o) + static_cast<size_t>(chunk) * kLatTile + row;
+        const bool live = row < cut.x;
+        const int from = min(row, cut.x - 1);
+        const float2 *ml = p.rec_ml + from;
+        const float4 *o = reinterpret_cast<const float4 *>(p.rec_o) + static_cast<size_t>(chunk) * kLatTile + from;
         uint16_t *out = p.out + (static_cast<size_t>(cut.y) + row) * kLatC + 4 * chunk;
         float m = -INFINITY, l = 0.f;
         if (two) {
@@ -701,9 +701,19 @@ __global__ void __launch_bounds__(kLatMergeThreads, 3) latent_merge_kernel(const
                 w[2 * c] = pack2_bf16_cvt((g0 * v[0][c].x + g1 * v[1][c].x) * inv, (g0 * v[0][c].y + g1 * v[1][c].y) * inv);
                 w[2 * c + 1] = pack2_bf16_cvt((g0 * v[0][c].z + g1 * v[1][c].z) * inv, (g0 * v[0][c].w + g1 * v[1][c].w) * inv);
             }
+            // two lanes write a row's 32 bytes together, then the other's: a lane's own 16, in 32 rows at once, take a
+            // transaction each
+            const bool odd = lane & 1;
+            uint32_t other[4];
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-                *reinterpret_cast<uint4 *>(out + 8 * c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+            for (int c = 0; c < 4; ++c) other[c] = __shfl_xor_sync(~0u, odd ? w[c] : w[4 + c], 1);
+            uint16_t *even_out = out - (odd ? kLatC : 0) + (odd ? 8 : 0);
+            if (row - (odd ? 1 : 0) < cut.x)
+                *reinterpret_cast<uint4 *>(even_out) =
+                    odd ? make_uint4(other[0], other[1], other[2], other[3]) : make_uint4(w[0], w[1], w[2], w[3]);
+            if (row + (odd ? 0 : 1) < cut.x)
+                *reinterpret_cast<uint4 *>(even_out + kLatC) =
+                    odd ? make_uint4(w[4], w[5], w[6], w[7]) : make_uint4(other[0], other[1], other[2], other[3]);
         } else {
             constexpr int N = 8;
             float a[4] = {};
@@ -736,9 +746,9 @@ __global__ void __launch_bounds__(kLatMergeThreads, 3) latent_merge_kernel(const
                 }
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            *reinterpret_cast<uint2 *>(out) = make_uint2(pack2_bf16_cvt(a[0] * inv, a[1] * inv), pack2_bf16_cvt(a[2] * inv, a[3] * inv));
+            if (live) *reinterpret_cast<uint2 *>(out) = make_uint2(pack2_bf16_cvt(a[0] * inv, a[1] * inv), pack2_bf16_cvt(a[2] * inv, a[3] * inv));
         }
-        if (p.lse && chunk == 0) p.lse[static_cast<size_t>(cut.y) + row] = (m + log2f(l)) * 0.69314718055994531f;
+        if (p.lse && live && chunk == 0) p.lse[static_cast<size_t>(cut.y) + row] = (m + log2f(l)) * 0.69314718055994531f;
     }
     grid_dependents_launch();
 }
