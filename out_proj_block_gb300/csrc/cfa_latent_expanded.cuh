@@ -584,30 +584,30 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     uint8_t *stage = smem + S::kQ + 3 * t * kExpChunk + (row - lane) * 128;
 #pragma unroll 1
                     for (int c = 0; c < kLatV; c += 64) {
-                        uint32_t v[64];
                         __syncwarp();
+                        uint4 y[8];
                         if (any) {
+                            uint32_t v[64];
                             tmem_ld_x32(t_o + c, v);
                             tmem_ld_x32(t_o + c + 32, v + 32);
                             tmem_wait_ld();
-                        } else {
 #pragma unroll
-                            for (int e = 0; e < 64; ++e) v[e] = 0u;
-                        }
+                            for (int e = 0; e < 8; ++e) {
+                                uint32_t w[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            uint32_t w[4];
+                                for (int k = 0; k < 4; ++k)
+                                    w[k] = pack2_bf16_cvt(__uint_as_float(v[8 * e + 2 * k]) * inv, __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
+                                *reinterpret_cast<uint4 *>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                            __syncwarp();
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                w[k] = pack2_bf16_cvt(__uint_as_float(v[8 * e + 2 * k]) * inv, __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
-                            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                        __syncwarp();
-                        uint4 y[8];
+                            for (int e = 0; e < 8; ++e) {
+                                const int k = 4 * e + (lane >> 3);
+                                y[e] = *reinterpret_cast<const uint4 *>(stage + k * 128 + (((lane & 7) ^ (k & 7)) << 4));
+                            }
+                        } else {  // (without keys the tile has no queries: the next item's may be landing there)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int k = 4 * e + (lane >> 3);
-                            y[e] = *reinterpret_cast<const uint4 *>(stage + k * 128 + (((lane & 7) ^ (k & 7)) << 4));
+                            for (int e = 0; e < 8; ++e) y[e] = make_uint4(0u, 0u, 0u, 0u);
                         }
                         uint16_t *out = p.out + ((tok - lane) * p.H + x.h) * kLatV + c + 8 * (lane & 7);
 #pragma unroll
