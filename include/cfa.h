@@ -755,7 +755,8 @@ cfa_status cfa_latent_unfold(cfa_latent *latent, int n_tokens, const void *o_lat
  *         or NULL
  * A token that sees no row gets 0 and lse -inf. Tokens outside [cu[0], cu[n_seqs]) stay as
  * they were. scale 0 means 1/sqrt(192); scale times log2 e must be finite in 32 bits. Rows
- * that a token does not see do not change it, whatever they hold. Flagged in the status word
+ * that a token does not see do not change it, whatever they hold. A score that is NaN or +inf makes
+ * its token's head NaN; whether a row with such values and score -inf (weight 0) does is not defined. Flagged in the status word
  * as CFA_ERR_INVALID_ARG: offsets cu that are not ascending within [0, n_tokens], or more than
  * 2^29 blocks of 128 rows over all tiles of 128 token heads (nothing is written then); a length outside
  * [0, table_width * page_size] (taken as 0); a page id outside [0, n_pages) where a row is read
@@ -775,7 +776,9 @@ cfa_status cfa_latent_attention(cfa_latent *latent, int n_tokens, int n_seqs, co
  * are the last of its keys' tokens: with n query tokens and L keys, token i sees the first
  * L - n + i + 1 keys.
  *   out bf16 [n_tokens, n_heads, 128], lse fp32 [n_tokens, n_heads] or NULL, as cfa_latent_attention
- *   computes them from k = [key | k_rope] and value, scale and unseen keys as there.
+ *   computes them from k = [key | k_rope] and value, scale and unseen keys as there. Values that are not
+ *   finite stay in their dim; where only some tokens of a request see one, a slow pass behind the
+ *   call adds it to those.
  * q_stride a multiple of 8, kv_stride and k_rope_stride too. A token that sees no key gets 0 and lse
  * -inf; tokens outside the requests stay as they were. Flagged (CFA_ERR_INVALID_ARG from
  * cfa_latent_status, nothing written): cu or cu_k that are not ascending within [0, n_tokens]

@@ -29,6 +29,13 @@
 // are bitwise reproducible. A row's maximum is followed lazily, a published method: O is rescaled
 // only when it grew by more than 8 (a factor 2^8, far inside fp32).
 //
+// Measured, with the merge (one GB300): 64 requests of some 8K rows, 128 heads 88 us (385 MB read once;
+// floor 57); 200 of some 2K, 32 heads 72 us (floor 47); 16 with four drafted tokens each, 20 heads 26 us; one of 4K rows
+// 16 us. In the middle of a run memory bounds it, at 6.2 TB/s (products take 2490 clocks of a block of keys,
+// the rows 2900); beside that stand the start (scan, first queries and keys: 9 us), the cut tiles' records (4 us, and 5
+// to 11 to merge them) and, with short requests, a tile's end, some 8000 clocks. Merging in the block that ends last
+// instead of in a second kernel took 105 us for the first of these.
+//
 // Weights are rounded to bf16 for their product with the values (tensor cores take both operands in
 // one type; 2^-8 each, the size of the result's own rounding); their sum, the maxima, the outputs
 // and the records are fp32.
@@ -49,12 +56,13 @@ namespace cfa {
 constexpr int kLatChunk = 64 * 128;        // 64 rows of 64 dims
 // a block of keys takes three slots of three chunks of keys and two slots of four chunks of values
 // (both key halves of 128 dims): each wait, arrival and commit costs its warp 100 clocks or more, which slots of
-// single chunks could not hide (5000 clocks a block instead of NNNN)
+// single chunks could not hide (5000 clocks a block instead of 2500)
 constexpr int kLatKSlots = 3, kLatKSlot = 3 * kLatChunk, kLatVSlots = 2, kLatVSlot = 4 * kLatChunk;
 constexpr int kLatQChunks = kLatRow / 64;  // 9
-constexpr int kLatAhead = 1;                // blocks of keys that are asked for in L2 ahead of their copies
-constexpr int kLatPeek = 3;                 // blocks before a tile's end that the next one's data are
-constexpr int kLatShare = 2;                // least units of a run
+constexpr int kLatAhead = 1;                // blocks of keys that are asked for in L2 ahead of their copies (64 requests of
+                                            // some 8K rows, 128 heads: with 1, 2, 3, 4, 6 91, 94, 98, 105, 118 us)
+constexpr int kLatPeek = 3;                 // blocks before a tile's end that the next one's first data are asked for
+constexpr int kLatShare = 2;                // least units of a run (1, 2, 4: one request of 4K rows 17.7, 16.4, 18.1 us)
 constexpr int kLatWarps = kLatAttnThreads / 32;
 
 // Shared memory, the same in both blocks of a cluster (an instruction that spans them has one

