@@ -342,7 +342,8 @@ cfa_latent *cfa_latent_create(int max_seqs, int max_tokens, int n_heads, int pag
         cudaMalloc(&p->rec_o, sizeof(float) * rec_rows * kLatC) != cudaSuccess ||
         // (twice the rows: the expanded form's records are 512 rows of 128 dims, one a cluster)
         cudaMalloc(&p->rec_ml, 2 * sizeof(float2) * rec_rows) != cudaSuccess ||
-        cudaMalloc(&p->cuts, sizeof(int4) * static_cast<size_t>(p->runs)) != cudaSuccess) {
+        // (twice the runs: two tiles of a split task)
+        cudaMalloc(&p->cuts, 2 * sizeof(int4) * static_cast<size_t>(p->runs)) != cudaSuccess) {
         cudaGetLastError();
         latent_free(p);
         delete p;
@@ -551,7 +552,7 @@ cfa_status cfa_latent_describe(const cfa_latent *p, char *buf, int len) {
                   "\"interleaved\": %d, \"scaling\": %d, \"num_sms\": %d, \"runs\": %d, \"smem_bytes\": %d, "
                   "\"workspace_bytes\": %lld}",
                   p->max_seqs, p->max_tokens, p->nh, p->ps, p->rope, p->interleaved, p->scaling, p->num_sms, p->runs,
-                  cfa::latent_attention_smem(), 2ll * p->runs * cfa::kLatTile * (4 * kLatC + 16) + 16ll * p->runs);
+                  cfa::latent_attention_smem(), 2ll * p->runs * cfa::kLatTile * (4 * kLatC + 16) + 32ll * p->runs);
     return CFA_OK;
 }
 

@@ -96,7 +96,7 @@ struct LatentExpandedParams {
     float *rec_o;            // records of parts: unnormalised outputs in 16-byte chunks [32][512 rows][4]
     float2 *rec_ml;          // and each row's maximum (base 2) and sum
     int *rest;               // for the merge: how many tasks are split,
-    int4 *splits;            // and of each its first row's place, rows, parts and first record
+    int4 *splits;            // and of each of their two tiles its first row's place, rows, parts and first record
     int T, S, B, H;
     FastDiv by_H;
     float scale_log2;

@@ -5,28 +5,30 @@
 //
 // for each query token and head over the keys that the token sees. A row without any is 0 with lse -inf.
 //
-// A task is a head of a request and 512 of its tokens; 192 dims of scores and 128 of values are 640
-// operations a query and key, so products bound it. A cluster of two blocks takes a task as two tiles of
-// 256 rows (128 to either block) with the tcgen05 instructions that span both: a block of 128 keys is S = Q K^T
-// (12 instructions of 256 x 128 x 16) and O += P V (8) for either tile, and either block holds half of it, 64 keys
-// for the scores and 64 dims for the values. In one block's own instructions (128 x 128 x 16) the
-// scores' two operands kept shared memory busy for 92 clocks each, where the arithmetic takes 64, and left room
-// for little more than one block of keys. TMEM holds S and O of both tiles (4 x 128 columns), the weights P as
-// bf16 in place of the scores. A tile's next scores need its weights' product to have ended, so while one tile's
-// softmax runs (a thread a row), the other's products do: the tiles take turns. The last commit that a
-// tile's scores wait for covers the product before them, so O may be rescaled then; that is done lazily, when a
-// row's maximum grew by more than 8 (a factor 2^8, far inside fp32), a published method.
+// A task is two tiles of 256 tokens of a request and head, 128 rows to either block of a cluster; 192 dims of scores
+// and 128 of values are 640 operations a query and key, so products bound it. They are the tcgen05 instructions that
+// span both blocks: a block of 128 keys is S = Q K^T (12 instructions of 256 x 128 x 16) and O += P V (8) for a
+// tile, and either block holds half of it, 64 keys for the scores and 64 dims for the values. In one block's own
+// instructions (128 x 128 x 16) the scores' two operands kept shared memory busy for 92 clocks each, where the
+// arithmetic takes 64, and left room for little more than one block of keys. TMEM holds S and O of both tiles (4 x 128
+// columns), the weights P as bf16 in place of the scores. A tile's next scores need its weights' product to have
+// ended, so while one tile's softmax runs (a thread a row), the other's products do: the tiles take turns. The last
+// commit that a tile's scores wait for covers the product before them, so O may be rescaled then; that is done
+// lazily, when a row's maximum grew by more than 8 (a factor 2^8, far inside fp32), a published method.
 //
-// Tasks are dealt out in turn to one cluster per pair of SMs, those of most keys first and each round in
-// the other direction; in the order of requests instead, five prompts of 763 to 1500 tokens took the last cluster
-// 20% longer than the mean. What does not fill the last round is split along the keys; its parts leave records,
-// which a second kernel merges in order, so results are bitwise reproducible.
+// Which tiles make a task: two heads' of the same tokens, or two in a row of one head (kExpShared). Tasks are dealt out
+// in turn to one cluster per pair of SMs, those of most keys first and each round in the other direction; in the order
+// of requests instead, five prompts of 763 to 1500 tokens took the last cluster 20% longer than the mean. What does
+// not fill the last round is split along the keys; its parts leave records, which a second kernel merges in order, so
+// results are bitwise reproducible.
 //
-// Measured, with the merge (one GB300): 1024 tokens behind 2500 keys, 128 heads: 192 us (1.32 PFLOP/s); five
-// prompts of up to 1500 tokens, 32 heads: 114 us (0.65). A block of keys takes 2950 clocks of 512 rows, of
-// which products are 2560; a task's begin and end 7000, its last blocks, which one tile alone sees or
-// whose keys are masked, 5000 each. Tiles that go through the tasks each by itself, so that one's last
-// blocks run beside the other's next task, took more in the middle (3200 to 3500 clocks a block) than they saved.
+// Measured, with the merge (one GB300): 1024 tokens behind 2500 keys, 128 heads: 194 us (1.30 PFLOP/s); five
+// prompts of up to 1500 tokens, 32 heads: 95 us (0.79). A block of keys takes some 3100 clocks of 512 rows, of which
+// products are 2560: the softmax of a tile, 1250, and the two hand-overs, 400, take longer than the other's products. A
+// task's begin and end take some 9000. Values are looked over for what is not finite by the warps of the
+// softmax: the warp that relays took 4300 clocks for a block, at the end of every tile two of them. Tiles that go through
+// the tasks each by itself, so that one's last blocks run beside the other's next task, took more in the middle (3200 to
+// 3500 clocks a block) than they saved.
 //
 // Weights are rounded to bf16 for their product with the values (2^-8 each, the size of the result's own
 // rounding); their sum, the maxima, the outputs and the records are fp32.
@@ -47,6 +49,11 @@ namespace cfa {
 constexpr int kExpChunk = 128 * 128;   // 128 rows of 64 dims
 constexpr int kExpSlots = 3;           // blocks of keys and of values in flight
 constexpr int kExpKSlot = 3 * 64 * 128, kExpVSlot = 128 * 128;
+// Keys from which on two tiles in a row of a head make a task, and blocks of keys are loaded once for both. Below, two
+// heads' tiles do, which end together: of two in a row the first sees two blocks fewer. Two in a row always and never, in
+// us: 1024 tokens behind 2500, 128 heads 184 and 191; a prompt of 8192, 16 heads 215 and 217; five of 763 to
+// 1500, 32 heads 105 and 96; 300 tokens 16 times 83 and 72.
+constexpr int kExpShared = 2560;
 constexpr int kExpPeek = 3;            // blocks before an item's end that the next one's queries are asked for in L2
 constexpr int kExpTile = 256;          // tokens of a tile, half of them to either block
 constexpr int kExpRows = 2 * kExpTile; // tokens of a task
@@ -64,14 +71,17 @@ struct ExpSmem {
     static constexpr int kBarsEnd = kDrain + 8;
     static constexpr int kMisc = kBarsEnd;                    // flags, TMEM address
     static constexpr int kSums = kMisc + 16;                  // int [12]: the scan's sums
-    static constexpr int kTasks = kSums + 64;                 // int [kExpMaxTasks]: a head's tasks, the dearest first
-    static constexpr int kBytes = kTasks + 4 * (kPagedMaxTokens / kExpRows + kPagedMaxSeqs);
+    static constexpr int kList = kSums + 64;                  // int [kExpMaxEntries]: what tasks are made of, the dearest first
+    static constexpr int kBytes = kList + 4 * (kPagedMaxTokens / kExpTile + kPagedMaxSeqs);
 };
 static_assert(ExpSmem::kBytes <= 227 * 1024, "it fits");
-// Tasks of a head at most, and how the list names one.
-constexpr int kExpMaxTasks = kPagedMaxTokens / kExpRows + kPagedMaxSeqs;
-constexpr int kExpTaskBits = 12;
-static_assert(kPagedMaxTokens / kExpRows < 1 << kExpTaskBits, "a request's task fits its bits");
+// An entry of the list: a request, a tile of it by its 256 tokens, whether the next tile belongs to it too, and
+// how many entries before it are of two tiles.
+constexpr int kExpMaxEntries = kPagedMaxTokens / kExpTile + kPagedMaxSeqs;
+constexpr int kExpNameBits = 20, kExpReqBits = 10;
+static_assert(kPagedMaxSeqs <= 1 << kExpReqBits && 2 * kPagedMaxTokens / kExpTile <= 1 << (kExpNameBits - kExpReqBits) &&
+              kExpMaxEntries <= 1 << (31 - kExpNameBits), "they fit their bits");
+static_assert(8 * kExpMaxEntries <= ExpSmem::kK, "the list is made where the queries go");
 
 // Tasks and how they are dealt out to `grid` clusters, from what a scan over the requests finds.
 struct ExpPlan {
@@ -87,25 +97,51 @@ CFA_HD ExpPlan latent_expanded_plan(int tasks, int grid) {
     return p;
 }
 
-// A task's part.
-struct ExpItem {
-    int req, h, tile;          // request, head, which 512 of its tokens
+// A tile's part: 256 tokens of a request and head, and some of its blocks of keys.
+struct ExpPart {
+    int h, first;              // head, first token of the tile in the request
     int tok0, n, k0, len;      // the request's tokens and keys
-    int part, parts;           // which of how many parts of its blocks
-    int b0, end0, end1;        // first block of keys, and behind the last one that each tile sees
-    int rec;                   // its record's number
-    __device__ __forceinline__ int end(int t) const { return t ? end1 : end0; }
-    __device__ __forceinline__ int last() const { return max(end0, end1); }
-    __device__ __forceinline__ int rows(int t) const { return max(0, min(kExpTile, n - tile * kExpRows - kExpTile * t)); }
+    int b0, end;               // blocks of keys
+    __device__ __forceinline__ int rows() const { return max(0, min(kExpTile, n - first)); }
     // keys that token i of the request sees
     __device__ __forceinline__ int visible(int i) const { return max(0, min(len, len - n + i + 1)); }
 };
+// A task's part.
+struct ExpItem {
+    ExpPart a, b;              // of either tile
+    bool shared;               // of the same keys: blocks are loaded once for both
+    int part, parts;           // which of how many parts
+    int rec;                   // its record's number
+    __device__ __forceinline__ int blocks() const { return max(a.end - a.b0, b.end - b.b0); }
+    // Blocks that are loaded; and the place among them of tile t's j-th (they go by turns).
+    __device__ __forceinline__ int loaded() const { return shared ? blocks() : a.end - a.b0 + b.end - b.b0; }
+    __device__ __forceinline__ int place(int t, int j) const {
+        return shared ? j : j + (t ? min(j + 1, a.end - a.b0) : min(j, b.end - b.b0));
+    }
+};
 
-// Lists a head's tasks in smem, (request << 12 | which 512 tokens), those of most blocks first: dealt out in turn
-// and back, they come out even, and what is left for the last round is cheap. The number of all
-// heads', or -1 where the offsets are not in order. `work` holds 8 kExpMaxTasks bytes. By all threads of the block.
+// The entries of a request: fn(name, keys) for every one.
+template <typename Fn>
+__device__ __forceinline__ int latent_expanded_entries(int b, int n, int len, const Fn &fn) {
+    int entries = 0;
+    CFA_ROLLED for (int i = 0; i * kExpTile < n; ++entries) {
+        const int keys = min(len, max(0, len - n + (i + 2) * kExpTile));  // (half a block more or less is no matter)
+        const bool two = keys > kExpShared && (i + 1) * kExpTile < n;
+        fn(b << (kExpNameBits - kExpReqBits) | i << 1 | (two ? 1 : 0), keys);
+        i += two ? 2 : 1;
+    }
+    return entries;
+}
+// Tasks of the entries before entry `at`: an entry of two tiles makes a task for every head, one of a single tile for
+// every two heads.
+__device__ __forceinline__ int latent_expanded_start(const LatentExpandedParams &p, int at, int twos) {
+    return twos * p.H + (at - twos) * ((p.H + 1) / 2);
+}
+// Lists the entries in smem, those of most blocks first: dealt out in turn and back, tasks come out even, and
+// what is left for the last round is cheap. The number of tasks, or -1 where the offsets are not in order, and of
+// entries. `work` holds 8 bytes an entry. By all threads of the block.
 template <int kThreads>
-__device__ __forceinline__ int latent_expanded_list(const LatentExpandedParams &p, int *list, int2 *work, int *sums) {
+__device__ __forceinline__ int latent_expanded_list(const LatentExpandedParams &p, int *list, int2 *work, int *sums, int &entries) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + kThreads - 1) / kThreads, first = tid * per, last = min(p.B, first + per);
     int mine = 0;
@@ -113,7 +149,7 @@ __device__ __forceinline__ int latent_expanded_list(const LatentExpandedParams &
     CFA_ROLLED for (int b = first; b < last; ++b) {
         const int a = __ldcg(p.cu + b), e = __ldcg(p.cu + b + 1), ka = __ldcg(p.cu_k + b), ke = __ldcg(p.cu_k + b + 1);
         if (a < 0 || e < a || e > p.T || ka < 0 || ke < ka || ke > p.S) bad = true;
-        else mine += (e - a + kExpRows - 1) / kExpRows;
+        else mine += latent_expanded_entries(b, e - a, ke - ka, [](int, int) {});
     }
     int scan = mine;
     CFA_ROLLED for (int o = 1; o < 32; o <<= 1) {
@@ -128,47 +164,66 @@ __device__ __forceinline__ int latent_expanded_list(const LatentExpandedParams &
         if (w < warp) at += sums[w];
         all += sums[w];
     }
+    entries = refused ? 0 : all;
     if (refused) return -1;
-    CFA_ROLLED for (int b = first; b < last; ++b) {
-        const int tok0 = __ldcg(p.cu + b), n = __ldcg(p.cu + b + 1) - tok0;
-        const int len = __ldcg(p.cu_k + b + 1) - __ldcg(p.cu_k + b);
-        CFA_ROLLED for (int i = 0; i * kExpRows < n; ++i)  // (named by its keys: half of them more or less is no matter)
-            work[at++] = make_int2(min(len, max(0, len - n + (i + 1) * kExpRows)), b << kExpTaskBits | i);
-    }
+    CFA_ROLLED for (int b = first; b < last; ++b)
+        latent_expanded_entries(b, __ldcg(p.cu + b + 1) - __ldcg(p.cu + b), __ldcg(p.cu_k + b + 1) - __ldcg(p.cu_k + b),
+                                [&](int name, int keys) { work[at++] = make_int2(keys, name); });
     __syncthreads();
+    int twos = 0;
     CFA_ROLLED for (int i = tid; i < all; i += kThreads) {
         const int2 x = work[i];
-        int rank = 0;
-        CFA_ROLLED for (int j = 0; j < all; ++j) rank += work[j].x > x.x || (work[j].x == x.x && j < i);
-        list[rank] = x.y;
+        int rank = 0, before = 0;
+        twos = 0;
+        CFA_ROLLED for (int j = 0; j < all; ++j) {
+            const int2 y = work[j];
+            const int ahead = y.x > x.x || (y.x == x.x && j < i);
+            rank += ahead;
+            before += ahead & y.y;
+            twos += y.y & 1;
+        }
+        list[rank] = before << kExpNameBits | x.y;
     }
+    if (tid == 0) sums[0] = twos;  // (the first thread has an entry if anyone has)
     __syncthreads();
-    return all * p.H;
+    return latent_expanded_start(p, all, sums[0]);
 }
 
+// 256 tokens from `first` on of request b and head h; their blocks.
+__device__ __forceinline__ int latent_expanded_tile(const LatentExpandedParams &p, int b, int first, int h, ExpPart &x) {
+    x = ExpPart{};
+    if (h >= p.H) return 0;
+    x.h = h;
+    x.first = first;
+    x.tok0 = __ldcg(p.cu + b);
+    x.n = __ldcg(p.cu + b + 1) - x.tok0;
+    x.k0 = __ldcg(p.cu_k + b);
+    x.len = __ldcg(p.cu_k + b + 1) - x.k0;
+    return (x.visible(x.first + x.rows() - 1) + 127) / 128;
+}
 // Task number `task`, part `part` of at most `parts`; false where it has fewer.
-__device__ __forceinline__ bool latent_expanded_item(const LatentExpandedParams &p, const int *list, int task, int part,
+__device__ __forceinline__ bool latent_expanded_item(const LatentExpandedParams &p, const int *list, int entries, int task, int part,
                                                      int parts, ExpItem &x) {
-    const int at = task / p.by_H, lo = list[at] >> kExpTaskBits;
-    x.req = lo;
-    x.h = task - at * p.H;
-    x.tile = list[at] & ((1 << kExpTaskBits) - 1);
-    x.tok0 = __ldcg(p.cu + lo);
-    x.n = __ldcg(p.cu + lo + 1) - x.tok0;
-    x.k0 = __ldcg(p.cu_k + lo);
-    x.len = __ldcg(p.cu_k + lo + 1) - x.k0;
-    auto blocks_of = [&](int t) {
-        const int rows = x.rows(t);
-        return rows > 0 ? (x.visible(x.tile * kExpRows + kExpTile * t + rows - 1) + 127) / 128 : 0;
-    };
-    const int e0 = blocks_of(0), e1 = blocks_of(1), blocks = max(e0, e1);
+    int lo = 0, hi = entries;  // the last entry whose tasks begin no later
+    CFA_ROLLED while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (latent_expanded_start(p, mid, list[mid] >> kExpNameBits) <= task) lo = mid;
+        else hi = mid;
+    }
+    const int name = list[lo], k = task - latent_expanded_start(p, lo, name >> kExpNameBits);
+    const int req = name >> (kExpNameBits - kExpReqBits) & ((1 << kExpReqBits) - 1);
+    const int first = (name >> 1 & ((1 << (kExpNameBits - kExpReqBits - 1)) - 1)) * kExpTile;
+    x.shared = name & 1;
+    const int na = latent_expanded_tile(p, req, first, x.shared ? k : 2 * k, x.a);
+    const int nb = latent_expanded_tile(p, req, x.shared ? first + kExpTile : first, x.shared ? k : 2 * k + 1, x.b), blocks = max(na, nb);
     x.part = part;
     x.parts = max(1, min(parts, blocks / kExpLeast));
     if (part >= x.parts) return false;
-    x.b0 = blocks * part / x.parts;
-    const int b1 = blocks * (part + 1) / x.parts;
-    x.end0 = max(x.b0, min(b1, e0));
-    x.end1 = max(x.b0, min(b1, e1));
+    const int from = blocks * part / x.parts, to = blocks * (part + 1) / x.parts;
+    x.a.b0 = from;
+    x.a.end = max(from, min(to, na));
+    x.b.b0 = from;
+    x.b.end = max(from, min(to, nb));
     return true;
 }
 
@@ -186,7 +241,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     int *misc = reinterpret_cast<int *>(smem + S::kMisc);
     volatile int *timed_out = misc;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 1);
-    int *list = reinterpret_cast<int *>(smem + S::kTasks);
+    int *list = reinterpret_cast<int *>(smem + S::kList);
 
     // a thread a barrier, with the arrivals it expects
     if (tid < (S::kBarsEnd - S::kBars) / 8) {
@@ -210,8 +265,9 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     tcgen05_fence_before();
     cluster_arrive();  // (the other block's barriers are ready behind the wait below)
     grid_dependency_wait();
+    int entries;
     const int tasks = latent_expanded_list<kExpThreads>(p, list, reinterpret_cast<int2 *>(smem + S::kQ),  // (free yet)
-                                                        reinterpret_cast<int *>(smem + S::kSums));
+                                                        reinterpret_cast<int *>(smem + S::kSums), entries);
     tcgen05_fence_after();
     if (blockIdx.x == 0 && tid == 0 && tasks < 0) atomicOr(p.status, kStatusBadLengthBit);
     grid_dependents_launch();
@@ -225,10 +281,10 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     // The cluster's item of round r; false where it has none.
     auto item = [&](int r, ExpItem &x) {
         const int at = r & 1 ? grid - 1 - cluster : cluster;
-        if (r < plan.full) return latent_expanded_item(p, list, r * grid + at, 0, 1, x);
+        if (r < plan.full) return latent_expanded_item(p, list, entries, r * grid + at, 0, 1, x);
         const int task = at / plan.parts, part = at - task * plan.parts;
         x.rec = at;
-        return task < plan.rest && latent_expanded_item(p, list, plan.full * grid + task, part, plan.parts, x);
+        return task < plan.rest && latent_expanded_item(p, list, entries, plan.full * grid + task, part, plan.parts, x);
     };
     const int rounds = plan.full + (plan.rest > 0);
     // The first item from round r on, r becomes the round behind it; false at the end.
@@ -254,55 +310,68 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             ExpItem x, ahead;
             bool have = next(r, x);
             for (; ok && have; x = ahead) {
-                const int last = x.last();
-                have = next(r, ahead);
-                CFA_ROLLED for (int b = x.b0; ok && b < last; ++b, ++n) {
+                const int blocks = x.blocks();
+                auto load = [&](const ExpPart &z, int j) {  // a block's keys or values
+                    if (!ok || j >= z.end - z.b0) return;
                     const uint32_t slot = n % kExpSlots, again = n / kExpSlots;
                     const int full = (values ? S::kFullV : S::kFullK) + 8 * slot;
                     if (again > 0) ok = wait_warp((values ? S::kEmptyV : S::kEmptyK) + 8 * slot, (again - 1) & 1, kSiteStageEmpty);
-                    if (!ok) break;
+                    if (!ok) return;
                     if (elect_one()) {
                         if (!values) {  // 64 of the keys
                             const uint32_t dst = base + S::kK + slot * kExpKSlot;
-                            const int y = x.k0 + 128 * b + 64 * rank;
+                            const int y = z.k0 + 128 * (z.b0 + j) + 64 * rank;
                             mbar_arrive_expect_tx(base + full, kExpKSlot);
-                            tma_load_2d(dst, &tm_kv, x.h * kLatKv, y, base + full);
-                            tma_load_2d(dst + 64 * 128, &tm_kv, x.h * kLatKv + 64, y, base + full);
+                            tma_load_2d(dst, &tm_kv, z.h * kLatKv, y, base + full);
+                            tma_load_2d(dst + 64 * 128, &tm_kv, z.h * kLatKv + 64, y, base + full);
                             tma_load_2d(dst + 2 * 64 * 128, &tm_rope, 0, y, base + full);
                         } else {        // 64 of the dims
                             const uint32_t dst = base + S::kV + slot * kExpVSlot;
-                            const int dim = x.h * kLatKv + kLatN + 64 * rank, y = x.k0 + 128 * b;
+                            const int dim = z.h * kLatKv + kLatN + 64 * rank, y = z.k0 + 128 * (z.b0 + j);
                             mbar_arrive_expect_tx(base + full, kExpVSlot);
                             tma_load_2d(dst, &tm_kv, dim, y, base + full);
                             tma_load_2d(dst + 64 * 128, &tm_kv, dim, y + 64, base + full);
-                            if (have && b == max(x.b0, last - kExpPeek)) {
-                                // the next item's queries, in L2 by the time they are loaded
-#pragma unroll 1
-                                for (int i = 0; i < 6; ++i)
-                                    if (ahead.end(i / 3) > ahead.b0)
-                                        tma_prefetch_2d(&tm_q, ahead.h * kLatQ + 64 * (i % 3),
-                                                        ahead.tok0 + ahead.tile * kExpRows + kExpTile * (i / 3) + 128 * rank);
-                            }
                         }
                     }
                     __syncwarp();
-                    if (values || b > x.b0) continue;
-                    // the queries behind the first keys, which find room earlier
-                    CFA_ROLLED for (int t = 0; ok && t < 2; ++t) {
-                        if (x.end(t) == x.b0) continue;
-                        if (queried >> t & 1) ok = wait_warp(S::kEmptyQ + 8 * t, ~queries >> t & 1, kSiteStageEmpty);
-                        if (!ok) break;
-                        if (elect_one()) {
-                            const uint32_t full_q = base + S::kFullQ + 8 * t;
-                            mbar_arrive_expect_tx(full_q, 3 * kExpChunk);
+                    ++n;
+                };
+                auto query = [&](const ExpPart &z, int t) {
+                    if (!ok || z.end == z.b0) return;
+                    if (queried >> t & 1) ok = wait_warp(S::kEmptyQ + 8 * t, ~queries >> t & 1, kSiteStageEmpty);
+                    if (!ok) return;
+                    if (elect_one()) {
+                        const uint32_t full_q = base + S::kFullQ + 8 * t;
+                        mbar_arrive_expect_tx(full_q, 3 * kExpChunk);
 #pragma unroll
-                            for (int c = 0; c < 3; ++c)
-                                tma_load_2d(base + S::kQ + (3 * t + c) * kExpChunk, &tm_q, x.h * kLatQ + 64 * c,
-                                            x.tok0 + x.tile * kExpRows + kExpTile * t + 128 * rank, full_q);
-                        }
+                        for (int c = 0; c < 3; ++c)
+                            tma_load_2d(base + S::kQ + (3 * t + c) * kExpChunk, &tm_q, z.h * kLatQ + 64 * c, z.tok0 + z.first + 128 * rank,
+                                        full_q);
+                    }
+                    __syncwarp();
+                    queried |= 1u << t;
+                    queries ^= 1u << t;
+                };
+                // the next item's queries, in L2 by the time they are loaded
+                auto ask = [&](const ExpPart &z) {
+                    if (z.end == z.b0 || !elect_one()) return;
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) tma_prefetch_2d(&tm_q, z.h * kLatQ + 64 * c, z.tok0 + z.first + 128 * rank);
+                };
+                if (blocks == 0) have = next(r, ahead);
+                CFA_ROLLED for (int j = 0; ok && j < blocks; ++j) {
+                    if (!x.shared) load(x.a, j);
+                    load(x.b, j);
+                    if (!values && j == 0) {  // the queries behind the first keys, which find room earlier
+                        query(x.a, 0);
+                        query(x.b, 1);
+                    }
+                    if (j == 0) have = next(r, ahead);  // (behind the first copies)
+                    if (values && have && j == max(0, blocks - kExpPeek)) {
+                        ask(ahead.a);
                         __syncwarp();
-                        queried |= 1u << t;
-                        queries ^= 1u << t;
+                        ask(ahead.b);
+                        __syncwarp();
                     }
                 }
             }
@@ -321,8 +390,8 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             __syncwarp();
         } else if (warp == kExpRelayWarp) {
             // ----------------------------------------------------------------- relay warp
-            // tells the issuing block what has landed, in the order in which the products take it: keys of a
-            // block ahead, values
+            // tells the issuing block what has landed, in the order in which the products take it: by turns of a tile,
+            // keys of a block ahead, values
             uint32_t nk = 0, nv = 0, queries = 0;
             const uint32_t ready_k = map_to_rank(base + S::kReadyK, 0), ready_v = map_to_rank(base + S::kReadyV, 0),
                            ready_q = map_to_rank(base + S::kReadyQ, 0);
@@ -339,51 +408,29 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             int r = 0;
             ExpItem x;
             while (ok && next(r, x)) {
-                if (x.last() == x.b0) continue;
-                // keys that every row of a tile sees, and that any row of the task does
-                const int some0 = x.visible(x.tile * kExpRows), some1 = x.visible(x.tile * kExpRows + kExpTile);
-                const int all = x.visible(min(x.n, x.tile * kExpRows + kExpRows) - 1);
-                keys();
-                CFA_ROLLED for (int t = 0; t < 2; ++t) {
-                    if (x.end(t) == x.b0) continue;
+                auto begin = [&](const ExpPart &z, int t) {
+                    if (z.end == z.b0) return;
+                    if (t == 1 || !x.shared) keys();
+                };
+                auto query = [&](const ExpPart &z, int t) {
+                    if (z.end == z.b0) return;
                     pass_on(S::kFullQ + 8 * t, ready_q + 8 * t, queries >> t & 1);
                     queries ^= 1u << t;
-                }
-                CFA_ROLLED for (int b = x.b0; ok && b < x.last(); ++b, ++nv) {
-                    if (b + 1 < x.last()) keys();
-                    const uint32_t slot = nv % kExpSlots;
-                    ok = ok && wait_warp(S::kFullV + 8 * slot, (nv / kExpSlots) & 1, kSiteStageFull);
-                    const int begin = (b < x.end0 ? some0 : some1) - 128 * b, end = all - 128 * b;
-                    if (ok && begin < 128) {
-                        // Keys from `begin` on are not seen by every row, from `end` on by none. A masked weight is 0, and 0
-                        // times NaN is NaN: what is not finite of the first becomes 0, and the merge adds it to the rows that
-                        // see it; the others become 0. (A lane 16 bytes of every fourth row; of a row's chunks any order will do.)
-                        uint8_t *v = smem + S::kV + slot * kExpVSlot + (lane >> 3) * 128 + ((lane & 7) << 4);
-                        CFA_ROLLED for (int k0 = max(0, begin) & ~31; k0 < 128; k0 += 32) {
-                            uint4 d[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) d[i] = *reinterpret_cast<const uint4 *>(v + k0 * 128 + i * 512);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int k = k0 + 4 * i + (lane >> 3);
-                                // an exponent of ones and the 1 added to it carry into the sign's place
-                                auto carry = [](uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; };
-                                const uint32_t odd = (carry(d[i].x) | carry(d[i].y) | carry(d[i].z) | carry(d[i].w)) & 0x80008000u;
-                                if (k < begin || (k < end && odd == 0u)) continue;
-                                uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                                if (k < end) {
-                                    *p.odd = 1u;
-                                    w = make_uint4(d[i].x & ~odd_bf16x2(d[i].x), d[i].y & ~odd_bf16x2(d[i].y),
-                                                   d[i].z & ~odd_bf16x2(d[i].z), d[i].w & ~odd_bf16x2(d[i].w));
-                                }
-                                *reinterpret_cast<uint4 *>(v + k0 * 128 + i * 512) = w;
-                            }
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    if (ok && elect_one()) mbar_arrive_pair(ready_v + 8 * slot);
-                    __syncwarp();
+                };
+                auto block = [&](const ExpPart &z, int j) {
+                    const int b = z.b0 + j;
+                    if (b + 1 < z.end) keys();
+                    if (b >= z.end) return;
+                    pass_on(S::kFullV + 8 * (nv % kExpSlots), ready_v + 8 * (nv % kExpSlots), (nv / kExpSlots) & 1);
+                    ++nv;
+                };
+                begin(x.a, 0);
+                begin(x.b, 1);
+                query(x.a, 0);
+                query(x.b, 1);
+                CFA_ROLLED for (int j = 0; ok && j < x.blocks(); ++j) {
+                    if (!x.shared) block(x.a, j);
+                    block(x.b, j);
                 }
             }
         } else if (warp == kExpMmaWarp && rank == 0) {
@@ -392,45 +439,49 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             const uint32_t idesc_s = umma_idesc_bf16(256, 128, false, false), idesc_o = umma_idesc_bf16(256, 128, false, true);
             const uint64_t q0 = umma_smem_desc(base + S::kQ, 16, 1024), k0 = umma_smem_desc(base + S::kK, 16, 1024),
                            v0 = umma_smem_desc(base + S::kV, kExpVSlot, 1024);
-            uint32_t n = 0, queries = 0, weights = 0;  // blocks before the item's; phases, a bit a tile
+            uint32_t n = 0, queries = 0, weights = 0;  // blocks loaded before the item's; phases, a bit a tile
             bool ok = true;
             int r = 0;
             ExpItem x, ahead;
             bool have = next(r, x);
             for (; ok && have; x = ahead) {
-                const int last = x.last(), b0 = x.b0;
-                // By one thread: scores of tile t and block b. `frees`: nobody reads the keys after.
-                auto scores = [&](int t, int b, bool frees) {
-                    const uint32_t slot = (n + b - b0) % kExpSlots;
+                const int na = x.a.end - x.a.b0, nb = x.b.end - x.b.b0, blocks = max(na, nb);
+                // By one thread: the scores of tile t's block j.
+                auto scores = [&](int t, uint32_t k) {
+                    const uint32_t slot = k % kExpSlots;
                     const uint64_t a = q0 + 3 * t * (kExpChunk >> 4), bd = k0 + slot * (kExpKSlot >> 4);
 #pragma unroll
                     for (int ks = 0; ks < 12; ++ks)  // 32 bytes a step
                         umma2_bf16(tm + 128 * t, a + (ks >> 2) * (kExpChunk >> 4) + 2 * (ks & 3),
                                    bd + (ks >> 2) * (64 * 128 >> 4) + 2 * (ks & 3), idesc_s, ks > 0);
-                    if (frees) umma2_commit(base + S::kEmptyK + 8 * slot);
+                    if (t == 1 || !x.shared) umma2_commit(base + S::kEmptyK + 8 * slot);
                     umma2_commit(base + S::kScores + 8 * t);
                 };
-                auto keys = [&](int b) {
-                    const uint32_t k = n + b - b0;
-                    ok = ok && wait_warp(S::kReadyK + 8 * (k % kExpSlots), (k / kExpSlots) & 1, kSiteStageFull);
+                // Keys or values of tile t's block j have landed (with shared ones the first tile waits for both).
+                auto landed = [&](int ready, int t, int j, uint32_t k) {
+                    if (x.shared && t == 1 && j < na) return;
+                    ok = ok && wait_warp(ready + 8 * (k % kExpSlots), (k / kExpSlots) & 1, kSiteStageFull);
                 };
-                if (last > b0) keys(b0);
                 CFA_ROLLED for (int t = 0; ok && t < 2; ++t) {
-                    if (x.end(t) == b0) continue;
-                    ok = wait_warp(S::kReadyQ + 8 * t, queries >> t & 1, kSiteQExchange);
+                    if ((t ? nb : na) == 0) continue;
+                    const uint32_t k = n + x.place(t, 0);
+                    landed(S::kReadyK, t, 0, k);
+                    ok = ok && wait_warp(S::kReadyQ + 8 * t, queries >> t & 1, kSiteQExchange);
                     queries ^= 1u << t;
                     tcgen05_fence_after();
-                    if (ok && elect_one()) scores(t, b0, t == 1 || x.end1 == b0);
+                    if (ok && elect_one()) scores(t, k);
                     __syncwarp();
                 }
                 have = next(r, ahead);  // (beside the first softmax)
-                CFA_ROLLED for (int b = b0; ok && b < last; ++b) {
-                    const uint32_t slot = (n + b - b0) % kExpSlots;
-                    if (b + 1 < last) keys(b + 1);
-                    ok = ok && wait_warp(S::kReadyV + 8 * slot, ((n + b - b0) / kExpSlots) & 1, kSiteStageFull);
+                CFA_ROLLED for (int j = 0; ok && j < blocks; ++j) {
                     CFA_ROLLED for (int t = 0; ok && t < 2; ++t) {
-                        if (b >= x.end(t)) continue;
-                        ok = wait_warp(S::kWeights + 8 * t, weights >> t & 1, kSiteSoftmaxExchange);
+                        const int end = t ? nb : na;
+                        if (j >= end) continue;
+                        const bool more = j + 1 < end;
+                        const uint32_t k = n + x.place(t, j + 1), v = n + x.place(t, j), slot = v % kExpSlots;
+                        if (more) landed(S::kReadyK, t, j + 1, k);
+                        landed(S::kReadyV, t, j, v);
+                        ok = ok && wait_warp(S::kWeights + 8 * t, weights >> t & 1, kSiteSoftmaxExchange);
                         weights ^= 1u << t;
                         tcgen05_fence_after();
                         // the product and the next scores in one go: between two goes the tensor core runs dry for some 400 clocks
@@ -438,16 +489,16 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
 #pragma unroll
                             for (int ks = 0; ks < 8; ++ks)  // 16 keys of 128 bytes a step
                                 umma2_bf16_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * ks, v0 + slot * (kExpVSlot >> 4) + 128 * ks,
-                                              idesc_o, b > b0 || ks > 0);
-                            if (t == 1 || b >= x.end1) umma2_commit(base + S::kEmptyV + 8 * slot);
+                                              idesc_o, j > 0 || ks > 0);
+                            if (t == 1 || !x.shared) umma2_commit(base + S::kEmptyV + 8 * slot);
                             // behind the last product there are no more scores, but the tile's warps learn that it ended
-                            if (b + 1 < x.end(t)) scores(t, b + 1, t == 1 || b + 1 >= x.end1);
+                            if (more) scores(t, k);
                             else umma2_commit(base + S::kScores + 8 * t);
                         }
                         __syncwarp();
                     }
                 }
-                n += last - b0;
+                n += x.loaded();
             }
             if (elect_one() && *timed_out) {
                 // a wait gave up: the products in flight end before the blocks do
@@ -466,23 +517,26 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         const uint32_t t_s = tmem + lanes + 128 * t, t_o = tmem + lanes + 256 + 128 * t;
         const int scores = S::kScores + 8 * t;
         const uint32_t weights = map_to_rank(base + S::kWeights, 0) + 8 * t;
-        uint32_t scored = 0;  // phases
+        uint32_t scored = 0, nv = 0;  // phases; both tiles' blocks before the item's
         int r = 0;
         ExpItem x, ahead;
         bool have = next(r, x);
         for (; have; x = ahead) {
-            // of a split task, for the merge: where its rows are and how many parts it has
-            if (r > plan.full && plan.parts > 1 && x.part == 0 && rank == 0 && tid == 0)
-                p.splits[x.rec / plan.parts] = make_int4((x.tok0 + x.tile * kExpRows) * p.H + x.h, min(kExpRows, x.n - x.tile * kExpRows),
-                                                         x.parts, x.rec);
-            const int first = x.tile * kExpRows + kExpTile * t + 128 * rank;  // this block's first token of the tile
-            const int rows = max(0, min(128, x.rows(t) - 128 * rank));
+            const ExpPart z = t ? x.b : x.a;
+            // of a split task, for the merge: where a tile's rows are and how many parts it has
+            if (r > plan.full && plan.parts > 1 && x.part == 0 && rank == 0 && row == 0)
+                p.splits[2 * (x.rec / plan.parts) + t] = make_int4((z.tok0 + z.first) * p.H + z.h, z.rows(), x.parts, x.rec);
+            const int first = z.first + 128 * rank;  // this block's first token of the tile
+            const int rows = max(0, min(128, z.rows() - 128 * rank));
             const bool live = row < rows, warp_live = row - lane < rows;
             // (rows past the last see what that one sees, so that their warp takes no masked blocks for them: they took 20%
             // of the time of a prompt that ends inside a warp's rows)
-            const int see = x.visible(first + min(row, max(rows, 1) - 1));
+            const int see = z.visible(first + min(row, max(rows, 1) - 1));
+            // keys that every row of the tile sees, and that any does to whom they belong; blocks whose values it looks over
+            const int some = z.visible(z.first), all = t || x.shared ? x.b.visible(x.b.first + x.b.rows() - 1) : z.visible(z.first + z.rows() - 1);
+            const int look = x.shared && t ? x.a.end : z.b0;
             float m = -INFINITY, l = 0.f;
-            CFA_ROLLED for (int b = x.b0; b < x.end(t); ++b, ++scored) {
+            CFA_ROLLED for (int b = z.b0; b < z.end; ++b, ++scored) {
                 wait(scores, scored & 1, kSiteSoftmaxExchange);
                 __syncwarp();
                 tcgen05_fence_after();
@@ -512,7 +566,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                         const float g = m == mn ? 1.f : exp2_ftz(m - mn);
                         m = mn;
                         l *= g;
-                        if (b > x.b0) {
+                        if (b > z.b0) {
 #pragma unroll 1
                             for (int c = 0; c < kLatV; c += 32) {
                                 uint32_t v[32];
@@ -545,11 +599,39 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     l += both.x + both.y;
                     tmem_wait_st();
                 }
+                if (some < 128 * (b + 1) && b >= look) {
+                    // Keys from `some` on are not seen by every row, from `all` on by none. A masked weight is 0, and 0
+                    // times NaN is NaN: what is not finite becomes 0, and the merge adds it to the rows that see it. (A
+                    // thread 16 bytes of every 16th row; of a row's chunks any order will do.)
+                    const uint32_t at = nv + x.place(t, b - z.b0);
+                    wait(S::kFullV + 8 * (at % kExpSlots), (at / kExpSlots) & 1, kSiteStageFull);
+                    __syncwarp();
+                    uint8_t *v = smem + S::kV + at % kExpSlots * kExpVSlot + (row >> 3) * 128 + ((row & 7) << 4);
+                    const int k0 = 128 * b + (row >> 3);
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t m2 = max_abs_bf16x8(most, *reinterpret_cast<const uint4 *>(v + i * 2048));
+                        most = k0 + 16 * i < some ? most : m2;
+                    }
+                    if (odd_bf16x2(most) != 0u) {
+                        CFA_ROLLED for (int i = 0; i < 8; ++i) {
+                            const int k = k0 + 16 * i;
+                            if (k < some) continue;
+                            uint4 w = *reinterpret_cast<const uint4 *>(v + i * 2048);
+                            const uint32_t f = odd_bf16x2(w.x), h = odd_bf16x2(w.y), o = odd_bf16x2(w.z), q = odd_bf16x2(w.w);
+                            if ((f | h | o | q) != 0u && k < all) *p.odd = 1u;
+                            *reinterpret_cast<uint4 *>(v + i * 2048) = make_uint4(w.x & ~f, w.y & ~h, w.z & ~o, w.w & ~q);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                }
                 tcgen05_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_pair(weights);
             }
-            const bool any = x.end(t) > x.b0;
+            nv += x.loaded();
+            const bool any = z.end > z.b0;
             have = next(r, ahead);  // (its loads are on their way meanwhile)
             if (any) {
                 wait(scores, scored & 1, kSiteKvExchange);
@@ -560,7 +642,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             // ---- the tile's results, or its record
             if (warp_live) {
                 const int in_task = kExpTile * t + 128 * rank + row;
-                const size_t tok = static_cast<size_t>(x.tok0 + first + row);
+                const size_t tok = static_cast<size_t>(z.tok0 + first + row);
                 if (x.parts > 1) {
                     if (live) p.rec_ml[x.rec * kExpRows + in_task] = make_float2(m, l);
                     float *rec_o = p.rec_o + static_cast<size_t>(x.rec) * kExpRows * kLatV + 4 * in_task;
@@ -577,7 +659,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                                 make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                     }
                 } else {
-                    if (p.lse && live) p.lse[tok * p.H + x.h] = (m + log2f(l)) * 0.69314718055994531f;
+                    if (p.lse && live) p.lse[tok * p.H + z.h] = (m + log2f(l)) * 0.69314718055994531f;
                     const float inv = l == 0.f ? 0.f : 1.f / l;
                     // through the tile's first chunk of queries, which nobody reads any more, so that a row's 128 bytes
                     // are written together
@@ -609,7 +691,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
 #pragma unroll
                             for (int e = 0; e < 8; ++e) y[e] = make_uint4(0u, 0u, 0u, 0u);
                         }
-                        uint16_t *out = p.out + ((tok - lane) * p.H + x.h) * kLatV + c + 8 * (lane & 7);
+                        uint16_t *out = p.out + ((tok - lane) * p.H + z.h) * kLatV + c + 8 * (lane & 7);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const int k = 4 * e + (lane >> 3);
@@ -677,9 +759,9 @@ __global__ void __launch_bounds__(kLatMergeThreads, 3) latent_expanded_merge_ker
     const int lane = threadIdx.x & 31, warps = static_cast<int>(gridDim.x) * (kLatMergeThreads / 32);
     constexpr int kRec = kExpRows * (kLatV / 4);
     CFA_ROLLED for (int i = static_cast<int>(blockIdx.x) * (kLatMergeThreads / 32) + (threadIdx.x >> 5); i < rest * 128; i += warps) {
-        const int4 x = __ldcg(p.splits + (i >> 7));  // the first row's place, rows, parts, the first record
-        const int row = (i & 15) * 32 + lane, chunk = (i >> 4 & 7) * 4, parts = x.z;
-        if (parts == 1 || row >= x.y) continue;
+        const int4 x = __ldcg(p.splits + 2 * (i >> 7) + (i >> 3 & 1));  // the tile's first row's place, rows, parts, the first record
+        const int row = (i & 15) * 32 + lane, in_tile = row % kExpTile, chunk = (i >> 4 & 7) * 4, parts = x.z;
+        if (parts == 1 || in_tile >= x.y) continue;
         const float2 *ml = p.rec_ml + x.w * kExpRows + row;
         const float4 *o = reinterpret_cast<const float4 *>(p.rec_o) + static_cast<size_t>(x.w) * kRec + chunk * kExpRows + row;
         float m = -INFINITY, l = 0.f;
@@ -704,7 +786,7 @@ __global__ void __launch_bounds__(kLatMergeThreads, 3) latent_expanded_merge_ker
             }
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const size_t at = static_cast<size_t>(x.x) + static_cast<size_t>(row) * p.H;
+        const size_t at = static_cast<size_t>(x.x) + static_cast<size_t>(in_tile) * p.H;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
             *reinterpret_cast<uint4 *>(p.out + at * kLatV + 4 * chunk + 8 * c) =

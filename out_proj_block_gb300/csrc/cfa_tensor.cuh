@@ -71,6 +71,15 @@ __device__ __forceinline__ float exp2_ftz(float x) {
 __device__ __forceinline__ uint32_t odd_bf16x2(uint32_t v) {
     return ((((v & 0x7f807f80u) + 0x00800080u) >> 15) & 0x00010001u) * 0xffffu;
 }
+// The larger magnitudes of two pairs of bf16, NaN where there is one (signs mean nothing); and of 16 bytes.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t m;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+}
+__device__ __forceinline__ uint32_t max_abs_bf16x8(uint32_t m, uint4 v) {
+    return max_abs_bf16x2(max_abs_bf16x2(m, max_abs_bf16x2(v.x, v.y)), max_abs_bf16x2(v.z, v.w));
+}
 
 // Two fp32 lanes in one instruction.
 __device__ __forceinline__ uint64_t pair_f32(float a, float b) {

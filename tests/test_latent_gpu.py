@@ -528,24 +528,25 @@ def test_expanded_refused_offsets(cfa, which):
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("where", ["key", "rope", "value"])
-def test_expanded_keys_not_seen_do_not_show(cfa, bad, where):
-    c = prompts(5, 3, [(200, 300), (150, 150)])
-    with cfa.Latent(2, 512, 3, 64) as plan:
+@pytest.mark.parametrize("n,L,j", [(200, 300, 250), (600, 2900, 2500), (600, 2900, 2750)])
+def test_expanded_keys_not_seen_do_not_show(cfa, bad, where, n, L, j):
+    c = prompts(5, 3, [(n, L), (150, 150)])
+    with cfa.Latent(2, 1024, 3, 64) as plan:
         good, gl = expanded(plan, c)
-        key, tok = c["ck"][0] + 250, 200 - 300 + 250  # the first token that sees the key
+        key, tok = c["ck"][0] + j, n - L + j  # the first token that sees the key
         at = dict(key=c["kv"][key, 1, 5:6], rope=c["k_rope"][key, 9:10], value=c["kv"][key, 1, 128 + 5:128 + 6])[where]
         at.fill_(bad)
         out, lse = expanded(plan, c)
         assert plan.status() == cfa.CFA_OK
     assert same_bits(out[:tok], good[:tok]) and torch.equal(lse[:tok], gl[:tok])
-    assert same_bits(out[200:], good[200:])
+    assert same_bits(out[n:], good[n:])
     if where == "value":
-        x = f64(out[tok:200, 1, 5])
+        x = f64(out[tok:n, 1, 5])
         assert (np.isnan(x) if math.isnan(bad) else x == bad).all()
-        out[tok:200, 1, 5] = good[tok:200, 1, 5]
+        out[tok:n, 1, 5] = good[tok:n, 1, 5]
         assert same_bits(out, good) and torch.equal(lse, gl)
     else:
-        assert same_bits(out[tok:200, 0], good[tok:200, 0]) or where == "rope"
+        assert same_bits(out[tok:n, 0], good[tok:n, 0]) or where == "rope"
 
 
 @pytest.mark.parametrize("H,pairs", [
@@ -553,6 +554,8 @@ def test_expanded_keys_not_seen_do_not_show(cfa, bad, where):
     (2, [(1 + n % 3, 40 + n) for n in range(300)]),
     (1, [(2500, 2500)]),                                         # tiles that are cut, and joined
     (7, [(130, 2100), (257, 257), (1, 3000), (300, 150)]),
+    (3, [(600, 3000), (257, 2700), (800, 2900)]),                # two tiles in a row of a head in a task
+    (1, [(2800, 2800), (513, 2561)]),
     (300, [(3, 140)]),
     (20, [(512 - n, 100 + n) for n in range(40)]),               # first halves that see no key, one after another
 ])
