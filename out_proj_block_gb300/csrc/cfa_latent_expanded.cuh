@@ -189,18 +189,6 @@ __device__ __forceinline__ int latent_expanded_list(const LatentExpandedParams &
     return latent_expanded_start(p, all, sums[0]);
 }
 
-// 256 tokens from `first` on of request b and head h; their blocks.
-__device__ __forceinline__ int latent_expanded_tile(const LatentExpandedParams &p, int b, int first, int h, ExpPart &x) {
-    x = ExpPart{};
-    if (h >= p.H) return 0;
-    x.h = h;
-    x.first = first;
-    x.tok0 = __ldcg(p.cu + b);
-    x.n = __ldcg(p.cu + b + 1) - x.tok0;
-    x.k0 = __ldcg(p.cu_k + b);
-    x.len = __ldcg(p.cu_k + b + 1) - x.k0;
-    return (x.visible(x.first + x.rows() - 1) + 127) / 128;
-}
 // Task number `task`, part `part` of at most `parts`; false where it has fewer.
 __device__ __forceinline__ bool latent_expanded_item(const LatentExpandedParams &p, const int *list, int entries, int task, int part,
                                                      int parts, ExpItem &x) {
@@ -213,13 +201,22 @@ __device__ __forceinline__ bool latent_expanded_item(const LatentExpandedParams 
     const int name = list[lo], k = task - latent_expanded_start(p, lo, name >> kExpNameBits);
     const int req = name >> (kExpNameBits - kExpReqBits) & ((1 << kExpReqBits) - 1);
     const int first = (name >> 1 & ((1 << (kExpNameBits - kExpReqBits - 1)) - 1)) * kExpTile;
+    const int tok0 = __ldcg(p.cu + req), tok1 = __ldcg(p.cu + req + 1), k0 = __ldcg(p.cu_k + req), k1 = __ldcg(p.cu_k + req + 1);
     x.shared = name & 1;
-    const int na = latent_expanded_tile(p, req, first, x.shared ? k : 2 * k, x.a);
-    const int nb = latent_expanded_tile(p, req, x.shared ? first + kExpTile : first, x.shared ? k : 2 * k + 1, x.b), blocks = max(na, nb);
+    x.a = ExpPart{x.shared ? k : 2 * k, first, tok0, tok1 - tok0, k0, k1 - k0, 0, 0};
+    x.b = x.a;
+    if (x.shared) x.b.first += kExpTile;
+    else if (++x.b.h >= p.H) x.b.n = 0;  // (the last of an odd number of heads is alone)
+    auto blocks_of = [](const ExpPart &z) { return z.rows() > 0 ? (z.visible(z.first + z.rows() - 1) + 127) / 128 : 0; };
+    const int na = blocks_of(x.a), nb = blocks_of(x.b), blocks = max(na, nb);
     x.part = part;
     x.parts = max(1, min(parts, blocks / kExpLeast));
     if (part >= x.parts) return false;
-    const int from = blocks * part / x.parts, to = blocks * (part + 1) / x.parts;
+    int from = 0, to = blocks;
+    if (x.parts > 1) {  // (a division takes 150 clocks)
+        from = blocks * part / x.parts;
+        to = blocks * (part + 1) / x.parts;
+    }
     x.a.b0 = from;
     x.a.end = max(from, min(to, na));
     x.b.b0 = from;
