@@ -34,6 +34,8 @@
 // rounding); their sum, the maxima, the outputs and the records are fp32.
 #pragma once
 
+#include <type_traits>
+
 #include <cuda.h>
 
 #include "cfa_device.cuh"
@@ -533,7 +535,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             const int some = z.visible(z.first), all = t || x.shared ? x.b.visible(x.b.first + x.b.rows() - 1) : z.visible(z.first + z.rows() - 1);
             const int look = x.shared && t ? x.a.end : z.b0;
             float m = -INFINITY, l = 0.f;
-            CFA_ROLLED for (int b = z.b0; b < z.end; ++b, ++scored) {
+            auto block = [&](auto masked, int b) {  // of keys; masked: that not every row sees as a whole
                 wait(scores, scored & 1, kSiteSoftmaxExchange);
                 __syncwarp();
                 tcgen05_fence_after();
@@ -543,7 +545,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     for (int c = 0; c < 128; c += 32) tmem_ld_x32(t_s + c, s + c);
                     tmem_wait_ld();
                     const int lim = see - 128 * b;
-                    if (!__all_sync(~0u, lim >= 128)) {
+                    if (masked.value && !__all_sync(~0u, lim >= 128)) {
                         const int least = __reduce_min_sync(~0u, lim);
 #pragma unroll
                         for (int g = 0; g < 128; g += 32)
@@ -596,7 +598,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     l += both.x + both.y;
                     tmem_wait_st();
                 }
-                if (some < 128 * (b + 1) && b >= look) {
+                if (masked.value && b >= look) {
                     // Keys from `some` on are not seen by every row, from `all` on by none. A masked weight is 0, and 0
                     // times NaN is NaN: what is not finite becomes 0, and the merge adds it to the rows that see it. (A
                     // thread 16 bytes of every 16th row; of a row's chunks any order will do.)
@@ -626,7 +628,12 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 tcgen05_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_pair(weights);
-            }
+                ++scored;
+            };
+            // (a loop for each: what few blocks need, in one loop with the others, made theirs 100 clocks longer)
+            const int whole = max(z.b0, min(z.end, some / 128));
+            CFA_ROLLED for (int b = z.b0; b < whole; ++b) block(std::false_type{}, b);
+            CFA_ROLLED for (int b = whole; b < z.end; ++b) block(std::true_type{}, b);
             nv += x.loaded();
             const bool any = z.end > z.b0;
             have = next(r, ahead);  // (its loads are on their way meanwhile)
