@@ -293,7 +293,7 @@ cfa_status launch_attention(cfa_latent *p, const AttnArgs &a, void *stream) {
                                  cfa::kLatAttnThreads, static_cast<size_t>(cfa::latent_attention_smem()), stream, args);
     if (st != CFA_OK) return st;
     void *margs[1] = {&kp};
-    return launch(cfa::latent_merge_kernel_ptr(), dim3(3u * static_cast<unsigned>(p->num_sms)),
+    return launch(cfa::latent_merge_kernel_ptr(), dim3(2u * static_cast<unsigned>(p->num_sms)),
                   cfa::kLatMergeThreads, 0, stream, margs);
 }
 

@@ -29,12 +29,13 @@
 // are bitwise reproducible. A row's maximum is followed lazily, a published method: O is rescaled
 // only when it grew by more than 8 (a factor 2^8, far inside fp32).
 //
-// Measured, with the merge (one GB300): 64 requests of some 8K rows, 128 heads 88 us (385 MB read once;
-// floor 57); 200 of some 2K, 32 heads 72 us (floor 47); 16 with four drafted tokens each, 20 heads 26 us; one of 4K rows
-// 16 us. In the middle of a run memory bounds it, at 6.2 TB/s (products take 2490 clocks of a block of keys,
-// the rows 2900); beside that stand the start (scan, first queries and keys: 9 us), the cut tiles' records (4 us, and 5
-// to 11 to merge them) and, with short requests, a tile's end, some 8000 clocks. Merging in the block that ends last
-// instead of in a second kernel took 105 us for the first of these.
+// Measured, with the merge (one GB300): 64 requests of some 8K rows, 128 heads 85 us (385 MB read once;
+// floor 57); 200 of some 2K, 32 heads 71 us (floor 47); 16 with up to four drafted tokens, 20 heads 25 us; one of 4K
+// rows 16 us. In the middle of a run memory bounds it, at 6.2 TB/s (products take 2490 clocks of a block of keys,
+// the rows 2900); beside that stand the start (scan, first queries and keys: 8 us), the cut tiles' records (1 to 6 us,
+// and 5 to 10 to merge them, 2 of which the launch takes) and, with short requests, a tile's end, some 8000 clocks.
+// Merging in the block that ends last instead of in a second kernel took 16 us more for the first of these; merging by
+// all blocks behind a wait for one another wants a cooperative launch, which costs 2 us by itself.
 //
 // Weights are rounded to bf16 for their product with the values (tensor cores take both operands in
 // one type; 2^-8 each, the size of the result's own rounding); their sum, the maxima, the outputs
@@ -654,20 +655,95 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     }
 }
 
-// Merges the records of the tiles that runs' ends cut. A warp takes 32 rows (a lane a row) of a tile, and 16 of
-// their dims where the tile has two pieces, 4 where it has more, whose records are read eight at a time: what
-// counts is that enough loads are on their way.
-__global__ void __launch_bounds__(kLatMergeThreads, 3) latent_merge_kernel(const __grid_constant__ LatentAttnParams p) {
-    constexpr int kWarps = kLatMergeThreads / 32, kRec = kLatTile * (kLatC / 4);
+// A warp's part of the merge of a tile: 32 rows, a lane a row, and kChunks times 4 dims; the records of its pieces are
+// read kMost at a time.
+template <int kChunks, int kMost>
+__device__ __forceinline__ void latent_merge_rows(const LatentAttnParams &p, int4 cut, int run, int row0, int chunk) {
+    constexpr int kRec = kLatTile * (kLatC / 4);
+    const int lane = threadIdx.x & 31, row = row0 + lane, from = min(row, cut.x - 1), last = cut.z;
+    const float2 *ml = p.rec_ml + from;
+    const float4 *o = reinterpret_cast<const float4 *>(p.rec_o) + static_cast<size_t>(chunk) * kLatTile + from;
+    float m = -INFINITY, l = 0.f, a[kChunks][4] = {};
+    CFA_ROLLED for (int k = run; k <= last; k += kMost) {
+        float2 s[kMost];
+        float4 v[kMost][kChunks];
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+            s[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) v[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k + i <= last) {
+                const int rec = 2 * (k + i) + (k + i == run);  // the first run's second record, the others' first
+                s[i] = __ldcg(ml + rec * kLatTile);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) v[i][c] = __ldcg(o + static_cast<size_t>(rec) * kRec + c * kLatTile);
+            }
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) top = fmaxf(top, s[i].x);
+        const float f = top == -INFINITY ? 0.f : top, g0 = exp2_ftz(m - f);
+        m = top;
+        l *= g0;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[c][e] *= g0;
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+            const float g = exp2_ftz(s[i].x - f);
+            l += g * s[i].y;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                a[c][0] += g * v[i][c].x; a[c][1] += g * v[i][c].y; a[c][2] += g * v[i][c].z; a[c][3] += g * v[i][c].w;
+            }
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t w[2 * kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        w[2 * c] = pack2_bf16_cvt(a[c][0] * inv, a[c][1] * inv);
+        w[2 * c + 1] = pack2_bf16_cvt(a[c][2] * inv, a[c][3] * inv);
+    }
+    uint16_t *out = p.out + (static_cast<size_t>(cut.y) + row) * kLatC + 4 * chunk;
+    if constexpr (kChunks >= 4) {
+        // two lanes write 32 bytes of a row together, then the other's: a lane's own 16, in 32 rows at once, take a
+        // transaction each
+        const bool odd = lane & 1;
+        uint16_t *even_out = out - (odd ? kLatC : 0) + (odd ? 8 : 0);
+#pragma unroll
+        for (int h = 0; h < kChunks / 4; ++h) {
+            uint32_t other[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) other[c] = __shfl_xor_sync(~0u, odd ? w[8 * h + c] : w[8 * h + 4 + c], 1);
+            if (row - (odd ? 1 : 0) < cut.x)
+                *reinterpret_cast<uint4 *>(even_out + 16 * h) =
+                    odd ? make_uint4(other[0], other[1], other[2], other[3]) : make_uint4(w[8 * h], w[8 * h + 1], w[8 * h + 2], w[8 * h + 3]);
+            if (row + (odd ? 0 : 1) < cut.x)
+                *reinterpret_cast<uint4 *>(even_out + kLatC + 16 * h) =
+                    odd ? make_uint4(w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7]) : make_uint4(other[0], other[1], other[2], other[3]);
+        }
+    } else if (row < cut.x) {
+        if constexpr (kChunks == 2) *reinterpret_cast<uint4 *>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+        else *reinterpret_cast<uint2 *>(out) = make_uint2(w[0], w[1]);
+    }
+    if (p.lse && row < cut.x && chunk == 0) p.lse[static_cast<size_t>(cut.y) + row] = (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// Merges the records of the tiles that runs' ends cut. What counts is that enough loads are on their way: a warp has
+// 16 of 16 bytes a lane, of as many dims as that is for the tile's pieces.
+__global__ void __launch_bounds__(kLatMergeThreads, 2) latent_merge_kernel(const __grid_constant__ LatentAttnParams p) {
+    constexpr int kWarps = kLatMergeThreads / 32;
     __shared__ int4 cuts[kLatMergeThreads];
     __shared__ int before[kLatMergeThreads + 1], sums[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();
     // every block lists the tasks: a run's tile, by rows and dims
+    auto chunks_of = [](int pieces) { return pieces <= 2 ? 8 : pieces <= 4 ? 4 : pieces <= 8 ? 2 : 1; };
     int4 cut = make_int4(0, 0, 0, 0);  // rows, the first one's place, the tile's last run
     if (tid < p.runs) cut = __ldcg(p.cuts + tid);
-    const int tasks = (cut.x + 31) / 32 * (cut.z == tid + 1 ? kLatC / 16 : kLatC / 4);
-    int scan = tasks;
+    int scan = (cut.x + 31) / 32 * (kLatC / 4 / chunks_of(cut.z - tid + 1));
     CFA_ROLLED for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(~0u, scan, o);
         if (lane >= o) scan += v;
@@ -688,82 +764,12 @@ __global__ void __launch_bounds__(kLatMergeThreads, 3) latent_merge_kernel(const
             else hi = mid;
         }
         cut = cuts[lo];
-        const int run = lo, last = cut.z, groups = (cut.x + 31) / 32, at = task - before[lo];
-        const bool two = last == run + 1;
-        const int row = at % groups * 32 + lane, chunk = at / groups * (two ? 4 : 1);
-        const bool live = row < cut.x;
-        const int from = min(row, cut.x - 1);
-        const float2 *ml = p.rec_ml + from;
-        const float4 *o = reinterpret_cast<const float4 *>(p.rec_o) + static_cast<size_t>(chunk) * kLatTile + from;
-        uint16_t *out = p.out + (static_cast<size_t>(cut.y) + row) * kLatC + 4 * chunk;
-        float m = -INFINITY, l = 0.f;
-        if (two) {
-            const int r0 = 2 * run + 1, r1 = 2 * run + 2;
-            const float2 s0 = __ldcg(ml + r0 * kLatTile), s1 = __ldcg(ml + r1 * kLatTile);
-            float4 v[2][4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                v[0][c] = __ldcg(o + static_cast<size_t>(r0) * kRec + c * kLatTile);
-                v[1][c] = __ldcg(o + static_cast<size_t>(r1) * kRec + c * kLatTile);
-            }
-            m = fmaxf(s0.x, s1.x);
-            const float f = m == -INFINITY ? 0.f : m, g0 = exp2_ftz(s0.x - f), g1 = exp2_ftz(s1.x - f);
-            l = g0 * s0.y + g1 * s1.y;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            uint32_t w[8];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                w[2 * c] = pack2_bf16_cvt((g0 * v[0][c].x + g1 * v[1][c].x) * inv, (g0 * v[0][c].y + g1 * v[1][c].y) * inv);
-                w[2 * c + 1] = pack2_bf16_cvt((g0 * v[0][c].z + g1 * v[1][c].z) * inv, (g0 * v[0][c].w + g1 * v[1][c].w) * inv);
-            }
-            // two lanes write a row's 32 bytes together, then the other's: a lane's own 16, in 32 rows at once, take a
-            // transaction each
-            const bool odd = lane & 1;
-            uint32_t other[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) other[c] = __shfl_xor_sync(~0u, odd ? w[c] : w[4 + c], 1);
-            uint16_t *even_out = out - (odd ? kLatC : 0) + (odd ? 8 : 0);
-            if (row - (odd ? 1 : 0) < cut.x)
-                *reinterpret_cast<uint4 *>(even_out) =
-                    odd ? make_uint4(other[0], other[1], other[2], other[3]) : make_uint4(w[0], w[1], w[2], w[3]);
-            if (row + (odd ? 0 : 1) < cut.x)
-                *reinterpret_cast<uint4 *>(even_out + kLatC) =
-                    odd ? make_uint4(w[4], w[5], w[6], w[7]) : make_uint4(other[0], other[1], other[2], other[3]);
-        } else {
-            constexpr int N = 8;
-            float a[4] = {};
-            CFA_ROLLED for (int k = run; k <= last; k += N) {
-                float2 s[N];
-                float4 v[N];
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    s[i] = make_float2(-INFINITY, 0.f);
-                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (k + i <= last) {
-                        const int rec = 2 * (k + i) + (k + i == run);  // the first run's second record, the others' first
-                        s[i] = __ldcg(ml + rec * kLatTile);
-                        v[i] = __ldcg(o + static_cast<size_t>(rec) * kRec);
-                    }
-                }
-                float top = m;
-#pragma unroll
-                for (int i = 0; i < N; ++i) top = fmaxf(top, s[i].x);
-                const float f = top == -INFINITY ? 0.f : top, g0 = exp2_ftz(m - f);
-                m = top;
-                l *= g0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) a[e] *= g0;
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float g = exp2_ftz(s[i].x - f);
-                    l += g * s[i].y;
-                    a[0] += g * v[i].x; a[1] += g * v[i].y; a[2] += g * v[i].z; a[3] += g * v[i].w;
-                }
-            }
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            if (live) *reinterpret_cast<uint2 *>(out) = make_uint2(pack2_bf16_cvt(a[0] * inv, a[1] * inv), pack2_bf16_cvt(a[2] * inv, a[3] * inv));
-        }
-        if (p.lse && live && chunk == 0) p.lse[static_cast<size_t>(cut.y) + row] = (m + log2f(l)) * 0.69314718055994531f;
+        const int groups = (cut.x + 31) / 32, at = task - before[lo], row = at % groups * 32;
+        const int chunks = chunks_of(cut.z - lo + 1), chunk = at / groups * chunks;
+        if (chunks == 8) latent_merge_rows<8, 2>(p, cut, lo, row, chunk);
+        else if (chunks == 4) latent_merge_rows<4, 4>(p, cut, lo, row, chunk);
+        else if (chunks == 2) latent_merge_rows<2, 8>(p, cut, lo, row, chunk);
+        else latent_merge_rows<1, 16>(p, cut, lo, row, chunk);
     }
     grid_dependents_launch();
 }
