@@ -604,41 +604,41 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             } else {
                 if (p.lse && half == 0 && live) p.lse[out_row] = (m + log2f(l)) * 0.69314718055994531f;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                // through the warp's rows of P (32 of 128 bytes), so that a row's 128 bytes are written
-                // together: a thread's own 16 bytes, in 32 rows at once, take a transaction each
-                uint8_t *stage = smem + S::kP + half * kLatChunk + row_group * 128;
+                // two lanes write 32 bytes of a row together, then the other's: a lane's own 16, in 32 rows at once, take a
+                // transaction each
+                const int odd = lane & 1;
+                uint16_t *out = p.out + (out_row - odd) * kLatC + 256 * half + 8 * odd;
+                const bool even_live = row - odd < here, odd_live = row - odd + 1 < here;
 #pragma unroll 1
-                for (int c = 0; c < 256; c += 64) {
-                    uint32_t v[64];
+                for (int c = 0; c < 256; c += 32) {
+                    uint32_t v[32];
                     __syncwarp();
                     if (any) {
                         tmem_ld_x32(tmem + lanes + 128 + c, v);
-                        tmem_ld_x32(tmem + lanes + 128 + c + 32, v + 32);
                         tmem_wait_ld();
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) v[e] = 0u;
+                        for (int e = 0; e < 32; ++e) v[e] = 0u;
                     }
+                    uint32_t w[16], y[8];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        w[e] = pack2_bf16_cvt(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            w[k] = pack2_bf16_cvt(__uint_as_float(v[8 * e + 2 * k]) * inv, __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
-                        *reinterpret_cast<uint4 *>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        const int at = 8 * (e >> 2) + (e & 3);  // 32 bytes are two lanes' 16
+                        y[e] = __shfl_xor_sync(~0u, odd ? w[at] : w[at + 4], 1);
                     }
-                    __syncwarp();
-                    uint4 y[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int r = 4 * e + (lane >> 3);
-                        y[e] = *reinterpret_cast<const uint4 *>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-                    }
-                    uint16_t *out = p.out + (out_row - lane) * kLatC + 256 * half + c + 8 * (lane & 7);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int r = 4 * e + (lane >> 3);
-                        if (row_group + r < here) *reinterpret_cast<uint4 *>(out + r * kLatC) = y[e];
+                    for (int h = 0; h < 2; ++h) {
+                        if (even_live)
+                            *reinterpret_cast<uint4 *>(out + c + 16 * h) =
+                                odd ? make_uint4(y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3])
+                                    : make_uint4(w[8 * h], w[8 * h + 1], w[8 * h + 2], w[8 * h + 3]);
+                        if (odd_live)
+                            *reinterpret_cast<uint4 *>(out + kLatC + c + 16 * h) =
+                                odd ? make_uint4(w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7])
+                                    : make_uint4(y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3]);
                     }
                 }
             }
