@@ -52,7 +52,7 @@ struct LatentHeadsParams {
 };
 
 constexpr int kHeadsTokens = 16;       // of a block, where there are few
-constexpr int kHeadsMmaThreads = 192;  // four warps for the results, a load warp, one that issues the products
+constexpr int kHeadsMmaThreads = 320;  // two warpgroups for the results, a load warp, one that issues the products
 
 // ------------------------------------------------------- attention over rows
 

@@ -4,10 +4,11 @@
 // unfolding, the 128 value dims (32 of 128 x 128 x 16). Blocks, one to an SM, take runs of jobs in the
 // order of heads and tokens, so that a head's weights are loaded once or twice (64 KB, two buffers; 128 KB, one) and
 // stay in shared memory while the tokens' rows stream through: memory bounds it, with the weights no part of it. A load
-// warp, one that issues the products, and four that bring results from one of two accumulators in TMEM
-// through shared memory to whole boxes of 64 columns (TMA stores, which end at the last token by themselves).
+// warp, one that issues the products, and two warpgroups that bring results from one of two accumulators in TMEM
+// through shared memory to whole boxes of 64 columns, by turns (TMA stores, which end at the last token by
+// themselves; one warpgroup instead took 3% more).
 //
-// Measured (one GB300): 777 tokens of 32 heads in 11.7 us (42 MB, floor 6.2; on mma.sync 15.8 to 18.3), 1000 tokens
+// Measured (one GB300): 777 tokens of 32 heads in 11.4 us (42 MB, floor 6.2; on mma.sync 15.8 to 18.3), 1000 tokens
 // of 128 heads in 46 us (213 MB, floor 31); 1000 of 128 heads out 34.6 us (181 MB, floor 26.6; on mma.sync
 // 46 to 54). The weights read again for every 64 or 128 tokens, out of L2, held the others back.
 #pragma once
@@ -27,10 +28,11 @@ struct HeadsMma {
     static constexpr int kCols = FOLD ? 256 : kLatV;                   // of a job's result
     static constexpr int kSplit = FOLD ? kLatC / kCols : 1;            // jobs of a head's 128 tokens
     static constexpr int kWeights = kChunks * kCols * 128;             // bytes
-    static constexpr int kWSlots = FOLD ? 2 : 1, kXSlots = 4, kOutSlots = 2;
+    static constexpr int kWSlots = FOLD ? 2 : 1, kXSlots = FOLD ? 2 : 4;
+    static constexpr int kOutSlots = FOLD ? 2 : 1;                     // of either warpgroup
     static constexpr int kBox = 128 * 128;                             // 128 tokens of 64 dims
     static constexpr int kW = 0, kX = kW + kWSlots * kWeights, kOut = kX + kXSlots * kBox;
-    static constexpr int kBars = kOut + kOutSlots * kBox;
+    static constexpr int kBars = kOut + 2 * kOutSlots * kBox;
     static constexpr int kFullW = kBars, kEmptyW = kFullW + 8 * kWSlots, kFullX = kEmptyW + 8 * kWSlots,
                          kEmptyX = kFullX + 8 * kXSlots, kFullAcc = kEmptyX + 8 * kXSlots, kEmptyAcc = kFullAcc + 16,
                          kDrain = kEmptyAcc + 16, kBarsEnd = kDrain + 8;
@@ -63,7 +65,7 @@ latent_heads_mma_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_c
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 1);
     if (tid < (S::kBarsEnd - S::kBars) / 8) {
         const int at = S::kBars + 8 * tid;
-        mbar_init(base + at, at >= S::kEmptyAcc && at < S::kDrain ? 4 : 1);  // the warps that read an accumulator
+        mbar_init(base + at, at >= S::kEmptyAcc && at < S::kDrain ? 8 : 1);  // the warps that read an accumulator
         fence_mbar_init();
     }
     if (tid == 0) misc[0] = 0;
@@ -188,19 +190,22 @@ latent_heads_mma_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_c
         __syncwarp();
     } else {
         // ---------------------------------------------------------------------- results
-        const uint32_t lanes = static_cast<uint32_t>(warp) << 21;  // TMEM lanes of this warp
+        const int group = warp >= 4, row = 32 * (warp & 3) + lane;  // of the two warpgroups; token of the tile
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lanes of this warp
+        auto meet = [&]() { asm volatile("bar.sync %0, 128;" :: "r"(1 + group) : "memory"); };
+        const int out0 = S::kOut + group * S::kOutSlots * S::kBox, thread = 128 * group + row;
         uint32_t n_out = 0;
         int w = w0, t = t0;
         CFA_ROLLED for (int j = 0; j < n_jobs; ++j) {
             const uint32_t acc = j & 1;
             const int h = w / S::kSplit, part = w % S::kSplit;
-            uint4 rot[8];  // the rotated dims pass through
+            uint4 rot[4];  // the rotated dims pass through
             const bool copies = FOLD && part == 0;
-            const uint16_t *src = p.x + h * kLatQ + kLatN + 8 * (tid & 7);
+            const uint16_t *src = p.x + h * kLatQ + kLatN + 8 * (thread & 7);
             if (copies) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int tok = 128 * t + 16 * i + (tid >> 3);
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = 128 * t + 32 * i + (thread >> 3);
                     if (tok < p.T) rot[i] = *reinterpret_cast<const uint4 *>(src + tok * p.x_stride);
                 }
             }
@@ -208,45 +213,45 @@ latent_heads_mma_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_c
             __syncwarp();
             tcgen05_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < S::kCols; c += 64, ++n_out) {
+            for (int c = 64 * group; c < S::kCols; c += 128, ++n_out) {
                 uint32_t v[64];
                 tmem_ld_x32(tmem + lanes + 256 * acc + c, v);
                 tmem_ld_x32(tmem + lanes + 256 * acc + c + 32, v + 32);
                 tmem_wait_ld();
-                if (c + 64 == S::kCols) {  // the accumulator is read
+                if (c + 128 >= S::kCols) {  // the accumulator is read
                     tcgen05_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(base + S::kEmptyAcc + 8 * acc);
                 }
-                if (tid == 0) bulk_wait_read<S::kOutSlots - 1>();  // the slot's last store has read it
-                compute_bar<128>();
-                const int slot = S::kOut + (n_out % S::kOutSlots) * S::kBox;
+                if (row == 0) bulk_wait_read<S::kOutSlots - 1>();  // the slot's last store has read it
+                meet();
+                const int slot = out0 + (n_out % S::kOutSlots) * S::kBox;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     uint32_t o[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         o[k] = pack2_bf16_cvt(__uint_as_float(v[8 * e + 2 * k]), __uint_as_float(v[8 * e + 2 * k + 1]));
-                    *reinterpret_cast<uint4 *>(smem + slot + tid * 128 + ((e ^ (tid & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(smem + slot + row * 128 + ((e ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 fence_proxy_async_smem();
-                compute_bar<128>();
-                if (tid == 0) {
+                meet();
+                if (row == 0) {
                     tma_store_2d(&tm_y, FOLD ? h * kLatRow + S::kCols * part + c : h * kLatV + c, 128 * t, base + slot);
                     bulk_commit();
                 }
             }
             if (copies) {
-                uint16_t *dst = p.y + h * kLatRow + kLatC + 8 * (tid & 7);
+                uint16_t *dst = p.y + h * kLatRow + kLatC + 8 * (thread & 7);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int tok = 128 * t + 16 * i + (tid >> 3);
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = 128 * t + 32 * i + (thread >> 3);
                     if (tok < p.T) *reinterpret_cast<uint4 *>(dst + static_cast<size_t>(tok) * p.H * kLatRow) = rot[i];
                 }
             }
             if (++t == tiles) t = 0, ++w;
         }
-        if (tid == 0) bulk_wait_all();
+        if (row == 0) bulk_wait_all();
     }
     tcgen05_fence_before();
     __syncthreads();
