@@ -739,6 +739,7 @@ __global__ void __launch_bounds__(kLatMergeThreads, 2) latent_merge_kernel(const
     __shared__ int before[kLatMergeThreads + 1], sums[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();
+    grid_dependents_launch();
     // every block lists the tasks: a run's tile, by rows and dims
     auto chunks_of = [](int pieces) { return pieces <= 2 ? 8 : pieces <= 4 ? 4 : pieces <= 8 ? 2 : 1; };
     int4 cut = make_int4(0, 0, 0, 0);  // rows, the first one's place, the tile's last run
@@ -771,7 +772,6 @@ __global__ void __launch_bounds__(kLatMergeThreads, 2) latent_merge_kernel(const
         else if (chunks == 2) latent_merge_rows<2, 8>(p, cut, lo, row, chunk);
         else latent_merge_rows<1, 16>(p, cut, lo, row, chunk);
     }
-    grid_dependents_launch();
 }
 
 }  // namespace cfa
