@@ -69,7 +69,7 @@ struct ExpSmem {
     static constexpr int kFullK = kBars, kEmptyK = kFullK + 8 * kExpSlots, kReadyK = kEmptyK + 8 * kExpSlots;
     static constexpr int kFullV = kReadyK + 8 * kExpSlots, kEmptyV = kFullV + 8 * kExpSlots, kReadyV = kEmptyV + 8 * kExpSlots;
     static constexpr int kFullQ = kReadyV + 8 * kExpSlots, kEmptyQ = kFullQ + 16, kReadyQ = kEmptyQ + 16;  // a tile each
-    static constexpr int kScores = kReadyQ + 16, kWeights = kScores + 16, kDrain = kWeights + 16;
+    static constexpr int kScores = kReadyQ + 16, kEnded = kScores + 16, kWeights = kEnded + 16, kDrain = kWeights + 16;
     static constexpr int kBarsEnd = kDrain + 8;
     static constexpr int kMisc = kBarsEnd;                    // flags, TMEM address
     static constexpr int kSums = kMisc + 16;                  // int [12]: the scan's sums
@@ -248,8 +248,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         uint32_t count = 1;
         if ((at >= S::kReadyK && at < S::kFullV) || (at >= S::kReadyV && at < S::kFullQ) || (at >= S::kReadyQ && at < S::kScores))
             count = 2;  // the relays of both blocks
-        if (at >= S::kEmptyQ && at < S::kReadyQ) count = 4;   // a tile's warps
-        if (at >= S::kWeights && at < S::kDrain) count = 8;   // and those of both blocks
+        if (at >= S::kWeights && at < S::kDrain) count = 8;   // a tile's warps of both blocks
         mbar_init(base + at, count);
         fence_mbar_init();
     }
@@ -445,8 +444,8 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             bool have = next(r, x);
             for (; ok && have; x = ahead) {
                 const int na = x.a.end - x.a.b0, nb = x.b.end - x.b.b0, blocks = max(na, nb);
-                // By one thread: the scores of tile t's block j.
-                auto scores = [&](int t, uint32_t k) {
+                // By one thread: the scores of tile t from loaded block k.
+                auto scores = [&](int t, uint32_t k, bool last) {
                     const uint32_t slot = k % kExpSlots;
                     const uint64_t a = q0 + 3 * t * (kExpChunk >> 4), bd = k0 + slot * (kExpKSlot >> 4);
 #pragma unroll
@@ -455,6 +454,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                                    bd + (ks >> 2) * (64 * 128 >> 4) + 2 * (ks & 3), idesc_s, ks > 0);
                     if (t == 1 || !x.shared) umma2_commit(base + S::kEmptyK + 8 * slot);
                     umma2_commit(base + S::kScores + 8 * t);
+                    if (last) umma2_commit(base + S::kEmptyQ + 8 * t);
                 };
                 // Keys or values of tile t's block j have landed (with shared ones the first tile waits for both).
                 auto landed = [&](int ready, int t, int j, uint32_t k) {
@@ -468,7 +468,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     ok = ok && wait_warp(S::kReadyQ + 8 * t, queries >> t & 1, kSiteQExchange);
                     queries ^= 1u << t;
                     tcgen05_fence_after();
-                    if (ok && elect_one()) scores(t, k);
+                    if (ok && elect_one()) scores(t, k, (t ? nb : na) == 1);
                     __syncwarp();
                 }
                 have = next(r, ahead);  // (beside the first softmax)
@@ -490,9 +490,8 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                                 umma2_bf16_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * ks, v0 + slot * (kExpVSlot >> 4) + 128 * ks,
                                               idesc_o, j > 0 || ks > 0);
                             if (t == 1 || !x.shared) umma2_commit(base + S::kEmptyV + 8 * slot);
-                            // behind the last product there are no more scores, but the tile's warps learn that it ended
-                            if (more) scores(t, k);
-                            else umma2_commit(base + S::kScores + 8 * t);
+                            if (more) scores(t, k, j + 2 == end);
+                            else umma2_commit(base + S::kEnded + 8 * t);
                         }
                         __syncwarp();
                     }
@@ -515,6 +514,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lanes of this warp
         const uint32_t t_s = tmem + lanes + 128 * t, t_o = tmem + lanes + 256 + 128 * t;
         const int scores = S::kScores + 8 * t;
+        uint32_t ended = 0;  // phase
         const uint32_t weights = map_to_rank(base + S::kWeights, 0) + 8 * t;
         uint32_t scored = 0, nv = 0;  // phases; both tiles' blocks before the item's
         int r = 0;
@@ -637,10 +637,7 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             nv += x.loaded();
             const bool any = z.end > z.b0;
             have = next(r, ahead);  // (its loads are on their way meanwhile)
-            if (any) {
-                wait(scores, scored & 1, kSiteKvExchange);
-                ++scored;
-            }
+            if (any) wait(S::kEnded + 8 * t, ended++ & 1, kSiteKvExchange);
             __syncwarp();
             tcgen05_fence_after();
             // ---- the tile's results, or its record
@@ -665,49 +662,48 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 } else {
                     if (p.lse && live) p.lse[tok * p.H + z.h] = (m + log2f(l)) * 0.69314718055994531f;
                     const float inv = l == 0.f ? 0.f : 1.f / l;
-                    // through the tile's first chunk of queries, which nobody reads any more, so that a row's 128 bytes
-                    // are written together
-                    uint8_t *stage = smem + S::kQ + 3 * t * kExpChunk + (row - lane) * 128;
+                    // two lanes write 32 bytes of a row together, then the other's: a lane's own 16, in 32 rows at once, take a
+                    // transaction each
+                    const int odd = lane & 1;
+                    const size_t next_row = static_cast<size_t>(p.H) * kLatV;
+                    uint16_t *out = p.out + ((tok - odd) * p.H + z.h) * kLatV + 8 * odd;
+                    const bool even_live = row - odd < rows, odd_live = row - odd + 1 < rows;
 #pragma unroll 1
-                    for (int c = 0; c < kLatV; c += 64) {
+                    for (int c = 0; c < kLatV; c += 32) {
+                        uint32_t v[32];
                         __syncwarp();
-                        uint4 y[8];
                         if (any) {
-                            uint32_t v[64];
                             tmem_ld_x32(t_o + c, v);
-                            tmem_ld_x32(t_o + c + 32, v + 32);
                             tmem_wait_ld();
+                        } else {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    w[k] = pack2_bf16_cvt(__uint_as_float(v[8 * e + 2 * k]) * inv, __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
-                                *reinterpret_cast<uint4 *>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                            __syncwarp();
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const int k = 4 * e + (lane >> 3);
-                                y[e] = *reinterpret_cast<const uint4 *>(stage + k * 128 + (((lane & 7) ^ (k & 7)) << 4));
-                            }
-                        } else {  // (without keys the tile has no queries: the next item's may be landing there)
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) y[e] = make_uint4(0u, 0u, 0u, 0u);
+                            for (int e = 0; e < 32; ++e) v[e] = 0u;
                         }
-                        uint16_t *out = p.out + ((tok - lane) * p.H + z.h) * kLatV + c + 8 * (lane & 7);
+                        uint32_t w[16], y[8];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            w[e] = pack2_bf16_cvt(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const int k = 4 * e + (lane >> 3);
-                            if (row - lane + k < rows) *reinterpret_cast<uint4 *>(out + static_cast<size_t>(k) * p.H * kLatV) = y[e];
+                            const int at = 8 * (e >> 2) + (e & 3);  // 32 bytes are two lanes' 16
+                            y[e] = __shfl_xor_sync(~0u, odd ? w[at] : w[at + 4], 1);
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (even_live)
+                                *reinterpret_cast<uint4 *>(out + c + 16 * h) =
+                                    odd ? make_uint4(y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3])
+                                        : make_uint4(w[8 * h], w[8 * h + 1], w[8 * h + 2], w[8 * h + 3]);
+                            if (odd_live)
+                                *reinterpret_cast<uint4 *>(out + next_row + c + 16 * h) =
+                                    odd ? make_uint4(w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7])
+                                        : make_uint4(y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3]);
                         }
                     }
-                    fence_proxy_async_smem();  // (the next queries come by the asynchronous proxy)
                 }
             }
             tcgen05_fence_before();
             __syncwarp();
-            if (any && lane == 0) mbar_arrive(base + S::kEmptyQ + 8 * t);
         }
     }
     tcgen05_fence_before();
