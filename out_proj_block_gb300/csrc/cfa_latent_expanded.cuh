@@ -22,13 +22,13 @@
 // not fill the last round is split along the keys; its parts leave records, which a second kernel merges in order, so
 // results are bitwise reproducible.
 //
-// Measured, with the merge (one GB300): 1024 tokens behind 2500 keys, 128 heads: 194 us (1.30 PFLOP/s); five
-// prompts of up to 1500 tokens, 32 heads: 95 us (0.79). A block of keys takes some 3100 clocks of 512 rows, of which
-// products are 2560: the softmax of a tile, 1250, and the two hand-overs, 400, take longer than the other's products. A
-// task's begin and end take some 9000. Values are looked over for what is not finite by the warps of the
-// softmax: the warp that relays took 4300 clocks for a block, at the end of every tile two of them. Tiles that go through
-// the tasks each by itself, so that one's last blocks run beside the other's next task, took more in the middle (3200 to
-// 3500 clocks a block) than they saved.
+// Measured, with the merge (one GB300): 1024 tokens behind 2500 keys, 128 heads: 192 us (1.32 PFLOP/s); five
+// prompts of up to 1500 tokens, 32 heads: 92 us (0.82). A block of keys takes 2820 clocks of 512 rows, of which
+// products are 2560: the softmax of a tile, 1070, and the two hand-overs, 400, take as long as the other's products. A
+// task's begin, end and masked blocks take some 7000 beside that. Values are looked over for what is not finite by the
+// warps of the softmax: the warp that relays took 4300 clocks for a block, at the end of every tile two of them. Tiles
+// that go through the tasks each by itself, so that one's last blocks run beside the other's next task, took more in the
+// middle (3200 to 3500 clocks a block) than they saved.
 //
 // Weights are rounded to bf16 for their product with the values (2^-8 each, the size of the result's own
 // rounding); their sum, the maxima, the outputs and the records are fp32.
@@ -53,8 +53,8 @@ constexpr int kExpSlots = 3;           // blocks of keys and of values in flight
 constexpr int kExpKSlot = 3 * 64 * 128, kExpVSlot = 128 * 128;
 // Keys from which on two tiles in a row of a head make a task, and blocks of keys are loaded once for both. Below, two
 // heads' tiles do, which end together: of two in a row the first sees two blocks fewer. Two in a row always and never, in
-// us: 1024 tokens behind 2500, 128 heads 184 and 191; a prompt of 8192, 16 heads 215 and 217; five of 763 to
-// 1500, 32 heads 105 and 96; 300 tokens 16 times 83 and 72.
+// us (before other steps): 1024 tokens behind 2500, 128 heads 184 and 191; a prompt of 8192, 16 heads 215 and 217; five
+// of 763 to 1500, 32 heads 105 and 96; 300 tokens 16 times 83 and 72.
 constexpr int kExpShared = 2560;
 constexpr int kExpPeek = 3;            // blocks before an item's end that the next one's queries are asked for in L2
 constexpr int kExpTile = 256;          // tokens of a tile, half of them to either block
