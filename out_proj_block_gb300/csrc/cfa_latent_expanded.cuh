@@ -82,7 +82,7 @@ static_assert(ExpSmem::kBytes <= 227 * 1024, "it fits");
 constexpr int kExpMaxEntries = kPagedMaxTokens / kExpTile + kPagedMaxSeqs;
 constexpr int kExpNameBits = 20, kExpReqBits = 10;
 static_assert(kPagedMaxSeqs <= 1 << kExpReqBits && 2 * kPagedMaxTokens / kExpTile <= 1 << (kExpNameBits - kExpReqBits) &&
-              kExpMaxEntries <= 1 << (31 - kExpNameBits), "they fit their bits");
+              kExpMaxEntries <= 1 << (31 - kExpNameBits) && kExpMaxEntries <= 1 << 11, "they fit their bits");
 static_assert(8 * kExpMaxEntries <= ExpSmem::kK, "the list is made where the queries go");
 
 // Tasks and how they are dealt out to `grid` clusters, from what a scan over the requests finds.
@@ -170,20 +170,24 @@ __device__ __forceinline__ int latent_expanded_list(const LatentExpandedParams &
     if (refused) return -1;
     CFA_ROLLED for (int b = first; b < last; ++b)
         latent_expanded_entries(b, __ldcg(p.cu + b + 1) - __ldcg(p.cu + b), __ldcg(p.cu_k + b + 1) - __ldcg(p.cu_k + b),
-                                [&](int name, int keys) { work[at++] = make_int2(keys, name); });
+                                [&](int name, int keys) {
+                                    // (a key that no other entry has: blocks, then the order of requests)
+                                    work[at] = make_int2(min((keys + 127) / 128, (1 << 20) - 1) << 11 | (kExpMaxEntries - 1 - at), name);
+                                    ++at;
+                                });
     __syncthreads();
     int twos = 0;
     CFA_ROLLED for (int i = tid; i < all; i += kThreads) {
         const int2 x = work[i];
-        int rank = 0, before = 0;
+        int ahead = 0;
         twos = 0;
-        CFA_ROLLED for (int j = 0; j < all; ++j) {
+#pragma unroll 8
+        for (int j = 0; j < all; ++j) {
             const int2 y = work[j];
-            const int ahead = y.x > x.x || (y.x == x.x && j < i);
-            rank += ahead;
-            before += ahead & y.y;
             twos += y.y & 1;
+            ahead += y.x > x.x ? (y.y & 1) << 16 | 1 : 0;  // entries, and from bit 16 on those of two tiles
         }
+        const int rank = ahead & 0xffff, before = ahead >> 16;
         list[rank] = before << kExpNameBits | x.y;
     }
     if (tid == 0) sums[0] = twos;  // (the first thread has an entry if anyone has)
