@@ -29,9 +29,9 @@
 // are bitwise reproducible. A row's maximum is followed lazily, a published method: O is rescaled
 // only when it grew by more than 8 (a factor 2^8, far inside fp32).
 //
-// Measured, with the merge (one GB300): 64 requests of some 8K rows, 128 heads 85 us (385 MB read once;
-// floor 57); 200 of some 2K, 32 heads 71 us (floor 47); 16 with up to four drafted tokens, 20 heads 25 us; one of 4K
-// rows 16 us. In the middle of a run memory bounds it, at 6.2 TB/s (products take 2490 clocks of a block of keys,
+// Measured, with the merge (one GB300): 64 requests of some 8K rows, 128 heads 86 us (385 MB read once;
+// floor 57); 200 of some 2K, 32 heads 72 us (floor 47); 16 with up to four drafted tokens, 20 heads 24 us; one of 4K
+// rows 15.5 us. In the middle of a run memory bounds it, at 6.2 TB/s (products take 2490 clocks of a block of keys,
 // the rows 2900); beside that stand the start (scan, first queries and keys: 8 us), the cut tiles' records (1 to 6 us,
 // and 5 to 10 to merge them, 2 of which the launch takes) and, with short requests, a tile's end, some 8000 clocks.
 // Merging in the block that ends last instead of in a second kernel took 16 us more for the first of these; merging by
