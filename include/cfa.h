@@ -777,8 +777,8 @@ cfa_status cfa_latent_attention(cfa_latent *latent, int n_tokens, int n_seqs, co
  * L - n + i + 1 keys.
  *   out bf16 [n_tokens, n_heads, 128], lse fp32 [n_tokens, n_heads] or NULL, as cfa_latent_attention
  *   computes them from k = [key | k_rope] and value, scale and unseen keys as there. Values that are not
- *   finite stay in their dim; where only some tokens of a request see one, a slow pass behind the
- *   call adds it to those.
+ *   finite stay in their dim; where only some tokens of a request see one, a pass over the keys of the
+ *   tokens beside them, behind the attention, adds it to those.
  * q_stride a multiple of 8, kv_stride and k_rope_stride too. A token that sees no key gets 0 and lse
  * -inf; tokens outside the requests stay as they were. Flagged (CFA_ERR_INVALID_ARG from
  * cfa_latent_status, nothing written): cu or cu_k that are not ascending within [0, n_tokens]

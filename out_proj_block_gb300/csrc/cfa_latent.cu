@@ -41,7 +41,7 @@ struct cfa_latent {
     float magnitude = 1.0f;
     unsigned long long turns[cfa::kLatR / 2] = {};
     // workspace
-    unsigned *words = nullptr;  // [0] status, [1..3] the expanded form's merge (odd, rest)
+    unsigned *words = nullptr;  // kLatWords: [0] status, [1..] the expanded form's merge (odd, rest, odd_tiles)
     float *rec_o = nullptr;     // records of the attention's pieces
     float2 *rec_ml = nullptr;
     int4 *cuts = nullptr;
@@ -338,7 +338,7 @@ cfa_latent *cfa_latent_create(int max_seqs, int max_tokens, int n_heads, int pag
     p->runs = std::min(sms / 2, cfa::kLatMaxRuns);
     const size_t rec_rows = 2u * static_cast<size_t>(p->runs) * cfa::kLatTile;
     if (!allow_smem() ||
-        cudaMalloc(&p->words, 4 * sizeof(unsigned)) != cudaSuccess || !clear_words(p->words, 4) ||
+        cudaMalloc(&p->words, cfa::kLatWords * sizeof(unsigned)) != cudaSuccess || !clear_words(p->words, cfa::kLatWords) ||
         cudaMalloc(&p->rec_o, sizeof(float) * rec_rows * kLatC) != cudaSuccess ||
         // (twice the rows: the expanded form's records are 512 rows of 128 dims, one a cluster)
         cudaMalloc(&p->rec_ml, 2 * sizeof(float2) * rec_rows) != cudaSuccess ||
@@ -467,6 +467,7 @@ cfa_status cfa_latent_expanded(cfa_latent *p, int n_tokens, int n_keys, int n_se
     kp.lse = lse;
     kp.status = p->words;
     kp.odd = p->words + 1;
+    kp.odd_tiles = reinterpret_cast<unsigned char *>(p->words + 4);
     kp.rec_o = p->rec_o;
     kp.rec_ml = p->rec_ml;
     kp.T = n_tokens;
@@ -552,7 +553,7 @@ cfa_status cfa_latent_describe(const cfa_latent *p, char *buf, int len) {
                   "\"interleaved\": %d, \"scaling\": %d, \"num_sms\": %d, \"runs\": %d, \"smem_bytes\": %d, "
                   "\"workspace_bytes\": %lld}",
                   p->max_seqs, p->max_tokens, p->nh, p->ps, p->rope, p->interleaved, p->scaling, p->num_sms, p->runs,
-                  cfa::latent_attention_smem(), 2ll * p->runs * cfa::kLatTile * (4 * kLatC + 16) + 32ll * p->runs);
+                  cfa::latent_attention_smem(), 2ll * p->runs * cfa::kLatTile * (4 * kLatC + 16) + 32ll * p->runs + cfa::kExpMarks);
     return CFA_OK;
 }
 

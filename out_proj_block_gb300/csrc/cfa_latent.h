@@ -5,6 +5,7 @@
 
 #include <cuda_runtime.h>
 
+#include "cfa_paged.h"
 #include "cfa_paged_split.h"
 
 namespace cfa {
@@ -93,6 +94,7 @@ struct LatentExpandedParams {
     float *lse;              // [T][H] or null
     unsigned *status;
     unsigned *odd;           // {a value that is not finite was cleared, arrivals of the merge's blocks}; 0 between calls
+    unsigned char *odd_tiles;  // [kExpMarks] for every 256 tokens: it was in a tile that begins among them; 0 between calls
     float *rec_o;            // records of parts: unnormalised outputs in 16-byte chunks [32][512 rows][4]
     float2 *rec_ml;          // and each row's maximum (base 2) and sum
     int *rest;               // for the merge: how many tasks are split,
@@ -108,5 +110,8 @@ constexpr int kExpLoadWarp = 8, kExpMmaWarp = 10, kExpRelayWarp = 11;
 constexpr int kExpThreads = 384;
 constexpr int kExpMaxParts = 8;  // of a task of the last round
 constexpr int kExpLeast = 3;     // least blocks of a part
+constexpr int kExpTile = 256;    // tokens of a tile, half of them to either block of a cluster
+constexpr int kExpMarks = kPagedMaxTokens / kExpTile;
+constexpr int kLatWords = 4 + kExpMarks / 4;  // of a plan: status; odd, its arrivals, rest; odd_tiles
 
 }  // namespace cfa
