@@ -757,8 +757,9 @@ cfa_status cfa_latent_unfold(cfa_latent *latent, int n_tokens, const void *o_lat
  * they were. scale 0 means 1/sqrt(192); scale times log2 e must be finite in 32 bits. Rows
  * that a token does not see do not change it, whatever they hold. A score that is NaN or +inf makes
  * its token's head NaN; whether a row with such values and score -inf (weight 0) does is not defined. Flagged in the status word
- * as CFA_ERR_INVALID_ARG: offsets cu that are not ascending within [0, n_tokens], or more than
- * 2^29 blocks of 128 rows over all tiles of 128 token heads (nothing is written then); a length outside
+ * as CFA_ERR_INVALID_ARG: offsets cu that are not ascending within [0, n_tokens], or 2^30 - 1 units or
+ * more, a tile of 128 of a request's token heads having two and one for each block of 128 rows that its
+ * last token sees (nothing is written then); a length outside
  * [0, table_width * page_size] (taken as 0); a page id outside [0, n_pages) where a row is read
  * (it counts as zeros). o_lat and lse must not overlap an input or each other.
  */

@@ -145,14 +145,13 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     {
         int *sums = reinterpret_cast<int *>(smem + S::kSums);
         const int per = (p.B + kLatAttnThreads - 1) / kLatAttnThreads, first = tid * per, last = min(p.B, first + per);
-        auto more = [](int a, int b) { return min(a + b, kLatMaxUnits); };
         int units = 0;
         bool bad = false;
         LatentRequest r{};  // (with no more requests than threads read once)
         CFA_ROLLED for (int b = first; b < last; ++b) {
             r = request(b);
             if (r.tok0 < 0 || r.n < 0 || r.n > p.T || r.tok0 > p.T - r.n) bad = true;
-            else units = more(units, latent_units(r, p.H, p.by_H));
+            else units = latent_more(units, latent_units(r, p.H, p.by_H));
             if (blockIdx.x == 0) {
                 const int len = __ldcg(p.lens + b);
                 if (len < 0 || len > static_cast<long long>(p.width) * p.page_size) atomicOr(p.status, kStatusBadLengthBit);
@@ -161,7 +160,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         int scan = units;
         CFA_ROLLED for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(~0u, scan, o);
-            if (lane >= o) scan = more(scan, v);
+            if (lane >= o) scan = latent_more(scan, v);
         }
         if (lane == 31) sums[warp] = scan;
         if (tid == 0) misc[2] = -1;
@@ -169,17 +168,17 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         int before = 0, all = 0;
 #pragma unroll
         for (int w = 0; w < kLatWarps; ++w) {
-            if (w < warp) before = more(before, sums[w]);
-            all = more(all, sums[w]);
+            if (w < warp) before = latent_more(before, sums[w]);
+            all = latent_more(all, sums[w]);
         }
-        const bool valid = !refused && all < kLatMaxUnits;
+        const bool valid = !refused && latent_fits(all);
         if (blockIdx.x == 0 && tid == 0 && !valid) atomicOr(p.status, kStatusBadLengthBit);
         const int share = max(kLatShare, (all + p.runs - 1) / p.runs);
         const long long from = static_cast<long long>(run) * share;
         const int u0 = valid ? static_cast<int>(min(from, static_cast<long long>(all))) : 0;
         const int u1 = valid ? static_cast<int>(min(from + share, static_cast<long long>(all))) : 0;
         // the thread in whose requests the run begins
-        int at = more(before, scan - units);
+        int at = latent_more(before, scan - units);
         if (u0 < u1 && u0 >= at && u0 < at + units) {
             int b = first;
             CFA_ROLLED for (; per > 1 && b < last; ++b) {

@@ -65,6 +65,10 @@ CFA_HD int latent_units(const LatentRequest &r, int H, const FastDiv &by_H) {
     return units > kLatMaxUnits ? kLatMaxUnits : static_cast<int>(units);
 }
 
+// Units of several requests together, and whether a call may have that many.
+CFA_HD int latent_more(int a, int b) { return paged_min(a + b, kLatMaxUnits); }
+CFA_HD bool latent_fits(int units) { return units < kLatMaxUnits; }
+
 // A part of one tile.
 struct LatentPiece {
     LatentRequest r;
