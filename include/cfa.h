@@ -756,7 +756,8 @@ cfa_status cfa_latent_unfold(cfa_latent *latent, int n_tokens, const void *o_lat
  * A token that sees no row gets 0 and lse -inf. Tokens outside [cu[0], cu[n_seqs]) stay as
  * they were. scale 0 means 1/sqrt(192); scale times log2 e must be finite in 32 bits. Rows
  * that a token does not see do not change it, whatever they hold. A score that is NaN or +inf makes
- * its token's head NaN; whether a row with such values and score -inf (weight 0) does is not defined. Flagged in the status word
+ * its token's head NaN; whether a row with such values and score -inf (weight 0) does is not defined. Where all
+ * scores are -inf the result is that of a token that sees no row, or NaN. Flagged in the status word
  * as CFA_ERR_INVALID_ARG: offsets cu that are not ascending within [0, n_tokens], or 2^30 - 1 units or
  * more, a tile of 128 of a request's token heads having two and one for each block of 128 rows that its
  * last token sees (nothing is written then); a length outside
@@ -779,7 +780,9 @@ cfa_status cfa_latent_attention(cfa_latent *latent, int n_tokens, int n_seqs, co
  *   out bf16 [n_tokens, n_heads, 128], lse fp32 [n_tokens, n_heads] or NULL, as cfa_latent_attention
  *   computes them from k = [key | k_rope] and value, scale and unseen keys as there. Values that are not
  *   finite stay in their dim; where only some tokens of a request see one, a pass over the keys of the
- *   tokens beside them, behind the attention, adds it to those.
+ *   tokens beside them, behind the attention, adds it to those. An infinite value whose weight is 0 in 32 bits
+ *   shows as infinity or NaN, one or the other by where its key lies. A key with score -inf and finite values
+ *   has weight 0, and a token's head with no other keys gets 0 and lse -inf.
  * q_stride a multiple of 8, kv_stride and k_rope_stride too. A token that sees no key gets 0 and lse
  * -inf; tokens outside the requests stay as they were. Flagged (CFA_ERR_INVALID_ARG from
  * cfa_latent_status, nothing written): cu or cu_k that are not ascending within [0, n_tokens]
