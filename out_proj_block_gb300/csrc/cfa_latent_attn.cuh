@@ -603,8 +603,6 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             } else {
                 if (p.lse && half == 0 && live) p.lse[out_row] = (m + log2f(l)) * 0.69314718055994531f;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                // two lanes write 32 bytes of a row together, then the other's: a lane's own 16, in 32 rows at once, take a
-                // transaction each
                 const int odd = lane & 1;
                 uint16_t *out = p.out + (out_row - odd) * kLatC + 256 * half + 8 * odd;
                 const bool even_live = row - odd < here, odd_live = row - odd + 1 < here;
@@ -619,26 +617,12 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] = 0u;
                     }
-                    uint32_t w[16], y[8];
+                    uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         w[e] = pack2_bf16_cvt(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int at = 8 * (e >> 2) + (e & 3);  // 32 bytes are two lanes' 16
-                        y[e] = __shfl_xor_sync(~0u, odd ? w[at] : w[at + 4], 1);
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (even_live)
-                            *reinterpret_cast<uint4 *>(out + c + 16 * h) =
-                                odd ? make_uint4(y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3])
-                                    : make_uint4(w[8 * h], w[8 * h + 1], w[8 * h + 2], w[8 * h + 3]);
-                        if (odd_live)
-                            *reinterpret_cast<uint4 *>(out + kLatC + c + 16 * h) =
-                                odd ? make_uint4(w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7])
-                                    : make_uint4(y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3]);
-                    }
+                    for (int h = 0; h < 2; ++h) write_rows_in_pairs(out + c + 16 * h, kLatC, w + 8 * h, even_live, odd_live);
                 }
             }
             tcgen05_fence_before();
@@ -707,22 +691,10 @@ __device__ __forceinline__ void latent_merge_rows(const LatentAttnParams &p, int
     }
     uint16_t *out = p.out + (static_cast<size_t>(cut.y) + row) * kLatC + 4 * chunk;
     if constexpr (kChunks >= 4) {
-        // two lanes write 32 bytes of a row together, then the other's: a lane's own 16, in 32 rows at once, take a
-        // transaction each
-        const bool odd = lane & 1;
-        uint16_t *even_out = out - (odd ? kLatC : 0) + (odd ? 8 : 0);
+        const int odd = lane & 1;
 #pragma unroll
-        for (int h = 0; h < kChunks / 4; ++h) {
-            uint32_t other[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) other[c] = __shfl_xor_sync(~0u, odd ? w[8 * h + c] : w[8 * h + 4 + c], 1);
-            if (row - (odd ? 1 : 0) < cut.x)
-                *reinterpret_cast<uint4 *>(even_out + 16 * h) =
-                    odd ? make_uint4(other[0], other[1], other[2], other[3]) : make_uint4(w[8 * h], w[8 * h + 1], w[8 * h + 2], w[8 * h + 3]);
-            if (row + (odd ? 0 : 1) < cut.x)
-                *reinterpret_cast<uint4 *>(even_out + kLatC + 16 * h) =
-                    odd ? make_uint4(w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7]) : make_uint4(other[0], other[1], other[2], other[3]);
-        }
+        for (int h = 0; h < kChunks / 4; ++h)
+            write_rows_in_pairs(out - odd * kLatC + 8 * odd + 16 * h, kLatC, w + 8 * h, row - odd < cut.x, row + 1 - odd < cut.x);
     } else if (row < cut.x) {
         if constexpr (kChunks == 2) *reinterpret_cast<uint4 *>(out) = make_uint4(w[0], w[1], w[2], w[3]);
         else *reinterpret_cast<uint2 *>(out) = make_uint2(w[0], w[1]);

@@ -668,8 +668,6 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 } else {
                     if (p.lse && live) p.lse[tok * p.H + z.h] = (m + log2f(l)) * 0.69314718055994531f;
                     const float inv = l == 0.f ? 0.f : 1.f / l;
-                    // two lanes write 32 bytes of a row together, then the other's: a lane's own 16, in 32 rows at once, take a
-                    // transaction each
                     const int odd = lane & 1;
                     const size_t next_row = static_cast<size_t>(p.H) * kLatV;
                     uint16_t *out = p.out + ((tok - odd) * p.H + z.h) * kLatV + 8 * odd;
@@ -685,26 +683,12 @@ latent_expanded_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
 #pragma unroll
                             for (int e = 0; e < 32; ++e) v[e] = 0u;
                         }
-                        uint32_t w[16], y[8];
+                        uint32_t w[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
                             w[e] = pack2_bf16_cvt(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int at = 8 * (e >> 2) + (e & 3);  // 32 bytes are two lanes' 16
-                            y[e] = __shfl_xor_sync(~0u, odd ? w[at] : w[at + 4], 1);
-                        }
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (even_live)
-                                *reinterpret_cast<uint4 *>(out + c + 16 * h) =
-                                    odd ? make_uint4(y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3])
-                                        : make_uint4(w[8 * h], w[8 * h + 1], w[8 * h + 2], w[8 * h + 3]);
-                            if (odd_live)
-                                *reinterpret_cast<uint4 *>(out + next_row + c + 16 * h) =
-                                    odd ? make_uint4(w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7])
-                                        : make_uint4(y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3]);
-                        }
+                        for (int h = 0; h < 2; ++h) write_rows_in_pairs(out + c + 16 * h, next_row, w + 8 * h, even_live, odd_live);
                     }
                 }
             }

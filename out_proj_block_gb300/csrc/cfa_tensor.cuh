@@ -112,6 +112,20 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(~0u, v, 0); }
 
+// Lanes hold rows, an even lane's and the next one's behind one another in memory, and w 32 bytes of each: two lanes write
+// 32 bytes of a row together, then the other's. A lane's own 16, in 32 rows at once, take a transaction each.
+// `out` is the even row's 32 bytes, at this lane's half of them; `next` elements on are the odd row's. By a whole warp.
+__device__ __forceinline__ void write_rows_in_pairs(uint16_t *out, size_t next, const uint32_t *w, bool even_live, bool odd_live) {
+    const bool odd = threadIdx.x & 1;
+    uint32_t other[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) other[c] = __shfl_xor_sync(~0u, odd ? w[c] : w[4 + c], 1);
+    if (even_live)
+        *reinterpret_cast<uint4 *>(out) = odd ? make_uint4(other[0], other[1], other[2], other[3]) : make_uint4(w[0], w[1], w[2], w[3]);
+    if (odd_live)
+        *reinterpret_cast<uint4 *>(out + next) = odd ? make_uint4(w[4], w[5], w[6], w[7]) : make_uint4(other[0], other[1], other[2], other[3]);
+}
+
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
