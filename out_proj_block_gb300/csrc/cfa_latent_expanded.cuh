@@ -14,7 +14,8 @@
 // columns), the weights P as bf16 in place of the scores. A tile's next scores need its weights' product to have
 // ended, so while one tile's softmax runs (a thread a row), the other's products do: the tiles take turns. The last
 // commit that a tile's scores wait for covers the product before them, so O may be rescaled then; that is done
-// lazily, when a row's maximum grew by more than 8 (a factor 2^8, far inside fp32), a published method.
+// lazily, when a row's maximum grew by more than 8: o is the same quotient whatever m is, as both of its sums carry
+// 2^-m (weights up to 2^8, far inside fp32).
 //
 // Which tiles make a task: two heads' of the same tokens, or two in a row of one head (kExpShared). Tasks are dealt out
 // in turn to one cluster per pair of SMs, those of most keys first and each round in the other direction; in the order
