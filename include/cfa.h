@@ -557,8 +557,12 @@ enum {
  * head_dim; 0 turns the rotation off. scaling is one of the three above;
  * by parts, with r = original_ctx f_i / 2 pi turns over the original context
  * and g = clamp((r - low_turns) / (high_turns - low_turns), 0, 1), the
- * frequency is g f_i + (1 - g) f_i / factor. Needs theta >= 1, factor >= 1,
- * 0 < magnitude <= 1e6, all finite, and by parts 0 <= low_turns < high_turns and
+ * frequency is g f_i + (1 - g) f_i / factor: linear in the turns. Code that ramps
+ * linearly in the pair's index i instead, between the indices at which a pair makes
+ * high_turns and low_turns (rounded down and up), has other frequencies for the pairs
+ * between, and no arguments here give those: check which of the two a checkpoint was
+ * trained on. Needs theta >= 1, factor >= 1, 0 < magnitude <= 1e6, all finite, and by
+ * parts 0 <= low_turns < high_turns and
  * original_ctx >= 1 (CFA_ERR_INVALID_ARG; a rotary_dim that is no multiple of
  * 16 or above head_dim: CFA_ERR_UNSUPPORTED). Held on the host: a recorded
  * graph keeps the rotation it was recorded with.
@@ -704,7 +708,10 @@ void cfa_latent_destroy(cfa_latent *latent);
 
 /*
  * The rotation of the following cfa_latent_append and cfa_latent_layer calls, over the 64
- * rotated dims; arguments as cfa_paged_set_rope. theta 0 turns it off.
+ * rotated dims; arguments as cfa_paged_set_rope. theta 0 turns it off. magnitude multiplies the
+ * rotated dims of queries and keys, so those dims' part of a score by its square. A model whose
+ * magnitude belongs to the whole score, all 192 dims, has magnitude 1 here and the square of its own in
+ * the attention's scale (magnitude^2 / sqrt(192)).
  */
 cfa_status cfa_latent_set_rope(cfa_latent *latent, double theta, int interleaved, int scaling,
                                double factor, double low_turns, double high_turns,

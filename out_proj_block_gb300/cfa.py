@@ -1117,7 +1117,9 @@ class Latent:
                  factor: float = 1.0, low_turns: float = 1.0, high_turns: float = 32.0,
                  original_ctx: int = 4096, magnitude: float = 1.0) -> None:
         """The rotation of the following append and layer calls (cfa_latent_set_rope);
-        theta 0: no rotation."""
+        theta 0: no rotation. "by_parts" ramps linearly in a pair's turns, not in its index.
+        magnitude is that of the 64 rotated dims; one of the whole score goes, squared, into the
+        attention's scale."""
         if scaling not in ROPE_SCALINGS:
             raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
         st = _lib.cfa_latent_set_rope(self.handle, float(theta), 1 if interleaved else 0,
