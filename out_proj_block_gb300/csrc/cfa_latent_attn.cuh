@@ -30,7 +30,7 @@
 // its sums carry 2^-m, so O is rescaled only when the maximum grew by more than 8 (weights up to 2^8, far
 // inside fp32).
 //
-// Measured, with the merge (one GB300): 64 requests of some 8K rows, 128 heads 86 us (385 MB read once;
+// Measured, with the merge (one GB300): 64 requests of some 8K rows, 128 heads 87 us (385 MB read once;
 // floor 57); 200 of some 2K, 32 heads 72 us (floor 47); 16 with up to four drafted tokens, 20 heads 24 us; one of 4K
 // rows 15.5 us. In the middle of a run memory bounds it, at 6.2 TB/s (products take 2490 clocks of a block of keys,
 // the rows 2900); beside that stand the start (scan, first queries and keys: 8 us), the cut tiles' records (1 to 6 us,
@@ -61,10 +61,11 @@ constexpr int kLatChunk = 64 * 128;        // 64 rows of 64 dims
 // single chunks could not hide (5000 clocks a block instead of 2500)
 constexpr int kLatKSlots = 3, kLatKSlot = 3 * kLatChunk, kLatVSlots = 2, kLatVSlot = 4 * kLatChunk;
 constexpr int kLatQChunks = kLatRow / 64;  // 9
+// Measured with three sets of inputs in turn, which come out 1 to 4% apart from the figures above:
 constexpr int kLatAhead = 1;                // blocks of keys that are asked for in L2 ahead of their copies (64 requests of
-                                            // some 8K rows, 128 heads: with 1, 2, 3, 4, 6 91, 94, 98, 105, 118 us)
+                                            // some 8K rows, 128 heads: with 1, 2, 3, 4, 6 84, 87, 91, 98, 113 us)
 constexpr int kLatPeek = 3;                 // blocks before a tile's end that the next one's first data are asked for
-constexpr int kLatShare = 2;                // least units of a run (1, 2, 4: one request of 4K rows 17.7, 16.4, 18.1 us)
+constexpr int kLatShare = 2;                // least units of a run (1, 2, 4: one request of 4K rows 18.0, 16.0, 17.8 us)
 constexpr int kLatWarps = kLatAttnThreads / 32;
 
 // Shared memory, the same in both blocks of a cluster (an instruction that spans them has one

@@ -54,8 +54,12 @@ constexpr int kExpSlots = 3;           // blocks of keys and of values in flight
 constexpr int kExpKSlot = 3 * 64 * 128, kExpVSlot = 128 * 128;
 // Keys from which on two tiles in a row of a head make a task, and blocks of keys are loaded once for both. Below, two
 // heads' tiles do, which end together: of two in a row the first sees two blocks fewer. Two in a row always and never, in
-// us (before other steps): 1024 tokens behind 2500, 128 heads 184 and 191; a prompt of 8192, 16 heads 215 and 217; five
-// of 763 to 1500, 32 heads 105 and 96; 300 tokens 16 times 83 and 72.
+// us, by keys 1024, 1500, 2200, 2600, 3600, 4500: 1024 tokens of 128 heads 69 and 62, 93 and 92, 126 and 126, 142 and 144,
+// 187 and 191, 225 and 234; 512 tokens of 128 heads 47 and 46, 60 and 59, 78 and 77, 87 and 86, 111 and 111, 132 and 133;
+// of four requests of 512 tokens and 128 heads (to 2200) 136 and 134, 179 and 180, 243 and 258; 2048 tokens of 32 heads
+// (from 2200) 59 and 55, 68 and 64, 92 and 88, 113 and 109. So where the two cross goes by the number of tasks too, from
+// 1400 keys on to beyond 4500; of 108 shapes any switch from 1600 to 4000 is in the mean within 0.2% of any other.
+// Short prompts want one below: five of 763 to 1500, 32 heads 105 and 91; 300 tokens 16 times 81 and 69.
 constexpr int kExpShared = 2560;
 constexpr int kExpPeek = 3;            // blocks before an item's end that the next one's queries are asked for in L2
 constexpr int kExpRows = 2 * kExpTile; // tokens of a task

@@ -8,8 +8,8 @@
 // is split into many small blocks, over the result's columns; unfold's four warps each take a quarter of the sum,
 // joined in their order. mma.sync is enough.
 //
-// Measured (one GB300, calls back to back from Python, which itself takes 4.5 us): 4 tokens of 128 heads in 5.6 us
-// (17.6 MB, floor 2.6); 1 token out 4.6 us (floor 2.5). The rule between the two forms is in
+// Measured (one GB300, calls back to back from Python, which itself takes 4.5 us): 4 tokens of 128 heads in 5.3 us
+// (17.6 MB, floor 2.6); 1 token out 5.1 us (floor 2.5). The rule between the two forms is in
 // cfa_latent.cu.
 #pragma once
 

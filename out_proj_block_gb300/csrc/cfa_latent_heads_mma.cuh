@@ -8,8 +8,8 @@
 // through shared memory to whole boxes of 64 columns, by turns (TMA stores, which end at the last token by
 // themselves; one warpgroup instead took 3% more).
 //
-// Measured (one GB300): 777 tokens of 32 heads in 11.4 us (42 MB, floor 6.2; on mma.sync 15.8 to 18.3), 1000 tokens
-// of 128 heads in 46 us (213 MB, floor 31); 1000 of 128 heads out 34.6 us (181 MB, floor 26.6; on mma.sync
+// Measured (one GB300): 777 tokens of 32 heads in 11.6 us (42 MB, floor 6.2; on mma.sync 15.8 to 18.3), 1000 tokens
+// of 128 heads in 46.5 us (213 MB, floor 31); 1000 of 128 heads out 34.7 us (181 MB, floor 26.6; on mma.sync
 // 46 to 54). The weights read again for every 64 or 128 tokens, out of L2, held the others back.
 #pragma once
 

@@ -23,7 +23,9 @@ __device__ __forceinline__ void umma2_bf16(uint32_t d_tmem, uint64_t a_desc, uin
 // Arrives on a barrier of either block (an address from map_to_rank). What it tells of are writes of the
 // asynchronous proxy, or ones that a proxy fence has put in front of it, to the arriving
 // block's own shared memory, which that block's own tensor core reads. The form that releases at cluster scope
-// takes 1100 clocks each time: 16,000 for a block of keys that should take 3000.
+// takes 1100 clocks each time: 16,000 for a block of keys that should take 3000. By the letter of the memory model
+// this one, which releases at block scope, does not order those writes for the other block's issuing thread: that a
+// product that it issues behind its wait reads them is an assumption about the hardware.
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t remote_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(remote_bar) : "memory");
 }
